@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 import threading
 from typing import Optional
@@ -23,9 +24,10 @@ TWELL_OK = 0
 TWELL_ERR_UNSUPPORTED = 2
 TWELL_BF16 = 0
 TWELL_F32 = 1
+TWELL_E4M3 = 2
 (OP_GATE_PACK, OP_FFN_FUSED_FWD, OP_HYBRID_FWD, OP_HYBRID_BWD, OP_HYBRID_ROUTE, OP_FFN_UNION_FWD, OP_FFN_DECODE,
- OP_FFN_TILE_UNION_FWD, OP_FFN_GATE_UNION_FWD) = range(9)
-DECODE_MAX_N = 16  # twell_ffn_decode takes batches of at most this many tokens
+ OP_FFN_TILE_UNION_FWD, OP_FFN_GATE_UNION_FWD, OP_ADD_RMSNORM_BWD, OP_PAGED_ATTN) = range(11)
+DECODE_MAX_N = 16  # twell_ffn_decode and twell_w4_matvec take batches of at most this many tokens
 STATUS_NAMES = {0: "TWELL_OK", 1: "TWELL_ERR_INVALID", 2: "TWELL_ERR_UNSUPPORTED", 3: "TWELL_ERR_BACKUP_FULL",
                 4: "TWELL_ERR_TIMEOUT", 5: "TWELL_ERR_DEVICE_CHECK", 6: "TWELL_ERR_CUDA",
                 7: "TWELL_ERR_WORKSPACE"}
@@ -37,7 +39,10 @@ EXPORTS = ("twell_packed_vals_bytes", "twell_packed_idx_bytes", "twell_packed_cn
            "twell_gate_gemm", "twell_gemm_test", "twell_column_activity", "twell_gather_rows",
            "twell_read_status", "twell_status_string", "twell_device_info", "twell_wait_probe",
            "twell_ffn_fused_fwd_f16down", "twell_convert_f16", "twell_ffn_decode", "twell_ffn_tile_union_fwd",
-           "twell_count_nonzeros", "twell_convert_f16_transposed", "twell_ffn_gate_union_fwd")
+           "twell_count_nonzeros", "twell_convert_f16_transposed", "twell_ffn_gate_union_fwd",
+           "twell_add_rmsnorm_fwd", "twell_add_rmsnorm_bwd", "twell_kv_append", "twell_kv_gather",
+           "twell_paged_attn_decode", "twell_w4_words_bytes", "twell_w4_scales_bytes", "twell_w4_quantize",
+           "twell_w4_matvec")
 
 
 class TwellError(RuntimeError):
@@ -58,6 +63,14 @@ class _Hybrid(ctypes.Structure):
                 ("u", ctypes.c_void_p), ("col", ctypes.c_void_p), ("cnt", ctypes.c_void_p),
                 ("backup_rows", ctypes.c_void_p), ("n_backup", ctypes.c_void_p), ("A_b", ctypes.c_void_p),
                 ("U_b", ctypes.c_void_p), ("l1", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -110,6 +123,19 @@ def load(path: str = LIB_PATH):
                 "twell_count_nonzeros": (st, [ctypes.POINTER(_Packed), vp, vp, vp]),
                 "twell_gather_rows": (st, [vp, i32, vp, i32, i32, ctypes.c_int, vp, vp, vp]),
                 "twell_gemm_test": (st, [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
+                "twell_add_rmsnorm_fwd": (st, [vp, vp, vp, i32, i32, ctypes.c_float, ctypes.c_int, ctypes.c_int, vp, vp,
+                                               vp, vp, i32, vp, vp]),
+                "twell_add_rmsnorm_bwd": (st, [vp, vp, vp, vp, vp, i32, i32, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                               vp, vp, vp, sz, vp]),
+                "twell_kv_append": (st, [ctypes.POINTER(_KVCache), vp, vp, ctypes.c_int64, ctypes.c_int64, vp, i32, vp,
+                                         vp]),
+                "twell_kv_gather": (st, [ctypes.POINTER(_KVCache), vp, i32, vp, vp, vp, vp]),
+                "twell_paged_attn_decode": (st, [vp, ctypes.c_int64, ctypes.POINTER(_KVCache), vp, vp, i32, i32, i32,
+                                                 ctypes.c_float, i32, vp, vp, vp, sz, vp, vp]),
+                "twell_w4_words_bytes": (sz, [i32, i32]),
+                "twell_w4_scales_bytes": (sz, [i32, i32, i32]),
+                "twell_w4_quantize": (st, [vp, i32, i32, i32, vp, vp, vp, vp]),
+                "twell_w4_matvec": (st, [vp, vp, vp, i32, i32, i32, i32, vp, vp]),
                 "twell_read_status": (st, [vp, vp]),
                 "twell_status_string": (ctypes.c_char_p, [ctypes.c_int]),
                 "twell_device_info": (st, [ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]),
@@ -794,3 +820,327 @@ def twell_hybrid_route_noalloc(a: TwELL, K: int, ctx: Hybrid, stream=None) -> Hy
     _check(load().twell_hybrid_route_noalloc(ctypes.byref(sa), K, ctypes.byref(sc), _stream(stream)),
            "twell_hybrid_route_noalloc")
     return ctx
+
+
+# ------------------------------------------------------------------- the decoder layer around the FFN
+
+def _raw_stream(stream, device) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _status_ptr(status, device) -> int:
+    if status is None:
+        status = _status_bufs.get(device.index)
+        if status is None:
+            status = status_buffer(device)
+    return status.data_ptr()
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _need(t: torch.Tensor, shape, dtype, what: str, device=None) -> torch.Tensor:
+    """A contiguous tensor of that shape and type on that device, or ValueError."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    if t.device != device if device is not None else not t.is_cuda:
+        raise ValueError(f"{what} is on {t.device}")
+    return t
+
+
+_layer_ws = {}
+
+
+def _stream_workspace(op: int, nbytes: int, device, stream, raw: int) -> torch.Tensor:
+    """A workspace per operator, device and stream, grown on demand: calls on one stream run one after
+    the other, so they can share it. It is allocated on that stream, so that an outgrown one is not
+    handed out again before the calls that use it are done."""
+    key = (op, device.index, raw)
+    ws = _layer_ws.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        _layer_ws[key] = ws
+    return ws
+
+
+@dataclasses.dataclass
+class Rows8:
+    """Rows in e4m3 with scales: values[i, j] * scale[i, j // group] (group 0: one scale a row)."""
+
+    values: torch.Tensor  # [N, d] float8_e4m3fn
+    scale: torch.Tensor  # [N, groups] fp32
+    group: int
+
+    @staticmethod
+    def empty(n_rows: int, d: int, group: int = 0, device=None):
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        ng = -(-d // group) if group else 1
+        return Rows8(torch.empty((n_rows, d), dtype=torch.float8_e4m3fn, device=device),
+                     torch.empty((n_rows, ng), dtype=torch.float32, device=device), group)
+
+
+def _rmsnorm_fwd(x, w, res, eps, h, y, y8, rstd, stream):
+    N, d = x.shape
+    dev = x.device
+    _need(x, (N, d), x.dtype, "x")
+    _need(w, (d,), x.dtype, "w", dev)
+    rt = x.dtype
+    if res is not None:
+        rt = res.dtype
+        _need(res, (N, d), rt, "res", dev)
+        h = _need(h, (N, d), rt, "h", dev) if h is not None else torch.empty_like(res)
+    elif h is not None:
+        raise ValueError("h is the sum x + res: without res it is x")
+    if rstd is not None:
+        _need(rstd, (N,), torch.float32, "rstd", dev)
+    if y is not None:
+        _need(y, (N, d), x.dtype, "y", dev)
+    q = sc = None
+    group = 0
+    if y8 is not None:
+        group = y8.group
+        q = _need(y8.values, (N, d), torch.float8_e4m3fn, "the 8-bit rows", dev)
+        sc = _need(y8.scale, (N, -(-d // group) if group else 1), torch.float32, "the 8-bit rows' scale", dev)
+    _check(load().twell_add_rmsnorm_fwd(x.data_ptr(), _p(res), w.data_ptr(), N, d, eps, _dtype_code(x.dtype),
+                                        _dtype_code(rt), _p(h), _p(y), _p(q), _p(sc), group, _p(rstd),
+                                        _raw_stream(stream, dev)),
+           "twell_add_rmsnorm_fwd")
+    return h
+
+
+def twell_add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, res: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                          rstd: Optional[torch.Tensor] = None, training: bool = False, stream=None):
+    """The residual addition and RMS norm: h = x + res, y = h * rstd * w with rstd = 1/sqrt(mean(h^2) + eps).
+
+    x [N, d] and w [d] in one type (bf16 or fp32), res in that type or fp32. Returns (y, h, rstd): h is None
+    without res (it is x then), rstd None unless training is set or a buffer given. h may be res itself
+    and y may be x: the call then works in place."""
+    N = x.shape[0]
+    y = y if y is not None else torch.empty_like(x)
+    if rstd is None and training:
+        rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
+    return y, _rmsnorm_fwd(x, w, res, eps, h, y, None, rstd, stream), rstd
+
+
+def twell_add_rmsnorm_fwd_q8(x: torch.Tensor, w: torch.Tensor, res: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                             group: int = 0, out: Optional[Rows8] = None, y: Optional[torch.Tensor] = None,
+                             h: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                             training: bool = False, stream=None):
+    """twell_add_rmsnorm_fwd with y in e4m3, one scale a row (group 0) or per 128 columns (group 128):
+    returns (Rows8, h, rstd). y is written in x's type as well when a buffer for it is given."""
+    N, d = x.shape
+    out = out if out is not None else Rows8.empty(N, d, group, x.device)
+    if rstd is None and training:
+        rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
+    return out, _rmsnorm_fwd(x, w, res, eps, h, y, out, rstd, stream), rstd
+
+
+def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor,
+                          dh: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                          dw: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of the call above from its h (x where it had no res) and rstd: returns (dx, dw), dx the
+    gradient of x and of res alike, dw fp32. dy, dh (the gradient that reaches h from the residual
+    stream, or None) and dx share a type, bf16 or fp32."""
+    N, d = h.shape
+    dev = h.device
+    _need(h, (N, d), h.dtype, "h")
+    _need(dy, (N, d), dy.dtype, "dy", dev)
+    _need(w, (d,), w.dtype, "w", dev)
+    _need(rstd, (N,), torch.float32, "rstd", dev)
+    if dh is not None:
+        _need(dh, (N, d), dy.dtype, "dh", dev)
+    dx = _need(dx, (N, d), dy.dtype, "dx", dev) if dx is not None else torch.empty_like(dy)
+    dw = _need(dw, (d,), torch.float32, "dw", dev) if dw is not None else torch.empty((d,), dtype=torch.float32, device=dev)
+    s = _raw_stream(stream, dev)
+    lib = load()
+    if ws is None:
+        ws = _stream_workspace(OP_ADD_RMSNORM_BWD, lib.twell_workspace_bytes(OP_ADD_RMSNORM_BWD, N, d, 1, 0, 0, 0), dev,
+                               stream, s)
+    _check(lib.twell_add_rmsnorm_bwd(dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dh), N, d,
+                                     _dtype_code(w.dtype), _dtype_code(h.dtype), _dtype_code(dy.dtype), dx.data_ptr(),
+                                     dw.data_ptr(), ws.data_ptr(), ws.numel(), s),
+           "twell_add_rmsnorm_bwd")
+    return dx, dw
+
+
+class KVCache:
+    """A paged key-value cache in device memory (twell_kv_cache in include/twell.h): k and v
+    [n_pages, n_kv_heads, page_size, head_dim] in bf16, or in float8_e4m3fn with fp32 scales
+    [n_pages, n_kv_heads, page_size]. Any strides with head_dim contiguous will do (a [n_pages, page_size,
+    n_kv_heads, head_dim] buffer permuted, halves of one buffer), the same for k and v. Token slot
+    s is offset s % page_size of page s // page_size."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or not k.is_cuda:
+            raise ValueError("k and v must be device tensors of one shape [n_pages, n_kv_heads, page_size, head_dim] and type")
+        if k.stride() != v.stride() or (k.numel() > 0 and k.stride(3) != 1):
+            raise ValueError("k and v must have the same strides, head_dim contiguous")
+        q8 = k.dtype == torch.float8_e4m3fn
+        if not q8 and k.dtype != torch.bfloat16:
+            raise TypeError(f"unsupported cache type {k.dtype}")
+        sp = sh = 0
+        if q8:
+            for s in (k_scale, v_scale):
+                if s is None or s.shape != k.shape[:3] or s.dtype != torch.float32 or s.device != k.device:
+                    raise ValueError("an e4m3 cache needs fp32 scales [n_pages, n_kv_heads, page_size]")
+            if k_scale.stride() != v_scale.stride() or (k.shape[2] > 1 and k_scale.stride(2) != 1):
+                raise ValueError("the scales must have the same strides, a page's tokens adjacent")
+            sp, sh = k_scale.stride(0), k_scale.stride(1)
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        # a page of one token has no token stride of its own
+        ts = k.stride(2) if self.page_size > 1 else self.head_dim
+        self._c = _KVCache(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
+                           TWELL_E4M3 if q8 else TWELL_BF16, k.data_ptr(), v.data_ptr(), _p(k_scale), _p(v_scale),
+                           k.stride(0), k.stride(1), ts, sp, sh)
+        self._ref = ctypes.pointer(self._c)
+
+    @staticmethod
+    def empty(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+              device=None):
+        """An empty cache; its slots hold nothing until they are written (an e4m3 cache's scales are zero)."""
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        k, v = (torch.empty((n_pages, n_kv_heads, page_size, head_dim), dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return KVCache(k, v)
+        return KVCache(k, v, *(torch.zeros((n_pages, n_kv_heads, page_size), dtype=torch.float32, device=device)
+                               for _ in range(2)))
+
+
+def _slots(slots: torch.Tensor, device) -> torch.Tensor:
+    if slots.dim() != 1:
+        raise ValueError("slots must be one int32 per token")
+    return _need(slots, slots.shape, torch.int32, "slots", device)
+
+
+def twell_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, status=None,
+                    stream=None) -> None:
+    """Write n tokens' keys and values (bf16 [n, n_kv_heads, head_dim]; any token stride, heads
+    contiguous) to their slots (int32 [n], -1 = skip), quantised where the cache is in e4m3."""
+    n = _slots(slots, cache.device).numel()
+    shape, inner = (n, cache.n_kv_heads, cache.head_dim), (cache.head_dim, 1)
+    for t, what in ((k, "k"), (v, "v")):
+        if t.shape != shape or t.dtype != torch.bfloat16 or t.device != cache.device or (n and t.stride()[1:] != inner):
+            raise ValueError(f"{what} must be bf16 {shape} on {cache.device} with contiguous heads")
+    row = cache.n_kv_heads * cache.head_dim
+    _check(load().twell_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else row,
+                                  v.stride(0) if n > 1 else row, slots.data_ptr(), n, _status_ptr(status, cache.device),
+                                  _raw_stream(stream, cache.device)),
+           "twell_kv_append")
+
+
+def twell_kv_gather(cache: KVCache, slots: torch.Tensor, k_out: Optional[torch.Tensor] = None,
+                    v_out: Optional[torch.Tensor] = None, status=None, stream=None):
+    """Read slots back: (k, v), bf16 [n, n_kv_heads, head_dim]; zeros for slot -1."""
+    n = _slots(slots, cache.device).numel()
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    k_out, v_out = (_need(t, shape, torch.bfloat16, what, cache.device) if t is not None else
+                    torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+                    for t, what in ((k_out, "k_out"), (v_out, "v_out")))
+    _check(load().twell_kv_gather(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                                  _status_ptr(status, cache.device), _raw_stream(stream, cache.device)),
+           "twell_kv_gather")
+    return k_out, v_out
+
+
+def twell_paged_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                            scale: Optional[float] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, status=None,
+                            stream=None):
+    """Attention of one new token per sequence over the paged cache: returns (out, lse).
+
+    q bf16 [B, n_q_heads, head_dim] (any sequence stride, heads contiguous); page_table int32
+    [B, max_pages]; seq_lens int32 [B] (the new token's own slot counted, if it is to be seen); scale
+    1/sqrt(head_dim) unless given; window > 0 keeps the last `window` tokens. out bf16, written; lse fp32
+    [B, n_q_heads] (natural logarithm of the sum of exponentials) is written when a buffer is given. A
+    sequence of length 0 gives zeros and -inf."""
+    dev = cache.device
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != dev or q.shape[2] != cache.head_dim or \
+            (q.numel() and q.stride()[1:] != (cache.head_dim, 1)):
+        raise ValueError(f"q must be bf16 [B, n_q_heads, {cache.head_dim}] on {dev} with contiguous heads")
+    B, n_q, hd = q.shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    _need(page_table, (B, page_table.shape[1]), torch.int32, "page_table", dev)
+    _need(seq_lens, (B,), torch.int32, "seq_lens", dev)
+    out = _need(out, (B, n_q, hd), torch.bfloat16, "out", dev) if out is not None else \
+        torch.empty((B, n_q, hd), dtype=torch.bfloat16, device=dev)
+    if lse is not None:
+        _need(lse, (B, n_q), torch.float32, "lse", dev)
+    s = _raw_stream(stream, dev)
+    lib = load()
+    if ws is None:
+        ws = _stream_workspace(OP_PAGED_ATTN, lib.twell_workspace_bytes(OP_PAGED_ATTN, B, hd, 1, 0, 0, 0), dev, stream, s)
+    _check(lib.twell_paged_attn_decode(q.data_ptr(), q.stride(0) if B > 1 else n_q * hd, cache._ref,
+                                       page_table.data_ptr(), seq_lens.data_ptr(), B, n_q, page_table.shape[1],
+                                       scale if scale is not None else 1.0 / math.sqrt(hd), window, out.data_ptr(),
+                                       _p(lse), ws.data_ptr(), ws.numel(), _status_ptr(status, dev), s),
+           "twell_paged_attn_decode")
+    return out, lse
+
+
+@dataclasses.dataclass
+class W4Weights:
+    """4-bit weights [n, k] with a bf16 scale per `group` columns, in the layout of include/twell.h."""
+
+    words: torch.Tensor  # int32 [ceil(n/16), ceil(k/128), 8, 4, 2, 4]
+    scales: torch.Tensor  # bf16 [ceil(n/16), ceil(k/128), 8, 2, 128/group]
+    n: int
+    k: int
+    group: int
+
+    def __post_init__(self):
+        if self.group not in (32, 64, 128) or self.n <= 0 or self.k <= 0 or self.k % 32 or self.k % self.group:
+            raise ValueError("W4Weights: group 32, 64 or 128, k a multiple of 32 and of group")
+        tiles = (-(-self.n // 16), -(-self.k // 128))
+        _need(self.words, tiles + (8, 4, 2, 4), torch.int32, "words")
+        _need(self.scales, tiles + (8, 2, 128 // self.group), torch.bfloat16, "scales", self.words.device)
+
+    def dequantize(self) -> torch.Tensor:
+        """The fp32 weights [n, k] that the codes stand for (a check, not a fast path)."""
+        nt, kt = self.words.shape[:2]
+        shift = torch.tensor([[0, 16], [4, 20], [8, 24], [12, 28]], device=self.words.device, dtype=torch.int32)
+        c = (self.words[..., None, None] >> shift) & 15
+        c = c.permute(0, 4, 2, 1, 5, 3, 6, 7).reshape(nt * 16, kt * 128)
+        s = self.scales.permute(0, 3, 2, 1, 4).reshape(nt * 16, -1).float().repeat_interleave(self.group, dim=1)
+        return ((c - 8).float() * s)[:self.n, :self.k]
+
+
+def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=None) -> W4Weights:
+    """bf16 weights [n, k] quantised to 4 bits with a scale per `group` columns, laid out for
+    twell_w4_matvec (once per weight)."""
+    if W.dim() != 2:
+        raise ValueError("W must be a 2-D bf16 tensor")
+    n, k = W.shape
+    _need(W, (n, k), torch.bfloat16, "W")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    nt, kt = -(-n // 16), -(-k // 128)
+    words = torch.empty((nt, kt, 8, 4, 2, 4), dtype=torch.int32, device=W.device)
+    scales = torch.empty((nt, kt, 8, 2, 128 // group), dtype=torch.bfloat16, device=W.device)
+    out = W4Weights(words, scales, n, k, group)
+    _check(load().twell_w4_quantize(W.data_ptr(), n, k, group, words.data_ptr(), scales.data_ptr(),
+                                    _status_ptr(status, W.device), _raw_stream(stream, W.device)),
+           "twell_w4_quantize")
+    return out
+
+
+def twell_w4_matvec(x: torch.Tensor, W: W4Weights, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = x W^T (bf16) for at most DECODE_MAX_N tokens and 4-bit weights."""
+    N = x.shape[0]
+    dev = x.device
+    _need(x, (N, W.k), torch.bfloat16, "x", W.words.device)
+    y = _need(y, (N, W.n), torch.bfloat16, "y", dev) if y is not None else \
+        torch.empty((N, W.n), dtype=torch.bfloat16, device=dev)
+    _check(load().twell_w4_matvec(x.data_ptr(), W.words.data_ptr(), W.scales.data_ptr(), N, W.n, W.k, W.group,
+                                  y.data_ptr(), _raw_stream(stream, dev)),
+           "twell_w4_matvec")
+    return y

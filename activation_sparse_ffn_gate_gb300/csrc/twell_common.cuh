@@ -493,6 +493,9 @@ twell_status down_small(const __half* H, const void* Wd16t_s, int N, int d, int 
 size_t tile_union_ws_bytes(int N, int f);
 // Bytes of the workspace twell_ffn_decode needs (twell_decode.cu).
 size_t decode_ws_bytes(int N, int d, int f, int T);
+// Bytes of the workspaces of twell_add_rmsnorm_bwd (twell_norm.cu) and twell_paged_attn_decode (twell_attn.cu).
+size_t norm_bwd_ws_bytes(int N, int d);
+size_t paged_attn_ws_bytes(int B, int hd);
 
 // 2-D tensor map over a row-major matrix of 16-bit elements: `inner` contiguous elements per row,
 // `outer` rows, row pitch `ld` elements; box [box_inner, box_outer]; 128-byte swizzle; zero fill

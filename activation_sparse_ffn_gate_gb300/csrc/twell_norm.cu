@@ -1,0 +1,357 @@
+// twell_norm.cu -- the residual addition and RMS norm that stand before the FFN, forward and backward.
+//
+//   h = x + r,  s = 1 / sqrt(mean(h^2) + eps),  y = h s w
+//   dx = s (g - xh mean(g xh)) + dh  with  xh = h s, g = dy w;   dw = sum over rows of dy xh
+//
+// Both passes are bounded by memory traffic: every element is read and written once, a row stays in
+// registers between its statistics and its output, 8 elements (one chunk) a thread, so a row is
+// spread over d / 8 threads (two chunks a thread above 8192 columns). Rows of few columns share a
+// block. All sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the fp32
+// values (y from the unrounded h, so that it does not depend on the residual stream's type).
+#include "twell_common.cuh"
+#include "twell_ops.cuh"
+
+namespace twell {
+namespace {
+
+constexpr int kNormMaxD = 16384;
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMinThreads = 256;  // rows of few columns share a block of this many threads
+
+// How a row of d columns is spread over a block: `wpr` warps a row, `rpb` rows a block.
+struct NormShape {
+    int ch, wpr, rpb;
+    explicit NormShape(int d)
+    {
+        const int chunks = d / 8;
+        ch = chunks <= kNormMaxThreads ? 1 : 2;
+        wpr = (chunks + 32 * ch - 1) / (32 * ch);
+        rpb = wpr * 32 >= kNormMinThreads ? 1 : kNormMinThreads / (wpr * 32);
+    }
+    int threads() const { return 32 * wpr * rpb; }
+};
+
+// Sum (or maximum, of values >= 0) over the `wpr` warps of a row; every thread of the block takes part.
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* red, int wpr)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    if (wpr == 1) return v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = warp / wpr * wpr;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = lane < wpr ? red[first + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    return v;
+}
+
+struct NormFwdArgs {
+    const void* x;
+    const void* res;
+    const void* w;
+    void* h;
+    void* y;
+    uint8_t* y8;
+    float* scale;
+    float* rstd;
+    int N, d, group, ng, wpr, rpb;
+    float eps;
+};
+
+template <typename T, typename R, int CH>
+__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const NormFwdArgs a)
+{
+    __shared__ float red[2][32];
+    pdl_begin();
+    const int per_row = 32 * a.wpr;
+    const int t = static_cast<int>(threadIdx.x) % per_row;
+    const long long row = static_cast<long long>(blockIdx.x) * a.rpb + threadIdx.x / per_row;
+    const bool live = row < a.N;
+    const int chunks = a.d / 8;
+    const size_t base = static_cast<size_t>(live ? row : 0) * a.d;
+
+    float h[CH][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = t + i * per_row;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+        if (live && c < chunks) {
+            load8(static_cast<const T*>(a.x) + base + c * 8, h[i]);
+            if (a.res != nullptr) {
+                float r[8];
+                load8(static_cast<const R*>(a.res) + base + c * 8, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = t + i * per_row;
+        if (a.h != nullptr && live && c < chunks) store8(static_cast<R*>(a.h) + base + c * 8, h[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+    }
+    ss = row_reduce<false>(ss, red[0], a.wpr);
+    const float s = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+    if (a.rstd != nullptr && live && t == 0) a.rstd[row] = s;
+
+    float top[CH];
+    float row_top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = t + i * per_row;
+        top[i] = 0.0f;
+        if (c < chunks) {
+            float w[8];
+            load8(static_cast<const T*>(a.w) + c * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[i][e] = h[i][e] * s * w[e];
+                top[i] = fmaxf(top[i], fabsf(h[i][e]));
+            }
+            if (a.y != nullptr && live) store8(static_cast<T*>(a.y) + base + c * 8, h[i]);
+        }
+        row_top = fmaxf(row_top, top[i]);
+    }
+    if (a.y8 == nullptr) return;
+    if (a.group == a.d) {
+        row_top = row_reduce<true>(row_top, red[1], a.wpr);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) top[i] = row_top;
+    } else {  // groups of 128 columns: 16 lanes next to each other
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = t + i * per_row;
+        if (!live || c >= chunks) continue;
+        const Scale8 q(top[i]);
+        *reinterpret_cast<uint2*>(a.y8 + base + c * 8) = q.pack8(h[i]);
+        const int per_group = a.group / 8;
+        if (c % per_group == 0) a.scale[static_cast<size_t>(row) * a.ng + c / per_group] = q.scale;
+    }
+}
+
+struct NormBwdArgs {
+    const void* dy;
+    const void* h;
+    const void* w;
+    const void* dh;
+    const float* rstd;
+    void* dx;
+    float* part;  // [gridDim.x * rpb, d]
+    int N, d, wpr, rpb;
+};
+
+// Rows blockIdx.x * rpb + ..., then every gridDim.x * rpb-th one; the weights stay in registers and
+// the rows' shares of dw are added there too, one partial row of dw for each row slot of the grid.
+template <typename T, typename R, typename G, int CH>
+__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const NormBwdArgs a)
+{
+    __shared__ float red[2][32];
+    pdl_begin();
+    const int per_row = 32 * a.wpr;
+    const int t = static_cast<int>(threadIdx.x) % per_row;
+    const int sub = static_cast<int>(threadIdx.x) / per_row;
+    const int chunks = a.d / 8;
+    float dw[CH][8], w[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = t + i * per_row;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] = w[i][e] = 0.0f;
+        if (c < chunks) load8(static_cast<const T*>(a.w) + c * 8, w[i]);
+    }
+    const long long step = static_cast<long long>(gridDim.x) * a.rpb;
+    int flip = 0;
+    for (long long r0 = static_cast<long long>(blockIdx.x) * a.rpb; r0 < a.N; r0 += step, flip ^= 1) {
+        const long long row = r0 + sub;
+        const bool live = row < a.N;
+        const size_t base = static_cast<size_t>(live ? row : 0) * a.d;
+        const float s = live ? a.rstd[row] : 0.0f;
+        float dy[CH][8], xh[CH][8];
+        float p = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = t + i * per_row;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dy[i][e] = xh[i][e] = 0.0f;
+            if (live && c < chunks) {
+                load8(static_cast<const G*>(a.dy) + base + c * 8, dy[i]);
+                load8(static_cast<const R*>(a.h) + base + c * 8, xh[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[i][e] *= s;
+                dw[i][e] = fmaf(dy[i][e], xh[i][e], dw[i][e]);
+                dy[i][e] *= w[i][e];
+                p = fmaf(dy[i][e], xh[i][e], p);
+            }
+        }
+        p = row_reduce<false>(p, red[flip], a.wpr) / static_cast<float>(a.d);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = t + i * per_row;
+            if (!live || c >= chunks) continue;
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = s * (dy[i][e] - xh[i][e] * p);
+            if (a.dh != nullptr) {
+                float u[8];
+                load8(static_cast<const G*>(a.dh) + base + c * 8, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += u[e];
+            }
+            store8(static_cast<G*>(a.dx) + base + c * 8, o);
+        }
+    }
+    float* part = a.part + (static_cast<size_t>(blockIdx.x) * a.rpb + sub) * a.d;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = t + i * per_row;
+        if (c < chunks) store8(part + c * 8, dw[i]);
+    }
+}
+
+// dw[c] = sum over p of part[p][c]: 32 columns a block, 32 threads a column, each over every 32nd
+// partial row, their sums added by a fixed tree: the same dw from call to call.
+__global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __restrict__ part, int P, int d,
+                                                              float* __restrict__ dw)
+{
+    __shared__ float sums[32][33];
+    pdl_begin();
+    const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float v = 0.0f;
+    if (c < d) {
+#pragma unroll 8
+        for (int p = way; p < P; p += 32) v += part[static_cast<size_t>(p) * d + c];
+    }
+    sums[way][lane] = v;
+    __syncthreads();
+    v = sums[lane][way];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * 32 + way < d) dw[blockIdx.x * 32 + way] = v;
+}
+
+// Blocks of the backward pass: enough for kNormBwdThreads threads on each SM, no more than rows.
+constexpr int kNormBwdThreads = 1280;
+int bwd_blocks(int N, const NormShape& S, int sms)
+{
+    const int per_sm = std::max(1, kNormBwdThreads / S.threads());
+    const long long need = (static_cast<long long>(N) + S.rpb - 1) / S.rpb;
+    return static_cast<int>(std::min<long long>(need, static_cast<long long>(sms) * per_sm));
+}
+// The workspace is sized for this many SMs, whatever the device, so that its size is the same with
+// and without one; the launch uses the device's own number up to it.
+constexpr int kNormMaxSms = 160;
+
+template <typename T, typename R>
+twell_status run_norm_fwd(const NormFwdArgs& a, const NormShape& S, cudaStream_t s)
+{
+    auto kern = S.ch == 1 ? add_rmsnorm_fwd_kernel<T, R, 1> : add_rmsnorm_fwd_kernel<T, R, 2>;
+    return twell_host::launch_dep(kern, dim3((a.N + S.rpb - 1) / S.rpb), dim3(S.threads()), 0, s, a);
+}
+
+template <typename T, typename R, typename G>
+twell_status run_norm_bwd(const NormBwdArgs& a, const NormShape& S, int blocks, float* dw, cudaStream_t s)
+{
+    auto kern = S.ch == 1 ? add_rmsnorm_bwd_kernel<T, R, G, 1> : add_rmsnorm_bwd_kernel<T, R, G, 2>;
+    twell_status st = twell_host::launch_dep(kern, dim3(blocks), dim3(S.threads()), 0, s, a);
+    if (st != TWELL_OK) return st;
+    return twell_host::launch_dep(add_rmsnorm_dw_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s,
+                                  static_cast<const float*>(a.part), blocks * S.rpb, a.d, dw);
+}
+
+}  // namespace
+}  // namespace twell
+
+size_t twell_host::norm_bwd_ws_bytes(int N, int d)
+{
+    if (N <= 0 || d % 8 != 0 || d > twell::kNormMaxD) return 0;
+    const twell::NormShape S(d);
+    return static_cast<size_t>(twell::bwd_blocks(N, S, twell::kNormMaxSms)) * S.rpb * d * 4;
+}
+
+using namespace twell_host;
+
+static bool norm_types_ok(twell_dtype dtype, twell_dtype res_dtype)
+{
+    return (dtype == TWELL_BF16 && (res_dtype == TWELL_BF16 || res_dtype == TWELL_F32)) ||
+           (dtype == TWELL_F32 && res_dtype == TWELL_F32);
+}
+
+extern "C" twell_status twell_add_rmsnorm_fwd(const void* x, const void* res, const void* w, int32_t N, int32_t d,
+                                              float eps, twell_dtype dtype, twell_dtype res_dtype, void* h_out, void* y,
+                                              void* y8, float* y8_scale, int32_t group, float* rstd, void* stream)
+{
+    if (N < 0 || d <= 0 || d % 8 != 0 || w == nullptr || !(eps >= 0.0f)) return TWELL_ERR_INVALID;
+    if (y8 != nullptr && group != 0 && group != 128) return TWELL_ERR_UNSUPPORTED;
+    if (!norm_types_ok(dtype, res_dtype) || d > twell::kNormMaxD) return TWELL_ERR_UNSUPPORTED;
+    if (N == 0) return TWELL_OK;
+    if (x == nullptr || (y == nullptr && y8 == nullptr) || (y8 != nullptr && y8_scale == nullptr)) return TWELL_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(res) || !aligned16(w) || !aligned16(h_out) || !aligned16(y) || !aligned16(y8) ||
+        !aligned16(y8_scale) || !aligned16(rstd))
+        return TWELL_ERR_INVALID;
+    const twell::NormShape S(d);
+    const int g = group == 0 ? d : group;
+    const twell::NormFwdArgs a{x,    res, w, h_out, y,  static_cast<uint8_t*>(y8), y8_scale, rstd, N, d,
+                               g, (d + g - 1) / g, S.wpr, S.rpb, eps};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == TWELL_F32) return twell::run_norm_fwd<float, float>(a, S, s);
+    if (res_dtype == TWELL_F32) return twell::run_norm_fwd<__nv_bfloat16, float>(a, S, s);
+    return twell::run_norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, S, s);
+}
+
+extern "C" twell_status twell_add_rmsnorm_bwd(const void* dy, const void* h, const void* w, const float* rstd,
+                                              const void* dh, int32_t N, int32_t d, twell_dtype dtype,
+                                              twell_dtype res_dtype, twell_dtype grad_dtype, void* dx, float* dw,
+                                              void* ws, size_t ws_bytes, void* stream)
+{
+    if (N < 0 || d <= 0 || d % 8 != 0 || w == nullptr || dw == nullptr || !aligned16(dw)) return TWELL_ERR_INVALID;
+    if (!norm_types_ok(dtype, res_dtype) || (grad_dtype != TWELL_BF16 && grad_dtype != TWELL_F32) ||
+        d > twell::kNormMaxD)
+        return TWELL_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0)
+        return cudaMemsetAsync(dw, 0, static_cast<size_t>(d) * 4, s) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+    if (dy == nullptr || h == nullptr || rstd == nullptr || dx == nullptr) return TWELL_ERR_INVALID;
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(w) || !aligned16(rstd) || !aligned16(dh) || !aligned16(dx))
+        return TWELL_ERR_INVALID;
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < norm_bwd_ws_bytes(N, d)) return TWELL_ERR_WORKSPACE;
+    DevInfo dev;
+    if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
+    const twell::NormShape S(d);
+    const int blocks = twell::bwd_blocks(N, S, std::min(dev.sm_count, twell::kNormMaxSms));
+    const twell::NormBwdArgs a{dy, h, w, dh, rstd, dx, static_cast<float*>(ws), N, d, S.wpr, S.rpb};
+    using bf = __nv_bfloat16;
+    const bool g32 = grad_dtype == TWELL_F32;
+    if (dtype == TWELL_F32)
+        return g32 ? twell::run_norm_bwd<float, float, float>(a, S, blocks, dw, s)
+                   : twell::run_norm_bwd<float, float, bf>(a, S, blocks, dw, s);
+    if (res_dtype == TWELL_F32)
+        return g32 ? twell::run_norm_bwd<bf, float, float>(a, S, blocks, dw, s)
+                   : twell::run_norm_bwd<bf, float, bf>(a, S, blocks, dw, s);
+    return g32 ? twell::run_norm_bwd<bf, bf, float>(a, S, blocks, dw, s)
+               : twell::run_norm_bwd<bf, bf, bf>(a, S, blocks, dw, s);
+}

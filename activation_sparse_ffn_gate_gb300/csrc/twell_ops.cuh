@@ -1,0 +1,72 @@
+// twell_ops.cuh -- helpers shared by the operators around the FFN (norm, key-value cache, attention
+// over it, 4-bit products): 8-element loads and stores, and the 8-bit rounding with its scale.
+#pragma once
+
+#include <algorithm>
+
+#include "twell_common.cuh"
+
+namespace twell {
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&o)[8])
+{
+    unpack16(*reinterpret_cast<const uint4*>(p), o, static_cast<__nv_bfloat16*>(nullptr));
+}
+__device__ __forceinline__ void load8(const float* p, float (&o)[8])
+{
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+    o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&o)[8])
+{
+    *reinterpret_cast<uint4*>(p) = pack16(o, static_cast<__nv_bfloat16*>(nullptr));
+}
+__device__ __forceinline__ void store8(float* p, const float (&o)[8])
+{
+    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+}
+
+// 8-bit rounding of values whose largest magnitude is `top`: code = e4m3(v * (448 / a)) to nearest
+// even, a = max(top, 2^-60), so that 448 / a stays finite and a row of zeros has codes 0; the code
+// stands for code * scale, scale = a / 448. A row that holds an infinity has an infinite scale and
+// codes 0 or NaN; a NaN element has the code NaN and does not count toward `top`.
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxMin = 8.6736173798840355e-19f;  // 2^-60
+
+struct Scale8 {
+    float scale, mul;
+    __device__ __forceinline__ explicit Scale8(float top)
+    {
+        const float a = fmaxf(top, kAmaxMin);
+        scale = a / kE4m3Max;
+        mul = kE4m3Max / a;
+    }
+    // two codes, the first in the low byte
+    __device__ __forceinline__ uint32_t pack2(float a, float b) const
+    {
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b * mul), "f"(a * mul));
+        return r;
+    }
+    __device__ __forceinline__ uint2 pack8(const float (&v)[8]) const
+    {
+        return make_uint2(pack2(v[0], v[1]) | (pack2(v[2], v[3]) << 16), pack2(v[4], v[5]) | (pack2(v[6], v[7]) << 16));
+    }
+};
+
+// Two e4m3 codes (low byte first) as an fp16 pair; every e4m3 value is exact in fp16.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint16_t v)
+{
+    const uint32_t h = e4m3x2_f16x2(v);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace twell

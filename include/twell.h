@@ -58,7 +58,8 @@ typedef enum {
     TWELL_ERR_WORKSPACE = 7    /* workspace missing or smaller than twell_workspace_bytes() */
 } twell_status;
 
-typedef enum { TWELL_BF16 = 0, TWELL_F32 = 1 } twell_dtype;
+/* TWELL_E4M3 (8 bits, largest value 448) is an element type of the key-value cache only. */
+typedef enum { TWELL_BF16 = 0, TWELL_F32 = 1, TWELL_E4M3 = 2 } twell_dtype;
 
 typedef enum {
     TWELL_OP_GATE_PACK = 0,
@@ -69,7 +70,9 @@ typedef enum {
     TWELL_OP_FFN_UNION_FWD = 5,
     TWELL_OP_FFN_DECODE = 6,
     TWELL_OP_FFN_TILE_UNION_FWD = 7,
-    TWELL_OP_FFN_GATE_UNION_FWD = 8
+    TWELL_OP_FFN_GATE_UNION_FWD = 8,
+    TWELL_OP_ADD_RMSNORM_BWD = 9, /* N rows of d columns; the other arguments are not used */
+    TWELL_OP_PAGED_ATTN = 10      /* N sequences, d = head_dim; the other arguments are not used */
 } twell_op;
 
 /* A TwELL matrix of gate activations a = ReLU(G), [n_rows, n_cols] ([TG] "Вот тут и решает TwELL";
@@ -356,6 +359,119 @@ TWELL_API twell_status twell_column_activity(const twell_packed* a, int32_t* col
  * row index outside [0, n_src) is reported as TWELL_ERR_DEVICE_CHECK and its output row is 0. */
 TWELL_API twell_status twell_gather_rows(const void* src, int32_t n_src, const int32_t* rows, int32_t n,
                                int32_t d, twell_dtype dtype, void* dst, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The operators of a decoder layer around the FFN. They take what stands before and beside it: the
+ * residual addition with its RMS norm, the projections' products at decode batch sizes with 4-bit
+ * weights, the paged key-value cache and the attention of one new token over it. The pages describe
+ * the FFN only; these follow the conventions above (asynchronous, caller-owned memory, 16-byte
+ * aligned pointers, host-checked arguments), and every launch is a programmatic dependent of the
+ * one before it on its stream.
+ */
+
+/* h = x + res,  s = 1 / sqrt(mean(h^2) + eps),  y = h s w  for every row of x [N, d].
+ * x, w [d] and y have type `dtype`, res and h_out `res_dtype`: (TWELL_BF16, TWELL_BF16),
+ * (TWELL_BF16, TWELL_F32) or (TWELL_F32, TWELL_F32), else TWELL_ERR_UNSUPPORTED. res may be null
+ * (then h = x); h_out (h rounded to res_dtype) and rstd [N] (s, fp32, for the backward call) are
+ * written when not null. At least one of y and y8 must not be null. y8 [N, d] receives y in e4m3
+ * with y8_scale [N, ng]: per group of `group` columns (0: one group a row, ng = 1; 128: ng =
+ * ceil(d / 128); else TWELL_ERR_UNSUPPORTED), a = max(|y|, 2^-60), scale = a / 448, code = y * (448 / a)
+ * rounded to nearest even; a code stands for code * scale. All sums are fp32; y and y8 are rounded
+ * once, from the fp32 h. h_out may be res, and y may be x. d a multiple of 8 up to 16384.
+ */
+TWELL_API twell_status twell_add_rmsnorm_fwd(const void* x, const void* res, const void* w, int32_t N, int32_t d,
+                                   float eps, twell_dtype dtype, twell_dtype res_dtype, void* h_out, void* y,
+                                   void* y8, float* y8_scale, int32_t group, float* rstd, void* stream);
+
+/* Gradients of <y, dy> + <h, dh> for the call above, from its h [N, d] (res_dtype; h_out, or x where
+ * there was no res) and rstd [N]: dx [N, d] = s (g - xh mean(g xh)) + dh with xh = h s, g = dy w -- the
+ * gradient of x and of res alike -- and dw [d] (fp32, overwritten) = sum over rows of dy xh. dy, dh
+ * (null: zero) and dx have type grad_dtype, TWELL_BF16 or TWELL_F32 (the FFN's backward call gives an fp32
+ * dx). dw is summed in a fixed order: the same from call to call. dx may be dy or dh. ws:
+ * twell_workspace_bytes(TWELL_OP_ADD_RMSNORM_BWD, N, d, 1, 0, 0, 0) bytes.
+ */
+TWELL_API twell_status twell_add_rmsnorm_bwd(const void* dy, const void* h, const void* w, const float* rstd,
+                                   const void* dh, int32_t N, int32_t d, twell_dtype dtype, twell_dtype res_dtype,
+                                   twell_dtype grad_dtype, void* dx, float* dw, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* A paged key-value cache (host struct; device memory owned by the caller). Key and value of token
+ * slot s = page * page_size + offset and head h start at element
+ *   page * page_stride + h * head_stride + offset * token_stride
+ * of k and of v (head_dim contiguous elements). dtype is TWELL_BF16, or TWELL_E4M3 with the fp32 scales
+ * k_scale, v_scale at page * scale_page_stride + h * scale_head_stride + offset: a code stands for
+ * code * scale. page_size is a power of two up to 1024, head_dim a multiple of 16 up to 256,
+ * n_pages * page_size < 2^31; strides in elements, k and v strides multiples of 16 bytes. Addresses are
+ * formed in 64 bits. */
+typedef struct {
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    twell_dtype dtype;
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t token_stride;
+    int64_t scale_page_stride;
+    int64_t scale_head_stride;
+} twell_kv_cache;
+
+/* Writes n tokens' keys and values into the cache: k, v bf16, token i's heads at k + i * ldk (elements,
+ * a multiple of 8, at least n_kv_heads * head_dim: slices of a fused projection are fine), to slot
+ * slots[i] (device int32; -1: the token is skipped; any other slot outside the cache is reported as
+ * TWELL_ERR_DEVICE_CHECK and skipped; two tokens with the same slot: either may win). An e4m3
+ * cache gets, per token and head, a = max(|values|, 2^-60), scale = a / 448 and the codes of
+ * value * (448 / a), rounded to nearest even. */
+TWELL_API twell_status twell_kv_append(const twell_kv_cache* cache, const void* k, const void* v, int64_t ldk,
+                             int64_t ldv, const int32_t* slots, int32_t n, int32_t* dev_status, void* stream);
+
+/* Reads n slots back: k_out, v_out bf16 [n, n_kv_heads, head_dim] (code * scale rounded once); rows of
+ * slots -1 are zeros, and so are those of slots outside the cache, which are reported as
+ * TWELL_ERR_DEVICE_CHECK. */
+TWELL_API twell_status twell_kv_gather(const twell_kv_cache* cache, const int32_t* slots, int32_t n, void* k_out,
+                             void* v_out, int32_t* dev_status, void* stream);
+
+/* Attention of one new token per sequence over the cache. For sequence b < B and query head i (key head
+ * i / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads): with len = seq_lens[b] and t over the
+ * visible tokens [max(0, len - window), len) (window 0: all of them),
+ *   out[b][i] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q[b][i] . k_t),  lse[b][i] = log sum_t p_t
+ * (natural logarithm, fp32; lse may be null). Nothing visible: out = 0, lse = -inf. Token t of sequence
+ * b is at offset t % page_size of page page_table[b * max_pages + t / page_size] (device int32; entries
+ * past the last visible token are not read). q bf16, sequence b's heads at q + b * q_stride (elements, a
+ * multiple of 8); out bf16 [B, n_q_heads, head_dim]. head_dim 64, 96, 128 or 256; B <= 4096. A length
+ * outside [0, max_pages * page_size] is clamped and reported as TWELL_ERR_DEVICE_CHECK; a page
+ * outside the cache is reported and its tokens do not count. Sums, maxima and the join of split sequences
+ * are fp32, in an order that depends on the lengths alone: the same out from call to call. ws:
+ * twell_workspace_bytes(TWELL_OP_PAGED_ATTN, B, head_dim, 1, 0, 0, 0) bytes; its contents need not be
+ * initialised, and two calls in flight at the same time must not share it. */
+TWELL_API twell_status twell_paged_attn_decode(const void* q, int64_t q_stride, const twell_kv_cache* cache,
+                                     const int32_t* page_table, const int32_t* seq_lens, int32_t B,
+                                     int32_t n_q_heads, int32_t max_pages, float scale, int32_t window, void* out,
+                                     float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* 4-bit weights W [n, k] with a bf16 scale per `group` columns (32, 64 or 128; k a multiple of 32 and of
+ * group): W[r][c] = scale[r][c / group] * (code - 8), code 0..15. Layout, n rounded up to 16 and k to 128
+ * (padding: codes 8, scales 0): words uint32 [ceil(n/16)][ceil(k/128)][8 g][4 c][2 half][4 j], a word
+ * holding row 16 tile + 8 half + g, columns 128 tile + 32 j + 8 c + (0..7), column 2i of the 8 in bits
+ * 4i..4i+3 and column 2i + 1 in bits 16+4i..19+4i; scales bf16 [ceil(n/16)][ceil(k/128)][8 g][2 half]
+ * [128/group]. Sizes in bytes (0 on invalid arguments): */
+TWELL_API size_t twell_w4_words_bytes(int32_t n, int32_t k);
+TWELL_API size_t twell_w4_scales_bytes(int32_t n, int32_t k, int32_t group);
+
+/* Quantises W [n, k] (bf16, row-major) into that layout: per group scale = bf16(max|w| / 7), code =
+ * clamp(round(w / scale), -8, 7) + 8 (ties to even). A weight that is not finite is reported as
+ * TWELL_ERR_DEVICE_CHECK. */
+TWELL_API twell_status twell_w4_quantize(const void* W, int32_t n, int32_t k, int32_t group, void* words,
+                               void* scales, int32_t* dev_status, void* stream);
+
+/* y [N, n] = x W^T for x [N, k] (bf16), 0 <= N <= 16 (else TWELL_ERR_UNSUPPORTED), W as above: x and the
+ * codes enter exactly, sums are fp32 in a fixed order, y is rounded once to bf16. */
+TWELL_API twell_status twell_w4_matvec(const void* x, const void* words, const void* scales, int32_t N, int32_t n,
+                             int32_t k, int32_t group, void* y, void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * Test exports. They run the same device code as the calls above on a gate matrix the caller
