@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 import threading
@@ -824,15 +825,22 @@ def twell_hybrid_route_noalloc(a: TwELL, K: int, ctx: Hybrid, stream=None) -> Hy
 
 # ------------------------------------------------------------------- the decoder layer around the FFN
 
-def _raw_stream(stream, device) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+# A decode step makes many calls whose kernels take a few microseconds, so these check and marshal with as
+# few operations as they can: integers for devices and streams, no objects made per call.
+
+_DTYPE_CODES = {torch.bfloat16: TWELL_BF16, torch.float32: TWELL_F32}
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _status_ptr(status, device) -> int:
+def _raw_stream(stream, index: int) -> int:
+    return _current_raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _status_ptr(status, index: int) -> int:
     if status is None:
-        status = _status_bufs.get(device.index)
+        status = _status_bufs.get(index)
         if status is None:
-            status = status_buffer(device)
+            status = status_buffer(torch.device("cuda", index))
     return status.data_ptr()
 
 
@@ -840,28 +848,44 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _need(t: torch.Tensor, shape, dtype, what: str, device=None) -> torch.Tensor:
-    """A contiguous tensor of that shape and type on that device, or ValueError."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not "
-                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    if t.device != device if device is not None else not t.is_cuda:
+def _index(t: torch.Tensor, what: str) -> int:
+    i = t.get_device()
+    if i < 0:
         raise ValueError(f"{what} is on {t.device}")
+    return i
+
+
+def _need(t: torch.Tensor, shape, dtype, what: str, index: int) -> torch.Tensor:
+    """A contiguous tensor of that shape and type on that CUDA device, or ValueError."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, not "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t
+
+
+def _code(dtype: torch.dtype) -> int:
+    c = _DTYPE_CODES.get(dtype)
+    return c if c is not None else _dtype_code(dtype)
 
 
 _layer_ws = {}
 
 
-def _stream_workspace(op: int, nbytes: int, device, stream, raw: int) -> torch.Tensor:
+@functools.lru_cache(maxsize=4096)
+def _layer_ws_bytes(op: int, N: int, d: int) -> int:
+    return int(load().twell_workspace_bytes(op, N, d, 1, 0, 0, 0))
+
+
+def _stream_workspace(op: int, N: int, d: int, index: int, stream, raw: int) -> torch.Tensor:
     """A workspace per operator, device and stream, grown on demand: calls on one stream run one after
     the other, so they can share it. It is allocated on that stream, so that an outgrown one is not
     handed out again before the calls that use it are done."""
-    key = (op, device.index, raw)
+    nbytes = _layer_ws_bytes(op, N, d)
+    key = (op, index, raw)
     ws = _layer_ws.get(key)
     if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(index)):
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=torch.device("cuda", index))
         _layer_ws[key] = ws
     return ws
 
@@ -883,31 +907,32 @@ class Rows8:
 
 
 def _rmsnorm_fwd(x, w, res, eps, h, y, y8, rstd, stream):
-    N, d = x.shape
-    dev = x.device
-    _need(x, (N, d), x.dtype, "x")
-    _need(w, (d,), x.dtype, "w", dev)
-    rt = x.dtype
+    dev = _index(x, "x")
+    dt = rt = x.dtype
+    shape = x.shape
+    N, d = shape
+    _need(x, shape, dt, "x", dev)
+    _need(w, (d,), dt, "w", dev)
     if res is not None:
         rt = res.dtype
-        _need(res, (N, d), rt, "res", dev)
-        h = _need(h, (N, d), rt, "h", dev) if h is not None else torch.empty_like(res)
+        _need(res, shape, rt, "res", dev)
+        h = torch.empty_like(res) if h is None else _need(h, shape, rt, "h", dev)
     elif h is not None:
         raise ValueError("h is the sum x + res: without res it is x")
     if rstd is not None:
         _need(rstd, (N,), torch.float32, "rstd", dev)
     if y is not None:
-        _need(y, (N, d), x.dtype, "y", dev)
+        _need(y, shape, dt, "y", dev)
     q = sc = None
     group = 0
     if y8 is not None:
         group = y8.group
-        q = _need(y8.values, (N, d), torch.float8_e4m3fn, "the 8-bit rows", dev)
-        sc = _need(y8.scale, (N, -(-d // group) if group else 1), torch.float32, "the 8-bit rows' scale", dev)
-    _check(load().twell_add_rmsnorm_fwd(x.data_ptr(), _p(res), w.data_ptr(), N, d, eps, _dtype_code(x.dtype),
-                                        _dtype_code(rt), _p(h), _p(y), _p(q), _p(sc), group, _p(rstd),
-                                        _raw_stream(stream, dev)),
-           "twell_add_rmsnorm_fwd")
+        q = _need(y8.values, shape, torch.float8_e4m3fn, "the 8-bit rows", dev).data_ptr()
+        sc = _need(y8.scale, (N, -(-d // group) if group else 1), torch.float32, "the 8-bit rows' scale", dev).data_ptr()
+    code = (_lib or load()).twell_add_rmsnorm_fwd(x.data_ptr(), _p(res), w.data_ptr(), N, d, eps, _code(dt), _code(rt),
+                                                  _p(h), _p(y), q, sc, group, _p(rstd), _raw_stream(stream, dev))
+    if code:
+        _check(code, "twell_add_rmsnorm_fwd")
     return h
 
 
@@ -945,25 +970,26 @@ def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rs
     """Gradients of the call above from its h (x where it had no res) and rstd: returns (dx, dw), dx the
     gradient of x and of res alike, dw fp32. dy, dh (the gradient that reaches h from the residual
     stream, or None) and dx share a type, bf16 or fp32."""
-    N, d = h.shape
-    dev = h.device
-    _need(h, (N, d), h.dtype, "h")
-    _need(dy, (N, d), dy.dtype, "dy", dev)
+    dev = _index(h, "h")
+    shape = h.shape
+    N, d = shape
+    gt = dy.dtype
+    _need(h, shape, h.dtype, "h", dev)
+    _need(dy, shape, gt, "dy", dev)
     _need(w, (d,), w.dtype, "w", dev)
     _need(rstd, (N,), torch.float32, "rstd", dev)
     if dh is not None:
-        _need(dh, (N, d), dy.dtype, "dh", dev)
-    dx = _need(dx, (N, d), dy.dtype, "dx", dev) if dx is not None else torch.empty_like(dy)
-    dw = _need(dw, (d,), torch.float32, "dw", dev) if dw is not None else torch.empty((d,), dtype=torch.float32, device=dev)
+        _need(dh, shape, gt, "dh", dev)
+    dx = torch.empty_like(dy) if dx is None else _need(dx, shape, gt, "dx", dev)
+    dw = torch.empty((d,), dtype=torch.float32, device=h.device) if dw is None else _need(dw, (d,), torch.float32, "dw", dev)
     s = _raw_stream(stream, dev)
-    lib = load()
     if ws is None:
-        ws = _stream_workspace(OP_ADD_RMSNORM_BWD, lib.twell_workspace_bytes(OP_ADD_RMSNORM_BWD, N, d, 1, 0, 0, 0), dev,
-                               stream, s)
-    _check(lib.twell_add_rmsnorm_bwd(dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dh), N, d,
-                                     _dtype_code(w.dtype), _dtype_code(h.dtype), _dtype_code(dy.dtype), dx.data_ptr(),
-                                     dw.data_ptr(), ws.data_ptr(), ws.numel(), s),
-           "twell_add_rmsnorm_bwd")
+        ws = _stream_workspace(OP_ADD_RMSNORM_BWD, N, d, dev, stream, s)
+    code = (_lib or load()).twell_add_rmsnorm_bwd(dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dh), N, d,
+                                                  _code(w.dtype), _code(h.dtype), _code(gt), dx.data_ptr(), dw.data_ptr(),
+                                                  ws.data_ptr(), ws.numel(), s)
+    if code:
+        _check(code, "twell_add_rmsnorm_bwd")
     return dx, dw
 
 
@@ -995,7 +1021,8 @@ class KVCache:
             raise ValueError("a bf16 cache has no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
+        self._inner = (self.head_dim, 1)
         # a page of one token has no token stride of its own
         ts = k.stride(2) if self.page_size > 1 else self.head_dim
         self._c = _KVCache(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
@@ -1015,39 +1042,39 @@ class KVCache:
                                for _ in range(2)))
 
 
-def _slots(slots: torch.Tensor, device) -> torch.Tensor:
-    if slots.dim() != 1:
-        raise ValueError("slots must be one int32 per token")
-    return _need(slots, slots.shape, torch.int32, "slots", device)
-
-
 def twell_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, status=None,
                     stream=None) -> None:
     """Write n tokens' keys and values (bf16 [n, n_kv_heads, head_dim]; any token stride, heads
     contiguous) to their slots (int32 [n], -1 = skip), quantised where the cache is in e4m3."""
-    n = _slots(slots, cache.device).numel()
-    shape, inner = (n, cache.n_kv_heads, cache.head_dim), (cache.head_dim, 1)
+    n = slots.numel()
+    dev = cache.index
+    _need(slots, (n,), torch.int32, "slots", dev)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    lk = lv = shape[1] * shape[2]
     for t, what in ((k, "k"), (v, "v")):
-        if t.shape != shape or t.dtype != torch.bfloat16 or t.device != cache.device or (n and t.stride()[1:] != inner):
+        if t.shape != shape or t.dtype != torch.bfloat16 or t.get_device() != dev or (n and t.stride()[1:] != cache._inner):
             raise ValueError(f"{what} must be bf16 {shape} on {cache.device} with contiguous heads")
-    row = cache.n_kv_heads * cache.head_dim
-    _check(load().twell_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else row,
-                                  v.stride(0) if n > 1 else row, slots.data_ptr(), n, _status_ptr(status, cache.device),
-                                  _raw_stream(stream, cache.device)),
-           "twell_kv_append")
+    if n > 1:
+        lk, lv = k.stride(0), v.stride(0)
+    code = (_lib or load()).twell_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), lk, lv, slots.data_ptr(), n,
+                                            _status_ptr(status, dev), _raw_stream(stream, dev))
+    if code:
+        _check(code, "twell_kv_append")
 
 
 def twell_kv_gather(cache: KVCache, slots: torch.Tensor, k_out: Optional[torch.Tensor] = None,
                     v_out: Optional[torch.Tensor] = None, status=None, stream=None):
     """Read slots back: (k, v), bf16 [n, n_kv_heads, head_dim]; zeros for slot -1."""
-    n = _slots(slots, cache.device).numel()
+    n = slots.numel()
+    dev = cache.index
+    _need(slots, (n,), torch.int32, "slots", dev)
     shape = (n, cache.n_kv_heads, cache.head_dim)
-    k_out, v_out = (_need(t, shape, torch.bfloat16, what, cache.device) if t is not None else
-                    torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-                    for t, what in ((k_out, "k_out"), (v_out, "v_out")))
-    _check(load().twell_kv_gather(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
-                                  _status_ptr(status, cache.device), _raw_stream(stream, cache.device)),
-           "twell_kv_gather")
+    k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if t is None else
+                    _need(t, shape, torch.bfloat16, what, dev) for t, what in ((k_out, "k_out"), (v_out, "v_out")))
+    code = (_lib or load()).twell_kv_gather(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                                            _status_ptr(status, dev), _raw_stream(stream, dev))
+    if code:
+        _check(code, "twell_kv_gather")
     return k_out, v_out
 
 
@@ -1062,28 +1089,31 @@ def twell_paged_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.T
     1/sqrt(head_dim) unless given; window > 0 keeps the last `window` tokens. out bf16, written; lse fp32
     [B, n_q_heads] (natural logarithm of the sum of exponentials) is written when a buffer is given. A
     sequence of length 0 gives zeros and -inf."""
-    dev = cache.device
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != dev or q.shape[2] != cache.head_dim or \
-            (q.numel() and q.stride()[1:] != (cache.head_dim, 1)):
-        raise ValueError(f"q must be bf16 [B, n_q_heads, {cache.head_dim}] on {dev} with contiguous heads")
-    B, n_q, hd = q.shape
+    dev = cache.index
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or q.dtype != torch.bfloat16 or q.get_device() != dev or \
+            (q.numel() and q.stride()[1:] != cache._inner):
+        raise ValueError(f"q must be bf16 [B, n_q_heads, {cache.head_dim}] on {cache.device} with contiguous heads")
+    B, n_q, hd = shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be int32 [B, max_pages]")
-    _need(page_table, (B, page_table.shape[1]), torch.int32, "page_table", dev)
+    pages = page_table.shape[1]
+    _need(page_table, (B, pages), torch.int32, "page_table", dev)
     _need(seq_lens, (B,), torch.int32, "seq_lens", dev)
-    out = _need(out, (B, n_q, hd), torch.bfloat16, "out", dev) if out is not None else \
-        torch.empty((B, n_q, hd), dtype=torch.bfloat16, device=dev)
+    out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if out is None else \
+        _need(out, shape, torch.bfloat16, "out", dev)
     if lse is not None:
         _need(lse, (B, n_q), torch.float32, "lse", dev)
     s = _raw_stream(stream, dev)
-    lib = load()
     if ws is None:
-        ws = _stream_workspace(OP_PAGED_ATTN, lib.twell_workspace_bytes(OP_PAGED_ATTN, B, hd, 1, 0, 0, 0), dev, stream, s)
-    _check(lib.twell_paged_attn_decode(q.data_ptr(), q.stride(0) if B > 1 else n_q * hd, cache._ref,
-                                       page_table.data_ptr(), seq_lens.data_ptr(), B, n_q, page_table.shape[1],
-                                       scale if scale is not None else 1.0 / math.sqrt(hd), window, out.data_ptr(),
-                                       _p(lse), ws.data_ptr(), ws.numel(), _status_ptr(status, dev), s),
-           "twell_paged_attn_decode")
+        ws = _stream_workspace(OP_PAGED_ATTN, B, hd, dev, stream, s)
+    code = (_lib or load()).twell_paged_attn_decode(q.data_ptr(), q.stride(0) if B > 1 else n_q * hd, cache._ref,
+                                                    page_table.data_ptr(), seq_lens.data_ptr(), B, n_q, pages,
+                                                    1.0 / math.sqrt(hd) if scale is None else scale, window,
+                                                    out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(),
+                                                    _status_ptr(status, dev), s)
+    if code:
+        _check(code, "twell_paged_attn_decode")
     return out, lse
 
 
@@ -1101,8 +1131,9 @@ class W4Weights:
         if self.group not in (32, 64, 128) or self.n <= 0 or self.k <= 0 or self.k % 32 or self.k % self.group:
             raise ValueError("W4Weights: group 32, 64 or 128, k a multiple of 32 and of group")
         tiles = (-(-self.n // 16), -(-self.k // 128))
-        _need(self.words, tiles + (8, 4, 2, 4), torch.int32, "words")
-        _need(self.scales, tiles + (8, 2, 128 // self.group), torch.bfloat16, "scales", self.words.device)
+        self.index = _index(self.words, "words")
+        _need(self.words, tiles + (8, 4, 2, 4), torch.int32, "words", self.index)
+        _need(self.scales, tiles + (8, 2, 128 // self.group), torch.bfloat16, "scales", self.index)
 
     def dequantize(self) -> torch.Tensor:
         """The fp32 weights [n, k] that the codes stand for (a check, not a fast path)."""
@@ -1120,7 +1151,8 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
     if W.dim() != 2:
         raise ValueError("W must be a 2-D bf16 tensor")
     n, k = W.shape
-    _need(W, (n, k), torch.bfloat16, "W")
+    dev = _index(W, "W")
+    _need(W, (n, k), torch.bfloat16, "W", dev)
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     nt, kt = -(-n // 16), -(-k // 128)
@@ -1128,7 +1160,7 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
     scales = torch.empty((nt, kt, 8, 2, 128 // group), dtype=torch.bfloat16, device=W.device)
     out = W4Weights(words, scales, n, k, group)
     _check(load().twell_w4_quantize(W.data_ptr(), n, k, group, words.data_ptr(), scales.data_ptr(),
-                                    _status_ptr(status, W.device), _raw_stream(stream, W.device)),
+                                    _status_ptr(status, dev), _raw_stream(stream, dev)),
            "twell_w4_quantize")
     return out
 
@@ -1136,11 +1168,12 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
 def twell_w4_matvec(x: torch.Tensor, W: W4Weights, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T (bf16) for at most DECODE_MAX_N tokens and 4-bit weights."""
     N = x.shape[0]
-    dev = x.device
-    _need(x, (N, W.k), torch.bfloat16, "x", W.words.device)
-    y = _need(y, (N, W.n), torch.bfloat16, "y", dev) if y is not None else \
-        torch.empty((N, W.n), dtype=torch.bfloat16, device=dev)
-    _check(load().twell_w4_matvec(x.data_ptr(), W.words.data_ptr(), W.scales.data_ptr(), N, W.n, W.k, W.group,
-                                  y.data_ptr(), _raw_stream(stream, dev)),
-           "twell_w4_matvec")
+    dev = W.index
+    _need(x, (N, W.k), torch.bfloat16, "x", dev)
+    y = torch.empty((N, W.n), dtype=torch.bfloat16, device=x.device) if y is None else \
+        _need(y, (N, W.n), torch.bfloat16, "y", dev)
+    code = (_lib or load()).twell_w4_matvec(x.data_ptr(), W.words.data_ptr(), W.scales.data_ptr(), N, W.n, W.k, W.group,
+                                            y.data_ptr(), _raw_stream(stream, dev))
+    if code:
+        _check(code, "twell_w4_matvec")
     return y

@@ -4,12 +4,12 @@
 //
 // What bounds it is the cache: every visible key and value is read once for all the query heads
 // that share it, 2 x heads per key flops a byte, so the kernel is laid out to keep reads in flight.
-//   - Split over the length. The work is the list of 16-token tiles of every (sequence, key head), in
+//   - Split over the length. The work is the list of 32-token tiles of every (sequence, key head), in
 //     that order, cut into equal contiguous ranges, one a warp of a grid of one block an SM: a batch
 //     of ragged lengths and a single long sequence are balanced alike, and no range is empty of work
-//     while another is long. A warp streams its tiles through its own shared-memory ring with
-//     16-byte asynchronous copies (rows beyond the visible range are filled with zeros and never
-//     read), across sequence boundaries, so that the ring stays full.
+//     while another is long. A warp streams its tiles, keys and values in turn, through its own
+//     shared-memory ring with 16-byte asynchronous copies (rows beyond the visible range are filled
+//     with zeros and never read), across sequence boundaries, so that the ring stays full.
 //   - The products are small matrix products with the tokens (for q . k) and the dimensions (for the
 //     output) on the 16-row side of mma.sync m16n8k16 and the query heads on its 8 columns: a
 //     group of up to 8 query heads costs what one does. tcgen05's 64 to 128 rows a tile would be
@@ -17,14 +17,16 @@
 //     the products. The scores' fragment becomes the second product's operand by an 8x8 transpose
 //     (movmatrix); with a bf16 cache the weights go in as hi + lo bf16 parts (~16 bits), with an
 //     e4m3 cache as fp16 (11 bits).
+//   - A batch whose (sequence, key head)s are no more than the SMs and short (at most kPairTiles tiles a warp by
+//     the page table's width) skips the list: one block each, which needs no second kernel.
 //   - Running maximum m and sum l in fp32, per query head. For an e4m3 cache the value's scale s_t is
 //     folded into the weight, w_t = p_t s_t, and m runs over score + log2 s_t, so that the fp16
 //     weights stay in (0, 1] whatever the scales. The query is brought to [1, 2) by a power of two
 //     before its fp16 rounding (exact for bf16 values down to 2^-14 of the largest).
-//   - Joining. A (sequence, key head) that lies within one warp's range is finished there. Otherwise
-//     each part leaves (m, l, unnormalised o) in fp32 in the workspace; a block whose whole range lies
-//     in one (sequence, key head) first joins its warps' parts in shared memory, and a second kernel
-//     joins what is left, in ascending order: the result does not depend on scheduling.
+//   - Joining. A (sequence, key head) that lies within one warp's range is finished there. The parts
+//     (m, l, unnormalised o, fp32) of one that spans warps of a block are joined by the block, through
+//     shared memory; one that spans blocks leaves a part a block in the workspace, and a second kernel
+//     joins those. Parts are joined in ascending order: the result does not depend on scheduling.
 #include "twell_kv.cuh"
 #include "twell_mma.cuh"
 #include "twell_ops.cuh"
@@ -32,10 +34,12 @@
 namespace twell {
 namespace {
 
-constexpr int kTileTokens = 16;
+constexpr int kTileTokens = 32;
+constexpr int kMTiles = kTileTokens / 16;  // 16-token rows of a product
 constexpr int kAttnMaxSeqs = 4096;
-constexpr int kAttnMaxSms = 160;    // the workspace is sized for this many blocks, whatever the device
-constexpr int kAttnMaxWarps = 16;   // and this many warps a block
+constexpr int kAttnMaxSms = 160;   // the workspace is sized for this many blocks, whatever the device
+constexpr int kAttnMaxWarps = 16;  // and this many warps a block
+constexpr int kPairTiles = 1;      // see "pairs" in run_attn
 constexpr float kNegInf = -INFINITY;
 
 // HD: head_dim; Q8: e4m3 cache; NT: query heads of one key head handled together, in eights.
@@ -44,16 +48,18 @@ struct AttnCfg {
     static constexpr int kRow = HD * (Q8 ? 1 : 2);      // bytes of a token's key or value
     static constexpr int kChunks = kRow / 16;
     static constexpr int kSwizzle = kChunks % 8 == 0 ? 7 : (kChunks % 4 == 0 ? 3 : 1);
-    static constexpr int kHalf = kTileTokens * kRow;    // bytes of a tile's keys (then its values)
-    static constexpr int kStage = 2 * kHalf + (Q8 ? 2 * kTileTokens * 4 : 0);
+    static constexpr int kHalf = kTileTokens * kRow;    // bytes of a tile's keys, or its values
+    static constexpr int kSlot = kHalf + (Q8 ? 2 * kTileTokens * 4 : 0);  // with keys: both scales behind them
     static constexpr int kWarps = HD == 256 ? (Q8 ? 8 : 4) : ((Q8 || HD == 64) && NT == 1 ? 16 : 8);
-    static constexpr int kStages = std::min(8, 204800 / (kWarps * kStage));
+    static constexpr int kFit = 212000 / (kWarps * kSlot);
+    static constexpr int kSlots = kFit >= 7 ? 7 : kFit >= 5 ? 5 : 3;  // odd: keys are requested while keys are used
+    static_assert(kFit >= 3, "the ring overlaps copies with the products");
     static constexpr int kMt = HD / 16;                 // 16-dimension tiles of the output
-    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kRing = kSlots * kSlot;        // bytes of a warp's ring
     static constexpr int kPartF = NT * kMt * 128;       // floats of a part's o, then NT * 16 of m and l
     static constexpr int kPart = kPartF + NT * 16;
-    static constexpr int kJoin = kWarps * kPart * 4;    // the block's join, in the ring's place
-    static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin);
+    static constexpr int kSmem = kWarps * kRing;
+    static_assert(kPart * 4 <= kRing, "a warp leaves its last part in its ring");
 };
 
 struct AttnArgs {
@@ -67,10 +73,12 @@ struct AttnArgs {
     int64_t q_stride;      // elements between two sequences' queries
     int B, n_q, G, blocks; // blocks: groups of 8 NT query heads per key head
     int max_pages, window;
+    int pairs;             // 1: one block a (sequence, key head)
     float scale_log2;      // scale * log2(e)
-    uint32_t* prefix;      // [B + 1] tiles before each sequence, of one key head
-    int* desc;             // [workers] the (sequence, key head) that a worker's start is the first to split, or -1
-    float* part;           // [2 * workers][kPart]
+    int2* split;           // [blocks] the (sequence, key head) that a block's start is the first to split, or -1,
+                           // and the last block that holds some of it
+    float* block_part;     // [2 * blocks][kPart] 0: of a (sequence, key head) from an earlier block, 1: into a later
+    float* head_part;      // [workers][kPart] a warp's part of a (sequence, key head) that ends inside its range
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid)
@@ -125,8 +133,6 @@ __device__ __forceinline__ float exp2_approx(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t f16_pack(float lo, float hi) { return f16x2_rn(lo, hi); }
-
 // The visible tokens of a sequence, [first, len), and its tiles, counted from the tile of `first`.
 struct SeqSpan {
     int len, first, tile0, tiles;
@@ -148,21 +154,24 @@ struct Cursor {
     {
         s = SeqSpan(__ldg(a.lens + b), a.max_pages << a.c.page_shift, a.window);
     }
-    // item < total: the place of the item-th tile
-    __device__ __forceinline__ void seek(const AttnArgs& a, const uint32_t* prefix, int HV, long long item)
+    // item < total: the place of the item-th tile; returns the first tile of its (sequence, key head)
+    __device__ __forceinline__ long long seek(const AttnArgs& a, const uint32_t* prefix, int HV, long long item)
     {
-        int lo = 0, hi = a.B;  // prefix[lo] * HV <= item < prefix[hi] * HV
+        // its tile among those of one key head, were the heads of a sequence taken together
+        const uint32_t at = (item >> 32) == 0 ? static_cast<uint32_t>(item) / HV : static_cast<uint32_t>(item / HV);
+        int lo = 0, hi = a.B;  // prefix[lo] <= at < prefix[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (static_cast<long long>(prefix[mid]) * HV <= item) lo = mid;
+            if (prefix[mid] <= at) lo = mid;
             else hi = mid;
         }
         b = lo;
         const uint32_t n = prefix[b + 1] - prefix[b];
         const long long rem = item - static_cast<long long>(prefix[b]) * HV;
-        hv = static_cast<int>(rem / n);
+        hv = (rem >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(rem) / n) : static_cast<int>(rem / n);
         tile = static_cast<int>(rem - static_cast<long long>(hv) * n);
         load(a);
+        return item - tile;
     }
     __device__ __forceinline__ void next(const AttnArgs& a, int HV)
     {
@@ -177,22 +186,27 @@ struct Cursor {
     }
 };
 
-// The list of `total` tiles cut into equal ranges: range w of W starts at total * w / W, formed from the
-// quotient and the remainder of total / W so that each start costs a 32-bit division. Few tiles use
-// fewer blocks, one tile a warp.
+// The list of `total` tiles cut into W equal ranges, one a warp of as many blocks as that takes (fewer
+// tiles than warps: one each). Range w starts at total * w / W, formed from the quotient and the
+// remainder of total / W so that each start costs a 32-bit division.
 struct Ranges {
     long long quot;
     uint32_t rem, W;
     int blocks;
+    __device__ __forceinline__ Ranges() : quot(0), rem(0), W(1), blocks(1) {}
     __device__ __forceinline__ Ranges(long long total, int max_blocks, int warps)
     {
-        const long long need = (total + warps - 1) / warps;
-        blocks = static_cast<int>(need < 1 ? 1 : (need < max_blocks ? need : max_blocks));
-        W = static_cast<uint32_t>(blocks * warps);
-        quot = total / W;
+        const uint32_t most = static_cast<uint32_t>(max_blocks * warps);
+        W = total >= most ? most : (total > 1 ? static_cast<uint32_t>(total) : 1u);
+        blocks = static_cast<int>((W + warps - 1) / warps);
+        quot = (total >> 32) == 0 ? static_cast<uint32_t>(total) / W : total / W;
         rem = static_cast<uint32_t>(total - quot * W);
     }
-    __device__ __forceinline__ long long start(uint32_t w) const { return quot * w + rem * w / W; }
+    __device__ __forceinline__ long long start(uint32_t w) const
+    {
+        w = min(w, W);
+        return quot * w + rem * w / W;
+    }
 };
 
 // Physical 16-byte chunk of a tile's row: spread so that the rows that are read together by the
@@ -224,6 +238,7 @@ struct AttnState {
         }
     }
 
+    // The query's fragments, as bf16: requested here, brought into their final form by finish_q.
     __device__ __forceinline__ void load_q(const AttnArgs& a, int b, int hv, int lane)
     {
         const int g = lane >> 2, c = lane & 3;
@@ -239,96 +254,124 @@ struct AttnState {
                     q[n][2 * i] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 2 * c)) : 0u;
                     q[n][2 * i + 1] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 8 + 2 * c)) : 0u;
                 }
-                qs[n][0] = qs[n][1] = a.scale_log2;
             } else {
-                uint32_t raw[kQ];
-                float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kQ / 8; ++i) {
                     const bool on = live && 4 * i + c < HD / 16;
-                    const uint32_t* p = reinterpret_cast<const uint32_t*>(src + 64 * i + 16 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        raw[8 * i + e] = on ? __ldg(p + e) : 0u;
-                        const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[8 * i + e]));
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
+                    const uint4* p = reinterpret_cast<const uint4*>(src + 64 * i + 16 * c);
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u), u = on ? __ldg(p) : zero, v = on ? __ldg(p + 1) : zero;
+                    q[n][8 * i] = u.x, q[n][8 * i + 1] = u.y, q[n][8 * i + 2] = u.z, q[n][8 * i + 3] = u.w;
+                    q[n][8 * i + 4] = v.x, q[n][8 * i + 5] = v.y, q[n][8 * i + 6] = v.z, q[n][8 * i + 7] = v.w;
                 }
+            }
+        }
+    }
+    __device__ __forceinline__ void finish_q(const AttnArgs& a, int lane)
+    {
+        const int c = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            qs[n][0] = qs[n][1] = a.scale_log2;
+            if constexpr (Q8) {
+                // the largest magnitude, as bf16 bits, over the head's four lanes; its power of two taken out
+                __nv_bfloat162 m2 = __float2bfloat162_rn(0.0f);
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    const uint32_t u = q[n][i] & 0x7fff7fffu;
+                    m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162*>(&u));
+                }
+                float top = fmaxf(__low2float(m2), __high2float(m2));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
                 const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
 #pragma unroll
                 for (int i = 0; i < kQ; ++i) {
-                    const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[i]));
+                    const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&q[n][i]));
                     q[n][i] = f16x2_rn(f.x * down, f.y * down);
                 }
-                qs[n][0] = __shfl_sync(0xffffffffu, up, 8 * c) * a.scale_log2;
-                qs[n][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4) * a.scale_log2;
+                qs[n][0] *= __shfl_sync(0xffffffffu, up, 8 * c);
+                qs[n][1] *= __shfl_sync(0xffffffffu, up, 8 * c + 4);
             }
         }
     }
 
-    // One tile: its keys at `st`, its values C::kHalf behind, its scales behind those; bit t of `vis` says
-    // whether token t of the 16 is visible.
-    __device__ __forceinline__ void tile(uint32_t st, uint32_t vis, int lane)
+    // The weights of a tile's tokens from its keys at `st` (and both scales behind them), as fragments of the
+    // second product; bit t of `vis` says whether token t is visible.
+    uint32_t ph[kMTiles][NT][2], pl[kMTiles][NT][2];
+    __device__ __forceinline__ void scores(uint32_t st, uint32_t vis, int lane)
     {
         const int g = lane >> 2, c = lane & 3;
-        float sc[NT][4];
+        float x[kMTiles][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+        for (int t = 0; t < kMTiles; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[t][n][0] = x[t][n][1] = x[t][n][2] = x[t][n][3] = 0.0f;
         if constexpr (!Q8) {
             const int row = lane & 15, hi8 = lane >> 4;
 #pragma unroll
-            for (int i = 0; i < HD / 16; ++i) {
-                uint32_t k[4];
-                ldsm_x4(k, st + row * C::kRow + swizzled<C>(row, 2 * i + hi8, false) * 16);
+            for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(sc[n], k[0], k[1], k[2], k[3], q[n][2 * i], q[n][2 * i + 1]);
-            }
+                for (int t = 0; t < kMTiles; ++t) {
+                    uint32_t k[4];
+                    ldsm_x4(k, st + (16 * t + row) * C::kRow + swizzled<C>(row, 2 * i + hi8, false) * 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_bf16(x[t][n], k[0], k[1], k[2], k[3], q[n][2 * i], q[n][2 * i + 1]);
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < kQ / 8; ++i) {
-                uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0;
-                if (HD % 64 == 0 || 4 * i + c < HD / 16) {
-                    k0 = lds128(st + g * C::kRow + swizzled<C>(g, 4 * i + c, true) * 16);
-                    k1 = lds128(st + (g + 8) * C::kRow + swizzled<C>(g + 8, 4 * i + c, true) * 16);
-                }
+            for (int i = 0; i < kQ / 8; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w0 = e == 0 ? k0.x : e == 1 ? k0.y : e == 2 ? k0.z : k0.w;
-                    const uint32_t w1 = e == 0 ? k1.x : e == 1 ? k1.y : e == 2 ? k1.z : k1.w;
-                    const uint32_t a0 = e4m3x2_f16x2(static_cast<uint16_t>(w0)), a1 = e4m3x2_f16x2(static_cast<uint16_t>(w1));
-                    const uint32_t a2 = e4m3x2_f16x2(static_cast<uint16_t>(w0 >> 16)),
-                                   a3 = e4m3x2_f16x2(static_cast<uint16_t>(w1 >> 16));
+                for (int t = 0; t < kMTiles; ++t) {
+                    uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0;
+                    if (HD % 64 == 0 || 4 * i + c < HD / 16) {
+                        k0 = lds128(st + (16 * t + g) * C::kRow + swizzled<C>(g, 4 * i + c, true) * 16);
+                        k1 = lds128(st + (16 * t + g + 8) * C::kRow + swizzled<C>(g, 4 * i + c, true) * 16);
+                    }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16(sc[n], a0, a1, a2, a3, q[n][8 * i + 2 * e], q[n][8 * i + 2 * e + 1]);
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t w0 = e == 0 ? k0.x : e == 1 ? k0.y : e == 2 ? k0.z : k0.w;
+                        const uint32_t w1 = e == 0 ? k1.x : e == 1 ? k1.y : e == 2 ? k1.z : k1.w;
+                        const uint32_t a0 = e4m3x2_f16x2(static_cast<uint16_t>(w0)), a1 = e4m3x2_f16x2(static_cast<uint16_t>(w1));
+                        const uint32_t a2 = e4m3x2_f16x2(static_cast<uint16_t>(w0 >> 16)),
+                                       a3 = e4m3x2_f16x2(static_cast<uint16_t>(w1 >> 16));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(x[t][n], a0, a1, a2, a3, q[n][8 * i + 2 * e], q[n][8 * i + 2 * e + 1]);
+                    }
                 }
-            }
         }
 
-        // scores (base 2) of tokens g and g + 8 for heads 2c and 2c + 1; weights
-        const bool on0 = (vis >> g) & 1u, on1 = (vis >> (g + 8)) & 1u;
-        float ks0 = 1.0f, ks1 = 1.0f, vs0 = 1.0f, vs1 = 1.0f, lv0 = 0.0f, lv1 = 0.0f;
-        if constexpr (Q8) {
-            const uint32_t sp = st + 2 * C::kHalf;
-            ks0 = __uint_as_float(lds32(sp + 4 * g));
-            ks1 = __uint_as_float(lds32(sp + 4 * (g + 8)));
-            vs0 = __uint_as_float(lds32(sp + 64 + 4 * g));
-            vs1 = __uint_as_float(lds32(sp + 64 + 4 * (g + 8)));
-            lv0 = __log2f(fmaxf(vs0, kAmaxMin));
-            lv1 = __log2f(fmaxf(vs1, kAmaxMin));
-        }
-        uint32_t ph[NT][2], pl[NT][2];
+        // scores (base 2) of tokens 16t + g and 16t + g + 8 for heads 2c and 2c + 1
+        float vs[kMTiles][2], lv[kMTiles][2];
+#pragma unroll
+        for (int t = 0; t < kMTiles; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int tok = 16 * t + 8 * h + g;
+                const bool on = (vis >> tok) & 1u;
+                float ks = 1.0f;
+                vs[t][h] = 1.0f;
+                lv[t][h] = 0.0f;
+                if constexpr (Q8) {
+                    ks = __uint_as_float(lds32(st + C::kHalf + 4 * tok));
+                    vs[t][h] = __uint_as_float(lds32(st + C::kHalf + 4 * kTileTokens + 4 * tok));
+                    lv[t][h] = __log2f(fmaxf(vs[t][h], kAmaxMin));
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    x[t][n][2 * h] = on ? fmaf(x[t][n][2 * h], qs[n][0] * ks, lv[t][h]) : kNegInf;
+                    x[t][n][2 * h + 1] = on ? fmaf(x[t][n][2 * h + 1], qs[n][1] * ks, lv[t][h]) : kNegInf;
+                }
+            }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float x[4];
-            x[0] = on0 ? fmaf(sc[n][0], qs[n][0] * ks0, lv0) : kNegInf;
-            x[1] = on0 ? fmaf(sc[n][1], qs[n][1] * ks0, lv0) : kNegInf;
-            x[2] = on1 ? fmaf(sc[n][2], qs[n][0] * ks1, lv1) : kNegInf;
-            x[3] = on1 ? fmaf(sc[n][3], qs[n][1] * ks1, lv1) : kNegInf;
-            float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
+            float t0 = kNegInf, t1 = kNegInf;
+#pragma unroll
+            for (int t = 0; t < kMTiles; ++t) {
+                t0 = fmaxf(t0, fmaxf(x[t][n][0], x[t][n][2]));
+                t1 = fmaxf(t1, fmaxf(x[t][n][1], x[t][n][3]));
+            }
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) {
                 t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, s));
@@ -351,77 +394,90 @@ struct AttnState {
                 }
             }
             const float b0 = m[n][0] == kNegInf ? 0.0f : m[n][0], b1 = m[n][1] == kNegInf ? 0.0f : m[n][1];
-            float p[4];
-            p[0] = exp2_approx(x[0] - lv0 - b0);
-            p[1] = exp2_approx(x[1] - lv0 - b1);
-            p[2] = exp2_approx(x[2] - lv1 - b0);
-            p[3] = exp2_approx(x[3] - lv1 - b1);
-            l[n][0] += p[0] + p[2];
-            l[n][1] += p[1] + p[3];
-            if constexpr (Q8) {
-                ph[n][0] = transpose8(f16_pack(p[0] * vs0, p[1] * vs0));
-                ph[n][1] = transpose8(f16_pack(p[2] * vs1, p[3] * vs1));
-            } else {
-                const uint32_t h0 = bf16x2_rn(p[0], p[1]), h1 = bf16x2_rn(p[2], p[3]);
-                const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
-                const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h1));
-                ph[n][0] = transpose8(h0);
-                ph[n][1] = transpose8(h1);
-                pl[n][0] = transpose8(bf16x2_rn(p[0] - r0.x, p[1] - r0.y));
-                pl[n][1] = transpose8(bf16x2_rn(p[2] - r1.x, p[3] - r1.y));
+#pragma unroll
+            for (int t = 0; t < kMTiles; ++t) {
+                float p[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    p[2 * h] = exp2_approx(x[t][n][2 * h] - lv[t][h] - b0);
+                    p[2 * h + 1] = exp2_approx(x[t][n][2 * h + 1] - lv[t][h] - b1);
+                }
+                l[n][0] += p[0] + p[2];
+                l[n][1] += p[1] + p[3];
+                if constexpr (Q8) {
+                    ph[t][n][0] = transpose8(f16x2_rn(p[0] * vs[t][0], p[1] * vs[t][0]));
+                    ph[t][n][1] = transpose8(f16x2_rn(p[2] * vs[t][1], p[3] * vs[t][1]));
+                } else {
+                    const uint32_t h0 = bf16x2_rn(p[0], p[1]), h1 = bf16x2_rn(p[2], p[3]);
+                    const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
+                    const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h1));
+                    ph[t][n][0] = transpose8(h0);
+                    ph[t][n][1] = transpose8(h1);
+                    pl[t][n][0] = transpose8(bf16x2_rn(p[0] - r0.x, p[1] - r0.y));
+                    pl[t][n][1] = transpose8(bf16x2_rn(p[2] - r1.x, p[3] - r1.y));
+                }
             }
         }
+    }
 
-        // o += v^T p: dimensions on the rows
-        const uint32_t sv = st + C::kHalf;
+    // o += v^T p from the tile's values at `sv`: dimensions on the rows
+    __device__ __forceinline__ void values(uint32_t sv, int lane)
+    {
+        const int g = lane >> 2, c = lane & 3;
         if constexpr (!Q8) {
             const int row = (lane & 7) + ((lane & 16) >> 1), odd = (lane >> 3) & 1;
 #pragma unroll
-            for (int i = 0; i < C::kMt; ++i) {
-                uint32_t v[4];
-                ldsm_x4_trans(v, sv + row * C::kRow + swizzled<C>(row, 2 * i + odd, false) * 16);
+            for (int t = 0; t < kMTiles; ++t)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_bf16(o[i][n], v[0], v[1], v[2], v[3], ph[n][0], ph[n][1]);
-                    mma_bf16(o[i][n], v[0], v[1], v[2], v[3], pl[n][0], pl[n][1]);
+                for (int i = 0; i < C::kMt; ++i) {
+                    uint32_t v[4];
+                    ldsm_x4_trans(v, sv + (16 * t + row) * C::kRow + swizzled<C>(row, 2 * i + odd, false) * 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_bf16(o[i][n], v[0], v[1], v[2], v[3], ph[t][n][0], ph[t][n][1]);
+                        mma_bf16(o[i][n], v[0], v[1], v[2], v[3], pl[t][n][0], pl[t][n][1]);
+                    }
                 }
-            }
         } else {
-            // lane (g, c): dimensions g HD / 8 ... of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+            // lane (g, c): dimensions g HD / 8 ... of tokens 16t + 2c, 2c + 1, 2c + 8, 2c + 9
             constexpr int W = HD / 32;  // words of a token's dimensions
             constexpr int V = HD == 96 ? 1 : (W < 4 ? W : 4);  // words a load
 #pragma unroll
-            for (int w0 = 0; w0 < W; w0 += V) {
-                uint32_t v[4][V];
+            for (int t = 0; t < kMTiles; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 2 * c + (r & 1) + (r >> 1) * 8;
-                    const int byte = g * (HD / 8) + 4 * w0;
-                    const uint32_t ad = sv + row * C::kRow + swizzled<C>(row, byte >> 4, true) * 16 + (byte & 15);
-                    if constexpr (V == 4) {
-                        const uint4 u = lds128(ad);
-                        v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
-                    } else if constexpr (V == 2) {
-                        const uint2 u = lds64(ad);
-                        v[r][0] = u.x, v[r][1] = u.y;
-                    } else {
-                        v[r][0] = lds32(ad);
+                for (int w0 = 0; w0 < W; w0 += V) {
+                    uint32_t v[4][V];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 2 * c + (r & 1) + (r >> 1) * 8;
+                        const int byte = g * (HD / 8) + 4 * w0;
+                        const uint32_t ad =
+                            sv + (16 * t + row) * C::kRow + swizzled<C>(row, byte >> 4, true) * 16 + (byte & 15);
+                        if constexpr (V == 4) {
+                            const uint4 u = lds128(ad);
+                            v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
+                        } else if constexpr (V == 2) {
+                            const uint2 u = lds64(ad);
+                            v[r][0] = u.x, v[r][1] = u.y;
+                        } else {
+                            v[r][0] = lds32(ad);
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < V; ++w) {
+                        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+                        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = h ? x1 : x0, y = h ? y1 : y0;
+                            const uint32_t a0 = e4m3x2_f16x2(static_cast<uint16_t>(x)), a1 = e4m3x2_f16x2(static_cast<uint16_t>(x >> 16));
+                            const uint32_t a2 = e4m3x2_f16x2(static_cast<uint16_t>(y)), a3 = e4m3x2_f16x2(static_cast<uint16_t>(y >> 16));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(o[2 * (w0 + w) + h][n], a0, a1, a2, a3, ph[t][n][0], ph[t][n][1]);
+                        }
                     }
                 }
-#pragma unroll
-                for (int w = 0; w < V; ++w) {
-                    const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-                    const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x = h ? x1 : x0, y = h ? y1 : y0;
-                        const uint32_t a0 = e4m3x2_f16x2(static_cast<uint16_t>(x)), a1 = e4m3x2_f16x2(static_cast<uint16_t>(x >> 16));
-                        const uint32_t a2 = e4m3x2_f16x2(static_cast<uint16_t>(y)), a3 = e4m3x2_f16x2(static_cast<uint16_t>(y >> 16));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(o[2 * (w0 + w) + h][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-                    }
-                }
-            }
         }
     }
 
@@ -491,164 +547,306 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int b, int hv, int 
             l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+// Parts joined for one float4 of o (fragment `ni` = eight heads x dimension tile, this lane) and the two heads it
+// belongs to: their maximum first, then the sums under it, so that no exponential waits for the one before.
+template <class C>
+struct Joined {
+    float m0 = kNegInf, m1 = kNegInf, l0 = 0.0f, l1 = 0.0f;
+    float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+
+    // part(i), i < count: where part i is
+    template <typename F>
+    __device__ __forceinline__ Joined(int count, int ni, int lane, F part)
+    {
+        const int ml = C::kPartF + ni / C::kMt * 16 + 2 * (lane & 3);
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float2 pm = *reinterpret_cast<const float2*>(part(i) + ml);
+            m0 = fmaxf(m0, pm.x);
+            m1 = fmaxf(m1, pm.y);
+        }
+        const float b0 = m0 == kNegInf ? 0.0f : m0, b1 = m1 == kNegInf ? 0.0f : m1;
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float* p = part(i);
+            const float2 pm = *reinterpret_cast<const float2*>(p + ml), pl = *reinterpret_cast<const float2*>(p + ml + 8);
+            const float4 v = reinterpret_cast<const float4*>(p)[ni * 32 + lane];
+            const float f0 = exp2_approx(pm.x - b0), f1 = exp2_approx(pm.y - b1);
+            r[0] = fmaf(v.x, f0, r[0]);
+            r[1] = fmaf(v.y, f1, r[1]);
+            r[2] = fmaf(v.z, f0, r[2]);
+            r[3] = fmaf(v.w, f1, r[3]);
+            l0 = fmaf(pl.x, f0, l0);
+            l1 = fmaf(pl.y, f1, l1);
+        }
+    }
+    __device__ __forceinline__ Joined() {}
+    __device__ __forceinline__ void store(float* part, int ni, int lane) const
+    {
+        reinterpret_cast<float4*>(part)[ni * 32 + lane] = make_float4(r[0], r[1], r[2], r[3]);
+        if (ni % C::kMt == 0 && lane < 4) {
+            float* ml = part + C::kPartF + ni / C::kMt * 16 + 2 * lane;
+            *reinterpret_cast<float2*>(ml) = make_float2(m0, m1);
+            *reinterpret_cast<float2*>(ml + 8) = make_float2(l0, l1);
+        }
+    }
+};
+
+template <int HD, bool Q8, int NT>
+__device__ __forceinline__ void store_joined(const AttnArgs& a, int bhv, int HV, int ni, int lane,
+                                             const Joined<AttnCfg<HD, Q8, NT>>& J)
+{
+    constexpr int kMt = AttnCfg<HD, Q8, NT>::kMt;
+    const int b = bhv / HV, hv = bhv % HV, e = ni / kMt;
+    store_out<HD, Q8, NT>(a, b, hv, e, ni % kMt, lane, J.r, J.l0, J.l1);
+    if (ni % kMt == 0 && lane < 4) {
+        store_lse<NT>(a, b, hv, e * 8 + 2 * lane, J.m0, J.l0);
+        store_lse<NT>(a, b, hv, e * 8 + 2 * lane + 1, J.m1, J.l1);
+    }
+}
+
 template <int HD, bool Q8, int NT>
 __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_attn_kernel(const AttnArgs a)
 {
     using C = AttnCfg<HD, Q8, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t sums[32];
+    // the (sequence, key head)s that span warps of this block: [0] the one that ends inside warp 0's range,
+    // [1 + w] the one whose first part in this block is warp w's last; bhv -1: none
+    __shared__ long long run_i0[C::kWarps + 1], run_i1[C::kWarps + 1];
+    __shared__ int run_bhv[C::kWarps + 1];
+    __shared__ long long warp_start[C::kWarps + 1];  // the warps' ranges
     uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + C::kSmem);  // [B + 1]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_begin();
 
-    // tiles before each sequence (of one key head): a scan over the lengths, by every block for itself
     const int cap = a.max_pages << a.c.page_shift;
-    const int per = (a.B + blockDim.x - 1) / blockDim.x;
-    const int b0 = threadIdx.x * per, b1 = min(b0 + per, a.B);
-    uint32_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int raw = __ldg(a.lens + b);
-        if ((raw < 0 || raw > cap) && blockIdx.x == 0) report(a.status, TWELL_ERR_DEVICE_CHECK);
-        mine += SeqSpan(raw, cap, a.window).tiles;
-    }
-    uint32_t run = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += u;
-    }
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) run += sums[w];
-    run -= mine;
-    for (int b = b0; b < b1; ++b) {
-        prefix[b] = run;
-        run += SeqSpan(__ldg(a.lens + b), cap, a.window).tiles;
-        if (b == a.B - 1) prefix[a.B] = run;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= a.B; b += blockDim.x) a.prefix[b] = prefix[b];
-
-    // sequences with nothing visible: zeros, lse = -inf
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (prefix[b + 1] != prefix[b]) continue;
-        uint32_t* p = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(b) * a.n_q * HD);
-        for (int i = threadIdx.x; i < a.n_q * HD / 2; i += blockDim.x) p[i] = 0u;
-        if (a.lse != nullptr)
-            for (int i = threadIdx.x; i < a.n_q; i += blockDim.x) a.lse[static_cast<int64_t>(b) * a.n_q + i] = kNegInf;
-    }
-
     const int HV = a.c.heads * a.blocks;
-    const long long total = static_cast<long long>(prefix[a.B]) * HV;
-    const Ranges R(total, gridDim.x, C::kWarps);
-    if (static_cast<int>(blockIdx.x) >= R.blocks) return;
-    const int w = blockIdx.x * C::kWarps + warp;
+    long long total = 0, seg0 = 0;  // tiles in the list; the first tile of the (sequence, key head) at this warp's start
+    Cursor cur;                     // where this warp's next tile to be used is
+    Ranges R;
+    int w0 = 0;                     // the block's first range
+    if (a.pairs) {
+        // the list is the block's own (sequence, key head)
+        cur.b = blockIdx.x / HV;
+        cur.hv = blockIdx.x % HV;
+        const int raw = __ldg(a.lens + cur.b);
+        if ((raw < 0 || raw > cap) && threadIdx.x == 0) report(a.status, TWELL_ERR_DEVICE_CHECK);
+        cur.s = SeqSpan(raw, cap, a.window);
+        if (cur.s.tiles == 0) {
+            const int first = cur.hv % a.blocks * 8 * NT, heads = min(8 * NT, a.G - first);
+            const int64_t row = static_cast<int64_t>(cur.b) * a.n_q + cur.hv / a.blocks * a.G + first;
+            uint32_t* p = reinterpret_cast<uint32_t*>(a.out + row * HD);
+            for (int i = threadIdx.x; i < heads * HD / 2; i += blockDim.x) p[i] = 0u;
+            if (a.lse != nullptr && threadIdx.x < heads) a.lse[row + threadIdx.x] = kNegInf;
+            return;
+        }
+        total = cur.s.tiles;
+        R = Ranges(total, 1, C::kWarps);
+    } else {
+        // tiles before each sequence (of one key head): a scan over the lengths, by every block for itself, and
+        // for up to kWarpSeqs sequences by every warp (all write the same values), which needs no barrier
+        constexpr int kWarpSeqs = 128;
+        if (a.B <= kWarpSeqs) {
+            int raw[kWarpSeqs / 32];
+#pragma unroll
+            for (int i = 0; i < kWarpSeqs / 32; ++i) raw[i] = 32 * i + lane < a.B ? __ldg(a.lens + 32 * i + lane) : 0;
+            uint32_t carry = 0;
+#pragma unroll
+            for (int i = 0; i < kWarpSeqs / 32; ++i) {
+                if (32 * i >= a.B) break;
+                if ((raw[i] < 0 || raw[i] > cap) && blockIdx.x == 0) report(a.status, TWELL_ERR_DEVICE_CHECK);
+                const uint32_t mine = SeqSpan(raw[i], cap, a.window).tiles;
+                uint32_t run = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += u;
+                }
+                if (32 * i + lane < a.B) prefix[32 * i + lane] = carry + run - mine;
+                carry += __shfl_sync(0xffffffffu, run, 31);
+            }
+            if (lane == 0) prefix[a.B] = carry;
+            __syncwarp();
+        } else {
+            const int per = (a.B + blockDim.x - 1) / blockDim.x;
+            const int b0 = threadIdx.x * per, b1 = min(b0 + per, a.B);
+            uint32_t mine = 0;
+#pragma unroll 4
+            for (int b = b0; b < b1; ++b) {
+                const int raw = __ldg(a.lens + b);
+                if ((raw < 0 || raw > cap) && blockIdx.x == 0) report(a.status, TWELL_ERR_DEVICE_CHECK);
+                mine += SeqSpan(raw, cap, a.window).tiles;
+            }
+            uint32_t run = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += u;
+            }
+            if (lane == 31) sums[warp] = run;
+            __syncthreads();
+            for (int i = 0; i < warp; ++i) run += sums[i];
+            run -= mine;
+            for (int b = b0; b < b1; ++b) {
+                prefix[b] = run;
+                run += SeqSpan(__ldg(a.lens + b), cap, a.window).tiles;
+                if (b == a.B - 1) prefix[a.B] = run;
+            }
+            __syncthreads();
+        }
+        // sequences with nothing visible: zeros, lse = -inf
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            if (prefix[b + 1] != prefix[b]) continue;
+            uint32_t* p = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(b) * a.n_q * HD);
+            for (int i = threadIdx.x; i < a.n_q * HD / 2; i += blockDim.x) p[i] = 0u;
+            if (a.lse != nullptr)
+                for (int i = threadIdx.x; i < a.n_q; i += blockDim.x) a.lse[static_cast<int64_t>(b) * a.n_q + i] = kNegInf;
+        }
+        total = static_cast<long long>(prefix[a.B]) * HV;
+        R = Ranges(total, gridDim.x, C::kWarps);
+        if (static_cast<int>(blockIdx.x) >= R.blocks) {
+            if (threadIdx.x == 0) a.split[blockIdx.x] = make_int2(-1, 0);
+            return;
+        }
+        w0 = blockIdx.x * C::kWarps;
+    }
+    const int w = w0 + warp;
     const long long start = R.start(w), end = R.start(w + 1);
-    const long long c_start = R.start(blockIdx.x * C::kWarps), c_end = R.start((blockIdx.x + 1) * C::kWarps);
-
-    // the block's range: within one (sequence, key head), or even all of it
-    bool inside = false, whole = false;
-    Cursor cur;  // where this warp's next tile to be used is
-    if (start < total) cur.seek(a, prefix, HV, start);
-    const long long seg0 = start - cur.tile;  // first tile of the (sequence, key head) at `start`
-    if (c_end > c_start) {
-        Cursor at;
-        at.seek(a, prefix, HV, c_start);
-        const long long s0 = c_start - at.tile, s1 = s0 + at.s.tiles;
-        inside = c_end <= s1;
-        whole = inside && s0 == c_start && s1 == c_end;
-    }
-    if (lane == 0) {
-        int d = -1;
-        if (w > 0 && start < total && start > seg0 && R.start(w - 1) <= seg0 && !whole)
-            d = cur.b * HV + cur.hv;
-        a.desc[w] = d;
-    }
+    if (a.pairs) cur.tile = static_cast<int>(start);
+    else if (start < end) seg0 = cur.seek(a, prefix, HV, start);
+    const int bhv0 = cur.b * HV + cur.hv;
 
     const int n = static_cast<int>(end - start);
-    const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
+    uint8_t* ring_ptr = smem + warp * C::kRing;
+    const uint32_t ring = smem_u32(ring_ptr);
     Cursor ahead = cur;  // where the next tile to be requested is
-    int page = 0;        // of token `lane` of that tile (lanes 0..15), -1 where nothing is read
-    auto load_page = [&]() {
-        page = -1;
-        const int pos = (ahead.s.tile0 + ahead.tile) * kTileTokens + (lane & 15);
-        if (pos >= ahead.s.first && pos < ahead.s.len) {
-            page = __ldg(a.table + static_cast<int64_t>(ahead.b) * a.max_pages + (pos >> a.c.page_shift));
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.n_pages)) {
-                report(a.status, TWELL_ERR_DEVICE_CHECK);
-                page = -1;
+    int page = 0;        // of token `lane` of that tile
+    auto load_page = [&](const Cursor& at) -> int {
+        const int pos = (at.s.tile0 + at.tile) * kTileTokens + lane;
+        if (pos < at.s.first || pos >= at.s.len) return -1;
+        return __ldg(a.table + static_cast<int64_t>(at.b) * a.max_pages + (pos >> a.c.page_shift));
+    };
+    // The tile whose keys and values are being requested: its visible tokens (those of bad pages are left out) as
+    // bits and where its rows are. A tile that lies in one page is copied from one address: lane `lane` takes chunk
+    // `lane`, `lane` + 32, ..., kStep bytes apart where a page's tokens are adjacent.
+    constexpr int kElt = Q8 ? 1 : 2, kCopies = C::kHalf / 512;
+    constexpr bool kWholeRows = 32 % C::kChunks == 0;  // 32 chunks are whole rows
+    const bool packed = kWholeRows && a.c.page_shift >= 5 && a.c.token_stride * kElt == C::kRow;
+    uint32_t tile_vis = 0;
+    int64_t tile_off = 0;  // bytes: of the tile, where it is copied from one address, else of token `lane`
+    auto request = [&](const void* base, uint32_t dst) {
+        const uint8_t* src = static_cast<const uint8_t*>(base);
+        if (packed && tile_vis == 0xffffffffu) {
+            src += tile_off + lane * 16;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int id = i * 32 + lane, row = id / C::kChunks, ch = id % C::kChunks;
+                cp_async16(dst + row * C::kRow + swizzled<C>(row, ch, Q8) * 16, src + i * 512, true);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int id = i * 32 + lane, row = id / C::kChunks, ch = id % C::kChunks;
+                const int64_t ro = __shfl_sync(0xffffffffu, tile_off, row);
+                cp_async16(dst + row * C::kRow + swizzled<C>(row, ch, Q8) * 16, src + ro + ch * 16, (tile_vis >> row) & 1u);
             }
         }
     };
-    // Requests a tile into a ring stage; returns its visible tokens (those of bad pages are left out) as bits.
-    auto request = [&](int stage) -> uint32_t {
-        const int pos = (ahead.s.tile0 + ahead.tile) * kTileTokens + (lane & 15);
-        const int in_page = pos & ((1 << a.c.page_shift) - 1);
-        const int head = ahead.hv / a.blocks;
-        const uint32_t valid = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-        const int64_t off =
-            page >= 0 ? (page * a.c.page_stride + head * a.c.head_stride + in_page * a.c.token_stride) * (Q8 ? 1 : 2) : 0;
-        const uint32_t st = ring + stage * C::kStage;
-        const uint8_t* kb = static_cast<const uint8_t*>(a.c.k);
-        const uint8_t* vb = static_cast<const uint8_t*>(a.c.v);
-#pragma unroll
-        for (int i = 0; i < C::kHalf / 512; ++i) {
-            const int id = i * 32 + lane, row = id / C::kChunks, ch = id % C::kChunks;
-            const int64_t ro = __shfl_sync(0xffffffffu, off, row) + ch * 16;
-            const bool on = (valid >> row) & 1u;
-            const uint32_t dst = st + row * C::kRow + swizzled<C>(row, ch, Q8) * 16;
-            cp_async16(dst, kb + ro, on);
-            cp_async16(dst + C::kHalf, vb + ro, on);
+    auto request_keys = [&](uint32_t dst) {  // of the tile at `ahead`, from `page`
+        const int pos = (ahead.s.tile0 + ahead.tile) * kTileTokens + lane;
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.n_pages)) {
+            if (pos >= ahead.s.first && pos < ahead.s.len) report(a.status, TWELL_ERR_DEVICE_CHECK);
+            page = -1;
         }
+        tile_vis = __ballot_sync(0xffffffffu, page >= 0);
+        const int in_page = pos & ((1 << a.c.page_shift) - 1), head = ahead.hv / a.blocks;
+        tile_off = page >= 0 ? (page * a.c.page_stride + head * a.c.head_stride + in_page * a.c.token_stride) * kElt : 0;
         if constexpr (Q8) {
             const int64_t so = page >= 0 ? page * a.c.scale_page + head * a.c.scale_head + in_page : 0;
-            cp_async4(st + 2 * C::kHalf + 4 * lane, (lane < 16 ? a.c.k_scale : a.c.v_scale) + so, page >= 0);
+            cp_async4(dst + C::kHalf + 4 * lane, a.c.k_scale + so, page >= 0);
+            cp_async4(dst + C::kHalf + 4 * (kTileTokens + lane), a.c.v_scale + so, page >= 0);
         }
-        return valid;
+        if (packed && tile_vis == 0xffffffffu) tile_off = __shfl_sync(0xffffffffu, tile_off, 0);
+        request(a.c.k, dst);
     };
 
+    // Slots of the ring hold keys and values in turn; kSlots - 1 are requested ahead.
+    constexpr int kAhead = (C::kSlots - 1) / 2;  // tiles
     AttnState<HD, Q8, NT> S;
-    int slot = 0;              // 0: the segment at the worker's start, 1: a later one
-    uint32_t valid_ring = 0;   // lane i: the visible tokens of ring stage i's tile
-    if (n > 0) load_page();
+    uint32_t vis_ring = 0;  // lane i: the visible tokens of the tile i (modulo 32) of the range
+    if (n > 0) S.load_q(a, cur.b, cur.hv, lane);
+    int pages[kAhead + 1];  // of the first tiles, requested together
+    {
+        Cursor at = cur;
 #pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s) {
+        for (int s = 0; s <= kAhead; ++s) {
+            pages[s] = s < n ? load_page(at) : -1;
+            if (s + 1 < n) at.next(a, HV);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
         if (s < n) {
-            const uint32_t v = request(s);
-            if (lane == s) valid_ring = v;
+            page = pages[s];
+            request_keys(ring + 2 * s * C::kSlot);
+            if (lane == s) vis_ring = tile_vis;
+        }
+        cp_commit();
+        if (s < n) {
+            request(a.c.v, ring + (2 * s + 1) * C::kSlot);
             ahead.next(a, HV);
-            if (s + 1 < n) load_page();
         }
         cp_commit();
     }
-    int stage = 0;
+    page = pages[kAhead];
+    S.reset();
+    S.finish_q(a, lane);
+    if (threadIdx.x <= C::kWarps) {
+        run_bhv[threadIdx.x] = -1;
+        warp_start[threadIdx.x] = R.start(w0 + threadIdx.x);
+    }
+    if (threadIdx.x == 0 && !a.pairs) {  // is this block's start the first to split its (sequence, key head)?
+        int2 sp = make_int2(-1, 0);
+        if (blockIdx.x > 0 && start > seg0 && R.start(w0 - C::kWarps) <= seg0) {
+            const long long seg1 = seg0 + cur.s.tiles;  // the last tile is in the range of warp ceil(seg1 W / total) - 1
+            sp = make_int2(bhv0, static_cast<int>((seg1 * R.W + total - 1) / total - 1) / C::kWarps);
+        }
+        a.split[blockIdx.x] = sp;
+    }
+    __syncthreads();  // run_bhv, warp_start
+
+    uint32_t slot = 0, free_slot = C::kSlots - 1;  // to be used, to be requested into
+    auto advance = [&]() {
+        free_slot = slot;
+        slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+    };
     for (int it = 0; it < n; ++it) {
-        cp_wait<C::kStages - 2>();
+        cp_wait<C::kSlots - 2>();
+        __syncwarp();  // all lanes' copies of this slot are visible, and the one before has been read by all
+        const uint32_t vis = __shfl_sync(0xffffffffu, vis_ring, it & 31);
+        if (it + kAhead < n) {
+            request_keys(ring + free_slot * C::kSlot);
+            if (lane == ((it + kAhead) & 31)) vis_ring = tile_vis;
+        }
+        cp_commit();
+        S.scores(ring + slot * C::kSlot, vis, lane);
+        advance();
+        cp_wait<C::kSlots - 2>();
         __syncwarp();
-        const uint32_t vis = __shfl_sync(0xffffffffu, valid_ring, stage);
-        {
-            const int s = stage == 0 ? C::kStages - 1 : stage - 1;
-            if (it + C::kStages - 1 < n) {
-                const uint32_t v = request(s);
-                if (lane == s) valid_ring = v;
-                ahead.next(a, HV);
-                if (it + C::kStages < n) load_page();
-            }
-            cp_commit();
+        if (it + kAhead < n) {
+            request(a.c.v, ring + free_slot * C::kSlot);
+            ahead.next(a, HV);
+            if (it + kAhead + 1 < n) page = load_page(ahead);
         }
-        if (it == 0 || cur.tile == 0) {
-            S.load_q(a, cur.b, cur.hv, lane);
-            S.reset();
-        }
-        S.tile(ring + stage * C::kStage, vis, lane);
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+        cp_commit();
+        S.values(ring + slot * C::kSlot, lane);
+        advance();
 
         const bool seg_end = cur.tile + 1 == cur.s.tiles;
         if (seg_end || it + 1 == n) {
             S.close();
-            const bool complete = seg_end && it >= cur.tile;  // its first tile was this warp's too
-            if (complete && !inside) {
+            if (seg_end && it >= cur.tile) {  // its first tile was this warp's too
 #pragma unroll
                 for (int e = 0; e < NT; ++e) {
 #pragma unroll
@@ -659,219 +857,171 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
                         store_lse<NT>(a, cur.b, cur.hv, e * 8 + 2 * lane + 1, S.m[e][1], S.l[e][1]);
                     }
                 }
-            } else if (!inside) {
-                S.store_part(a.part + (static_cast<int64_t>(w) * 2 + slot) * C::kPart, lane);
+            } else if (it + 1 < n) {  // ends inside the range, began before it
+                S.store_part(a.head_part + static_cast<int64_t>(w) * C::kPart, lane);
+                if (warp == 0 && lane == 0) {
+                    run_i0[0] = seg0;
+                    run_i1[0] = start + it + 1;
+                    run_bhv[0] = bhv0;
+                }
+            } else {  // the last of the range
+                cp_wait<0>();
+                __syncwarp();
+                S.store_part(reinterpret_cast<float*>(ring_ptr), lane);
+                const long long i0 = end - 1 - cur.tile;
+                if (lane == 0 && (i0 >= start || warp == 0)) {
+                    run_i0[1 + warp] = i0;
+                    run_i1[1 + warp] = i0 + cur.s.tiles;
+                    run_bhv[1 + warp] = cur.b * HV + cur.hv;
+                }
             }
-        }
-        if (seg_end) slot = 1;
-        if (it + 1 < n) cur.next(a, HV);
-    }
-    cp_wait<0>();
-    if (!inside) return;
-
-    // every warp's range lies in one (sequence, key head): join the parts in shared memory
-    __syncthreads();
-    float* jp = reinterpret_cast<float*>(smem);
-    if (n == 0) S.reset();
-    S.store_part(jp + warp * C::kPart, lane);
-    __syncthreads();
-    Cursor at;
-    at.seek(a, prefix, HV, c_start);
-    float* dst = a.part + static_cast<int64_t>(blockIdx.x) * C::kWarps * 2 * C::kPart;
-    for (int t = threadIdx.x; t < NT * C::kMt * 32; t += blockDim.x) {
-        const int ni = t >> 5, e = ni / C::kMt, h = 2 * (lane & 3);  // (ni, lane): this thread's float4
-        float m0 = kNegInf, m1 = kNegInf;
-#pragma unroll
-        for (int p = 0; p < C::kWarps; ++p) {
-            m0 = fmaxf(m0, jp[p * C::kPart + C::kPartF + e * 16 + h]);
-            m1 = fmaxf(m1, jp[p * C::kPart + C::kPartF + e * 16 + h + 1]);
-        }
-        float r[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-        for (int p = 0; p < C::kWarps; ++p) {
-            const float* pp = jp + p * C::kPart;
-            const float pm0 = pp[C::kPartF + e * 16 + h], pm1 = pp[C::kPartF + e * 16 + h + 1];
-            const float f0 = pm0 == kNegInf ? 0.0f : exp2_approx(pm0 - m0), f1 = pm1 == kNegInf ? 0.0f : exp2_approx(pm1 - m1);
-            const float4 v = reinterpret_cast<const float4*>(pp)[t];
-            r[0] = fmaf(v.x, f0, r[0]);
-            r[1] = fmaf(v.y, f1, r[1]);
-            r[2] = fmaf(v.z, f0, r[2]);
-            r[3] = fmaf(v.w, f1, r[3]);
-            l0 = fmaf(pp[C::kPartF + e * 16 + 8 + h], f0, l0);
-            l1 = fmaf(pp[C::kPartF + e * 16 + 8 + h + 1], f1, l1);
-        }
-        if (whole) {
-            store_out<HD, Q8, NT>(a, at.b, at.hv, e, ni % C::kMt, lane, r, l0, l1);
-            if (ni % C::kMt == 0 && lane < 4) {
-                store_lse<NT>(a, at.b, at.hv, e * 8 + h, m0, l0);
-                store_lse<NT>(a, at.b, at.hv, e * 8 + h + 1, m1, l1);
+            if (it + 1 < n) {
+                cur.next(a, HV);
+                S.load_q(a, cur.b, cur.hv, lane);
+                S.reset();
+                S.finish_q(a, lane);
             }
         } else {
-            reinterpret_cast<float4*>(dst)[t] = make_float4(r[0], r[1], r[2], r[3]);
-            if (ni % C::kMt == 0 && lane < 4) {
-                dst[C::kPartF + e * 16 + h] = m0;
-                dst[C::kPartF + e * 16 + h + 1] = m1;
-                dst[C::kPartF + e * 16 + 8 + h] = l0;
-                dst[C::kPartF + e * 16 + 8 + h + 1] = l1;
-            }
+            ++cur.tile;
         }
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // join the parts of what spans warps: one fragment of one of them a warp at a time
+    const uint32_t runs = __ballot_sync(0xffffffffu, lane <= C::kWarps && run_bhv[min(lane, C::kWarps)] >= 0);
+    const int items = __popc(runs) * (NT * C::kMt);
+    const long long c_start = warp_start[0], c_end = warp_start[C::kWarps];
+    for (int it = warp; it < items; it += C::kWarps) {
+        const int ni = it % (NT * C::kMt);
+        const int run = __fns(runs, 0, it / (NT * C::kMt) + 1);
+        const long long i0 = run_i0[run], i1 = run_i1[run];
+        const float* head = a.head_part + static_cast<int64_t>(w0) * C::kPart;
+        // the run's warps: from run - 1 to the last whose range starts before i1; that one has left its part in
+        // the workspace if its range goes on beyond i1
+        const int first = max(run - 1, 0);
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, lane == first || (lane < C::kWarps && lane > first && run != 0 &&
+                                                                             warp_start[min(lane, C::kWarps)] < i1)));
+        const bool last_head = run == 0 || (last != first && warp_start[last + 1] > i1);
+        const Joined<C> J(last - first + 1, ni, lane, [&](int i) {
+            const int q = first + i;
+            return q == last && last_head ? head + static_cast<int64_t>(q) * C::kPart
+                                          : reinterpret_cast<const float*>(smem + q * C::kRing);
+        });
+        if (i0 >= c_start && i1 <= c_end) store_joined<HD, Q8, NT>(a, run_bhv[run], HV, ni, lane, J);
+        else J.store(a.block_part + (2 * static_cast<int64_t>(blockIdx.x) + (i0 < c_start ? 0 : 1)) * C::kPart, ni, lane);
     }
 }
 
-// Joins the parts of the (sequence, key head)s that a worker of main block blockIdx.x was the first to
-// split off: kGroups groups of threads, one float4 of the output a thread; a single split is shared
-// by all groups (each takes every kGroups-th part), several are dealt out to them.
+// Joins the parts of the (sequence, key head) that main block blockIdx.x's start is the first to split: the second part
+// of the block before, the first ones of this and the following blocks. The parts' weights are formed once for the
+// block; then kGroups groups of threads, one float4 of the output a thread, take every kGroups-th part.
 template <int HD, bool Q8, int NT>
 struct JoinCfg {
-    static constexpr int kElems = NT * (HD / 16) * 32;
-    static constexpr int kGroups = 1024 / kElems;
-    static constexpr int kThreads = kGroups * kElems;
+    static constexpr int kFrags = NT * (HD / 16);
+    static constexpr int kGroups = std::max(1, 32 / kFrags);
+    static constexpr int kThreads = kGroups * kFrags * 32;
+    static constexpr int kBatch = 6;  // parts of a group requested before the weights are known
 };
 template <int HD, bool Q8, int NT>
-__global__ void __launch_bounds__(JoinCfg<HD, Q8, NT>::kThreads)
-    paged_attn_join_kernel(const AttnArgs a, int main_blocks)
+__global__ void __launch_bounds__(JoinCfg<HD, Q8, NT>::kThreads, 1) paged_attn_join_kernel(const AttnArgs a)
 {
     using C = AttnCfg<HD, Q8, NT>;
-    using J = JoinCfg<HD, Q8, NT>;
-    constexpr int kElems = J::kElems, kGroups = J::kGroups;
-    constexpr int kMaxParts = kAttnMaxSms + 2 * kAttnMaxWarps;
-    __shared__ int s_desc[C::kWarps];
-    __shared__ int s_list[kGroups][kMaxParts];  // parts in ascending order, -1 where there is none
-    __shared__ float4 s_sum[J::kThreads];
-    __shared__ float s_m[kGroups][NT * 8], s_l[kGroups][NT * 8];
+    using K = JoinCfg<HD, Q8, NT>;
+    constexpr int kHeads = NT * 8;
+    __shared__ float4 s_sum[K::kThreads];
+    __shared__ float s_m[kAttnMaxSms + 1][kHeads], s_l[kAttnMaxSms + 1][kHeads];
+    __shared__ float s_top[kHeads], s_tot[kHeads];
     pdl_begin();
-    const int HV = a.c.heads * a.blocks;
-    const long long total = static_cast<long long>(a.prefix[a.B]) * HV;
-    const Ranges R(total, main_blocks, C::kWarps);
-    if (static_cast<int>(blockIdx.x) >= R.blocks) return;
-    if (threadIdx.x < C::kWarps) s_desc[threadIdx.x] = a.desc[blockIdx.x * C::kWarps + threadIdx.x];
-    __syncthreads();
-    int owned = 0;
+    const int2 sp = a.split[blockIdx.x];
+    if (sp.x < 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / K::kFrags, ni = warp % K::kFrags;
+    const int count = sp.y - static_cast<int>(blockIdx.x) + 2;
+    const float* first = a.block_part + (2 * static_cast<int64_t>(blockIdx.x) - 1) * C::kPart;
+    auto part = [&](int p) { return first + (p == 0 ? 0 : 2 * static_cast<int64_t>(p) - 1) * C::kPart; };
+    float4 v[K::kBatch];
 #pragma unroll
-    for (int i = 0; i < C::kWarps; ++i) owned += s_desc[i] >= 0;
-    const int grp = threadIdx.x / kElems, t = threadIdx.x % kElems;
-    const int lane = threadIdx.x & 31;
-    const int e = (t >> 5) / C::kMt, dim = (t >> 5) % C::kMt, h = 2 * (lane & 3);
-    const bool shared_by_all = owned == 1;
-
-    for (int k0 = 0; k0 < owned; k0 += shared_by_all ? 1 : kGroups) {
-        // this group's split: the (k0 + grp)-th owned one (or the only one)
-        const int want = shared_by_all ? 0 : k0 + grp;
-        int wi = -1;
-        for (int i = 0, s = 0; i < C::kWarps; ++i)
-            if (s_desc[i] >= 0 && s++ == want) wi = i;
-        const bool live = wi >= 0;
-        int b = 0, hv = 0, count = 0;
-        if (live) {
-            b = s_desc[wi] / HV;
-            hv = s_desc[wi] % HV;
-            const uint32_t p0 = a.prefix[b], nt = a.prefix[b + 1] - p0;
-            const long long I0 = static_cast<long long>(p0) * HV + static_cast<long long>(hv) * nt, I1 = I0 + nt;
-            // candidates: the warps of the first block that holds some of [I0, I1), one for each block
-            // between, the warps of the last; a block inside [I0, I1) has left one part, its first warp's
-            const int blk0 = (static_cast<int>(blockIdx.x) * C::kWarps + wi - 1) / C::kWarps;
-            const int blk1 = static_cast<int>((I1 * R.W + total - 1) / total - 1) / C::kWarps;
-            const int mid = max(blk1 - blk0 - 1, 0);
-            count = blk1 > blk0 ? 2 * C::kWarps + mid : C::kWarps;
-            for (int i = t; i < count; i += kElems) {
-                uint32_t w = blk0 * C::kWarps + i;
-                bool one = false;
-                if (i >= C::kWarps + mid) {
-                    w = blk1 * C::kWarps + (i - C::kWarps - mid);
-                } else if (i >= C::kWarps) {
-                    w = (blk0 + 1 + i - C::kWarps) * C::kWarps;
-                    one = true;
-                }
-                const uint32_t blk = w / C::kWarps * C::kWarps;
-                const long long s = R.start(w), en = R.start(w + 1), cs = R.start(blk), ce = R.start(blk + C::kWarps);
-                int entry = -1;
-                if (one || (cs >= I0 && ce <= I1)) {
-                    if (w == blk && ce > cs) entry = static_cast<int>(2 * w);
-                } else if (en > s && s < I1 && en > I0) {
-                    entry = static_cast<int>(2 * w + (s < I0 ? 1 : 0));
-                }
-                s_list[grp][i] = entry;
-            }
-        }
-        __syncthreads();
-        float m0 = kNegInf, m1 = kNegInf, l0 = 0.0f, l1 = 0.0f;
-        float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const int step = shared_by_all ? kGroups : 1;
-#pragma unroll 4
-        for (int p = shared_by_all ? grp : 0; p < count; p += step) {
-            const int entry = s_list[grp][p];
-            if (entry < 0) continue;
-            const float* pp = a.part + static_cast<int64_t>(entry) * C::kPart;
-            const float4 v = reinterpret_cast<const float4*>(pp)[t];
-            const float2 pm = *reinterpret_cast<const float2*>(pp + C::kPartF + e * 16 + h);
-            const float2 pl = *reinterpret_cast<const float2*>(pp + C::kPartF + e * 16 + 8 + h);
-            const float n0 = fmaxf(m0, pm.x), n1 = fmaxf(m1, pm.y);
-            const float f0 = m0 == kNegInf ? 0.0f : exp2_approx(m0 - n0), f1 = m1 == kNegInf ? 0.0f : exp2_approx(m1 - n1);
-            const float g0 = pm.x == kNegInf ? 0.0f : exp2_approx(pm.x - n0),
-                        g1 = pm.y == kNegInf ? 0.0f : exp2_approx(pm.y - n1);
-            m0 = n0;
-            m1 = n1;
-            r[0] = r[0] * f0 + v.x * g0;
-            r[1] = r[1] * f1 + v.y * g1;
-            r[2] = r[2] * f0 + v.z * g0;
-            r[3] = r[3] * f1 + v.w * g1;
-            l0 = l0 * f0 + pl.x * g0;
-            l1 = l1 * f1 + pl.y * g1;
-        }
-        if (shared_by_all) {  // the groups' sums, in group order
-            s_sum[threadIdx.x] = make_float4(r[0], r[1], r[2], r[3]);
-            if (dim == 0 && lane < 4) {
-                s_m[grp][e * 8 + h] = m0;
-                s_m[grp][e * 8 + h + 1] = m1;
-                s_l[grp][e * 8 + h] = l0;
-                s_l[grp][e * 8 + h + 1] = l1;
-            }
-            __syncthreads();
-            m0 = m1 = kNegInf;
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                m0 = fmaxf(m0, s_m[q][e * 8 + h]);
-                m1 = fmaxf(m1, s_m[q][e * 8 + h + 1]);
-            }
-            r[0] = r[1] = r[2] = r[3] = l0 = l1 = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                const float q0 = s_m[q][e * 8 + h], q1 = s_m[q][e * 8 + h + 1];
-                const float f0 = q0 == kNegInf ? 0.0f : exp2_approx(q0 - m0), f1 = q1 == kNegInf ? 0.0f : exp2_approx(q1 - m1);
-                const float4 v = s_sum[q * kElems + t];
-                r[0] = fmaf(v.x, f0, r[0]);
-                r[1] = fmaf(v.y, f1, r[1]);
-                r[2] = fmaf(v.z, f0, r[2]);
-                r[3] = fmaf(v.w, f1, r[3]);
-                l0 = fmaf(s_l[q][e * 8 + h], f0, l0);
-                l1 = fmaf(s_l[q][e * 8 + h + 1], f1, l1);
-            }
-        }
-        if (live && (!shared_by_all || grp == 0)) {
-            store_out<HD, Q8, NT>(a, b, hv, e, dim, lane, r, l0, l1);
-            if (dim == 0 && lane < 4) {
-                store_lse<NT>(a, b, hv, e * 8 + h, m0, l0);
-                store_lse<NT>(a, b, hv, e * 8 + h + 1, m1, l1);
-            }
-        }
-        __syncthreads();
+    for (int i = 0; i < K::kBatch; ++i) {
+        const int p = grp + i * K::kGroups;
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p < count) v[i] = reinterpret_cast<const float4*>(part(p))[ni * 32 + lane];
     }
+    for (int i = threadIdx.x; i < count * kHeads; i += K::kThreads) {
+        const int p = i / kHeads, h = i % kHeads;
+        const float* ml = part(p) + C::kPartF + (h >> 3) * 16 + (h & 7);
+        s_m[p][h] = ml[0];
+        s_l[p][h] = ml[8];
+    }
+    __syncthreads();
+    for (int h = warp; h < kHeads; h += K::kThreads / 32) {
+        float top = kNegInf, tot = 0.0f;
+        for (int p = lane; p < count; p += 32) top = fmaxf(top, s_m[p][h]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float b = top == kNegInf ? 0.0f : top;
+        for (int p = lane; p < count; p += 32) {
+            const float f = exp2_approx(s_m[p][h] - b);
+            s_m[p][h] = f;
+            tot = fmaf(s_l[p][h], f, tot);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+        if (lane == 0) {
+            s_top[h] = top;
+            s_tot[h] = tot;
+        }
+    }
+    __syncthreads();
+    Joined<C> J;
+    const int h = ni / C::kMt * 8 + 2 * (lane & 3);
+    auto add = [&](const float4& u, float f0, float f1) {
+        J.r[0] = fmaf(u.x, f0, J.r[0]);
+        J.r[1] = fmaf(u.y, f1, J.r[1]);
+        J.r[2] = fmaf(u.z, f0, J.r[2]);
+        J.r[3] = fmaf(u.w, f1, J.r[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < K::kBatch; ++i) {
+        const int p = grp + i * K::kGroups;
+        if (p < count) add(v[i], s_m[p][h], s_m[p][h + 1]);
+    }
+#pragma unroll 4
+    for (int p = grp + K::kBatch * K::kGroups; p < count; p += K::kGroups)
+        add(reinterpret_cast<const float4*>(part(p))[ni * 32 + lane], s_m[p][h], s_m[p][h + 1]);
+    if (K::kGroups > 1) {  // the groups' sums, in group order
+        s_sum[threadIdx.x] = make_float4(J.r[0], J.r[1], J.r[2], J.r[3]);
+        __syncthreads();
+        if (grp != 0) return;
+#pragma unroll
+        for (int q = 1; q < K::kGroups; ++q) add(s_sum[(q * K::kFrags + ni) * 32 + lane], 1.0f, 1.0f);
+    }
+    J.m0 = s_top[h];
+    J.m1 = s_top[h + 1];
+    J.l0 = s_tot[h];
+    J.l1 = s_tot[h + 1];
+    store_joined<HD, Q8, NT>(a, sp.x, a.c.heads * a.blocks, ni, lane, J);
 }
 
 template <int HD, bool Q8, int NT>
-twell_status run_attn(const AttnArgs& a, int sms, cudaStream_t s)
+twell_status run_attn(AttnArgs& a, int sms, cudaStream_t s)
 {
     using C = AttnCfg<HD, Q8, NT>;
     static_assert(NT * C::kWarps <= kAttnMaxWarps, "the workspace holds kAttnMaxWarps warps' parts of eight heads");
-    static_assert(C::kStages >= 2, "the ring overlaps copies with the products");
     auto kern = paged_attn_kernel<HD, Q8, NT>;
+    static std::atomic<uint64_t> allowed{0};
+    if (twell_host::allow_smem(kern, C::kSmem + (kAttnMaxSeqs + 1) * 4, allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    // pairs: what the page table's width allows to be visible, in tiles
+    const long long cap = static_cast<long long>(a.max_pages) << a.c.page_shift;
+    const long long seen = a.window > 0 ? std::min<long long>(cap, static_cast<long long>(a.window) + kTileTokens - 1) : cap;
+    const long long pairs = static_cast<long long>(a.B) * a.c.heads * a.blocks;
+    a.pairs = pairs <= sms && (seen + kTileTokens - 1) / kTileTokens <= kPairTiles * C::kWarps;
+    if (a.pairs)
+        return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(pairs)), dim3(C::kWarps * 32), C::kSmem, s, a);
     const size_t smem = C::kSmem + (static_cast<size_t>(a.B) + 1) * 4;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return TWELL_ERR_CUDA;
     twell_status st = twell_host::launch_dep(kern, dim3(sms), dim3(C::kWarps * 32), smem, s, a);
     if (st != TWELL_OK) return st;
     return twell_host::launch_dep(paged_attn_join_kernel<HD, Q8, NT>, dim3(sms), dim3(JoinCfg<HD, Q8, NT>::kThreads), 0,
-                                  s, a, sms);
+                                  s, a);
 }
 
 template <int HD, bool Q8>
@@ -889,14 +1039,13 @@ twell_status run_heads(AttnArgs& a, int sms, cudaStream_t s)
 }
 
 struct AttnWs {
-    size_t prefix = 0, desc = 0, part = 0, total = 0;
-    AttnWs(int B, int hd)
+    size_t split = 0, block_part = 0, head_part = 0, total = 0;
+    explicit AttnWs(int hd)
     {
-        auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
-        const size_t workers = static_cast<size_t>(kAttnMaxSms) * kAttnMaxWarps;
-        desc = up((static_cast<size_t>(B) + 1) * 4);
-        part = desc + up(workers * 4);
-        total = part + 2 * workers * (static_cast<size_t>(hd) * 8 + 16) * 4;
+        const size_t part = (static_cast<size_t>(hd) * 8 + 16) * 4;  // of eight heads
+        block_part = kAttnMaxSms * sizeof(int2);
+        head_part = block_part + 2 * kAttnMaxSms * 2 * part;
+        total = head_part + static_cast<size_t>(kAttnMaxSms) * kAttnMaxWarps * part;
     }
 };
 
@@ -905,7 +1054,7 @@ struct AttnWs {
 
 size_t twell_host::paged_attn_ws_bytes(int B, int hd)
 {
-    return B > 0 && hd > 0 ? twell::AttnWs(B, hd).total : 0;
+    return B > 0 && hd > 0 ? twell::AttnWs(hd).total : 0;
 }
 
 using namespace twell_host;
@@ -932,7 +1081,7 @@ extern "C" twell_status twell_paged_attn_decode(const void* q, int64_t q_stride,
     if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || q_stride % 8 != 0 ||
         (B > 1 && q_stride < static_cast<int64_t>(n_q_heads) * hd))
         return TWELL_ERR_INVALID;
-    const twell::AttnWs L(B, hd);
+    const twell::AttnWs L(hd);
     if (ws == nullptr || !aligned16(ws) || ws_bytes < L.total) return TWELL_ERR_WORKSPACE;
     DevInfo dev;
     if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
@@ -950,9 +1099,9 @@ extern "C" twell_status twell_paged_attn_decode(const void* q, int64_t q_stride,
     a.max_pages = max_pages;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.prefix = reinterpret_cast<uint32_t*>(base + L.prefix);
-    a.desc = reinterpret_cast<int*>(base + L.desc);
-    a.part = reinterpret_cast<float*>(base + L.part);
+    a.split = reinterpret_cast<int2*>(base + L.split);
+    a.block_part = reinterpret_cast<float*>(base + L.block_part);
+    a.head_part = reinterpret_cast<float*>(base + L.head_part);
     const int sms = std::min(dev.sm_count, twell::kAttnMaxSms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.c.q8) {

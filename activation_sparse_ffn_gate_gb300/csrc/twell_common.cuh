@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "twell.h"
 
 namespace twell {
@@ -512,6 +514,22 @@ inline twell_status launch_status()
 {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+// Allow `kern` up to `bytes` of dynamic shared memory, the most that any of its launches takes, on the current
+// device. `done` is the caller's, one for each kernel: a bit for each device it has been allowed on, so that a
+// kernel launched often is asked about once.
+template <typename K>
+twell_status allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done)
+{
+    DevInfo d;
+    if (dev_info(&d) != TWELL_OK) return TWELL_ERR_CUDA;
+    const uint64_t bit = 1ull << d.device;
+    if (done.load(std::memory_order_relaxed) & bit) return TWELL_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+        return TWELL_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return TWELL_OK;
 }
 
 // Launch `kern` as a programmatic dependent of the kernel before it on `s`; the kernel must begin

@@ -3,8 +3,11 @@
 // as bf16.
 //
 // Both are bounded by memory traffic. A row (one token's key and value of one head) is handled by
-// head_dim / 8 neighbouring lanes, 16 bytes of bf16 a lane, key and value in flight together; the
-// row's largest magnitude is a shuffle over those lanes, so a row is read once.
+// neighbouring lanes, key and value in flight together. Writing: head_dim / 8 lanes, 16 bytes of bf16 a lane; the
+// row's largest magnitudes are a shuffle over those lanes (key and value as one bf16 pair), and the four
+// quotients of a row (both scales and both factors) are formed by different lanes with one division. Reading:
+// head_dim / 8 lanes, so that a warp's 16-byte stores are contiguous, and with many rows kGatherRows rows a thread,
+// all requested before the first is used.
 #include "twell_kv.cuh"
 #include "twell_ops.cuh"
 
@@ -12,16 +15,18 @@ namespace twell {
 namespace {
 
 constexpr int kKvThreads = 256;
+constexpr int kGatherRows = 4;
 
-// The row of this thread: `lpr` lanes a row (a power of two, head_dim / 8 of them active).
+// Row `i` of this thread: LPR lanes a row (a power of two), 8 elements a lane, the lanes past head_dim idle.
 struct KvRow {
     int token, head, col;
     bool live;
 };
-template <int LPR>
-__device__ __forceinline__ KvRow kv_row(int n, int heads, int hd)
+template <int LPR, int RPT>
+__device__ __forceinline__ KvRow kv_row(int i, int n, int heads, int hd)
 {
-    const unsigned id = blockIdx.x * (kKvThreads / LPR) + threadIdx.x / LPR;
+    constexpr unsigned kPer = kKvThreads / LPR;
+    const unsigned id = (blockIdx.x * RPT + i) * kPer + threadIdx.x / LPR;
     KvRow r;
     r.col = static_cast<int>(threadIdx.x % LPR) * 8;
     r.token = static_cast<int>(id / static_cast<unsigned>(heads));
@@ -30,13 +35,20 @@ __device__ __forceinline__ KvRow kv_row(int n, int heads, int hd)
     return r;
 }
 
-// The slot of a token: -1 where it has none or the slot does not exist (which is recorded).
-__device__ __forceinline__ int checked_slot(const int32_t* slots, int token, const KvView& c, int32_t* status)
+// A token's slot, -1 where it has none or the slot does not exist (which is recorded).
+__device__ __forceinline__ int checked_slot(int s, const KvView& c, int32_t* status)
 {
-    const int s = slots[token];
     if (s >= 0 && (s >> c.page_shift) < c.n_pages) return s;
     if (s != -1) report(status, TWELL_ERR_DEVICE_CHECK);
     return -1;
+}
+
+// The largest magnitude of 8 bf16 values, as a bf16 pair of which either may be it (NaN ignored).
+__device__ __forceinline__ __nv_bfloat162 top8(const uint4& v)
+{
+    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(w);
+    return __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
 }
 
 template <int LPR, bool Q8>
@@ -46,14 +58,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvView c, c
                                                                int32_t* status)
 {
     pdl_begin();
-    const KvRow r = kv_row<LPR>(n, c.heads, c.hd);
+    const KvRow r = kv_row<LPR, 1>(0, n, c.heads, c.hd);
     uint4 kv[2] = {};
     int slot = -1;
     if (r.live) {
         const int64_t in = static_cast<int64_t>(r.head) * c.hd + r.col;
         kv[0] = ldg_stream16(k + r.token * ldk + in);
         kv[1] = ldg_stream16(v + r.token * ldv + in);
-        slot = checked_slot(slots, r.token, c, status);
+        slot = checked_slot(__ldg(slots + r.token), c, status);
     }
     const int64_t off = slot >= 0 ? c.row(slot, r.head) + r.col : 0;
     if constexpr (!Q8) {
@@ -61,61 +73,87 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvView c, c
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + off) = kv[0];
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + off) = kv[1];
     } else {
+        const __nv_bfloat162 tk = top8(kv[0]), tv = top8(kv[1]);
+        __nv_bfloat162 top = __hmax2(__lows2bfloat162(tk, tv), __highs2bfloat162(tk, tv));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float x[8];
-            unpack16(kv[i], x, static_cast<__nv_bfloat16*>(nullptr));
-            float top = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (slot < 0) continue;
-            const Scale8 q(top);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(i == 0 ? c.k : c.v) + off) = q.pack8(x);
-            if (r.col == 0) (i == 0 ? c.k_scale : c.v_scale)[c.scale_row(slot, r.head)] = q.scale;
-        }
+        for (int o = LPR / 2; o > 0; o >>= 1) top = __hmax2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // quarters of the row's lanes: the key's scale, its factor, the value's scale, its factor
+        const int lane = threadIdx.x % LPR, part = lane / (LPR / 4);
+        const float a = fmaxf(part < 2 ? __low2float(top) : __high2float(top), kAmaxMin);
+        const float num = (part & 1) ? kE4m3Max : a, den = (part & 1) ? a : kE4m3Max;
+        const float quot = num / den;
+        const int row0 = static_cast<int>(threadIdx.x & 31) - lane;
+        const float mk = __shfl_sync(0xffffffffu, quot, row0 + LPR / 4);
+        const float mv = __shfl_sync(0xffffffffu, quot, row0 + 3 * (LPR / 4));
+        // the lanes that hold the scales may lie past head_dim: they take the slot from the row's first lane
+        const int row_slot = __shfl_sync(0xffffffffu, slot, row0);
+        if (row_slot >= 0 && (lane == 0 || lane == LPR / 2))
+            (lane == 0 ? c.k_scale : c.v_scale)[c.scale_row(row_slot, r.head)] = quot;
+        if (slot < 0) return;
+        float x[8];
+        unpack16(kv[0], x, static_cast<__nv_bfloat16*>(nullptr));
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.k) + off) = Scale8{0.0f, mk}.pack8(x);
+        unpack16(kv[1], x, static_cast<__nv_bfloat16*>(nullptr));
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.v) + off) = Scale8{0.0f, mv}.pack8(x);
     }
 }
 
-template <int LPR, bool Q8>
+template <int LPR, bool Q8, int RPT>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvView c, const int32_t* __restrict__ slots, int n,
                                                                __nv_bfloat16* __restrict__ k_out,
                                                                __nv_bfloat16* __restrict__ v_out, int32_t* status)
 {
     pdl_begin();
-    const KvRow r = kv_row<LPR>(n, c.heads, c.hd);
-    if (!r.live) return;
-    const int slot = checked_slot(slots, r.token, c, status);
-    const int64_t out = (static_cast<int64_t>(r.token) * c.heads + r.head) * c.hd + r.col;
-    uint4 kv[2] = {};
-    if (slot >= 0) {
-        const int64_t off = c.row(slot, r.head) + r.col;
+    int slot[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const KvRow r = kv_row<LPR, RPT>(i, n, c.heads, c.hd);
+        slot[i] = r.live ? __ldg(slots + r.token) : -1;
+    }
+    uint4 kv[RPT][2];  // an e4m3 row: its 8 codes in x and y, its scale in z
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const KvRow r = kv_row<LPR, RPT>(i, n, c.heads, c.hd);
+        const int s = checked_slot(slot[i], c, status);
+        kv[i][0] = kv[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (s < 0) continue;
+        const int64_t off = c.row(s, r.head) + r.col;
         if constexpr (!Q8) {
-            kv[0] = ldg_stream16(static_cast<const __nv_bfloat16*>(c.k) + off);
-            kv[1] = ldg_stream16(static_cast<const __nv_bfloat16*>(c.v) + off);
+            kv[i][0] = ldg_stream16(static_cast<const __nv_bfloat16*>(c.k) + off);
+            kv[i][1] = ldg_stream16(static_cast<const __nv_bfloat16*>(c.v) + off);
         } else {
-            const int64_t so = c.scale_row(slot, r.head);
+            const int64_t so = c.scale_row(s, r.head);
             const uint2 kc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + off));
             const uint2 vc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + off));
-            const float s[2] = {__ldg(c.k_scale + so), __ldg(c.v_scale + so)};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint2 q = i == 0 ? kc : vc;
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w = e < 2 ? q.x : q.y;
-                    const float2 p = e4m3x2_f32(static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xffffu));
-                    x[2 * e] = p.x * s[i];
-                    x[2 * e + 1] = p.y * s[i];
-                }
-                kv[i] = pack16(x, static_cast<__nv_bfloat16*>(nullptr));
-            }
+            kv[i][0] = make_uint4(kc.x, kc.y, __float_as_uint(__ldg(c.k_scale + so)), 0u);
+            kv[i][1] = make_uint4(vc.x, vc.y, __float_as_uint(__ldg(c.v_scale + so)), 0u);
         }
     }
-    *reinterpret_cast<uint4*>(k_out + out) = kv[0];
-    *reinterpret_cast<uint4*>(v_out + out) = kv[1];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const KvRow r = kv_row<LPR, RPT>(i, n, c.heads, c.hd);
+        if (!r.live) continue;
+        const int64_t out = (static_cast<int64_t>(r.token) * c.heads + r.head) * c.hd + r.col;
+        if constexpr (Q8) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint4 q = kv[i][p];
+                const float s = __uint_as_float(q.z);
+                const float2 f0 = e4m3x2_f32(static_cast<uint16_t>(q.x)), f1 = e4m3x2_f32(static_cast<uint16_t>(q.x >> 16));
+                const float2 f2 = e4m3x2_f32(static_cast<uint16_t>(q.y)), f3 = e4m3x2_f32(static_cast<uint16_t>(q.y >> 16));
+                const float x[8] = {f0.x * s, f0.y * s, f1.x * s, f1.y * s, f2.x * s, f2.y * s, f3.x * s, f3.y * s};
+                kv[i][p] = pack16(x, static_cast<__nv_bfloat16*>(nullptr));
+            }
+        }
+        st_stream16(k_out + out, kv[i][0]);
+        st_stream16(v_out + out, kv[i][1]);
+    }
+}
+
+inline unsigned kv_blocks(long long rows, int lpr, int rpt)
+{
+    const long long per = static_cast<long long>(kKvThreads / lpr) * rpt;
+    return static_cast<unsigned>((rows + per - 1) / per);
 }
 
 template <int LPR>
@@ -124,9 +162,8 @@ twell_status run_append(const KvView& c, const void* k, const void* v, int64_t l
 {
     using bf = __nv_bfloat16;
     const long long rows = static_cast<long long>(n) * c.heads;
-    const int per = kKvThreads / LPR;
     auto kern = c.q8 ? kv_append_kernel<LPR, true> : kv_append_kernel<LPR, false>;
-    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kKvThreads), 0, s, c,
+    return twell_host::launch_dep(kern, dim3(kv_blocks(rows, LPR, 1)), dim3(kKvThreads), 0, s, c,
                                   static_cast<const bf*>(k), static_cast<const bf*>(v), ldk, ldv, slots, n, status);
 }
 
@@ -136,10 +173,12 @@ twell_status run_gather(const KvView& c, const int32_t* slots, int n, void* k_ou
 {
     using bf = __nv_bfloat16;
     const long long rows = static_cast<long long>(n) * c.heads;
-    const int per = kKvThreads / LPR;
-    auto kern = c.q8 ? kv_gather_kernel<LPR, true> : kv_gather_kernel<LPR, false>;
-    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kKvThreads), 0, s, c,
-                                  slots, n, static_cast<bf*>(k_out), static_cast<bf*>(v_out), status);
+    // several rows a thread once that still gives every SM several blocks
+    const int rpt = rows * LPR >= 4ll * kGatherRows * kKvThreads * 152 ? kGatherRows : 1;
+    auto kern = rpt == 1 ? (c.q8 ? kv_gather_kernel<LPR, true, 1> : kv_gather_kernel<LPR, false, 1>)
+                         : (c.q8 ? kv_gather_kernel<LPR, true, kGatherRows> : kv_gather_kernel<LPR, false, kGatherRows>);
+    return twell_host::launch_dep(kern, dim3(kv_blocks(rows, LPR, rpt)), dim3(kKvThreads), 0, s, c, slots, n,
+                                  static_cast<bf*>(k_out), static_cast<bf*>(v_out), status);
 }
 
 constexpr long long kMaxRows = 1ll << 31;  // rows (tokens x heads) of one call

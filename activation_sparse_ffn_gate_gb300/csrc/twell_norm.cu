@@ -3,11 +3,10 @@
 //   h = x + r,  s = 1 / sqrt(mean(h^2) + eps),  y = h s w
 //   dx = s (g - xh mean(g xh)) + dh  with  xh = h s, g = dy w;   dw = sum over rows of dy xh
 //
-// Both passes are bounded by memory traffic: every element is read and written once, a row stays in
-// registers between its statistics and its output, 8 elements (one chunk) a thread, so a row is
-// spread over d / 8 threads (two chunks a thread above 8192 columns). Rows of few columns share a
-// block. All sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the fp32
-// values (y from the unrounded h, so that it does not depend on the residual stream's type).
+// Both passes are bounded by memory traffic: every element is read and written once, and a row stays in
+// registers between its statistics and its output. A row is spread over `wpr` warps, CH chunks of 8
+// elements a thread. All sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the
+// fp32 values (y from the unrounded h, so that it does not depend on the residual stream's type).
 #include "twell_common.cuh"
 #include "twell_ops.cuh"
 
@@ -15,16 +14,19 @@ namespace twell {
 namespace {
 
 constexpr int kNormMaxD = 16384;
-constexpr int kNormMaxThreads = 1024;
-constexpr int kNormMinThreads = 256;  // rows of few columns share a block of this many threads
+constexpr int kNormMaxThreads = 512;
+constexpr int kNormMinThreads = 128;  // rows of few columns share a block of this many threads
 
-// How a row of d columns is spread over a block: `wpr` warps a row, `rpb` rows a block.
+// How a row of d columns is spread over a block: `ch` chunks of 8 elements a thread, `wpr` warps a row, `rpb` rows
+// a block. One chunk a thread as far as the block goes: more threads in flight hide more of the latency than
+// longer threads save instructions (16384 rows of 2560, forward into e4m3: 72.7 us with one chunk, 75.0 with two,
+// 91.0 with four; backward 103.8, 105.6, 137.4).
 struct NormShape {
     int ch, wpr, rpb;
     explicit NormShape(int d)
     {
         const int chunks = d / 8;
-        ch = chunks <= kNormMaxThreads ? 1 : 2;
+        ch = chunks <= kNormMaxThreads ? 1 : (chunks <= 2 * kNormMaxThreads ? 2 : 4);
         wpr = (chunks + 32 * ch - 1) / (32 * ch);
         rpb = wpr * 32 >= kNormMinThreads ? 1 : kNormMinThreads / (wpr * 32);
     }
@@ -64,87 +66,82 @@ struct NormFwdArgs {
     float* scale;
     float* rstd;
     int N, d, group, ng, wpr, rpb;
-    float eps;
+    float eps, inv_d;
 };
 
 template <typename T, typename R, int CH>
 __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const NormFwdArgs a)
 {
-    __shared__ float red[2][32];
+    __shared__ float red[2][kNormMaxThreads / 32];
     pdl_begin();
     const int per_row = 32 * a.wpr;
     const int t = static_cast<int>(threadIdx.x) % per_row;
     const long long row = static_cast<long long>(blockIdx.x) * a.rpb + threadIdx.x / per_row;
     const bool live = row < a.N;
-    const int chunks = a.d / 8;
-    const size_t base = static_cast<size_t>(live ? row : 0) * a.d;
+    const int chunks = live ? a.d / 8 : 0;
+    const size_t base = static_cast<size_t>(live ? row : 0) * a.d + t * 8;
+    const int step = per_row * 8;
 
-    float h[CH][8];
+    float h[CH][8], r[CH][8];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = t + i * per_row;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
-        if (live && c < chunks) {
-            load8(static_cast<const T*>(a.x) + base + c * 8, h[i]);
-            if (a.res != nullptr) {
-                float r[8];
-                load8(static_cast<const R*>(a.res) + base + c * 8, r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] += r[e];
-            }
+        for (int e = 0; e < 8; ++e) h[i][e] = r[i][e] = 0.0f;
+        if (t + i * per_row < chunks) {
+            load8(static_cast<const T*>(a.x) + base + i * step, h[i]);
+            if (a.res != nullptr) load8(static_cast<const R*>(a.res) + base + i * step, r[i]);
         }
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = t + i * per_row;
-        if (a.h != nullptr && live && c < chunks) store8(static_cast<R*>(a.h) + base + c * 8, h[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+        for (int e = 0; e < 8; ++e) {
+            h[i][e] += r[i][e];
+            ss = fmaf(h[i][e], h[i][e], ss);
+        }
+        if (a.h != nullptr && t + i * per_row < chunks) store8(static_cast<R*>(a.h) + base + i * step, h[i]);
     }
     ss = row_reduce<false>(ss, red[0], a.wpr);
-    const float s = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+    const float s = rsqrtf(fmaf(ss, a.inv_d, a.eps));
     if (a.rstd != nullptr && live && t == 0) a.rstd[row] = s;
 
     float top[CH];
-    float row_top = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = t + i * per_row;
         top[i] = 0.0f;
-        if (c < chunks) {
+        if (t + i * per_row < chunks) {
             float w[8];
-            load8(static_cast<const T*>(a.w) + c * 8, w);
+            load8(static_cast<const T*>(a.w) + t * 8 + i * step, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[i][e] = h[i][e] * s * w[e];
                 top[i] = fmaxf(top[i], fabsf(h[i][e]));
             }
-            if (a.y != nullptr && live) store8(static_cast<T*>(a.y) + base + c * 8, h[i]);
+            if (a.y != nullptr) store8(static_cast<T*>(a.y) + base + i * step, h[i]);
         }
-        row_top = fmaxf(row_top, top[i]);
     }
     if (a.y8 == nullptr) return;
     if (a.group == a.d) {
-        row_top = row_reduce<true>(row_top, red[1], a.wpr);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) top[i] = row_top;
+        for (int i = 1; i < CH; ++i) top[0] = fmaxf(top[0], top[i]);
+        top[0] = row_reduce<true>(top[0], red[1], a.wpr);
+#pragma unroll
+        for (int i = 1; i < CH; ++i) top[i] = top[0];
     } else {  // groups of 128 columns: 16 lanes next to each other
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
+        for (int o = 8; o > 0; o >>= 1) {
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+            for (int i = 0; i < CH; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
         }
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = t + i * per_row;
-        if (!live || c >= chunks) continue;
-        const Scale8 q(top[i]);
-        *reinterpret_cast<uint2*>(a.y8 + base + c * 8) = q.pack8(h[i]);
-        const int per_group = a.group / 8;
-        if (c % per_group == 0) a.scale[static_cast<size_t>(row) * a.ng + c / per_group] = q.scale;
+        if (c >= chunks) continue;
+        const Scale8 q = Scale8::approx(top[i]);
+        *reinterpret_cast<uint2*>(a.y8 + base + i * step) = q.pack8(h[i]);
+        if (a.group == a.d ? c == 0 : (c & 15) == 0) a.scale[static_cast<size_t>(row) * a.ng + (c >> 4)] = q.scale;
     }
 }
 
@@ -157,79 +154,73 @@ struct NormBwdArgs {
     void* dx;
     float* part;  // [gridDim.x * rpb, d]
     int N, d, wpr, rpb;
+    float inv_d;
 };
 
 // Rows blockIdx.x * rpb + ..., then every gridDim.x * rpb-th one; the weights stay in registers and
 // the rows' shares of dw are added there too, one partial row of dw for each row slot of the grid.
+// With one chunk a thread an SM holds 1024 threads (64 registers each), with more 512.
+constexpr int norm_threads_per_sm(int ch) { return ch == 1 ? 1024 : 512; }
 template <typename T, typename R, typename G, int CH>
-__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const NormBwdArgs a)
+__global__ void __launch_bounds__(kNormMaxThreads, norm_threads_per_sm(CH) / kNormMaxThreads) add_rmsnorm_bwd_kernel(const NormBwdArgs a)
 {
-    __shared__ float red[2][32];
+    __shared__ float red[2][kNormMaxThreads / 32];
     pdl_begin();
     const int per_row = 32 * a.wpr;
     const int t = static_cast<int>(threadIdx.x) % per_row;
     const int sub = static_cast<int>(threadIdx.x) / per_row;
-    const int chunks = a.d / 8;
-    float dw[CH][8], w[CH][8];
+    const int chunks = a.d / 8, step = per_row * 8;
+    constexpr int KW = CH <= 2 ? CH : 1;  // chunks whose weights stay in registers; else they are read again (L1)
+    float dw[CH][8], w[KW][8];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = t + i * per_row;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = w[i][e] = 0.0f;
-        if (c < chunks) load8(static_cast<const T*>(a.w) + c * 8, w[i]);
+        for (int e = 0; e < 8; ++e) dw[i][e] = w[i % KW][e] = 0.0f;
+        if (KW == CH && t + i * per_row < chunks) load8(static_cast<const T*>(a.w) + t * 8 + i * step, w[i % KW]);
     }
-    const long long step = static_cast<long long>(gridDim.x) * a.rpb;
+    const long long rows = static_cast<long long>(gridDim.x) * a.rpb;
     int flip = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * a.rpb; r0 < a.N; r0 += step, flip ^= 1) {
-        const long long row = r0 + sub;
-        const bool live = row < a.N;
-        const size_t base = static_cast<size_t>(live ? row : 0) * a.d;
-        const float s = live ? a.rstd[row] : 0.0f;
-        float dy[CH][8], xh[CH][8];
+    for (long long r0 = static_cast<long long>(blockIdx.x) * a.rpb; r0 < a.N; r0 += rows, flip ^= 1) {
+        const bool live = r0 + sub < a.N;
+        const int mine = live ? chunks : 0;
+        const size_t base = static_cast<size_t>(live ? r0 + sub : 0) * a.d + t * 8;
+        const float s = live ? a.rstd[r0 + sub] : 0.0f;
+        float dy[CH][8], xh[CH][8], o[CH][8];
         float p = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = t + i * per_row;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dy[i][e] = xh[i][e] = 0.0f;
-            if (live && c < chunks) {
-                load8(static_cast<const G*>(a.dy) + base + c * 8, dy[i]);
-                load8(static_cast<const R*>(a.h) + base + c * 8, xh[i]);
+            for (int e = 0; e < 8; ++e) dy[i][e] = xh[i][e] = o[i][e] = 0.0f;
+            if (t + i * per_row < mine) {
+                load8(static_cast<const G*>(a.dy) + base + i * step, dy[i]);
+                load8(static_cast<const R*>(a.h) + base + i * step, xh[i]);
+                if (a.dh != nullptr) load8(static_cast<const G*>(a.dh) + base + i * step, o[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+            if (KW != CH && t + i * per_row < mine) load8(static_cast<const T*>(a.w) + t * 8 + i * step, w[i % KW]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 xh[i][e] *= s;
                 dw[i][e] = fmaf(dy[i][e], xh[i][e], dw[i][e]);
-                dy[i][e] *= w[i][e];
+                dy[i][e] *= w[i % KW][e];
                 p = fmaf(dy[i][e], xh[i][e], p);
             }
         }
-        p = row_reduce<false>(p, red[flip], a.wpr) / static_cast<float>(a.d);
+        p = row_reduce<false>(p, red[flip], a.wpr) * a.inv_d;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = t + i * per_row;
-            if (!live || c >= chunks) continue;
-            float o[8];
+            if (t + i * per_row >= mine) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = s * (dy[i][e] - xh[i][e] * p);
-            if (a.dh != nullptr) {
-                float u[8];
-                load8(static_cast<const G*>(a.dh) + base + c * 8, u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] += u[e];
-            }
-            store8(static_cast<G*>(a.dx) + base + c * 8, o);
+            for (int e = 0; e < 8; ++e) o[i][e] = fmaf(s, fmaf(-xh[i][e], p, dy[i][e]), o[i][e]);
+            store8(static_cast<G*>(a.dx) + base + i * step, o[i]);
         }
     }
-    float* part = a.part + (static_cast<size_t>(blockIdx.x) * a.rpb + sub) * a.d;
+    float* part = a.part + (static_cast<size_t>(blockIdx.x) * a.rpb + sub) * a.d + t * 8;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = t + i * per_row;
-        if (c < chunks) store8(part + c * 8, dw[i]);
-    }
+    for (int i = 0; i < CH; ++i)
+        if (t + i * per_row < chunks) store8(part + i * step, dw[i]);
 }
 
 // dw[c] = sum over p of part[p][c]: 32 columns a block, 32 threads a column, each over every 32nd
@@ -254,11 +245,11 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __res
     if (lane == 0 && blockIdx.x * 32 + way < d) dw[blockIdx.x * 32 + way] = v;
 }
 
-// Blocks of the backward pass: enough for kNormBwdThreads threads on each SM, no more than rows.
-constexpr int kNormBwdThreads = 1280;
+// Blocks of the backward pass: what an SM holds at once, on each SM, no more than rows. A block more than that
+// would run alone at the end (2560 columns, 320 threads: 103.8 us with the 3 that fit, 124.5 with 4).
 int bwd_blocks(int N, const NormShape& S, int sms)
 {
-    const int per_sm = std::max(1, kNormBwdThreads / S.threads());
+    const int per_sm = std::max(1, norm_threads_per_sm(S.ch) / S.threads());
     const long long need = (static_cast<long long>(N) + S.rpb - 1) / S.rpb;
     return static_cast<int>(std::min<long long>(need, static_cast<long long>(sms) * per_sm));
 }
@@ -269,14 +260,16 @@ constexpr int kNormMaxSms = 160;
 template <typename T, typename R>
 twell_status run_norm_fwd(const NormFwdArgs& a, const NormShape& S, cudaStream_t s)
 {
-    auto kern = S.ch == 1 ? add_rmsnorm_fwd_kernel<T, R, 1> : add_rmsnorm_fwd_kernel<T, R, 2>;
+    auto kern = S.ch == 1 ? add_rmsnorm_fwd_kernel<T, R, 1> : S.ch == 2 ? add_rmsnorm_fwd_kernel<T, R, 2>
+                                                                        : add_rmsnorm_fwd_kernel<T, R, 4>;
     return twell_host::launch_dep(kern, dim3((a.N + S.rpb - 1) / S.rpb), dim3(S.threads()), 0, s, a);
 }
 
 template <typename T, typename R, typename G>
 twell_status run_norm_bwd(const NormBwdArgs& a, const NormShape& S, int blocks, float* dw, cudaStream_t s)
 {
-    auto kern = S.ch == 1 ? add_rmsnorm_bwd_kernel<T, R, G, 1> : add_rmsnorm_bwd_kernel<T, R, G, 2>;
+    auto kern = S.ch == 1 ? add_rmsnorm_bwd_kernel<T, R, G, 1> : S.ch == 2 ? add_rmsnorm_bwd_kernel<T, R, G, 2>
+                                                                           : add_rmsnorm_bwd_kernel<T, R, G, 4>;
     twell_status st = twell_host::launch_dep(kern, dim3(blocks), dim3(S.threads()), 0, s, a);
     if (st != TWELL_OK) return st;
     return twell_host::launch_dep(add_rmsnorm_dw_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s,
@@ -314,9 +307,9 @@ extern "C" twell_status twell_add_rmsnorm_fwd(const void* x, const void* res, co
         !aligned16(y8_scale) || !aligned16(rstd))
         return TWELL_ERR_INVALID;
     const twell::NormShape S(d);
-    const int g = group == 0 ? d : group;
+    const int g = group == 0 || d <= 128 ? d : group;
     const twell::NormFwdArgs a{x,    res, w, h_out, y,  static_cast<uint8_t*>(y8), y8_scale, rstd, N, d,
-                               g, (d + g - 1) / g, S.wpr, S.rpb, eps};
+                               g, (d + g - 1) / g, S.wpr, S.rpb, eps, 1.0f / static_cast<float>(d)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == TWELL_F32) return twell::run_norm_fwd<float, float>(a, S, s);
     if (res_dtype == TWELL_F32) return twell::run_norm_fwd<__nv_bfloat16, float>(a, S, s);
@@ -343,7 +336,8 @@ extern "C" twell_status twell_add_rmsnorm_bwd(const void* dy, const void* h, con
     if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
     const twell::NormShape S(d);
     const int blocks = twell::bwd_blocks(N, S, std::min(dev.sm_count, twell::kNormMaxSms));
-    const twell::NormBwdArgs a{dy, h, w, dh, rstd, dx, static_cast<float*>(ws), N, d, S.wpr, S.rpb};
+    const twell::NormBwdArgs a{dy, h, w, dh, rstd, dx, static_cast<float*>(ws), N, d, S.wpr, S.rpb,
+                               1.0f / static_cast<float>(d)};
     using bf = __nv_bfloat16;
     const bool g32 = grad_dtype == TWELL_F32;
     if (dtype == TWELL_F32)

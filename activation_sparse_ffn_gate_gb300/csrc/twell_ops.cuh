@@ -37,11 +37,13 @@ constexpr float kAmaxMin = 8.6736173798840355e-19f;  // 2^-60
 
 struct Scale8 {
     float scale, mul;
-    __device__ __forceinline__ explicit Scale8(float top)
+    // both to about 2^-23, for values that carry an error of that size themselves
+    __device__ __forceinline__ static Scale8 approx(float top)
     {
         const float a = fmaxf(top, kAmaxMin);
-        scale = a / kE4m3Max;
-        mul = kE4m3Max / a;
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
+        return {a * (1.0f / kE4m3Max), kE4m3Max * r};
     }
     // two codes, the first in the low byte
     __device__ __forceinline__ uint32_t pack2(float a, float b) const

@@ -5,13 +5,14 @@
 // cores' fragments want them: a tile of 16 rows by 128 columns is 1 KB, lane (g, c) of a warp (g < 8,
 // c < 4) owning 32 consecutive bytes of it: for rows g and g + 8, the columns 32j + 8c .. + 7, j < 4. A
 // word holds 8 columns of a row, column 2i in bits 4i .. 4i + 3 and column 2i + 1 in bits 16 + 4i ..., so
-// one shift and mask gives the pair an mma.sync m16n8k16 register wants. The pair becomes bf16
-// exactly (128 + code by a bit pattern, minus 136); rows are the product's 16-row side and tokens its
-// 8 columns, a group's products are summed in fp32 by the tensor core and added to the total times
-// the group's scale in fp32, so x and the codes enter exactly. Scales lie beside the tile in the same
-// order ([g][half][128 / group]).
-// A block takes one row tile, its warps every n-th column tile each; their sums are added in warp
-// order in shared memory (no atomics: the same y from call to call).
+// one shift and mask gives the pair an mma.sync m16n8k16 register wants: or-ed into bf16 128.0, it is the pair
+// 128 + code, exactly. Rows are the product's 16-row side and tokens its 8 columns; a group's products are
+// summed in fp32 by the tensor core on top of -136 sum x (so that what is summed is (code - 8) x; sum x of each
+// group comes from a product with ones, once for all rows of a block) and added to the total times the group's
+// scale in fp32. Scales lie beside the tile in the same order ([g][half][128 / group]).
+// A block takes up to 4 row tiles and its warps every n-th column tile of them each: a fragment of x is loaded once
+// for those row tiles, and a warp copies weights, scales and x into its own shared-memory ring a column tile
+// ahead. The warps' sums are added in warp order in shared memory (no atomics: the same y from call to call).
 #include "twell_mma.cuh"
 #include "twell_ops.cuh"
 
@@ -19,13 +20,22 @@ namespace twell {
 namespace {
 
 constexpr int kW4MaxN = 16;
-constexpr int kW4Warps = 8;
+constexpr int kW4Warps = 8;   // most a block has; two blocks share an SM
+constexpr int kW4Slot = 1152; // bytes of a weight tile in the ring: its words, then its scales (at most 128 bytes)
+constexpr int kW4Stages = 2;
+// Row tiles a block, by the token columns (in eights): what lets two blocks' rings share an SM.
+constexpr int w4_tiles(int nb) { return nb == 1 ? 4 : 3; }
+constexpr int w4_stage(int nb, int rt) { return rt * kW4Slot + nb * 2048; }  // 8 tokens by 128 columns of x: 2 KB
 
 template <int GROUP>
 struct W4Scales;  // the scales of one lane's two rows in a tile: [row half][128 / GROUP]
 template <>
 struct W4Scales<32> {
     uint4 v;
+    __device__ __forceinline__ void load(uint32_t at)
+    {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    }
     __device__ __forceinline__ float get(int half, int grp) const
     {
         const uint32_t w = half ? (grp < 2 ? v.z : v.w) : (grp < 2 ? v.x : v.y);
@@ -35,6 +45,10 @@ struct W4Scales<32> {
 template <>
 struct W4Scales<64> {
     uint2 v;
+    __device__ __forceinline__ void load(uint32_t at)
+    {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    }
     __device__ __forceinline__ float get(int half, int grp) const
     {
         const uint32_t w = half ? v.y : v.x;
@@ -44,88 +58,182 @@ struct W4Scales<64> {
 template <>
 struct W4Scales<128> {
     uint32_t v;
+    __device__ __forceinline__ void load(uint32_t at) { asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at)); }
     __device__ __forceinline__ float get(int half, int) const
     {
         return __uint_as_float(half ? (v & 0xffff0000u) : (v << 16));
     }
 };
 
-// Codes of one pair of columns as bf16 values code - 8.
+// Codes of one pair of columns as bf16 values 128 + code.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i)
 {
-    const uint32_t b = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), __floats2bfloat162_rn(136.0f, 136.0f));
-    return *reinterpret_cast<const uint32_t*>(&v);
+    return ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
 }
 
-template <int GROUP, int NB>
-__global__ void __launch_bounds__(32 * kW4Warps) w4_matvec_kernel(const __nv_bfloat16* __restrict__ x,
-                                                                  const uint4* __restrict__ words,
-                                                                  const W4Scales<GROUP>* __restrict__ scales, int N,
-                                                                  int n, int k, int kt, __nv_bfloat16* __restrict__ y)
+// D = A * B + C, C the same for a lane's two rows.
+__device__ __forceinline__ void mma_bf16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %11, %10, %11};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
+// 16 bytes, or zeros where `on` is false.
+__device__ __forceinline__ void w4_copy16(uint32_t dst, const void* src, bool on = true)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 w4_lds128(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+
+// Row tiles [nt * block / blocks, nt * (block + 1) / blocks), at most RT of them.
+template <int GROUP, int NB, int RT>
+__global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                     const uint8_t* __restrict__ words,
+                                                                     const uint8_t* __restrict__ scales, int N, int n,
+                                                                     int k, int nt, int kt, __nv_bfloat16* __restrict__ y)
 {
     constexpr int kGroups = 128 / GROUP, kPer = GROUP / 32;  // groups a tile, 32-column steps a group
-    __shared__ float part[kW4Warps][16][8 * NB + 1];
+    constexpr int kCols = 8 * NB;
+    constexpr int kScaleBytes = 32 * kGroups;                // of a tile
+    constexpr int kStage = w4_stage(NB, RT);                 // of a warp: the weight tiles, then x
+    constexpr int kRing = kW4Stages * kStage;
+    static_assert(RT * kCols * 17 * 4 <= kRing, "a warp leaves its sums in its ring");
+    extern __shared__ __align__(128) uint8_t smem[];
     pdl_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    float acc[NB][4] = {};
-    const size_t tile0 = static_cast<size_t>(blockIdx.x) * kt;
-    for (int t = warp; t < kt; t += kW4Warps) {
-        const uint4* wp = words + (tile0 + t) * 64 + 2 * lane;
-        const uint4 w0 = ldg_stream16(wp), w1 = ldg_stream16(wp + 1);
-        const W4Scales<GROUP> sc = scales[(tile0 + t) * 8 + g];
-        uint4 xv[NB][4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, g = lane >> 2, c = lane & 3;
+    const int r0 = static_cast<int>(static_cast<long long>(nt) * blockIdx.x / gridDim.x);
+    const int tiles = static_cast<int>(static_cast<long long>(nt) * (blockIdx.x + 1) / gridDim.x) - r0;
+    const uint32_t ring = smem_u32(smem) + warp * kRing;
+    // this lane's pieces: of a weight tile 16 bytes at 16 lane and 512 behind, of x the chunk lane % 16 of rows
+    // lane / 16, lane / 16 + 2, ... (chunks of odd rows swapped in fours, for the banks of the fragments' reads)
+    const uint8_t* wsrc[RT];
+    const uint8_t* ssrc[RT];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+    for (int r = 0; r < RT; ++r) {  // (a block with fewer tiles repeats its last one: no branch between them)
+        const size_t tile = static_cast<size_t>(r0 + min(r, tiles - 1)) * kt;
+        wsrc[r] = words + tile * 1024 + lane * 16;
+        ssrc[r] = scales + tile * kScaleBytes + lane * 16;
+    }
+    const __nv_bfloat16* xsrc = x + static_cast<size_t>(lane >> 4) * k + (lane & 15) * 8;
+    const uint32_t xdst = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4) << 2)) * 16;
+    auto request = [&](int t, int stage) {
+        if (t < kt) {
+            const uint32_t st = ring + stage * kStage;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = 128 * t + 32 * j + 8 * c;
-                xv[b][j] = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * b + g < N && col < k)
-                    xv[b][j] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(8 * b + g) * k + col));
+            for (int r = 0; r < RT; ++r) {
+                const uint32_t dst = st + r * kW4Slot + lane * 16;
+                w4_copy16(dst, wsrc[r] + static_cast<size_t>(t) * 1024);
+                w4_copy16(dst + 512, wsrc[r] + static_cast<size_t>(t) * 1024 + 512);
+                if (lane < kScaleBytes / 16) w4_copy16(dst + 1024, ssrc[r] + static_cast<size_t>(t) * kScaleBytes);
             }
+            const bool in_k = 128 * t + (lane & 15) * 8 < k;
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q) {
-            float d[NB][4];
-#pragma unroll
-            for (int p = 0; p < kPer; ++p) {
-                const int j = q * kPer + p;
-                const uint32_t u = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
-                const uint32_t v = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
-                const uint32_t u0 = w4_pair(u, 0), u1 = w4_pair(u, 1), u2 = w4_pair(u, 2), u3 = w4_pair(u, 3);
-                const uint32_t v0 = w4_pair(v, 0), v1 = w4_pair(v, 1), v2 = w4_pair(v, 2), v3 = w4_pair(v, 3);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if (p == 0) mma_bf16_first(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
-                    else mma_bf16(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
-                    mma_bf16(d[b], u2, v2, u3, v3, xv[b][j].z, xv[b][j].w);
-                }
-            }
-            const float s0 = sc.get(0, q), s1 = sc.get(1, q);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                acc[b][0] = fmaf(s0, d[b][0], acc[b][0]);
-                acc[b][1] = fmaf(s0, d[b][1], acc[b][1]);
-                acc[b][2] = fmaf(s1, d[b][2], acc[b][2]);
-                acc[b][3] = fmaf(s1, d[b][3], acc[b][3]);
+            for (int i = 0; i < 4 * NB; ++i) {
+                const bool on = in_k && 2 * i + (lane >> 4) < N;
+                const __nv_bfloat16* src = on ? xsrc + static_cast<size_t>(2 * i) * k + 128 * t : x;
+                w4_copy16(st + RT * kW4Slot + xdst + i * 512, src, on);
             }
         }
-    }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        part[warp][g][8 * b + 2 * c] = acc[b][0];
-        part[warp][g][8 * b + 2 * c + 1] = acc[b][1];
-        part[warp][g + 8][8 * b + 2 * c] = acc[b][2];
-        part[warp][g + 8][8 * b + 2 * c + 1] = acc[b][3];
+    for (int s = 0; s < kW4Stages - 1; ++s) request(warp + s * warps, s);
+
+    float acc[RT][NB][4] = {};
+    int stage = 0;
+    for (int t = warp; t < kt; t += warps) {
+        __syncwarp();  // the stage to be overwritten has been read by all lanes
+        request(t + (kW4Stages - 1) * warps, stage == 0 ? kW4Stages - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kW4Stages - 1) : "memory");
+        __syncwarp();  // all lanes' copies of this stage are visible
+        const uint32_t st = ring + stage * kStage;
+        uint4 xv[NB][4];
+        float base[NB][kGroups][2];  // -136 sum x of each group, for tokens 2c and 2c + 1
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                xv[b][j] = w4_lds128(st + RT * kW4Slot + (8 * b + g) * 256 + ((4 * j + c) ^ ((g & 1) << 2)) * 16);
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) {
+                constexpr uint32_t kOnes = 0x3f803f80u;
+                float d[4];
+#pragma unroll
+                for (int p = 0; p < kPer; ++p) {
+                    const uint4 v = xv[b][q * kPer + p];
+                    if (p == 0) mma_bf16_first(d, kOnes, kOnes, kOnes, kOnes, v.x, v.y);
+                    else mma_bf16(d, kOnes, kOnes, kOnes, kOnes, v.x, v.y);
+                    mma_bf16(d, kOnes, kOnes, kOnes, kOnes, v.z, v.w);
+                }
+                base[b][q][0] = -136.0f * d[0];
+                base[b][q][1] = -136.0f * d[1];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const uint32_t at = st + r * kW4Slot;
+            const uint4 w0 = w4_lds128(at + lane * 32), w1 = w4_lds128(at + lane * 32 + 16);
+            W4Scales<GROUP> sc;
+            sc.load(at + 1024 + g * (kScaleBytes / 8));
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) {
+                float d[NB][4];
+#pragma unroll
+                for (int p = 0; p < kPer; ++p) {
+                    const int j = q * kPer + p;
+                    const uint32_t u = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
+                    const uint32_t v = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
+                    const uint32_t u0 = w4_pair(u, 0), u1 = w4_pair(u, 1), u2 = w4_pair(u, 2), u3 = w4_pair(u, 3);
+                    const uint32_t v0 = w4_pair(v, 0), v1 = w4_pair(v, 1), v2 = w4_pair(v, 2), v3 = w4_pair(v, 3);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        if (p == 0) mma_bf16_from(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y, base[b][q][0], base[b][q][1]);
+                        else mma_bf16(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
+                        mma_bf16(d[b], u2, v2, u3, v3, xv[b][j].z, xv[b][j].w);
+                    }
+                }
+                const float s0 = sc.get(0, q), s1 = sc.get(1, q);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    acc[r][b][0] = fmaf(s0, d[b][0], acc[r][b][0]);
+                    acc[r][b][1] = fmaf(s0, d[b][1], acc[r][b][1]);
+                    acc[r][b][2] = fmaf(s1, d[b][2], acc[r][b][2]);
+                    acc[r][b][3] = fmaf(s1, d[b][3], acc[r][b][3]);
+                }
+            }
+        }
+        stage = stage + 1 == kW4Stages ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    // sums: [row tiles][token columns][17] of each warp, in its ring
+    float* part = reinterpret_cast<float*>(smem + warp * kRing);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        float* p = part + r * (kCols * 17);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            p[(8 * b + 2 * c) * 17 + g] = acc[r][b][0];
+            p[(8 * b + 2 * c + 1) * 17 + g] = acc[r][b][1];
+            p[(8 * b + 2 * c) * 17 + g + 8] = acc[r][b][2];
+            p[(8 * b + 2 * c + 1) * 17 + g + 8] = acc[r][b][3];
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * N; i += blockDim.x) {
-        const int r = i & 15, tok = i >> 4;
-        const int row = blockIdx.x * 16 + r;
+    for (int i = threadIdx.x; i < 16 * tiles * N; i += blockDim.x) {
+        const int tok = i / (16 * tiles), row = i - tok * (16 * tiles);  // row of the block's tiles
+        const float* p = reinterpret_cast<const float*>(smem) + (row >> 4) * (kCols * 17) + tok * 17 + (row & 15);
         float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kW4Warps; ++w) v += part[w][r][tok];
-        if (row < n) y[static_cast<size_t>(tok) * n + row] = __float2bfloat16_rn(v);
+        for (int w = 0; w < warps; ++w) v += p[w * (kRing / 4)];
+        if (16 * r0 + row < n) y[static_cast<size_t>(tok) * n + 16 * r0 + row] = __float2bfloat16_rn(v);
     }
 }
 
@@ -170,14 +278,45 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* _
     }
 }
 
+constexpr size_t w4_smem(int warps, int nb, int rt)
+{
+    return static_cast<size_t>(warps) * kW4Stages * w4_stage(nb, rt);
+}
+
+template <int GROUP, int NB, int RT>
+twell_status launch_w4(const void* x, const void* words, const void* scales, int N, int n, int k, void* y, int blocks,
+                       cudaStream_t s)
+{
+    const int nt = (n + 15) / 16, kt = (k + 127) / 128;
+    // every warp takes the same number of column tiles where that is possible
+    const int each = (kt + kW4Warps - 1) / kW4Warps, warps = (kt + each - 1) / each;
+    const size_t smem = w4_smem(warps, NB, RT);
+    auto kern = w4_matvec_kernel<GROUP, NB, RT>;
+    static std::atomic<uint64_t> allowed{0};
+    if (twell_host::allow_smem(kern, w4_smem(kW4Warps, NB, RT), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    return twell_host::launch_dep(kern, dim3(blocks), dim3(32 * warps), smem, s, static_cast<const __nv_bfloat16*>(x),
+                                  static_cast<const uint8_t*>(words), static_cast<const uint8_t*>(scales), N, n, k, nt,
+                                  kt, static_cast<__nv_bfloat16*>(y));
+}
+
 template <int GROUP>
 twell_status run_w4(const void* x, const void* words, const void* scales, int N, int n, int k, void* y, cudaStream_t s)
 {
-    auto kern = N <= 8 ? w4_matvec_kernel<GROUP, 1> : w4_matvec_kernel<GROUP, 2>;
-    return twell_host::launch_dep(kern, dim3((n + 15) / 16), dim3(32 * kW4Warps), 0, s,
-                                  static_cast<const __nv_bfloat16*>(x), static_cast<const uint4*>(words),
-                                  static_cast<const W4Scales<GROUP>*>(scales), N, n, k, (k + 127) / 128,
-                                  static_cast<__nv_bfloat16*>(y));
+    twell_host::DevInfo dev;
+    if (twell_host::dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
+    // two blocks an SM as long as their row tiles cover the rows, then whole rounds of them
+    const int nt = (n + 15) / 16, slots = 2 * dev.sm_count, per = w4_tiles(N <= 8 ? 1 : 2);
+    const int blocks = nt <= slots ? nt : slots * ((nt + per * slots - 1) / (per * slots));
+    const int most = (nt + blocks - 1) / blocks;
+    if (N <= 8) {
+        if (most == 1) return launch_w4<GROUP, 1, 1>(x, words, scales, N, n, k, y, blocks, s);
+        if (most == 2) return launch_w4<GROUP, 1, 2>(x, words, scales, N, n, k, y, blocks, s);
+        if (most == 3) return launch_w4<GROUP, 1, 3>(x, words, scales, N, n, k, y, blocks, s);
+        return launch_w4<GROUP, 1, 4>(x, words, scales, N, n, k, y, blocks, s);
+    }
+    if (most == 1) return launch_w4<GROUP, 2, 1>(x, words, scales, N, n, k, y, blocks, s);
+    if (most == 2) return launch_w4<GROUP, 2, 2>(x, words, scales, N, n, k, y, blocks, s);
+    return launch_w4<GROUP, 2, 3>(x, words, scales, N, n, k, y, blocks, s);
 }
 
 bool w4_shape_ok(int n, int k, int group) { return n > 0 && k > 0 && group > 0 && k % 32 == 0 && k % group == 0; }
