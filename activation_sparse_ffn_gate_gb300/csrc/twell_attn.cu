@@ -50,7 +50,10 @@ struct AttnCfg {
     static constexpr int kSwizzle = kChunks % 8 == 0 ? 7 : (kChunks % 4 == 0 ? 3 : 1);
     static constexpr int kHalf = kTileTokens * kRow;    // bytes of a tile's keys, or its values
     static constexpr int kSlot = kHalf + (Q8 ? 2 * kTileTokens * 4 : 0);  // with keys: both scales behind them
-    static constexpr int kWarps = HD == 256 ? (Q8 ? 8 : 4) : ((Q8 || HD == 64) && NT == 1 ? 16 : 8);
+    // Enough warps to keep up with the copies, few enough for three slots each and for ranges that are many tiles
+    // long: 64 sequences of up to 16384 tokens, e4m3, head_dim 128: 97.9 us with 16 warps, 94.7 with 12, 98.6 with 8;
+    // 8 of up to 32768, e4m3, head_dim 64: 35.9, 43.8, 41.0.
+    static constexpr int kWarps = HD == 256 ? (Q8 ? 8 : 4) : NT == 2 || kHalf > 4096 ? 8 : kHalf > 2048 ? 12 : 16;
     static constexpr int kFit = 212000 / (kWarps * kSlot);
     static constexpr int kSlots = kFit >= 7 ? 7 : kFit >= 5 ? 5 : 3;  // odd: keys are requested while keys are used
     static_assert(kFit >= 3, "the ring overlaps copies with the products");
@@ -238,8 +241,8 @@ struct AttnState {
         }
     }
 
-    // The query's fragments, as bf16: requested here, brought into their final form by finish_q.
-    __device__ __forceinline__ void load_q(const AttnArgs& a, int b, int hv, int lane)
+    // A query's fragments, as bf16: requested here, brought into their final form by finish_q.
+    __device__ __forceinline__ static void load_q(uint32_t (&q)[NT][kQ], const AttnArgs& a, int b, int hv, int lane)
     {
         const int g = lane >> 2, c = lane & 3;
         const int kvh = hv / a.blocks, first = (hv % a.blocks) * 8 * NT;
@@ -547,16 +550,17 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int b, int hv, int 
             l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// Parts joined for one float4 of o (fragment `ni` = eight heads x dimension tile, this lane) and the two heads it
-// belongs to: their maximum first, then the sums under it, so that no exponential waits for the one before.
-template <class C>
+// Parts joined for F float4 of o (fragments ni .. ni + F - 1 = eight heads x F dimension tiles, this lane) and the two
+// heads they belong to: their maximum first, then the sums under it, so that no exponential waits for the one before.
+template <class C, int F>
 struct Joined {
     float m0 = kNegInf, m1 = kNegInf, l0 = 0.0f, l1 = 0.0f;
-    float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float r[F][4] = {};
 
+    __device__ __forceinline__ Joined() {}
     // part(i), i < count: where part i is
-    template <typename F>
-    __device__ __forceinline__ Joined(int count, int ni, int lane, F part)
+    template <typename P>
+    __device__ __forceinline__ Joined(int count, int ni, int lane, P part)
     {
         const int ml = C::kPartF + ni / C::kMt * 16 + 2 * (lane & 3);
 #pragma unroll 4
@@ -566,24 +570,29 @@ struct Joined {
             m1 = fmaxf(m1, pm.y);
         }
         const float b0 = m0 == kNegInf ? 0.0f : m0, b1 = m1 == kNegInf ? 0.0f : m1;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < count; ++i) {
             const float* p = part(i);
             const float2 pm = *reinterpret_cast<const float2*>(p + ml), pl = *reinterpret_cast<const float2*>(p + ml + 8);
-            const float4 v = reinterpret_cast<const float4*>(p)[ni * 32 + lane];
             const float f0 = exp2_approx(pm.x - b0), f1 = exp2_approx(pm.y - b1);
-            r[0] = fmaf(v.x, f0, r[0]);
-            r[1] = fmaf(v.y, f1, r[1]);
-            r[2] = fmaf(v.z, f0, r[2]);
-            r[3] = fmaf(v.w, f1, r[3]);
             l0 = fmaf(pl.x, f0, l0);
             l1 = fmaf(pl.y, f1, l1);
+#pragma unroll
+            for (int f = 0; f < F; ++f) add(f, reinterpret_cast<const float4*>(p)[(ni + f) * 32 + lane], f0, f1);
         }
     }
-    __device__ __forceinline__ Joined() {}
+    __device__ __forceinline__ void add(int f, const float4& v, float f0, float f1)
+    {
+        r[f][0] = fmaf(v.x, f0, r[f][0]);
+        r[f][1] = fmaf(v.y, f1, r[f][1]);
+        r[f][2] = fmaf(v.z, f0, r[f][2]);
+        r[f][3] = fmaf(v.w, f1, r[f][3]);
+    }
     __device__ __forceinline__ void store(float* part, int ni, int lane) const
     {
-        reinterpret_cast<float4*>(part)[ni * 32 + lane] = make_float4(r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            reinterpret_cast<float4*>(part)[(ni + f) * 32 + lane] = make_float4(r[f][0], r[f][1], r[f][2], r[f][3]);
         if (ni % C::kMt == 0 && lane < 4) {
             float* ml = part + C::kPartF + ni / C::kMt * 16 + 2 * lane;
             *reinterpret_cast<float2*>(ml) = make_float2(m0, m1);
@@ -592,13 +601,14 @@ struct Joined {
     }
 };
 
-template <int HD, bool Q8, int NT>
+template <int HD, bool Q8, int NT, int F>
 __device__ __forceinline__ void store_joined(const AttnArgs& a, int bhv, int HV, int ni, int lane,
-                                             const Joined<AttnCfg<HD, Q8, NT>>& J)
+                                             const Joined<AttnCfg<HD, Q8, NT>, F>& J)
 {
     constexpr int kMt = AttnCfg<HD, Q8, NT>::kMt;
     const int b = bhv / HV, hv = bhv % HV, e = ni / kMt;
-    store_out<HD, Q8, NT>(a, b, hv, e, ni % kMt, lane, J.r, J.l0, J.l1);
+#pragma unroll
+    for (int f = 0; f < F; ++f) store_out<HD, Q8, NT>(a, b, hv, e, ni % kMt + f, lane, J.r[f], J.l0, J.l1);
     if (ni % kMt == 0 && lane < 4) {
         store_lse<NT>(a, b, hv, e * 8 + 2 * lane, J.m0, J.l0);
         store_lse<NT>(a, b, hv, e * 8 + 2 * lane + 1, J.m1, J.l1);
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
     constexpr int kAhead = (C::kSlots - 1) / 2;  // tiles
     AttnState<HD, Q8, NT> S;
     uint32_t vis_ring = 0;  // lane i: the visible tokens of the tile i (modulo 32) of the range
-    if (n > 0) S.load_q(a, cur.b, cur.hv, lane);
+    if (n > 0) S.load_q(S.q, a, cur.b, cur.hv, lane);
     int pages[kAhead + 1];  // of the first tiles, requested together
     {
         Cursor at = cur;
@@ -816,6 +826,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
     }
     __syncthreads();  // run_bhv, warp_start
 
+    Cursor next;
     uint32_t slot = 0, free_slot = C::kSlots - 1;  // to be used, to be requested into
     auto advance = [&]() {
         free_slot = slot;
@@ -825,6 +836,13 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
         cp_wait<C::kSlots - 2>();
         __syncwarp();  // all lanes' copies of this slot are visible, and the one before has been read by all
         const uint32_t vis = __shfl_sync(0xffffffffu, vis_ring, it & 31);
+        const bool seg_end = cur.tile + 1 == cur.s.tiles;
+        uint32_t next_q[NT][AttnState<HD, Q8, NT>::kQ];  // of the (sequence, key head) that the next tile begins
+        if (seg_end && it + 1 < n) {
+            next = cur;
+            next.next(a, HV);
+            S.load_q(next_q, a, next.b, next.hv, lane);
+        }
         if (it + kAhead < n) {
             request_keys(ring + free_slot * C::kSlot);
             if (lane == ((it + kAhead) & 31)) vis_ring = tile_vis;
@@ -843,7 +861,6 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
         S.values(ring + slot * C::kSlot, lane);
         advance();
 
-        const bool seg_end = cur.tile + 1 == cur.s.tiles;
         if (seg_end || it + 1 == n) {
             S.close();
             if (seg_end && it >= cur.tile) {  // its first tile was this warp's too
@@ -876,8 +893,11 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
                 }
             }
             if (it + 1 < n) {
-                cur.next(a, HV);
-                S.load_q(a, cur.b, cur.hv, lane);
+                cur = next;
+#pragma unroll
+                for (int e = 0; e < NT; ++e)
+#pragma unroll
+                    for (int i = 0; i < AttnState<HD, Q8, NT>::kQ; ++i) S.q[e][i] = next_q[e][i];
                 S.reset();
                 S.finish_q(a, lane);
             }
@@ -888,13 +908,16 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
     cp_wait<0>();
     __syncthreads();
 
-    // join the parts of what spans warps: one fragment of one of them a warp at a time
+    // join the parts of what spans warps: kF fragments of one of them a warp at a time
+    constexpr int kF = C::kMt % 4 == 0 ? 4 : 3, kItems = NT * C::kMt / kF;
     const uint32_t runs = __ballot_sync(0xffffffffu, lane <= C::kWarps && run_bhv[min(lane, C::kWarps)] >= 0);
-    const int items = __popc(runs) * (NT * C::kMt);
+    const int items = __popc(runs) * kItems;
     const long long c_start = warp_start[0], c_end = warp_start[C::kWarps];
     for (int it = warp; it < items; it += C::kWarps) {
-        const int ni = it % (NT * C::kMt);
-        const int run = __fns(runs, 0, it / (NT * C::kMt) + 1);
+        const int ni = it % kItems * kF;
+        uint32_t rest = runs;  // the (it / kItems)-th run
+        for (int i = it / kItems; i > 0; --i) rest &= rest - 1u;
+        const int run = __ffs(rest) - 1;
         const long long i0 = run_i0[run], i1 = run_i1[run];
         const float* head = a.head_part + static_cast<int64_t>(w0) * C::kPart;
         // the run's warps: from run - 1 to the last whose range starts before i1; that one has left its part in
@@ -903,12 +926,12 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, lane == first || (lane < C::kWarps && lane > first && run != 0 &&
                                                                              warp_start[min(lane, C::kWarps)] < i1)));
         const bool last_head = run == 0 || (last != first && warp_start[last + 1] > i1);
-        const Joined<C> J(last - first + 1, ni, lane, [&](int i) {
+        const Joined<C, kF> J(last - first + 1, ni, lane, [&](int i) {
             const int q = first + i;
             return q == last && last_head ? head + static_cast<int64_t>(q) * C::kPart
                                           : reinterpret_cast<const float*>(smem + q * C::kRing);
         });
-        if (i0 >= c_start && i1 <= c_end) store_joined<HD, Q8, NT>(a, run_bhv[run], HV, ni, lane, J);
+        if (i0 >= c_start && i1 <= c_end) store_joined<HD, Q8, NT, kF>(a, run_bhv[run], HV, ni, lane, J);
         else J.store(a.block_part + (2 * static_cast<int64_t>(blockIdx.x) + (i0 < c_start ? 0 : 1)) * C::kPart, ni, lane);
     }
 }
@@ -921,7 +944,7 @@ struct JoinCfg {
     static constexpr int kFrags = NT * (HD / 16);
     static constexpr int kGroups = std::max(1, 32 / kFrags);
     static constexpr int kThreads = kGroups * kFrags * 32;
-    static constexpr int kBatch = 6;  // parts of a group requested before the weights are known
+    static constexpr int kBatch = 8;  // parts of a group requested before the weights are known
 };
 template <int HD, bool Q8, int NT>
 __global__ void __launch_bounds__(JoinCfg<HD, Q8, NT>::kThreads, 1) paged_attn_join_kernel(const AttnArgs a)
@@ -972,34 +995,28 @@ __global__ void __launch_bounds__(JoinCfg<HD, Q8, NT>::kThreads, 1) paged_attn_j
         }
     }
     __syncthreads();
-    Joined<C> J;
+    Joined<C, 1> J;
     const int h = ni / C::kMt * 8 + 2 * (lane & 3);
-    auto add = [&](const float4& u, float f0, float f1) {
-        J.r[0] = fmaf(u.x, f0, J.r[0]);
-        J.r[1] = fmaf(u.y, f1, J.r[1]);
-        J.r[2] = fmaf(u.z, f0, J.r[2]);
-        J.r[3] = fmaf(u.w, f1, J.r[3]);
-    };
 #pragma unroll
     for (int i = 0; i < K::kBatch; ++i) {
         const int p = grp + i * K::kGroups;
-        if (p < count) add(v[i], s_m[p][h], s_m[p][h + 1]);
+        if (p < count) J.add(0, v[i], s_m[p][h], s_m[p][h + 1]);
     }
 #pragma unroll 4
     for (int p = grp + K::kBatch * K::kGroups; p < count; p += K::kGroups)
-        add(reinterpret_cast<const float4*>(part(p))[ni * 32 + lane], s_m[p][h], s_m[p][h + 1]);
+        J.add(0, reinterpret_cast<const float4*>(part(p))[ni * 32 + lane], s_m[p][h], s_m[p][h + 1]);
     if (K::kGroups > 1) {  // the groups' sums, in group order
-        s_sum[threadIdx.x] = make_float4(J.r[0], J.r[1], J.r[2], J.r[3]);
+        s_sum[threadIdx.x] = make_float4(J.r[0][0], J.r[0][1], J.r[0][2], J.r[0][3]);
         __syncthreads();
         if (grp != 0) return;
 #pragma unroll
-        for (int q = 1; q < K::kGroups; ++q) add(s_sum[(q * K::kFrags + ni) * 32 + lane], 1.0f, 1.0f);
+        for (int q = 1; q < K::kGroups; ++q) J.add(0, s_sum[(q * K::kFrags + ni) * 32 + lane], 1.0f, 1.0f);
     }
     J.m0 = s_top[h];
     J.m1 = s_top[h + 1];
     J.l0 = s_tot[h];
     J.l1 = s_tot[h + 1];
-    store_joined<HD, Q8, NT>(a, sp.x, a.c.heads * a.blocks, ni, lane, J);
+    store_joined<HD, Q8, NT, 1>(a, sp.x, a.c.heads * a.blocks, ni, lane, J);
 }
 
 template <int HD, bool Q8, int NT>

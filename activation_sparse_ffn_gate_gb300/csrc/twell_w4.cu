@@ -5,11 +5,10 @@
 // cores' fragments want them: a tile of 16 rows by 128 columns is 1 KB, lane (g, c) of a warp (g < 8,
 // c < 4) owning 32 consecutive bytes of it: for rows g and g + 8, the columns 32j + 8c .. + 7, j < 4. A
 // word holds 8 columns of a row, column 2i in bits 4i .. 4i + 3 and column 2i + 1 in bits 16 + 4i ..., so
-// one shift and mask gives the pair an mma.sync m16n8k16 register wants: or-ed into bf16 128.0, it is the pair
-// 128 + code, exactly. Rows are the product's 16-row side and tokens its 8 columns; a group's products are
-// summed in fp32 by the tensor core on top of -136 sum x (so that what is summed is (code - 8) x; sum x of each
-// group comes from a product with ones, once for all rows of a block) and added to the total times the group's
-// scale in fp32. Scales lie beside the tile in the same order ([g][half][128 / group]).
+// one shift and mask gives the pair an mma.sync m16n8k16 register wants. The pair becomes bf16 exactly (or-ed into
+// 128.0 it is 128 + code; minus 136); rows are the product's 16-row side and tokens its 8 columns, a group's
+// products are summed in fp32 by the tensor core and added to the total times the group's scale in fp32, so x and
+// the codes enter exactly. Scales lie beside the tile in the same order ([g][half][128 / group]).
 // A block takes up to 4 row tiles and its warps every n-th column tile of them each: a fragment of x is loaded once
 // for those row tiles, and a warp copies weights, scales and x into its own shared-memory ring a column tile
 // ahead. The warps' sums are added in warp order in shared memory (no atomics: the same y from call to call).
@@ -65,26 +64,17 @@ struct W4Scales<128> {
     }
 };
 
-// Codes of one pair of columns as bf16 values 128 + code.
+// A pair of columns of a word as bf16 values code - 8, exactly.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i)
 {
-    return ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const uint32_t b = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), __floats2bfloat162_rn(136.0f, 136.0f));
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// D = A * B + C, C the same for a lane's two rows.
-__device__ __forceinline__ void mma_bf16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1, float c0, float c1)
+__device__ __forceinline__ void w4_copy16(uint32_t dst, const void* src)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%10, %11, %10, %11};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
-}
-
-// 16 bytes, or zeros where `on` is false.
-__device__ __forceinline__ void w4_copy16(uint32_t dst, const void* src, bool on = true)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 w4_lds128(uint32_t a)
 {
@@ -114,33 +104,52 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_
     const uint32_t ring = smem_u32(smem) + warp * kRing;
     // this lane's pieces: of a weight tile 16 bytes at 16 lane and 512 behind, of x the chunk lane % 16 of rows
     // lane / 16, lane / 16 + 2, ... (chunks of odd rows swapped in fours, for the banks of the fragments' reads)
-    const uint8_t* wsrc[RT];
-    const uint8_t* ssrc[RT];
+    const size_t first = static_cast<size_t>(r0) * kt + warp;
+    const uint8_t* wsrc = words + first * 1024 + lane * 16;
+    const uint8_t* ssrc = scales + first * kScaleBytes + lane * 16;
+    size_t row_of[RT];  // row tile r, in tiles (a block with fewer repeats its last one: no branch between them)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {  // (a block with fewer tiles repeats its last one: no branch between them)
-        const size_t tile = static_cast<size_t>(r0 + min(r, tiles - 1)) * kt;
-        wsrc[r] = words + tile * 1024 + lane * 16;
-        ssrc[r] = scales + tile * kScaleBytes + lane * 16;
-    }
-    const __nv_bfloat16* xsrc = x + static_cast<size_t>(lane >> 4) * k + (lane & 15) * 8;
-    const uint32_t xdst = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4) << 2)) * 16;
+    for (int r = 0; r < RT; ++r) row_of[r] = static_cast<size_t>(min(r, tiles - 1)) * kt;
+    const int xrow = lane >> 4, xcol = (lane & 15) * 8;
+    const __nv_bfloat16* xsrc = x + static_cast<size_t>(xrow) * k + 128 * warp + xcol;
+    const size_t xstep = 2 * static_cast<size_t>(k);
+    const uint32_t xdst = RT * kW4Slot + xrow * 256 + ((lane & 15) ^ (xrow << 2)) * 16;
+    // rows of x past the last token are zeros in both stages; columns past the last one become so in their stage
+    auto zero16 = [](uint32_t at) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < 4 * NB; ++i)
+        if (2 * i + xrow >= N) {
+#pragma unroll
+            for (int s = 0; s < kW4Stages; ++s) zero16(ring + s * kStage + xdst + i * 512);
+        }
     auto request = [&](int t, int stage) {
         if (t < kt) {
             const uint32_t st = ring + stage * kStage;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const uint32_t dst = st + r * kW4Slot + lane * 16;
-                w4_copy16(dst, wsrc[r] + static_cast<size_t>(t) * 1024);
-                w4_copy16(dst + 512, wsrc[r] + static_cast<size_t>(t) * 1024 + 512);
-                if (lane < kScaleBytes / 16) w4_copy16(dst + 1024, ssrc[r] + static_cast<size_t>(t) * kScaleBytes);
+                const uint8_t* w = wsrc + row_of[r] * 1024;
+                w4_copy16(dst, w);
+                w4_copy16(dst + 512, w + 512);
+                if (lane < kScaleBytes / 16) w4_copy16(dst + 1024, ssrc + row_of[r] * kScaleBytes);
             }
-            const bool in_k = 128 * t + (lane & 15) * 8 < k;
+            if (128 * t + xcol < k) {
+                const __nv_bfloat16* src = xsrc;
 #pragma unroll
-            for (int i = 0; i < 4 * NB; ++i) {
-                const bool on = in_k && 2 * i + (lane >> 4) < N;
-                const __nv_bfloat16* src = on ? xsrc + static_cast<size_t>(2 * i) * k + 128 * t : x;
-                w4_copy16(st + RT * kW4Slot + xdst + i * 512, src, on);
+                for (int i = 0; i < 4 * NB; ++i) {
+                    if (2 * i + xrow < N) w4_copy16(st + xdst + i * 512, src);
+                    src += xstep;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i)
+                    if (2 * i + xrow < N) zero16(st + xdst + i * 512);
             }
+            wsrc += warps * 1024;
+            ssrc += warps * kScaleBytes;
+            xsrc += warps * 128;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -156,26 +165,11 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_
         __syncwarp();  // all lanes' copies of this stage are visible
         const uint32_t st = ring + stage * kStage;
         uint4 xv[NB][4];
-        float base[NB][kGroups][2];  // -136 sum x of each group, for tokens 2c and 2c + 1
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 xv[b][j] = w4_lds128(st + RT * kW4Slot + (8 * b + g) * 256 + ((4 * j + c) ^ ((g & 1) << 2)) * 16);
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                constexpr uint32_t kOnes = 0x3f803f80u;
-                float d[4];
-#pragma unroll
-                for (int p = 0; p < kPer; ++p) {
-                    const uint4 v = xv[b][q * kPer + p];
-                    if (p == 0) mma_bf16_first(d, kOnes, kOnes, kOnes, kOnes, v.x, v.y);
-                    else mma_bf16(d, kOnes, kOnes, kOnes, kOnes, v.x, v.y);
-                    mma_bf16(d, kOnes, kOnes, kOnes, kOnes, v.z, v.w);
-                }
-                base[b][q][0] = -136.0f * d[0];
-                base[b][q][1] = -136.0f * d[1];
-            }
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -195,7 +189,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_
                     const uint32_t v0 = w4_pair(v, 0), v1 = w4_pair(v, 1), v2 = w4_pair(v, 2), v3 = w4_pair(v, 3);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        if (p == 0) mma_bf16_from(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y, base[b][q][0], base[b][q][1]);
+                        if (p == 0) mma_bf16_first(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
                         else mma_bf16(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
                         mma_bf16(d[b], u2, v2, u3, v3, xv[b][j].z, xv[b][j].w);
                     }
@@ -306,7 +300,7 @@ twell_status run_w4(const void* x, const void* words, const void* scales, int N,
     if (twell_host::dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
     // two blocks an SM as long as their row tiles cover the rows, then whole rounds of them
     const int nt = (n + 15) / 16, slots = 2 * dev.sm_count, per = w4_tiles(N <= 8 ? 1 : 2);
-    const int blocks = nt <= slots ? nt : slots * ((nt + per * slots - 1) / (per * slots));
+    const int blocks = std::min(nt, slots * ((nt + per * slots - 1) / (per * slots)));  // no block without a tile
     const int most = (nt + blocks - 1) / blocks;
     if (N <= 8) {
         if (most == 1) return launch_w4<GROUP, 1, 1>(x, words, scales, N, n, k, y, blocks, s);
