@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libtwell_gb300.so (the C ABI declared in include/twell.h).
+"""Thin binding over libtwell_gb300.so (the C ABI declared in include/twell.h): ctypes for the FFN's calls, the native
+module _twell_call for those that a decode step makes many of.
 
 Argument marshalling only: every step of the layer runs in the library's CUDA kernels. PyTorch
 provides device memory and the current CUDA stream. The functions carry the C names; each
@@ -10,8 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-import functools
-import math
+import importlib
 import os
 import threading
 from typing import Optional
@@ -76,11 +76,12 @@ class _KVCache(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_native = None  # the module _twell_call, once load() has imported it
 
 
 def load(path: str = LIB_PATH):
-    """Load the library (raises if it has not been built)."""
-    global _lib
+    """Load the library and the native calls beside it (raises if they have not been built)."""
+    global _lib, _native
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -145,6 +146,11 @@ def load(path: str = LIB_PATH):
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+            try:
+                _native = importlib.import_module("._twell_call", __package__)
+            except ImportError as e:
+                raise RuntimeError(f"the native calls are missing ({e}): build them with "
+                                   "activation_sparse_ffn_gate_gb300.build.build()") from e
             _lib = lib
     return _lib
 
@@ -825,69 +831,23 @@ def twell_hybrid_route_noalloc(a: TwELL, K: int, ctx: Hybrid, stream=None) -> Hy
 
 # ------------------------------------------------------------------- the decoder layer around the FFN
 
-# A decode step makes many calls whose kernels take a few microseconds, so these check and marshal with as
-# few operations as they can: integers for devices and streams, no objects made per call.
+# A decode step makes many calls whose kernels take a few microseconds, so their tensors are checked and their
+# pointers, stream and workspace taken by the native module _twell_call (csrc/twell_call.cpp): a tensor of the wrong
+# shape, type, layout or device raises ValueError there.
 
-_DTYPE_CODES = {torch.bfloat16: TWELL_BF16, torch.float32: TWELL_F32}
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+def _calls():
+    """The native module (load() imports it beside the library)."""
+    if _native is None:
+        load()
+    return _native
 
 
-def _raw_stream(stream, index: int) -> int:
-    return _current_raw_stream(index) if stream is None else stream.cuda_stream
-
-
-def _status_ptr(status, index: int) -> int:
+def _status(status, index: int) -> torch.Tensor:
     if status is None:
         status = _status_bufs.get(index)
         if status is None:
             status = status_buffer(torch.device("cuda", index))
-    return status.data_ptr()
-
-
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _index(t: torch.Tensor, what: str) -> int:
-    i = t.get_device()
-    if i < 0:
-        raise ValueError(f"{what} is on {t.device}")
-    return i
-
-
-def _need(t: torch.Tensor, shape, dtype, what: str, index: int) -> torch.Tensor:
-    """A contiguous tensor of that shape and type on that CUDA device, or ValueError."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != index:
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, not "
-                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t
-
-
-def _code(dtype: torch.dtype) -> int:
-    c = _DTYPE_CODES.get(dtype)
-    return c if c is not None else _dtype_code(dtype)
-
-
-_layer_ws = {}
-
-
-@functools.lru_cache(maxsize=4096)
-def _layer_ws_bytes(op: int, N: int, d: int) -> int:
-    return int(load().twell_workspace_bytes(op, N, d, 1, 0, 0, 0))
-
-
-def _stream_workspace(op: int, N: int, d: int, index: int, stream, raw: int) -> torch.Tensor:
-    """A workspace per operator, device and stream, grown on demand: calls on one stream run one after
-    the other, so they can share it. It is allocated on that stream, so that an outgrown one is not
-    handed out again before the calls that use it are done."""
-    nbytes = _layer_ws_bytes(op, N, d)
-    key = (op, index, raw)
-    ws = _layer_ws.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(index)):
-            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=torch.device("cuda", index))
-        _layer_ws[key] = ws
-    return ws
+    return status
 
 
 @dataclasses.dataclass
@@ -906,36 +866,6 @@ class Rows8:
                      torch.empty((n_rows, ng), dtype=torch.float32, device=device), group)
 
 
-def _rmsnorm_fwd(x, w, res, eps, h, y, y8, rstd, stream):
-    dev = _index(x, "x")
-    dt = rt = x.dtype
-    shape = x.shape
-    N, d = shape
-    _need(x, shape, dt, "x", dev)
-    _need(w, (d,), dt, "w", dev)
-    if res is not None:
-        rt = res.dtype
-        _need(res, shape, rt, "res", dev)
-        h = torch.empty_like(res) if h is None else _need(h, shape, rt, "h", dev)
-    elif h is not None:
-        raise ValueError("h is the sum x + res: without res it is x")
-    if rstd is not None:
-        _need(rstd, (N,), torch.float32, "rstd", dev)
-    if y is not None:
-        _need(y, shape, dt, "y", dev)
-    q = sc = None
-    group = 0
-    if y8 is not None:
-        group = y8.group
-        q = _need(y8.values, shape, torch.float8_e4m3fn, "the 8-bit rows", dev).data_ptr()
-        sc = _need(y8.scale, (N, -(-d // group) if group else 1), torch.float32, "the 8-bit rows' scale", dev).data_ptr()
-    code = (_lib or load()).twell_add_rmsnorm_fwd(x.data_ptr(), _p(res), w.data_ptr(), N, d, eps, _code(dt), _code(rt),
-                                                  _p(h), _p(y), q, sc, group, _p(rstd), _raw_stream(stream, dev))
-    if code:
-        _check(code, "twell_add_rmsnorm_fwd")
-    return h
-
-
 def twell_add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, res: Optional[torch.Tensor] = None, eps: float = 1e-6,
                           y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
                           rstd: Optional[torch.Tensor] = None, training: bool = False, stream=None):
@@ -944,11 +874,17 @@ def twell_add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, res: Optional[torch.
     x [N, d] and w [d] in one type (bf16 or fp32), res in that type or fp32. Returns (y, h, rstd): h is None
     without res (it is x then), rstd None unless training is set or a buffer given. h may be res itself
     and y may be x: the call then works in place."""
-    N = x.shape[0]
-    y = y if y is not None else torch.empty_like(x)
+    if y is None:
+        y = torch.empty_like(x)
+    if h is None and res is not None:
+        h = torch.empty_like(res)
     if rstd is None and training:
-        rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
-    return y, _rmsnorm_fwd(x, w, res, eps, h, y, None, rstd, stream), rstd
+        rstd = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    code = (_native or _calls()).add_rmsnorm_fwd(x, w, res, eps, h, y, None, None, 0, rstd,
+                                                 None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "twell_add_rmsnorm_fwd")
+    return y, h, rstd
 
 
 def twell_add_rmsnorm_fwd_q8(x: torch.Tensor, w: torch.Tensor, res: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -957,11 +893,17 @@ def twell_add_rmsnorm_fwd_q8(x: torch.Tensor, w: torch.Tensor, res: Optional[tor
                              training: bool = False, stream=None):
     """twell_add_rmsnorm_fwd with y in e4m3, one scale a row (group 0) or per 128 columns (group 128):
     returns (Rows8, h, rstd). y is written in x's type as well when a buffer for it is given."""
-    N, d = x.shape
-    out = out if out is not None else Rows8.empty(N, d, group, x.device)
+    if out is None:
+        out = Rows8.empty(*x.shape, group, x.device)
+    if h is None and res is not None:
+        h = torch.empty_like(res)
     if rstd is None and training:
-        rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
-    return out, _rmsnorm_fwd(x, w, res, eps, h, y, out, rstd, stream), rstd
+        rstd = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    code = (_native or _calls()).add_rmsnorm_fwd(x, w, res, eps, h, y, out.values, out.scale, out.group, rstd,
+                                                 None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "twell_add_rmsnorm_fwd")
+    return out, h, rstd
 
 
 def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor,
@@ -970,24 +912,12 @@ def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rs
     """Gradients of the call above from its h (x where it had no res) and rstd: returns (dx, dw), dx the
     gradient of x and of res alike, dw fp32. dy, dh (the gradient that reaches h from the residual
     stream, or None) and dx share a type, bf16 or fp32."""
-    dev = _index(h, "h")
-    shape = h.shape
-    N, d = shape
-    gt = dy.dtype
-    _need(h, shape, h.dtype, "h", dev)
-    _need(dy, shape, gt, "dy", dev)
-    _need(w, (d,), w.dtype, "w", dev)
-    _need(rstd, (N,), torch.float32, "rstd", dev)
-    if dh is not None:
-        _need(dh, shape, gt, "dh", dev)
-    dx = torch.empty_like(dy) if dx is None else _need(dx, shape, gt, "dx", dev)
-    dw = torch.empty((d,), dtype=torch.float32, device=h.device) if dw is None else _need(dw, (d,), torch.float32, "dw", dev)
-    s = _raw_stream(stream, dev)
-    if ws is None:
-        ws = _stream_workspace(OP_ADD_RMSNORM_BWD, N, d, dev, stream, s)
-    code = (_lib or load()).twell_add_rmsnorm_bwd(dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _p(dh), N, d,
-                                                  _code(w.dtype), _code(h.dtype), _code(gt), dx.data_ptr(), dw.data_ptr(),
-                                                  ws.data_ptr(), ws.numel(), s)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dw is None:
+        dw = torch.empty(h.shape[1:], dtype=torch.float32, device=h.device)
+    code = (_native or _calls()).add_rmsnorm_bwd(dy, h, w, rstd, dh, dx, dw, ws,
+                                                 None if stream is None else stream.cuda_stream)
     if code:
         _check(code, "twell_add_rmsnorm_bwd")
     return dx, dw
@@ -1022,13 +952,13 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
-        self._inner = (self.head_dim, 1)
         # a page of one token has no token stride of its own
         ts = k.stride(2) if self.page_size > 1 else self.head_dim
         self._c = _KVCache(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
-                           TWELL_E4M3 if q8 else TWELL_BF16, k.data_ptr(), v.data_ptr(), _p(k_scale), _p(v_scale),
+                           TWELL_E4M3 if q8 else TWELL_BF16, k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if q8 else None,
+                           v_scale.data_ptr() if q8 else None,
                            k.stride(0), k.stride(1), ts, sp, sh)
-        self._ref = ctypes.pointer(self._c)
+        self._at = ctypes.addressof(self._c)
 
     @staticmethod
     def empty(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
@@ -1046,18 +976,9 @@ def twell_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: tor
                     stream=None) -> None:
     """Write n tokens' keys and values (bf16 [n, n_kv_heads, head_dim]; any token stride, heads
     contiguous) to their slots (int32 [n], -1 = skip), quantised where the cache is in e4m3."""
-    n = slots.numel()
     dev = cache.index
-    _need(slots, (n,), torch.int32, "slots", dev)
-    shape = (n, cache.n_kv_heads, cache.head_dim)
-    lk = lv = shape[1] * shape[2]
-    for t, what in ((k, "k"), (v, "v")):
-        if t.shape != shape or t.dtype != torch.bfloat16 or t.get_device() != dev or (n and t.stride()[1:] != cache._inner):
-            raise ValueError(f"{what} must be bf16 {shape} on {cache.device} with contiguous heads")
-    if n > 1:
-        lk, lv = k.stride(0), v.stride(0)
-    code = (_lib or load()).twell_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), lk, lv, slots.data_ptr(), n,
-                                            _status_ptr(status, dev), _raw_stream(stream, dev))
+    code = (_native or _calls()).kv_append(cache._at, dev, k, v, slots, _status(status, dev),
+                                           None if stream is None else stream.cuda_stream)
     if code:
         _check(code, "twell_kv_append")
 
@@ -1065,14 +986,13 @@ def twell_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: tor
 def twell_kv_gather(cache: KVCache, slots: torch.Tensor, k_out: Optional[torch.Tensor] = None,
                     v_out: Optional[torch.Tensor] = None, status=None, stream=None):
     """Read slots back: (k, v), bf16 [n, n_kv_heads, head_dim]; zeros for slot -1."""
-    n = slots.numel()
     dev = cache.index
-    _need(slots, (n,), torch.int32, "slots", dev)
-    shape = (n, cache.n_kv_heads, cache.head_dim)
-    k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if t is None else
-                    _need(t, shape, torch.bfloat16, what, dev) for t, what in ((k_out, "k_out"), (v_out, "v_out")))
-    code = (_lib or load()).twell_kv_gather(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
-                                            _status_ptr(status, dev), _raw_stream(stream, dev))
+    if k_out is None:
+        k_out = torch.empty((slots.numel(), cache.n_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty((slots.numel(), cache.n_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+    code = (_native or _calls()).kv_gather(cache._at, dev, slots, k_out, v_out, _status(status, dev),
+                                           None if stream is None else stream.cuda_stream)
     if code:
         _check(code, "twell_kv_gather")
     return k_out, v_out
@@ -1090,28 +1010,12 @@ def twell_paged_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.T
     [B, n_q_heads] (natural logarithm of the sum of exponentials) is written when a buffer is given. A
     sequence of length 0 gives zeros and -inf."""
     dev = cache.index
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != cache.head_dim or q.dtype != torch.bfloat16 or q.get_device() != dev or \
-            (q.numel() and q.stride()[1:] != cache._inner):
-        raise ValueError(f"q must be bf16 [B, n_q_heads, {cache.head_dim}] on {cache.device} with contiguous heads")
-    B, n_q, hd = shape
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be int32 [B, max_pages]")
-    pages = page_table.shape[1]
-    _need(page_table, (B, pages), torch.int32, "page_table", dev)
-    _need(seq_lens, (B,), torch.int32, "seq_lens", dev)
-    out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if out is None else \
-        _need(out, shape, torch.bfloat16, "out", dev)
-    if lse is not None:
-        _need(lse, (B, n_q), torch.float32, "lse", dev)
-    s = _raw_stream(stream, dev)
-    if ws is None:
-        ws = _stream_workspace(OP_PAGED_ATTN, B, hd, dev, stream, s)
-    code = (_lib or load()).twell_paged_attn_decode(q.data_ptr(), q.stride(0) if B > 1 else n_q * hd, cache._ref,
-                                                    page_table.data_ptr(), seq_lens.data_ptr(), B, n_q, pages,
-                                                    1.0 / math.sqrt(hd) if scale is None else scale, window,
-                                                    out.data_ptr(), _p(lse), ws.data_ptr(), ws.numel(),
-                                                    _status_ptr(status, dev), s)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    code = (_native or _calls()).paged_attn_decode(q, cache._at, dev, page_table, seq_lens, scale, window, out, lse, ws,
+                                                   _status(status, dev), None if stream is None else stream.cuda_stream)
     if code:
         _check(code, "twell_paged_attn_decode")
     return out, lse
@@ -1131,9 +1035,10 @@ class W4Weights:
         if self.group not in (32, 64, 128) or self.n <= 0 or self.k <= 0 or self.k % 32 or self.k % self.group:
             raise ValueError("W4Weights: group 32, 64 or 128, k a multiple of 32 and of group")
         tiles = (-(-self.n // 16), -(-self.k // 128))
-        self.index = _index(self.words, "words")
-        _need(self.words, tiles + (8, 4, 2, 4), torch.int32, "words", self.index)
-        _need(self.scales, tiles + (8, 2, 128 // self.group), torch.bfloat16, "scales", self.index)
+        for t, shape, dtype, what in ((self.words, tiles + (8, 4, 2, 4), torch.int32, "words"),
+                                      (self.scales, tiles + (8, 2, 128 // self.group), torch.bfloat16, "scales")):
+            if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.words.device:
+                raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on one device")
 
     def dequantize(self) -> torch.Tensor:
         """The fp32 weights [n, k] that the codes stand for (a check, not a fast path)."""
@@ -1148,32 +1053,27 @@ class W4Weights:
 def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=None) -> W4Weights:
     """bf16 weights [n, k] quantised to 4 bits with a scale per `group` columns, laid out for
     twell_w4_matvec (once per weight)."""
-    if W.dim() != 2:
-        raise ValueError("W must be a 2-D bf16 tensor")
-    n, k = W.shape
-    dev = _index(W, "W")
-    _need(W, (n, k), torch.bfloat16, "W", dev)
+    if W.dim() != 2 or W.dtype != torch.bfloat16 or not W.is_contiguous() or not W.is_cuda:
+        raise ValueError("W must be a contiguous 2-D bf16 tensor on the GPU")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
+    n, k = W.shape
     nt, kt = -(-n // 16), -(-k // 128)
     words = torch.empty((nt, kt, 8, 4, 2, 4), dtype=torch.int32, device=W.device)
     scales = torch.empty((nt, kt, 8, 2, 128 // group), dtype=torch.bfloat16, device=W.device)
     out = W4Weights(words, scales, n, k, group)
-    _check(load().twell_w4_quantize(W.data_ptr(), n, k, group, words.data_ptr(), scales.data_ptr(),
-                                    _status_ptr(status, dev), _raw_stream(stream, dev)),
+    _check(load().twell_w4_quantize(_ptr(W), n, k, group, _ptr(words), _ptr(scales), _ptr(_status(status, W.get_device())),
+                                    _stream(stream)),
            "twell_w4_quantize")
     return out
 
 
 def twell_w4_matvec(x: torch.Tensor, W: W4Weights, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T (bf16) for at most DECODE_MAX_N tokens and 4-bit weights."""
-    N = x.shape[0]
-    dev = W.index
-    _need(x, (N, W.k), torch.bfloat16, "x", dev)
-    y = torch.empty((N, W.n), dtype=torch.bfloat16, device=x.device) if y is None else \
-        _need(y, (N, W.n), torch.bfloat16, "y", dev)
-    code = (_lib or load()).twell_w4_matvec(x.data_ptr(), W.words.data_ptr(), W.scales.data_ptr(), N, W.n, W.k, W.group,
-                                            y.data_ptr(), _raw_stream(stream, dev))
+    if y is None:
+        y = torch.empty((x.shape[0], W.n), dtype=torch.bfloat16, device=x.device)
+    code = (_native or _calls()).w4_matvec(x, W.words, W.scales, W.n, W.k, W.group, y,
+                                           None if stream is None else stream.cuda_stream)
     if code:
         _check(code, "twell_w4_matvec")
     return y

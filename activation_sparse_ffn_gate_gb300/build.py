@@ -1,8 +1,8 @@
-"""Build libtwell_gb300.so in-tree with nvcc for sm_103a.
+"""Build libtwell_gb300.so in-tree with nvcc for sm_103a, and the native calls (_twell_call.so) with g++.
 
 Each CUDA translation unit is compiled in parallel, then linked into one shared library with the
 static CUDA runtime (no link-time dependency on libcuda: the TMA descriptor encoder is fetched
-from the driver at run time).
+from the driver at run time). The native calls are one C++ file against PyTorch's headers, linked to that library.
 """
 from __future__ import annotations
 
@@ -17,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtwell_gb300.so")
+CALL = os.path.join(PKG, "_twell_call.so")
 
 SOURCES = ["twell_host.cu", "twell_gate.cu", "twell_ffn.cu", "twell_pack.cu", "twell_hybrid.cu", "twell_light.cu",
            "twell_union.cu", "twell_union_small.cu", "twell_decode.cu", "twell_tile_union.cu", "twell_norm.cu",
@@ -36,8 +37,32 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+
+def _call_flags():
+    """Compiler and linker flags of the native calls: PyTorch's headers and libraries, CUDA's headers, Python's."""
+    import sysconfig
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    lib = os.path.join(torch_dir, "lib")
+    compile_flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I" + INCLUDE,
+                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        compile_flags += ["-isystem", d]
+    link_flags = ["-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + lib, "-L" + PKG,
+                  "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    return compile_flags, link_flags
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, CALL)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -52,14 +77,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout, r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    compile_flags, link_flags = _call_flags()
+
+    def compile_call():
+        obj = os.path.join(BUILD, "twell_call.o")
+        _run(["g++", *compile_flags, "-c", os.path.join(CSRC, "twell_call.cpp"), "-o", obj], "g++ failed for twell_call.cpp")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        call_obj = ex.submit(compile_call)
         objs = list(ex.map(compile_one, SOURCES))
+        call_obj = call_obj.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link failed")
     os.replace(tmp, LIB)
+    tmp = CALL + f".{os.getpid()}.tmp"
+    _run(["g++", "-shared", "-o", tmp, call_obj, *link_flags], "link of the native calls failed")
+    os.replace(tmp, CALL)
     return LIB
 
 

@@ -148,3 +148,30 @@ def test_enums_match_the_header():
     for name in ("TWELL_OP_ADD_RMSNORM_BWD", "TWELL_OP_PAGED_ATTN"):
         assert int(re.search(name + r" = (\d+)", src).group(1)) == getattr(binding, name[len("TWELL_"):])
     assert int(re.search(r"TWELL_E4M3 = (\d+)", src).group(1)) == binding.TWELL_E4M3
+
+
+def test_native_calls_refuse_before_the_device(lib):
+    """The native module checks what it is given: no tensor, a tensor on the host, another number of arguments."""
+    import torch
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.twell_add_rmsnorm_fwd(x, x[0])
+    with pytest.raises(TypeError):
+        binding._native.add_rmsnorm_fwd(x, x[0])
+    with pytest.raises(TypeError):
+        binding._native.w4_matvec(1, x, x, 16, 128, 64, x, None)
+    with pytest.raises(ValueError):
+        binding._native.w4_matvec(x, x, x, 16, 128, 64, x, None)
+
+
+def test_missing_native_calls_are_not_passed_over(lib, monkeypatch):
+    """Without the native module load() raises: there is no slower way around it."""
+    import importlib
+
+    def missing(name, package=None):
+        raise ImportError(name)
+
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(importlib, "import_module", missing)
+    with pytest.raises(RuntimeError):
+        binding.load()
