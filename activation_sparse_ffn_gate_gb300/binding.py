@@ -911,7 +911,7 @@ def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rs
                           dw: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
     """Gradients of the call above from its h (x where it had no res) and rstd: returns (dx, dw), dx the
     gradient of x and of res alike, dw fp32. dy, dh (the gradient that reaches h from the residual
-    stream, or None) and dx share a type, bf16 or fp32."""
+    stream, or None) and dx share a type, bf16 or fp32. ws as in twell_paged_attn_decode."""
     if dx is None:
         dx = torch.empty_like(dy)
     if dw is None:
@@ -1008,7 +1008,8 @@ def twell_paged_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.T
     [B, max_pages]; seq_lens int32 [B] (the new token's own slot counted, if it is to be seen); scale
     1/sqrt(head_dim) unless given; window > 0 keeps the last `window` tokens. out bf16, written; lse fp32
     [B, n_q_heads] (natural logarithm of the sum of exponentials) is written when a buffer is given. A
-    sequence of length 0 gives zeros and -inf."""
+    sequence of length 0 gives zeros and -inf. ws: the caller's workspace; without one the calls of a stream share
+    theirs, so give one to a call captured into a graph that may replay beside other calls."""
     dev = cache.index
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)

@@ -335,9 +335,9 @@ struct AttnState {
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t w0 = e == 0 ? k0.x : e == 1 ? k0.y : e == 2 ? k0.z : k0.w;
                         const uint32_t w1 = e == 0 ? k1.x : e == 1 ? k1.y : e == 2 ? k1.z : k1.w;
-                        const uint32_t a0 = e4m3x2_f16x2(static_cast<uint16_t>(w0)), a1 = e4m3x2_f16x2(static_cast<uint16_t>(w1));
-                        const uint32_t a2 = e4m3x2_f16x2(static_cast<uint16_t>(w0 >> 16)),
-                                       a3 = e4m3x2_f16x2(static_cast<uint16_t>(w1 >> 16));
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_f16(w0, a0, a2);
+                        e4m3x4_f16(w1, a1, a3);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma_f16(x[t][n], a0, a1, a2, a3, q[n][8 * i + 2 * e], q[n][8 * i + 2 * e + 1]);
@@ -473,8 +473,9 @@ struct AttnState {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t x = h ? x1 : x0, y = h ? y1 : y0;
-                            const uint32_t a0 = e4m3x2_f16x2(static_cast<uint16_t>(x)), a1 = e4m3x2_f16x2(static_cast<uint16_t>(x >> 16));
-                            const uint32_t a2 = e4m3x2_f16x2(static_cast<uint16_t>(y)), a3 = e4m3x2_f16x2(static_cast<uint16_t>(y >> 16));
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_f16(x, a0, a1);
+                            e4m3x4_f16(y, a2, a3);
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
                                 mma_f16(o[2 * (w0 + w) + h][n], a0, a1, a2, a3, ph[t][n][0], ph[t][n][1]);
@@ -1091,7 +1092,7 @@ extern "C" twell_status twell_paged_attn_decode(const void* q, int64_t q_stride,
     if (hd != 64 && hd != 96 && hd != 128 && hd != 256) return TWELL_ERR_UNSUPPORTED;
     const long long cap = static_cast<long long>(max_pages) << a.c.page_shift;
     if (B > twell::kAttnMaxSeqs || cap > INT32_MAX - 16 || B * (cap / twell::kTileTokens + 1) > INT32_MAX ||
-        static_cast<long long>(B) * n_q_heads > INT32_MAX)
+        n_q_heads > 65535 || static_cast<long long>(B) * n_q_heads > INT32_MAX)
         return TWELL_ERR_UNSUPPORTED;
     if (B == 0) return TWELL_OK;
     if (q == nullptr || page_table == nullptr || seq_lens == nullptr || out == nullptr) return TWELL_ERR_INVALID;

@@ -17,7 +17,8 @@ namespace {
 constexpr int kKvThreads = 256;
 constexpr int kGatherRows = 4;
 
-// Row `i` of this thread: LPR lanes a row (a power of two), 8 elements a lane, the lanes past head_dim idle.
+// Row `i` of this thread: LPR lanes a row (a power of two), 8 elements a lane, the lanes past head_dim idle. The rows of a
+// block are one head's of consecutive tokens: neighbours in a page of the cache.
 struct KvRow {
     int token, head, col;
     bool live;
@@ -26,11 +27,11 @@ template <int LPR, int RPT>
 __device__ __forceinline__ KvRow kv_row(int i, int n, int heads, int hd)
 {
     constexpr unsigned kPer = kKvThreads / LPR;
-    const unsigned id = (blockIdx.x * RPT + i) * kPer + threadIdx.x / LPR;
+    const unsigned unit = blockIdx.x * RPT + i, tile = unit / static_cast<unsigned>(heads);
     KvRow r;
     r.col = static_cast<int>(threadIdx.x % LPR) * 8;
-    r.token = static_cast<int>(id / static_cast<unsigned>(heads));
-    r.head = static_cast<int>(id % static_cast<unsigned>(heads));
+    r.head = static_cast<int>(unit - tile * heads);
+    r.token = static_cast<int>(tile * kPer + threadIdx.x / LPR);
     r.live = r.token < n && r.col < hd;
     return r;
 }
@@ -150,20 +151,22 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvView c, c
     }
 }
 
-inline unsigned kv_blocks(long long rows, int lpr, int rpt)
+// Units of kKvThreads / lpr tokens of one head: what a block takes at a time.
+inline long long kv_units(int n, int heads, int lpr)
 {
-    const long long per = static_cast<long long>(kKvThreads / lpr) * rpt;
-    return static_cast<unsigned>((rows + per - 1) / per);
+    const long long per = kKvThreads / lpr;
+    return (n + per - 1) / per * heads;
 }
 
+// One unit a block: with two or four the larger threads cost more occupancy than they gained (16001 tokens of 8 heads of
+// 128 into e4m3: 18.2 us with one, 19.8 with two, 20.4 with four).
 template <int LPR>
 twell_status run_append(const KvView& c, const void* k, const void* v, int64_t ldk, int64_t ldv, const int32_t* slots,
                         int n, int32_t* status, cudaStream_t s)
 {
     using bf = __nv_bfloat16;
-    const long long rows = static_cast<long long>(n) * c.heads;
     auto kern = c.q8 ? kv_append_kernel<LPR, true> : kv_append_kernel<LPR, false>;
-    return twell_host::launch_dep(kern, dim3(kv_blocks(rows, LPR, 1)), dim3(kKvThreads), 0, s, c,
+    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(kv_units(n, c.heads, LPR))), dim3(kKvThreads), 0, s, c,
                                   static_cast<const bf*>(k), static_cast<const bf*>(v), ldk, ldv, slots, n, status);
 }
 
@@ -172,16 +175,17 @@ twell_status run_gather(const KvView& c, const int32_t* slots, int n, void* k_ou
                         cudaStream_t s)
 {
     using bf = __nv_bfloat16;
-    const long long rows = static_cast<long long>(n) * c.heads;
-    // several rows a thread once that still gives every SM several blocks
-    const int rpt = rows * LPR >= 4ll * kGatherRows * kKvThreads * 152 ? kGatherRows : 1;
+    const long long units = kv_units(n, c.heads, LPR);
+    // several units a block once that still gives every SM several blocks (30011 tokens of 8 heads of 128 from e4m3: 33.6 us
+    // with one, 30.0 with four)
+    const int rpt = units >= 4ll * kGatherRows * 152 ? kGatherRows : 1;
     auto kern = rpt == 1 ? (c.q8 ? kv_gather_kernel<LPR, true, 1> : kv_gather_kernel<LPR, false, 1>)
                          : (c.q8 ? kv_gather_kernel<LPR, true, kGatherRows> : kv_gather_kernel<LPR, false, kGatherRows>);
-    return twell_host::launch_dep(kern, dim3(kv_blocks(rows, LPR, rpt)), dim3(kKvThreads), 0, s, c, slots, n,
+    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>((units + rpt - 1) / rpt)), dim3(kKvThreads), 0, s, c, slots, n,
                                   static_cast<bf*>(k_out), static_cast<bf*>(v_out), status);
 }
 
-constexpr long long kMaxRows = 1ll << 31;  // rows (tokens x heads) of one call
+constexpr long long kMaxRows = 1ll << 30;  // rows (tokens x heads) of one call: indices stay in 32 bits
 
 }  // namespace
 }  // namespace twell

@@ -65,6 +65,16 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
     return r;
 }
+// Four codes as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t v, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
 __device__ __forceinline__ float2 e4m3x2_f32(uint16_t v)
 {
     const uint32_t h = e4m3x2_f16x2(v);

@@ -22,6 +22,7 @@ constexpr int kW4MaxN = 16;
 constexpr int kW4Warps = 8;   // most a block has; two blocks share an SM
 constexpr int kW4Slot = 1152; // bytes of a weight tile in the ring: its words, then its scales (at most 128 bytes)
 constexpr int kW4Stages = 2;
+constexpr int kW4Direct = 2;  // column tiles a warp may have to take them straight into registers
 // Row tiles a block, by the token columns (in eights): what lets two blocks' rings share an SM.
 constexpr int w4_tiles(int nb) { return nb == 1 ? 4 : 3; }
 constexpr int w4_stage(int nb, int rt) { return rt * kW4Slot + nb * 2048; }  // 8 tokens by 128 columns of x: 2 KB
@@ -67,9 +68,11 @@ struct W4Scales<128> {
 // A pair of columns of a word as bf16 values code - 8, exactly.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i)
 {
-    const uint32_t b = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), __floats2bfloat162_rn(136.0f, 136.0f));
-    return *reinterpret_cast<const uint32_t*>(&v);
+    uint32_t b;  // (a & b) | c in one instruction
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+    uint32_t v;  // 1.0 b - 136.0
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(b), "r"(0x3f803f80u), "r"(0xc308c308u));
+    return v;
 }
 
 __device__ __forceinline__ void w4_copy16(uint32_t dst, const void* src)
@@ -83,6 +86,93 @@ __device__ __forceinline__ uint4 w4_lds128(uint32_t a)
     return r;
 }
 
+// One tile of weights against the tokens' fragments: group sums by the tensor core, added under their scales.
+template <int GROUP, int NB>
+__device__ __forceinline__ void w4_tile(const uint4& w0, const uint4& w1, const W4Scales<GROUP>& sc, const uint4 (&xv)[NB][4],
+                                        float (&acc)[NB][4])
+{
+    constexpr int kGroups = 128 / GROUP, kPer = GROUP / 32;  // groups a tile, 32-column steps a group
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+        float d[NB][4];
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int j = q * kPer + p;
+            const uint32_t u = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
+            const uint32_t v = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
+            const uint32_t u0 = w4_pair(u, 0), u1 = w4_pair(u, 1), u2 = w4_pair(u, 2), u3 = w4_pair(u, 3);
+            const uint32_t v0 = w4_pair(v, 0), v1 = w4_pair(v, 1), v2 = w4_pair(v, 2), v3 = w4_pair(v, 3);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (p == 0) mma_bf16_first(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
+                else mma_bf16(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
+                mma_bf16(d[b], u2, v2, u3, v3, xv[b][j].z, xv[b][j].w);
+            }
+        }
+        const float s0 = sc.get(0, q), s1 = sc.get(1, q);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            acc[b][0] = fmaf(s0, d[b][0], acc[b][0]);
+            acc[b][1] = fmaf(s0, d[b][1], acc[b][1]);
+            acc[b][2] = fmaf(s1, d[b][2], acc[b][2]);
+            acc[b][3] = fmaf(s1, d[b][3], acc[b][3]);
+        }
+    }
+}
+
+// One row tile a block and at most kW4Direct column tiles a warp: everything is requested at once, into registers.
+template <int GROUP, int NB>
+__global__ void __launch_bounds__(32 * kW4Warps) w4_small_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                 const uint8_t* __restrict__ words,
+                                                                 const uint8_t* __restrict__ scales, int N, int n, int k,
+                                                                 int kt, __nv_bfloat16* __restrict__ y)
+{
+    constexpr int kGroups = 128 / GROUP, kScaleBytes = 32 * kGroups;
+    __shared__ float part[kW4Warps][8 * NB][17];
+    pdl_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, g = lane >> 2, c = lane & 3;
+    uint4 w0[kW4Direct], w1[kW4Direct], xv[kW4Direct][NB][4];
+    W4Scales<GROUP> sc[kW4Direct];
+#pragma unroll
+    for (int i = 0; i < kW4Direct; ++i) {
+        const int t = warp + i * warps;
+        w0[i] = w1[i] = make_uint4(0u, 0u, 0u, 0u);
+        sc[i] = {};
+        if (t < kt) {
+            const size_t tile = static_cast<size_t>(blockIdx.x) * kt + t;
+            w0[i] = ldg_stream16(words + tile * 1024 + lane * 32);
+            w1[i] = ldg_stream16(words + tile * 1024 + lane * 32 + 16);
+            sc[i] = reinterpret_cast<const W4Scales<GROUP>*>(scales + tile * kScaleBytes)[g];
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = 128 * t + 32 * j + 8 * c;
+                xv[i][b][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * b + g < N && col < k)
+                    xv[i][b][j] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(8 * b + g) * k + col));
+            }
+    }
+    float acc[NB][4] = {};
+#pragma unroll
+    for (int i = 0; i < kW4Direct; ++i) w4_tile<GROUP, NB>(w0[i], w1[i], sc[i], xv[i], acc);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        part[warp][8 * b + 2 * c][g] = acc[b][0];
+        part[warp][8 * b + 2 * c + 1][g] = acc[b][1];
+        part[warp][8 * b + 2 * c][g + 8] = acc[b][2];
+        part[warp][8 * b + 2 * c + 1][g + 8] = acc[b][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * N; i += blockDim.x) {
+        float v = 0.0f;
+        for (int w = 0; w < warps; ++w) v += part[w][i >> 4][i & 15];
+        const int row = 16 * blockIdx.x + (i & 15);
+        if (row < n) y[static_cast<size_t>(i >> 4) * n + row] = __float2bfloat16_rn(v);
+    }
+}
+
 // Row tiles [nt * block / blocks, nt * (block + 1) / blocks), at most RT of them.
 template <int GROUP, int NB, int RT>
 __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_bfloat16* __restrict__ x,
@@ -90,9 +180,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_
                                                                      const uint8_t* __restrict__ scales, int N, int n,
                                                                      int k, int nt, int kt, __nv_bfloat16* __restrict__ y)
 {
-    constexpr int kGroups = 128 / GROUP, kPer = GROUP / 32;  // groups a tile, 32-column steps a group
     constexpr int kCols = 8 * NB;
-    constexpr int kScaleBytes = 32 * kGroups;                // of a tile
+    constexpr int kScaleBytes = 32 * (128 / GROUP);          // of a tile
     constexpr int kStage = w4_stage(NB, RT);                 // of a warp: the weight tiles, then x
     constexpr int kRing = kW4Stages * kStage;
     static_assert(RT * kCols * 17 * 4 <= kRing, "a warp leaves its sums in its ring");
@@ -177,32 +266,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_matvec_kernel(const __nv_
             const uint4 w0 = w4_lds128(at + lane * 32), w1 = w4_lds128(at + lane * 32 + 16);
             W4Scales<GROUP> sc;
             sc.load(at + 1024 + g * (kScaleBytes / 8));
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                float d[NB][4];
-#pragma unroll
-                for (int p = 0; p < kPer; ++p) {
-                    const int j = q * kPer + p;
-                    const uint32_t u = j == 0 ? w0.x : j == 1 ? w0.y : j == 2 ? w0.z : w0.w;
-                    const uint32_t v = j == 0 ? w1.x : j == 1 ? w1.y : j == 2 ? w1.z : w1.w;
-                    const uint32_t u0 = w4_pair(u, 0), u1 = w4_pair(u, 1), u2 = w4_pair(u, 2), u3 = w4_pair(u, 3);
-                    const uint32_t v0 = w4_pair(v, 0), v1 = w4_pair(v, 1), v2 = w4_pair(v, 2), v3 = w4_pair(v, 3);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        if (p == 0) mma_bf16_first(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
-                        else mma_bf16(d[b], u0, v0, u1, v1, xv[b][j].x, xv[b][j].y);
-                        mma_bf16(d[b], u2, v2, u3, v3, xv[b][j].z, xv[b][j].w);
-                    }
-                }
-                const float s0 = sc.get(0, q), s1 = sc.get(1, q);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    acc[r][b][0] = fmaf(s0, d[b][0], acc[r][b][0]);
-                    acc[r][b][1] = fmaf(s0, d[b][1], acc[r][b][1]);
-                    acc[r][b][2] = fmaf(s1, d[b][2], acc[r][b][2]);
-                    acc[r][b][3] = fmaf(s1, d[b][3], acc[r][b][3]);
-                }
-            }
+            w4_tile<GROUP, NB>(w0, w1, sc, xv, acc[r]);
         }
         stage = stage + 1 == kW4Stages ? 0 : stage + 1;
     }
@@ -284,6 +348,10 @@ twell_status launch_w4(const void* x, const void* words, const void* scales, int
     const int nt = (n + 15) / 16, kt = (k + 127) / 128;
     // every warp takes the same number of column tiles where that is possible
     const int each = (kt + kW4Warps - 1) / kW4Warps, warps = (kt + each - 1) / each;
+    if (RT == 1 && each <= kW4Direct)
+        return twell_host::launch_dep(w4_small_kernel<GROUP, NB>, dim3(blocks), dim3(32 * warps), 0, s,
+                                      static_cast<const __nv_bfloat16*>(x), static_cast<const uint8_t*>(words),
+                                      static_cast<const uint8_t*>(scales), N, n, k, kt, static_cast<__nv_bfloat16*>(y));
     const size_t smem = w4_smem(warps, NB, RT);
     auto kern = w4_matvec_kernel<GROUP, NB, RT>;
     static std::atomic<uint64_t> allowed{0};
@@ -314,6 +382,7 @@ twell_status run_w4(const void* x, const void* words, const void* scales, int N,
 }
 
 bool w4_shape_ok(int n, int k, int group) { return n > 0 && k > 0 && group > 0 && k % 32 == 0 && k % group == 0; }
+constexpr int kW4MaxDim = 1 << 24;
 bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 
 }  // namespace
@@ -339,7 +408,7 @@ extern "C" twell_status twell_w4_quantize(const void* W, int32_t n, int32_t k, i
     if (!twell::w4_shape_ok(n, k, group) || W == nullptr || words == nullptr || scales == nullptr ||
         dev_status == nullptr || !aligned16(W) || !aligned16(words) || !aligned16(scales))
         return TWELL_ERR_INVALID;
-    if (!twell::w4_group_ok(group)) return TWELL_ERR_UNSUPPORTED;
+    if (!twell::w4_group_ok(group) || n > twell::kW4MaxDim || k > twell::kW4MaxDim) return TWELL_ERR_UNSUPPORTED;
     const long long tiles = ((n + 15ll) / 16) * ((k + 127ll) / 128);
     if (tiles > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
     return launch_dep(twell::w4_quantize_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0,
@@ -353,7 +422,8 @@ extern "C" twell_status twell_w4_matvec(const void* x, const void* words, const 
     if (N < 0 || !twell::w4_shape_ok(n, k, group) || words == nullptr || scales == nullptr || !aligned16(words) ||
         !aligned16(scales))
         return TWELL_ERR_INVALID;
-    if (N > twell::kW4MaxN || !twell::w4_group_ok(group)) return TWELL_ERR_UNSUPPORTED;
+    if (N > twell::kW4MaxN || !twell::w4_group_ok(group) || n > twell::kW4MaxDim || k > twell::kW4MaxDim)
+        return TWELL_ERR_UNSUPPORTED;
     if (N == 0) return TWELL_OK;
     if (x == nullptr || y == nullptr || !aligned16(x) || !aligned16(y)) return TWELL_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -442,7 +442,7 @@ TWELL_API twell_status twell_kv_gather(const twell_kv_cache* cache, const int32_
  * (natural logarithm, fp32; lse may be null). Nothing visible: out = 0, lse = -inf. Token t of sequence
  * b is at offset t % page_size of page page_table[b * max_pages + t / page_size] (device int32; entries
  * past the last visible token are not read). q bf16, sequence b's heads at q + b * q_stride (elements, a
- * multiple of 8); out bf16 [B, n_q_heads, head_dim]. head_dim 64, 96, 128 or 256; B <= 4096. A length
+ * multiple of 8); out bf16 [B, n_q_heads, head_dim]. head_dim 64, 96, 128 or 256; B <= 4096, n_q_heads < 65536. A length
  * outside [0, max_pages * page_size] is clamped and reported as TWELL_ERR_DEVICE_CHECK; a page
  * outside the cache is reported and its tokens do not count. Sums, maxima and the join of split sequences
  * are fp32, in an order that depends on the lengths alone: the same out from call to call. ws:
@@ -455,7 +455,7 @@ TWELL_API twell_status twell_paged_attn_decode(const void* q, int64_t q_stride, 
 
 /* 4-bit weights W [n, k] with a bf16 scale per `group` columns (32, 64 or 128; k a multiple of 32 and of
  * group): W[r][c] = scale[r][c / group] * (code - 8), code 0..15. Layout, n rounded up to 16 and k to 128
- * (padding: codes 8, scales 0): words uint32 [ceil(n/16)][ceil(k/128)][8 g][4 c][2 half][4 j], a word
+ * (padding: codes 8, scales 0; n and k at most 2^24): words uint32 [ceil(n/16)][ceil(k/128)][8 g][4 c][2 half][4 j], a word
  * holding row 16 tile + 8 half + g, columns 128 tile + 32 j + 8 c + (0..7), column 2i of the 8 in bits
  * 4i..4i+3 and column 2i + 1 in bits 16+4i..19+4i; scales bf16 [ceil(n/16)][ceil(k/128)][8 g][2 half]
  * [128/group]. Sizes in bytes (0 on invalid arguments): */

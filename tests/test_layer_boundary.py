@@ -105,7 +105,8 @@ def test_attention_refuses(lib):
     for bad in (dict(q=None), dict(table=None), dict(lens=None), dict(out=None), dict(st=None), dict(B=-1), dict(nq=0), dict(nq=3),
                 dict(mp=0), dict(window=-1), dict(q=ODD), dict(out=ODD), dict(lse=ODD), dict(qs=255), dict(qs=128)):
         assert f(**bad) == INVALID, bad
-    for bad in (dict(cache=_cache(head_dim=80, token_stride=80)), dict(B=4097), dict(mp=1 << 27), dict(B=4096, mp=1 << 20)):
+    for bad in (dict(cache=_cache(head_dim=80, token_stride=80)), dict(B=4097), dict(mp=1 << 27), dict(B=4096, mp=1 << 20),
+                dict(nq=65536, qs=65536 * 64)):
         assert f(**bad) == UNSUPPORTED, bad
     for bad in (dict(ws=None), dict(ws=ODD), dict(nb=need - 1)):
         assert f(**bad) == WORKSPACE, bad
@@ -122,8 +123,9 @@ def test_w4_refuses(lib):
     for bad in (dict(x=None), dict(w=None), dict(s=None), dict(y=None), dict(N=-1), dict(n=0), dict(k=0), dict(k=96), dict(x=ODD),
                 dict(w=ODD), dict(s=ODD), dict(y=ODD)):
         assert m(**bad) == INVALID, bad
-    for bad in (dict(N=17), dict(k=256, g=256)):
+    for bad in (dict(N=17), dict(k=256, g=256), dict(n=(1 << 24) + 1), dict(k=(1 << 24) + 128)):
         assert m(**bad) == UNSUPPORTED, bad
+    assert q(n=(1 << 24) + 1) == UNSUPPORTED
     assert m(N=0, x=None) == OK
 
 
