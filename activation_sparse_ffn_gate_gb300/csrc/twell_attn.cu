@@ -17,8 +17,8 @@
 //     the products. The scores' fragment becomes the second product's operand by an 8x8 transpose
 //     (movmatrix); with a bf16 cache the weights go in as hi + lo bf16 parts (~16 bits), with an
 //     e4m3 cache as fp16 (11 bits).
-//   - A batch whose (sequence, key head)s are no more than the SMs and short (at most kPairTiles tiles a warp by
-//     the page table's width) skips the list: one block each, which needs no second kernel.
+//   - A batch of short sequences whose (sequence, key head)s about fill the SMs skips the list: one block each,
+//     which needs no second kernel (the rule is in run_attn).
 //   - Running maximum m and sum l in fp32, per query head. For an e4m3 cache the value's scale s_t is
 //     folded into the weight, w_t = p_t s_t, and m runs over score + log2 s_t, so that the fp16
 //     weights stay in (0, 1] whatever the scales. The query is brought to [1, 2) by a power of two
@@ -39,7 +39,8 @@ constexpr int kMTiles = kTileTokens / 16;  // 16-token rows of a product
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxSms = 160;   // the workspace is sized for this many blocks, whatever the device
 constexpr int kAttnMaxWarps = 16;  // and this many warps a block
-constexpr int kPairTiles = 1;      // see "pairs" in run_attn
+// When a block takes a whole (sequence, key head): see run_attn.
+constexpr int kPairIdle = 2, kPairTiles = 8;
 constexpr float kNegInf = -INFINITY;
 
 // HD: head_dim; Q8: e4m3 cache; NT: query heads of one key head handled together, in eights.
@@ -1028,11 +1029,15 @@ twell_status run_attn(AttnArgs& a, int sms, cudaStream_t s)
     auto kern = paged_attn_kernel<HD, Q8, NT>;
     static std::atomic<uint64_t> allowed{0};
     if (twell_host::allow_smem(kern, C::kSmem + (kAttnMaxSeqs + 1) * 4, allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    // pairs: what the page table's width allows to be visible, in tiles
+    // One block for each (sequence, key head), without the list and its second kernel, where they fit the SMs and what the
+    // page table's width lets be visible is few tiles a warp: at most kPairTiles, and at most kPairIdle times the share
+    // of the SMs that would idle (38 sequences of up to 1000 / 2000 tokens, 4 key heads of 128: 12.3 / 18.0 us against 16.3 /
+    // 20.2 through the list; but 8 of up to 2000 with 8 key heads, e4m3: 15.2 against 11.3).
     const long long cap = static_cast<long long>(a.max_pages) << a.c.page_shift;
     const long long seen = a.window > 0 ? std::min<long long>(cap, static_cast<long long>(a.window) + kTileTokens - 1) : cap;
     const long long pairs = static_cast<long long>(a.B) * a.c.heads * a.blocks;
-    a.pairs = pairs <= sms && (seen + kTileTokens - 1) / kTileTokens <= kPairTiles * C::kWarps;
+    const long long each = (seen + static_cast<long long>(kTileTokens) * C::kWarps - 1) / (kTileTokens * C::kWarps);
+    a.pairs = pairs <= sms && each <= kPairTiles && each * (sms - pairs) <= static_cast<long long>(kPairIdle) * sms;
     if (a.pairs)
         return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(pairs)), dim3(C::kWarps * 32), C::kSmem, s, a);
     const size_t smem = C::kSmem + (static_cast<size_t>(a.B) + 1) * 4;
