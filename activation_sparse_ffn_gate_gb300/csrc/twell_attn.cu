@@ -743,8 +743,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
     // bits and where its rows are. A tile that lies in one page is copied from one address: lane `lane` takes chunk
     // `lane`, `lane` + 32, ..., kStep bytes apart where a page's tokens are adjacent.
     constexpr int kElt = Q8 ? 1 : 2, kCopies = C::kHalf / 512;
-    constexpr bool kWholeRows = 32 % C::kChunks == 0;  // 32 chunks are whole rows
-    const bool packed = kWholeRows && a.c.page_shift >= 5 && a.c.token_stride * kElt == C::kRow;
+    const bool packed = (1 << a.c.page_shift) >= kTileTokens && a.c.token_stride * kElt == C::kRow;
     uint32_t tile_vis = 0;
     int64_t tile_off = 0;  // bytes: of the tile, where it is copied from one address, else of token `lane`
     auto request = [&](const void* base, uint32_t dst) {

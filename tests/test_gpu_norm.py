@@ -233,3 +233,25 @@ def test_refusals(cuda_dev):
         binding.twell_add_rmsnorm_bwd(x, x, w, torch.ones(3, device=cuda_dev))
     with pytest.raises(ValueError):
         binding.twell_add_rmsnorm_bwd(x, x, w, torch.ones(4, device=cuda_dev), dh=x.float())
+
+
+# More rows than the device holds at once, so that a block goes over several: a row's results are those of the row
+# alone, bit for bit, and within the bounds of a row.
+@pytest.mark.parametrize("rt", [BF, F32, None])
+@pytest.mark.parametrize("N,d", [(40001, 8), (5003, 136), (3001, 1208), (2001, 4096), (701, 8192)])
+def test_forward_many_rows(cuda_dev, N, d, rt):
+    x, w = _rand(cuda_dev, (N, d), BF, 31), _rand(cuda_dev, (d,), BF, 32)
+    res = _rand(cuda_dev, (N, d), rt, 33, 4.0) if rt is not None else None
+    y, h, rstd = binding.twell_add_rmsnorm_fwd(x, w, res, EPS, training=True)
+    y8, _, _ = binding.twell_add_rmsnorm_fwd_q8(x, w, res, EPS, 128)
+    _, rs, ry = _ref_fwd(x, res, w)
+    _within(rstd, rs, 64 * U * rs, "rstd")
+    _within(y, ry, (_half(BF) + 64 * U) * ry.abs(), "y")
+    for lo in (0, N // 2, N - 3):
+        rows = slice(lo, lo + 3)
+        part = None if res is None else res[rows]
+        one, _, _ = binding.twell_add_rmsnorm_fwd(x[rows], w, part, EPS)
+        assert torch.equal(one, y[rows])
+        one8, _, _ = binding.twell_add_rmsnorm_fwd_q8(x[rows], w, part, EPS, 128)
+        assert torch.equal(one8.values.view(torch.uint8), y8.values[rows].view(torch.uint8))
+        assert torch.equal(one8.scale, y8.scale[rows])
