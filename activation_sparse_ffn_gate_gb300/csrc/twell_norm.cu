@@ -3,10 +3,12 @@
 //   h = x + r,  s = 1 / sqrt(mean(h^2) + eps),  y = h s w
 //   dx = s (g - xh mean(g xh)) + dh  with  xh = h s, g = dy w;   dw = sum over rows of dy xh
 //
-// Both passes are bounded by memory traffic: every element is read and written once, and a row stays in
-// registers between its statistics and its output. A row is spread over `wpr` warps, CH chunks of 8
-// elements a thread. All sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the
-// fp32 values (y from the unrounded h, so that it does not depend on the residual stream's type).
+// Both passes are bounded by memory traffic where rows are wide: every element is read and written once, and a row
+// stays in registers between its statistics and its output. A row is spread over `wpr` warps, CH chunks of 8 elements
+// a thread. 16-bit rows are bounded as much by the instructions, so that the arithmetic is on pairs of fp32 numbers
+// and a row's sum takes one exchange (30000 x 1024 into e4m3: 37.7 us -> 32.7; with an fp32 stream 56.1 -> 49.9, what
+// its bytes take). All sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the fp32 values
+// (y from the unrounded h, so that it does not depend on the residual stream's type).
 #include "twell_common.cuh"
 #include "twell_ops.cuh"
 
@@ -22,7 +24,7 @@ constexpr int kNormMinThreads = 128;  // rows of few columns share a block of th
 // How a row of d columns is spread over a block: `ch` chunks of 8 elements a thread, `wpr` warps a row, `rpb` rows
 // a block. One chunk a thread as far as a block goes: more threads in flight hide more of the latency than
 // longer threads save instructions (16384 rows of 2560, forward into e4m3: 72.7 us with one chunk, 75.0 with two,
-// 91.0 with four; backward 103.8, 105.6, 137.4; 3000 rows of 8192 in bf16: 33.4 with one, 42.3 with two, backward
+// 91.0 with four; backward 103.8, 105.6, 137.4; 3000 rows of 8192 in bf16: 40.5 with one, 42.3 with two, backward
 // 48.5 and 61.7).
 struct NormShape {
     int ch, wpr, rpb;
@@ -36,27 +38,47 @@ struct NormShape {
     int threads() const { return 32 * wpr * rpb; }
 };
 
-// Sum (or maximum, of values >= 0) over the `wpr` warps of a row; every thread of the block takes part.
+// How a thread takes part in the sums over its row: its warp's place in the row's slot of shared memory. Slots of up to
+// 8 warps are read whole by every thread, so that they are filled up with zeros to 4 or 8.
+struct RowSlot {
+    int wpr, first, warp, fill;
+    __device__ __forceinline__ RowSlot(int wpr, int sub, int t)
+        : wpr(wpr), first(sub * 4), warp(sub * 4 + (t >> 5)), fill((t >> 5) == wpr - 1 && wpr <= 8 ? (8 - wpr) & 3 : 0)
+    {
+    }
+};
+
+// Sum (or maximum, of values >= 0) over a row; every thread of the block takes part.
 template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* red, int wpr)
+__device__ __forceinline__ float warp_reduce(float v)
 {
+    if constexpr (MAX) {
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
     }
-    if (wpr == 1) return v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = warp / wpr * wpr;
-    if (lane == 0) red[warp] = v;
+}
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* red, const RowSlot& k)
+{
+    v = warp_reduce<MAX>(v);
+    if (k.wpr == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane <= k.fill) red[k.warp + lane] = lane == 0 ? v : 0.0f;
     __syncthreads();
-    v = lane < wpr ? red[first + lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
+    if (k.wpr <= 8) {
+        const float4 a = *reinterpret_cast<const float4*>(red + k.first);
+        v = MAX ? fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)) : (a.x + a.y) + (a.z + a.w);
+        if (k.wpr > 4) {
+            const float4 b = *reinterpret_cast<const float4*>(red + 4);
+            const float u = MAX ? fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)) : (b.x + b.y) + (b.z + b.w);
+            v = MAX ? fmaxf(v, u) : v + u;
+        }
+        return v;
     }
-    return v;
+    return warp_reduce<MAX>(lane < k.wpr ? red[lane] : 0.0f);
 }
 
 // 8 elements as they lie in memory, to be unpacked later.
@@ -66,24 +88,25 @@ struct Raw8 {
     __device__ __forceinline__ void load(const E* p)
     {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) v[i] = *reinterpret_cast<const uint4*>(p + i * (16 / sizeof(E)));
+        for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i)
+            v[i] = *reinterpret_cast<const uint4*>(p + i * (16 / sizeof(E)));
     }
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void get(float (&o)[8]) const
+    __device__ __forceinline__ void get(F2 (&o)[4]) const
     {
         if constexpr (sizeof(E) == 2) {
-            unpack16(v[0], o, static_cast<__nv_bfloat16*>(nullptr));
+            float f[8];
+            unpack16(v[0], f, static_cast<__nv_bfloat16*>(nullptr));
+            to_f2(f, o);
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                o[4 * i] = __uint_as_float(v[i].x);
-                o[4 * i + 1] = __uint_as_float(v[i].y);
-                o[4 * i + 2] = __uint_as_float(v[i].z);
-                o[4 * i + 3] = __uint_as_float(v[i].w);
+                o[2 * i] = F2::of(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                o[2 * i + 1] = F2::of(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
             }
         }
     }
@@ -102,43 +125,78 @@ struct NormFwdArgs {
     float eps, inv_d;
 };
 
-// What follows the loads of one row: h = x + r is in `h`, its part of the weights comes from weight(i).
-template <typename T, typename R, int CH, typename W>
-__device__ __forceinline__ void finish_row(const NormFwdArgs& a, float (&h)[CH][8], long long row, int t, int chunks, size_t base,
-                                           float (*red)[kNormMaxThreads / 32], const W& weight)
+// a.rpb rows a block.
+template <typename T, typename R, int CH>
+__global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const NormFwdArgs a)
 {
-    const int per_row = 32 * a.wpr, step = per_row * 8;
-    float ss = 0.0f;
+    __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
+    pdl_begin();
+    const int per_row = 32 * a.wpr;
+    const int t = static_cast<int>(threadIdx.x) % per_row, sub = static_cast<int>(threadIdx.x) / per_row;
+    const RowSlot slot(a.wpr, sub, t);
+    const long long row = static_cast<long long>(blockIdx.x) * a.rpb + sub;
+    const bool live = row < a.N;
+    const int chunks = live ? a.d / 8 : 0;
+    const size_t base = static_cast<size_t>(live ? row : 0) * a.d + t * 8;
+    const int step = per_row * 8;
+
+    Raw8<T> x[CH];  // unpacked only when every load is under way
+    Raw8<R> r[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        x[i].clear();
+        r[i].clear();
+        if (t + i * per_row < chunks) {
+            x[i].load(static_cast<const T*>(a.x) + base + i * step);
+            if (a.res != nullptr) r[i].load(static_cast<const R*>(a.res) + base + i * step);
+        }
+    }
+    F2 h[CH][4];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        F2 u[4];
+        x[i].get(h[i]);
+        r[i].get(u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[i][e] = h[i][e] + u[e];
+    }
+    F2 ss2 = F2::of(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+        for (int e = 0; e < 4; ++e) ss2 = fma2(h[i][e], h[i][e], ss2);
         if (a.h != nullptr && t + i * per_row < chunks) store8(static_cast<R*>(a.h) + base + i * step, h[i]);
     }
-    ss = row_reduce<false>(ss, red[0], a.wpr);
+    float ss, sb;
+    ss2.get(ss, sb);
+    ss = row_reduce<false>(ss + sb, red[0], slot);
     const float s = rsqrtf(fmaf(ss, a.inv_d, a.eps));
-    if (a.rstd != nullptr && t < chunks && t == 0) a.rstd[row] = s;
+    if (a.rstd != nullptr && t == 0 && t < chunks) a.rstd[row] = s;
 
+    const F2 s2 = F2::of(s, s);
     float top[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         top[i] = 0.0f;
         if (t + i * per_row < chunks) {
-            float w[8];
-            weight(i, w);
+            F2 w[4];
+            load8(static_cast<const T*>(a.w) + t * 8 + i * step, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[i][e] = h[i][e] * s * w[e];
-                top[i] = fmaxf(top[i], fabsf(h[i][e]));
-            }
+            for (int e = 0; e < 4; ++e) h[i][e] = h[i][e] * s2 * w[e];
             if (a.y != nullptr) store8(static_cast<T*>(a.y) + base + i * step, h[i]);
+            if (a.y8 != nullptr) {
+                float v[8];
+                from_f2(h[i], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[i] = fmaxf(top[i], fabsf(v[e]));
+            }
         }
     }
     if (a.y8 == nullptr) return;
     if (a.group == a.d) {
 #pragma unroll
         for (int i = 1; i < CH; ++i) top[0] = fmaxf(top[0], top[i]);
-        top[0] = row_reduce<true>(top[0], red[1], a.wpr);
+        top[0] = row_reduce<true>(top[0], red[1], slot);
 #pragma unroll
         for (int i = 1; i < CH; ++i) top[i] = top[0];
     } else {  // groups of 128 columns: 16 lanes next to each other
@@ -158,82 +216,6 @@ __device__ __forceinline__ void finish_row(const NormFwdArgs& a, float (&h)[CH][
     }
 }
 
-// a.rpb rows a block.
-template <typename T, typename R, int CH>
-__global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const NormFwdArgs a)
-{
-    __shared__ float red[2][kNormMaxThreads / 32];
-    pdl_begin();
-    const int per_row = 32 * a.wpr;
-    const int t = static_cast<int>(threadIdx.x) % per_row;
-    const long long row = static_cast<long long>(blockIdx.x) * a.rpb + threadIdx.x / per_row;
-    const bool live = row < a.N;
-    const int chunks = live ? a.d / 8 : 0;
-    const size_t base = static_cast<size_t>(live ? row : 0) * a.d + t * 8;
-    const int step = per_row * 8;
-
-    float h[CH][8], r[CH][8];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = r[i][e] = 0.0f;
-        if (t + i * per_row < chunks) {
-            load8(static_cast<const T*>(a.x) + base + i * step, h[i]);
-            if (a.res != nullptr) load8(static_cast<const R*>(a.res) + base + i * step, r[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] += r[i][e];
-    }
-    finish_row<T, R, CH>(a, h, row, t, chunks, base, red,
-                         [&](int i, float (&w)[8]) { load8(static_cast<const T*>(a.w) + t * 8 + i * step, w); });
-}
-
-// Rows blockIdx.x * rpb + ..., then every gridDim.x * rpb-th one; the next row is requested before this one is reduced,
-// the weights stay in registers. One chunk a thread. For 16-bit rows, which put too little in flight one a block:
-// 16384 x 2560 with a 16-bit stream 58.6 -> 53.9 us, 30000 x 1024 into e4m3 without one 37.7 -> 34.5. With an fp32
-// stream it is not faster (2560 columns 72.9 -> 80.6).
-constexpr int kFwdThreadsPerSm = 1024;
-template <typename T, typename R>
-__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_ahead_kernel(const NormFwdArgs a)
-{
-    __shared__ float red[2][2][kNormMaxThreads / 32];
-    pdl_begin();
-    const int per_row = 32 * a.wpr;
-    const int t = static_cast<int>(threadIdx.x) % per_row, sub = static_cast<int>(threadIdx.x) / per_row;
-    const int all = a.d / 8;
-    const long long rows = static_cast<long long>(gridDim.x) * a.rpb;
-    Raw8<T> next_x, weight;
-    Raw8<R> next_r;
-    auto request = [&](long long row) {
-        next_x.clear();
-        next_r.clear();
-        if (row < a.N && t < all) {
-            const size_t at = static_cast<size_t>(row) * a.d + t * 8;
-            next_x.load(static_cast<const T*>(a.x) + at);
-            if (a.res != nullptr) next_r.load(static_cast<const R*>(a.res) + at);
-        }
-    };
-    request(static_cast<long long>(blockIdx.x) * a.rpb + sub);
-    weight.clear();
-    if (t < all) weight.load(static_cast<const T*>(a.w) + t * 8);
-    int flip = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * a.rpb; r0 < a.N; r0 += rows, flip ^= 1) {
-        const long long row = r0 + sub;
-        const bool live = row < a.N;
-        float h[1][8], r[8];
-        next_x.get(h[0]);
-        next_r.get(r);
-        request(row + rows);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[0][e] += r[e];
-        finish_row<T, R, 1>(a, h, row, t, live ? all : 0, static_cast<size_t>(live ? row : 0) * a.d + t * 8, red[flip],
-                            [&](int, float (&w)[8]) { weight.get(w); });
-    }
-}
-
 struct NormBwdArgs {
     const void* dy;
     const void* h;
@@ -246,102 +228,146 @@ struct NormBwdArgs {
     float inv_d;
 };
 
-// Rows blockIdx.x * rpb + ..., then every gridDim.x * rpb-th one; the weights stay in registers and
-// the rows' shares of dw are added there too; a block leaves one partial row of dw, its rows' sums added in order.
+// Rows blockIdx.x * rpb + ..., then every gridDim.x * rpb-th one; the rows' shares of dw are added in registers and
+// a block leaves one partial row of dw, its rows' sums added in order. The weights wait in shared memory, read and
+// written by their own thread alone: there are no registers for them beside a row's.
 // With one chunk a thread an SM holds 1024 threads (64 registers each), with more 512.
 constexpr int norm_threads_per_sm(int ch) { return ch == 1 ? 1024 : 512; }
 template <typename T, typename R, typename G, int CH>
-__global__ void __launch_bounds__(max_threads(CH), norm_threads_per_sm(CH) / max_threads(CH)) add_rmsnorm_bwd_kernel(const NormBwdArgs a)
+__global__ void __launch_bounds__(max_threads(CH), norm_threads_per_sm(CH) / max_threads(CH))
+    add_rmsnorm_bwd_kernel(const NormBwdArgs a)
 {
-    __shared__ float red[2][kNormMaxThreads / 32];
-    __shared__ float rows_dw[8 * kNormMinThreads];  // of a block with several rows
+    __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
+    // A thread's 8 weights while the block goes over its rows, then its share of dw where a block has several rows.
+    extern __shared__ float4 own[];  // [2][blockDim.x]
     pdl_begin();
     const int per_row = 32 * a.wpr;
-    const int t = static_cast<int>(threadIdx.x) % per_row;
-    const int sub = static_cast<int>(threadIdx.x) / per_row;
+    const int t = static_cast<int>(threadIdx.x) % per_row, sub = static_cast<int>(threadIdx.x) / per_row;
+    const RowSlot slot(a.wpr, sub, t);
     const int chunks = a.d / 8, step = per_row * 8;
-    constexpr int KW = CH <= 2 ? CH : 1;  // chunks whose weights stay in registers; else they are read again (L1)
-    float dw[CH][8], w[KW][8];
+    const F2 zero = F2::of(0.0f, 0.0f);
+    F2 dw[CH][4];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = w[i % KW][e] = 0.0f;
-        if (KW == CH && t + i * per_row < chunks) load8(static_cast<const T*>(a.w) + t * 8 + i * step, w[i % KW]);
+        for (int e = 0; e < 4; ++e) dw[i][e] = zero;
     }
-    const long long rows = static_cast<long long>(gridDim.x) * a.rpb;
-    // With 16-bit h the next row is requested before this one is reduced: too little would be in flight otherwise
-    // (16384 x 2048, 16-bit gradients: 52.9 -> 44.3 us). With fp32 h it would not fit the registers (1208 columns: 61 -> 75).
-    constexpr bool kAhead = CH == 1 && sizeof(R) == 2;
+    auto keep = [&](const F2 (&v)[4]) {
+        float f[8];
+        from_f2(v, f);
+        own[threadIdx.x] = make_float4(f[0], f[1], f[2], f[3]);
+        own[blockDim.x + threadIdx.x] = make_float4(f[4], f[5], f[6], f[7]);
+    };
+    auto kept = [&](F2 (&v)[4], int thread) {
+        const float4 l = own[thread], h = own[blockDim.x + thread];
+        v[0] = F2::of(l.x, l.y), v[1] = F2::of(l.z, l.w), v[2] = F2::of(h.x, h.y), v[3] = F2::of(h.z, h.w);
+    };
+    if (CH == 1) {
+        F2 w[4] = {zero, zero, zero, zero};
+        if (t < chunks) load8(static_cast<const T*>(a.w) + t * 8, w);
+        keep(w);
+    }
+    // With 16-bit h and gradients the next row is requested before this one is reduced: too little would be in flight
+    // otherwise (6000 x 5120: 72.5 -> 54.0 us, 16384 x 2048 without dh 45.2 -> 41.7). Wider rows would not fit the registers
+    // (fp32 gradients of 31220 x 368: 25.8 us so, 31.0 with the next row).
+    constexpr bool kAhead = CH == 1 && sizeof(R) == 2 && sizeof(G) == 2;
+    const unsigned N = a.N, rows = gridDim.x * a.rpb;  // no sum of the two passes 32 bits
     Raw8<G> next_dy;
     Raw8<R> next_h;
     float next_s = 0.0f;
-    auto request = [&](long long row) {
-        next_dy.clear();
-        next_h.clear();
-        next_s = 0.0f;
-        if (row < a.N) {
+    next_dy.clear();  // zeros for the threads past the row's end, which request nothing
+    next_h.clear();
+    auto request = [&](unsigned row, size_t at) {
+        if (row < N) {
             next_s = a.rstd[row];
             if (t < chunks) {
-                next_dy.load(static_cast<const G*>(a.dy) + static_cast<size_t>(row) * a.d + t * 8);
-                next_h.load(static_cast<const R*>(a.h) + static_cast<size_t>(row) * a.d + t * 8);
+                next_dy.load(static_cast<const G*>(a.dy) + at);
+                next_h.load(static_cast<const R*>(a.h) + at);
             }
         }
     };
-    if constexpr (kAhead) request(static_cast<long long>(blockIdx.x) * a.rpb + sub);
+    unsigned row = blockIdx.x * a.rpb + sub;
+    size_t at = static_cast<size_t>(row) * a.d + t * 8;
+    if constexpr (kAhead) request(row, at);
     int flip = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * a.rpb; r0 < a.N; r0 += rows, flip ^= 1) {
-        const bool live = r0 + sub < a.N;
+    const size_t far = static_cast<size_t>(rows) * a.d;
+    for (; row - sub < N; row += rows, at += far, flip ^= 1) {
+        const bool live = row < N;
         const int mine = live ? chunks : 0;
-        const size_t base = static_cast<size_t>(live ? r0 + sub : 0) * a.d + t * 8;
-        const float s = kAhead ? next_s : live ? a.rstd[r0 + sub] : 0.0f;
-        float dy[CH][8], xh[CH][8], o[CH][8];
-        float p = 0.0f;
+        const float s = kAhead ? next_s : live ? a.rstd[row] : 0.0f;
+        const F2 s2 = F2::of(s, s);
+        Raw8<G> raw_dy[CH], dh[CH];  // unpacked only when every load is under way
+        Raw8<R> raw_h[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dy[i][e] = xh[i][e] = o[i][e] = 0.0f;
-            if (kAhead) {
-                next_dy.get(dy[i]);
-                next_h.get(xh[i]);
+            if (!kAhead) {
+                raw_dy[i].clear();
+                raw_h[i].clear();
             }
             if (t + i * per_row < mine) {
                 if (!kAhead) {
-                    load8(static_cast<const G*>(a.dy) + base + i * step, dy[i]);
-                    load8(static_cast<const R*>(a.h) + base + i * step, xh[i]);
+                    raw_dy[i].load(static_cast<const G*>(a.dy) + at + i * step);
+                    raw_h[i].load(static_cast<const R*>(a.h) + at + i * step);
                 }
-                if (a.dh != nullptr) load8(static_cast<const G*>(a.dh) + base + i * step, o[i]);
+                if (CH == 1 && a.dh != nullptr) dh[i].load(static_cast<const G*>(a.dh) + at + i * step);
             }
         }
+        F2 dy[CH][4], xh[CH][4];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            if (KW != CH && t + i * per_row < mine) load8(static_cast<const T*>(a.w) + t * 8 + i * step, w[i % KW]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[i][e] *= s;
-                dw[i][e] = fmaf(dy[i][e], xh[i][e], dw[i][e]);
-                dy[i][e] *= w[i % KW][e];
-                p = fmaf(dy[i][e], xh[i][e], p);
+            if constexpr (kAhead) {
+                next_dy.get(dy[i]);
+                next_h.get(xh[i]);
+            } else {
+                raw_dy[i].get(dy[i]);
+                raw_h[i].get(xh[i]);
             }
         }
-        if constexpr (kAhead) request(r0 + rows + sub);
-        p = row_reduce<false>(p, red[flip], a.wpr) * a.inv_d;
+        F2 p2 = zero;
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                F2 w[4] = {zero, zero, zero, zero};
+                if (CH == 1) kept(w, threadIdx.x);
+                else if (t + i * per_row < mine) load8(static_cast<const T*>(a.w) + t * 8 + i * step, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    xh[i][e] = xh[i][e] * s2;
+                    dw[i][e] = fma2(dy[i][e], xh[i][e], dw[i][e]);
+                    dy[i][e] = dy[i][e] * w[e];
+                    p2 = fma2(dy[i][e], xh[i][e], p2);
+                }
+            }
+        }
+        if constexpr (kAhead) request(row + rows, at + far);
+        float p, pb;
+        p2.get(p, pb);
+        p = row_reduce<false>(p + pb, red[flip], slot) * -a.inv_d;
+        p2 = F2::of(p, p);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             if (t + i * per_row >= mine) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[i][e] = fmaf(s, fmaf(-xh[i][e], p, dy[i][e]), o[i][e]);
-            store8(static_cast<G*>(a.dx) + base + i * step, o[i]);
+            for (int e = 0; e < 4; ++e) dy[i][e] = fma2(xh[i][e], p2, dy[i][e]) * s2;
+            if (a.dh != nullptr) {
+                F2 o[4];
+                if (CH > 1) dh[i].load(static_cast<const G*>(a.dh) + at + i * step);  // no registers for it before
+                dh[i].get(o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dy[i][e] = dy[i][e] + o[e];
+            }
+            store8(static_cast<G*>(a.dx) + at + i * step, dy[i]);
         }
     }
     if (CH == 1 && a.rpb > 1) {
-        store8(rows_dw + threadIdx.x * 8, dw[0]);
+        keep(dw[0]);
         __syncthreads();
         if (sub > 0) return;
         for (int s = 1; s < a.rpb; ++s) {
-            float u[8];
-            load8(rows_dw + (s * per_row + t) * 8, u);
+            F2 u[4];
+            kept(u, s * per_row + t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dw[0][e] += u[e];
+            for (int e = 0; e < 4; ++e) dw[0][e] = dw[0][e] + u[e];
         }
     }
     float* part = a.part + static_cast<size_t>(blockIdx.x) * a.d + t * 8;
@@ -387,24 +413,18 @@ int bwd_blocks(int N, const NormShape& S, int sms)
 constexpr int kNormMaxSms = 160;
 
 template <typename T, typename R>
-twell_status run_norm_fwd(const NormFwdArgs& a, const NormShape& S, int sms, cudaStream_t s)
+twell_status run_norm_fwd(const NormFwdArgs& a, const NormShape& S, cudaStream_t s)
 {
-    const long long need = (static_cast<long long>(a.N) + S.rpb - 1) / S.rpb;
-    if constexpr (sizeof(R) == 2) {
-        if (S.ch == 1) {
-            const long long blocks = std::min<long long>(need, static_cast<long long>(sms) * (kFwdThreadsPerSm / S.threads()));
-            return twell_host::launch_dep(add_rmsnorm_fwd_ahead_kernel<T, R>, dim3(static_cast<unsigned>(blocks)), dim3(S.threads()), 0, s, a);
-        }
-    }
     auto kern = S.ch == 1 ? add_rmsnorm_fwd_kernel<T, R, 1> : add_rmsnorm_fwd_kernel<T, R, 4>;
-    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(need)), dim3(S.threads()), 0, s, a);
+    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>((static_cast<long long>(a.N) + S.rpb - 1) / S.rpb)),
+                                  dim3(S.threads()), 0, s, a);
 }
 
 template <typename T, typename R, typename G>
 twell_status run_norm_bwd(const NormBwdArgs& a, const NormShape& S, int blocks, float* dw, cudaStream_t s)
 {
     auto kern = S.ch == 1 ? add_rmsnorm_bwd_kernel<T, R, G, 1> : add_rmsnorm_bwd_kernel<T, R, G, 4>;
-    twell_status st = twell_host::launch_dep(kern, dim3(blocks), dim3(S.threads()), 0, s, a);
+    twell_status st = twell_host::launch_dep(kern, dim3(blocks), dim3(S.threads()), S.ch == 1 ? S.threads() * 32 : 0, s, a);
     if (st != TWELL_OK) return st;
     return twell_host::launch_dep(add_rmsnorm_dw_kernel, dim3(a.d / kDwCols), dim3(kDwCols * kDwWays), 0, s,
                                   static_cast<const float*>(a.part), blocks, a.d, dw);
@@ -444,12 +464,10 @@ extern "C" twell_status twell_add_rmsnorm_fwd(const void* x, const void* res, co
     const int g = group == 0 || d <= 128 ? d : group;
     const twell::NormFwdArgs a{x,    res, w, h_out, y,  static_cast<uint8_t*>(y8), y8_scale, rstd, N, d,
                                g, (d + g - 1) / g, S.wpr, S.rpb, eps, 1.0f / static_cast<float>(d)};
-    DevInfo dev;
-    if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == TWELL_F32) return twell::run_norm_fwd<float, float>(a, S, dev.sm_count, s);
-    if (res_dtype == TWELL_F32) return twell::run_norm_fwd<__nv_bfloat16, float>(a, S, dev.sm_count, s);
-    return twell::run_norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, S, dev.sm_count, s);
+    if (dtype == TWELL_F32) return twell::run_norm_fwd<float, float>(a, S, s);
+    if (res_dtype == TWELL_F32) return twell::run_norm_fwd<__nv_bfloat16, float>(a, S, s);
+    return twell::run_norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, S, s);
 }
 
 extern "C" twell_status twell_add_rmsnorm_bwd(const void* dy, const void* h, const void* w, const float* rstd,

@@ -28,6 +28,63 @@ __device__ __forceinline__ void store8(float* p, const float (&o)[8])
     *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
 }
 
+// Two fp32 numbers in one register pair, for the instructions that work on both.
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ static F2 of(float a, float b)
+    {
+        F2 r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+        return r;
+    }
+    __device__ __forceinline__ void get(float& a, float& b) const
+    {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ void to_f2(const float (&v)[8], F2 (&o)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = F2::of(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void from_f2(const F2 (&v)[4], float (&o)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i].get(o[2 * i], o[2 * i + 1]);
+}
+template <typename E>
+__device__ __forceinline__ void load8(const E* p, F2 (&o)[4])
+{
+    float v[8];
+    load8(p, v);
+    to_f2(v, o);
+}
+template <typename E>
+__device__ __forceinline__ void store8(E* p, const F2 (&v)[4])
+{
+    float o[8];
+    from_f2(v, o);
+    store8(p, o);
+}
+
 // 8-bit rounding of values whose largest magnitude is `top`: code = e4m3(v * (448 / a)) to nearest
 // even, a = max(top, 2^-60), so that 448 / a stays finite and a row of zeros has codes 0; the code
 // stands for code * scale, scale = a / 448. A row that holds an infinity has an infinite scale and
@@ -46,11 +103,22 @@ struct Scale8 {
         return {a * (1.0f / kE4m3Max), kE4m3Max * r};
     }
     // two codes, the first in the low byte
-    __device__ __forceinline__ uint32_t pack2(float a, float b) const
+    __device__ __forceinline__ static uint32_t round2(float a, float b)
     {
         uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b * mul), "f"(a * mul));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
         return r;
+    }
+    __device__ __forceinline__ uint32_t pack2(float a, float b) const { return round2(a * mul, b * mul); }
+    __device__ __forceinline__ uint2 pack8(const F2 (&v)[4]) const
+    {
+        const F2 m = F2::of(mul, mul);
+        F2 s[4];
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = v[i] * m;
+        from_f2(s, o);
+        return make_uint2(round2(o[0], o[1]) | (round2(o[2], o[3]) << 16), round2(o[4], o[5]) | (round2(o[6], o[7]) << 16));
     }
     __device__ __forceinline__ uint2 pack8(const float (&v)[8]) const
     {
