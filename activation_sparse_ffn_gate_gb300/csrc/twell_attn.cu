@@ -18,7 +18,8 @@
 //     (movmatrix); with a bf16 cache the weights go in as hi + lo bf16 parts (~16 bits), with an
 //     e4m3 cache as fp16 (11 bits).
 //   - A batch of short sequences whose (sequence, key head)s about fill the SMs skips the list: one block each,
-//     which needs no second kernel (the rule is in run_attn).
+//     which needs no second kernel; a large batch of short ones is dealt out in whole (sequence, key head)s, equally
+//     many a warp, and needs neither (the rules are in run_attn).
 //   - Running maximum m and sum l in fp32, per query head. For an e4m3 cache the value's scale s_t is
 //     folded into the weight, w_t = p_t s_t, and m runs over score + log2 s_t, so that the fp16
 //     weights stay in (0, 1] whatever the scales. The query is brought to [1, 2) by a power of two
@@ -41,6 +42,8 @@ constexpr int kAttnMaxSms = 160;   // the workspace is sized for this many block
 constexpr int kAttnMaxWarps = 16;  // and this many warps a block
 // When a block takes a whole (sequence, key head): see run_attn.
 constexpr int kPairIdle = 2, kPairTiles = 8;
+// When a warp takes whole ones: likewise.
+constexpr int kWholeTiles = 8, kWholeExtra = 4;
 constexpr float kNegInf = -INFINITY;
 
 // HD: head_dim; Q8: e4m3 cache; NT: query heads of one key head handled together, in eights.
@@ -59,6 +62,7 @@ struct AttnCfg {
     static constexpr int kSlots = kFit >= 7 ? 7 : kFit >= 5 ? 5 : 3;  // odd: keys are requested while keys are used
     static_assert(kFit >= 3, "the ring overlaps copies with the products");
     static constexpr int kMt = HD / 16;                 // 16-dimension tiles of the output
+    static constexpr int kF = kMt % 4 == 0 ? 4 : 3;     // of them joined and stored together
     static constexpr int kRing = kSlots * kSlot;        // bytes of a warp's ring
     static constexpr int kPartF = NT * kMt * 128;       // floats of a part's o, then NT * 16 of m and l
     static constexpr int kPart = kPartF + NT * 16;
@@ -78,6 +82,7 @@ struct AttnArgs {
     int B, n_q, G, blocks; // blocks: groups of 8 NT query heads per key head
     int max_pages, window;
     int pairs;             // 1: one block a (sequence, key head)
+    int whole;             // 1: whole (sequence, key head)s, equally many a warp
     float scale_log2;      // scale * log2(e)
     int2* split;           // [blocks] the (sequence, key head) that a block's start is the first to split, or -1,
                            // and the last block that holds some of it
@@ -517,29 +522,45 @@ struct AttnState {
     }
 };
 
-// Final values of one fragment element group: dimension tile i, eight heads n, lane's four sums r with
-// their heads' totals l; all 32 lanes of a warp call it for the same (n, i).
-template <int HD, bool Q8, int NT>
-__device__ __forceinline__ void store_out(const AttnArgs& a, int b, int hv, int n, int i, int lane, const float (&r)[4],
+// Final values of F fragments next to each other: dimension tiles i .. i + F - 1, eight heads n, the lane's four sums
+// each with their heads' totals l; all 32 lanes of a warp call it for the same (n, i). i is a multiple of F.
+template <int HD, bool Q8, int NT, int F>
+__device__ __forceinline__ void store_out(const AttnArgs& a, int b, int hv, int n, int i, int lane, const float (&r)[F][4],
                                           float l0, float l1)
 {
     const int g = lane >> 2, c = lane & 3;
     const int kvh = hv / a.blocks, first = (hv % a.blocks) * 8 * NT + n * 8;
     const float i0 = l0 > 0.0f || l0 != l0 ? 1.0f / l0 : 0.0f, i1 = l1 > 0.0f || l1 != l1 ? 1.0f / l1 : 0.0f;
     __nv_bfloat16* base = a.out + (static_cast<int64_t>(b) * a.n_q + kvh * a.G) * HD;
-    if constexpr (!Q8) {  // rows g and g + 8 of the tile, heads 2c and 2c + 1
-        const uint32_t x = transpose8(bf16x2_rn(r[0] * i0, r[1] * i1)), y = transpose8(bf16x2_rn(r[2] * i0, r[3] * i1));
-        if (first + g < a.G) {
-            uint32_t* p = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(first + g) * HD + 16 * i + 2 * c);
-            p[0] = x;
-            p[4] = y;
+    if constexpr (!Q8) {  // rows g and g + 8 of a tile, heads 2c and 2c + 1
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const uint32_t x = transpose8(bf16x2_rn(r[f][0] * i0, r[f][1] * i1));
+            const uint32_t y = transpose8(bf16x2_rn(r[f][2] * i0, r[f][3] * i1));
+            if (first + g < a.G) {
+                uint32_t* p = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(first + g) * HD + 16 * (i + f) + 2 * c);
+                p[0] = x;
+                p[4] = y;
+            }
         }
-    } else {  // dimensions g HD / 8 + 2i and the next, heads 2c and 2c + 1
-        const int d = g * (HD / 8) + 2 * i, j = first + 2 * c;
-        if (j < a.G)
-            *reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(j) * HD + d) = bf16x2_rn(r[0] * i0, r[2] * i0);
-        if (j + 1 < a.G)
-            *reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(j + 1) * HD + d) = bf16x2_rn(r[1] * i1, r[3] * i1);
+    } else {  // dimensions g HD / 8 + 2i and the 2F - 1 after it, heads 2c and 2c + 1
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t x[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+                x[f] = h ? bf16x2_rn(r[f][1] * i1, r[f][3] * i1) : bf16x2_rn(r[f][0] * i0, r[f][2] * i0);
+            const int head = first + 2 * c + h;
+            if (head >= a.G) continue;
+            uint32_t* p = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(head) * HD + g * (HD / 8) + 2 * i);
+            if constexpr (F % 4 == 0) {
+#pragma unroll
+                for (int f = 0; f < F; f += 4) *reinterpret_cast<uint4*>(p + f) = make_uint4(x[f], x[f + 1], x[f + 2], x[f + 3]);
+            } else {
+#pragma unroll
+                for (int f = 0; f < F; ++f) p[f] = x[f];
+            }
+        }
     }
 }
 
@@ -609,12 +630,22 @@ __device__ __forceinline__ void store_joined(const AttnArgs& a, int bhv, int HV,
 {
     constexpr int kMt = AttnCfg<HD, Q8, NT>::kMt;
     const int b = bhv / HV, hv = bhv % HV, e = ni / kMt;
-#pragma unroll
-    for (int f = 0; f < F; ++f) store_out<HD, Q8, NT>(a, b, hv, e, ni % kMt + f, lane, J.r[f], J.l0, J.l1);
+    store_out<HD, Q8, NT, F>(a, b, hv, e, ni % kMt, lane, J.r, J.l0, J.l1);
     if (ni % kMt == 0 && lane < 4) {
         store_lse<NT>(a, b, hv, e * 8 + 2 * lane, J.m0, J.l0);
         store_lse<NT>(a, b, hv, e * 8 + 2 * lane + 1, J.m1, J.l1);
     }
+}
+
+// The results of a key-head block of a sequence with nothing visible: zeros, lse = -inf. By `threads` threads.
+template <int HD, int NT>
+__device__ __forceinline__ void empty_heads(const AttnArgs& a, int b, int hv, int thread, int threads)
+{
+    const int first = hv % a.blocks * 8 * NT, heads = min(8 * NT, a.G - first);
+    const int64_t row = static_cast<int64_t>(b) * a.n_q + hv / a.blocks * a.G + first;
+    uint32_t* p = reinterpret_cast<uint32_t*>(a.out + row * HD);
+    for (int i = thread; i < heads * HD / 2; i += threads) p[i] = 0u;
+    if (a.lse != nullptr && thread < heads) a.lse[row + thread] = kNegInf;
 }
 
 template <int HD, bool Q8, int NT>
@@ -634,6 +665,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
 
     const int cap = a.max_pages << a.c.page_shift;
     const int HV = a.c.heads * a.blocks;
+    long long whole_tiles = 0;  // tiles of the warp's whole (sequence, key head)s
     long long total = 0, seg0 = 0;  // tiles in the list; the first tile of the (sequence, key head) at this warp's start
     Cursor cur;                     // where this warp's next tile to be used is
     Ranges R;
@@ -646,15 +678,33 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
         if ((raw < 0 || raw > cap) && threadIdx.x == 0) report(a.status, TWELL_ERR_DEVICE_CHECK);
         cur.s = SeqSpan(raw, cap, a.window);
         if (cur.s.tiles == 0) {
-            const int first = cur.hv % a.blocks * 8 * NT, heads = min(8 * NT, a.G - first);
-            const int64_t row = static_cast<int64_t>(cur.b) * a.n_q + cur.hv / a.blocks * a.G + first;
-            uint32_t* p = reinterpret_cast<uint32_t*>(a.out + row * HD);
-            for (int i = threadIdx.x; i < heads * HD / 2; i += blockDim.x) p[i] = 0u;
-            if (a.lse != nullptr && threadIdx.x < heads) a.lse[row + threadIdx.x] = kNegInf;
+            empty_heads<HD, NT>(a, cur.b, cur.hv, threadIdx.x, blockDim.x);
             return;
         }
         total = cur.s.tiles;
         R = Ranges(total, 1, C::kWarps);
+    } else if (a.whole) {
+        // the warp's share of them, and the tiles in it
+        const uint32_t P = static_cast<uint32_t>(a.B) * HV, W = gridDim.x * C::kWarps, v = blockIdx.x * C::kWarps + warp;
+        const uint32_t p0 = static_cast<uint32_t>(static_cast<uint64_t>(P) * v / W);
+        const uint32_t p1 = static_cast<uint32_t>(static_cast<uint64_t>(P) * (v + 1) / W);
+        bool found = false;
+        for (uint32_t p = p0; p < p1;) {
+            const uint32_t b = p / HV, hv = p - b * HV, here = min(p1, (b + 1) * HV) - p;  // of one sequence
+            const int raw = __ldg(a.lens + b);
+            if ((raw < 0 || raw > cap) && lane == 0) report(a.status, TWELL_ERR_DEVICE_CHECK);
+            const SeqSpan s(raw, cap, a.window);
+            whole_tiles += static_cast<long long>(s.tiles) * here;
+            if (s.tiles == 0) {
+                for (uint32_t h = hv; h < hv + here; ++h) empty_heads<HD, NT>(a, b, h, lane, 32);
+            } else if (!found) {
+                found = true;
+                cur.b = b;
+                cur.hv = hv;
+                cur.s = s;
+            }
+            p += here;
+        }
     } else {
         // tiles before each sequence (of one key head): a scan over the lengths, by every block for itself, and
         // for up to kWarpSeqs sequences by every warp (all write the same values), which needs no barrier
@@ -724,9 +774,9 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
         w0 = blockIdx.x * C::kWarps;
     }
     const int w = w0 + warp;
-    const long long start = R.start(w), end = R.start(w + 1);
+    const long long start = a.whole ? 0 : R.start(w), end = a.whole ? whole_tiles : R.start(w + 1);
     if (a.pairs) cur.tile = static_cast<int>(start);
-    else if (start < end) seg0 = cur.seek(a, prefix, HV, start);
+    else if (!a.whole && start < end) seg0 = cur.seek(a, prefix, HV, start);
     const int bhv0 = cur.b * HV + cur.hv;
 
     const int n = static_cast<int>(end - start);
@@ -817,7 +867,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
         run_bhv[threadIdx.x] = -1;
         warp_start[threadIdx.x] = R.start(w0 + threadIdx.x);
     }
-    if (threadIdx.x == 0 && !a.pairs) {  // is this block's start the first to split its (sequence, key head)?
+    if (threadIdx.x == 0 && !a.pairs && !a.whole) {  // is this block's start the first to split its (sequence, key head)?
         int2 sp = make_int2(-1, 0);
         if (blockIdx.x > 0 && start > seg0 && R.start(w0 - C::kWarps) <= seg0) {
             const long long seg1 = seg0 + cur.s.tiles;  // the last tile is in the range of warp ceil(seg1 W / total) - 1
@@ -868,8 +918,14 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
 #pragma unroll
                 for (int e = 0; e < NT; ++e) {
 #pragma unroll
-                    for (int i = 0; i < C::kMt; ++i)
-                        store_out<HD, Q8, NT>(a, cur.b, cur.hv, e, i, lane, S.o[i][e], S.l[e][0], S.l[e][1]);
+                    for (int i = 0; i < C::kMt; i += C::kF) {
+                        float r[C::kF][4];
+#pragma unroll
+                        for (int f = 0; f < C::kF; ++f)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) r[f][k] = S.o[i + f][e][k];
+                        store_out<HD, Q8, NT, C::kF>(a, cur.b, cur.hv, e, i, lane, r, S.l[e][0], S.l[e][1]);
+                    }
                     if (lane < 4) {
                         store_lse<NT>(a, cur.b, cur.hv, e * 8 + 2 * lane, S.m[e][0], S.l[e][0]);
                         store_lse<NT>(a, cur.b, cur.hv, e * 8 + 2 * lane + 1, S.m[e][1], S.l[e][1]);
@@ -910,7 +966,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
     __syncthreads();
 
     // join the parts of what spans warps: kF fragments of one of them a warp at a time
-    constexpr int kF = C::kMt % 4 == 0 ? 4 : 3, kItems = NT * C::kMt / kF;
+    constexpr int kF = C::kF, kItems = NT * C::kMt / kF;
     const uint32_t runs = __ballot_sync(0xffffffffu, lane <= C::kWarps && run_bhv[min(lane, C::kWarps)] >= 0);
     const int items = __popc(runs) * kItems;
     const long long c_start = warp_start[0], c_end = warp_start[C::kWarps];
@@ -1037,11 +1093,17 @@ twell_status run_attn(AttnArgs& a, int sms, cudaStream_t s)
     const long long pairs = static_cast<long long>(a.B) * a.c.heads * a.blocks;
     const long long each = (seen + static_cast<long long>(kTileTokens) * C::kWarps - 1) / (kTileTokens * C::kWarps);
     a.pairs = pairs <= sms && each <= kPairTiles && each * (sms - pairs) <= static_cast<long long>(kPairIdle) * sms;
+    // More of them, of few tiles each: whole ones a warp, equally many, without the scan over the lengths, the search and
+    // the second kernel; as long as the fullest warp has at most kWholeExtra tiles more than its share of the table's
+    // width (125 sequences of 256 tokens, 8 key heads of 128: 32.1 -> 23.2 us; 40 of up to 53, 4 key heads of 256: 9.9 ->
+    // 7.3; but 40 of up to 256 with 8 key heads, e4m3, 12.3 against 11.8 through the list).
+    const long long warps = static_cast<long long>(sms) * C::kWarps, tiles = (seen + kTileTokens - 1) / kTileTokens;
+    a.whole = !a.pairs && tiles <= kWholeTiles && (pairs + warps - 1) / warps * tiles <= pairs * tiles / warps + kWholeExtra;
     if (a.pairs)
         return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(pairs)), dim3(C::kWarps * 32), C::kSmem, s, a);
     const size_t smem = C::kSmem + (static_cast<size_t>(a.B) + 1) * 4;
     twell_status st = twell_host::launch_dep(kern, dim3(sms), dim3(C::kWarps * 32), smem, s, a);
-    if (st != TWELL_OK) return st;
+    if (st != TWELL_OK || a.whole) return st;
     return twell_host::launch_dep(paged_attn_join_kernel<HD, Q8, NT>, dim3(sms), dim3(JoinCfg<HD, Q8, NT>::kThreads), 0,
                                   s, a);
 }

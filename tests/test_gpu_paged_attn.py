@@ -306,3 +306,47 @@ def test_refusals(cuda_dev):
     assert e.value.code == 7
     out, _ = f(c.q[:0], c.cache, c.table[:0], c.lens_d[:0])
     assert out.shape == (0, 4, 64)
+
+
+def _short_lens(B, top, seed):
+    """Lengths 0 .. top, with runs of empty sequences at the start, inside and at the end."""
+    g = torch.Generator("cpu").manual_seed(seed)
+    lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    lens[:3] = [0, 0, top]
+    lens[B // 2:B // 2 + 20] = [0] * 20
+    lens[-2:] = [1, 0]
+    return lens
+
+
+# Batches whose (sequence, key head)s are more than the SMs and few tiles each.
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("B,H,G,hd,ps,top", [(170, 8, 3, 64, 16, 33), (100, 3, 16, 128, 32, 256), (64, 5, 7, 96, 8, 100),
+                                            (90, 4, 10, 256, 32, 31), (300, 1, 1, 128, 1, 5), (400, 16, 2, 64, 32, 64)])
+def test_many_short_sequences(cuda_dev, B, H, G, hd, ps, top, dtype):
+    c = Case(cuda_dev, _short_lens(B, top, B), H, G, hd, ps, dtype, seed=B, extra_cols=0)
+    out, lse = c.run()
+    c.check(out, lse)
+    assert torch.equal(out, c.run()[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_many_sequences_under_a_window(cuda_dev, dtype):
+    c = Case(cuda_dev, _short_lens(120, 400, 3), 4, 4, 64, 16, dtype, seed=3)
+    for window in (1, 31, 40, 100):
+        c.check(*c.run(window=window), window=window)
+
+
+def test_many_empty_sequences(cuda_dev):
+    c = Case(cuda_dev, [0] * 500, 4, 4, 64, 16, BF, seed=4)
+    c.check(*c.run())
+
+
+def test_many_short_sequences_with_bad_lengths(cuda_dev):
+    lens = _short_lens(200, 48, 6)
+    c = Case(cuda_dev, lens, 2, 4, 64, 16, BF, seed=6, extra_cols=0)
+    good, _ = c.run()
+    full = [b for b, n in enumerate(lens) if n == 48]
+    c.lens_d[full[0]], c.lens_d[199] = 1000, -7  # past the table: clamped; negative: nothing
+    out, lse = c.run()
+    assert binding.twell_read_status() == 5
+    assert torch.equal(out, good) and (lse[199] == -math.inf).all()
