@@ -6,9 +6,9 @@
 // Both passes are bounded by memory traffic where rows are wide: every element is read and written once, and a row
 // stays in registers between its statistics and its output. A row is spread over `wpr` warps, CH chunks of 8 elements
 // a thread. 16-bit rows are bounded as much by the instructions, so that the arithmetic is on pairs of fp32 numbers
-// and a row's sum takes one exchange (30000 x 1024 into e4m3: 37.7 us -> 32.7; with an fp32 stream 56.1 -> 49.9, what
-// its bytes take). All sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the fp32 values
-// (y from the unrounded h, so that it does not depend on the residual stream's type).
+// and a row's sum takes one exchange (30000 x 1024, fp32 stream, into e4m3: 56.1 us -> 49.8, what its bytes take). All
+// sums are in fp32; y, the 8-bit codes and the gradients are rounded once, from the fp32 values (y from the unrounded
+// h, so that it does not depend on the residual stream's type).
 #include "twell_common.cuh"
 #include "twell_ops.cuh"
 
@@ -21,21 +21,32 @@ constexpr int kNormLongThreads = 512;  // with more
 constexpr int max_threads(int ch) { return ch == 1 ? kNormMaxThreads : kNormLongThreads; }
 constexpr int kNormMinThreads = 128;  // rows of few columns share a block of this many threads
 
-// How a row of d columns is spread over a block: `ch` chunks of 8 elements a thread, `wpr` warps a row, `rpb` rows
-// a block. One chunk a thread as far as a block goes: more threads in flight hide more of the latency than
-// longer threads save instructions (16384 rows of 2560, forward into e4m3: 72.7 us with one chunk, 75.0 with two,
-// 91.0 with four; backward 103.8, 105.6, 137.4; 3000 rows of 8192 in bf16: 40.5 with one, 42.3 with two, backward
-// 48.5 and 61.7).
+// How a row of d columns is spread over a block: at least `least` chunks of 8 elements a thread (`ch`), `wpr` warps a
+// row, `rpb` rows a block. The backward pass takes one chunk a thread as far as a block goes: a row's values and its
+// share of dw fill the registers (16384 rows of 2560: 103.8 us with one, 105.6 with two, 137.4 with four; 3000 rows of
+// 8192 in bf16: 48.5 and 61.7). The forward pass: fwd_chunks.
 struct NormShape {
     int ch, wpr, rpb;
-    explicit NormShape(int d)
+    explicit NormShape(int d, int least = 1)
     {
         const int chunks = d / 8;
-        ch = chunks <= kNormMaxThreads ? 1 : 4;
+        ch = chunks <= kNormMaxThreads ? least : 4;
         wpr = (chunks + 32 * ch - 1) / (32 * ch);
         rpb = wpr * 32 >= kNormMinThreads ? 1 : kNormMinThreads / (wpr * 32);
     }
     int threads() const { return 32 * wpr * rpb; }
+};
+// A thread's row in its block and place in the row. Several rows a block: of one or two warps each (no division).
+struct RowPlace {
+    int sub, t;
+    __device__ __forceinline__ RowPlace(int wpr, int rpb) : sub(0), t(static_cast<int>(threadIdx.x))
+    {
+        static_assert(kNormMinThreads == 128, "rows that share a block have one or two warps");
+        if (rpb > 1) {
+            sub = t >> (4 + wpr);
+            t -= sub << (4 + wpr);
+        }
+    }
 };
 
 // How a thread takes part in the sums over its row: its warp's place in the row's slot of shared memory. Slots of up to
@@ -79,6 +90,53 @@ __device__ __forceinline__ float row_reduce(float v, float* red, const RowSlot& 
         return v;
     }
     return warp_reduce<MAX>(lane < k.wpr ? red[lane] : 0.0f);
+}
+
+// The sum over a row of which each thread holds CH chunks' sums, in the order of one chunk a thread, so that a row's
+// result does not depend on how many rows are with it: the chunks' butterflies over the lanes share their shuffles (the
+// halves of the lanes go on with one each), and the shared memory has a place for each chunk of each warp.
+template <int CH>
+__device__ __forceinline__ float row_sum(const float (&v)[CH], float* red, const RowSlot& k, int d)
+{
+    if constexpr (CH == 1) {
+        return row_reduce<false>(v[0], red, k);
+    } else {
+        const int lane = threadIdx.x & 31, warps = (d + 255) / 256;  // warps of a row at one chunk a thread
+        float s[CH / 2];
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+            const float keep = lane < 16 ? v[2 * i] : v[2 * i + 1], give = lane < 16 ? v[2 * i + 1] : v[2 * i];
+            s[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+        }
+        int chunk = lane >> 4;
+        float u = s[0];
+        if constexpr (CH == 4) {
+            const bool low = (lane & 8) == 0;
+            u = (low ? s[0] : s[1]) + __shfl_xor_sync(0xffffffffu, low ? s[1] : s[0], 8);
+            chunk += low ? 0 : 2;
+        } else {
+            u += __shfl_xor_sync(0xffffffffu, u, 8);
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+        const int first = k.first * (CH / 2), mine = k.warp - k.first;
+        if ((lane & (32 / CH - 1)) == 0) red[first + chunk * k.wpr + mine] = u;
+        // an odd number of warps at two chunks leaves two places of the last four
+        if (CH == 2 && (k.wpr & 1) && mine == 0 && (lane & 15) == 1) red[first + 2 * k.wpr + chunk] = 0.0f;
+        __syncthreads();
+        if (warps <= 8) {
+            const float4 a = *reinterpret_cast<const float4*>(red + first);
+            u = (a.x + a.y) + (a.z + a.w);
+            if (warps > 4) {
+                const float4 b = *reinterpret_cast<const float4*>(red + first + 4);
+                u += (b.x + b.y) + (b.z + b.w);
+            }
+            return u;
+        }
+        u = lane < warps ? red[lane] : 0.0f;
+        if (lane + 32 < warps) u += red[lane + 32];
+        return warp_reduce<false>(u);
+    }
 }
 
 // 8 elements as they lie in memory, to be unpacked later.
@@ -129,15 +187,16 @@ struct NormFwdArgs {
 template <typename T, typename R, int CH>
 __global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const NormFwdArgs a)
 {
-    __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
+    __shared__ __align__(16) float red[2][kNormMaxD / 256];
     pdl_begin();
     const int per_row = 32 * a.wpr;
-    const int t = static_cast<int>(threadIdx.x) % per_row, sub = static_cast<int>(threadIdx.x) / per_row;
+    const RowPlace at_row(a.wpr, a.rpb);
+    const int t = at_row.t, sub = at_row.sub;
     const RowSlot slot(a.wpr, sub, t);
-    const long long row = static_cast<long long>(blockIdx.x) * a.rpb + sub;
-    const bool live = row < a.N;
-    const int chunks = live ? a.d / 8 : 0;
-    const size_t base = static_cast<size_t>(live ? row : 0) * a.d + t * 8;
+    const unsigned row = blockIdx.x * a.rpb + sub, d = a.d;
+    const bool live = row < static_cast<unsigned>(a.N);
+    const int chunks = live ? d / 8 : 0;
+    const size_t base = static_cast<size_t>(row) * d + t * 8;
     const int step = per_row * 8;
 
     Raw8<T> x[CH];  // unpacked only when every load is under way
@@ -160,16 +219,18 @@ __global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[i][e] = h[i][e] + u[e];
     }
-    F2 ss2 = F2::of(0.0f, 0.0f);
+    float part[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+        F2 ss2 = F2::of(0.0f, 0.0f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss2 = fma2(h[i][e], h[i][e], ss2);
+        float odd;
+        ss2.get(part[i], odd);
+        part[i] += odd;
         if (a.h != nullptr && t + i * per_row < chunks) store8(static_cast<R*>(a.h) + base + i * step, h[i]);
     }
-    float ss, sb;
-    ss2.get(ss, sb);
-    ss = row_reduce<false>(ss + sb, red[0], slot);
+    const float ss = row_sum<CH>(part, red[0], slot, a.d);
     const float s = rsqrtf(fmaf(ss, a.inv_d, a.eps));
     if (a.rstd != nullptr && t == 0 && t < chunks) a.rstd[row] = s;
 
@@ -212,7 +273,7 @@ __global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const 
         if (c >= chunks) continue;
         const Scale8 q = Scale8::approx(top[i]);
         *reinterpret_cast<uint2*>(a.y8 + base + i * step) = q.pack8(h[i]);
-        if (a.group == a.d ? c == 0 : (c & 15) == 0) a.scale[static_cast<size_t>(row) * a.ng + (c >> 4)] = q.scale;
+        if (a.group == a.d ? c == 0 : (c & 15) == 0) a.scale[static_cast<size_t>(row) * static_cast<unsigned>(a.ng) + (c >> 4)] = q.scale;
     }
 }
 
@@ -242,7 +303,8 @@ __global__ void __launch_bounds__(max_threads(CH), norm_threads_per_sm(CH) / max
     extern __shared__ float4 own[];  // [2][blockDim.x]
     pdl_begin();
     const int per_row = 32 * a.wpr;
-    const int t = static_cast<int>(threadIdx.x) % per_row, sub = static_cast<int>(threadIdx.x) / per_row;
+    const RowPlace at_row(a.wpr, a.rpb);
+    const int t = at_row.t, sub = at_row.sub;
     const RowSlot slot(a.wpr, sub, t);
     const int chunks = a.d / 8, step = per_row * 8;
     const F2 zero = F2::of(0.0f, 0.0f);
@@ -412,10 +474,23 @@ int bwd_blocks(int N, const NormShape& S, int sms)
 // and without one; the launch uses the device's own number up to it.
 constexpr int kNormMaxSms = 160;
 
+// Chunks a thread of the forward pass. One while the rows do not fill the device's threads; then two, so that each
+// thread has more under way and a row's sums take fewer warps (30000 x 1024 into e4m3 without a stream 32.5 -> 25.4 us,
+// 2000 x 2048 in bf16 5.7 -> 5.5; with an fp32 stream within 3% either way), and four where a row of 16-bit elements is
+// wide (8192 columns in bf16: 34.6 us with one, 33.5 with two, 29.4 with four; but 1024 columns 33.4 with two, 34.7 with
+// four). A row of 256 columns or fewer is one warp's.
+int fwd_chunks(int N, int d, twell_dtype res_dtype, int sms)
+{
+    if (d <= 256 || static_cast<long long>(N) * d <= 8ll * 2048 * sms) return 1;
+    return res_dtype == TWELL_BF16 && d >= 4096 ? 4 : 2;
+}
+
 template <typename T, typename R>
 twell_status run_norm_fwd(const NormFwdArgs& a, const NormShape& S, cudaStream_t s)
 {
-    auto kern = S.ch == 1 ? add_rmsnorm_fwd_kernel<T, R, 1> : add_rmsnorm_fwd_kernel<T, R, 4>;
+    auto kern = S.ch == 1   ? add_rmsnorm_fwd_kernel<T, R, 1>
+                : S.ch == 2 ? add_rmsnorm_fwd_kernel<T, R, 2>
+                            : add_rmsnorm_fwd_kernel<T, R, 4>;
     return twell_host::launch_dep(kern, dim3(static_cast<unsigned>((static_cast<long long>(a.N) + S.rpb - 1) / S.rpb)),
                                   dim3(S.threads()), 0, s, a);
 }
@@ -460,7 +535,9 @@ extern "C" twell_status twell_add_rmsnorm_fwd(const void* x, const void* res, co
     if (!aligned16(x) || !aligned16(res) || !aligned16(w) || !aligned16(h_out) || !aligned16(y) || !aligned16(y8) ||
         !aligned16(y8_scale) || !aligned16(rstd))
         return TWELL_ERR_INVALID;
-    const twell::NormShape S(d);
+    DevInfo dev;
+    if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
+    const twell::NormShape S(d, twell::fwd_chunks(N, d, res_dtype, dev.sm_count));
     const int g = group == 0 || d <= 128 ? d : group;
     const twell::NormFwdArgs a{x,    res, w, h_out, y,  static_cast<uint8_t*>(y8), y8_scale, rstd, N, d,
                                g, (d + g - 1) / g, S.wpr, S.rpb, eps, 1.0f / static_cast<float>(d)};

@@ -255,3 +255,30 @@ def test_forward_many_rows(cuda_dev, N, d, rt):
         one8, _, _ = binding.twell_add_rmsnorm_fwd_q8(x[rows], w, part, EPS, 128)
         assert torch.equal(one8.values.view(torch.uint8), y8.values[rows].view(torch.uint8))
         assert torch.equal(one8.scale, y8.scale[rows])
+
+
+# Batches that fill the device's threads, whose rows are spread over them otherwise than a few rows are: within the bounds
+# of a row, and still the row's results alone, bit for bit.
+@pytest.mark.parametrize("out", ["same", "whole", "groups"])
+@pytest.mark.parametrize("types", [(BF, BF), (BF, F32), (F32, F32), (BF, None)])
+@pytest.mark.parametrize("N,d", [(9001, 288), (2600, 1000), (1300, 2560), (700, 4104), (400, 8192)])
+def test_forward_wide_batches(cuda_dev, N, d, types, out):
+    dt, rt = types
+    x, w = _rand(cuda_dev, (N, d), dt, 41), _rand(cuda_dev, (d,), dt, 42)
+    res = _rand(cuda_dev, (N, d), rt, 43, 4.0) if rt is not None else None
+    rh, rs, ry = _ref_fwd(x, res, w)
+    if out == "same":
+        y, h, rstd = binding.twell_add_rmsnorm_fwd(x, w, res, EPS, training=True)
+        _within(y, ry, (_half(dt) + 64 * U) * ry.abs(), "y")
+        _within(rstd, rs, 64 * U * rs, "rstd")
+        few = binding.twell_add_rmsnorm_fwd(x[-5:], w, None if res is None else res[-5:], EPS, training=True)
+        assert torch.equal(few[0], y[-5:]) and torch.equal(few[2], rstd[-5:])
+    else:
+        group = 128 if out == "groups" else 0
+        y8, h, _ = binding.twell_add_rmsnorm_fwd_q8(x, w, res, EPS, group)
+        _check8(y8, ry, group)
+        few, _, _ = binding.twell_add_rmsnorm_fwd_q8(x[-5:], w, None if res is None else res[-5:], EPS, group)
+        assert torch.equal(few.values.view(torch.uint8), y8.values[-5:].view(torch.uint8))
+        assert torch.equal(few.scale, y8.scale[-5:])
+    if res is not None:
+        _within(h, rh, (_half(rt) + 4 * U) * rh.abs(), "h")
