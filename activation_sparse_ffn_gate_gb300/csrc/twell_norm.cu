@@ -271,9 +271,10 @@ __global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const 
     for (int i = 0; i < CH; ++i) {
         const int c = t + i * per_row;
         if (c >= chunks) continue;
-        const Scale8 q = Scale8::approx(top[i]);
+        const Scale8 q = Scale8::of(top[i]);
         *reinterpret_cast<uint2*>(a.y8 + base + i * step) = q.pack8(h[i]);
-        if (a.group == a.d ? c == 0 : (c & 15) == 0) a.scale[static_cast<size_t>(row) * static_cast<unsigned>(a.ng) + (c >> 4)] = q.scale;
+        if (a.group == a.d ? c == 0 : (c & 15) == 0)
+            a.scale[static_cast<size_t>(row) * static_cast<unsigned>(a.ng) + (c >> 4)] = q.scale;
     }
 }
 

@@ -94,13 +94,12 @@ constexpr float kAmaxMin = 8.6736173798840355e-19f;  // 2^-60
 
 struct Scale8 {
     float scale, mul;
-    // both to about 2^-23, for values that carry an error of that size themselves
-    __device__ __forceinline__ static Scale8 approx(float top)
+    // The factor is rounded once: with a reciprocal to 2^-23 2% to 10% more codes would fall to the other side of a tie
+    // (30000 x 1024 then takes 25.3 us, so 26.2); the scale's own error of 2^-23 moves no code.
+    __device__ __forceinline__ static Scale8 of(float top)
     {
         const float a = fmaxf(top, kAmaxMin);
-        float r;
-        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
-        return {a * (1.0f / kE4m3Max), kE4m3Max * r};
+        return {a * (1.0f / kE4m3Max), kE4m3Max / a};
     }
     // two codes, the first in the low byte
     __device__ __forceinline__ static uint32_t round2(float a, float b)
