@@ -15,15 +15,17 @@
 //     group of up to 8 query heads costs what one does. tcgen05's 64 to 128 rows a tile would be
 //     filled by 16 tokens a warp only after a block-wide exchange, and nothing here is bounded by
 //     the products. The scores' fragment becomes the second product's operand by an 8x8 transpose
-//     (movmatrix); with a bf16 cache the weights go in as hi + lo bf16 parts (~16 bits), with an
-//     e4m3 cache as fp16 (11 bits).
+//     (movmatrix); the weights go in as hi + lo parts, bf16 with a bf16 cache (~16 bits) and fp16 with an
+//     e4m3 cache (22 bits, of the largest weight 2^-40).
 //   - A batch of short sequences whose (sequence, key head)s about fill the SMs skips the list: one block each,
 //     which needs no second kernel; a large batch of short ones is dealt out in whole (sequence, key head)s, equally
 //     many a warp, and needs neither (the rules are in run_attn).
 //   - Running maximum m and sum l in fp32, per query head. For an e4m3 cache the value's scale s_t is
-//     folded into the weight, w_t = p_t s_t, and m runs over score + log2 s_t, so that the fp16
-//     weights stay in (0, 1] whatever the scales. The query is brought to [1, 2) by a power of two
-//     before its fp16 rounding (exact for bf16 values down to 2^-14 of the largest).
+//     folded into the weight, w_t = p_t s_t, and m runs over score + log2 s_t, so that the largest weight is
+//     2^15 whatever the scales: the fp16 parts then hold weights down to 2^-40 of it (with a largest weight of 1
+//     and one part, 131071 tokens of 2^-26 each, 0.2% of the sum, were lost). p_t is formed times 2^32, so that it
+//     neither overflows nor vanishes as long as a sequence's scales lie within 2^90 of one another. The query is
+//     brought to [1, 2) by a power of two before its fp16 rounding (exact for bf16 values down to 2^-14 of the largest).
 //   - Joining. A (sequence, key head) that lies within one warp's range is finished there. The parts
 //     (m, l, unnormalised o, fp32) of one that spans warps of a block are joined by the block, through
 //     shared memory; one that spans blocks leaves a part a block in the workspace, and a second kernel
@@ -45,6 +47,12 @@ constexpr int kPairIdle = 2, kPairTiles = 8;
 // When a warp takes whole ones: likewise.
 constexpr int kWholeTiles = 8, kWholeExtra = 4;
 constexpr float kNegInf = -INFINITY;
+// An e4m3 cache's sums: l is held times 2^kLift, the weights and o times 2^kUp (see scores); scales under kScaleMin count
+// as that in the running maximum.
+constexpr float kLift = 32.0f, kUp = 15.0f;
+constexpr float kWeight = 7.62939453125e-06f;        // 2^(kUp - kLift)
+constexpr float kOut = 131072.0f;                    // 2^(kLift - kUp)
+constexpr float kScaleMin = 2.8421709430404007e-14f;  // 2^-45
 
 // HD: head_dim; Q8: e4m3 cache; NT: query heads of one key head handled together, in eights.
 template <int HD, bool Q8, int NT>
@@ -365,7 +373,8 @@ struct AttnState {
                 if constexpr (Q8) {
                     ks = __uint_as_float(lds32(st + C::kHalf + 4 * tok));
                     vs[t][h] = __uint_as_float(lds32(st + C::kHalf + 4 * kTileTokens + 4 * tok));
-                    lv[t][h] = __log2f(fmaxf(vs[t][h], kAmaxMin));
+                    lv[t][h] = __log2f(fmaxf(vs[t][h], kScaleMin));
+                    vs[t][h] *= kWeight;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -402,7 +411,8 @@ struct AttnState {
                     o[i][n][3] *= f1;
                 }
             }
-            const float b0 = m[n][0] == kNegInf ? 0.0f : m[n][0], b1 = m[n][1] == kNegInf ? 0.0f : m[n][1];
+            const float lift = Q8 ? kLift : 0.0f;
+            const float b0 = (m[n][0] == kNegInf ? 0.0f : m[n][0]) - lift, b1 = (m[n][1] == kNegInf ? 0.0f : m[n][1]) - lift;
 #pragma unroll
             for (int t = 0; t < kMTiles; ++t) {
                 float p[4];
@@ -414,8 +424,14 @@ struct AttnState {
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];
                 if constexpr (Q8) {
-                    ph[t][n][0] = transpose8(f16x2_rn(p[0] * vs[t][0], p[1] * vs[t][0]));
-                    ph[t][n][1] = transpose8(f16x2_rn(p[2] * vs[t][1], p[3] * vs[t][1]));
+                    const float w0 = p[0] * vs[t][0], w1 = p[1] * vs[t][0], w2 = p[2] * vs[t][1], w3 = p[3] * vs[t][1];
+                    const uint32_t h0 = f16x2_rn(w0, w1), h1 = f16x2_rn(w2, w3);
+                    const float2 r0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                    const float2 r1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                    ph[t][n][0] = transpose8(h0);
+                    ph[t][n][1] = transpose8(h1);
+                    pl[t][n][0] = transpose8(f16x2_rn(w0 - r0.x, w1 - r0.y));
+                    pl[t][n][1] = transpose8(f16x2_rn(w2 - r1.x, w3 - r1.y));
                 } else {
                     const uint32_t h0 = bf16x2_rn(p[0], p[1]), h1 = bf16x2_rn(p[2], p[3]);
                     const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
@@ -483,8 +499,10 @@ struct AttnState {
                             e4m3x4_f16(x, a0, a1);
                             e4m3x4_f16(y, a2, a3);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                            for (int n = 0; n < NT; ++n) {
                                 mma_f16(o[2 * (w0 + w) + h][n], a0, a1, a2, a3, ph[t][n][0], ph[t][n][1]);
+                                mma_f16(o[2 * (w0 + w) + h][n], a0, a1, a2, a3, pl[t][n][0], pl[t][n][1]);
+                            }
                         }
                     }
                 }
@@ -530,7 +548,8 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int hv, int 
 {
     const int g = lane >> 2, c = lane & 3;
     const int kvh = hv / a.blocks, first = (hv % a.blocks) * 8 * NT + n * 8;
-    const float i0 = l0 > 0.0f || l0 != l0 ? 1.0f / l0 : 0.0f, i1 = l1 > 0.0f || l1 != l1 ? 1.0f / l1 : 0.0f;
+    constexpr float kOne = Q8 ? kOut : 1.0f;
+    const float i0 = l0 > 0.0f || l0 != l0 ? kOne / l0 : 0.0f, i1 = l1 > 0.0f || l1 != l1 ? kOne / l1 : 0.0f;
     __nv_bfloat16* base = a.out + (static_cast<int64_t>(b) * a.n_q + kvh * a.G) * HD;
     if constexpr (!Q8) {  // rows g and g + 8 of a tile, heads 2c and 2c + 1
 #pragma unroll
@@ -564,13 +583,13 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int hv, int 
     }
 }
 
-template <int NT>
+template <bool Q8, int NT>
 __device__ __forceinline__ void store_lse(const AttnArgs& a, int b, int hv, int head, float m, float l)
 {
     const int kvh = hv / a.blocks, j = (hv % a.blocks) * 8 * NT + head;
     if (a.lse != nullptr && j < a.G)
         a.lse[static_cast<int64_t>(b) * a.n_q + kvh * a.G + j] =
-            l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+            l == 0.0f ? kNegInf : (m + (log2f(l) - (Q8 ? kLift : 0.0f))) * 0.69314718055994531f;
 }
 
 // Parts joined for F float4 of o (fragments ni .. ni + F - 1 = eight heads x F dimension tiles, this lane) and the two
@@ -632,8 +651,8 @@ __device__ __forceinline__ void store_joined(const AttnArgs& a, int bhv, int HV,
     const int b = bhv / HV, hv = bhv % HV, e = ni / kMt;
     store_out<HD, Q8, NT, F>(a, b, hv, e, ni % kMt, lane, J.r, J.l0, J.l1);
     if (ni % kMt == 0 && lane < 4) {
-        store_lse<NT>(a, b, hv, e * 8 + 2 * lane, J.m0, J.l0);
-        store_lse<NT>(a, b, hv, e * 8 + 2 * lane + 1, J.m1, J.l1);
+        store_lse<Q8, NT>(a, b, hv, e * 8 + 2 * lane, J.m0, J.l0);
+        store_lse<Q8, NT>(a, b, hv, e * 8 + 2 * lane + 1, J.m1, J.l1);
     }
 }
 
@@ -927,8 +946,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, Q8, NT>::kWarps * 32, 1) paged_att
                         store_out<HD, Q8, NT, C::kF>(a, cur.b, cur.hv, e, i, lane, r, S.l[e][0], S.l[e][1]);
                     }
                     if (lane < 4) {
-                        store_lse<NT>(a, cur.b, cur.hv, e * 8 + 2 * lane, S.m[e][0], S.l[e][0]);
-                        store_lse<NT>(a, cur.b, cur.hv, e * 8 + 2 * lane + 1, S.m[e][1], S.l[e][1]);
+                        store_lse<Q8, NT>(a, cur.b, cur.hv, e * 8 + 2 * lane, S.m[e][0], S.l[e][0]);
+                        store_lse<Q8, NT>(a, cur.b, cur.hv, e * 8 + 2 * lane + 1, S.m[e][1], S.l[e][1]);
                     }
                 }
             } else if (it + 1 < n) {  // ends inside the range, began before it

@@ -350,3 +350,69 @@ def test_many_short_sequences_with_bad_lengths(cuda_dev):
     out, lse = c.run()
     assert binding.twell_read_status() == 5
     assert torch.equal(out, good) and (lse[199] == -math.inf).all()
+
+
+def _direct(dev, k, v, q, scale):
+    """One sequence over an e4m3 cache of one key head whose values are exact codes: k, v [n, hd] as power-of-two scales
+    times codes; returns out, lse, the references of lse and out in 64 bits, sum p |v| and the largest p amax|v|."""
+    n, hd = k.shape
+    ps = 64
+    pages = -(-n // ps)
+    parts = []
+    for x in (k, v):
+        top = x.double().abs().amax(-1)
+        s = torch.where(top > 0, 2.0 ** (torch.log2(top.clamp_min(1e-300)).floor() - 7), torch.ones_like(top)).float()
+        codes = torch.zeros((pages * ps, hd))
+        codes[:n] = x / s[:, None]
+        assert torch.equal(codes[:n].to(E4).double() * s.double()[:, None], x.double())
+        scales = torch.zeros(pages * ps)
+        scales[:n] = s
+        parts += [codes.to(E4).view(pages, 1, ps, hd).to(dev), scales.view(pages, 1, ps).to(dev)]
+    cache = binding.KVCache(parts[0], parts[2], parts[1], parts[3])
+    table = torch.arange(pages, dtype=torch.int32, device=dev).view(1, pages)
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    lse = torch.empty((1, 1), dtype=F32, device=dev)
+    out, _ = binding.twell_paged_attn_decode(q.to(BF).view(1, 1, hd).to(dev), cache, table, lens, scale=scale, lse=lse)
+    z = scale * (k.double() @ q.to(BF).double())
+    rl = torch.logsumexp(z, 0)
+    p = torch.exp(z - rl)
+    return (out.cpu().double().view(hd), lse.item(), rl.item(), p @ v.double(), p @ v.double().abs(),
+            (p * v.double().abs().amax(-1)).max().item())
+
+
+@pytest.mark.parametrize("n", [600, 131072])
+def test_many_small_weights_in_an_8bit_cache(cuda_dev, n):
+    """One token of nearly all the mass and a long tail of 2^-26 of it each, seen alone in half of the dimensions. A weight
+    is off by 2^-22 of itself, 2^-40 of the largest and the score's error, here below 2^-14 as in the file's bounds: the
+    tail's share is within 2^-12 of itself, and its bf16 rounding."""
+    hd = 64
+    k, v = torch.zeros((n, hd)), torch.zeros((n, hd))
+    k[0] = 2.25 / hd  # q . k of the first token: 18, under a scale that makes it 26 in base 2
+    v[0, :hd // 2] = 1.0
+    v[1:, hd // 2:] = 1.0
+    out, lse, rl, ro, _, _ = _direct(cuda_dev, k, v, torch.full((hd,), 8.0), 26 * math.log(2) / 18)
+    assert ((out - ro).abs() <= (2.0 ** -8 + 2.0 ** -12) * ro.abs()).all(), (out, ro)
+    assert abs(lse - rl) <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 26, 2.0 ** -26])
+def test_values_of_very_different_sizes_in_an_8bit_cache(cuda_dev, ratio):
+    """Every 50th value is `ratio` times the others, in the first half of the dimensions; the second half holds the other
+    values alone. The weights' bounds of the test above; 2^-40 of the largest weight is, in values, n 2^-40 of the
+    largest p amax|v|."""
+    hd, n = 128, 1000
+    g = torch.Generator("cpu").manual_seed(30)
+    k = torch.randint(-8, 9, (n, hd), generator=g).float() / 8
+    v = torch.randint(1, 16, (n, hd), generator=g).float() / 8
+    v[:, 0] = v[:, hd // 2] = 15 / 8
+    loud = torch.arange(n) % 50 == 7
+    v[loud] *= ratio
+    v[loud, hd // 2:] = 0
+    v[~loud, :hd // 2] = 0
+    q = torch.randint(-8, 9, (hd,), generator=g).float() / 8
+    out, lse, rl, ro, mass, top = _direct(cuda_dev, k, v, q, 1 / math.sqrt(hd))
+    e = hd * 2.0 ** -22 / math.sqrt(hd) * hd
+    w = 2 * (2 * e + 2.0 ** -14 + 2.0 ** -20)
+    err, bound = (out - ro).abs(), 2.0 ** -8 * ro.abs() + w * mass + n * 2.0 ** -40 * top
+    assert (err <= bound).all(), (err / bound).max().item()
+    assert abs(lse - rl) <= e + 2.0 ** -14
