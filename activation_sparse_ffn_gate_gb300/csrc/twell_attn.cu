@@ -373,7 +373,8 @@ struct AttnState {
                 if constexpr (Q8) {
                     ks = __uint_as_float(lds32(st + C::kHalf + 4 * tok));
                     vs[t][h] = __uint_as_float(lds32(st + C::kHalf + 4 * kTileTokens + 4 * tok));
-                    lv[t][h] = __log2f(fmaxf(vs[t][h], kScaleMin));
+                    // of a value that is not finite: any, so that m and l, which do not depend on values, stay finite
+                    lv[t][h] = __log2f(vs[t][h] < INFINITY ? fmaxf(vs[t][h], kScaleMin) : 1.0f);
                     vs[t][h] *= kWeight;
                 }
 #pragma unroll

@@ -416,3 +416,29 @@ def test_values_of_very_different_sizes_in_an_8bit_cache(cuda_dev, ratio):
     err, bound = (out - ro).abs(), 2.0 ** -8 * ro.abs() + w * mass + n * 2.0 ** -40 * top
     assert (err <= bound).all(), (err / bound).max().item()
     assert abs(lse - rl) <= e + 2.0 ** -14
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_lse_does_not_depend_on_values(cuda_dev, bad, dtype):
+    """A value that is not finite makes its head's output so, and leaves lse alone; sequences of the three sizes that
+    a batch's forms take, the value in a full tile and in the last one."""
+    lens = [9000, 70, 33]
+    c = Case(cuda_dev, lens, 2, 4, 64, 16, dtype, seed=31)
+    out, lse = c.run()
+    for b, t in ((0, 4001), (1, 69)):
+        slot = torch.tensor([int(c.table[b, t // 16]) * 16 + t % 16], dtype=torch.int32, device=cuda_dev)
+        k, v = binding.twell_kv_gather(c.cache, slot)
+        v[0, 1, 5] = bad
+        rest = [x.view(torch.uint8) if x.dtype == E4 else x for x in
+                (c.cache.k, c.cache.v[:, :1]) + (() if dtype == BF else (c.cache.k_scale, c.cache.v_scale[:, :1]))]
+        kept = [x.clone() for x in rest]
+        binding.twell_kv_append(c.cache, k, v, slot)
+        for x, y in zip(rest, kept):  # the keys and the other head's values as they were, not rounded once more
+            x.copy_(y)
+    new, nl = c.run()
+    # an e4m3 row with an infinity has an infinite scale: log2 of the others' stays in the running maximum, so that
+    # the same sums are formed under other maxima
+    assert torch.isfinite(nl).all() and ((nl - lse).abs() <= 2.0 ** -14).all()
+    assert not torch.isfinite(new[:2, 4:, 5]).any()
+    assert torch.equal(new[2], out[2]) and torch.equal(new[:, :4], out[:, :4])
