@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <map>
+#include <mutex>
 #include <tuple>
 
 #include "twell.h"
@@ -92,28 +93,40 @@ float number(PyObject* o)
     return static_cast<float>(v);
 }
 
-// The workspace of one operator on one device and stream, grown on demand: calls on one stream run one after the other,
-// so they can share it. It is allocated on that stream, so that an outgrown one is not handed out again before the calls
-// that use it are done. The map is never destroyed (its tensors would outlive the CUDA context).
-const at::Tensor& workspace(twell_op op, int32_t N, int32_t d, int dev, const c10::cuda::CUDAStream& s)
+// A call's workspace: its memory, held while the call launches, and the lock that its launches are made under where
+// other calls use the same one.
+struct Workspace {
+    at::Tensor t;
+    std::mutex* turn;
+};
+
+// The workspace of one operator on one device and stream, grown on demand: the kernels of one stream run one after the
+// other, so calls can share it, each making its launches (two where a second kernel reads what a first left there)
+// without another thread's between them. It is allocated on that stream, so that an outgrown one is not handed out again
+// before the calls that use it are done. The map is never destroyed (its tensors would outlive the CUDA context).
+Workspace workspace(twell_op op, int32_t N, int32_t d, int dev, const c10::cuda::CUDAStream& s)
 {
-    static auto* all = new std::map<std::tuple<int, int, cudaStream_t>, at::Tensor>();
+    struct Shared {
+        at::Tensor t;
+        std::mutex turn;
+    };
+    static auto* all = new std::map<std::tuple<int, int, cudaStream_t>, Shared>();
     const int64_t bytes = std::max<int64_t>(static_cast<int64_t>(twell_workspace_bytes(op, N, d, 1, 0, 0, 0)), 1);
-    at::Tensor& t = (*all)[{static_cast<int>(op), dev, s.stream()}];
-    if (!t.defined() || t.numel() < bytes) {
+    Shared& w = (*all)[{static_cast<int>(op), dev, s.stream()}];
+    if (!w.t.defined() || w.t.numel() < bytes) {
         const c10::cuda::CUDAStreamGuard guard(s);
-        t = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+        w.t = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
     }
-    return t;
+    return {w.t, &w.turn};
 }
 
 // The caller's workspace, or the stream's.
-const at::Tensor& workspace(PyObject* o, twell_op op, int32_t N, int32_t d, int dev, const c10::cuda::CUDAStream& s)
+Workspace workspace(PyObject* o, twell_op op, int32_t N, int32_t d, int dev, const c10::cuda::CUDAStream& s)
 {
     if (o == Py_None) return workspace(op, N, d, dev, s);
     const at::Tensor* t = tensor(o, "ws");
     need(t, "ws", at::kByte, {t->numel()}, dev);
-    return *t;
+    return {*t, nullptr};
 }
 
 const twell_kv_cache* cache_at(PyObject* o)
@@ -136,12 +149,20 @@ int64_t heads_stride(const at::Tensor& t, const char* what, int64_t n, int64_t h
     return n > 1 ? t.stride(0) : heads * hd;
 }
 
+// The C call, without the interpreter's lock; under a shared workspace's own, which is taken and given back while the
+// interpreter's is not held, so that neither waits for the other.
 template <typename F>
-PyObject* call(F f)
+PyObject* call(F f, std::mutex* turn = nullptr)
 {
     twell_status st;
-    Py_BEGIN_ALLOW_THREADS st = f();
-    Py_END_ALLOW_THREADS return PyLong_FromLong(st);
+    Py_BEGIN_ALLOW_THREADS
+    {
+        std::unique_lock<std::mutex> lock;
+        if (turn != nullptr) lock = std::unique_lock<std::mutex>(*turn);
+        st = f();
+    }
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
 }
 
 PyObject* count_error(const char* name, Py_ssize_t want, Py_ssize_t got)
@@ -203,14 +224,14 @@ PyObject* add_rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* pdx = need(tensor(a[5], "dx"), "dx", g, {N, d}, dev);
     void* pdw = need(tensor(a[6], "dw"), "dw", at::kFloat, {d}, dev);
     const auto s = stream_of(a[8], dev);
-    const at::Tensor& ws = workspace(a[7], TWELL_OP_ADD_RMSNORM_BWD, static_cast<int32_t>(N), static_cast<int32_t>(d), dev, s);
-    void* pws = ws.data_ptr();
-    const size_t bytes = static_cast<size_t>(ws.numel());
+    const Workspace ws = workspace(a[7], TWELL_OP_ADD_RMSNORM_BWD, static_cast<int32_t>(N), static_cast<int32_t>(d), dev, s);
+    void* pws = ws.t.data_ptr();
+    const size_t bytes = static_cast<size_t>(ws.t.numel());
     return call([&] {
         return twell_add_rmsnorm_bwd(pdy, ph, pw, static_cast<const float*>(prs), pdh, static_cast<int32_t>(N),
                                      static_cast<int32_t>(d), ct, cr, cg, pdx, static_cast<float*>(pdw), pws, bytes,
                                      s.stream());
-    });
+    }, ws.turn);
     END_HANDLE_TH_ERRORS
 }
 
@@ -276,14 +297,14 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     const float scale = number(a[5]);
     const int32_t window = integer(a[6]);
     const auto s = stream_of(a[11], dev);
-    const at::Tensor& ws = workspace(a[9], TWELL_OP_PAGED_ATTN, static_cast<int32_t>(B), static_cast<int32_t>(hd), dev, s);
-    void* pws = ws.data_ptr();
-    const size_t bytes = static_cast<size_t>(ws.numel());
+    const Workspace ws = workspace(a[9], TWELL_OP_PAGED_ATTN, static_cast<int32_t>(B), static_cast<int32_t>(hd), dev, s);
+    void* pws = ws.t.data_ptr();
+    const size_t bytes = static_cast<size_t>(ws.t.numel());
     return call([&] {
         return twell_paged_attn_decode(q.data_ptr(), stride, c, static_cast<const int32_t*>(pt), static_cast<const int32_t*>(pl),
                                        static_cast<int32_t>(B), static_cast<int32_t>(H), static_cast<int32_t>(table.size(1)), scale,
                                        window, po, static_cast<float*>(ps), pws, bytes, static_cast<int32_t*>(st), s.stream());
-    });
+    }, ws.turn);
     END_HANDLE_TH_ERRORS
 }
 

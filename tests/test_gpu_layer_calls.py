@@ -1,0 +1,80 @@
+"""How the operators around the FFN are called: from several threads, on other streams, in CUDA graphs. What is
+computed is checked elsewhere; here every result is compared bit for bit with that of the plain call."""
+import threading
+
+import pytest
+import torch
+
+from activation_sparse_ffn_gate_gb300 import binding, build
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_dev):
+    build.build()
+    binding.load()
+    binding.status_buffer(cuda_dev).zero_()
+    yield
+    assert binding.twell_read_status() == 0, "device status was raised"
+
+
+def _rand(dev, *shape, seed, dtype=BF, scale=1.0):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g)).to(dtype).to(dev)
+
+
+class Attn:
+    """An attention whose sequences are split over many blocks: parts in the workspace, joined by a second kernel."""
+
+    def __init__(self, dev, seed, n=6000, B=2, hd=128):
+        k, v = (_rand(dev, 40 * B, 2, 64, hd, seed=seed + i, dtype=F32).to(BF) for i in (0, 1))
+        pages = -(-n // 64)
+        self.cache = binding.KVCache(k, v)
+        self.table = (torch.arange(B * pages, dtype=torch.int32, device=dev) % (40 * B)).view(B, pages)
+        self.lens = torch.tensor([n - 13 * i for i in range(B)], dtype=torch.int32, device=dev)
+        self.q = _rand(dev, B, 8, hd, seed=seed + 2)
+
+    def __call__(self, **kw):
+        return binding.twell_paged_attn_decode(self.q, self.cache, self.table, self.lens, **kw)[0]
+
+
+class Grad:
+    """A norm's backward: partial rows of dw in the workspace, added by a second kernel."""
+
+    def __init__(self, dev, seed, N=900, d=1024):
+        self.h, self.dy = _rand(dev, N, d, seed=seed, dtype=F32), _rand(dev, N, d, seed=seed + 1, dtype=F32)
+        self.w = _rand(dev, d, seed=seed + 2, dtype=F32)
+        self.rstd = torch.rsqrt(self.h.square().mean(-1) + 1e-6)
+
+    def __call__(self, **kw):
+        return torch.cat([t.reshape(-1) for t in
+                          binding.twell_add_rmsnorm_bwd(self.dy, self.h, self.w, self.rstd, **kw)])
+
+
+@pytest.mark.parametrize("what", [Attn, Grad])
+def test_threads_that_share_a_stream(cuda_dev, what):
+    """The default stream is the same for all threads, and so is its workspace; a call's two launches stay together."""
+    calls = [what(cuda_dev, 10 * i) for i in range(6)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in calls], []
+    start = threading.Barrier(len(calls))
+
+    def run(i):
+        try:
+            start.wait()
+            for _ in range(60):
+                got[i].append(calls[i]())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    assert all(torch.equal(o, w) for os, w in zip(got, want) for o in os)
