@@ -1009,7 +1009,7 @@ def twell_paged_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.T
     1/sqrt(head_dim) unless given; window > 0 keeps the last `window` tokens. out bf16, written; lse fp32
     [B, n_q_heads] (natural logarithm of the sum of exponentials) is written when a buffer is given. A
     sequence of length 0 gives zeros and -inf. ws: the caller's workspace; without one the calls of a stream share
-    theirs, so give one to a call captured into a graph that may replay beside other calls."""
+    theirs, and a call that is captured into a graph has its own in the graph's memory."""
     dev = cache.index
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)

@@ -9,9 +9,11 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -100,23 +102,40 @@ struct Workspace {
     std::mutex* turn;
 };
 
-// The workspace of one operator on one device and stream, grown on demand: the kernels of one stream run one after the
-// other, so calls can share it, each making its launches (two where a second kernel reads what a first left there)
-// without another thread's between them. It is allocated on that stream, so that an outgrown one is not handed out again
-// before the calls that use it are done. The map is never destroyed (its tensors would outlive the CUDA context).
+// Bytes that any call of an operator needs. Its buffers have this size from the start (10 MB and 26 MB) and are never
+// replaced.
+int64_t most_bytes(twell_op op)
+{
+    if (op == TWELL_OP_PAGED_ATTN) return static_cast<int64_t>(twell_workspace_bytes(op, 1, 256, 1, 0, 0, 0));
+    size_t most = 1;
+    for (int32_t d = 8; d <= 16384; d += 8) most = std::max(most, twell_workspace_bytes(op, INT32_MAX, d, 1, 0, 0, 0));
+    return static_cast<int64_t>(most);
+}
+
+at::Tensor bytes_on(int64_t n, int dev, const c10::cuda::CUDAStream& s)
+{
+    const c10::cuda::CUDAStreamGuard guard(s);
+    return at::empty({n}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+}
+
+// The workspace of one operator on one device and stream: the kernels of one stream run one after the other, so calls can
+// share it, each making its launches (two where a second kernel reads what a first left there) without another thread's
+// between them. A call that is being captured into a graph gets one of its own, from the graph's memory: the graph
+// may replay on any stream, beside any other call. The map is never destroyed (its tensors would outlive the
+// CUDA context).
 Workspace workspace(twell_op op, int32_t N, int32_t d, int dev, const c10::cuda::CUDAStream& s)
 {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    C10_CUDA_CHECK(cudaStreamIsCapturing(s.stream(), &capture));
+    if (capture != cudaStreamCaptureStatusNone)
+        return {bytes_on(std::max<int64_t>(static_cast<int64_t>(twell_workspace_bytes(op, N, d, 1, 0, 0, 0)), 1), dev, s), nullptr};
     struct Shared {
         at::Tensor t;
         std::mutex turn;
     };
     static auto* all = new std::map<std::tuple<int, int, cudaStream_t>, Shared>();
-    const int64_t bytes = std::max<int64_t>(static_cast<int64_t>(twell_workspace_bytes(op, N, d, 1, 0, 0, 0)), 1);
     Shared& w = (*all)[{static_cast<int>(op), dev, s.stream()}];
-    if (!w.t.defined() || w.t.numel() < bytes) {
-        const c10::cuda::CUDAStreamGuard guard(s);
-        w.t = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
-    }
+    if (!w.t.defined()) w.t = bytes_on(most_bytes(op), dev, s);
     return {w.t, &w.turn};
 }
 

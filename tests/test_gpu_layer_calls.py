@@ -78,3 +78,55 @@ def test_threads_that_share_a_stream(cuda_dev, what):
     torch.cuda.synchronize()
     assert not errors
     assert all(torch.equal(o, w) for os, w in zip(got, want) for o in os)
+
+
+def _capture(call, stream):
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = call()
+    return graph, out
+
+
+@pytest.mark.parametrize("small,large", [(lambda dev: Grad(dev, 1, 400, 256), lambda dev: Grad(dev, 4, 4000, 8192)),
+                                         (lambda dev: Attn(dev, 1, hd=64), lambda dev: Attn(dev, 4, hd=256))],
+                         ids=["grad", "attn"])
+def test_a_graph_writes_to_no_ones_memory(cuda_dev, small, large):
+    """A larger call on the stream after the capture, then tensors that fill what the allocator has free: they keep their
+    values through the replays, and the graph's results are the call's."""
+    call, more = small(cuda_dev), large(cuda_dev)
+    want = call()
+    side = torch.cuda.Stream()
+    graph, out = _capture(call, side)
+    with torch.cuda.stream(side):
+        more()
+        side.synchronize()
+        fills = [torch.full((n,), 7, dtype=torch.uint8, device=cuda_dev) for n in [1 << 20] * 40 + [1 << 22] * 20]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(bool((t == 7).all()) for t in fills)
+
+
+@pytest.mark.parametrize("what", [Attn, Grad])
+def test_a_graph_replays_beside_other_calls(cuda_dev, what):
+    """Two graphs captured on one stream and plain calls on that stream, all at once on three streams."""
+    a, b, c = (what(cuda_dev, 10 * i) for i in range(3))
+    want = [x() for x in (a, b, c)]
+    side, others = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(2)]
+    graphs = [_capture(x, side) for x in (a, b)]
+    got = []
+    for _ in range(30):
+        for (g, _), s in zip(graphs, others):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(side):
+            got.append(c())
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1], want[0]) and torch.equal(graphs[1][1], want[1])
+    assert all(torch.equal(o, want[2]) for o in got)
