@@ -1063,9 +1063,10 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
     words = torch.empty((nt, kt, 8, 4, 2, 4), dtype=torch.int32, device=W.device)
     scales = torch.empty((nt, kt, 8, 2, 128 // group), dtype=torch.bfloat16, device=W.device)
     out = W4Weights(words, scales, n, k, group)
-    _check(load().twell_w4_quantize(_ptr(W), n, k, group, _ptr(words), _ptr(scales), _ptr(_status(status, W.get_device())),
-                                    _stream(stream)),
-           "twell_w4_quantize")
+    with torch.cuda.device(W.device):
+        _check(load().twell_w4_quantize(_ptr(W), n, k, group, _ptr(words), _ptr(scales),
+                                        _ptr(_status(status, W.get_device())), _stream(stream)),
+               "twell_w4_quantize")
     return out
 
 

@@ -168,11 +168,13 @@ int64_t heads_stride(const at::Tensor& t, const char* what, int64_t n, int64_t h
     return n > 1 ? t.stride(0) : heads * hd;
 }
 
-// The C call, without the interpreter's lock; under a shared workspace's own, which is taken and given back while the
+// The C call on device `dev`, which is made current for it (the entries launch on the current device, and a default
+// stream's handle is the same on all), without the interpreter's lock; under a shared workspace's own, which is taken and given back while the
 // interpreter's is not held, so that neither waits for the other.
 template <typename F>
-PyObject* call(F f, std::mutex* turn = nullptr)
+PyObject* call(int dev, F f, std::mutex* turn = nullptr)
 {
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     twell_status st;
     Py_BEGIN_ALLOW_THREADS
     {
@@ -217,7 +219,7 @@ PyObject* add_rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* pd = need(tensor(a[9], "rstd", true), "rstd", at::kFloat, {N}, dev);
     const float eps = number(a[3]);
     const auto s = stream_of(a[10], dev);
-    return call([&] {
+    return call(dev, [&] {
         return twell_add_rmsnorm_fwd(px, pr, pw, static_cast<int32_t>(N), static_cast<int32_t>(d), eps, ct, cr, ph, py_, p8,
                                      static_cast<float*>(ps), group, static_cast<float*>(pd), s.stream());
     });
@@ -246,7 +248,7 @@ PyObject* add_rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     const Workspace ws = workspace(a[7], TWELL_OP_ADD_RMSNORM_BWD, static_cast<int32_t>(N), static_cast<int32_t>(d), dev, s);
     void* pws = ws.t.data_ptr();
     const size_t bytes = static_cast<size_t>(ws.t.numel());
-    return call([&] {
+    return call(dev, [&] {
         return twell_add_rmsnorm_bwd(pdy, ph, pw, static_cast<const float*>(prs), pdh, static_cast<int32_t>(N),
                                      static_cast<int32_t>(d), ct, cr, cg, pdx, static_cast<float*>(pdw), pws, bytes,
                                      s.stream());
@@ -268,7 +270,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int64_t ldv = heads_stride(v, "v", m, c->n_kv_heads, c->head_dim, dev);
     void* st = need(tensor(a[5], "status"), "status", at::kInt, {1}, dev);
     const auto s = stream_of(a[6], dev);
-    return call([&] {
+    return call(dev, [&] {
         return twell_kv_append(c, k.data_ptr(), v.data_ptr(), ldk, ldv, static_cast<const int32_t*>(psl), static_cast<int32_t>(m),
                                static_cast<int32_t*>(st), s.stream());
     });
@@ -289,7 +291,7 @@ PyObject* kv_gather(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* pv = need(tensor(a[4], "v_out"), "v_out", at::kBFloat16, {m, H, hd}, dev);
     void* st = need(tensor(a[5], "status"), "status", at::kInt, {1}, dev);
     const auto s = stream_of(a[6], dev);
-    return call([&] {
+    return call(dev, [&] {
         return twell_kv_gather(c, static_cast<const int32_t*>(psl), static_cast<int32_t>(m), pk, pv, static_cast<int32_t*>(st),
                                s.stream());
     });
@@ -319,7 +321,7 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     const Workspace ws = workspace(a[9], TWELL_OP_PAGED_ATTN, static_cast<int32_t>(B), static_cast<int32_t>(hd), dev, s);
     void* pws = ws.t.data_ptr();
     const size_t bytes = static_cast<size_t>(ws.t.numel());
-    return call([&] {
+    return call(dev, [&] {
         return twell_paged_attn_decode(q.data_ptr(), stride, c, static_cast<const int32_t*>(pt), static_cast<const int32_t*>(pl),
                                        static_cast<int32_t>(B), static_cast<int32_t>(H), static_cast<int32_t>(table.size(1)), scale,
                                        window, po, static_cast<float*>(ps), pws, bytes, static_cast<int32_t*>(st), s.stream());
@@ -344,7 +346,7 @@ PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t n)
     const void* ps = need(&scales, "scales", at::kBFloat16, {nt, kt, 8, 2, 128 / group}, dev);
     void* po = need(tensor(a[6], "y"), "y", at::kBFloat16, {N, rows}, dev);
     const auto s = stream_of(a[7], dev);
-    return call([&] {
+    return call(dev, [&] {
         return twell_w4_matvec(px, pw, ps, static_cast<int32_t>(N), static_cast<int32_t>(rows), static_cast<int32_t>(cols), group, po,
                                s.stream());
     });

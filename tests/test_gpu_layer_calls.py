@@ -130,3 +130,19 @@ def test_a_graph_replays_beside_other_calls(cuda_dev, what):
     torch.cuda.synchronize()
     assert torch.equal(graphs[0][1], want[0]) and torch.equal(graphs[1][1], want[1])
     assert all(torch.equal(o, want[2]) for o in got)
+
+
+def test_the_tensors_device_is_made_current(cuda_dev, monkeypatch):
+    """With one device there is nothing else to be on: the quantiser, which sets the device in Python, is seen to do so. The
+    other calls do it in the native module, whose call() takes the device and cannot be made without."""
+    seen = []
+    device = torch.cuda.device
+
+    class Seen(device):
+        def __enter__(self):
+            seen.append(self.idx)
+            return super().__enter__()
+
+    monkeypatch.setattr(torch.cuda, "device", Seen)
+    binding.twell_w4_quantize(_rand(cuda_dev, 16, 128, seed=1))
+    assert seen == [cuda_dev.index]
