@@ -176,3 +176,73 @@ def test_training_step_of_the_ffn_half(cuda_dev):
     ((norm * P[0].grad).sum() + (r * dh.double()).sum()).backward()
     for got, want in zip(grads, (r.grad, wn.grad, P[1].grad, P[2].grad, P[3].grad)):
         assert got.dtype == torch.float32 and _rel(got, want) <= 5e-3
+
+
+def _busy(dev):
+    """Allocations and fills on the current stream, as a program makes them beside another stream's work."""
+    return [torch.full((n,), 3.0, dtype=BF, device=dev) for n in (256, 1024, 4096, 16384, 65536) for _ in range(20)]
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_decode_on_another_stream(cuda_dev, first):
+    """A step with stream=s gives, bit for bit, what it gives on the current stream: the rotation is queued on s, and what
+    the current stream allocates and fills meanwhile is none of the step's memory."""
+    def rotate(q, k):
+        seen.append(torch.cuda.current_stream())
+        q.mul_(-0.5)
+        k.mul_(2.0)
+
+    seen = []
+    hd, hq, hk, B, n = 128, 8, 2, 6, 300
+    layer = _layer(cuda_dev, 512, 1024, hq, hk, hd, rotate=rotate)
+    table = torch.arange(B * 5, dtype=torch.int32, device=cuda_dev).view(B, 5)
+    past = [_rand(cuda_dev, B * n, hk, hd, seed=s) for s in (1, 2)]
+    pos = torch.arange(n, device=cuda_dev)
+    slots = (table[:, pos // 64] * 64 + pos % 64).to(torch.int32).reshape(-1)
+    new = (table[:, n // 64] * 64 + n % 64).to(torch.int32)
+    lens = torch.full((B,), n + 1, dtype=torch.int32, device=cuda_dev)
+    x = _rand(cuda_dev, B, 512, seed=91)
+    h = None if first else _rand(cuda_dev, B, 512, seed=92, dtype=torch.float32)
+
+    def steps(stream):
+        cache = binding.KVCache.empty(B * 5, 64, hk, hd, BF, cuda_dev)
+        binding.twell_kv_append(cache, *past, slots)
+        torch.cuda.synchronize()
+        outs, other = [], []
+        for _ in range(8):
+            outs.append(layer.decode(x, h, cache, new, table, lens, stream=stream))
+            other += _busy(cuda_dev)
+        torch.cuda.synchronize()
+        return outs, other
+
+    want, _ = steps(None)
+    s = torch.cuda.Stream()
+    seen.clear()
+    got, other = steps(s)
+    assert seen == [s] * 8
+    for (a, b), (c, d) in zip(got, want):
+        assert torch.equal(a, c) and torch.equal(b, d)
+    assert all(bool((t == 3.0).all()) for t in other)
+
+
+def test_training_step_on_another_stream(cuda_dev):
+    N, d, f, K = 64, 256, 512, 300
+    h, delta = _rand(cuda_dev, N, d, seed=1, dtype=torch.float32, scale=2.0), _rand(cuda_dev, N, d, seed=2)
+    w = (1 + _rand(cuda_dev, d, seed=3, scale=0.1).float()).to(BF)
+    Wg, Wu = (_rand(cuda_dev, f, d, seed=s, scale=d ** -0.5) for s in (4, 5))
+    Wd = _rand(cuda_dev, f, d, seed=6, scale=f ** -0.5)
+    df, dh = _rand(cuda_dev, N, d, seed=7), _rand(cuda_dev, N, d, seed=8, dtype=torch.float32)
+
+    def step(stream):
+        torch.cuda.synchronize()
+        out, h1, saved = block.ffn_sublayer_fwd(delta, h, w, Wg, Wu, Wd, K, N, stream=stream)
+        other = _busy(cuda_dev)
+        grads = block.ffn_sublayer_bwd(df, dh, saved, stream=stream)
+        other += _busy(cuda_dev)
+        torch.cuda.synchronize()
+        assert all(bool((t == 3.0).all()) for t in other)
+        return out, h1, grads[0], grads[1]
+
+    want = step(None)
+    for a, b in zip(step(torch.cuda.Stream()), want):
+        assert torch.equal(a, b)
