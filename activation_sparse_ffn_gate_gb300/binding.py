@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import importlib
+import inspect
 import os
 import threading
 from typing import Optional
@@ -176,6 +178,37 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _under(stream):
+    """The context in which what is allocated belongs to `stream`."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _on_its_stream(fn):
+    """A call that is given a stream runs under it as a whole: the outputs and workspaces that it allocates belong to that
+    stream, as the kernels that write them do. On the current one their memory could still be in use by
+    that stream's work, and would go back to it while the kernels run."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        with _under(stream):
+            return fn(*args, **kwargs)
+
+    return call
+
+
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """The same for one output, for the calls that a decode step makes many of."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _under(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.bfloat16:
         return TWELL_BF16
@@ -278,6 +311,7 @@ class TwELL:
                        self.vals.data_ptr(), self.idx.data_ptr(), self.cnt.data_ptr())
 
 
+@_on_its_stream
 def twell_gate_pack(x: torch.Tensor, Wg_s: torch.Tensor, T: int = 128, out: Optional[TwELL] = None,
                     status: Optional[torch.Tensor] = None, stream=None,
                     vals_dtype: torch.dtype = torch.float32) -> TwELL:
@@ -294,6 +328,7 @@ def twell_gate_pack(x: torch.Tensor, Wg_s: torch.Tensor, T: int = 128, out: Opti
     return out
 
 
+@_on_its_stream
 def twell_ffn_fused_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd_s: torch.Tensor, a: TwELL,
                         y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                         stream=None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -311,6 +346,7 @@ def twell_ffn_fused_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd_s: torch.Tensor,
     return y
 
 
+@_on_its_stream
 def twell_convert_f16(src: torch.Tensor, out: Optional[torch.Tensor] = None, status=None,
                       stream=None) -> torch.Tensor:
     """A bf16 tensor converted to fp16 by the library (e.g. Wd_s for twell_ffn_fused_fwd_f16down)."""
@@ -324,6 +360,7 @@ def twell_convert_f16(src: torch.Tensor, out: Optional[torch.Tensor] = None, sta
     return out
 
 
+@_on_its_stream
 def twell_convert_f16_transposed(src: torch.Tensor, out: Optional[torch.Tensor] = None, status=None,
                                  stream=None) -> torch.Tensor:
     """The transpose of a 2-D bf16 tensor converted to fp16 by the library (e.g. Wd_s [f, d] -> Wd16t_s
@@ -339,6 +376,7 @@ def twell_convert_f16_transposed(src: torch.Tensor, out: Optional[torch.Tensor] 
     return out
 
 
+@_on_its_stream
 def twell_ffn_fused_fwd_f16down(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: torch.Tensor, a: TwELL,
                                 y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                                 stream=None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -410,6 +448,7 @@ class StreamedFFN:
 _union_ws = {}
 
 
+@_on_its_stream
 def twell_ffn_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16t_s: torch.Tensor, a: TwELL,
                         y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                         stream=None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -437,6 +476,7 @@ def twell_ffn_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16t_s: torch.Tens
     return y
 
 
+@_on_its_stream
 def twell_ffn_gate_union_fwd(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Tensor, Wd16t_s: torch.Tensor,
                              T: int = 128, out: Optional[TwELL] = None, y: Optional[torch.Tensor] = None,
                              status: Optional[torch.Tensor] = None, stream=None, ws: Optional[torch.Tensor] = None,
@@ -469,6 +509,7 @@ def twell_ffn_gate_union_fwd(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Te
 _tile_union_ws = {}
 
 
+@_on_its_stream
 def twell_ffn_tile_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: torch.Tensor, a: TwELL,
                              y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                              stream=None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -498,6 +539,7 @@ def twell_ffn_tile_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: torch.
 _decode_ws = {}
 
 
+@_on_its_stream
 def twell_ffn_decode(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Tensor, Wd_s: torch.Tensor, T: int = 128,
                      packed: Optional[TwELL] = None, y: Optional[torch.Tensor] = None,
                      status: Optional[torch.Tensor] = None, stream=None, ws: Optional[torch.Tensor] = None,
@@ -616,6 +658,7 @@ def ffn_forward(x, Wg_s, Wu_s, Wd_s, T: int = 128, packed: Optional[TwELL] = Non
     return twell_ffn_fused_fwd(x, Wu_s, Wd_s, a, y=y, status=status, stream=stream)
 
 
+@_on_its_stream
 def twell_unpack(a: TwELL, out: Optional[torch.Tensor] = None, status=None, stream=None) -> torch.Tensor:
     out = out if out is not None else torch.empty((a.n_rows, a.n_cols), dtype=a.dtype, device=a.vals.device)
     s = a.c_struct()
@@ -625,6 +668,7 @@ def twell_unpack(a: TwELL, out: Optional[torch.Tensor] = None, status=None, stre
     return out
 
 
+@_on_its_stream
 def twell_column_activity(a: TwELL, counts: Optional[torch.Tensor] = None, status=None, stream=None) -> torch.Tensor:
     """Per-column count of the rows of `a` that keep the column (added to `counts`, zeros if None)."""
     counts = counts if counts is not None else torch.zeros(a.n_cols, dtype=torch.int32, device=a.vals.device)
@@ -636,6 +680,7 @@ def twell_column_activity(a: TwELL, counts: Optional[torch.Tensor] = None, statu
     return counts
 
 
+@_on_its_stream
 def twell_count_nonzeros(a: TwELL, total: Optional[torch.Tensor] = None, status=None, stream=None) -> torch.Tensor:
     """Device int64 [1]: the number of kept entries of `a` (added to `total`, zeros if None)."""
     total = total if total is not None else torch.zeros(1, dtype=torch.int64, device=a.vals.device)
@@ -647,6 +692,7 @@ def twell_count_nonzeros(a: TwELL, total: Optional[torch.Tensor] = None, status=
     return total
 
 
+@_on_its_stream
 def twell_gather_rows(src: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tensor] = None, status=None,
                       stream=None) -> torch.Tensor:
     """out[i] = src[rows[i]] (rows: int32 device tensor)."""
@@ -673,6 +719,7 @@ def compact_weights(Wg_s, Wu_s, Wd_s, live: torch.Tensor, status=None, stream=No
     return tuple(twell_gather_rows(W, live, status=status, stream=stream) for W in (Wg_s, Wu_s, Wd_s))
 
 
+@_on_its_stream
 def twell_pack_from_gate(G: torch.Tensor, T: int = 128, out: Optional[TwELL] = None, status=None,
                          stream=None) -> TwELL:
     N, f = G.shape
@@ -685,6 +732,7 @@ def twell_pack_from_gate(G: torch.Tensor, T: int = 128, out: Optional[TwELL] = N
     return out
 
 
+@_on_its_stream
 def twell_gate_gemm(x: torch.Tensor, Wg_s: torch.Tensor, out: Optional[torch.Tensor] = None, status=None,
                     stream=None) -> torch.Tensor:
     N, d = x.shape
@@ -706,6 +754,7 @@ def twell_device_info():
     return sm.value, ma.value, mi.value
 
 
+@_on_its_stream
 def twell_gemm_test(A: torch.Tensor, B: torch.Tensor, a_mn: bool, b_mn: bool, status=None, stream=None) -> torch.Tensor:
     """C = A_logical @ B_logical (fp32) where A is [M,K] (or [K,M] if a_mn) and B is [N,K] (or [K,N] if b_mn)."""
     M = A.shape[1] if a_mn else A.shape[0]
@@ -777,6 +826,7 @@ def _workspace(op, N, d, f, K, cap, device, ws=None):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+@_on_its_stream
 def twell_hybrid_route_from_gate(G: torch.Tensor, K: int, backup_cap: int, ctx: Optional[Hybrid] = None, ws=None,
                                  stream=None) -> Hybrid:
     N, f = G.shape
@@ -788,6 +838,7 @@ def twell_hybrid_route_from_gate(G: torch.Tensor, K: int, backup_cap: int, ctx: 
     return ctx
 
 
+@_on_its_stream
 def twell_hybrid_fwd(x, Wg_s, Wu_s, Wd_s, K: int, backup_cap: int, l1_coef: float = 2e-5,
                      ctx: Optional[Hybrid] = None, y=None, ws=None, stream=None):
     """Hybrid-format training forward: returns (y, ctx)."""
@@ -803,6 +854,7 @@ def twell_hybrid_fwd(x, Wg_s, Wu_s, Wd_s, K: int, backup_cap: int, l1_coef: floa
     return y, ctx
 
 
+@_on_its_stream
 def twell_hybrid_bwd(x, Wg_s, Wu_s, Wd_s, ctx: Hybrid, dy, l1_coef: float = 2e-5, dx=None, dWg_s=None, dWu_s=None,
                      dWd_s=None, ws=None, stream=None):
     """Hybrid-format training backward: returns (dx, dWg_s, dWu_s, dWd_s), all fp32."""
@@ -875,11 +927,11 @@ def twell_add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, res: Optional[torch.
     without res (it is x then), rstd None unless training is set or a buffer given. h may be res itself
     and y may be x: the call then works in place."""
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     if h is None and res is not None:
-        h = torch.empty_like(res)
+        h = _empty(res.shape, res.dtype, res.device, stream)
     if rstd is None and training:
-        rstd = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+        rstd = _empty(x.shape[:1], torch.float32, x.device, stream)
     code = (_native or _calls()).add_rmsnorm_fwd(x, w, res, eps, h, y, None, None, 0, rstd,
                                                  None if stream is None else stream.cuda_stream)
     if code:
@@ -894,11 +946,13 @@ def twell_add_rmsnorm_fwd_q8(x: torch.Tensor, w: torch.Tensor, res: Optional[tor
     """twell_add_rmsnorm_fwd with y in e4m3, one scale a row (group 0) or per 128 columns (group 128):
     returns (Rows8, h, rstd). y is written in x's type as well when a buffer for it is given."""
     if out is None:
-        out = Rows8.empty(*x.shape, group, x.device)
+        ng = -(-x.shape[-1] // group) if group else 1
+        out = Rows8(_empty(x.shape, torch.float8_e4m3fn, x.device, stream),
+                    _empty((x.shape[0], ng), torch.float32, x.device, stream), group)
     if h is None and res is not None:
-        h = torch.empty_like(res)
+        h = _empty(res.shape, res.dtype, res.device, stream)
     if rstd is None and training:
-        rstd = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+        rstd = _empty(x.shape[:1], torch.float32, x.device, stream)
     code = (_native or _calls()).add_rmsnorm_fwd(x, w, res, eps, h, y, out.values, out.scale, out.group, rstd,
                                                  None if stream is None else stream.cuda_stream)
     if code:
@@ -913,9 +967,9 @@ def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rs
     gradient of x and of res alike, dw fp32. dy, dh (the gradient that reaches h from the residual
     stream, or None) and dx share a type, bf16 or fp32. ws as in twell_paged_attn_decode."""
     if dx is None:
-        dx = torch.empty_like(dy)
+        dx = _empty(dy.shape, dy.dtype, dy.device, stream)
     if dw is None:
-        dw = torch.empty(h.shape[1:], dtype=torch.float32, device=h.device)
+        dw = _empty(h.shape[1:], torch.float32, h.device, stream)
     code = (_native or _calls()).add_rmsnorm_bwd(dy, h, w, rstd, dh, dx, dw, ws,
                                                  None if stream is None else stream.cuda_stream)
     if code:
@@ -988,9 +1042,9 @@ def twell_kv_gather(cache: KVCache, slots: torch.Tensor, k_out: Optional[torch.T
     """Read slots back: (k, v), bf16 [n, n_kv_heads, head_dim]; zeros for slot -1."""
     dev = cache.index
     if k_out is None:
-        k_out = torch.empty((slots.numel(), cache.n_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+        k_out = _empty((slots.numel(), cache.n_kv_heads, cache.head_dim), torch.bfloat16, cache.device, stream)
     if v_out is None:
-        v_out = torch.empty((slots.numel(), cache.n_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+        v_out = _empty((slots.numel(), cache.n_kv_heads, cache.head_dim), torch.bfloat16, cache.device, stream)
     code = (_native or _calls()).kv_gather(cache._at, dev, slots, k_out, v_out, _status(status, dev),
                                            None if stream is None else stream.cuda_stream)
     if code:
@@ -1012,7 +1066,7 @@ def twell_paged_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.T
     theirs, and a call that is captured into a graph has its own in the graph's memory."""
     dev = cache.index
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+        out = _empty(q.shape, torch.bfloat16, cache.device, stream)
     if scale is None:
         scale = cache.head_dim ** -0.5
     code = (_native or _calls()).paged_attn_decode(q, cache._at, dev, page_table, seq_lens, scale, window, out, lse, ws,
@@ -1051,6 +1105,7 @@ class W4Weights:
         return ((c - 8).float() * s)[:self.n, :self.k]
 
 
+@_on_its_stream
 def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=None) -> W4Weights:
     """bf16 weights [n, k] quantised to 4 bits with a scale per `group` columns, laid out for
     twell_w4_matvec (once per weight)."""
@@ -1073,7 +1128,7 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
 def twell_w4_matvec(x: torch.Tensor, W: W4Weights, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T (bf16) for at most DECODE_MAX_N tokens and 4-bit weights."""
     if y is None:
-        y = torch.empty((x.shape[0], W.n), dtype=torch.bfloat16, device=x.device)
+        y = _empty((x.shape[0], W.n), torch.bfloat16, x.device, stream)
     code = (_native or _calls()).w4_matvec(x, W.words, W.scales, W.n, W.k, W.group, y,
                                            None if stream is None else stream.cuda_stream)
     if code:

@@ -146,3 +146,74 @@ def test_the_tensors_device_is_made_current(cuda_dev, monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", Seen)
     binding.twell_w4_quantize(_rand(cuda_dev, 16, 128, seed=1))
     assert seen == [cuda_dev.index]
+
+
+def _owner(t):
+    """The stream whose memory a tensor lies in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not a tensor of the allocator's")
+
+
+def _calls(dev):
+    """Every call that allocates its outputs, by name: what it returns on a stream."""
+    x, w = _rand(dev, 8, 512, seed=1), _rand(dev, 512, seed=2)
+    x32 = x.float()
+    rstd = torch.rsqrt(x32.square().mean(-1) + 1e-6)
+    Wg, Wu, Wd = (_rand(dev, 512, 512, seed=s, scale=0.04) for s in (3, 4, 5))
+    Wd16, Wd16t = binding.twell_convert_f16(Wd), binding.twell_convert_f16_transposed(Wd)
+    xl = _rand(dev, 256, 512, seed=6)
+    a = binding.twell_gate_pack(xl, Wg)
+    G = torch.relu(_rand(dev, 256, 512, seed=7))
+    cache = binding.KVCache.empty(2, 16, 2, 128, BF, dev)
+    slots = torch.arange(4, dtype=torch.int32, device=dev)
+    binding.twell_kv_append(cache, x.view(8, 4, 128)[:4, :2], x.view(8, 4, 128)[:4, 2:], slots)
+    table, lens = torch.zeros((8, 1), dtype=torch.int32, device=dev), torch.full((8,), 4, dtype=torch.int32, device=dev)
+    P = binding.twell_w4_quantize(Wg)
+    y, ctx = binding.twell_hybrid_fwd(xl, Wg, Wu, Wd, 400, 256)
+    return {
+        "add_rmsnorm_fwd": lambda s: binding.twell_add_rmsnorm_fwd(x, w, x32, training=True, stream=s),
+        "add_rmsnorm_fwd_q8": lambda s: (lambda r: (r[0].values, r[0].scale, *r[1:]))(
+            binding.twell_add_rmsnorm_fwd_q8(x, w, x32, group=128, training=True, stream=s)),
+        "add_rmsnorm_bwd": lambda s: binding.twell_add_rmsnorm_bwd(x32, x32, w, rstd, stream=s),
+        "kv_gather": lambda s: binding.twell_kv_gather(cache, slots, stream=s),
+        "paged_attn_decode": lambda s: binding.twell_paged_attn_decode(x.view(8, 4, 128), cache, table, lens, stream=s)[:1],
+        "w4_quantize": lambda s: (lambda r: (r.words, r.scales))(binding.twell_w4_quantize(Wg, stream=s)),
+        "w4_matvec": lambda s: [binding.twell_w4_matvec(x, P, stream=s)],
+        "gate_pack": lambda s: (lambda r: (r.vals, r.idx, r.cnt))(binding.twell_gate_pack(xl, Wg, stream=s)),
+        "ffn_fused_fwd": lambda s: [binding.twell_ffn_fused_fwd(xl, Wu, Wd, a, stream=s)],
+        "ffn_fused_fwd_f16down": lambda s: [binding.twell_ffn_fused_fwd_f16down(xl, Wu, Wd16, a, stream=s)],
+        "ffn_union_fwd": lambda s: [binding.twell_ffn_union_fwd(xl, Wu, Wd16t, a, stream=s)],
+        "ffn_gate_union_fwd": lambda s: [binding.twell_ffn_gate_union_fwd(xl, Wg, Wu, Wd16t, stream=s)[0]],
+        "ffn_tile_union_fwd": lambda s: [binding.twell_ffn_tile_union_fwd(xl, Wu, Wd16, a, stream=s)],
+        "ffn_decode": lambda s: [binding.twell_ffn_decode(x, Wg, Wu, Wd, stream=s)[0]],
+        "convert_f16": lambda s: [binding.twell_convert_f16(Wd, stream=s)],
+        "convert_f16_transposed": lambda s: [binding.twell_convert_f16_transposed(Wd, stream=s)],
+        "unpack": lambda s: [binding.twell_unpack(a, stream=s)],
+        "column_activity": lambda s: [binding.twell_column_activity(a, stream=s)],
+        "count_nonzeros": lambda s: [binding.twell_count_nonzeros(a, stream=s)],
+        "gather_rows": lambda s: [binding.twell_gather_rows(Wg, slots, stream=s)],
+        "pack_from_gate": lambda s: (lambda r: (r.vals, r.cnt))(binding.twell_pack_from_gate(G, stream=s)),
+        "gate_gemm": lambda s: [binding.twell_gate_gemm(xl, Wg, stream=s)],
+        "hybrid_route_from_gate": lambda s: [binding.twell_hybrid_route_from_gate(G, 400, 256, stream=s).cnt],
+        "hybrid_fwd": lambda s: (lambda r: (r[0], r[1].a))(binding.twell_hybrid_fwd(xl, Wg, Wu, Wd, 400, 256, stream=s)),
+        "hybrid_bwd": lambda s: binding.twell_hybrid_bwd(xl, Wg, Wu, Wd, ctx, y, stream=s),
+    }
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(cuda_dev):
+    """Outputs that a call allocates lie in the memory of the stream that it is given; a stream of another library's, a
+    handle alone, will do."""
+    calls = _calls(cuda_dev)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = s.cuda_stream
+
+    for name, call in calls.items():
+        for stream in (s, Handle()):
+            outs = call(stream)
+            s.synchronize()
+            assert all(_owner(t) == s.cuda_stream for t in outs), name
