@@ -174,7 +174,8 @@ int64_t heads_stride(const at::Tensor& t, const char* what, int64_t n, int64_t h
 template <typename F>
 PyObject* call(int dev, F f, std::mutex* turn = nullptr)
 {
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+    c10::cuda::OptionalCUDAGuard guard;
+    if (c10::cuda::current_device() != dev) guard.set_index(static_cast<c10::DeviceIndex>(dev));
     twell_status st;
     Py_BEGIN_ALLOW_THREADS
     {
