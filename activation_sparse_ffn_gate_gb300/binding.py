@@ -30,6 +30,7 @@ TWELL_F32 = 1
 TWELL_E4M3 = 2
 (OP_GATE_PACK, OP_FFN_FUSED_FWD, OP_HYBRID_FWD, OP_HYBRID_BWD, OP_HYBRID_ROUTE, OP_FFN_UNION_FWD, OP_FFN_DECODE,
  OP_FFN_TILE_UNION_FWD, OP_FFN_GATE_UNION_FWD, OP_ADD_RMSNORM_BWD, OP_PAGED_ATTN) = range(11)
+INT32_MAX = 2 ** 31 - 1  # sizes are 32 bits wide in the C ABI
 DECODE_MAX_N = 16  # twell_ffn_decode and twell_w4_matvec take batches of at most this many tokens
 STATUS_NAMES = {0: "TWELL_OK", 1: "TWELL_ERR_INVALID", 2: "TWELL_ERR_UNSUPPORTED", 3: "TWELL_ERR_BACKUP_FULL",
                 4: "TWELL_ERR_TIMEOUT", 5: "TWELL_ERR_DEVICE_CHECK", 6: "TWELL_ERR_CUDA",
@@ -990,6 +991,8 @@ class KVCache:
             raise ValueError("k and v must be device tensors of one shape [n_pages, n_kv_heads, page_size, head_dim] and type")
         if k.stride() != v.stride() or (k.numel() > 0 and k.stride(3) != 1):
             raise ValueError("k and v must have the same strides, head_dim contiguous")
+        if max(k.shape) > INT32_MAX:
+            raise ValueError(f"the cache's sizes must fit 32 bits, not {tuple(k.shape)}")
         q8 = k.dtype == torch.float8_e4m3fn
         if not q8 and k.dtype != torch.bfloat16:
             raise TypeError(f"unsupported cache type {k.dtype}")
@@ -1114,6 +1117,8 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     n, k = W.shape
+    if max(n, k) > INT32_MAX:
+        raise ValueError(f"the weights' sizes must fit 32 bits, not {n} x {k}")
     nt, kt = -(-n // 16), -(-k // 128)
     words = torch.empty((nt, kt, 8, 4, 2, 4), dtype=torch.int32, device=W.device)
     scales = torch.empty((nt, kt, 8, 2, 128 // group), dtype=torch.bfloat16, device=W.device)

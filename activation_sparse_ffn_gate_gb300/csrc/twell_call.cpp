@@ -155,6 +155,17 @@ const twell_kv_cache* cache_at(PyObject* o)
     return static_cast<const twell_kv_cache*>(p);
 }
 
+// A tensor's size, which the C ABI takes in 32 bits.
+int32_t size32(int64_t n, const char* what)
+{
+    if (n > INT32_MAX) {
+        std::ostringstream s;
+        s << what << ": " << n << " does not fit 32 bits";
+        C10_THROW_ERROR(ValueError, s.str());
+    }
+    return static_cast<int32_t>(n);
+}
+
 // [n, heads, head_dim] bf16 with contiguous heads and any token stride, which is returned.
 int64_t heads_stride(const at::Tensor& t, const char* what, int64_t n, int64_t heads, int64_t hd, int dev)
 {
@@ -202,7 +213,7 @@ PyObject* add_rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     const at::Tensor &x = *tensor(a[0], "x"), *res = tensor(a[2], "res", true), *h = tensor(a[4], "h", true);
     const int dev = device_of(x, "x");
     if (x.dim() != 2) C10_THROW_ERROR(ValueError, "x must have two dimensions");
-    const int64_t N = x.size(0), d = x.size(1);
+    const int32_t N = size32(x.size(0), "rows of x"), d = size32(x.size(1), "columns of x");
     const auto t = x.scalar_type();
     const auto rt = res ? res->scalar_type() : t;
     const twell_dtype ct = code(x), cr = res ? code(*res) : ct;
@@ -216,13 +227,13 @@ PyObject* add_rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* py_ = need(tensor(a[5], "y", true), "y", t, {N, d}, dev);
     void* p8 = need(tensor(a[6], "the 8-bit rows", true), "the 8-bit rows", at::kFloat8_e4m3fn, {N, d}, dev);
     void* ps = need(tensor(a[7], "the 8-bit rows' scale", true), "the 8-bit rows' scale", at::kFloat,
-                    {N, group ? (d + group - 1) / group : 1}, dev);
+                    {N, group ? (static_cast<int64_t>(d) + group - 1) / group : 1}, dev);
     void* pd = need(tensor(a[9], "rstd", true), "rstd", at::kFloat, {N}, dev);
     const float eps = number(a[3]);
     const auto s = stream_of(a[10], dev);
     return call(dev, [&] {
-        return twell_add_rmsnorm_fwd(px, pr, pw, static_cast<int32_t>(N), static_cast<int32_t>(d), eps, ct, cr, ph, py_, p8,
-                                     static_cast<float*>(ps), group, static_cast<float*>(pd), s.stream());
+        return twell_add_rmsnorm_fwd(px, pr, pw, N, d, eps, ct, cr, ph, py_, p8, static_cast<float*>(ps), group,
+                                     static_cast<float*>(pd), s.stream());
     });
     END_HANDLE_TH_ERRORS
 }
@@ -235,7 +246,7 @@ PyObject* add_rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     const at::Tensor &dy = *tensor(a[0], "dy"), &h = *tensor(a[1], "h"), &w = *tensor(a[2], "w");
     const int dev = device_of(h, "h");
     if (h.dim() != 2) C10_THROW_ERROR(ValueError, "h must have two dimensions");
-    const int64_t N = h.size(0), d = h.size(1);
+    const int32_t N = size32(h.size(0), "rows of h"), d = size32(h.size(1), "columns of h");
     const twell_dtype ct = code(w), cr = code(h), cg = code(dy);
     const auto g = dy.scalar_type();
     const void* ph = need(&h, "h", h.scalar_type(), {N, d}, dev);
@@ -246,13 +257,12 @@ PyObject* add_rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* pdx = need(tensor(a[5], "dx"), "dx", g, {N, d}, dev);
     void* pdw = need(tensor(a[6], "dw"), "dw", at::kFloat, {d}, dev);
     const auto s = stream_of(a[8], dev);
-    const Workspace ws = workspace(a[7], TWELL_OP_ADD_RMSNORM_BWD, static_cast<int32_t>(N), static_cast<int32_t>(d), dev, s);
+    const Workspace ws = workspace(a[7], TWELL_OP_ADD_RMSNORM_BWD, N, d, dev, s);
     void* pws = ws.t.data_ptr();
     const size_t bytes = static_cast<size_t>(ws.t.numel());
     return call(dev, [&] {
-        return twell_add_rmsnorm_bwd(pdy, ph, pw, static_cast<const float*>(prs), pdh, static_cast<int32_t>(N),
-                                     static_cast<int32_t>(d), ct, cr, cg, pdx, static_cast<float*>(pdw), pws, bytes,
-                                     s.stream());
+        return twell_add_rmsnorm_bwd(pdy, ph, pw, static_cast<const float*>(prs), pdh, N, d, ct, cr, cg, pdx,
+                                     static_cast<float*>(pdw), pws, bytes, s.stream());
     }, ws.turn);
     END_HANDLE_TH_ERRORS
 }
@@ -265,14 +275,14 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     const twell_kv_cache* c = cache_at(a[0]);
     const int dev = integer(a[1]);
     const at::Tensor &k = *tensor(a[2], "k"), &v = *tensor(a[3], "v"), &slots = *tensor(a[4], "slots");
-    const int64_t m = slots.numel();
+    const int32_t m = size32(slots.numel(), "slots");
     const void* psl = need(&slots, "slots", at::kInt, {m}, dev);
     const int64_t ldk = heads_stride(k, "k", m, c->n_kv_heads, c->head_dim, dev);
     const int64_t ldv = heads_stride(v, "v", m, c->n_kv_heads, c->head_dim, dev);
     void* st = need(tensor(a[5], "status"), "status", at::kInt, {1}, dev);
     const auto s = stream_of(a[6], dev);
     return call(dev, [&] {
-        return twell_kv_append(c, k.data_ptr(), v.data_ptr(), ldk, ldv, static_cast<const int32_t*>(psl), static_cast<int32_t>(m),
+        return twell_kv_append(c, k.data_ptr(), v.data_ptr(), ldk, ldv, static_cast<const int32_t*>(psl), m,
                                static_cast<int32_t*>(st), s.stream());
     });
     END_HANDLE_TH_ERRORS
@@ -286,15 +296,14 @@ PyObject* kv_gather(PyObject*, PyObject* const* a, Py_ssize_t n)
     const twell_kv_cache* c = cache_at(a[0]);
     const int dev = integer(a[1]);
     const at::Tensor& slots = *tensor(a[2], "slots");
-    const int64_t m = slots.numel(), H = c->n_kv_heads, hd = c->head_dim;
+    const int32_t m = size32(slots.numel(), "slots"), H = c->n_kv_heads, hd = c->head_dim;
     const void* psl = need(&slots, "slots", at::kInt, {m}, dev);
     void* pk = need(tensor(a[3], "k_out"), "k_out", at::kBFloat16, {m, H, hd}, dev);
     void* pv = need(tensor(a[4], "v_out"), "v_out", at::kBFloat16, {m, H, hd}, dev);
     void* st = need(tensor(a[5], "status"), "status", at::kInt, {1}, dev);
     const auto s = stream_of(a[6], dev);
     return call(dev, [&] {
-        return twell_kv_gather(c, static_cast<const int32_t*>(psl), static_cast<int32_t>(m), pk, pv, static_cast<int32_t*>(st),
-                               s.stream());
+        return twell_kv_gather(c, static_cast<const int32_t*>(psl), m, pk, pv, static_cast<int32_t*>(st), s.stream());
     });
     END_HANDLE_TH_ERRORS
 }
@@ -309,9 +318,10 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     const at::Tensor &q = *tensor(a[0], "q"), &table = *tensor(a[3], "page_table");
     if (q.dim() != 3) C10_THROW_ERROR(ValueError, "q must be bf16 [B, n_q_heads, head_dim]");
     if (table.dim() != 2) C10_THROW_ERROR(ValueError, "page_table must be int32 [B, max_pages]");
-    const int64_t B = q.size(0), H = q.size(1), hd = c->head_dim;
+    const int32_t B = size32(q.size(0), "sequences"), H = size32(q.size(1), "query heads"), hd = c->head_dim;
+    const int32_t max_pages = size32(table.size(1), "page_table's columns");
     const int64_t stride = heads_stride(q, "q", B, H, hd, dev);
-    const void* pt = need(&table, "page_table", at::kInt, {B, table.size(1)}, dev);
+    const void* pt = need(&table, "page_table", at::kInt, {B, max_pages}, dev);
     const void* pl = need(tensor(a[4], "seq_lens"), "seq_lens", at::kInt, {B}, dev);
     void* po = need(tensor(a[7], "out"), "out", at::kBFloat16, {B, H, hd}, dev);
     void* ps = need(tensor(a[8], "lse", true), "lse", at::kFloat, {B, H}, dev);
@@ -319,13 +329,13 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     const float scale = number(a[5]);
     const int32_t window = integer(a[6]);
     const auto s = stream_of(a[11], dev);
-    const Workspace ws = workspace(a[9], TWELL_OP_PAGED_ATTN, static_cast<int32_t>(B), static_cast<int32_t>(hd), dev, s);
+    const Workspace ws = workspace(a[9], TWELL_OP_PAGED_ATTN, B, hd, dev, s);
     void* pws = ws.t.data_ptr();
     const size_t bytes = static_cast<size_t>(ws.t.numel());
     return call(dev, [&] {
         return twell_paged_attn_decode(q.data_ptr(), stride, c, static_cast<const int32_t*>(pt), static_cast<const int32_t*>(pl),
-                                       static_cast<int32_t>(B), static_cast<int32_t>(H), static_cast<int32_t>(table.size(1)), scale,
-                                       window, po, static_cast<float*>(ps), pws, bytes, static_cast<int32_t*>(st), s.stream());
+                                       B, H, max_pages, scale, window, po, static_cast<float*>(ps), pws, bytes,
+                                       static_cast<int32_t*>(st), s.stream());
     }, ws.turn);
     END_HANDLE_TH_ERRORS
 }
@@ -337,19 +347,19 @@ PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t n)
     TWELL_ARGS("w4_matvec", 8);
     const at::Tensor &x = *tensor(a[0], "x"), &words = *tensor(a[1], "words"), &scales = *tensor(a[2], "scales");
     const int dev = device_of(words, "words");
-    const int64_t rows = integer(a[3]), cols = integer(a[4]);
+    const int32_t rows = integer(a[3]), cols = integer(a[4]);
     const int32_t group = integer(a[5]);
     if (x.dim() != 2) C10_THROW_ERROR(ValueError, "x must have two dimensions");
     if (rows <= 0 || cols <= 0 || group <= 0 || group > 128 || 128 % group != 0) C10_THROW_ERROR(ValueError, "the weights' sizes");
-    const int64_t N = x.size(0), nt = (rows + 15) / 16, kt = (cols + 127) / 128;
+    const int32_t N = size32(x.size(0), "rows of x");
+    const int64_t nt = (static_cast<int64_t>(rows) + 15) / 16, kt = (static_cast<int64_t>(cols) + 127) / 128;
     const void* px = need(&x, "x", at::kBFloat16, {N, cols}, dev);
     const void* pw = need(&words, "words", at::kInt, {nt, kt, 8, 4, 2, 4}, dev);
     const void* ps = need(&scales, "scales", at::kBFloat16, {nt, kt, 8, 2, 128 / group}, dev);
     void* po = need(tensor(a[6], "y"), "y", at::kBFloat16, {N, rows}, dev);
     const auto s = stream_of(a[7], dev);
     return call(dev, [&] {
-        return twell_w4_matvec(px, pw, ps, static_cast<int32_t>(N), static_cast<int32_t>(rows), static_cast<int32_t>(cols), group, po,
-                               s.stream());
+        return twell_w4_matvec(px, pw, ps, N, rows, cols, group, po, s.stream());
     });
     END_HANDLE_TH_ERRORS
 }

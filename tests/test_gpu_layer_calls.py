@@ -217,3 +217,34 @@ def test_what_a_call_allocates_belongs_to_its_stream(cuda_dev):
             outs = call(stream)
             s.synchronize()
             assert all(_owner(t) == s.cuda_stream for t in outs), name
+
+
+def _claims(t, shape):
+    """A tensor over t's memory that says it has that shape: what no call may take at its word."""
+    types = {BF: "<i2", F32: "<f4", torch.int32: "<i4"}
+
+    class Claim:
+        __cuda_array_interface__ = {"shape": shape, "typestr": types[t.dtype], "data": (t.data_ptr(), False), "version": 2}
+
+    out = torch.as_tensor(Claim(), device=t.device)
+    return out.view(BF) if t.dtype == BF else out
+
+
+def test_sizes_past_32_bits_are_refused(cuda_dev):
+    """2^32 rows do not become none."""
+    n = 1 << 32
+    f, b, i = (torch.zeros(4096, dtype=t, device=cuda_dev) for t in (F32, BF, torch.int32))
+    x, w, rstd = _claims(f, (n, 8)), f[:8], _claims(f, (n,))
+    cache = binding.KVCache.empty(4, 16, 1, 64, BF, cuda_dev)
+    k, slots = _claims(b, (n, 1, 64)), _claims(i, (n,))
+    P = binding.twell_w4_quantize(_rand(cuda_dev, 16, 32, seed=1), 32)
+    for call in (lambda: binding.twell_add_rmsnorm_fwd(x, w, y=x), lambda: binding.twell_add_rmsnorm_bwd(x, x, w, rstd, dx=x),
+                 lambda: binding.twell_kv_append(cache, k, k, slots),
+                 lambda: binding.twell_kv_gather(cache, slots, k_out=k, v_out=k),
+                 lambda: binding.twell_paged_attn_decode(k, cache, _claims(i, (n, 1)), slots, out=k),
+                 lambda: binding.twell_paged_attn_decode(b[:64].view(1, 1, 64), cache, _claims(i, (1, n)), i[:1]),
+                 lambda: binding.twell_w4_matvec(_claims(b, (n, 32)), P, y=_claims(b, (n, 16))),
+                 lambda: binding.twell_w4_quantize(_claims(b, (n, 32)), 32),
+                 lambda: binding.KVCache(*(_claims(b, (n, 1, 16, 64)),) * 2)):
+        with pytest.raises(ValueError):
+            call()
