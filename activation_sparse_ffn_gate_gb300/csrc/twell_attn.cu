@@ -1177,7 +1177,7 @@ extern "C" twell_status twell_paged_attn_decode(const void* q, int64_t q_stride,
     const int hd = a.c.hd;
     if (hd != 64 && hd != 96 && hd != 128 && hd != 256) return TWELL_ERR_UNSUPPORTED;
     const long long cap = static_cast<long long>(max_pages) << a.c.page_shift;
-    if (B > twell::kAttnMaxSeqs || cap > INT32_MAX - 16 || B * (cap / twell::kTileTokens + 1) > INT32_MAX ||
+    if (B > twell::kAttnMaxSeqs || cap > INT32_MAX - twell::kTileTokens || B * (cap / twell::kTileTokens + 1) > INT32_MAX ||
         n_q_heads > 65535 || static_cast<long long>(B) * n_q_heads > INT32_MAX)
         return TWELL_ERR_UNSUPPORTED;
     if (B == 0) return TWELL_OK;

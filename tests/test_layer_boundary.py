@@ -177,3 +177,12 @@ def test_missing_native_calls_are_not_passed_over(lib, monkeypatch):
     monkeypatch.setattr(importlib, "import_module", missing)
     with pytest.raises(RuntimeError):
         binding.load()
+
+
+def test_attention_refuses_lengths_near_32_bits(lib):
+    """A length is rounded up to a tile of 32 tokens in 32 bits: tables whose length would not survive that are refused."""
+    need = lib.twell_workspace_bytes(binding.OP_PAGED_ATTN, 1, 64, 1, 0, 0, 0)
+    for ps, mp in ((1, (1 << 31) - 20), (1, (1 << 31) - 31), (8, (1 << 28) - 3), (1, (1 << 31) - 17)):
+        c = _cache(page_size=ps, page_stride=2 * 64 * ps, head_stride=64 * ps)
+        st = lib.twell_paged_attn_decode(A, 256, ctypes.byref(c), A, A, 1, 4, mp, 1.0, 0, A, None, A, need, A, None)
+        assert st == UNSUPPORTED, (ps, mp)
