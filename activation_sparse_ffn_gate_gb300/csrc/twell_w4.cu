@@ -19,13 +19,24 @@ namespace twell {
 namespace {
 
 constexpr int kW4MaxN = 16;
-constexpr int kW4Warps = 8;   // most a block has; two blocks share an SM
+constexpr int kW4Warps = 8;   // most a block has
 constexpr int kW4Slot = 1152; // bytes of a weight tile in the ring: its words, then its scales (at most 128 bytes)
 constexpr int kW4Stages = 2;
 constexpr int kW4Direct = 2;  // column tiles a warp may have to take them straight into registers
-// Row tiles a block, by the token columns (in eights): what lets two blocks' rings share an SM.
+// Most row tiles a block, by the token columns (in eights).
 constexpr int w4_tiles(int nb) { return nb == 1 ? 4 : 3; }
 constexpr int w4_stage(int nb, int rt) { return rt * kW4Slot + nb * 2048; }  // 8 tokens by 128 columns of x: 2 KB
+constexpr int w4_smem(int warps, int nb, int rt) { return warps * kW4Stages * w4_stage(nb, rt); }
+// Warps a block: as many as let two blocks share an SM, whose 228 KB of shared memory hold both rings and the 1 KB that goes
+// with each block. That is 8, but 7 with three row tiles and 9 to 16 tokens, where 8 left one block an SM and the
+// grid, of two an SM, took two rounds (14336 x 4096, 16 tokens: 12.3 us with 8, 11.1 with 7; 24577 x 4096 26.5 and 22.9; 9745 x
+// 8192 21.0 and 20.7; two row tiles and 8 warps: 13.3, 23.7, 23.0).
+constexpr int kW4SmBytes = 228 * 1024, kW4BlockBytes = 1024;
+constexpr int w4_warps(int nb, int rt)
+{
+    const int fit = (kW4SmBytes / 2 - kW4BlockBytes) / w4_smem(1, nb, rt);
+    return fit < kW4Warps ? fit : kW4Warps;
+}
 
 template <int GROUP>
 struct W4Scales;  // the scales of one lane's two rows in a tile: [row half][128 / GROUP]
@@ -336,26 +347,23 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* _
     }
 }
 
-constexpr size_t w4_smem(int warps, int nb, int rt)
-{
-    return static_cast<size_t>(warps) * kW4Stages * w4_stage(nb, rt);
-}
-
 template <int GROUP, int NB, int RT>
 twell_status launch_w4(const void* x, const void* words, const void* scales, int N, int n, int k, void* y, int blocks,
                        cudaStream_t s)
 {
     const int nt = (n + 15) / 16, kt = (k + 127) / 128;
     // every warp takes the same number of column tiles where that is possible
-    const int each = (kt + kW4Warps - 1) / kW4Warps, warps = (kt + each - 1) / each;
+    constexpr int kMost = w4_warps(NB, RT);
+    static_assert(2 * (w4_smem(kMost, NB, RT) + kW4BlockBytes) <= kW4SmBytes, "run_w4's grid is two blocks an SM");
+    const int each = (kt + kMost - 1) / kMost, warps = (kt + each - 1) / each;
     if (RT == 1 && each <= kW4Direct)
         return twell_host::launch_dep(w4_small_kernel<GROUP, NB>, dim3(blocks), dim3(32 * warps), 0, s,
                                       static_cast<const __nv_bfloat16*>(x), static_cast<const uint8_t*>(words),
                                       static_cast<const uint8_t*>(scales), N, n, k, kt, static_cast<__nv_bfloat16*>(y));
-    const size_t smem = w4_smem(warps, NB, RT);
+    const int smem = w4_smem(warps, NB, RT);
     auto kern = w4_matvec_kernel<GROUP, NB, RT>;
     static std::atomic<uint64_t> allowed{0};
-    if (twell_host::allow_smem(kern, w4_smem(kW4Warps, NB, RT), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    if (twell_host::allow_smem(kern, w4_smem(kMost, NB, RT), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
     return twell_host::launch_dep(kern, dim3(blocks), dim3(32 * warps), smem, s, static_cast<const __nv_bfloat16*>(x),
                                   static_cast<const uint8_t*>(words), static_cast<const uint8_t*>(scales), N, n, k, nt,
                                   kt, static_cast<__nv_bfloat16*>(y));

@@ -469,7 +469,8 @@ TWELL_API twell_status twell_w4_quantize(const void* W, int32_t n, int32_t k, in
                                void* scales, int32_t* dev_status, void* stream);
 
 /* y [N, n] = x W^T for x [N, k] (bf16), 0 <= N <= 16 (else TWELL_ERR_UNSUPPORTED), W as above: x and the
- * codes enter exactly, sums are fp32 in a fixed order, y is rounded once to bf16. */
+ * codes enter exactly, sums are fp32 in a fixed order, y is rounded once to bf16. A token's y is the same, bit for bit, in
+ * any batch of up to 8 tokens, and in any of 9 to 16. */
 TWELL_API twell_status twell_w4_matvec(const void* x, const void* words, const void* scales, int32_t N, int32_t n,
                              int32_t k, int32_t group, void* y, void* stream);
 

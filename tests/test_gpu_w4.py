@@ -125,3 +125,24 @@ def test_refusals(cuda_dev):
         with pytest.raises(ValueError):
             bad()
     assert binding.twell_w4_matvec(x[:0], P).shape == (0, 16)
+
+
+# Weights with more rows than two blocks an SM hold in two row tiles each, the last tile ragged: blocks of three and four row
+# tiles, in one round and in several, with 7 and 8 warps.
+@pytest.mark.parametrize("N", [1, 8, 9, 16])
+@pytest.mark.parametrize("k,group", [(2560, 128), (4096, 32), (4128, 32), (1024, 64)])
+@pytest.mark.parametrize("n", [9745, 14600, 24577])
+def test_many_rows(cuda_dev, n, k, group, N):
+    g = torch.Generator(cuda_dev).manual_seed(n + k)
+    W = (torch.randn((n, k), generator=g, device=cuda_dev) / k ** 0.5).to(BF)
+    P = binding.twell_w4_quantize(W, group)
+    x = torch.randn((N, k), generator=g, device=cuda_dev).to(BF)
+    y = binding.twell_w4_matvec(x, P)
+    w = P.dequantize().double()
+    ref = x.double() @ w.t()
+    bound = 2.0 ** -8 * ref.abs() + k * 2.0 ** -22 * (x.double().abs() @ w.abs().t())
+    err = (y.double() - ref).abs()
+    assert (err <= bound).all(), (err / bound.clamp_min(1e-300)).max().item()
+    assert torch.equal(y, binding.twell_w4_matvec(x, P))
+    few = 1 if N <= 8 else 9  # the same bits in a smaller batch of the same kind
+    assert torch.equal(y[:few], binding.twell_w4_matvec(x[:few].contiguous(), P))
