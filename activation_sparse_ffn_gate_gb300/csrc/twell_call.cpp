@@ -166,8 +166,12 @@ int32_t size32(int64_t n, const char* what)
     return static_cast<int32_t>(n);
 }
 
-// [n, heads, head_dim] bf16 with contiguous heads and any token stride, which is returned.
-int64_t heads_stride(const at::Tensor& t, const char* what, int64_t n, int64_t heads, int64_t hd, int dev)
+// [n, heads, head_dim] bf16 with contiguous heads and any token stride, and its address.
+struct Heads {
+    const void* at;
+    int64_t stride;
+};
+Heads need_heads(const at::Tensor& t, const char* what, int64_t n, int64_t heads, int64_t hd, int dev)
 {
     if (t.scalar_type() != at::kBFloat16 || t.sizes() != at::IntArrayRef({n, heads, hd}) || !t.is_cuda() || t.get_device() != dev ||
         (t.numel() > 0 && (t.stride(1) != hd || t.stride(2) != 1))) {
@@ -176,12 +180,12 @@ int64_t heads_stride(const at::Tensor& t, const char* what, int64_t n, int64_t h
           << text(t);
         C10_THROW_ERROR(ValueError, s.str());
     }
-    return n > 1 ? t.stride(0) : heads * hd;
+    return {t.data_ptr(), n > 1 ? t.stride(0) : heads * hd};
 }
 
 // The C call on device `dev`, which is made current for it (the entries launch on the current device, and a default
 // stream's handle is the same on all), without the interpreter's lock; under a shared workspace's own, which is taken and given back while the
-// interpreter's is not held, so that neither waits for the other.
+// interpreter's is not held, so that neither waits for the other. `f` throws nothing: no tensor is touched in it.
 template <typename F>
 PyObject* call(int dev, F f, std::mutex* turn = nullptr)
 {
@@ -277,12 +281,12 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     const at::Tensor &k = *tensor(a[2], "k"), &v = *tensor(a[3], "v"), &slots = *tensor(a[4], "slots");
     const int32_t m = size32(slots.numel(), "slots");
     const void* psl = need(&slots, "slots", at::kInt, {m}, dev);
-    const int64_t ldk = heads_stride(k, "k", m, c->n_kv_heads, c->head_dim, dev);
-    const int64_t ldv = heads_stride(v, "v", m, c->n_kv_heads, c->head_dim, dev);
+    const Heads hk = need_heads(k, "k", m, c->n_kv_heads, c->head_dim, dev);
+    const Heads hv = need_heads(v, "v", m, c->n_kv_heads, c->head_dim, dev);
     void* st = need(tensor(a[5], "status"), "status", at::kInt, {1}, dev);
     const auto s = stream_of(a[6], dev);
     return call(dev, [&] {
-        return twell_kv_append(c, k.data_ptr(), v.data_ptr(), ldk, ldv, static_cast<const int32_t*>(psl), m,
+        return twell_kv_append(c, hk.at, hv.at, hk.stride, hv.stride, static_cast<const int32_t*>(psl), m,
                                static_cast<int32_t*>(st), s.stream());
     });
     END_HANDLE_TH_ERRORS
@@ -320,7 +324,7 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (table.dim() != 2) C10_THROW_ERROR(ValueError, "page_table must be int32 [B, max_pages]");
     const int32_t B = size32(q.size(0), "sequences"), H = size32(q.size(1), "query heads"), hd = c->head_dim;
     const int32_t max_pages = size32(table.size(1), "page_table's columns");
-    const int64_t stride = heads_stride(q, "q", B, H, hd, dev);
+    const Heads hq = need_heads(q, "q", B, H, hd, dev);
     const void* pt = need(&table, "page_table", at::kInt, {B, max_pages}, dev);
     const void* pl = need(tensor(a[4], "seq_lens"), "seq_lens", at::kInt, {B}, dev);
     void* po = need(tensor(a[7], "out"), "out", at::kBFloat16, {B, H, hd}, dev);
@@ -333,7 +337,7 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* pws = ws.t.data_ptr();
     const size_t bytes = static_cast<size_t>(ws.t.numel());
     return call(dev, [&] {
-        return twell_paged_attn_decode(q.data_ptr(), stride, c, static_cast<const int32_t*>(pt), static_cast<const int32_t*>(pl),
+        return twell_paged_attn_decode(hq.at, hq.stride, c, static_cast<const int32_t*>(pt), static_cast<const int32_t*>(pl),
                                        B, H, max_pages, scale, window, po, static_cast<float*>(ps), pws, bytes,
                                        static_cast<int32_t*>(st), s.stream());
     }, ws.turn);

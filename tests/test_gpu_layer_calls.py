@@ -248,3 +248,16 @@ def test_sizes_past_32_bits_are_refused(cuda_dev):
                  lambda: binding.KVCache(*(_claims(b, (n, 1, 16, 64)),) * 2)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_tensors_without_memory_raise(cuda_dev):
+    """A tensor that stands for others (inside a vmap) has no address: the error comes before the interpreter's lock is
+    given up."""
+    k, q = _rand(cuda_dev, 2, 3, 2, 64, seed=1), _rand(cuda_dev, 2, 3, 4, 64, seed=2)
+    cache = binding.KVCache.empty(2, 16, 2, 64, BF, cuda_dev)
+    slots, table = (torch.zeros(n, dtype=torch.int32, device=cuda_dev) for n in ((3,), (3, 1)))
+    out = torch.empty((3, 4, 64), dtype=BF, device=cuda_dev)
+    for call, t in ((lambda t: binding.twell_kv_append(cache, t, t, slots), k),
+                    (lambda t: binding.twell_paged_attn_decode(t, cache, table, slots, out=out), q)):
+        with pytest.raises(RuntimeError):
+            torch.vmap(call)(t)
