@@ -978,6 +978,15 @@ def twell_add_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rs
     return dx, dw
 
 
+def _strides(t: torch.Tensor) -> tuple:
+    """A tensor's strides, with that of a contiguous one for an axis of size one, which addresses nothing."""
+    out, dense = [], 1
+    for size, stride in zip(reversed(t.shape), reversed(t.stride())):
+        out.append(dense if size == 1 else stride)
+        dense *= size
+    return tuple(reversed(out))
+
+
 class KVCache:
     """A paged key-value cache in device memory (twell_kv_cache in include/twell.h): k and v
     [n_pages, n_kv_heads, page_size, head_dim] in bf16, or in float8_e4m3fn with fp32 scales
@@ -989,7 +998,8 @@ class KVCache:
                  v_scale: Optional[torch.Tensor] = None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or not k.is_cuda:
             raise ValueError("k and v must be device tensors of one shape [n_pages, n_kv_heads, page_size, head_dim] and type")
-        if k.stride() != v.stride() or (k.numel() > 0 and k.stride(3) != 1):
+        stride = _strides(k)
+        if stride != _strides(v) or (k.numel() > 0 and stride[3] != 1):
             raise ValueError("k and v must have the same strides, head_dim contiguous")
         if max(k.shape) > INT32_MAX:
             raise ValueError(f"the cache's sizes must fit 32 bits, not {tuple(k.shape)}")
@@ -1001,20 +1011,18 @@ class KVCache:
             for s in (k_scale, v_scale):
                 if s is None or s.shape != k.shape[:3] or s.dtype != torch.float32 or s.device != k.device:
                     raise ValueError("an e4m3 cache needs fp32 scales [n_pages, n_kv_heads, page_size]")
-            if k_scale.stride() != v_scale.stride() or (k.shape[2] > 1 and k_scale.stride(2) != 1):
+            sp, sh, st = _strides(k_scale)
+            if (sp, sh, st) != _strides(v_scale) or st != 1:
                 raise ValueError("the scales must have the same strides, a page's tokens adjacent")
-            sp, sh = k_scale.stride(0), k_scale.stride(1)
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
-        # a page of one token has no token stride of its own
-        ts = k.stride(2) if self.page_size > 1 else self.head_dim
         self._c = _KVCache(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
                            TWELL_E4M3 if q8 else TWELL_BF16, k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if q8 else None,
                            v_scale.data_ptr() if q8 else None,
-                           k.stride(0), k.stride(1), ts, sp, sh)
+                           *stride[:3], sp, sh)
         self._at = ctypes.addressof(self._c)
 
     @staticmethod

@@ -174,7 +174,7 @@ struct Heads {
 Heads need_heads(const at::Tensor& t, const char* what, int64_t n, int64_t heads, int64_t hd, int dev)
 {
     if (t.scalar_type() != at::kBFloat16 || t.sizes() != at::IntArrayRef({n, heads, hd}) || !t.is_cuda() || t.get_device() != dev ||
-        (t.numel() > 0 && (t.stride(1) != hd || t.stride(2) != 1))) {
+        (t.numel() > 0 && ((heads > 1 && t.stride(1) != hd) || t.stride(2) != 1))) {
         std::ostringstream s;
         s << what << " must be bf16 [" << n << ", " << heads << ", " << hd << "] on cuda:" << dev << " with contiguous heads, not "
           << text(t);

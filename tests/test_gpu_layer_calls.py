@@ -261,3 +261,35 @@ def test_tensors_without_memory_raise(cuda_dev):
                     (lambda t: binding.twell_paged_attn_decode(t, cache, table, slots, out=out), q)):
         with pytest.raises(RuntimeError):
             torch.vmap(call)(t)
+
+
+def test_axes_of_one_may_have_any_stride(cuda_dev):
+    """The stride of an axis of size one addresses nothing: one key head, one page, one token, one sequence."""
+    def strange(t, axis):  # the same tensor with another stride there
+        stride = list(t.stride())
+        assert t.shape[axis] == 1
+        stride[axis] = 3
+        return t.as_strided(t.shape, stride)
+
+    for dtype in (BF, torch.float8_e4m3fn):
+        k, v = (_rand(cuda_dev, 3, 1, 64, seed=s) for s in (1, 2))
+        slots = torch.arange(3, dtype=torch.int32, device=cuda_dev)
+        table, lens = torch.zeros((3, 1), dtype=torch.int32, device=cuda_dev), slots + 1
+        q = _rand(cuda_dev, 3, 1, 64, seed=3)
+        got = []
+        for odd in (False, True):
+            c = binding.KVCache.empty(1, 16, 1, 64, dtype, cuda_dev)
+            if odd:
+                parts = [strange(t, 0) for t in (c.k, c.v)] + [None if s is None else strange(s, 0) for s in (c.k_scale, c.v_scale)]
+                parts[1] = strange(parts[1], 1)  # of the values alone
+                if dtype != BF:
+                    parts[3] = strange(parts[3], 1)
+                c = binding.KVCache(*parts)
+                binding.twell_kv_append(c, strange(k, 1), v, slots)
+                got.append(binding.twell_paged_attn_decode(strange(q, 1), c, table, lens)[0])
+                one = binding.twell_paged_attn_decode(strange(q[:1], 0), c, table[:1], lens[:1])[0]
+                assert torch.equal(one, got[0][:1])
+            else:
+                binding.twell_kv_append(c, k, v, slots)
+                got.append(binding.twell_paged_attn_decode(q, c, table, lens)[0])
+        assert torch.equal(*got)
