@@ -82,9 +82,9 @@ _lib = None
 _native = None  # the module _twell_call, once load() has imported it
 
 
-def load(path: str = LIB_PATH):
-    """Load the library and the native calls beside it (raises if they have not been built)."""
-    global _lib, _native
+def _library(path: str = LIB_PATH):
+    """The library alone: what the calls that go through ctypes need."""
+    global _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -149,18 +149,27 @@ def load(path: str = LIB_PATH):
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
-            try:
-                _native = importlib.import_module("._twell_call", __package__)
-            except ImportError as e:
-                raise RuntimeError(f"the native calls are missing ({e}): build them with "
-                                   "activation_sparse_ffn_gate_gb300.build.build()") from e
             _lib = lib
     return _lib
 
 
+def load(path: str = LIB_PATH):
+    """Load the library and the native calls beside it (raises if either has not been built, or not for this torch)."""
+    global _native
+    first = _lib is None
+    lib = _library(path)
+    if first or _native is None:
+        try:
+            _native = importlib.import_module("._twell_call", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"the native calls are missing ({e}): build them with "
+                               "activation_sparse_ffn_gate_gb300.build.build()") from e
+    return lib
+
+
 def _status_string(code: int) -> str:
     try:
-        return load().twell_status_string(code).decode()
+        return _library().twell_status_string(code).decode()
     except Exception:  # the library itself failed to load
         return "?"
 
@@ -244,7 +253,7 @@ def fused_workspace(N: int, d: int, f: int, device=None, stream=None) -> torch.T
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     key = (dev.index, _stream(stream).value or 0)
-    n = int(load().twell_workspace_bytes(OP_FFN_FUSED_FWD, N, d, f, 8, 0, 0))
+    n = int(_library().twell_workspace_bytes(OP_FFN_FUSED_FWD, N, d, f, 8, 0, 0))
     buf = _fused_ws.get(key)
     if buf is None or buf.numel() < n:
         buf = torch.empty(n, dtype=torch.uint8, device=dev)
@@ -255,7 +264,7 @@ def fused_workspace(N: int, d: int, f: int, device=None, stream=None) -> torch.T
 def twell_read_status(status: Optional[torch.Tensor] = None, stream=None, reset: bool = True) -> int:
     """Synchronise the stream and return the device status code (optionally clearing it)."""
     status = status if status is not None else status_buffer()
-    code = load().twell_read_status(_ptr(status), _stream(stream))
+    code = _library().twell_read_status(_ptr(status), _stream(stream))
     if reset and code != TWELL_OK:
         status.zero_()
     return code
@@ -264,7 +273,7 @@ def twell_read_status(status: Optional[torch.Tensor] = None, stream=None, reset:
 def twell_wait_probe(arrive: bool, limit_ms: int, status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Run the library's bounded mbarrier wait on its own (test export): with arrive=False it runs
     out after limit_ms and records TWELL_ERR_TIMEOUT in the status word."""
-    _check(load().twell_wait_probe(1 if arrive else 0, int(limit_ms), _ptr(status if status is not None else
+    _check(_library().twell_wait_probe(1 if arrive else 0, int(limit_ms), _ptr(status if status is not None else
                                                                              status_buffer()), _stream(stream)),
            "twell_wait_probe")
 
@@ -323,7 +332,7 @@ def twell_gate_pack(x: torch.Tensor, Wg_s: torch.Tensor, T: int = 128, out: Opti
     f = Wg_s.shape[0]
     out = out if out is not None else TwELL.empty(N, f, T, vals_dtype, x.device)
     s = out.c_struct()
-    _check(load().twell_gate_pack(_ptr(x), _ptr(Wg_s), N, d, f, T, _dtype_code(x.dtype), ctypes.byref(s), None, 0,
+    _check(_library().twell_gate_pack(_ptr(x), _ptr(Wg_s), N, d, f, T, _dtype_code(x.dtype), ctypes.byref(s), None, 0,
                                   _ptr(status if status is not None else status_buffer(x.device)), _stream(stream)),
            "twell_gate_pack")
     return out
@@ -339,7 +348,7 @@ def twell_ffn_fused_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd_s: torch.Tensor,
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     ws = ws if ws is not None else fused_workspace(N, d, f, x.device, stream)
     s = a.c_struct()
-    _check(load().twell_ffn_fused_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), N, d, f,
+    _check(_library().twell_ffn_fused_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), N, d, f,
                                       _dtype_code(x.dtype), _ptr(y), _ptr(ws), ws.numel(),
                                       _ptr(status if status is not None else status_buffer(x.device)),
                                       _stream(stream)),
@@ -354,7 +363,7 @@ def twell_convert_f16(src: torch.Tensor, out: Optional[torch.Tensor] = None, sta
     if src.dtype != torch.bfloat16 or not src.is_contiguous():
         raise ValueError("src must be a contiguous bf16 tensor")
     out = out if out is not None else torch.empty(src.shape, dtype=torch.float16, device=src.device)
-    _check(load().twell_convert_f16(_ptr(src), _ptr(out), src.numel(),
+    _check(_library().twell_convert_f16(_ptr(src), _ptr(out), src.numel(),
                                     _ptr(status if status is not None else status_buffer(src.device)),
                                     _stream(stream)),
            "twell_convert_f16")
@@ -370,7 +379,7 @@ def twell_convert_f16_transposed(src: torch.Tensor, out: Optional[torch.Tensor] 
         raise ValueError("src must be a contiguous 2-D bf16 tensor")
     rows, cols = src.shape
     out = out if out is not None else torch.empty((cols, rows), dtype=torch.float16, device=src.device)
-    _check(load().twell_convert_f16_transposed(_ptr(src), _ptr(out), rows, cols,
+    _check(_library().twell_convert_f16_transposed(_ptr(src), _ptr(out), rows, cols,
                                                _ptr(status if status is not None else status_buffer(src.device)),
                                                _stream(stream)),
            "twell_convert_f16_transposed")
@@ -389,7 +398,7 @@ def twell_ffn_fused_fwd_f16down(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: tor
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     ws = ws if ws is not None else fused_workspace(N, d, f, x.device, stream)
     s = a.c_struct()
-    _check(load().twell_ffn_fused_fwd_f16down(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f,
+    _check(_library().twell_ffn_fused_fwd_f16down(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f,
                                               _ptr(y), _ptr(ws), ws.numel(),
                                               _ptr(status if status is not None else status_buffer(x.device)),
                                               _stream(stream)),
@@ -469,7 +478,7 @@ def twell_ffn_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16t_s: torch.Tens
             ws = torch.empty(n, dtype=torch.uint8, device=x.device)
             _union_ws[key] = ws
     s = a.c_struct()
-    _check(load().twell_ffn_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16t_s), ctypes.byref(s), N, d, f,
+    _check(_library().twell_ffn_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16t_s), ctypes.byref(s), N, d, f,
                                       _dtype_code(x.dtype), _ptr(y), _ptr(ws), ws.numel(),
                                       _ptr(status if status is not None else status_buffer(x.device)),
                                       _stream(stream)),
@@ -499,7 +508,7 @@ def twell_ffn_gate_union_fwd(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Te
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
             _union_ws[key] = ws
     s = out.c_struct()
-    _check(load().twell_ffn_gate_union_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd16t_s), N, d, f, T,
+    _check(_library().twell_ffn_gate_union_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd16t_s), N, d, f, T,
                                            _dtype_code(x.dtype), ctypes.byref(s), _ptr(y), _ptr(ws), ws.numel(),
                                            _ptr(status if status is not None else status_buffer(x.device)),
                                            _stream(stream)),
@@ -529,7 +538,7 @@ def twell_ffn_tile_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: torch.
             ws = torch.empty(n, dtype=torch.uint8, device=x.device)
             _tile_union_ws[key] = ws
     s = a.c_struct()
-    _check(load().twell_ffn_tile_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f, _ptr(y),
+    _check(_library().twell_ffn_tile_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f, _ptr(y),
                                            _ptr(ws), ws.numel(),
                                            _ptr(status if status is not None else status_buffer(x.device)),
                                            _stream(stream)),
@@ -558,7 +567,7 @@ def twell_ffn_decode(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Tensor, Wd
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
             _decode_ws[key] = ws
     s = packed.c_struct()
-    _check(load().twell_ffn_decode(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, T, ctypes.byref(s),
+    _check(_library().twell_ffn_decode(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, T, ctypes.byref(s),
                                    _ptr(y), _ptr(ws), ws.numel(),
                                    _ptr(status if status is not None else status_buffer(x.device)),
                                    _stream(stream)),
@@ -663,7 +672,7 @@ def ffn_forward(x, Wg_s, Wu_s, Wd_s, T: int = 128, packed: Optional[TwELL] = Non
 def twell_unpack(a: TwELL, out: Optional[torch.Tensor] = None, status=None, stream=None) -> torch.Tensor:
     out = out if out is not None else torch.empty((a.n_rows, a.n_cols), dtype=a.dtype, device=a.vals.device)
     s = a.c_struct()
-    _check(load().twell_unpack(ctypes.byref(s), _ptr(out),
+    _check(_library().twell_unpack(ctypes.byref(s), _ptr(out),
                                _ptr(status if status is not None else status_buffer(out.device)), _stream(stream)),
            "twell_unpack")
     return out
@@ -674,7 +683,7 @@ def twell_column_activity(a: TwELL, counts: Optional[torch.Tensor] = None, statu
     """Per-column count of the rows of `a` that keep the column (added to `counts`, zeros if None)."""
     counts = counts if counts is not None else torch.zeros(a.n_cols, dtype=torch.int32, device=a.vals.device)
     s = a.c_struct()
-    _check(load().twell_column_activity(ctypes.byref(s), _ptr(counts),
+    _check(_library().twell_column_activity(ctypes.byref(s), _ptr(counts),
                                         _ptr(status if status is not None else status_buffer(counts.device)),
                                         _stream(stream)),
            "twell_column_activity")
@@ -686,7 +695,7 @@ def twell_count_nonzeros(a: TwELL, total: Optional[torch.Tensor] = None, status=
     """Device int64 [1]: the number of kept entries of `a` (added to `total`, zeros if None)."""
     total = total if total is not None else torch.zeros(1, dtype=torch.int64, device=a.vals.device)
     s = a.c_struct()
-    _check(load().twell_count_nonzeros(ctypes.byref(s), _ptr(total),
+    _check(_library().twell_count_nonzeros(ctypes.byref(s), _ptr(total),
                                        _ptr(status if status is not None else status_buffer(total.device)),
                                        _stream(stream)),
            "twell_count_nonzeros")
@@ -700,7 +709,7 @@ def twell_gather_rows(src: torch.Tensor, rows: torch.Tensor, out: Optional[torch
     n_src, d = src.shape
     n = rows.numel()
     out = out if out is not None else torch.empty((n, d), dtype=src.dtype, device=src.device)
-    _check(load().twell_gather_rows(_ptr(src), n_src, _ptr(rows), n, d, _dtype_code(src.dtype), _ptr(out),
+    _check(_library().twell_gather_rows(_ptr(src), n_src, _ptr(rows), n, d, _dtype_code(src.dtype), _ptr(out),
                                     _ptr(status if status is not None else status_buffer(src.device)),
                                     _stream(stream)),
            "twell_gather_rows")
@@ -726,7 +735,7 @@ def twell_pack_from_gate(G: torch.Tensor, T: int = 128, out: Optional[TwELL] = N
     N, f = G.shape
     out = out if out is not None else TwELL.empty(N, f, T, G.dtype, G.device)
     s = out.c_struct()
-    _check(load().twell_pack_from_gate(_ptr(G), N, f, T, _dtype_code(G.dtype), ctypes.byref(s),
+    _check(_library().twell_pack_from_gate(_ptr(G), N, f, T, _dtype_code(G.dtype), ctypes.byref(s),
                                        _ptr(status if status is not None else status_buffer(G.device)),
                                        _stream(stream)),
            "twell_pack_from_gate")
@@ -739,19 +748,19 @@ def twell_gate_gemm(x: torch.Tensor, Wg_s: torch.Tensor, out: Optional[torch.Ten
     N, d = x.shape
     f = Wg_s.shape[0]
     out = out if out is not None else torch.empty((N, f), dtype=torch.float32, device=x.device)
-    _check(load().twell_gate_gemm(_ptr(x), _ptr(Wg_s), N, d, f, _ptr(out),
+    _check(_library().twell_gate_gemm(_ptr(x), _ptr(Wg_s), N, d, f, _ptr(out),
                                   _ptr(status if status is not None else status_buffer(x.device)), _stream(stream)),
            "twell_gate_gemm")
     return out
 
 
 def twell_workspace_bytes(op: int, N: int, d: int, f: int, tile: int = 128, K: int = 0, backup_cap: int = 0) -> int:
-    return int(load().twell_workspace_bytes(op, N, d, f, tile, K, backup_cap))
+    return int(_library().twell_workspace_bytes(op, N, d, f, tile, K, backup_cap))
 
 
 def twell_device_info():
     sm, ma, mi = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
-    _check(load().twell_device_info(ctypes.byref(sm), ctypes.byref(ma), ctypes.byref(mi)), "twell_device_info")
+    _check(_library().twell_device_info(ctypes.byref(sm), ctypes.byref(ma), ctypes.byref(mi)), "twell_device_info")
     return sm.value, ma.value, mi.value
 
 
@@ -762,7 +771,7 @@ def twell_gemm_test(A: torch.Tensor, B: torch.Tensor, a_mn: bool, b_mn: bool, st
     K = A.shape[0] if a_mn else A.shape[1]
     N = B.shape[1] if b_mn else B.shape[0]
     C = torch.empty((M, N), dtype=torch.float32, device=A.device)
-    _check(load().twell_gemm_test(_ptr(A), _ptr(B), M, N, K, int(a_mn), int(b_mn), _ptr(C),
+    _check(_library().twell_gemm_test(_ptr(A), _ptr(B), M, N, K, int(a_mn), int(b_mn), _ptr(C),
                                   _ptr(status if status is not None else status_buffer(A.device)), _stream(stream)),
            "twell_gemm_test")
     return C
@@ -834,7 +843,7 @@ def twell_hybrid_route_from_gate(G: torch.Tensor, K: int, backup_cap: int, ctx: 
     ctx = ctx if ctx is not None else Hybrid.empty(N, f, K, backup_cap, G.device)
     ws = _workspace(OP_HYBRID_ROUTE, N, 8, f, K, ctx.backup_cap, G.device, ws)
     s = ctx.c_struct()
-    _check(load().twell_hybrid_route_from_gate(_ptr(G), N, f, K, TWELL_BF16, ctypes.byref(s), _ptr(ws), ws.numel(),
+    _check(_library().twell_hybrid_route_from_gate(_ptr(G), N, f, K, TWELL_BF16, ctypes.byref(s), _ptr(ws), ws.numel(),
                                                _stream(stream)), "twell_hybrid_route_from_gate")
     return ctx
 
@@ -849,7 +858,7 @@ def twell_hybrid_fwd(x, Wg_s, Wu_s, Wd_s, K: int, backup_cap: int, l1_coef: floa
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     ws = _workspace(OP_HYBRID_FWD, N, d, f, K, ctx.backup_cap, x.device, ws)
     s = ctx.c_struct()
-    _check(load().twell_hybrid_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, K, ctypes.c_float(l1_coef),
+    _check(_library().twell_hybrid_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, K, ctypes.c_float(l1_coef),
                                    TWELL_BF16, ctypes.byref(s), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
            "twell_hybrid_fwd")
     return y, ctx
@@ -867,7 +876,7 @@ def twell_hybrid_bwd(x, Wg_s, Wu_s, Wd_s, ctx: Hybrid, dy, l1_coef: float = 2e-5
     dWd_s = dWd_s if dWd_s is not None else torch.empty((f, d), dtype=torch.float32, device=x.device)
     ws = _workspace(OP_HYBRID_BWD, N, d, f, ctx.K, ctx.backup_cap, x.device, ws)
     s = ctx.c_struct()
-    _check(load().twell_hybrid_bwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), _ptr(dy), N, d, f,
+    _check(_library().twell_hybrid_bwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), _ptr(dy), N, d, f,
                                    ctypes.c_float(l1_coef), _ptr(dx), _ptr(dWg_s), _ptr(dWu_s), _ptr(dWd_s), _ptr(ws),
                                    ws.numel(), _stream(stream)), "twell_hybrid_bwd")
     return dx, dWg_s, dWu_s, dWd_s
@@ -877,7 +886,7 @@ def twell_hybrid_route_noalloc(a: TwELL, K: int, ctx: Hybrid, stream=None) -> Hy
     """Route a packed TwELL (fp32 values, tile 128) into `ctx` with no workspace and no allocation
     in the library (see twell_hybrid_route_noalloc in include/twell.h for who needs this)."""
     sa, sc = a.c_struct(), ctx.c_struct()
-    _check(load().twell_hybrid_route_noalloc(ctypes.byref(sa), K, ctypes.byref(sc), _stream(stream)),
+    _check(_library().twell_hybrid_route_noalloc(ctypes.byref(sa), K, ctypes.byref(sc), _stream(stream)),
            "twell_hybrid_route_noalloc")
     return ctx
 
@@ -1132,7 +1141,7 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
     scales = torch.empty((nt, kt, 8, 2, 128 // group), dtype=torch.bfloat16, device=W.device)
     out = W4Weights(words, scales, n, k, group)
     with torch.cuda.device(W.device):
-        _check(load().twell_w4_quantize(_ptr(W), n, k, group, _ptr(words), _ptr(scales),
+        _check(_library().twell_w4_quantize(_ptr(W), n, k, group, _ptr(words), _ptr(scales),
                                         _ptr(_status(status, W.get_device())), _stream(stream)),
                "twell_w4_quantize")
     return out

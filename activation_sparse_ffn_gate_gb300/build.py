@@ -18,6 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtwell_gb300.so")
 CALL = os.path.join(PKG, "_twell_call.so")
+STAMP = os.path.join(BUILD, "twell_call.stamp")
 
 SOURCES = ["twell_host.cu", "twell_gate.cu", "twell_ffn.cu", "twell_pack.cu", "twell_hybrid.cu", "twell_light.cu",
            "twell_union.cu", "twell_union_small.cu", "twell_decode.cu", "twell_tile_union.cu", "twell_norm.cu",
@@ -61,8 +62,27 @@ def _call_flags():
     return compile_flags, link_flags
 
 
+def _call_stamp():
+    """What the native calls were built for besides their sources: PyTorch and Python."""
+    import torch
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, python {sys.version}\n"
+
+
+def _stale():
+    """Whether the library, and whether the native calls beside it, have to be built."""
+    def old(f):
+        return not os.path.exists(f) or os.path.getmtime(f) < _deps()
+
+    lib = old(LIB)
+    if lib or old(CALL) or not os.path.exists(STAMP):
+        return lib, True
+    with open(STAMP) as f:
+        return lib, f.read() != _call_stamp()
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, CALL)):
+    lib_stale, call_stale = (True, True) if force else _stale()
+    if not call_stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -86,15 +106,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         call_obj = ex.submit(compile_call)
-        objs = list(ex.map(compile_one, SOURCES))
-        call_obj = call_obj.result()
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    _run(cmd, "link failed")
-    os.replace(tmp, LIB)
+        if lib_stale:
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB + f".{os.getpid()}.tmp"
+            cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+            _run(cmd, "link failed")
+            os.replace(tmp, LIB)
+        call_obj = call_obj.result()  # the library is there by now: its own calls run without these
     tmp = CALL + f".{os.getpid()}.tmp"
     _run(["g++", "-shared", "-o", tmp, call_obj, *link_flags], "link of the native calls failed")
     os.replace(tmp, CALL)
+    with open(STAMP, "w") as f:
+        f.write(_call_stamp())
     return LIB
 
 

@@ -186,3 +186,25 @@ def test_attention_refuses_lengths_near_32_bits(lib):
         c = _cache(page_size=ps, page_stride=2 * 64 * ps, head_stride=64 * ps)
         st = lib.twell_paged_attn_decode(A, 256, ctypes.byref(c), A, A, 1, 4, mp, 1.0, 0, A, None, A, need, A, None)
         assert st == UNSUPPORTED, (ps, mp)
+
+
+def test_the_ffn_runs_without_the_native_calls(lib, monkeypatch):
+    """Its calls go through ctypes and need the library alone."""
+    import importlib
+
+    def missing(name, package=None):
+        raise ImportError(name)
+
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "_native", None)
+    monkeypatch.setattr(importlib, "import_module", missing)
+    assert binding.twell_workspace_bytes(binding.OP_FFN_FUSED_FWD, 64, 512, 1024) > 0
+    with pytest.raises(RuntimeError):
+        binding.load()
+
+
+def test_native_calls_are_built_again_for_another_torch(lib, monkeypatch):
+    import torch
+    assert build._stale() == (False, False)
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    assert build._stale() == (False, True)
