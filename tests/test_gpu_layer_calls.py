@@ -293,3 +293,24 @@ def test_axes_of_one_may_have_any_stride(cuda_dev):
                 binding.twell_kv_append(c, k, v, slots)
                 got.append(binding.twell_paged_attn_decode(q, c, table, lens)[0])
         assert torch.equal(*got)
+
+
+def test_a_threads_first_call(cuda_dev):
+    """A call may be the first thing that a thread does on the device."""
+    x, Wg = _rand(cuda_dev, 200, 512, seed=1), _rand(cuda_dev, 1024, 512, seed=2, scale=0.04)
+    want = binding.twell_gate_pack(x, Wg)
+    torch.cuda.synchronize()
+    got = []
+
+    def run():
+        try:
+            got.append(binding.twell_gate_pack(x, Wg))
+        except Exception as e:  # noqa: BLE001
+            got.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert isinstance(got[0], binding.TwELL), got
+    assert torch.equal(got[0].cnt, want.cnt) and torch.equal(binding.twell_unpack(got[0]), binding.twell_unpack(want))
