@@ -243,22 +243,33 @@ def status_buffer(device=None) -> torch.Tensor:
 
 
 _fused_ws = {}
+# Held over a call's launches where the workspace is the stream's: the kernels of one call read what the ones before left
+# there, and another thread's on the same stream must not come between them.
+_turn = threading.Lock()
 
 
+def _stream_workspace(cache: dict, n: int, device, stream) -> torch.Tensor:
+    """n bytes of the workspace of a device and stream in `cache`, grown on demand: the kernels of one stream run one after
+    the other, so calls can share it. A call that is being captured into a graph gets one of its own from the
+    graph's memory: the graph may replay on any stream, and after the shared one has been outgrown."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+    key = (device.index, _stream(stream).value or 0)
+    ws = cache.get(key)
+    if ws is None or ws.numel() < n:
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+        cache[key] = ws
+    return ws
+
+
+@_on_its_stream
 def fused_workspace(N: int, d: int, f: int, device=None, stream=None) -> torch.Tensor:
     """The workspace twell_ffn_fused_fwd needs for N rows, d_model d, d_ff f (work counter, split
-    plan and the partial rows of split rows), one per device and stream, grown on demand: calls on
-    one stream run one after the other, so they can share it."""
+    plan and the partial rows of split rows), one per device and stream."""
     dev = torch.device(device if device is not None else torch.cuda.current_device())
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    key = (dev.index, _stream(stream).value or 0)
-    n = int(_library().twell_workspace_bytes(OP_FFN_FUSED_FWD, N, d, f, 8, 0, 0))
-    buf = _fused_ws.get(key)
-    if buf is None or buf.numel() < n:
-        buf = torch.empty(n, dtype=torch.uint8, device=dev)
-        _fused_ws[key] = buf
-    return buf
+    return _stream_workspace(_fused_ws, twell_workspace_bytes(OP_FFN_FUSED_FWD, N, d, f, 8), dev, stream)
 
 
 def twell_read_status(status: Optional[torch.Tensor] = None, stream=None, reset: bool = True) -> int:
@@ -333,7 +344,7 @@ def twell_gate_pack(x: torch.Tensor, Wg_s: torch.Tensor, T: int = 128, out: Opti
     out = out if out is not None else TwELL.empty(N, f, T, vals_dtype, x.device)
     s = out.c_struct()
     _check(_library().twell_gate_pack(_ptr(x), _ptr(Wg_s), N, d, f, T, _dtype_code(x.dtype), ctypes.byref(s), None, 0,
-                                  _ptr(status if status is not None else status_buffer(x.device)), _stream(stream)),
+                                      _ptr(status if status is not None else status_buffer(x.device)), _stream(stream)),
            "twell_gate_pack")
     return out
 
@@ -348,11 +359,12 @@ def twell_ffn_fused_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd_s: torch.Tensor,
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     ws = ws if ws is not None else fused_workspace(N, d, f, x.device, stream)
     s = a.c_struct()
-    _check(_library().twell_ffn_fused_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), N, d, f,
-                                      _dtype_code(x.dtype), _ptr(y), _ptr(ws), ws.numel(),
-                                      _ptr(status if status is not None else status_buffer(x.device)),
-                                      _stream(stream)),
-           "twell_ffn_fused_fwd")
+    with _turn:
+        _check(_library().twell_ffn_fused_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), N, d, f,
+                                              _dtype_code(x.dtype), _ptr(y), _ptr(ws), ws.numel(),
+                                              _ptr(status if status is not None else status_buffer(x.device)),
+                                              _stream(stream)),
+               "twell_ffn_fused_fwd")
     return y
 
 
@@ -364,8 +376,8 @@ def twell_convert_f16(src: torch.Tensor, out: Optional[torch.Tensor] = None, sta
         raise ValueError("src must be a contiguous bf16 tensor")
     out = out if out is not None else torch.empty(src.shape, dtype=torch.float16, device=src.device)
     _check(_library().twell_convert_f16(_ptr(src), _ptr(out), src.numel(),
-                                    _ptr(status if status is not None else status_buffer(src.device)),
-                                    _stream(stream)),
+                                        _ptr(status if status is not None else status_buffer(src.device)),
+                                        _stream(stream)),
            "twell_convert_f16")
     return out
 
@@ -380,8 +392,8 @@ def twell_convert_f16_transposed(src: torch.Tensor, out: Optional[torch.Tensor] 
     rows, cols = src.shape
     out = out if out is not None else torch.empty((cols, rows), dtype=torch.float16, device=src.device)
     _check(_library().twell_convert_f16_transposed(_ptr(src), _ptr(out), rows, cols,
-                                               _ptr(status if status is not None else status_buffer(src.device)),
-                                               _stream(stream)),
+                                                   _ptr(status if status is not None else status_buffer(src.device)),
+                                                   _stream(stream)),
            "twell_convert_f16_transposed")
     return out
 
@@ -398,11 +410,12 @@ def twell_ffn_fused_fwd_f16down(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: tor
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     ws = ws if ws is not None else fused_workspace(N, d, f, x.device, stream)
     s = a.c_struct()
-    _check(_library().twell_ffn_fused_fwd_f16down(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f,
-                                              _ptr(y), _ptr(ws), ws.numel(),
-                                              _ptr(status if status is not None else status_buffer(x.device)),
-                                              _stream(stream)),
-           "twell_ffn_fused_fwd_f16down")
+    with _turn:
+        _check(_library().twell_ffn_fused_fwd_f16down(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f,
+                                                      _ptr(y), _ptr(ws), ws.numel(),
+                                                      _ptr(status if status is not None else status_buffer(x.device)),
+                                                      _stream(stream)),
+               "twell_ffn_fused_fwd_f16down")
     return y
 
 
@@ -471,18 +484,14 @@ def twell_ffn_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16t_s: torch.Tens
                          "(twell_convert_f16_transposed of Wd_s)")
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     if ws is None:
-        n = twell_workspace_bytes(OP_FFN_UNION_FWD, N, d, f)
-        key = (x.device.index, _stream(stream).value or 0)
-        ws = _union_ws.get(key)
-        if ws is None or ws.numel() < n:
-            ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-            _union_ws[key] = ws
+        ws = _stream_workspace(_union_ws, twell_workspace_bytes(OP_FFN_UNION_FWD, N, d, f), x.device, stream)
     s = a.c_struct()
-    _check(_library().twell_ffn_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16t_s), ctypes.byref(s), N, d, f,
-                                      _dtype_code(x.dtype), _ptr(y), _ptr(ws), ws.numel(),
-                                      _ptr(status if status is not None else status_buffer(x.device)),
-                                      _stream(stream)),
-           "twell_ffn_union_fwd")
+    with _turn:
+        _check(_library().twell_ffn_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16t_s), ctypes.byref(s), N, d, f,
+                                              _dtype_code(x.dtype), _ptr(y), _ptr(ws), ws.numel(),
+                                              _ptr(status if status is not None else status_buffer(x.device)),
+                                              _stream(stream)),
+               "twell_ffn_union_fwd")
     return y
 
 
@@ -501,18 +510,14 @@ def twell_ffn_gate_union_fwd(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Te
     out = out if out is not None else TwELL.empty(N, f, T, vals_dtype, x.device)
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     if ws is None:
-        n = twell_workspace_bytes(OP_FFN_GATE_UNION_FWD, N, d, f)
-        key = (x.device.index, _stream(stream).value or 0)
-        ws = _union_ws.get(key)
-        if ws is None or ws.numel() < n:
-            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
-            _union_ws[key] = ws
+        ws = _stream_workspace(_union_ws, twell_workspace_bytes(OP_FFN_GATE_UNION_FWD, N, d, f), x.device, stream)
     s = out.c_struct()
-    _check(_library().twell_ffn_gate_union_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd16t_s), N, d, f, T,
-                                           _dtype_code(x.dtype), ctypes.byref(s), _ptr(y), _ptr(ws), ws.numel(),
-                                           _ptr(status if status is not None else status_buffer(x.device)),
-                                           _stream(stream)),
-           "twell_ffn_gate_union_fwd")
+    with _turn:
+        _check(_library().twell_ffn_gate_union_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd16t_s), N, d, f, T,
+                                                   _dtype_code(x.dtype), ctypes.byref(s), _ptr(y), _ptr(ws), ws.numel(),
+                                                   _ptr(status if status is not None else status_buffer(x.device)),
+                                                   _stream(stream)),
+               "twell_ffn_gate_union_fwd")
     return y, out
 
 
@@ -531,18 +536,14 @@ def twell_ffn_tile_union_fwd(x: torch.Tensor, Wu_s: torch.Tensor, Wd16_s: torch.
         raise ValueError("Wd16_s must be fp16 (twell_convert_f16 of Wd_s)")
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     if ws is None:
-        n = twell_workspace_bytes(OP_FFN_TILE_UNION_FWD, N, d, f)
-        key = (x.device.index, _stream(stream).value or 0)
-        ws = _tile_union_ws.get(key)
-        if ws is None or ws.numel() < n:
-            ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-            _tile_union_ws[key] = ws
+        ws = _stream_workspace(_tile_union_ws, twell_workspace_bytes(OP_FFN_TILE_UNION_FWD, N, d, f), x.device, stream)
     s = a.c_struct()
-    _check(_library().twell_ffn_tile_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f, _ptr(y),
-                                           _ptr(ws), ws.numel(),
-                                           _ptr(status if status is not None else status_buffer(x.device)),
-                                           _stream(stream)),
-           "twell_ffn_tile_union_fwd")
+    with _turn:
+        _check(_library().twell_ffn_tile_union_fwd(_ptr(x), _ptr(Wu_s), _ptr(Wd16_s), ctypes.byref(s), N, d, f, _ptr(y),
+                                                   _ptr(ws), ws.numel(),
+                                                   _ptr(status if status is not None else status_buffer(x.device)),
+                                                   _stream(stream)),
+               "twell_ffn_tile_union_fwd")
     return y
 
 
@@ -560,18 +561,14 @@ def twell_ffn_decode(x: torch.Tensor, Wg_s: torch.Tensor, Wu_s: torch.Tensor, Wd
     packed = packed if packed is not None else TwELL.empty(N, f, T, vals_dtype, x.device)
     y = y if y is not None else torch.empty((N, d), dtype=x.dtype, device=x.device)
     if ws is None:
-        n = twell_workspace_bytes(OP_FFN_DECODE, N, d, f, T)
-        key = (x.device.index, _stream(stream).value or 0)
-        ws = _decode_ws.get(key)
-        if ws is None or ws.numel() < n:
-            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
-            _decode_ws[key] = ws
+        ws = _stream_workspace(_decode_ws, twell_workspace_bytes(OP_FFN_DECODE, N, d, f, T), x.device, stream)
     s = packed.c_struct()
-    _check(_library().twell_ffn_decode(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, T, ctypes.byref(s),
-                                   _ptr(y), _ptr(ws), ws.numel(),
-                                   _ptr(status if status is not None else status_buffer(x.device)),
-                                   _stream(stream)),
-           "twell_ffn_decode")
+    with _turn:
+        _check(_library().twell_ffn_decode(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, T, ctypes.byref(s),
+                                           _ptr(y), _ptr(ws), ws.numel(),
+                                           _ptr(status if status is not None else status_buffer(x.device)),
+                                           _stream(stream)),
+               "twell_ffn_decode")
     return y, packed
 
 
@@ -673,7 +670,7 @@ def twell_unpack(a: TwELL, out: Optional[torch.Tensor] = None, status=None, stre
     out = out if out is not None else torch.empty((a.n_rows, a.n_cols), dtype=a.dtype, device=a.vals.device)
     s = a.c_struct()
     _check(_library().twell_unpack(ctypes.byref(s), _ptr(out),
-                               _ptr(status if status is not None else status_buffer(out.device)), _stream(stream)),
+                                   _ptr(status if status is not None else status_buffer(out.device)), _stream(stream)),
            "twell_unpack")
     return out
 
@@ -684,8 +681,8 @@ def twell_column_activity(a: TwELL, counts: Optional[torch.Tensor] = None, statu
     counts = counts if counts is not None else torch.zeros(a.n_cols, dtype=torch.int32, device=a.vals.device)
     s = a.c_struct()
     _check(_library().twell_column_activity(ctypes.byref(s), _ptr(counts),
-                                        _ptr(status if status is not None else status_buffer(counts.device)),
-                                        _stream(stream)),
+                                            _ptr(status if status is not None else status_buffer(counts.device)),
+                                            _stream(stream)),
            "twell_column_activity")
     return counts
 
@@ -696,8 +693,8 @@ def twell_count_nonzeros(a: TwELL, total: Optional[torch.Tensor] = None, status=
     total = total if total is not None else torch.zeros(1, dtype=torch.int64, device=a.vals.device)
     s = a.c_struct()
     _check(_library().twell_count_nonzeros(ctypes.byref(s), _ptr(total),
-                                       _ptr(status if status is not None else status_buffer(total.device)),
-                                       _stream(stream)),
+                                           _ptr(status if status is not None else status_buffer(total.device)),
+                                           _stream(stream)),
            "twell_count_nonzeros")
     return total
 
@@ -710,8 +707,8 @@ def twell_gather_rows(src: torch.Tensor, rows: torch.Tensor, out: Optional[torch
     n = rows.numel()
     out = out if out is not None else torch.empty((n, d), dtype=src.dtype, device=src.device)
     _check(_library().twell_gather_rows(_ptr(src), n_src, _ptr(rows), n, d, _dtype_code(src.dtype), _ptr(out),
-                                    _ptr(status if status is not None else status_buffer(src.device)),
-                                    _stream(stream)),
+                                        _ptr(status if status is not None else status_buffer(src.device)),
+                                        _stream(stream)),
            "twell_gather_rows")
     return out
 
@@ -736,8 +733,8 @@ def twell_pack_from_gate(G: torch.Tensor, T: int = 128, out: Optional[TwELL] = N
     out = out if out is not None else TwELL.empty(N, f, T, G.dtype, G.device)
     s = out.c_struct()
     _check(_library().twell_pack_from_gate(_ptr(G), N, f, T, _dtype_code(G.dtype), ctypes.byref(s),
-                                       _ptr(status if status is not None else status_buffer(G.device)),
-                                       _stream(stream)),
+                                           _ptr(status if status is not None else status_buffer(G.device)),
+                                           _stream(stream)),
            "twell_pack_from_gate")
     return out
 
@@ -749,7 +746,7 @@ def twell_gate_gemm(x: torch.Tensor, Wg_s: torch.Tensor, out: Optional[torch.Ten
     f = Wg_s.shape[0]
     out = out if out is not None else torch.empty((N, f), dtype=torch.float32, device=x.device)
     _check(_library().twell_gate_gemm(_ptr(x), _ptr(Wg_s), N, d, f, _ptr(out),
-                                  _ptr(status if status is not None else status_buffer(x.device)), _stream(stream)),
+                                      _ptr(status if status is not None else status_buffer(x.device)), _stream(stream)),
            "twell_gate_gemm")
     return out
 
@@ -772,7 +769,7 @@ def twell_gemm_test(A: torch.Tensor, B: torch.Tensor, a_mn: bool, b_mn: bool, st
     N = B.shape[1] if b_mn else B.shape[0]
     C = torch.empty((M, N), dtype=torch.float32, device=A.device)
     _check(_library().twell_gemm_test(_ptr(A), _ptr(B), M, N, K, int(a_mn), int(b_mn), _ptr(C),
-                                  _ptr(status if status is not None else status_buffer(A.device)), _stream(stream)),
+                                      _ptr(status if status is not None else status_buffer(A.device)), _stream(stream)),
            "twell_gemm_test")
     return C
 
@@ -844,7 +841,7 @@ def twell_hybrid_route_from_gate(G: torch.Tensor, K: int, backup_cap: int, ctx: 
     ws = _workspace(OP_HYBRID_ROUTE, N, 8, f, K, ctx.backup_cap, G.device, ws)
     s = ctx.c_struct()
     _check(_library().twell_hybrid_route_from_gate(_ptr(G), N, f, K, TWELL_BF16, ctypes.byref(s), _ptr(ws), ws.numel(),
-                                               _stream(stream)), "twell_hybrid_route_from_gate")
+                                                   _stream(stream)), "twell_hybrid_route_from_gate")
     return ctx
 
 
@@ -859,7 +856,7 @@ def twell_hybrid_fwd(x, Wg_s, Wu_s, Wd_s, K: int, backup_cap: int, l1_coef: floa
     ws = _workspace(OP_HYBRID_FWD, N, d, f, K, ctx.backup_cap, x.device, ws)
     s = ctx.c_struct()
     _check(_library().twell_hybrid_fwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), N, d, f, K, ctypes.c_float(l1_coef),
-                                   TWELL_BF16, ctypes.byref(s), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
+                                       TWELL_BF16, ctypes.byref(s), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
            "twell_hybrid_fwd")
     return y, ctx
 
@@ -877,8 +874,8 @@ def twell_hybrid_bwd(x, Wg_s, Wu_s, Wd_s, ctx: Hybrid, dy, l1_coef: float = 2e-5
     ws = _workspace(OP_HYBRID_BWD, N, d, f, ctx.K, ctx.backup_cap, x.device, ws)
     s = ctx.c_struct()
     _check(_library().twell_hybrid_bwd(_ptr(x), _ptr(Wg_s), _ptr(Wu_s), _ptr(Wd_s), ctypes.byref(s), _ptr(dy), N, d, f,
-                                   ctypes.c_float(l1_coef), _ptr(dx), _ptr(dWg_s), _ptr(dWu_s), _ptr(dWd_s), _ptr(ws),
-                                   ws.numel(), _stream(stream)), "twell_hybrid_bwd")
+                                       ctypes.c_float(l1_coef), _ptr(dx), _ptr(dWg_s), _ptr(dWu_s), _ptr(dWd_s), _ptr(ws),
+                                       ws.numel(), _stream(stream)), "twell_hybrid_bwd")
     return dx, dWg_s, dWu_s, dWd_s
 
 
@@ -1142,7 +1139,7 @@ def twell_w4_quantize(W: torch.Tensor, group: int = 128, status=None, stream=Non
     out = W4Weights(words, scales, n, k, group)
     with torch.cuda.device(W.device):
         _check(_library().twell_w4_quantize(_ptr(W), n, k, group, _ptr(words), _ptr(scales),
-                                        _ptr(_status(status, W.get_device())), _stream(stream)),
+                                            _ptr(_status(status, W.get_device())), _stream(stream)),
                "twell_w4_quantize")
     return out
 

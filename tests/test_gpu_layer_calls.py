@@ -314,3 +314,37 @@ def test_a_threads_first_call(cuda_dev):
     torch.cuda.synchronize()
     assert isinstance(got[0], binding.TwELL), got
     assert torch.equal(got[0].cnt, want.cnt) and torch.equal(binding.twell_unpack(got[0]), binding.twell_unpack(want))
+
+
+class Ffn:
+    """The FFN by one of its paths: several kernels over one workspace."""
+
+    def __init__(self, dev, seed, N=8, path="decode", d=512, f=1024):
+        # 3% to 4% of the units are kept: the walk's order is fixed as long as few rows are cut into items
+        self.x = _rand(dev, N, d, seed=seed).abs()
+        self.W = [_rand(dev, f, d, seed=seed + i, scale=d ** -0.5) for i in (1, 2, 3)]
+        self.W[0] -= 0.1 * d ** -0.5
+        self.more = {"union": {"Wd16t_s": binding.twell_convert_f16_transposed(self.W[2])},
+                     "tile_union": {"Wd16_s": binding.twell_convert_f16(self.W[2])}}.get(path, {})
+        self.path = path
+
+    def __call__(self, **kw):
+        return binding.ffn_forward(self.x, *self.W, path=self.path, **self.more, **kw)
+
+
+PATHS = [("decode", 3, 16), ("walk", 200, 3000), ("union", 200, 3000), ("tile_union", 200, 3000)]
+
+
+@pytest.mark.parametrize("path,N", [(p, n) for p, n, _ in PATHS])
+def test_threads_that_share_a_stream_run_the_ffn(cuda_dev, path, N):
+    test_threads_that_share_a_stream(cuda_dev, lambda dev, seed: Ffn(dev, seed, N, path))
+
+
+@pytest.mark.parametrize("path,N,more", PATHS)
+def test_a_graph_of_the_ffn_writes_to_no_ones_memory(cuda_dev, path, N, more):
+    test_a_graph_writes_to_no_ones_memory(cuda_dev, lambda dev: Ffn(dev, 1, N, path), lambda dev: Ffn(dev, 9, more, path))
+
+
+@pytest.mark.parametrize("path,N", [(p, n) for p, n, _ in PATHS])
+def test_a_graph_of_the_ffn_replays_beside_other_calls(cuda_dev, path, N):
+    test_a_graph_replays_beside_other_calls(cuda_dev, lambda dev, seed: Ffn(dev, seed, N, path))
