@@ -59,9 +59,10 @@ class DecoderLayer:
 
 def ffn_sublayer_fwd(delta, h, ffn_norm, Wg_s, Wu_s, Wd_s, K: int, backup_cap: int, l1_coef: float = 2e-5,
                      eps: float = 1e-6, stream=None):
-    """The FFN's half of a layer, training: h' = delta + h, f = FFN(norm(h')). Returns (f, h', saved)."""
+    """The FFN's half of a layer, training: h' = delta + h (h None: delta), f = FFN(norm(h')). Returns (f, h', saved)."""
     with torch.cuda.stream(stream):
         y, h1, rstd = binding.twell_add_rmsnorm_fwd(delta, ffn_norm, h, eps, training=True)
+        h1 = delta if h1 is None else h1
         f, ctx = binding.twell_hybrid_fwd(y, Wg_s, Wu_s, Wd_s, K, backup_cap, l1_coef)
     return f, h1, (y, h1, rstd, ctx, ffn_norm, Wg_s, Wu_s, Wd_s, l1_coef)
 

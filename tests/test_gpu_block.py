@@ -246,3 +246,17 @@ def test_training_step_on_another_stream(cuda_dev):
     want = step(None)
     for a, b in zip(step(torch.cuda.Stream()), want):
         assert torch.equal(a, b)
+
+
+def test_training_step_without_a_stream_before_it(cuda_dev):
+    """h None, as in DecoderLayer.decode: the stream is delta itself, forward and backward."""
+    N, d, f, K = 64, 256, 512, 300
+    delta, w = _rand(cuda_dev, N, d, seed=2), (1 + _rand(cuda_dev, d, seed=3, scale=0.1).float()).to(BF)
+    Wg, Wu = (_rand(cuda_dev, f, d, seed=s, scale=d ** -0.5) for s in (4, 5))
+    Wd = _rand(cuda_dev, f, d, seed=6, scale=f ** -0.5)
+    df, dh = _rand(cuda_dev, N, d, seed=7), _rand(cuda_dev, N, d, seed=8, dtype=torch.float32)
+    out = []
+    for h in (None, torch.zeros_like(delta)):
+        f_out, h1, saved = block.ffn_sublayer_fwd(delta, h, w, Wg, Wu, Wd, K, N)
+        out.append((f_out, h1, *block.ffn_sublayer_bwd(df, dh, saved)))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
