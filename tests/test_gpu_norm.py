@@ -282,3 +282,21 @@ def test_forward_wide_batches(cuda_dev, N, d, types, out):
         assert torch.equal(few.scale, y8.scale[-5:])
     if res is not None:
         _within(h, rh, (_half(rt) + 4 * U) * rh.abs(), "h")
+
+
+@pytest.mark.parametrize("N,d", [(5, 136), (64, 1000), (33, 2560), (3, 8200)])
+def test_backward_from_the_forwards_own_values(cuda_dev, N, d):
+    """As training runs it: h rounded to bf16 and the rstd of the unrounded sum, against the gradients at that sum. Each
+    entry of xh is off by B of itself, so the mean of g xh by B mean|g xh| and their product by twice that and B^2; dw by B
+    sum|dy xh|: beside the bounds above."""
+    x, w = _rand(cuda_dev, (N, d), BF, 51), _rand(cuda_dev, (d,), BF, 52)
+    res, dy, dh = _rand(cuda_dev, (N, d), BF, 53, 4.0), _rand(cuda_dev, (N, d), F32, 54), _rand(cuda_dev, (N, d), F32, 55)
+    _, h, rstd = binding.twell_add_rmsnorm_fwd(x, w, res, EPS, training=True)
+    assert h.dtype == BF
+    dx, dw = binding.twell_add_rmsnorm_bwd(dy, h, w, rstd, dh)
+    rh, rs, _ = _ref_fwd(x, res, w)
+    rdx, big, rdw, sdw = _ref_bwd(dy, rh, w, rs, dh)
+    xh, g = rh * rs[:, None], dy.double() * w.double()
+    more = rs[:, None] * xh.abs() * (g * xh).abs().mean(-1, keepdim=True) * (2 * B + B * B)
+    _within(dx, rdx, 64 * U * big * (1 + B) + more, "dx")
+    _within(dw, rdw, (B + (N + 64) * U * (1 + B)) * sdw, "dw")
