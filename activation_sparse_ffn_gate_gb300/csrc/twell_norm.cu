@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(max_threads(CH)) add_rmsnorm_fwd_kernel(const 
         const Scale8 q = Scale8::of(top[i]);
         *reinterpret_cast<uint2*>(a.y8 + base + i * step) = q.pack8(h[i]);
         if (a.group == a.d ? c == 0 : (c & 15) == 0)
-            a.scale[static_cast<size_t>(row) * static_cast<unsigned>(a.ng) + (c >> 4)] = q.scale;
+            a.scale[static_cast<size_t>(row) * static_cast<unsigned>(a.ng) + (c >> 4)] = q.scale();
     }
 }
 

@@ -300,3 +300,21 @@ def test_backward_from_the_forwards_own_values(cuda_dev, N, d):
     more = rs[:, None] * xh.abs() * (g * xh).abs().mean(-1, keepdim=True) * (2 * B + B * B)
     _within(dx, rdx, 64 * U * big * (1 + B) + more, "dx")
     _within(dw, rdw, (B + (N + 64) * U * (1 + B)) * sdw, "dw")
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("N,d", [(3000, 136), (500, 2560), (7, 8200)])
+def test_scales_are_the_quotient(cuda_dev, N, d, group):
+    """scale = a / 448, the fp32 quotient of the largest magnitude (of y in fp32, as it is written beside the codes), and the
+    codes those of y * (448 / a)."""
+    x, w = _rand(cuda_dev, (N, d), F32, 61), _rand(cuda_dev, (d,), F32, 62)
+    y = torch.empty_like(x)
+    y8, _, _ = binding.twell_add_rmsnorm_fwd_q8(x, w, None, EPS, group, y=y)
+    width = group or d
+    for j, lo in enumerate(range(0, d, width)):
+        part = y[:, lo:lo + width]
+        a = part.abs().amax(1).clamp_min(2.0 ** -60)
+        top = torch.full_like(a, 448.0)  # tensors on both sides: a division by a number may become a product
+        assert torch.equal(y8.scale[:, j], a / top)
+        codes = (part * (top / a)[:, None]).to(torch.float8_e4m3fn)
+        assert torch.equal(y8.values[:, lo:lo + width].contiguous().view(torch.uint8), codes.view(torch.uint8))
