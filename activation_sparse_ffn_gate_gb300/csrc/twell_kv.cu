@@ -178,7 +178,9 @@ twell_status run_gather(const KvView& c, const int32_t* slots, int n, void* k_ou
     const long long units = kv_units(n, c.heads, LPR);
     // several units a block once that still gives every SM several blocks (30011 tokens of 8 heads of 128 from e4m3: 33.6 us
     // with one, 30.0 with four)
-    const int rpt = units >= 4ll * kGatherRows * 152 ? kGatherRows : 1;
+    twell_host::DevInfo dev;
+    if (twell_host::dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
+    const int rpt = units >= 4ll * kGatherRows * dev.sm_count ? kGatherRows : 1;
     auto kern = rpt == 1 ? (c.q8 ? kv_gather_kernel<LPR, true, 1> : kv_gather_kernel<LPR, false, 1>)
                          : (c.q8 ? kv_gather_kernel<LPR, true, kGatherRows> : kv_gather_kernel<LPR, false, kGatherRows>);
     return twell_host::launch_dep(kern, dim3(static_cast<unsigned>((units + rpt - 1) / rpt)), dim3(kKvThreads), 0, s, c, slots, n,
