@@ -9,8 +9,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "twell.h"
 
 namespace twell {
@@ -495,9 +493,6 @@ twell_status down_small(const __half* H, const void* Wd16t_s, int N, int d, int 
 size_t tile_union_ws_bytes(int N, int f);
 // Bytes of the workspace twell_ffn_decode needs (twell_decode.cu).
 size_t decode_ws_bytes(int N, int d, int f, int T);
-// Bytes of the workspaces of twell_add_rmsnorm_bwd (twell_norm.cu) and twell_paged_attn_decode (twell_attn.cu).
-size_t norm_bwd_ws_bytes(int N, int d);
-size_t paged_attn_ws_bytes(int B, int hd);
 
 // 2-D tensor map over a row-major matrix of 16-bit elements: `inner` contiguous elements per row,
 // `outer` rows, row pitch `ld` elements; box [box_inner, box_outer]; 128-byte swizzle; zero fill
@@ -514,22 +509,6 @@ inline twell_status launch_status()
 {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
-}
-
-// Allow `kern` up to `bytes` of dynamic shared memory, the most that any of its launches takes, on the current
-// device. `done` is the caller's, one for each kernel: a bit for each device it has been allowed on, so that a
-// kernel launched often is asked about once.
-template <typename K>
-twell_status allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done)
-{
-    DevInfo d;
-    if (dev_info(&d) != TWELL_OK) return TWELL_ERR_CUDA;
-    const uint64_t bit = 1ull << d.device;
-    if (done.load(std::memory_order_relaxed) & bit) return TWELL_OK;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-        return TWELL_ERR_CUDA;
-    done.fetch_or(bit, std::memory_order_relaxed);
-    return TWELL_OK;
 }
 
 // Launch `kern` as a programmatic dependent of the kernel before it on `s`; the kernel must begin

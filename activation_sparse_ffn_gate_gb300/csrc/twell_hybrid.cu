@@ -16,6 +16,7 @@
 
 #include "twell_gemm.cuh"
 #include "twell_light.cuh"
+#include "twell_ops.cuh"
 
 namespace twell {
 

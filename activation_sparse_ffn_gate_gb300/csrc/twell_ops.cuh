@@ -1,8 +1,10 @@
 // twell_ops.cuh -- helpers shared by the operators around the FFN (norm, key-value cache, attention
-// over it, 4-bit products): 8-element loads and stores, and the 8-bit rounding with its scale.
+// over it, 4-bit products): 8-element loads and stores, the 8-bit rounding with its scale, and on the host their
+// workspaces' sizes and the shared memory of their kernels.
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "twell_common.cuh"
 
@@ -151,3 +153,27 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint16_t v)
 }
 
 }  // namespace twell
+
+namespace twell_host {
+
+// Bytes of the workspaces of twell_add_rmsnorm_bwd (twell_norm.cu) and twell_paged_attn_decode (twell_attn.cu).
+size_t norm_bwd_ws_bytes(int N, int d);
+size_t paged_attn_ws_bytes(int B, int hd);
+
+// Allow `kern` up to `bytes` of dynamic shared memory, the most that any of its launches takes, on the current
+// device. `done` is the caller's, one for each kernel: a bit for each device it has been allowed on, so that a
+// kernel launched often is asked about once.
+template <typename K>
+twell_status allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done)
+{
+    DevInfo d;
+    if (dev_info(&d) != TWELL_OK) return TWELL_ERR_CUDA;
+    const uint64_t bit = 1ull << d.device;
+    if (done.load(std::memory_order_relaxed) & bit) return TWELL_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+        return TWELL_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return TWELL_OK;
+}
+
+}  // namespace twell_host
