@@ -1046,7 +1046,7 @@ class KVCache:
 def twell_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, status=None,
                     stream=None) -> None:
     """Write n tokens' keys and values (bf16 [n, n_kv_heads, head_dim]; any token stride, heads
-    contiguous) to their slots (int32 [n], -1 = skip), quantised where the cache is in e4m3."""
+    contiguous) to their slots (int32 [n], -1 = skip; no slot twice), quantised where the cache is in e4m3."""
     dev = cache.index
     code = (_native or _calls()).kv_append(cache._at, dev, k, v, slots, _status(status, dev),
                                            None if stream is None else stream.cuda_stream)

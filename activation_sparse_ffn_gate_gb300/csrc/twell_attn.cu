@@ -63,8 +63,8 @@ struct AttnCfg {
     static constexpr int kHalf = kTileTokens * kRow;    // bytes of a tile's keys, or its values
     static constexpr int kSlot = kHalf + (Q8 ? 2 * kTileTokens * 4 : 0);  // with keys: both scales behind them
     // Enough warps to keep up with the copies, few enough for three slots each and for ranges that are many tiles
-    // long: 64 sequences of up to 16384 tokens, e4m3, head_dim 128: 97.9 us with 16 warps, 94.7 with 12, 98.6 with 8;
-    // 8 of up to 32768, e4m3, head_dim 64: 35.9, 43.8, 41.0.
+    // long: 64 sequences of up to 16384 tokens, e4m3, head_dim 128: 93.1 us with 12 warps, 93.8 with 8 (16 have too few
+    // registers: 129.7); 8 of up to 32768, e4m3, head_dim 64: 35.1 with 16, 41.4 with 12, 41.5 with 8.
     static constexpr int kWarps = HD == 256 ? (Q8 ? 8 : 4) : NT == 2 || kHalf > 4096 ? 8 : kHalf > 2048 ? 12 : 16;
     static constexpr int kFit = 212000 / (kWarps * kSlot);
     static constexpr int kSlots = kFit >= 7 ? 7 : kFit >= 5 ? 5 : 3;  // odd: keys are requested while keys are used
@@ -1107,7 +1107,7 @@ twell_status run_attn(AttnArgs& a, int sms, cudaStream_t s)
     // One block for each (sequence, key head), without the list and its second kernel, where they fit the SMs and what the
     // page table's width lets be visible is few tiles a warp: at most kPairTiles, and at most kPairIdle times the share
     // of the SMs that would idle (38 sequences of up to 1000 / 2000 tokens, 4 key heads of 128: 12.3 / 18.0 us against 16.3 /
-    // 20.2 through the list; but 8 of up to 2000 with 8 key heads, e4m3: 15.2 against 11.3).
+    // 20.2 through the list; but 8 of up to 2000 with 8 key heads, e4m3: 16.6 against 11.6).
     const long long cap = static_cast<long long>(a.max_pages) << a.c.page_shift;
     const long long seen = a.window > 0 ? std::min<long long>(cap, static_cast<long long>(a.window) + kTileTokens - 1) : cap;
     const long long pairs = static_cast<long long>(a.B) * a.c.heads * a.blocks;
@@ -1116,7 +1116,7 @@ twell_status run_attn(AttnArgs& a, int sms, cudaStream_t s)
     // More of them, of few tiles each: whole ones a warp, equally many, without the scan over the lengths, the search and
     // the second kernel; as long as the fullest warp has at most kWholeExtra tiles more than its share of the table's
     // width (125 sequences of 256 tokens, 8 key heads of 128: 32.1 -> 23.2 us; 40 of up to 53, 4 key heads of 256: 9.9 ->
-    // 7.3; but 40 of up to 256 with 8 key heads, e4m3, 12.3 against 11.8 through the list).
+    // 7.3; but 40 of up to 256 with 8 key heads, e4m3, 12.8 against 12.0 through the list).
     const long long warps = static_cast<long long>(sms) * C::kWarps, tiles = (seen + kTileTokens - 1) / kTileTokens;
     a.whole = !a.pairs && tiles <= kWholeTiles && (pairs + warps - 1) / warps * tiles <= pairs * tiles / warps + kWholeExtra;
     if (a.pairs)

@@ -423,8 +423,8 @@ typedef struct {
 /* Writes n tokens' keys and values into the cache: k, v bf16, token i's heads at k + i * ldk (elements,
  * a multiple of 8, at least n_kv_heads * head_dim: slices of a fused projection are fine), to slot
  * slots[i] (device int32; -1: the token is skipped; any other slot outside the cache is reported as
- * TWELL_ERR_DEVICE_CHECK and skipped; two tokens with the same slot: either may win). An e4m3
- * cache gets, per token and head, a = max(|values|, 2^-60), scale = a / 448 and the codes of
+ * TWELL_ERR_DEVICE_CHECK and skipped; where two tokens of a call have the same slot, what it then holds is not
+ * defined: codes of one and a scale of the other among it). An e4m3 cache gets, per token and head, a = max(|values|, 2^-60), scale = a / 448 and the codes of
  * value * (448 / a), rounded to nearest even. */
 TWELL_API twell_status twell_kv_append(const twell_kv_cache* cache, const void* k, const void* v, int64_t ldk,
                              int64_t ldv, const int32_t* slots, int32_t n, int32_t* dev_status, void* stream);
@@ -445,7 +445,10 @@ TWELL_API twell_status twell_kv_gather(const twell_kv_cache* cache, const int32_
  * multiple of 8); out bf16 [B, n_q_heads, head_dim]. head_dim 64, 96, 128 or 256; B <= 4096, n_q_heads < 65536. A length
  * outside [0, max_pages * page_size] is clamped and reported as TWELL_ERR_DEVICE_CHECK; a page
  * outside the cache is reported and its tokens do not count. Sums, maxima and the join of split sequences
- * are fp32, in an order that depends on the lengths alone: the same out from call to call. ws:
+ * are fp32, in an order that the lengths, the batch, the table's width and the device's number of SMs fix: the same out
+ * from call to call. Softmax weights meet the values in two 16-bit parts: 16 bits with a bf16 cache; with an e4m3 one 22
+ * bits, down to 2^-40 of the sequence's largest weight times value scale, for value scales within 2^90 of one another. A
+ * value that is not finite leaves lse alone. ws:
  * twell_workspace_bytes(TWELL_OP_PAGED_ATTN, B, head_dim, 1, 0, 0, 0) bytes; its contents need not be
  * initialised, and two calls in flight at the same time must not share it. */
 TWELL_API twell_status twell_paged_attn_decode(const void* q, int64_t q_stride, const twell_kv_cache* cache,

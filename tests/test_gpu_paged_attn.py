@@ -8,6 +8,8 @@ additions), plus 2^-20 for its scaling, the maximum's subtraction and the expone
 those under fp16's normal range; the query's rounding to fp16 under a common power of two adds 2^-25 max|q| per
 element: hd 2^-24 max|q| max|k| scale. out is then within twice the weights' error times sum p |v|, sums included, plus
 one bf16 rounding, 2^-8 |out|. lse is within e + 2^-14.
+The bounds of an e4m3 cache are those of one fp16 part under a largest weight of 1; with two parts under 2^15, as they are,
+the tests of many small weights and of values of very different sizes hold it to more.
 """
 import math
 
