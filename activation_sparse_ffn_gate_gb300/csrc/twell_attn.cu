@@ -64,7 +64,7 @@ struct AttnCfg {
     static constexpr int kSlot = kHalf + (Q8 ? 2 * kTileTokens * 4 : 0);  // with keys: both scales behind them
     // Enough warps to keep up with the copies, few enough for three slots each and for ranges that are many tiles
     // long: 64 sequences of up to 16384 tokens, e4m3, head_dim 128: 93.1 us with 12 warps, 93.8 with 8 (16 have too few
-    // registers: 129.7); 8 of up to 32768, e4m3, head_dim 64: 35.1 with 16, 41.4 with 12, 41.5 with 8.
+    // registers: 129.7); 8 of up to 32768, e4m3, head_dim 64: 35.3 with 16, 41.4 with 12, 41.5 with 8.
     static constexpr int kWarps = HD == 256 ? (Q8 ? 8 : 4) : NT == 2 || kHalf > 4096 ? 8 : kHalf > 2048 ? 12 : 16;
     static constexpr int kFit = 212000 / (kWarps * kSlot);
     static constexpr int kSlots = kFit >= 7 ? 7 : kFit >= 5 ? 5 : 3;  // odd: keys are requested while keys are used
@@ -359,7 +359,9 @@ struct AttnState {
                 }
         }
 
-        // scores (base 2) of tokens 16t + g and 16t + g + 8 for heads 2c and 2c + 1
+        // scores (base 2) of tokens 16t + g and 16t + g + 8 for heads 2c and 2c + 1; with an e4m3 cache the values' scales
+        // and their log2, which the maximum alone contains, rounded up, so that no weight is above 2^kUp however large the
+        // scores are
         float vs[kMTiles][2], lv[kMTiles][2];
 #pragma unroll
         for (int t = 0; t < kMTiles; ++t)
@@ -379,8 +381,8 @@ struct AttnState {
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    x[t][n][2 * h] = on ? fmaf(x[t][n][2 * h], qs[n][0] * ks, lv[t][h]) : kNegInf;
-                    x[t][n][2 * h + 1] = on ? fmaf(x[t][n][2 * h + 1], qs[n][1] * ks, lv[t][h]) : kNegInf;
+                    x[t][n][2 * h] = on ? x[t][n][2 * h] * (qs[n][0] * ks) : kNegInf;
+                    x[t][n][2 * h + 1] = on ? x[t][n][2 * h + 1] * (qs[n][1] * ks) : kNegInf;
                 }
             }
 #pragma unroll
@@ -388,8 +390,13 @@ struct AttnState {
             float t0 = kNegInf, t1 = kNegInf;
 #pragma unroll
             for (int t = 0; t < kMTiles; ++t) {
-                t0 = fmaxf(t0, fmaxf(x[t][n][0], x[t][n][2]));
-                t1 = fmaxf(t1, fmaxf(x[t][n][1], x[t][n][3]));
+                if constexpr (Q8) {
+                    t0 = fmaxf(t0, fmaxf(__fadd_ru(x[t][n][0], lv[t][0]), __fadd_ru(x[t][n][2], lv[t][1])));
+                    t1 = fmaxf(t1, fmaxf(__fadd_ru(x[t][n][1], lv[t][0]), __fadd_ru(x[t][n][3], lv[t][1])));
+                } else {
+                    t0 = fmaxf(t0, fmaxf(x[t][n][0], x[t][n][2]));
+                    t1 = fmaxf(t1, fmaxf(x[t][n][1], x[t][n][3]));
+                }
             }
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) {
@@ -412,15 +419,15 @@ struct AttnState {
                     o[i][n][3] *= f1;
                 }
             }
-            const float lift = Q8 ? kLift : 0.0f;
-            const float b0 = (m[n][0] == kNegInf ? 0.0f : m[n][0]) - lift, b1 = (m[n][1] == kNegInf ? 0.0f : m[n][1]) - lift;
+            const float b0 = m[n][0] == kNegInf ? 0.0f : m[n][0], b1 = m[n][1] == kNegInf ? 0.0f : m[n][1];
+            auto weight = [](float x, float b) { return exp2_approx(Q8 ? x - b + kLift : x - b); };
 #pragma unroll
             for (int t = 0; t < kMTiles; ++t) {
                 float p[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    p[2 * h] = exp2_approx(x[t][n][2 * h] - lv[t][h] - b0);
-                    p[2 * h + 1] = exp2_approx(x[t][n][2 * h + 1] - lv[t][h] - b1);
+                    p[2 * h] = weight(x[t][n][2 * h], b0);
+                    p[2 * h + 1] = weight(x[t][n][2 * h + 1], b1);
                 }
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];

@@ -444,3 +444,18 @@ def test_lse_does_not_depend_on_values(cuda_dev, bad, dtype):
     assert torch.isfinite(nl).all() and ((nl - lse).abs() <= 2.0 ** -14).all()
     assert not torch.isfinite(new[:2, 4:, 5]).any()
     assert torch.equal(new[2], out[2]) and torch.equal(new[:, :4], out[:, :4])
+
+
+@pytest.mark.parametrize("size", [2.0 ** e for e in (10, 20, 22, 23, 24, 25, 26, 27)])
+def test_enormous_scores_in_an_8bit_cache(cuda_dev, size):
+    """Scores so large that log2 of a value's scale is lost in them: the token far above the others has all the mass, and
+    the output is its value, whatever its scale (the weight has to stay in fp16's range)."""
+    hd, n = 64, 70
+    g = torch.Generator("cpu").manual_seed(32)
+    for e in (-9, -4, -1, 0, 1, 3, 6, 9):
+        k, v = torch.zeros((n, hd)), torch.randint(-15, 16, (n, hd), generator=g).float() * 2.0 ** e / 8
+        k[:, 0] = 0.5
+        k[41, 0] = 1.0  # the others' scores are half of its
+        out, lse, rl, ro, _, _ = _direct(cuda_dev, k, v, torch.ones(hd), size)
+        assert ((out - ro).abs() <= 2.0 ** -8 * ro.abs() + 1e-30).all(), (size, e)
+        assert abs(lse - rl) <= 2.0 ** -22 * rl + 2.0 ** -14
