@@ -188,9 +188,10 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _under(stream):
-    """The context in which what is allocated belongs to `stream`."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+def under_stream(stream):
+    """The context in which calls are queued on `stream` and what is allocated belongs to it; None: the current one. Anything
+    that has a `cuda_stream` is a stream."""
+    return torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream) else
                              torch.cuda.ExternalStream(stream.cuda_stream))
 
 
@@ -205,7 +206,7 @@ def _on_its_stream(fn):
         stream = args[at] if len(args) > at else kwargs.get("stream")
         if stream is None:
             return fn(*args, **kwargs)
-        with _under(stream):
+        with under_stream(stream):
             return fn(*args, **kwargs)
 
     return call
@@ -215,7 +216,7 @@ def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """The same for one output, for the calls that a decode step makes many of."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with _under(stream):
+    with under_stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 

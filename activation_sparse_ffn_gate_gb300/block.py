@@ -43,7 +43,7 @@ class DecoderLayer:
         `slots`; seq_lens counts them."""
         N = delta.shape[0]
         hq, hk = self.n_heads, self.n_kv_heads
-        with torch.cuda.stream(stream):
+        with binding.under_stream(stream):
             y, h1, _ = binding.twell_add_rmsnorm_fwd(delta, self.attn_norm, h, self.eps)
             h1 = delta if h1 is None else h1
             qkv = binding.twell_w4_matvec(y, self.w_qkv).view(N, hq + 2 * hk, self.head_dim)
@@ -60,7 +60,7 @@ class DecoderLayer:
 def ffn_sublayer_fwd(delta, h, ffn_norm, Wg_s, Wu_s, Wd_s, K: int, backup_cap: int, l1_coef: float = 2e-5,
                      eps: float = 1e-6, stream=None):
     """The FFN's half of a layer, training: h' = delta + h (h None: delta), f = FFN(norm(h')). Returns (f, h', saved)."""
-    with torch.cuda.stream(stream):
+    with binding.under_stream(stream):
         y, h1, rstd = binding.twell_add_rmsnorm_fwd(delta, ffn_norm, h, eps, training=True)
         h1 = delta if h1 is None else h1
         f, ctx = binding.twell_hybrid_fwd(y, Wg_s, Wu_s, Wd_s, K, backup_cap, l1_coef)
@@ -71,7 +71,7 @@ def ffn_sublayer_bwd(df, dh, saved, stream=None):
     """Gradients of <f, df> + <h', dh> + the L1 term: df bf16, dh fp32 (the gradient that reaches h' from the
     layers above). Returns (d, dffn_norm, dWg_s, dWu_s, dWd_s), all fp32; d is the gradient of delta and h alike."""
     y, h1, rstd, ctx, ffn_norm, Wg_s, Wu_s, Wd_s, l1_coef = saved
-    with torch.cuda.stream(stream):
+    with binding.under_stream(stream):
         dy, dWg, dWu, dWd = binding.twell_hybrid_bwd(y, Wg_s, Wu_s, Wd_s, ctx, df, l1_coef)
         d, dn = binding.twell_add_rmsnorm_bwd(dy, h1, ffn_norm, rstd, dh, dx=dy)
     return d, dn, dWg, dWu, dWd

@@ -260,3 +260,23 @@ def test_training_step_without_a_stream_before_it(cuda_dev):
         f_out, h1, saved = block.ffn_sublayer_fwd(delta, h, w, Wg, Wu, Wd, K, N)
         out.append((f_out, h1, *block.ffn_sublayer_bwd(df, dh, saved)))
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_a_step_on_another_librarys_stream(cuda_dev):
+    """A stream that is a handle alone, as every call takes it."""
+    s = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = s.cuda_stream
+
+    layer = _layer(cuda_dev, 256, 512, 4, 2, 64)
+    table = torch.arange(3, dtype=torch.int32, device=cuda_dev)[:, None].contiguous()
+    slots, lens = table[:, 0] * 16, torch.ones(3, dtype=torch.int32, device=cuda_dev)
+    x = _rand(cuda_dev, 3, 256, seed=80)
+    outs = []
+    for stream in (None, Handle()):
+        cache = binding.KVCache.empty(3, 16, 2, 64, BF, cuda_dev)
+        torch.cuda.synchronize()
+        outs.append(layer.decode(x, None, cache, slots, table, lens, stream=stream)[0])
+        torch.cuda.synchronize()
+    assert torch.equal(*outs)
