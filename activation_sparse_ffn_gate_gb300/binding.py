@@ -154,11 +154,12 @@ def _library(path: str = LIB_PATH):
 
 
 def load(path: str = LIB_PATH):
-    """Load the library and the native calls beside it (raises if either has not been built, or not for this torch)."""
+    """Load the library and the native calls beside it (raises if either has not been built, or not for this torch). A library
+    from elsewhere has none beside it: the calls that need them load these, and say if they are missing."""
     global _native
     first = _lib is None
     lib = _library(path)
-    if first or _native is None:
+    if path == LIB_PATH and (first or _native is None):
         try:
             _native = importlib.import_module("._twell_call", __package__)
         except ImportError as e:

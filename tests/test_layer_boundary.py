@@ -208,3 +208,21 @@ def test_native_calls_are_built_again_for_another_torch(lib, monkeypatch):
     assert build._stale() == (False, False)
     monkeypatch.setattr(torch, "__version__", "0.0.0")
     assert build._stale() == (False, True)
+
+
+def test_a_library_from_elsewhere(lib, monkeypatch, tmp_path):
+    """load(path) takes a library that lies elsewhere, without native calls beside it."""
+    import importlib
+    import shutil
+
+    def missing(name, package=None):
+        raise ImportError(name)
+
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "_native", None)
+    monkeypatch.setattr(importlib, "import_module", missing)
+    path = str(shutil.copy(binding.LIB_PATH, tmp_path / "elsewhere.so"))
+    other = binding.load(path)
+    assert other._name == path and other.twell_workspace_bytes(binding.OP_FFN_FUSED_FWD, 64, 512, 1024, 8, 0, 0) > 0
+    with pytest.raises(RuntimeError):
+        binding.twell_add_rmsnorm_fwd(None, None, y=1)
