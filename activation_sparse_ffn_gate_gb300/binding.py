@@ -14,8 +14,10 @@ import dataclasses
 import functools
 import importlib
 import inspect
+import math
 import os
 import threading
+from fractions import Fraction
 from typing import Optional
 
 import torch
@@ -29,12 +31,12 @@ TWELL_BF16 = 0
 TWELL_F32 = 1
 TWELL_E4M3 = 2
 (OP_GATE_PACK, OP_FFN_FUSED_FWD, OP_HYBRID_FWD, OP_HYBRID_BWD, OP_HYBRID_ROUTE, OP_FFN_UNION_FWD, OP_FFN_DECODE,
- OP_FFN_TILE_UNION_FWD, OP_FFN_GATE_UNION_FWD, OP_ADD_RMSNORM_BWD, OP_PAGED_ATTN) = range(11)
+ OP_FFN_TILE_UNION_FWD, OP_FFN_GATE_UNION_FWD, OP_ADD_RMSNORM_BWD, OP_PAGED_ATTN, OP_LORA_ADD) = range(12)
 INT32_MAX = 2 ** 31 - 1  # sizes are 32 bits wide in the C ABI
 DECODE_MAX_N = 16  # twell_ffn_decode and twell_w4_matvec take batches of at most this many tokens
 STATUS_NAMES = {0: "TWELL_OK", 1: "TWELL_ERR_INVALID", 2: "TWELL_ERR_UNSUPPORTED", 3: "TWELL_ERR_BACKUP_FULL",
                 4: "TWELL_ERR_TIMEOUT", 5: "TWELL_ERR_DEVICE_CHECK", 6: "TWELL_ERR_CUDA",
-                7: "TWELL_ERR_WORKSPACE"}
+                7: "TWELL_ERR_WORKSPACE", 8: "TWELL_ERR_POOL_EMPTY"}
 
 # Every function the header declares; the CPU tests check that the library exports each one.
 EXPORTS = ("twell_packed_vals_bytes", "twell_packed_idx_bytes", "twell_packed_cnt_bytes", "twell_workspace_bytes",
@@ -46,7 +48,7 @@ EXPORTS = ("twell_packed_vals_bytes", "twell_packed_idx_bytes", "twell_packed_cn
            "twell_count_nonzeros", "twell_convert_f16_transposed", "twell_ffn_gate_union_fwd",
            "twell_add_rmsnorm_fwd", "twell_add_rmsnorm_bwd", "twell_kv_append", "twell_kv_gather",
            "twell_paged_attn_decode", "twell_w4_words_bytes", "twell_w4_scales_bytes", "twell_w4_quantize",
-           "twell_w4_matvec")
+           "twell_w4_matvec", "twell_rope_fwd", "twell_rope_bwd", "twell_kv_plan", "twell_lora_add")
 
 
 class TwellError(RuntimeError):
@@ -75,6 +77,21 @@ class _KVCache(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
+class _RopeHeads(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n_heads", ctypes.c_int32), ("in_batch", ctypes.c_int64),
+                ("in_token", ctypes.c_int64), ("in_head", ctypes.c_int64), ("out_batch", ctypes.c_int64),
+                ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("ring", ctypes.c_void_p), ("state", ctypes.c_void_p)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("k", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -141,6 +158,13 @@ def _library(path: str = LIB_PATH):
                 "twell_w4_scales_bytes": (sz, [i32, i32, i32]),
                 "twell_w4_quantize": (st, [vp, i32, i32, i32, vp, vp, vp, vp]),
                 "twell_w4_matvec": (st, [vp, vp, vp, i32, i32, i32, i32, vp, vp]),
+                "twell_rope_fwd": (st, [ctypes.POINTER(_RopeHeads), ctypes.POINTER(_RopeHeads), vp, ctypes.c_int64, vp,
+                                        ctypes.c_float, i32, i32, i32, i32, i32, ctypes.c_int, vp]),
+                "twell_rope_bwd": (st, [ctypes.POINTER(_RopeHeads), ctypes.POINTER(_RopeHeads), vp, ctypes.c_int64, vp,
+                                        ctypes.c_float, i32, i32, i32, i32, i32, ctypes.c_int, vp]),
+                "twell_kv_plan": (st, [ctypes.POINTER(_PagePool), vp, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+                "twell_lora_add": (st, [vp, ctypes.c_int64, vp, ctypes.c_int64, ctypes.POINTER(_Adapters), vp, i32, vp,
+                                        ctypes.c_int64, vp, sz, vp, vp]),
                 "twell_read_status": (st, [vp, vp]),
                 "twell_status_string": (ctypes.c_char_p, [ctypes.c_int]),
                 "twell_device_info": (st, [ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]),
@@ -905,6 +929,8 @@ def _calls():
 
 def _status(status, index: int) -> torch.Tensor:
     if status is None:
+        if index < 0:
+            raise ValueError("the call's tensors must be on a GPU")
         status = _status_bufs.get(index)
         if status is None:
             status = status_buffer(torch.device("cuda", index))
@@ -1155,3 +1181,172 @@ def twell_w4_matvec(x: torch.Tensor, W: W4Weights, y: Optional[torch.Tensor] = N
     if code:
         _check(code, "twell_w4_matvec")
     return y
+
+
+# What a served step needs beside the layer's own calls: the plan of its tokens, their rotation, and adapters.
+
+_PI = Fraction("3.14159265358979323846264338327950288419716939937510")  # to 2^-166
+
+
+def scaled_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: int = 0,
+                       low: Optional[float] = None, high: Optional[float] = None):
+    """(frequencies, factor) for Rotary: radians a position of each of rot_dim / 2 pairs, f_i = base^(-2i / rot_dim), changed
+    for contexts `factor` times as long as the `original` length a model was trained at:
+    "none"; "linear": f / factor; "base": base times factor^(rot_dim / (rot_dim - 2)), so that the first pair stays and the
+    last becomes f / factor; "bands": by the number of turns n_i = original f_i / 2 pi, f where n >= high (4), f / factor
+    where n <= low (1), between them (1 - s) f / factor + s f with s = (n - low) / (high - low); "ramp": by the index of the
+    pair, i(n) = rot_dim ln(original / (2 pi n)) / (2 ln base), f up to floor(i(high)) (high 32 turns), f / factor from
+    ceil(i(low)) (1 turn) on, a straight line between them, and turned values times 0.1 ln(factor) + 1."""
+    if rot_dim < 2 or rot_dim % 2 or not base > 1 or not factor >= 1:
+        raise ValueError("rot_dim must be even, base above 1 and factor at least 1")
+    if scaling in ("bands", "ramp") and original < 1:
+        raise ValueError(f"scaling {scaling!r} needs the original length")
+    if scaling == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling in ("none", "base"):
+        return f, 1.0
+    if scaling == "linear":
+        return [v / factor for v in f], 1.0
+    low, high = 1.0 if low is None else low, (4.0 if scaling == "bands" else 32.0) if high is None else high
+    if not 0 < low < high:
+        raise ValueError("low must be above 0 and below high")
+    if scaling == "bands":
+        share = [min(max((original * v / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for v in f]
+        return [v * s + v / factor * (1 - s) for v, s in zip(f, share)], 1.0
+    if scaling == "ramp":
+        at = [rot_dim * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (high, low)]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim - 1)
+        ramp = [min(max((i - first) / max(last - first, 0.001), 0.0), 1.0) for i in range(rot_dim // 2)]
+        return [v * (1 - r) + v / factor * r for v, r in zip(f, ramp)], 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"unknown scaling {scaling!r}")
+
+
+class Rotary:
+    """The rotation of heads of head_dim by positions: `frequencies` (radians a position, one a pair; any sequence or tensor,
+    taken in 64 bits: scaled_frequencies gives those of long contexts) for the first 2 len(frequencies) values of a head, in
+    pairs (i, i + half) or, interleaved, (2i, 2i + 1); turned values are multiplied by `factor`. Laid out once."""
+
+    def __init__(self, frequencies, head_dim: int, interleaved: bool = False, factor: float = 1.0, device=None):
+        f = [float(v) for v in (frequencies.tolist() if hasattr(frequencies, "tolist") else frequencies)]
+        if not f or 2 * len(f) > head_dim or not all(math.isfinite(v) for v in f):
+            raise ValueError("frequencies must be finite, one to head_dim / 2 of them")
+        if not (math.isfinite(factor) and factor > 0):
+            raise ValueError("factor must be positive")
+        # 2^64 times the turns a position, modulo 2^64, formed without rounding but for the last bit
+        turns = [round(Fraction(v) / (2 * _PI) * 2 ** 64) % 2 ** 64 for v in f]
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64).to(device)
+        self.head_dim, self.rot_dim, self.interleaved, self.factor = head_dim, 2 * len(f), bool(interleaved), float(factor)
+
+
+def _rope(backward, name, q, k, positions, rotary, q_out, k_out, stream):
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    if k_out is None and k is not None:
+        k_out = _empty(k.shape, k.dtype, k.device, stream)
+    code = (_native or _calls()).rope(q, k, positions, rotary.turns, rotary.factor, rotary.interleaved, rotary.head_dim, q_out,
+                                      k_out, backward, None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, name)
+    return q_out, k_out
+
+
+def twell_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rotary: Rotary,
+                   q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Queries and keys (or queries alone) turned by their tokens' positions: returns (q_out, k_out).
+
+    q and k [tokens, heads, head_dim] with int32 positions [tokens], or [sequences, tokens, heads, head_dim] with positions
+    [sequences, tokens] or [tokens]; bf16 or fp32, any strides with head_dim contiguous (slices of a fused projection,
+    head-first tensors transposed). q_out may be q and k_out k: the call then works in place."""
+    return _rope(False, "twell_rope_fwd", q, k, positions, rotary, q_out, k_out, stream)
+
+
+def twell_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor, rotary: Rotary,
+                   q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of twell_rope_fwd's outputs to those of its inputs: the same call with the opposite turn."""
+    return _rope(True, "twell_rope_bwd", dq, dk, positions, rotary, q_out, k_out, stream)
+
+
+@dataclasses.dataclass
+class PagePool:
+    """The pages of a cache that no sequence has (twell_page_pool in include/twell.h), for twell_kv_plan."""
+
+    ring: torch.Tensor  # int32 [n_pages]
+    state: torch.Tensor  # int32 [4]: first free cell, number of free pages, 0, 0
+    page_size: int
+
+    @staticmethod
+    def full(n_pages: int, page_size: int, device=None):
+        """All pages free."""
+        if not 0 <= n_pages <= INT32_MAX:
+            raise ValueError(f"the number of pages must fit 32 bits, not {n_pages}")
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        return PagePool(torch.arange(n_pages, dtype=torch.int32, device=device),
+                        torch.tensor([0, n_pages, 0, 0], dtype=torch.int32).to(device), page_size)
+
+
+@dataclasses.dataclass
+class StepPlan:
+    """A step's tokens, one request after the other; int32, of a padding token -1, 0 and -1."""
+
+    slots: torch.Tensor  # [n_tokens], for twell_kv_append
+    positions: torch.Tensor  # [n_tokens], for twell_rope_fwd
+    owner: torch.Tensor  # [n_tokens] the request's label, or its number
+    starts: torch.Tensor  # [B + 1] where each request's tokens begin
+
+
+def twell_kv_plan(pool: PagePool, page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, n_tokens: int,
+                  labels: Optional[torch.Tensor] = None, plan: Optional[StepPlan] = None,
+                  seq_lens_out: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None, status=None,
+                  stream=None) -> StepPlan:
+    """The plan of a step, made on the device: new_lens [B] new tokens of each request (0: none, -1: it has ended) behind the
+    seq_lens [B] that it has, in n_tokens rows (those past the last request's are padding).
+
+    New tokens get pages from the pool, which are written into page_table [B, max_pages]; the pages of requests that have
+    ended go back to it. seq_lens becomes the lengths after the step (0 for those that have ended) and the pool's state what
+    is left, both in place unless seq_lens_out and state_out are given. labels [B], an adapter's number say, become
+    the owner of their requests' tokens. All int32. A request whose tokens find no pages, row or place gets none: its tokens'
+    slots are -1, its length stays, and TWELL_ERR_POOL_EMPTY or TWELL_ERR_DEVICE_CHECK is recorded in the status."""
+    if plan is None:
+        dev = pool.ring.device
+        if not 0 <= n_tokens <= INT32_MAX:
+            raise ValueError(f"n_tokens must fit 32 bits, not {n_tokens}")
+        plan = StepPlan(*(_empty((n_tokens,), torch.int32, dev, stream) for _ in range(3)),
+                        _empty((page_table.shape[0] + 1,), torch.int32, dev, stream))
+    elif plan.slots.numel() != n_tokens:
+        raise ValueError(f"the plan has {plan.slots.numel()} rows, not {n_tokens}")
+    code = (_native or _calls()).kv_plan(pool.ring, pool.state, pool.page_size, page_table, seq_lens, new_lens, labels, plan.slots,
+                                         plan.positions, plan.owner, plan.starts,
+                                         seq_lens if seq_lens_out is None else seq_lens_out,
+                                         pool.state if state_out is None else state_out,
+                                         _status(status, pool.ring.get_device()), None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "twell_kv_plan")
+    return plan
+
+
+@dataclasses.dataclass
+class Adapters:
+    """Low-rank adapters of one projection (twell_adapters in include/twell.h): adapter i adds scale[i] b[i] a[i] to its
+    weights, of which the first ranks[i] rows of a[i] and columns of b[i] count (ranks None: all)."""
+
+    a: torch.Tensor  # bf16 [n_adapters, rank, k]
+    b: torch.Tensor  # bf16 [n_adapters, n, rank]
+    scale: torch.Tensor  # fp32 [n_adapters]
+    ranks: Optional[torch.Tensor] = None  # int32 [n_adapters]
+
+
+def twell_lora_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, ids: torch.Tensor,
+                   out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, status=None,
+                   stream=None) -> torch.Tensor:
+    """Each token's own adapter added to a shared projection's output: y [N, n] += scale b a x [N, k] of adapter ids [N] (int32,
+    any order; -1: none), in place, or into `out` when it is given. bf16, rows of any stride (slices of a fused
+    projection); up to 2^20 tokens. ws as in twell_paged_attn_decode."""
+    if out is None:
+        out = y
+    code = (_native or _calls()).lora_add(y, x, adapters.a, adapters.b, adapters.scale, adapters.ranks, ids, out, ws,
+                                          _status(status, x.get_device()), None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "twell_lora_add")
+    return out

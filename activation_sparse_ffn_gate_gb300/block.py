@@ -3,8 +3,9 @@ DECODE_MAX_N sequences, and the training step of the FFN's half of the layer.
 
 The residual stream travels as (delta, h): what the last sublayer added and the stream before it. The
 addition itself is the first half of twell_add_rmsnorm_fwd, so a sublayer reads and writes the stream once.
-Positions are the caller's business: `rotate`, if given, is called with the queries and keys of a step (views of
-the fused projection's output, to be changed in place) before the keys are stored.
+Positions turn the queries and keys of a step before the keys are stored: by `rotary`, from the positions that the step is
+given (twell_kv_plan makes them, with the slots), or by `rotate`, the caller's own, which is called with views of the fused
+projection's output, to be changed in place. Adapters of the projections are added for the tokens that have one.
 With a `stream`, a step runs under it: its kernels, what `rotate` queues, and the memory of what it returns.
 """
 from __future__ import annotations
@@ -35,24 +36,39 @@ class DecoderLayer:
     eps: float = 1e-6
     T: int = 128
     rotate: Optional[Callable[[torch.Tensor, torch.Tensor], None]] = None
+    rotary: Optional[binding.Rotary] = None
+    adapters_qkv: Optional[binding.Adapters] = None  # of w_qkv
+    adapters_out: Optional[binding.Adapters] = None  # of w_out
 
     def decode(self, delta: torch.Tensor, h: Optional[torch.Tensor], cache: binding.KVCache, slots: torch.Tensor,
-               page_table: torch.Tensor, seq_lens: torch.Tensor, window: int = 0, stream=None):
+               page_table: torch.Tensor, seq_lens: torch.Tensor, window: int = 0, stream=None,
+               positions: Optional[torch.Tensor] = None, adapter_ids: Optional[torch.Tensor] = None):
         """One new token per sequence: delta [N, d] bf16 and h [N, d] (bf16 or fp32; None for the first layer, whose
         stream is delta) in, the same pair for the next layer out. The tokens' keys and values go to
-        `slots`; seq_lens counts them."""
+        `slots`; seq_lens counts them. positions int32 [N] for `rotary`; adapter_ids int32 [N] (-1: none; without them no
+        adapter is added): what twell_kv_plan makes of the requests, where each has one new token."""
         N = delta.shape[0]
         hq, hk = self.n_heads, self.n_kv_heads
+        if self.rotary is not None and positions is None:
+            raise ValueError("a layer with `rotary` needs the tokens' positions")
         with binding.under_stream(stream):
             y, h1, _ = binding.twell_add_rmsnorm_fwd(delta, self.attn_norm, h, self.eps)
             h1 = delta if h1 is None else h1
-            qkv = binding.twell_w4_matvec(y, self.w_qkv).view(N, hq + 2 * hk, self.head_dim)
+            qkv = binding.twell_w4_matvec(y, self.w_qkv)
+            if self.adapters_qkv is not None and adapter_ids is not None:
+                binding.twell_lora_add(qkv, y, self.adapters_qkv, adapter_ids)
+            qkv = qkv.view(N, hq + 2 * hk, self.head_dim)
             q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+            if self.rotary is not None:
+                binding.twell_rope_fwd(q, k, positions, self.rotary, q, k)
             if self.rotate is not None:
                 self.rotate(q, k)
             binding.twell_kv_append(cache, k, v, slots)
             a, _ = binding.twell_paged_attn_decode(q, cache, page_table, seq_lens, window=window)
-            o = binding.twell_w4_matvec(a.view(N, hq * self.head_dim), self.w_out)
+            a = a.view(N, hq * self.head_dim)
+            o = binding.twell_w4_matvec(a, self.w_out)
+            if self.adapters_out is not None and adapter_ids is not None:
+                binding.twell_lora_add(o, a, self.adapters_out, adapter_ids)
             y, h2, _ = binding.twell_add_rmsnorm_fwd(o, self.ffn_norm, h1, self.eps)
             return binding.ffn_forward(y, self.Wg_s, self.Wu_s, self.Wd_s, T=self.T, path="auto"), h2
 

@@ -27,6 +27,8 @@ namespace {
 
 using Shape = std::initializer_list<int64_t>;
 
+constexpr int32_t kLoraMaxTokens = 1 << 20;  // of one twell_lora_add
+
 std::string text(const at::Tensor& t)
 {
     std::ostringstream s;
@@ -102,10 +104,12 @@ struct Workspace {
     std::mutex* turn;
 };
 
-// Bytes that any call of an operator needs. Its buffers have this size from the start (10 MB and 26 MB) and are never
+// Bytes that any call of an operator needs. Its buffers have this size from the start (10 MB, 26 MB and 4 MB) and are never
 // replaced.
 int64_t most_bytes(twell_op op)
 {
+    if (op == TWELL_OP_LORA_ADD)
+        return std::max<int64_t>(static_cast<int64_t>(twell_workspace_bytes(op, kLoraMaxTokens, 1, 1, 0, 0, 0)), 1);
     if (op == TWELL_OP_PAGED_ATTN) return static_cast<int64_t>(twell_workspace_bytes(op, 1, 256, 1, 0, 0, 0));
     size_t most = 1;
     for (int32_t d = 8; d <= 16384; d += 8) most = std::max(most, twell_workspace_bytes(op, INT32_MAX, d, 1, 0, 0, 0));
@@ -368,9 +372,129 @@ PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// A side of a rotation: [n, heads, head_dim] or [sequences, n, heads, head_dim], head_dim contiguous, in and out.
+twell_rope_heads rope_side(const at::Tensor& in, const at::Tensor& out, const char* what, const at::Tensor& like, int64_t hd, int dev)
+{
+    const int64_t dims = like.dim();
+    bool ok = true;
+    for (const at::Tensor* t : {&in, &out}) {
+        ok = ok && t->dim() == dims && t->scalar_type() == like.scalar_type() && t->is_cuda() && t->get_device() == dev;
+        if (!ok) break;
+        for (int64_t i = 0; i < dims - 2; ++i) ok = ok && t->size(i) == like.size(i);
+        ok = ok && t->size(dims - 2) == in.size(dims - 2) && t->size(dims - 1) == hd && (t->numel() == 0 || t->stride(dims - 1) == 1 || hd == 1);
+    }
+    if (!ok) {
+        std::ostringstream s;
+        s << what << " and where it goes must be of q's type, device, sequences and tokens, with contiguous heads of " << hd
+          << ", not " << text(in) << " and " << text(out);
+        C10_THROW_ERROR(ValueError, s.str());
+    }
+    auto batch = [&](const at::Tensor& t) { return dims == 4 ? t.stride(0) : int64_t{0}; };
+    return {in.data_ptr(), out.data_ptr(), size32(in.size(dims - 2), "heads"), batch(in), in.stride(dims - 3), in.stride(dims - 2),
+            batch(out), out.stride(dims - 3), out.stride(dims - 2)};
+}
+
+// q, k, positions, turns, factor, neighbours, head_dim, q_out, k_out, backward, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    TWELL_ARGS("rope", 11);
+    const at::Tensor &q = *tensor(a[0], "q"), *k = tensor(a[1], "k", true), &pos = *tensor(a[2], "positions");
+    const at::Tensor &turns = *tensor(a[3], "turns"), &q_out = *tensor(a[7], "q_out"), *k_out = tensor(a[8], "k_out", true);
+    const int dev = device_of(q, "q");
+    if (q.dim() != 3 && q.dim() != 4) C10_THROW_ERROR(ValueError, "q must be [tokens, heads, head_dim] or [sequences, tokens, heads, head_dim]");
+    if ((k == nullptr) != (k_out == nullptr)) C10_THROW_ERROR(ValueError, "k and k_out go together");
+    const twell_dtype ct = code(q);
+    const bool many = q.dim() == 4;
+    const int32_t B = many ? size32(q.size(0), "sequences") : 1, S = size32(q.size(many ? 1 : 0), "tokens");
+    const int32_t hd = integer(a[6]), neighbours = integer(a[5]), rot = size32(2 * turns.numel(), "the rotation's pairs");
+    const twell_rope_heads hq = rope_side(q, q_out, "q", q, hd, dev);
+    const twell_rope_heads hk = k ? rope_side(*k, *k_out, "k", q, hd, dev) : twell_rope_heads{};
+    const bool own = many && pos.dim() == 2;  // positions of each sequence's own
+    const void* pp = own ? need(&pos, "positions", at::kInt, {B, S}, dev) : need(&pos, "positions", at::kInt, {S}, dev);
+    const void* pt = need(&turns, "turns", at::kLong, {turns.numel()}, dev);
+    const float factor = number(a[4]);
+    const bool backward = integer(a[9]) != 0;
+    const auto s = stream_of(a[10], dev);
+    return call(dev, [&] {
+        return (backward ? twell_rope_bwd : twell_rope_fwd)(&hq, k ? &hk : nullptr, static_cast<const int32_t*>(pp), own ? S : 0,
+                                                            static_cast<const uint64_t*>(pt), factor, B, S, hd, rot, neighbours, ct,
+                                                            s.stream());
+    });
+    END_HANDLE_TH_ERRORS
+}
+
+// ring, state, page_size, page_table, seq_lens, new_lens, labels, slots, positions, owner, starts, seq_lens_out, state_out,
+// status, stream
+PyObject* kv_plan(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    TWELL_ARGS("kv_plan", 15);
+    const at::Tensor &ring = *tensor(a[0], "ring"), &table = *tensor(a[3], "page_table"), &slots = *tensor(a[7], "slots");
+    const int dev = device_of(ring, "ring");
+    if (table.dim() != 2) C10_THROW_ERROR(ValueError, "page_table must be int32 [B, max_pages]");
+    const int32_t B = size32(table.size(0), "requests"), max_pages = size32(table.size(1), "page_table's columns");
+    const int32_t M = size32(slots.numel(), "slots");
+    auto ints = [&](int i, const char* what, Shape shape, bool optional = false) {
+        return static_cast<int32_t*>(need(tensor(a[i], what, optional), what, at::kInt, shape, dev));
+    };
+    const twell_page_pool pool = {size32(ring.numel(), "pages"), integer(a[2]), ints(0, "ring", {ring.numel()}), ints(1, "state", {4})};
+    int32_t* pt = ints(3, "page_table", {B, max_pages});
+    const int32_t *pl = ints(4, "seq_lens", {B}), *pn = ints(5, "new_lens", {B}), *pb = ints(6, "labels", {B}, true);
+    int32_t *ps = ints(7, "slots", {M}), *pp = ints(8, "positions", {M}), *po = ints(9, "owner", {M});
+    int32_t* pst = ints(10, "starts", {static_cast<int64_t>(B) + 1});
+    int32_t *lo = ints(11, "seq_lens_out", {B}), *so = ints(12, "state_out", {4}), *st = ints(13, "status", {1});
+    const auto s = stream_of(a[14], dev);
+    return call(dev, [&] {
+        return twell_kv_plan(&pool, pt, max_pages, pl, pn, pb, B, M, ps, pp, po, pst, lo, so, st, s.stream());
+    });
+    END_HANDLE_TH_ERRORS
+}
+
+// [n, columns] bf16 with contiguous columns and any row stride, and its address.
+Heads need_rows(const at::Tensor& t, const char* what, int64_t n, int64_t columns, int dev)
+{
+    if (t.scalar_type() != at::kBFloat16 || t.sizes() != at::IntArrayRef({n, columns}) || !t.is_cuda() || t.get_device() != dev ||
+        (t.numel() > 0 && columns > 1 && t.stride(1) != 1)) {
+        std::ostringstream s;
+        s << what << " must be bf16 [" << n << ", " << columns << "] on cuda:" << dev << " with contiguous rows, not " << text(t);
+        C10_THROW_ERROR(ValueError, s.str());
+    }
+    return {t.data_ptr(), n > 1 ? t.stride(0) : columns};
+}
+
+// y, x, a, b, scale, ranks, ids, out, ws, status, stream
+PyObject* lora_add(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    TWELL_ARGS("lora_add", 11);
+    const at::Tensor &y = *tensor(a[0], "y"), &x = *tensor(a[1], "x"), &A = *tensor(a[2], "a"), &B = *tensor(a[3], "b");
+    const int dev = device_of(A, "a");
+    if (A.dim() != 3 || B.dim() != 3 || x.dim() != 2) C10_THROW_ERROR(ValueError, "a and b must have three dimensions, x two");
+    const int32_t L = size32(A.size(0), "adapters"), R = size32(A.size(1), "rank"), k = size32(A.size(2), "columns of a");
+    const int32_t rows = size32(B.size(1), "rows of b"), N = size32(x.size(0), "tokens");
+    twell_adapters ad = {L, R, k, rows, need(&A, "a", at::kBFloat16, {L, R, k}, dev), need(&B, "b", at::kBFloat16, {L, rows, R}, dev),
+                         static_cast<const float*>(need(tensor(a[4], "scale"), "scale", at::kFloat, {L}, dev)),
+                         static_cast<const int32_t*>(need(tensor(a[5], "ranks", true), "ranks", at::kInt, {L}, dev))};
+    const Heads hx = need_rows(x, "x", N, k, dev), hy = need_rows(y, "y", N, rows, dev), ho = need_rows(*tensor(a[7], "out"), "out", N, rows, dev);
+    const void* pi = need(tensor(a[6], "ids"), "ids", at::kInt, {N}, dev);
+    void* st = need(tensor(a[9], "status"), "status", at::kInt, {1}, dev);
+    if (N > kLoraMaxTokens) return PyLong_FromLong(TWELL_ERR_UNSUPPORTED);
+    const auto s = stream_of(a[10], dev);
+    const Workspace ws = workspace(a[8], TWELL_OP_LORA_ADD, N, 1, dev, s);
+    void* pws = ws.t.data_ptr();
+    const size_t bytes = static_cast<size_t>(ws.t.numel());
+    return call(dev, [&] {
+        return twell_lora_add(hy.at, hy.stride, hx.at, hx.stride, &ad, static_cast<const int32_t*>(pi), N, const_cast<void*>(ho.at),
+                              ho.stride, pws, bytes, static_cast<int32_t*>(st), s.stream());
+    }, ws.turn);
+    END_HANDLE_TH_ERRORS
+}
+
 #define TWELL_METHOD(NAME) {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(NAME)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TWELL_METHOD(add_rmsnorm_fwd), TWELL_METHOD(add_rmsnorm_bwd), TWELL_METHOD(kv_append),
                          TWELL_METHOD(kv_gather), TWELL_METHOD(paged_attn_decode), TWELL_METHOD(w4_matvec),
+                         TWELL_METHOD(rope),            TWELL_METHOD(kv_plan),         TWELL_METHOD(lora_add),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_twell_call", "Calls of libtwell_gb300.so on tensors.", -1, methods};
 

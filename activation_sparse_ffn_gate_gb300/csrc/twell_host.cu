@@ -133,6 +133,7 @@ const char* twell_status_string(twell_status s)
     case TWELL_ERR_DEVICE_CHECK: return "device-side check failed";
     case TWELL_ERR_CUDA: return "CUDA error";
     case TWELL_ERR_WORKSPACE: return "workspace missing or too small";
+    case TWELL_ERR_POOL_EMPTY: return "fewer free pages than needed";
     }
     return "unknown status";
 }

@@ -156,9 +156,11 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint16_t v)
 
 namespace twell_host {
 
-// Bytes of the workspaces of twell_add_rmsnorm_bwd (twell_norm.cu) and twell_paged_attn_decode (twell_attn.cu).
+// Bytes of the workspaces of twell_add_rmsnorm_bwd (twell_norm.cu), twell_paged_attn_decode (twell_attn.cu) and
+// twell_lora_add (twell_lora.cu).
 size_t norm_bwd_ws_bytes(int N, int d);
 size_t paged_attn_ws_bytes(int B, int hd);
+size_t lora_ws_bytes(int N);
 
 // Allow `kern` up to `bytes` of dynamic shared memory, the most that any of its launches takes, on the current
 // device. `done` is the caller's, one for each kernel: a bit for each device it has been allowed on, so that a

@@ -1,0 +1,297 @@
+// twell_plan.cu -- a served step's plan, made on the device: pages for the requests' new tokens from a ring of free ones, the
+// pages of requests that have ended back into it, and slot, position and owner of each of the step's tokens.
+//
+// Three sums over the requests say everything: of the new tokens (where a request's tokens lie in the step), of the pages
+// taken (which page of the ring is whose) and of the pages given back. Every block forms them for itself, in shared memory
+// (4096 requests are 32 KB to read, from L2 but for the first), and then does its share of the tokens and pages, each of
+// which finds its request by bisection. Pages are taken at the ring's head and given back behind its last free page, so that
+// within a call nothing is written that the call still reads, and the result does not depend on any order.
+// Bounded by the launch and a chain of loads (state and lengths, then pages) for a decode step, by the 12 bytes a token that
+// it writes for long prompts.
+#include "twell_common.cuh"
+#include "twell_ops.cuh"
+
+namespace twell {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxSeqs = 4096;
+constexpr int kPlanPer = kPlanMaxSeqs / kPlanThreads;  // most requests a thread
+constexpr int kPlanQuad = 4;                           // consecutive tokens a thread takes at a time
+constexpr int kEnded = -1;
+
+struct PlanArgs {
+    int32_t* ring;
+    int32_t* state;  // the ring's first free page, the number of free ones, a count that is zero between calls
+    int32_t* table;
+    const int32_t* lens;
+    const int32_t* news;
+    const int32_t* labels;
+    int32_t *slots, *positions, *owner, *starts, *lens_out, *state_out, *status;
+    int n_pages, page_shift, max_pages, B, M;
+};
+
+// Sums of non-negative numbers that stop at 2^31 - 1.
+__device__ __forceinline__ int sat_add(int a, int b)
+{
+    return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu));
+}
+
+// The sum over the threads before this one, and over all of them. `red` has a place for each warp.
+__device__ __forceinline__ int block_scan(int v, int* red, int& total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kPlanThreads / 32;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl = sat_add(incl, u);
+    }
+    if (lane == 31) red[warp] = incl;
+    __syncthreads();
+    int w = lane < warps ? red[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < warps; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w = sat_add(w, u);
+    }
+    total = __shfl_sync(0xffffffffu, w, warps - 1);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    const int excl = __shfl_up_sync(0xffffffffu, incl, 1);
+    __syncthreads();
+    return sat_add(warp ? before : 0, lane ? excl : 0);
+}
+
+// The last i < n with at[i] <= v (at ascending, at[0] <= v).
+__device__ __forceinline__ int last_at_most(const int* at, int n, int v)
+{
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int half = len >> 1;
+        if (at[lo + half] <= v) lo += half;
+        len -= half;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
+{
+    extern __shared__ int plan_smem[];
+    __shared__ int red[32];
+    __shared__ int s_taken, s_last;
+    pdl_begin();
+    int* start = plan_smem;          // [B + 1] of the requests' tokens in the step
+    int* past = start + a.B + 1;     // [B] tokens that they had, -1 where they get none
+    int* first = past + a.B;         // [B] of their pages among those taken
+    int* back = first + a.B;         // [B] of their pages among those given back
+    const int page = 1 << a.page_shift, tid = static_cast<int>(threadIdx.x);
+    int head = a.state[0], free = a.state[1];
+    bool bad = head < 0 || free < 0 || free > a.n_pages || (head >= a.n_pages && (head != 0 || free != 0));
+    if (bad) head = free = 0;  // nothing can be taken from or given to a ring that is not one
+    const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll);
+    const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
+    if (tid == 0) s_taken = 0;
+
+    // a request: tokens it had, its new ones, its end
+    int had[kPlanPer], add[kPlanPer];
+    bool ends[kPlanPer], wrong[kPlanPer];
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) {
+        had[i] = add[i] = 0;
+        ends[i] = wrong[i] = false;
+        if (i < per && b0 + i < a.B) {
+            had[i] = a.lens[b0 + i];
+            const int n = a.news[b0 + i];
+            add[i] = max(n, 0);
+            ends[i] = n == kEnded;
+            wrong[i] = n < kEnded || had[i] < 0 || static_cast<long long>(had[i]) + add[i] > cap;
+            sum = sat_add(sum, add[i]);
+        }
+    }
+    int total;
+    int at = block_scan(sum, red, total);
+    // pages: a request whose tokens do not all have a place in the step or in its row of the table gets none
+    int need[kPlanPer], gives[kPlanPer], need_sum = 0, gives_sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) {
+        need[i] = gives[i] = 0;
+        if (i < per && b0 + i < a.B) {
+            start[b0 + i] = at;
+            if (add[i] > 0 && static_cast<long long>(at) + add[i] > a.M) wrong[i] = true;
+            at = sat_add(at, add[i]);
+            if (!wrong[i]) {
+                const int held = (had[i] + page - 1) >> a.page_shift;
+                if (ends[i]) gives[i] = held;
+                else if (add[i] > 0) need[i] = static_cast<int>((static_cast<long long>(had[i]) + add[i] + page - 1) >> a.page_shift) - held;
+            }
+            bad |= wrong[i];
+            need_sum = sat_add(need_sum, need[i]);
+            gives_sum = sat_add(gives_sum, gives[i]);
+        }
+    }
+    if (tid == 0) start[a.B] = total;
+    int need_total, given;
+    int take = block_scan(need_sum, red, need_total);
+    int give = block_scan(gives_sum, red, given);
+    // more pages than there are: some are given back twice, and none are taken back
+    const bool refuse = static_cast<long long>(free) + given > a.n_pages;
+    if (refuse) given = 0;
+    bad |= refuse;
+    bool empty = false;
+    int taken = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) {
+        if (i < per && b0 + i < a.B) {
+            const bool none = need[i] > 0 && sat_add(take, need[i]) > free;
+            empty |= none;
+            past[b0 + i] = wrong[i] || none ? -1 : had[i];
+            first[b0 + i] = take;
+            back[b0 + i] = give;
+            take = sat_add(take, need[i]);
+            if (need[i] > 0 && !none) taken = take;
+            give = sat_add(give, gives[i]);
+            if (wrong[i] || none) add[i] = 0;
+            had[i] = ends[i] && !wrong[i] && !refuse ? 0 : had[i] + add[i];  // the length after the step
+        }
+    }
+    if (taken > 0) atomicMax(&s_taken, taken);
+    if (bad) report(a.status, TWELL_ERR_DEVICE_CHECK);
+    if (empty) report(a.status, TWELL_ERR_POOL_EMPTY);
+    __syncthreads();
+    taken = s_taken;
+
+    // lengths and state may be written where they were read once every block has read them: the last to say so does it
+    const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
+    bool commit = blockIdx.x == 0;
+    if (in_place && gridDim.x > 1) {
+        if (tid == 0) {
+            __threadfence();
+            s_last = atomicAdd(a.state + 2, 1) == static_cast<int>(gridDim.x) - 1;
+        }
+        __syncthreads();
+        commit = s_last != 0;
+    }
+    if (commit) {
+#pragma unroll
+        for (int i = 0; i < kPlanPer; ++i)
+            if (i < per && b0 + i < a.B) a.lens_out[b0 + i] = had[i];
+        for (int i = tid; i <= a.B; i += kPlanThreads) a.starts[i] = start[i];
+        if (tid == 0) {
+            const long long h = static_cast<long long>(head) + taken;
+            a.state_out[0] = static_cast<int>(h >= a.n_pages && a.n_pages > 0 ? h - a.n_pages : h);
+            a.state_out[1] = free - taken + given;
+            a.state_out[2] = a.state_out[3] = 0;
+            if (in_place && gridDim.x > 1) a.state[2] = 0;
+        }
+    }
+
+    auto ring_at = [&](int i) {  // the i-th cell from the head on, i < n_pages
+        const long long j = static_cast<long long>(head) + i;
+        return a.ring + (j >= a.n_pages ? j - a.n_pages : j);
+    };
+    auto row = [&](int b, int p) { return a.table + static_cast<long long>(b) * a.max_pages + p; };
+    const unsigned threads = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + tid;
+
+    // tokens, four at a time
+    const unsigned quads = (static_cast<unsigned>(a.M) + kPlanQuad - 1) / kPlanQuad;
+    for (unsigned u = me; u < quads; u += threads) {
+        const int i0 = static_cast<int>(u * kPlanQuad);
+        int slot[kPlanQuad], pos[kPlanQuad], own[kPlanQuad];
+        int b = a.B > 0 ? last_at_most(start, a.B, i0) : 0;
+        int known = -1, base = -1;  // the page of the sequence that `base` is the first slot of, -1 where there is none
+        int label = 0;
+        int label_of = -1;
+#pragma unroll
+        for (int e = 0; e < kPlanQuad; ++e) {
+            const int i = i0 + e;
+            slot[e] = own[e] = -1;
+            pos[e] = 0;
+            if (i >= min(total, a.M)) continue;
+            while (i >= start[b + 1]) ++b, known = -1;
+            if (label_of != b) {
+                label = a.labels ? __ldg(a.labels + b) : b;
+                label_of = b;
+            }
+            own[e] = label;
+            if (past[b] < 0) continue;
+            pos[e] = past[b] + (i - start[b]);
+            const int p = pos[e] >> a.page_shift;
+            if (p != known) {
+                const int held = (past[b] + page - 1) >> a.page_shift;
+                const int pg = p < held ? *row(b, p) : *ring_at(first[b] + p - held);
+                known = p;
+                base = -1;
+                if (pg >= 0 && pg < a.n_pages) base = pg << a.page_shift;
+                else report(a.status, TWELL_ERR_DEVICE_CHECK);
+            }
+            if (base >= 0) slot[e] = base + (pos[e] & (page - 1));
+        }
+        if (i0 + kPlanQuad <= a.M) {
+            *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4*>(a.owner + i0) = make_int4(own[0], own[1], own[2], own[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPlanQuad; ++e)
+                if (i0 + e < a.M) {
+                    a.slots[i0 + e] = slot[e];
+                    a.positions[i0 + e] = pos[e];
+                    a.owner[i0 + e] = own[e];
+                }
+        }
+    }
+    // pages taken, into the table
+    for (unsigned u = me; u < static_cast<unsigned>(taken); u += threads) {
+        const int j = static_cast<int>(u), b = last_at_most(first, a.B, j);
+        *row(b, ((past[b] + page - 1) >> a.page_shift) + j - first[b]) = *ring_at(j);
+    }
+    // pages given back, behind the free ones
+    for (unsigned u = me; u < static_cast<unsigned>(given); u += threads) {
+        const int j = static_cast<int>(u), b = last_at_most(back, a.B, j);
+        const int pg = *row(b, j - back[b]);
+        if (pg < 0 || pg >= a.n_pages) report(a.status, TWELL_ERR_DEVICE_CHECK);
+        *ring_at(free + j) = pg;
+    }
+}
+
+}  // namespace
+}  // namespace twell
+
+using namespace twell_host;
+
+extern "C" twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page_table, int32_t max_pages,
+                                      const int32_t* seq_lens, const int32_t* new_lens, const int32_t* labels, int32_t B,
+                                      int32_t n_tokens, int32_t* slots, int32_t* positions, int32_t* owner, int32_t* starts,
+                                      int32_t* seq_lens_out, int32_t* state_out, int32_t* dev_status, void* stream)
+{
+    if (pool == nullptr || pool->n_pages < 0 || pool->page_size <= 0 || max_pages <= 0 || B < 0 || n_tokens < 0)
+        return TWELL_ERR_INVALID;
+    if ((pool->page_size & (pool->page_size - 1)) != 0 || pool->page_size > 1024 || B > twell::kPlanMaxSeqs ||
+        static_cast<long long>(pool->n_pages) * pool->page_size > INT32_MAX || n_tokens > INT32_MAX - 65536)
+        return TWELL_ERR_UNSUPPORTED;
+    const void* need[] = {pool->state, starts, state_out, dev_status};
+    for (const void* p : need)
+        if (p == nullptr) return TWELL_ERR_INVALID;
+    if (pool->n_pages > 0 && pool->ring == nullptr) return TWELL_ERR_INVALID;
+    if (B > 0 && (page_table == nullptr || seq_lens == nullptr || new_lens == nullptr || seq_lens_out == nullptr))
+        return TWELL_ERR_INVALID;
+    if (n_tokens > 0 && (slots == nullptr || positions == nullptr || owner == nullptr)) return TWELL_ERR_INVALID;
+    if (!aligned16(slots) || !aligned16(positions) || !aligned16(owner)) return TWELL_ERR_INVALID;
+    const void* words[] = {pool->ring, pool->state, page_table, seq_lens, new_lens, labels, starts, seq_lens_out, state_out};
+    for (const void* p : words)
+        if (reinterpret_cast<uintptr_t>(p) % sizeof(int32_t) != 0) return TWELL_ERR_INVALID;
+    int shift = 0;
+    while ((1 << shift) < pool->page_size) ++shift;
+    const twell::PlanArgs a = {pool->ring, pool->state, page_table,   seq_lens,  new_lens,   labels, slots, positions, owner,
+                               starts,     seq_lens_out, state_out,   dev_status, pool->n_pages, shift, max_pages, B, n_tokens};
+    DevInfo dev;
+    if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
+    const size_t smem = (4 * static_cast<size_t>(B) + 1) * sizeof(int);
+    static std::atomic<uint64_t> allowed{0};
+    if (allow_smem(twell::kv_plan_kernel, (4 * twell::kPlanMaxSeqs + 1) * sizeof(int), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    const long long quads = (static_cast<long long>(n_tokens) + twell::kPlanQuad - 1) / twell::kPlanQuad;
+    const long long blocks = (quads + twell::kPlanThreads - 1) / twell::kPlanThreads;
+    return launch_dep(twell::kv_plan_kernel, dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < dev.sm_count ? blocks : dev.sm_count)),
+                      dim3(twell::kPlanThreads), smem, static_cast<cudaStream_t>(stream), a);
+}

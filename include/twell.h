@@ -55,7 +55,8 @@ typedef enum {
     TWELL_ERR_TIMEOUT = 4,     /* a bounded device-side wait ran out (device-reported) */
     TWELL_ERR_DEVICE_CHECK = 5,/* a device-side consistency check failed (device-reported) */
     TWELL_ERR_CUDA = 6,        /* a CUDA runtime call or kernel launch failed */
-    TWELL_ERR_WORKSPACE = 7    /* workspace missing or smaller than twell_workspace_bytes() */
+    TWELL_ERR_WORKSPACE = 7,   /* workspace missing or smaller than twell_workspace_bytes() */
+    TWELL_ERR_POOL_EMPTY = 8   /* twell_kv_plan: fewer free pages than the step's tokens need (device-reported) */
 } twell_status;
 
 /* TWELL_E4M3 (8 bits, largest value 448) is an element type of the key-value cache only. */
@@ -72,7 +73,8 @@ typedef enum {
     TWELL_OP_FFN_TILE_UNION_FWD = 7,
     TWELL_OP_FFN_GATE_UNION_FWD = 8,
     TWELL_OP_ADD_RMSNORM_BWD = 9, /* N rows of d columns; the other arguments are not used */
-    TWELL_OP_PAGED_ATTN = 10      /* N sequences, d = head_dim; the other arguments are not used */
+    TWELL_OP_PAGED_ATTN = 10,     /* N sequences, d = head_dim; the other arguments are not used */
+    TWELL_OP_LORA_ADD = 11        /* N tokens; the other arguments are not used */
 } twell_op;
 
 /* A TwELL matrix of gate activations a = ReLU(G), [n_rows, n_cols] ([TG] "Вот тут и решает TwELL";
@@ -476,6 +478,90 @@ TWELL_API twell_status twell_w4_quantize(const void* W, int32_t n, int32_t k, in
  * any batch of up to 8 tokens, and in any of 9 to 16. */
 TWELL_API twell_status twell_w4_matvec(const void* x, const void* words, const void* scales, int32_t N, int32_t n,
                              int32_t k, int32_t group, void* y, void* stream);
+
+/* Rotary positions. A side (queries or keys) of B sequences of S tokens: element j of head h of token t of sequence b is
+ * at in + b * in_batch + t * in_token + h * in_head + j and goes to out + b * out_batch + t * out_token + h * out_head + j.
+ * in may be out, with the same strides (the call then works in place); else the two do not overlap. The heads of an output
+ * lie apart. Strides in elements; addresses need only the element type's alignment (16-byte vectors are used where the
+ * addresses, strides and rot_dim allow them, 8-, 4- and 2-byte ones else). */
+typedef struct {
+    const void* in;
+    void* out;
+    int32_t n_heads;
+    int64_t in_batch, in_token, in_head;
+    int64_t out_batch, out_token, out_head;
+} twell_rope_heads;
+
+/* The first rot_dim values of each head (even, at most head_dim) are rot_dim / 2 pairs: (i, i + rot_dim / 2), or with
+ * neighbours = 1 (2i, 2i + 1). Pair i of a token at position p is turned by t = 2 pi p turns[i] / 2^64:
+ *   (a, b) -> factor (a cos t - b sin t, a sin t + b cos t)
+ * and the other values are copied. positions: device int32, of token t of sequence b at b * pos_batch + t (pos_batch 0: the
+ * same for all sequences), any value. turns: device uint64 [rot_dim / 2], 2^64 times the turns a position, modulo 2^64: the
+ * fraction of a turn is then exact for every position, and t is off by at most 2^-22. k may be null.
+ * dtype TWELL_BF16 or TWELL_F32; products in fp32, rounded once. factor > 0; head_dim <= 1024 and B * S * head_dim < 2^31
+ * (else TWELL_ERR_UNSUPPORTED). twell_rope_bwd takes gradients of the outputs to those of the inputs: the same with -t. */
+TWELL_API twell_status twell_rope_fwd(const twell_rope_heads* q, const twell_rope_heads* k, const int32_t* positions,
+                            int64_t pos_batch, const uint64_t* turns, float factor, int32_t B, int32_t S,
+                            int32_t head_dim, int32_t rot_dim, int32_t neighbours, twell_dtype dtype, void* stream);
+TWELL_API twell_status twell_rope_bwd(const twell_rope_heads* dq, const twell_rope_heads* dk, const int32_t* positions,
+                            int64_t pos_batch, const uint64_t* turns, float factor, int32_t B, int32_t S,
+                            int32_t head_dim, int32_t rot_dim, int32_t neighbours, twell_dtype dtype, void* stream);
+
+/* The pages of a cache that no sequence has (host struct; device memory owned by the caller): ring int32 [n_pages], of which
+ * the cells state[0], state[0] + 1, ... modulo n_pages hold the state[1] free pages; state[2] is 0 between calls and state[3]
+ * 0. All pages free: ring 0, 1, 2, ..., state 0, n_pages, 0, 0. page_size as in twell_kv_cache. */
+typedef struct {
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t* ring;
+    int32_t* state;
+} twell_page_pool;
+
+/* The plan of a step of B requests (B <= 4096, else TWELL_ERR_UNSUPPORTED), on the device: request b has seq_lens[b] tokens
+ * in the pages of row b of page_table [B, max_pages], and new_lens[b] new ones in this step (0: none; -1: it has ended). The
+ * step's tokens are the requests' new ones, one request after the other: starts [B + 1] receives where each one's begin
+ * (numbers past 2^31 - 1 as that). Token i of n_tokens receives its position in its sequence, its slot (for twell_kv_append)
+ * and its owner: labels[b], or b without labels. Tokens past the last request's receive slot -1, position 0, owner -1.
+ * New pages come from the ring's front, in the order of requests and positions, into the requests' rows; the pages of a
+ * request that has ended go to its back, where later calls find them, its row stays as it is and its length becomes 0.
+ * seq_lens_out [B] receives the lengths after the step and state_out [4] the pool's state; they may be seq_lens and
+ * pool->state. A request gets nothing (length and row stay, its tokens receive slot -1 and position 0) if
+ *  - the pages of the requests up to it that need any are more than the free ones: TWELL_ERR_POOL_EMPTY in *dev_status;
+ *  - its length is negative or does not fit its row, its new tokens do not fit n_tokens, or new_lens[b] < -1:
+ *    TWELL_ERR_DEVICE_CHECK.
+ * More pages given back than are missing (none are taken back then), a state outside the ring (nothing is taken or given
+ * then; the ring counts as empty from there on), and pages outside [0, n_pages) in a row or the ring (slot -1) are
+ * TWELL_ERR_DEVICE_CHECK too. Calls on one pool must follow one another. All integers: the same from call to call. */
+TWELL_API twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page_table, int32_t max_pages,
+                           const int32_t* seq_lens, const int32_t* new_lens, const int32_t* labels, int32_t B,
+                           int32_t n_tokens, int32_t* slots, int32_t* positions, int32_t* owner, int32_t* starts,
+                           int32_t* seq_lens_out, int32_t* state_out, int32_t* dev_status, void* stream);
+
+/* Low-rank adapters of one projection (host struct of device pointers): a bf16 [n_adapters, rank, k], b bf16 [n_adapters, n,
+ * rank], scale fp32 [n_adapters]; ranks int32 [n_adapters], or null: all `rank`. Of adapter i the first ranks[i] rows of a
+ * and columns of b count; the others may hold anything. k, n and rank multiples of 8, rank <= 128, n_adapters <= 4096, k and
+ * n <= 2^20. */
+typedef struct {
+    int32_t n_adapters;
+    int32_t rank;
+    int32_t k;
+    int32_t n;
+    const void* a;
+    const void* b;
+    const float* scale;
+    const int32_t* ranks;
+} twell_adapters;
+
+/* out[i] = y[i] + scale[c] b[c] (a[c] x[i]) with c = ids[i], for N <= 2^20 tokens in any order; out[i] = y[i] where c = -1.
+ * x [N, k], y and out [N, n] bf16, rows ldx, ldy and ldo elements apart (multiples of 8: slices of a fused projection are
+ * fine). out may be y with the same stride (rows without an adapter are then not touched); else they do not overlap. Sums are
+ * fp32 and out is rounded once; a[c] x[i] enters the second product with 16 bits or more. A row's result does not depend on
+ * the other tokens' rows or on their order. An id outside [-1, n_adapters) or a rank outside [0, rank] is reported as
+ * TWELL_ERR_DEVICE_CHECK and counts as -1. ws: twell_workspace_bytes(TWELL_OP_LORA_ADD, N, 1, 1, 0, 0, 0) bytes; two calls
+ * in flight at the same time must not share it. */
+TWELL_API twell_status twell_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const twell_adapters* ad,
+                            const int32_t* ids, int32_t N, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * Test exports. They run the same device code as the calls above on a gate matrix the caller
