@@ -70,7 +70,10 @@ def test_plan_refuses(lib):
         assert _plan(lib, **bad) == UNSUPPORTED, bad
 
 
-def _lora(lib, y=A, ldy=64, x=A, ldx=128, L=2, R=16, k=128, n=64, a=1 << 20, b=1 << 20, scale=1 << 20, ranks=None, ids=A, N=4, out=A,
+X = ctypes.c_void_p(1 << 22)
+
+
+def _lora(lib, y=A, ldy=64, x=X, ldx=128, L=2, R=16, k=128, n=64, a=1 << 20, b=1 << 20, scale=1 << 20, ranks=None, ids=A, N=4, out=A,
           ldo=64, ws=A, nb=1 << 30, st=A):
     ad = binding._Adapters(L, R, k, n, a, b, scale, ranks)
     return lib.twell_lora_add(y, ldy, x, ldx, ctypes.byref(ad), ids, N, out, ldo, ws, nb, st, None)
@@ -80,7 +83,7 @@ def test_lora_refuses(lib):
     for bad in (dict(y=None), dict(x=None), dict(a=None), dict(b=None), dict(scale=None), dict(ids=None), dict(out=None), dict(st=None),
                 dict(N=-1), dict(L=0), dict(R=0), dict(k=0), dict(n=0), dict(R=12), dict(k=100), dict(n=60), dict(y=ODD, out=ODD),
                 dict(x=ODD), dict(out=ODD), dict(a=(1 << 20) + 8), dict(b=(1 << 20) + 8), dict(scale=(1 << 20) + 2), dict(ids=BYTE),
-                dict(ranks=(1 << 20) + 1), dict(ldy=60), dict(ldx=120), dict(ldx=132), dict(ldo=56), dict(ldo=72)):
+                dict(ranks=(1 << 20) + 1), dict(ldy=60), dict(ldx=120), dict(ldx=132), dict(ldo=56), dict(ldo=72), dict(x=A)):
         assert _lora(lib, **bad) == INVALID, bad
     for bad in (dict(R=136), dict(L=4097), dict(N=(1 << 20) + 1), dict(k=(1 << 20) + 8, ldx=1 << 21), dict(n=(1 << 20) + 8, ldy=1 << 21, ldo=1 << 21)):
         assert _lora(lib, **bad) == UNSUPPORTED, bad
