@@ -27,7 +27,7 @@ namespace {
 
 using Shape = std::initializer_list<int64_t>;
 
-constexpr int32_t kLoraMaxTokens = 1 << 20;  // of one twell_lora_add
+constexpr int32_t kLoraMaxTokens = 1 << 20, kLoraMaxRank = 128;  // of one twell_lora_add
 
 std::string text(const at::Tensor& t)
 {
@@ -104,12 +104,12 @@ struct Workspace {
     std::mutex* turn;
 };
 
-// Bytes that any call of an operator needs. Its buffers have this size from the start (10 MB, 26 MB and 4 MB) and are never
+// Bytes that any call of an operator needs. Its buffers have this size from the start (10 MB, 26 MB and 9 MB) and are never
 // replaced.
 int64_t most_bytes(twell_op op)
 {
     if (op == TWELL_OP_LORA_ADD)
-        return std::max<int64_t>(static_cast<int64_t>(twell_workspace_bytes(op, kLoraMaxTokens, 1, 1, 0, 0, 0)), 1);
+        return std::max<int64_t>(static_cast<int64_t>(twell_workspace_bytes(op, kLoraMaxTokens, kLoraMaxRank, 1, 0, 0, 0)), 1);
     if (op == TWELL_OP_PAGED_ATTN) return static_cast<int64_t>(twell_workspace_bytes(op, 1, 256, 1, 0, 0, 0));
     size_t most = 1;
     for (int32_t d = 8; d <= 16384; d += 8) most = std::max(most, twell_workspace_bytes(op, INT32_MAX, d, 1, 0, 0, 0));
@@ -479,9 +479,9 @@ PyObject* lora_add(PyObject*, PyObject* const* a, Py_ssize_t n)
     const Heads hx = need_rows(x, "x", N, k, dev), hy = need_rows(y, "y", N, rows, dev), ho = need_rows(*tensor(a[7], "out"), "out", N, rows, dev);
     const void* pi = need(tensor(a[6], "ids"), "ids", at::kInt, {N}, dev);
     void* st = need(tensor(a[9], "status"), "status", at::kInt, {1}, dev);
-    if (N > kLoraMaxTokens) return PyLong_FromLong(TWELL_ERR_UNSUPPORTED);
+    if (N > kLoraMaxTokens || R > kLoraMaxRank) return PyLong_FromLong(TWELL_ERR_UNSUPPORTED);
     const auto s = stream_of(a[10], dev);
-    const Workspace ws = workspace(a[8], TWELL_OP_LORA_ADD, N, 1, dev, s);
+    const Workspace ws = workspace(a[8], TWELL_OP_LORA_ADD, N, R, dev, s);
     void* pws = ws.t.data_ptr();
     const size_t bytes = static_cast<size_t>(ws.t.numel());
     return call(dev, [&] {

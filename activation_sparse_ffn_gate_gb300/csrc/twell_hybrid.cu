@@ -864,7 +864,7 @@ extern "C" size_t twell_workspace_bytes(twell_op op, int32_t N, int32_t d, int32
     case TWELL_OP_HYBRID_BWD: return twell::HybridWs(N, d, f, K, backup_cap).bwd_total;
     case TWELL_OP_ADD_RMSNORM_BWD: return twell_host::norm_bwd_ws_bytes(N, d);
     case TWELL_OP_PAGED_ATTN: return twell_host::paged_attn_ws_bytes(N, d);
-    case TWELL_OP_LORA_ADD: return twell_host::lora_ws_bytes(N);
+    case TWELL_OP_LORA_ADD: return twell_host::lora_ws_bytes(N, d);
     }
     return 0;
 }

@@ -22,8 +22,8 @@ constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraCluster = 8;      // most blocks a tile
 constexpr int kLoraSmallN = 512;     // up to here every cluster finds its tile from the ids itself
-constexpr int kLoraSmallMT = 1;
 constexpr int kLoraGroupThreads = 1024;
+constexpr int kLoraPass = 16384;     // tokens of a larger batch that go together
 
 struct LoraArgs {
     const __nv_bfloat16 *a, *b, *x, *y;
@@ -39,20 +39,67 @@ struct LoraArgs {
     const int32_t* order;
 };
 
-// Shared memory of a block: floats of the warps' sums (then the fragments of t), of the blocks' sums.
-template <int MT, int RG, int RT>
+// Shared memory of a block: of each warp a ring of copies (in which it also leaves its sums), the fragments of t, the blocks'
+// sums. A ring's slots are the lane's own: 16 bytes a lane and vector, copied and read by the same lane.
+// BOTH: the kernel does both products, else the first alone.
+template <int MT, int RG, int RT, bool BOTH>
 struct LoraShape {
     static constexpr int kTok = 16 * MT;
     static constexpr int kWays = kLoraWarps / RG;     // warps that share a part of k
-    static constexpr int kRanks = RG * RT * 8;
-    static constexpr int kPitch = kRanks + 4;         // floats of a token's row
+    static constexpr int kWarpRanks = RT * 8;
+    static constexpr int kRanks = RG * kWarpRanks;
+    static constexpr int kPitch = kRanks + 4;         // floats of a token's row in the blocks' sums
     static constexpr int kBlock = RT == 2 ? 16 : 32;  // ranks of which a lane takes a quarter at a time
     static constexpr int kFrags = kRanks / 16;
     static constexpr int kSum = kTok * kPitch;
-    static constexpr int kFragFloats = MT * kFrags * 2 * 32 * 4;
-    static constexpr int kWarpSums = kWays * kSum > kFragFloats ? kWays * kSum : kFragFloats;
-    static constexpr size_t bytes(int cluster) { return sizeof(float) * (kWarpSums + static_cast<size_t>(cluster) * kSum); }
+    static constexpr int kIn = (2 * MT + RT) * 512;                              // a stage of the first product: 32 columns
+    static constexpr int kOut = 2 * MT * 512 + 4 * (kRanks / kBlock) * kBlock * 16;  // of the second: 32 columns of y and B's rows
+    static constexpr int kWarpSums = kTok * kWarpRanks * 4;
+    // room for three stages of the first product at least, and for kMinOut of the second beside the sums
+    static constexpr int kMinOut = RG == 1 ? 2 : 1;
+    static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut) : 12 * 1024;
+    static constexpr int kInStages = kRing / kIn > 4 ? 4 : kRing / kIn;
+    static constexpr int kOutStages = (kRing - kWarpSums) / kOut > 4 ? 4 : (kRing - kWarpSums) / kOut;
+    static constexpr int kFragBytes = MT * kFrags * 2 * 512;
+    static constexpr size_t bytes(int cluster)
+    {
+        if (BOTH) return kLoraWarps * kRing + kFragBytes + sizeof(float) * static_cast<size_t>(cluster) * kSum;
+        return kLoraWarps * kRing + (cluster > 1 ? sizeof(float) * kTok * kRanks : 0);
+    }
+    // a warp's sum of (token, rank) in floats: quads of ranks are exchanged between rows, for the banks
+    __device__ __forceinline__ static int at(int token, int rank)
+    {
+        return token * kWarpRanks + (((rank >> 2) ^ (token & (kWarpRanks / 4 - 1))) << 2) + (rank & 3);
+    }
 };
+
+// Copies of 16 or 8 bytes of which `bytes` are taken from memory and the rest is zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
+    return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at));
+    return r;
+}
 
 __device__ __forceinline__ void cluster_arrive()
 {
@@ -134,38 +181,133 @@ __device__ __forceinline__ void lora_find(const LoraArgs& g, int index, int* cou
     __syncthreads();
 }
 
-template <int MT, int RG, int RT, bool SMALL>
-__global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_kernel(const LoraArgs g)
+// t = A x over one block's part of k: a warp has kWarpRanks ranks and every kWays-th 64 columns, 32 a stage. Leaves the warps'
+// sums in their rings, which are free but for that; `between` runs once a warp's ring is (the copies of what comes next).
+template <typename S, int MT, int RG, int RT, typename F>
+__device__ __forceinline__ void lora_shrink(const LoraArgs& g, int id, int rank, int part, int blocks, const int (&token)[MT][2],
+                                            uint8_t* ring_at, F between)
 {
-    using S = LoraShape<MT, RG, RT>;
-    extern __shared__ __align__(16) float lora_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, c = lane & 3;
+    const uint32_t mine = smem_u32(ring_at) + lane * 16;
+    const int rg = warp % RG, way = warp / RG;
+    float acc[MT][RT][4] = {};
+    {
+        const int kb_all = (g.k + 63) / 64, kb0 = static_cast<int>(static_cast<long long>(kb_all) * part / blocks) + way,
+                  kb1 = static_cast<int>(static_cast<long long>(kb_all) * (part + 1) / blocks);
+        const int row0 = rg * S::kWarpRanks + gr;
+        // a warp whose ranks all lie past the adapter's has nothing to do
+        const int stages = rg * S::kWarpRanks < rank && kb0 < kb1 ? (kb1 - kb0 + S::kWays - 1) / S::kWays * 2 : 0;
+        const __nv_bfloat16* A = g.a + (static_cast<int64_t>(id) * g.R + row0) * g.k;
+        auto request = [&](int i, int slot) {
+            if (i < stages) {
+                const int col = 64 * (kb0 + (i >> 1) * S::kWays) + 32 * (i & 1) + 8 * c;
+                const uint32_t at = mine + slot * S::kIn;
+                const bool in = col < g.k;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const bool live = in && row0 + 8 * r < rank;
+                    copy16(at + r * 512, live ? A + static_cast<int64_t>(8 * r) * g.k + col : g.a, live ? 16 : 0);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const bool live = in && token[m][s] >= 0;
+                        copy16(at + (RT + 2 * m + s) * 512, live ? g.x + token[m][s] * g.ldx + col : g.x, live ? 16 : 0);
+                    }
+            }
+            copies_end();
+        };
+#pragma unroll
+        for (int i = 0; i < S::kInStages; ++i) request(i, i);
+        int slot = 0;
+        for (int i = 0; i < stages; ++i) {
+            copies_wait<S::kInStages - 1>();
+            const uint32_t at = mine + slot * S::kIn;
+            uint4 xv[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) xv[m][s] = lds16(at + (RT + 2 * m + s) * 512);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const uint4 w = lds16(at + r * 512);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    mma_bf16(acc[m][r], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, w.x, w.y);
+                    mma_bf16(acc[m][r], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, w.z, w.w);
+                }
+            }
+            request(i + S::kInStages, slot);  // all of the slot has been read: the products have taken it
+            slot = slot + 1 == S::kInStages ? 0 : slot + 1;
+        }
+    }
+    copies_wait<0>();
+    __syncwarp();  // the ring is free: what follows writes where other lanes' slots were
+    between();
+    float* sums = reinterpret_cast<float*>(ring_at);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            *reinterpret_cast<float2*>(sums + S::at(16 * m + gr, 8 * r + 2 * c)) = make_float2(acc[m][r][0], acc[m][r][1]);
+            *reinterpret_cast<float2*>(sums + S::at(16 * m + 8 + gr, 8 * r + 2 * c)) = make_float2(acc[m][r][2], acc[m][r][3]);
+        }
+}
+
+// The sum over the warps of four ranks of a token, from `smem`, the rings.
+template <typename S, int RG>
+__device__ __forceinline__ float4 lora_sum(const uint8_t* smem, int row, int quad)
+{
+    constexpr int kWarpQuads = S::kWarpRanks / 4;
+    const float* from = reinterpret_cast<const float*>(smem + quad / kWarpQuads * S::kRing) + S::at(row, quad % kWarpQuads * 4);
+    float4 v = *reinterpret_cast<const float4*>(from);
+#pragma unroll
+    for (int w = 1; w < S::kWays; ++w) {
+        const float4 u = *reinterpret_cast<const float4*>(from + w * RG * (S::kRing / 4));
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    return v;
+}
+
+// Four ranks of t under the scale, from r0 on: what lies past the rank is a row of zeros times x, NaN where x is infinite, and
+// becomes 0. Hi parts in x and y, lo parts in z and w.
+__device__ __forceinline__ uint4 lora_parts(const float4& v, int r0, int rank, float scale)
+{
+    uint4 o;
+    split2(r0 < rank ? v.x * scale : 0.0f, r0 + 1 < rank ? v.y * scale : 0.0f, o.x, o.z);
+    split2(r0 + 2 < rank ? v.z * scale : 0.0f, r0 + 3 < rank ? v.w * scale : 0.0f, o.y, o.w);
+    return o;
+}
+
+__device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
+{
+    if (id >= g.L) return 0;
+    const int rank = g.ranks ? __ldg(g.ranks + id) : g.R;
+    if (rank >= 0 && rank <= g.R) return rank;
+    report(g.status, TWELL_ERR_DEVICE_CHECK);
+    return 0;
+}
+
+// A batch of at most kLoraSmallN tokens, whole.
+template <int MT, int RG, int RT>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
+{
+    using S = LoraShape<MT, RG, RT, true>;
+    extern __shared__ __align__(16) uint8_t lora_smem[];
     __shared__ int tok[S::kTok];
     pdl_begin();
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2, c = lane & 3;
     const int blocks = static_cast<int>(cluster_blocks()), part = static_cast<int>(cluster_ctarank());
     const int index = static_cast<int>(blockIdx.x) / blocks;
     int id, tokens = 0;
-    if constexpr (SMALL) {
-        // the counts and numbers lie where the sums come later
-        lora_find<S::kTok>(g, index, reinterpret_cast<int*>(lora_smem),
-                           reinterpret_cast<uint16_t*>(reinterpret_cast<int*>(lora_smem) + g.L + 1), tok, id, tokens);
+    {
+        // the counts and numbers lie where the rings come later
+        int* count = reinterpret_cast<int*>(lora_smem);
+        lora_find<S::kTok>(g, index, count, reinterpret_cast<uint16_t*>(count + g.L + 1), tok, id, tokens);
         if (id < 0) return;
-    } else {
-        if (index >= *g.n_tiles) return;
-        const int4 t = g.tiles[index];
-        id = t.x;
-        tokens = t.z;
-        if (tid < S::kTok) tok[tid] = tid < tokens ? g.order[t.y + tid] : -1;
-        __syncthreads();
     }
-    int rank = 0;
-    if (id < g.L) {
-        rank = g.ranks ? __ldg(g.ranks + id) : g.R;
-        if (rank < 0 || rank > g.R) {
-            report(g.status, TWELL_ERR_DEVICE_CHECK);
-            rank = 0;
-        }
-    }
+    const int rank = lora_rank(g, id);
     const int nt_all = (g.n + 31) / 32, nt0 = static_cast<int>(static_cast<long long>(nt_all) * part / blocks),
               nt1 = static_cast<int>(static_cast<long long>(nt_all) * (part + 1) / blocks);
     if (rank == 0) {  // the same for all blocks of the cluster
@@ -179,118 +321,58 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_kernel(con
     }
     if (blocks > 1) cluster_arrive();  // this block runs: the others may write to its shared memory
 
-    // t = A x, this block's part of k: a warp has RT times 8 ranks and every kWays-th 64 columns
-    const __nv_bfloat16* A = g.a + static_cast<int64_t>(id) * g.R * g.k;
-    const int rg = warp % RG, way = warp / RG;
-    float acc[MT][RT][4] = {};
-    {
-        const int kb_all = (g.k + 63) / 64, kb0 = static_cast<int>(static_cast<long long>(kb_all) * part / blocks),
-                  kb1 = static_cast<int>(static_cast<long long>(kb_all) * (part + 1) / blocks);
-        const __nv_bfloat16* xrow[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int t = tok[16 * m + 8 * s + gr];
-                xrow[m][s] = t >= 0 ? g.x + t * g.ldx : nullptr;
-            }
-        const int row0 = rg * RT * 8 + gr;
-        for (int kb = kb0 + way; kb < kb1 && rg * RT * 8 < rank; kb += S::kWays) {
-            uint4 xv[2][MT][2], wv[2][RT];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int col = 64 * kb + 32 * h + 8 * c;
-                const bool in = col < g.k;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    wv[h][r] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && row0 + 8 * r < rank) wv[h][r] = ldg_stream16(A + static_cast<int64_t>(row0 + 8 * r) * g.k + col);
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        xv[h][m][s] = make_uint4(0u, 0u, 0u, 0u);
-                        if (in && xrow[m][s] != nullptr) xv[h][m][s] = __ldg(reinterpret_cast<const uint4*>(xrow[m][s] + col));
-                    }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const uint4 &u = xv[h][m][0], &v = xv[h][m][1], &w = wv[h][r];
-                        mma_bf16(acc[m][r], u.x, v.x, u.y, v.y, w.x, w.y);
-                        mma_bf16(acc[m][r], u.z, v.z, u.w, v.w, w.z, w.w);
-                    }
-        }
-    }
-
-    // y + B t, this block's part of n: a warp has every kLoraWarps-th 32 columns. The weights of its first ones are on their
-    // way while t is put together.
-    const __nv_bfloat16* B = g.b + static_cast<int64_t>(id) * g.n * g.R;
-    constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4, kWords = kPer / 2;
-    uint32_t bw[kKb][4][kWords];
-    auto load_b = [&](int nt) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int col = 32 * nt + 8 * (gr >> 1);
-            const __nv_bfloat16* row = B + static_cast<int64_t>(col + 2 * u + (gr & 1)) * g.R;
-#pragma unroll
-            for (int kb = 0; kb < kKb; ++kb) {
-                const int r0 = kb * S::kBlock + kPer * c;
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) bw[kb][u][w] = 0u;
-                if (col < g.n && r0 < rank) {
-                    if constexpr (kWords == 4) {
-                        const uint4 v = ldg_stream16(row + r0);
-                        bw[kb][u][0] = v.x, bw[kb][u][1] = v.y, bw[kb][u][2] = v.z, bw[kb][u][3] = v.w;
-                    } else {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + r0));
-                        bw[kb][u][0] = v.x, bw[kb][u][1] = v.y;
-                    }
-                }
-            }
-        }
-    };
-    // what lies past the rank counts for nothing, whatever it is
-    auto mask_b = [&] {
-        if (rank % kPer == 0) return;
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb)
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                const int left = rank - (kb * S::kBlock + kPer * c + 2 * w);
-                const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) bw[kb][u][w] &= keep;
-            }
-    };
-    if (nt0 + warp < nt1) load_b(nt0 + warp);
-
-    float* sums = lora_smem;
-    float* recv = lora_smem + S::kWarpSums;
+    int token[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            float* p = sums + way * S::kSum + (16 * m + gr) * S::kPitch + 8 * (rg * RT + r) + 2 * c;
-            *reinterpret_cast<float2*>(p) = make_float2(acc[m][r][0], acc[m][r][1]);
-            *reinterpret_cast<float2*>(p + 8 * S::kPitch) = make_float2(acc[m][r][2], acc[m][r][3]);
+        for (int s = 0; s < 2; ++s) token[m][s] = tok[16 * m + 8 * s + gr];
+    uint8_t* const ring_at = lora_smem + warp * S::kRing;
+    const uint32_t mine = smem_u32(ring_at) + lane * 16;
+
+    // y + B t, this block's part of n: a warp has every kLoraWarps-th 32 columns, of which the first are on their way while t is
+    // put together
+    constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4;  // ranks a lane takes at a time
+    const int out_stages = nt0 + warp < nt1 ? (nt1 - nt0 - warp + kLoraWarps - 1) / kLoraWarps : 0;
+    const __nv_bfloat16* B = g.b + static_cast<int64_t>(id) * g.n * g.R;
+    auto request_out = [&](int i, int slot) {
+        if (i < out_stages) {
+            const int base = 32 * (nt0 + warp + i * kLoraWarps), col = base + 8 * c, brow = base + 8 * (gr >> 1);
+            const uint32_t at = mine + S::kWarpSums + slot * S::kOut;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bool live = col < g.n && token[m][s] >= 0;
+                    copy16(at + (2 * m + s) * 512, live ? g.y + token[m][s] * g.ldy + col : g.y, live ? 16 : 0);
+                }
+#pragma unroll
+            for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    // what lies past the rank becomes zeros, whatever it is
+                    const int r0 = kb * S::kBlock + kPer * c, live = brow < g.n ? min(max(rank - r0, 0), kPer) : 0;
+                    const __nv_bfloat16* from = live ? B + static_cast<int64_t>(brow + 2 * u + (gr & 1)) * g.R + r0 : g.b;
+                    const uint32_t to = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
+                    if constexpr (kPer == 8) copy16(to, from, 2 * live);
+                    else copy8(to - lane * 8, from, 2 * live);
+                }
         }
+        copies_end();
+    };
+    const float scale = __ldg(g.scale + id);
+    lora_shrink<S, MT, RG, RT>(g, id, rank, part, blocks, token, ring_at, [&] {
+#pragma unroll
+        for (int i = 0; i < S::kOutStages; ++i) request_out(i, i);
+    });
     __syncthreads();
     if (blocks > 1) cluster_wait();
+    uint4* frags = reinterpret_cast<uint4*>(lora_smem + kLoraWarps * S::kRing);
+    float* recv = reinterpret_cast<float*>(lora_smem + kLoraWarps * S::kRing + S::kFragBytes);
     constexpr int kQuads = S::kRanks / 4;
     for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads) {
-        const int at = i / kQuads * S::kPitch + i % kQuads * 4;
-        float4 v = *reinterpret_cast<const float4*>(sums + at);
-#pragma unroll
-        for (int w = 1; w < S::kWays; ++w) {
-            const float4 u = *reinterpret_cast<const float4*>(sums + w * S::kSum + at);
-            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        }
-        float* to = recv + part * S::kSum + at;
+        const int row = i / kQuads, quad = i % kQuads;
+        const float4 v = lora_sum<S, RG>(lora_smem, row, quad);
+        float* to = recv + part * S::kSum + row * S::kPitch + quad * 4;
         if (blocks == 1) {
             *reinterpret_cast<float4*>(to) = v;
         } else {
@@ -304,145 +386,318 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_kernel(con
         __syncthreads();
     }
     // t, whole, under its scale, as the second product's fragments: [row tile][16 ranks][hi, lo][lane]
-    uint4* frags = reinterpret_cast<uint4*>(sums);
-    const float scale = __ldg(g.scale + id);
     for (int i = tid; i < MT * S::kFrags * 32; i += kLoraThreads) {
         const int l = i & 31, f = (i >> 5) % S::kFrags, m = (i >> 5) / S::kFrags;
         constexpr int kHalves = S::kBlock / 16;
         const int r0 = f / kHalves * S::kBlock + kPer * (l & 3) + 4 * (f % kHalves);
         const float* p = recv + (16 * m + (l >> 2)) * S::kPitch + r0;
-        float4 v[2];
+        uint4 t[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            v[s] = *reinterpret_cast<const float4*>(p + s * 8 * S::kPitch);
+            float4 v = *reinterpret_cast<const float4*>(p + s * 8 * S::kPitch);
             for (int d = 1; d < blocks; ++d) {
                 const float4 u = *reinterpret_cast<const float4*>(p + d * S::kSum + s * 8 * S::kPitch);
-                v[s].x += u.x, v[s].y += u.y, v[s].z += u.z, v[s].w += u.w;
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
-            // past the rank a row of zeros met x, which is NaN where x is infinite
-            v[s].x = r0 < rank ? v[s].x * scale : 0.0f;
-            v[s].y = r0 + 1 < rank ? v[s].y * scale : 0.0f;
-            v[s].z = r0 + 2 < rank ? v[s].z * scale : 0.0f;
-            v[s].w = r0 + 3 < rank ? v[s].w * scale : 0.0f;
+            t[s] = lora_parts(v, r0, rank, scale);
         }
-        uint4 hi, lo;
-        split2(v[0].x, v[0].y, hi.x, lo.x);
-        split2(v[1].x, v[1].y, hi.y, lo.y);
-        split2(v[0].z, v[0].w, hi.z, lo.z);
-        split2(v[1].z, v[1].w, hi.w, lo.w);
-        frags[((m * S::kFrags + f) * 2 + 0) * 32 + l] = hi;
-        frags[((m * S::kFrags + f) * 2 + 1) * 32 + l] = lo;
+        frags[((m * S::kFrags + f) * 2 + 0) * 32 + l] = make_uint4(t[0].x, t[1].x, t[0].y, t[1].y);
+        frags[((m * S::kFrags + f) * 2 + 1) * 32 + l] = make_uint4(t[0].z, t[1].z, t[0].w, t[1].w);
     }
     __syncthreads();
 
+    int slot = 0;
+    for (int i = 0; i < out_stages; ++i) {
+        copies_wait<S::kOutStages - 1>();
+        const uint32_t at = mine + S::kWarpSums + slot * S::kOut;
+        const int col = 32 * (nt0 + warp + i * kLoraWarps) + 8 * c;
+        float d[MT][4][4] = {};
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb) {
+            if (kb * S::kBlock >= rank) break;
+            uint4 bw[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t from = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
+                if constexpr (kPer == 8) {
+                    bw[u] = lds16(from);
+                } else {
+                    const uint2 v = lds8(from - lane * 8);
+                    bw[u] = make_uint4(v.x, v.y, 0u, 0u);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < S::kBlock / 16; ++h)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const uint4 a = frags[((m * S::kFrags + kb * (S::kBlock / 16) + h) * 2 + p) * 32 + lane];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            mma_bf16(d[m][u], a.x, a.y, a.z, a.w, h ? bw[u].z : bw[u].x, h ? bw[u].w : bw[u].y);
+                    }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float v[8];
+                unpack16(lds16(at + (2 * m + s) * 512), v, static_cast<__nv_bfloat16*>(nullptr));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    v[2 * u] += d[m][u][2 * s];
+                    v[2 * u + 1] += d[m][u][2 * s + 1];
+                }
+                if (col < g.n && token[m][s] >= 0) store8(g.out + token[m][s] * g.ldo + col, v);
+            }
+        request_out(i + S::kOutStages, slot);
+        slot = slot + 1 == S::kOutStages ? 0 : slot + 1;
+    }
+    copies_wait<0>();
+}
+
+// t of a larger batch: a tile's rows of it, as lora_parts has them, at the tokens' places in `order`. A cluster of blocks shares a
+// tile's k where tiles are few; each then adds up a share of the sums.
+template <int MT, int RG, int RT>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out)
+{
+    using S = LoraShape<MT, RG, RT, false>;
+    extern __shared__ __align__(16) uint8_t lora_smem[];
+    pdl_begin();
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2;
+    const int blocks = static_cast<int>(cluster_blocks()), part = static_cast<int>(cluster_ctarank());
+    const int index = static_cast<int>(blockIdx.x) / blocks;
+    if (index >= *g.n_tiles) return;
+    const int4 tile = g.tiles[index];
+    const int rank = lora_rank(g, tile.x);
+    if (rank == 0) return;
+    if (blocks > 1) cluster_arrive();
     int token[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) token[m][s] = tok[16 * m + 8 * s + gr];
-    for (int nt = nt0 + warp; nt < nt1; nt += kLoraWarps) {
-        const int col = 32 * nt + 8 * c;
-        uint4 yv[MT][2];
+        for (int s = 0; s < 2; ++s) {
+            const int i = 16 * m + 8 * s + gr;
+            token[m][s] = i < tile.z ? __ldg(g.order + tile.y + i) : -1;
+        }
+    const float scale = __ldg(g.scale + tile.x);
+    lora_shrink<S, MT, RG, RT>(g, tile.x, rank, part, blocks, token, lora_smem + warp * S::kRing, [] {});
+    __syncthreads();
+    constexpr int kQuads = S::kRanks / 4;
+    auto store = [&](int row, int quad, const float4& v) {
+        if (row < tile.z) t_out[static_cast<size_t>(tile.y + row) * kQuads + quad] = lora_parts(v, 4 * quad, rank, scale);
+    };
+    if (blocks == 1) {
+        for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads)
+            store(i / kQuads, i % kQuads, lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads));
+        return;
+    }
+    // quad i is added up by block i % blocks
+    float4* recv = reinterpret_cast<float4*>(lora_smem + kLoraWarps * S::kRing);
+    const int share = S::kTok * kQuads / blocks;
+    cluster_wait();
+    for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads)
+        st_cluster16(mapa_shared(smem_u32(recv + part * share + i / blocks), i % blocks), lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads));
+    cluster_arrive();
+    cluster_wait();
+    for (int j = tid; j < share; j += kLoraThreads) {
+        const int i = j * blocks + part;
+        float4 v = recv[j];
+        for (int d = 1; d < blocks; ++d) {
+            const float4 u = recv[d * share + j];
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        store(i / kQuads, i % kQuads, v);
+    }
+}
+
+// y + B t of a larger batch: a block has a tile's rows and 32 NT columns a warp, all of whose values are requested at once.
+template <int MT, int RG, int RT, int NT>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArgs g, const uint4* __restrict__ t_in, int most_tiles)
+{
+    using S = LoraShape<MT, RG, RT, false>;
+    pdl_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, c = lane & 3;
+    const int index = static_cast<int>(blockIdx.x % static_cast<unsigned>(most_tiles));
+    const int base = (static_cast<int>(blockIdx.x / static_cast<unsigned>(most_tiles)) * kLoraWarps + warp) * 32 * NT;
+    if (index >= *g.n_tiles || base >= g.n) return;
+    const int4 tile = g.tiles[index];
+    const int rank = lora_rank(g, tile.x);
+    if (rank == 0 && g.y == g.out) return;
+    int token[MT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (col < g.n && token[m][s] >= 0) yv[m][s] = *reinterpret_cast<const uint4*>(g.y + token[m][s] * g.ldy + col);
-        if (nt != nt0 + warp) load_b(nt);
-        mask_b();
-        float d[MT][4][4] = {};
+        for (int s = 0; s < 2; ++s) {
+            const int i = 16 * m + 8 * s + gr;
+            token[m][s] = i < tile.z ? __ldg(g.order + tile.y + i) : -1;
+        }
+    // the weights
+    constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4, kWords = kPer / 2;
+    uint32_t bw[NT][kKb][4][kWords];
+    const __nv_bfloat16* B = g.b + static_cast<int64_t>(tile.x) * g.n * g.R;
 #pragma unroll
-        for (int f = 0; f < S::kFrags; ++f) {
-            constexpr int kHalves = S::kBlock / 16;
-            const int kb = f / kHalves, h = f % kHalves;
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int brow = base + 32 * q + 8 * (gr >> 1);
+            const __nv_bfloat16* row = B + static_cast<int64_t>(brow + 2 * u + (gr & 1)) * g.R + kPer * c;
+#pragma unroll
+            for (int kb = 0; kb < kKb; ++kb) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (brow < g.n && kb * S::kBlock + kPer * c < rank) {
+                    if constexpr (kWords == 4) {
+                        v = __ldg(reinterpret_cast<const uint4*>(row + kb * S::kBlock));
+                    } else {
+                        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + kb * S::kBlock));
+                        v.x = w.x, v.y = w.y;
+                    }
+                }
+                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) bw[q][kb][u][w] = words[w];
+            }
+        }
+    uint4 yv[MT][2][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+                if (token[m][s] >= 0 && base + 32 * q + 8 * c < g.n)
+                    yv[m][s][q] = *reinterpret_cast<const uint4*>(g.y + token[m][s] * g.ldy + base + 32 * q + 8 * c);
+    if (rank % kPer != 0) {  // what lies past the rank counts for nothing, whatever it is
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                const int left = rank - (kb * S::kBlock + kPer * c + 2 * w);
+                const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+#pragma unroll
+                for (int q = 0; q < NT; ++q)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) bw[q][kb][u][w] &= keep;
+            }
+    }
+    constexpr int kQuads = S::kRanks / 4;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        float d[NT][4][4] = {};
+        const uint4* t0 = t_in + static_cast<size_t>(tile.y + min(16 * m + gr, tile.z - 1)) * kQuads + kPer / 4 * c;
+        const uint4* t1 = t_in + static_cast<size_t>(tile.y + min(16 * m + 8 + gr, tile.z - 1)) * kQuads + kPer / 4 * c;
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb) {
             if (kb * S::kBlock >= rank) break;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int h = 0; h < S::kBlock / 16; ++h) {
+                const uint4 p = __ldg(t0 + kb * (S::kBlock / 4) + h), r = __ldg(t1 + kb * (S::kBlock / 4) + h);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const uint4 a = frags[((m * S::kFrags + f) * 2 + p) * 32 + lane];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) mma_bf16(d[m][u], a.x, a.y, a.z, a.w, bw[kb][u][2 * h], bw[kb][u][2 * h + 1]);
-                }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (col < g.n && token[m][s] >= 0) {
-                    float v[8];
-                    unpack16(yv[m][s], v, static_cast<__nv_bfloat16*>(nullptr));
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        v[2 * u] += d[m][u][2 * s];
-                        v[2 * u + 1] += d[m][u][2 * s + 1];
+                        mma_bf16(d[q][u], p.x, r.x, p.y, r.y, bw[q][kb][u][2 * h], bw[q][kb][u][2 * h + 1]);
+                        mma_bf16(d[q][u], p.z, r.z, p.w, r.w, bw[q][kb][u][2 * h], bw[q][kb][u][2 * h + 1]);
                     }
-                    store8(g.out + token[m][s] * g.ldo + col, v);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                const int col = base + 32 * q + 8 * c;
+                if (token[m][s] < 0 || col >= g.n) continue;
+                if (rank > 0) {
+                    float v[8];
+                    unpack16(yv[m][s][q], v, static_cast<__nv_bfloat16*>(nullptr));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        v[2 * u] += d[q][u][2 * s];
+                        v[2 * u + 1] += d[q][u][2 * s + 1];
+                    }
+                    yv[m][s][q] = pack16(v, static_cast<__nv_bfloat16*>(nullptr));
                 }
+                *reinterpret_cast<uint4*>(g.out + token[m][s] * g.ldo + col) = yv[m][s][q];
+            }
     }
 }
 
 // The tiles of a larger batch: tokens counted by adapter, each adapter's given adjacent places in `order`, and a tile for each
-// TOK of these. One block: the counts are in its shared memory, and 16384 ids are 64 KB. Which token of an adapter comes
-// first is left to chance; a token's result does not depend on it.
-template <int TOK>
-__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int32_t* n_tiles, int4* tiles, int32_t* order)
+// tile_tokens of these. One block: the counts are in its shared memory, and a pass's ids are 64 KB, all requested before the
+// first is counted. Which token of an adapter comes first is left to chance; a token's result does not depend on it.
+__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int tile_tokens, int32_t* n_tiles,
+                                                                       int4* tiles, int32_t* order)
 {
-    extern __shared__ int count[];  // [L + 1] of tokens, then their first place
-    __shared__ int warp_sum[2][32];
+    constexpr int kPer = kLoraPass / kLoraGroupThreads;  // tokens a thread
+    extern __shared__ int count[];                       // [L + 1] of tokens, then their first place; [L + 1] of the first tiles
+    __shared__ int warp_sum[2][32], s_tiles;
     pdl_begin();
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    int* first_tile = count + g.L + 1;
+    int v[kPer];
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) v[r] = r * kLoraGroupThreads + tid < g.N ? __ldg(g.ids + r * kLoraGroupThreads + tid) : INT32_MIN;
     for (int i = tid; i <= g.L; i += kLoraGroupThreads) count[i] = 0;
     __syncthreads();
-    // every warp takes 32 tokens at a time; equal ids are counted by one lane
-    const int rounds = (g.N + kLoraGroupThreads - 1) / kLoraGroupThreads;
-    for (int r = 0; r < rounds; ++r) {
-        const int i = r * kLoraGroupThreads + tid;
-        const int id = i < g.N ? lora_id(g, g.ids[i]) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, id);
-        if (id >= 0 && (same & ((1u << lane) - 1)) == 0) atomicAdd(count + id, __popc(same));
+    // a token's number among those of its adapter; equal ids of a warp are counted by one lane
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+        if (r * kLoraGroupThreads >= g.N) break;
+        const bool live = r * kLoraGroupThreads + tid < g.N;
+        const int id = live ? lora_id(g, v[r]) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, id), below = same & ((1u << lane) - 1);
+        int first = 0;
+        if (live && below == 0) first = atomicAdd(count + id, __popc(same));
+        first = __shfl_sync(0xffffffffu, first, __ffs(same) - 1);
+        v[r] = live ? (id << 16) | (first + __popc(below)) : -1;  // at most 4096 adapters and 2^15 tokens
     }
     __syncthreads();
-    const int per = (g.L + 1 + kLoraGroupThreads - 1) / kLoraGroupThreads, l0 = tid * per;
+    const int per = (g.L + kLoraGroupThreads) / kLoraGroupThreads, l0 = tid * per, l1 = min(l0 + per, g.L + 1);
     int sum = 0, tsum = 0;
-    for (int l = l0; l < min(l0 + per, g.L + 1); ++l) {
+    for (int l = l0; l < l1; ++l) {
         sum += count[l];
-        tsum += (count[l] + TOK - 1) / TOK;
+        tsum += (count[l] + tile_tokens - 1) / tile_tokens;
     }
     int incl = sum, tincl = tsum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, tincl, o);
-        if (lane >= o) incl += u, tincl += v;
+        const int u = __shfl_up_sync(0xffffffffu, incl, o), w = __shfl_up_sync(0xffffffffu, tincl, o);
+        if (lane >= o) incl += u, tincl += w;
     }
     if (lane == 31) warp_sum[0][warp] = incl, warp_sum[1][warp] = tincl;
     __syncthreads();
     int w = warp_sum[0][lane], tw = warp_sum[1][lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, w, o), v = __shfl_up_sync(0xffffffffu, tw, o);
-        if (lane >= o) w += u, tw += v;
+        const int u = __shfl_up_sync(0xffffffffu, w, o), x = __shfl_up_sync(0xffffffffu, tw, o);
+        if (lane >= o) w += u, tw += x;
     }
     const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0)), tbefore = __shfl_sync(0xffffffffu, tw, max(warp - 1, 0));
     int at = incl - sum + (warp ? before : 0), tile = tincl - tsum + (warp ? tbefore : 0);
-    for (int l = l0; l < min(l0 + per, g.L + 1); ++l) {
+    for (int l = l0; l < l1; ++l) {
         const int have = count[l];
         count[l] = at;
-        for (int i = 0; i < have; i += TOK) tiles[tile++] = make_int4(l, at + i, min(TOK, have - i), 0);
+        first_tile[l] = tile;
         at += have;
+        tile += (have + tile_tokens - 1) / tile_tokens;
     }
-    if (tid == kLoraGroupThreads - 1) *n_tiles = tile;
+    if (tid == kLoraGroupThreads - 1) *n_tiles = s_tiles = tile;
     __syncthreads();
-    for (int r = 0; r < rounds; ++r) {
-        const int i = r * kLoraGroupThreads + tid;
-        const int v = i < g.N ? g.ids[i] : -1;
-        const int id = i < g.N ? (v >= 0 && v < g.L ? v : g.L) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, id);
-        const unsigned below = same & ((1u << lane) - 1);
-        int first = 0;
-        if (id >= 0 && below == 0) first = atomicAdd(count + id, __popc(same));
-        first = __shfl_sync(0xffffffffu, first, __ffs(same) - 1);
-        if (id >= 0) order[first + __popc(below)] = i;
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+        if (r * kLoraGroupThreads >= g.N) break;
+        if (v[r] >= 0) order[count[v[r] >> 16] + (v[r] & 0xffff)] = r * kLoraGroupThreads + tid;
+    }
+    for (int j = tid; j < s_tiles; j += kLoraGroupThreads) {
+        int l = 0, len = g.L + 1;  // the last adapter whose tiles begin at j or before
+        while (len > 1) {
+            const int half = len >> 1;
+            if (first_tile[l + half] <= j) l += half;
+            len -= half;
+        }
+        const int from = count[l] + (j - first_tile[l]) * tile_tokens;
+        tiles[j] = make_int4(l, from, min(tile_tokens, (l < g.L ? count[l + 1] : g.N) - from), 0);
     }
 }
 
@@ -454,8 +709,8 @@ int lora_blocks(long long tiles, int sms, int most)
     return b;
 }
 
-template <typename K>
-twell_status launch_lora(K kern, int clusters, int blocks, size_t smem, cudaStream_t s, const LoraArgs& g)
+template <typename... KArgs, typename... Args>
+twell_status launch_lora(void (*kern)(KArgs...), int clusters, int blocks, size_t smem, cudaStream_t s, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -470,57 +725,90 @@ twell_status launch_lora(K kern, int clusters, int blocks, size_t smem, cudaStre
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, g) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
-// Most blocks a tile whose sums fit an SM.
-template <int MT, int RG, int RT>
+// Most blocks a tile whose sums fit an SM, and two of them where one block's do.
+template <typename S>
 constexpr int most_blocks()
 {
     int b = kLoraCluster;
-    while (b > 1 && LoraShape<MT, RG, RT>::bytes(b) > (MT == 4 ? 220u : 110u) * 1024u) b /= 2;
+    while (b > 1 && S::bytes(b) > (S::bytes(1) <= 108u * 1024u ? 108u : 222u) * 1024u) b /= 2;
     return b;
 }
 
-template <int MT, int RG, int RT, bool SMALL>
-twell_status run_lora(const LoraArgs& g, int clusters, int sms, cudaStream_t s)
-{
-    using S = LoraShape<MT, RG, RT>;
-    constexpr int kMost = most_blocks<MT, RG, RT>();
-    // the small batches' counts and numbers share the memory of the sums
-    constexpr size_t kFind = SMALL ? sizeof(int) * (kLoraMaxAdapters + 1) + sizeof(uint16_t) * kLoraSmallN : 0;
-    const int blocks = SMALL ? kMost : lora_blocks(g.N / S::kTok, sms, kMost);
-    const size_t find = SMALL ? sizeof(int) * (g.L + 1) + sizeof(uint16_t) * kLoraSmallN : 0;
-    auto kern = lora_kernel<MT, RG, RT, SMALL>;
-    static std::atomic<uint64_t> allowed{0};
-    if (twell_host::allow_smem(kern, std::max(S::bytes(kMost), kFind), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    return launch_lora(kern, clusters, blocks, std::max(S::bytes(blocks), find), s, g);
-}
-
-template <int MT, bool SMALL>
-twell_status run_rank(const LoraArgs& g, int clusters, int sms, cudaStream_t s)
-{
-    if (g.R <= 16) return run_lora<MT, 1, 2, SMALL>(g, clusters, sms, s);
-    if (g.R <= 32) return run_lora<MT, 1, 4, SMALL>(g, clusters, sms, s);
-    if (g.R <= 64) return run_lora<MT, 2, 4, SMALL>(g, clusters, sms, s);
-    return run_lora<MT, 4, 4, SMALL>(g, clusters, sms, s);
-}
-
-constexpr int kLoraMT = 4;
 // Tiles of N tokens, at most.
 long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / tok + std::min(N, L + 1)); }
-// The workspace: the number of tiles, the tiles, the tokens' order.
-size_t lora_order_at(int N) { return 16 + 16 * static_cast<size_t>(lora_tiles(N, kLoraMaxAdapters, 16 * kLoraMT)); }
+
+template <int RG, int RT>
+twell_status run_small(const LoraArgs& g, int sms, cudaStream_t s)
+{
+    using S = LoraShape<1, RG, RT, true>;
+    constexpr int kMost = most_blocks<S>();
+    constexpr size_t kFind = sizeof(int) * (kLoraMaxAdapters + 1) + sizeof(uint16_t) * kLoraSmallN;
+    static_assert(kFind <= kLoraWarps * S::kRing, "the counts and numbers lie where the rings come later");
+    const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
+    int blocks = kMost;
+    while (blocks > 1 && tiles * blocks > 2 * sms - sms / 8) blocks /= 2;
+    auto kern = lora_kernel<1, RG, RT>;
+    static std::atomic<uint64_t> allowed{0};
+    if (twell_host::allow_smem(kern, S::bytes(kMost), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    return launch_lora(kern, tiles, blocks, S::bytes(blocks), s, g);
+}
+
+// Of the larger batches: 16-token rows of a tile; what the workspace holds of a pass.
+constexpr int kLoraMT = 2;
+constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+struct LoraWs {
+    size_t tiles, order, t, total;
+    LoraWs(int N, int R)
+    {
+        const int n = std::min(N, kLoraPass);
+        tiles = 16;
+        order = tiles + 16 * static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, 16 * kLoraMT));
+        t = (order + sizeof(int32_t) * static_cast<size_t>(n) + 15) / 16 * 16;
+        total = t + static_cast<size_t>(n) * lora_ranks(R) * 4;
+    }
+};
+
+template <int RG, int RT, int NT>
+twell_status run_pass(LoraArgs g, uint8_t* ws, int sms, cudaStream_t s)
+{
+    using S = LoraShape<kLoraMT, RG, RT, false>;
+    const LoraWs at(g.N, g.R);
+    int32_t* n_tiles = reinterpret_cast<int32_t*>(ws);
+    int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
+    int32_t* order = reinterpret_cast<int32_t*>(ws + at.order);
+    uint4* t = reinterpret_cast<uint4*>(ws + at.t);
+    twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g, S::kTok,
+                                             n_tiles, tiles, order);
+    if (st != TWELL_OK) return st;
+    g.n_tiles = n_tiles;
+    g.tiles = tiles;
+    g.order = order;
+    const int most = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
+    constexpr int kMost = most_blocks<S>();
+    const int blocks = lora_blocks(g.N / S::kTok, sms, kMost);
+    auto in = lora_in_kernel<kLoraMT, RG, RT>;
+    static std::atomic<uint64_t> allowed{0};
+    if (twell_host::allow_smem(in, S::bytes(kMost), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t);
+    if (st != TWELL_OK) return st;
+    constexpr int kCols = 32 * NT * kLoraWarps;
+    const long long out_blocks = static_cast<long long>(most) * ((g.n + kCols - 1) / kCols);
+    if (out_blocks > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
+    return twell_host::launch_dep(lora_out_kernel<kLoraMT, RG, RT, NT>, dim3(static_cast<unsigned>(out_blocks)), dim3(kLoraThreads), 0, s,
+                                  g, t, most);
+}
 
 }  // namespace
 }  // namespace twell
 
 using namespace twell_host;
 
-size_t twell_host::lora_ws_bytes(int N)
+size_t twell_host::lora_ws_bytes(int N, int R)
 {
-    if (N <= twell::kLoraSmallN) return 0;
-    return (twell::lora_order_at(N) + sizeof(int32_t) * static_cast<size_t>(N) + 15) / 16 * 16;
+    return N <= twell::kLoraSmallN || R > twell::kLoraMaxRank ? 0 : twell::LoraWs(N, R).total;
 }
 
 extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const twell_adapters* ad,
@@ -545,7 +833,7 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
         if (reinterpret_cast<uintptr_t>(p) % sizeof(int32_t) != 0) return TWELL_ERR_INVALID;
     if (ldy % 8 != 0 || ldx % 8 != 0 || ldo % 8 != 0 || ldy < ad->n || ldx < ad->k || ldo < ad->n) return TWELL_ERR_INVALID;
     if ((y == out && ldy != ldo) || x == out) return TWELL_ERR_INVALID;
-    const size_t need_ws = lora_ws_bytes(N);
+    const size_t need_ws = lora_ws_bytes(N, ad->rank);
     if (need_ws > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need_ws)) return TWELL_ERR_WORKSPACE;
     using bf = __nv_bfloat16;
     DevInfo dev;
@@ -555,17 +843,23 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
                          static_cast<const bf*>(y), static_cast<bf*>(out), ad->scale, ad->ranks, ids, dev_status,
                          ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, nullptr, nullptr, nullptr};
     if (N <= twell::kLoraSmallN)
-        return twell::run_rank<twell::kLoraSmallMT, true>(
-            g, static_cast<int>(twell::lora_tiles(N, g.L, 16 * twell::kLoraSmallMT)), dev.sm_count, s);
-    constexpr int kTok = 16 * twell::kLoraMT;
-    int32_t* n_tiles = static_cast<int32_t*>(ws);
-    int4* tiles = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + 16);
-    int32_t* order = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + twell::lora_order_at(N));
-    const twell_status st = launch_dep(twell::lora_group_kernel<kTok>, dim3(1), dim3(twell::kLoraGroupThreads),
-                                       sizeof(int) * (g.L + 1), s, g, n_tiles, tiles, order);
-    if (st != TWELL_OK) return st;
-    g.n_tiles = n_tiles;
-    g.tiles = tiles;
-    g.order = order;
-    return twell::run_rank<twell::kLoraMT, false>(g, static_cast<int>(twell::lora_tiles(N, g.L, kTok)), dev.sm_count, s);
+        return ad->rank <= 16   ? twell::run_small<1, 2>(g, dev.sm_count, s)
+               : ad->rank <= 32 ? twell::run_small<1, 4>(g, dev.sm_count, s)
+               : ad->rank <= 64 ? twell::run_small<2, 4>(g, dev.sm_count, s)
+                                : twell::run_small<4, 4>(g, dev.sm_count, s);
+    for (int at = 0; at < N; at += twell::kLoraPass) {
+        twell::LoraArgs p = g;
+        p.N = N - at < twell::kLoraPass ? N - at : twell::kLoraPass;
+        p.ids += at;
+        p.x += at * ldx;
+        p.y += at * ldy;
+        p.out += at * ldo;
+        uint8_t* w = static_cast<uint8_t*>(ws);
+        const twell_status st = ad->rank <= 16   ? twell::run_pass<1, 2, 2>(p, w, dev.sm_count, s)
+                                : ad->rank <= 32 ? twell::run_pass<1, 4, 2>(p, w, dev.sm_count, s)
+                                : ad->rank <= 64 ? twell::run_pass<2, 4, 1>(p, w, dev.sm_count, s)
+                                                 : twell::run_pass<4, 4, 1>(p, w, dev.sm_count, s);
+        if (st != TWELL_OK) return st;
+    }
+    return TWELL_OK;
 }

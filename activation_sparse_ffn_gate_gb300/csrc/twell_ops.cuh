@@ -160,7 +160,7 @@ namespace twell_host {
 // twell_lora_add (twell_lora.cu).
 size_t norm_bwd_ws_bytes(int N, int d);
 size_t paged_attn_ws_bytes(int B, int hd);
-size_t lora_ws_bytes(int N);
+size_t lora_ws_bytes(int N, int rank);
 
 // Allow `kern` up to `bytes` of dynamic shared memory, the most that any of its launches takes, on the current
 // device. `done` is the caller's, one for each kernel: a bit for each device it has been allowed on, so that a

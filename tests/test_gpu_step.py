@@ -228,7 +228,7 @@ def test_graphs_beside_calls(cuda_dev):
 
 def test_a_workspace_of_the_callers(cuda_dev):
     call = Lora(cuda_dev, 3)
-    n = binding.twell_workspace_bytes(binding.OP_LORA_ADD, call.x.shape[0], 1, 1)
+    n = binding.twell_workspace_bytes(binding.OP_LORA_ADD, call.x.shape[0], call.ad.a.shape[1], 1)
     ws = torch.full((max(n, 16),), 255, dtype=torch.uint8, device=cuda_dev)  # its contents do not matter
     assert torch.equal(call(ws=ws), call())
 

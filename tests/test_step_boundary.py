@@ -91,7 +91,7 @@ def test_lora_refuses(lib):
 
 
 def test_lora_workspace(lib):
-    ws = lambda N: lib.twell_workspace_bytes(binding.OP_LORA_ADD, N, 1, 1, 0, 0, 0)  # noqa: E731
+    ws = lambda N: lib.twell_workspace_bytes(binding.OP_LORA_ADD, N, 16, 1, 0, 0, 0)  # noqa: E731
     for N in (1, 64, 5000, 1 << 20):
         need = ws(N)
         assert ws(1 << 20) >= need >= ws(0)
