@@ -57,7 +57,7 @@ struct LoraShape {
     static constexpr int kWarpSums = kTok * kWarpRanks * 4;
     // room for three stages of the first product at least, and for kMinOut of the second beside the sums
     static constexpr int kMinOut = RG == 1 ? 2 : 1;
-    static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut) : 12 * 1024;
+    static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut) : (MT == 2 ? 12 : 24) * 1024;
     static constexpr int kInStages = kRing / kIn > 4 ? 4 : kRing / kIn;
     static constexpr int kOutStages = (kRing - kWarpSums) / kOut > 4 ? 4 : (kRing - kWarpSums) / kOut;
     static constexpr int kFragBytes = MT * kFrags * 2 * 512;
@@ -71,6 +71,16 @@ struct LoraShape {
     {
         return token * kWarpRanks + (((rank >> 2) ^ (token & (kWarpRanks / 4 - 1))) << 2) + (rank & 3);
     }
+};
+
+// Of the second product alone.
+template <int MT, int RG, int RT>
+struct LoraOutShape {
+    using In = LoraShape<MT, RG, RT, false>;
+    static constexpr int kRanks = In::kRanks, kBlock = In::kBlock, kFrags = In::kFrags, kStage = In::kOut;
+    static constexpr int kRing = (MT == 2 ? 12 : 24) * 1024;
+    static constexpr int kStages = kRing / kStage;
+    static constexpr size_t kBytes = kLoraWarps * kRing + In::kFragBytes;
 };
 
 // Copies of 16 or 8 bytes of which `bytes` are taken from memory and the rest is zeros.
@@ -289,6 +299,116 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
     return 0;
 }
 
+// y + B t over 32-column pieces nt0, nt0 + 1, ... nt1 - 1 of a block, of which a warp takes every kLoraWarps-th, through STAGES
+// slots of its own at `ring_at`.
+template <int MT, int RG, int RT>
+struct LoraOut {
+    using S = LoraOutShape<MT, RG, RT>;
+    static constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4;  // ranks a lane takes at a time
+    const LoraArgs& g;
+    const __nv_bfloat16* B;
+    const int (&token)[MT][2];
+    uint32_t mine;
+    int rank, first, stages;
+    __device__ __forceinline__ LoraOut(const LoraArgs& g, int id, int rank, int nt0, int nt1, const int (&token)[MT][2], const uint8_t* ring_at)
+        : g(g), B(g.b + static_cast<int64_t>(id) * g.n * g.R), token(token), rank(rank)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        mine = smem_u32(ring_at) + lane * 16;
+        first = nt0 + 2 * warp;
+        const int left = nt1 - first;  // a warp has pieces 0 and 1 of every 2 kLoraWarps
+        stages = left > 0 ? (left - 1) / (2 * kLoraWarps) * 2 + min((left - 1) % (2 * kLoraWarps) + 1, 2) : 0;
+    }
+    __device__ __forceinline__ int column(int i) const { return 32 * (first + (i >> 1) * (2 * kLoraWarps) + (i & 1)); }
+    template <int STAGES>
+    __device__ __forceinline__ void request(int i, int slot) const
+    {
+        if (i < stages) {
+            const int lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+            const int base = column(i), col = base + 8 * c, brow = base + 8 * (gr >> 1);
+            const uint32_t at = mine + slot * S::kStage;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bool live = col < g.n && token[m][s] >= 0;
+                    copy16(at + (2 * m + s) * 512, live ? g.y + token[m][s] * g.ldy + col : g.y, live ? 16 : 0);
+                }
+#pragma unroll
+            for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    // what lies past the rank becomes zeros, whatever it is
+                    const int r0 = kb * S::kBlock + kPer * c, live = brow < g.n ? min(max(rank - r0, 0), kPer) : 0;
+                    const __nv_bfloat16* from = live ? B + static_cast<int64_t>(brow + 2 * u + (gr & 1)) * g.R + r0 : g.b;
+                    const uint32_t to = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
+                    if constexpr (kPer == 8) copy16(to, from, 2 * live);
+                    else copy8(to - lane * 8, from, 2 * live);
+                }
+        }
+        copies_end();
+    }
+    // `frags`: t, [row tile][16 ranks][hi, lo][lane]
+    template <int STAGES>
+    __device__ __forceinline__ void run(const uint4* frags) const
+    {
+        const int lane = threadIdx.x & 31, c = lane & 3;
+        int slot = 0;
+        for (int i = 0; i < stages; ++i) {
+            copies_wait<STAGES - 1>();
+            const uint32_t at = mine + slot * S::kStage;
+            const int col = column(i) + 8 * c;
+            float d[MT][4][4] = {};
+#pragma unroll
+            for (int kb = 0; kb < kKb; ++kb) {
+                if (kb * S::kBlock >= rank) break;
+                uint4 bw[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t from = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
+                    if constexpr (kPer == 8) {
+                        bw[u] = lds16(from);
+                    } else {
+                        const uint2 v = lds8(from - lane * 8);
+                        bw[u] = make_uint4(v.x, v.y, 0u, 0u);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < S::kBlock / 16; ++h)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const uint4 a = frags[((m * S::kFrags + kb * (S::kBlock / 16) + h) * 2 + p) * 32 + lane];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                mma_bf16(d[m][u], a.x, a.y, a.z, a.w, h ? bw[u].z : bw[u].x, h ? bw[u].w : bw[u].y);
+                        }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    uint4 y = lds16(at + (2 * m + s) * 512);
+                    if (rank > 0) {
+                        float v[8];
+                        unpack16(y, v, static_cast<__nv_bfloat16*>(nullptr));
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            v[2 * u] += d[m][u][2 * s];
+                            v[2 * u + 1] += d[m][u][2 * s + 1];
+                        }
+                        y = pack16(v, static_cast<__nv_bfloat16*>(nullptr));
+                    }
+                    if (col < g.n && token[m][s] >= 0) *reinterpret_cast<uint4*>(g.out + token[m][s] * g.ldo + col) = y;
+                }
+            request<STAGES>(i + STAGES, slot);
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+        }
+        copies_wait<0>();
+    }
+};
+
 // A batch of at most kLoraSmallN tokens, whole.
 template <int MT, int RG, int RT>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
@@ -327,42 +447,13 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
 #pragma unroll
         for (int s = 0; s < 2; ++s) token[m][s] = tok[16 * m + 8 * s + gr];
     uint8_t* const ring_at = lora_smem + warp * S::kRing;
-    const uint32_t mine = smem_u32(ring_at) + lane * 16;
 
-    // y + B t, this block's part of n: a warp has every kLoraWarps-th 32 columns, of which the first are on their way while t is
-    // put together
-    constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4;  // ranks a lane takes at a time
-    const int out_stages = nt0 + warp < nt1 ? (nt1 - nt0 - warp + kLoraWarps - 1) / kLoraWarps : 0;
-    const __nv_bfloat16* B = g.b + static_cast<int64_t>(id) * g.n * g.R;
-    auto request_out = [&](int i, int slot) {
-        if (i < out_stages) {
-            const int base = 32 * (nt0 + warp + i * kLoraWarps), col = base + 8 * c, brow = base + 8 * (gr >> 1);
-            const uint32_t at = mine + S::kWarpSums + slot * S::kOut;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const bool live = col < g.n && token[m][s] >= 0;
-                    copy16(at + (2 * m + s) * 512, live ? g.y + token[m][s] * g.ldy + col : g.y, live ? 16 : 0);
-                }
-#pragma unroll
-            for (int kb = 0; kb < kKb; ++kb)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    // what lies past the rank becomes zeros, whatever it is
-                    const int r0 = kb * S::kBlock + kPer * c, live = brow < g.n ? min(max(rank - r0, 0), kPer) : 0;
-                    const __nv_bfloat16* from = live ? B + static_cast<int64_t>(brow + 2 * u + (gr & 1)) * g.R + r0 : g.b;
-                    const uint32_t to = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
-                    if constexpr (kPer == 8) copy16(to, from, 2 * live);
-                    else copy8(to - lane * 8, from, 2 * live);
-                }
-        }
-        copies_end();
-    };
+    // the first pieces of the second product are on their way while t is put together
+    const LoraOut<MT, RG, RT> out(g, id, rank, nt0, nt1, token, ring_at + S::kWarpSums);
     const float scale = __ldg(g.scale + id);
     lora_shrink<S, MT, RG, RT>(g, id, rank, part, blocks, token, ring_at, [&] {
 #pragma unroll
-        for (int i = 0; i < S::kOutStages; ++i) request_out(i, i);
+        for (int i = 0; i < S::kOutStages; ++i) out.template request<S::kOutStages>(i, i);
     });
     __syncthreads();
     if (blocks > 1) cluster_wait();
@@ -389,7 +480,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
     for (int i = tid; i < MT * S::kFrags * 32; i += kLoraThreads) {
         const int l = i & 31, f = (i >> 5) % S::kFrags, m = (i >> 5) / S::kFrags;
         constexpr int kHalves = S::kBlock / 16;
-        const int r0 = f / kHalves * S::kBlock + kPer * (l & 3) + 4 * (f % kHalves);
+        const int r0 = f / kHalves * S::kBlock + S::kBlock / 4 * (l & 3) + 4 * (f % kHalves);
         const float* p = recv + (16 * m + (l >> 2)) * S::kPitch + r0;
         uint4 t[2];
 #pragma unroll
@@ -405,62 +496,13 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
         frags[((m * S::kFrags + f) * 2 + 1) * 32 + l] = make_uint4(t[0].z, t[1].z, t[0].w, t[1].w);
     }
     __syncthreads();
-
-    int slot = 0;
-    for (int i = 0; i < out_stages; ++i) {
-        copies_wait<S::kOutStages - 1>();
-        const uint32_t at = mine + S::kWarpSums + slot * S::kOut;
-        const int col = 32 * (nt0 + warp + i * kLoraWarps) + 8 * c;
-        float d[MT][4][4] = {};
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb) {
-            if (kb * S::kBlock >= rank) break;
-            uint4 bw[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t from = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
-                if constexpr (kPer == 8) {
-                    bw[u] = lds16(from);
-                } else {
-                    const uint2 v = lds8(from - lane * 8);
-                    bw[u] = make_uint4(v.x, v.y, 0u, 0u);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < S::kBlock / 16; ++h)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const uint4 a = frags[((m * S::kFrags + kb * (S::kBlock / 16) + h) * 2 + p) * 32 + lane];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            mma_bf16(d[m][u], a.x, a.y, a.z, a.w, h ? bw[u].z : bw[u].x, h ? bw[u].w : bw[u].y);
-                    }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                float v[8];
-                unpack16(lds16(at + (2 * m + s) * 512), v, static_cast<__nv_bfloat16*>(nullptr));
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    v[2 * u] += d[m][u][2 * s];
-                    v[2 * u + 1] += d[m][u][2 * s + 1];
-                }
-                if (col < g.n && token[m][s] >= 0) store8(g.out + token[m][s] * g.ldo + col, v);
-            }
-        request_out(i + S::kOutStages, slot);
-        slot = slot + 1 == S::kOutStages ? 0 : slot + 1;
-    }
-    copies_wait<0>();
+    out.template run<S::kOutStages>(frags);
 }
 
 // t of a larger batch: a tile's rows of it, as lora_parts has them, at the tokens' places in `order`. A cluster of blocks shares a
 // tile's k where tiles are few; each then adds up a share of the sums.
 template <int MT, int RG, int RT>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out)
+__global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out)
 {
     using S = LoraShape<MT, RG, RT, false>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
@@ -512,16 +554,17 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
     }
 }
 
-// y + B t of a larger batch: a block has a tile's rows and 32 NT columns a warp, all of whose values are requested at once.
-template <int MT, int RG, int RT, int NT>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArgs g, const uint4* __restrict__ t_in, int most_tiles)
+// y + B t of a larger batch: a block has a tile's rows and a part of the columns, of which a warp takes every kLoraWarps-th 32.
+template <int MT, int RG, int RT>
+__global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_out_kernel(const LoraArgs g, const uint4* __restrict__ t_in, int most_tiles)
 {
-    using S = LoraShape<MT, RG, RT, false>;
+    using S = LoraOutShape<MT, RG, RT>;
+    extern __shared__ __align__(16) uint8_t lora_smem[];
     pdl_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, c = lane & 3;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2, c = lane & 3;
     const int index = static_cast<int>(blockIdx.x % static_cast<unsigned>(most_tiles));
-    const int base = (static_cast<int>(blockIdx.x / static_cast<unsigned>(most_tiles)) * kLoraWarps + warp) * 32 * NT;
-    if (index >= *g.n_tiles || base >= g.n) return;
+    const int part = static_cast<int>(blockIdx.x / static_cast<unsigned>(most_tiles)), parts = static_cast<int>(gridDim.x / static_cast<unsigned>(most_tiles));
+    if (index >= *g.n_tiles) return;
     const int4 tile = g.tiles[index];
     const int rank = lora_rank(g, tile.x);
     if (rank == 0 && g.y == g.out) return;
@@ -533,94 +576,30 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
             const int i = 16 * m + 8 * s + gr;
             token[m][s] = i < tile.z ? __ldg(g.order + tile.y + i) : -1;
         }
-    // the weights
-    constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4, kWords = kPer / 2;
-    uint32_t bw[NT][kKb][4][kWords];
-    const __nv_bfloat16* B = g.b + static_cast<int64_t>(tile.x) * g.n * g.R;
+    const int nt_all = (g.n + 31) / 32, nt0 = static_cast<int>(static_cast<long long>(nt_all) * part / parts),
+              nt1 = static_cast<int>(static_cast<long long>(nt_all) * (part + 1) / parts);
+    const LoraOut<MT, RG, RT> out(g, tile.x, rank, nt0, nt1, token, lora_smem + warp * S::kRing);
 #pragma unroll
-    for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int brow = base + 32 * q + 8 * (gr >> 1);
-            const __nv_bfloat16* row = B + static_cast<int64_t>(brow + 2 * u + (gr & 1)) * g.R + kPer * c;
-#pragma unroll
-            for (int kb = 0; kb < kKb; ++kb) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (brow < g.n && kb * S::kBlock + kPer * c < rank) {
-                    if constexpr (kWords == 4) {
-                        v = __ldg(reinterpret_cast<const uint4*>(row + kb * S::kBlock));
-                    } else {
-                        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + kb * S::kBlock));
-                        v.x = w.x, v.y = w.y;
-                    }
-                }
-                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) bw[q][kb][u][w] = words[w];
-            }
-        }
-    uint4 yv[MT][2][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int q = 0; q < NT; ++q)
-                if (token[m][s] >= 0 && base + 32 * q + 8 * c < g.n)
-                    yv[m][s][q] = *reinterpret_cast<const uint4*>(g.y + token[m][s] * g.ldy + base + 32 * q + 8 * c);
-    if (rank % kPer != 0) {  // what lies past the rank counts for nothing, whatever it is
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb)
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                const int left = rank - (kb * S::kBlock + kPer * c + 2 * w);
-                const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-#pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) bw[q][kb][u][w] &= keep;
-            }
-    }
+    for (int i = 0; i < S::kStages; ++i) out.template request<S::kStages>(i, i);
+    // t as the product's fragments
+    uint4* frags = reinterpret_cast<uint4*>(lora_smem + kLoraWarps * S::kRing);
     constexpr int kQuads = S::kRanks / 4;
+    if (rank > 0)
+        for (int i = tid; i < MT * S::kFrags * 32; i += kLoraThreads) {
+            const int l = i & 31, f = (i >> 5) % S::kFrags, m = (i >> 5) / S::kFrags;
+            constexpr int kHalves = S::kBlock / 16, kPer = S::kBlock / 4;
+            const int quad = (f / kHalves * S::kBlock + kPer * (l & 3)) / 4 + f % kHalves, row = 16 * m + (l >> 2);
+            uint4 t[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        float d[NT][4][4] = {};
-        const uint4* t0 = t_in + static_cast<size_t>(tile.y + min(16 * m + gr, tile.z - 1)) * kQuads + kPer / 4 * c;
-        const uint4* t1 = t_in + static_cast<size_t>(tile.y + min(16 * m + 8 + gr, tile.z - 1)) * kQuads + kPer / 4 * c;
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb) {
-            if (kb * S::kBlock >= rank) break;
-#pragma unroll
-            for (int h = 0; h < S::kBlock / 16; ++h) {
-                const uint4 p = __ldg(t0 + kb * (S::kBlock / 4) + h), r = __ldg(t1 + kb * (S::kBlock / 4) + h);
-#pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        mma_bf16(d[q][u], p.x, r.x, p.y, r.y, bw[q][kb][u][2 * h], bw[q][kb][u][2 * h + 1]);
-                        mma_bf16(d[q][u], p.z, r.z, p.w, r.w, bw[q][kb][u][2 * h], bw[q][kb][u][2 * h + 1]);
-                    }
+            for (int s = 0; s < 2; ++s) {
+                t[s] = make_uint4(0u, 0u, 0u, 0u);
+                if (row + 8 * s < tile.z) t[s] = __ldg(t_in + static_cast<size_t>(tile.y + row + 8 * s) * kQuads + quad);
             }
+            frags[((m * S::kFrags + f) * 2 + 0) * 32 + l] = make_uint4(t[0].x, t[1].x, t[0].y, t[1].y);
+            frags[((m * S::kFrags + f) * 2 + 1) * 32 + l] = make_uint4(t[0].z, t[1].z, t[0].w, t[1].w);
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int q = 0; q < NT; ++q) {
-                const int col = base + 32 * q + 8 * c;
-                if (token[m][s] < 0 || col >= g.n) continue;
-                if (rank > 0) {
-                    float v[8];
-                    unpack16(yv[m][s][q], v, static_cast<__nv_bfloat16*>(nullptr));
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        v[2 * u] += d[q][u][2 * s];
-                        v[2 * u + 1] += d[q][u][2 * s + 1];
-                    }
-                    yv[m][s][q] = pack16(v, static_cast<__nv_bfloat16*>(nullptr));
-                }
-                *reinterpret_cast<uint4*>(g.out + token[m][s] * g.ldo + col) = yv[m][s][q];
-            }
-    }
+    __syncthreads();
+    out.template run<S::kStages>(frags);
 }
 
 // The tiles of a larger batch: tokens counted by adapter, each adapter's given adjacent places in `order`, and a tile for each
@@ -756,8 +735,8 @@ twell_status run_small(const LoraArgs& g, int sms, cudaStream_t s)
     return launch_lora(kern, tiles, blocks, S::bytes(blocks), s, g);
 }
 
-// Of the larger batches: 16-token rows of a tile; what the workspace holds of a pass.
-constexpr int kLoraMT = 2;
+// Of the larger batches: what the workspace holds of a pass.
+constexpr int kLoraTile = 32;  // least tokens of a tile
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 struct LoraWs {
     size_t tiles, order, t, total;
@@ -765,16 +744,18 @@ struct LoraWs {
     {
         const int n = std::min(N, kLoraPass);
         tiles = 16;
-        order = tiles + 16 * static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, 16 * kLoraMT));
+        order = tiles + 16 * static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, kLoraTile));
         t = (order + sizeof(int32_t) * static_cast<size_t>(n) + 15) / 16 * 16;
         total = t + static_cast<size_t>(n) * lora_ranks(R) * 4;
     }
 };
 
-template <int RG, int RT, int NT>
+template <int MT, int RG, int RT>
 twell_status run_pass(LoraArgs g, uint8_t* ws, int sms, cudaStream_t s)
 {
-    using S = LoraShape<kLoraMT, RG, RT, false>;
+    using S = LoraShape<MT, RG, RT, false>;
+    using O = LoraOutShape<MT, RG, RT>;
+    static_assert(S::kTok >= kLoraTile, "the workspace has room for the tiles");
     const LoraWs at(g.N, g.R);
     int32_t* n_tiles = reinterpret_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
@@ -789,16 +770,21 @@ twell_status run_pass(LoraArgs g, uint8_t* ws, int sms, cudaStream_t s)
     const int most = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
     constexpr int kMost = most_blocks<S>();
     const int blocks = lora_blocks(g.N / S::kTok, sms, kMost);
-    auto in = lora_in_kernel<kLoraMT, RG, RT>;
-    static std::atomic<uint64_t> allowed{0};
-    if (twell_host::allow_smem(in, S::bytes(kMost), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    auto in = lora_in_kernel<MT, RG, RT>;
+    static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
+    if (twell_host::allow_smem(in, S::bytes(kMost), in_allowed) != TWELL_OK) return TWELL_ERR_CUDA;
     st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t);
     if (st != TWELL_OK) return st;
-    constexpr int kCols = 32 * NT * kLoraWarps;
-    const long long out_blocks = static_cast<long long>(most) * ((g.n + kCols - 1) / kCols);
+    auto out = lora_out_kernel<MT, RG, RT>;
+    if (twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    // a block's part of the columns: kOutRounds blocks an SM's place, but a ring's worth of pieces a warp at least
+    constexpr int kOutRounds = 2;
+    const long long places = (MT == 2 ? 2ll : 1ll) * sms * kOutRounds, tiles_about = std::max(1, g.N / S::kTok);
+    const int nt = (g.n + 31) / 32;
+    const int parts = static_cast<int>(std::max<long long>(1, std::min<long long>((places + tiles_about - 1) / tiles_about, nt / (kLoraWarps * O::kStages))));
+    const long long out_blocks = static_cast<long long>(most) * parts;
     if (out_blocks > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
-    return twell_host::launch_dep(lora_out_kernel<kLoraMT, RG, RT, NT>, dim3(static_cast<unsigned>(out_blocks)), dim3(kLoraThreads), 0, s,
-                                  g, t, most);
+    return twell_host::launch_dep(out, dim3(static_cast<unsigned>(out_blocks)), dim3(kLoraThreads), O::kBytes, s, g, t, most);
 }
 
 }  // namespace
@@ -855,10 +841,10 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
         p.y += at * ldy;
         p.out += at * ldo;
         uint8_t* w = static_cast<uint8_t*>(ws);
-        const twell_status st = ad->rank <= 16   ? twell::run_pass<1, 2, 2>(p, w, dev.sm_count, s)
-                                : ad->rank <= 32 ? twell::run_pass<1, 4, 2>(p, w, dev.sm_count, s)
-                                : ad->rank <= 64 ? twell::run_pass<2, 4, 1>(p, w, dev.sm_count, s)
-                                                 : twell::run_pass<4, 4, 1>(p, w, dev.sm_count, s);
+        const twell_status st = ad->rank <= 16   ? twell::run_pass<2, 1, 2>(p, w, dev.sm_count, s)
+                                : ad->rank <= 32 ? twell::run_pass<2, 1, 4>(p, w, dev.sm_count, s)
+                                : ad->rank <= 64 ? twell::run_pass<4, 2, 4>(p, w, dev.sm_count, s)
+                                                 : twell::run_pass<4, 4, 4>(p, w, dev.sm_count, s);
         if (st != TWELL_OK) return st;
     }
     return TWELL_OK;
