@@ -9,12 +9,14 @@
 // 2^64 is the fraction of a turn, whatever the position (an fp32 product is off by 0.06 rad a million positions away). The
 // upper 32 bits are cut into a quarter of a turn and a rest within +-1/8, whose sine and cosine are their power series.
 #include "twell_common.cuh"
+#include "twell_mma.cuh"
+#include "twell_ops.cuh"
 
 namespace twell {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRopeHeads = 4;       // heads a thread has under way at a time
+constexpr int kRopeWarps = 4;
+constexpr int kRopeThreads = 32 * kRopeWarps;
 constexpr int kRopeMaxDim = 1024;
 
 struct RopeSide {
@@ -30,7 +32,8 @@ struct RopeArgs {
     int q_heads, heads;  // heads: of q and k together
     int tokens, S, hd, rot;
     int pair_chunks, chunks;  // of a head: V pairs each, then those that are copied, 2 V elements each
-    int lanes;                // threads that share a token's chunk
+    int lanes;                // warps that share a chunk's heads: kRopeWarps of each of so many blocks
+    unsigned unit_blocks;
     float cos_factor, sin_factor;
 };
 
@@ -38,6 +41,33 @@ template <typename E, int V>
 struct alignas(V * sizeof(E)) RopeVec {
     E v[V];
 };
+template <typename E, int V>
+__device__ __forceinline__ void rope_unpack(const RopeVec<E, V>& x, float* o)
+{
+    if constexpr (sizeof(E) == 2 && V > 1) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = Elem<E>::to_f(x.v[i]);
+    }
+}
+template <typename E, int V>
+__device__ __forceinline__ void rope_pack(const float* o, RopeVec<E, V>& x)
+{
+    if constexpr (sizeof(E) == 2 && V > 1) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] = bf16x2_rn(o[2 * i], o[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x.v[i] = Elem<E>::from_f(o[i]);
+    }
+}
 
 // cos and sin of position x frequency. The rest r of the turn after the nearest quarter is at most pi / 4 in radians:
 // the series end at r^9 / 9! and r^10 / 10!, off by 2e-9 and 1e-10. What the rounding of r to fp32 adds is 2^-24 of it.
@@ -56,76 +86,89 @@ __device__ __forceinline__ void rope_turn(int32_t position, uint64_t turns, floa
     s = quarter & 2 ? -y : y;
 }
 
-// NEIGHBOURS: a pair is (2i, 2i + 1), else (i, i + rot / 2). Either way a chunk of V pairs is two vectors of V elements.
+// NEIGHBOURS: a pair is (2i, 2i + 1), else (i, i + rot / 2). Either way a chunk of V pairs is two vectors of V elements. A block
+// has 32 chunks (of one token after the other), each warp of it every lanes-th head of them.
 template <typename E, int V, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
 {
     using Vec = RopeVec<E, V>;
+    __shared__ float2 turn[V][32];
     pdl_begin();
-    const unsigned id = blockIdx.x * kRopeThreads + threadIdx.x;
-    const unsigned rest = id / static_cast<unsigned>(a.chunks), lane = rest / static_cast<unsigned>(a.tokens);
-    if (lane >= static_cast<unsigned>(a.lanes)) return;
-    const int chunk = static_cast<int>(id - rest * a.chunks), tok = static_cast<int>(rest - lane * a.tokens);
+    const unsigned u = blockIdx.x % a.unit_blocks * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+    const int lane = static_cast<int>(blockIdx.x / a.unit_blocks * kRopeWarps + warp);
+    const int tok = static_cast<int>(u / static_cast<unsigned>(a.chunks)), chunk = static_cast<int>(u - tok * a.chunks);
+    const bool live = tok < a.tokens;
     const int b = a.S == a.tokens ? 0 : tok / a.S, t = tok - b * a.S;
     const bool turned = chunk < a.pair_chunks;
     // where the chunk's two vectors begin in a head; the second of the last copied chunk may lie past it
     const int lo = turned ? chunk * (NEIGHBOURS ? 2 * V : V) : a.rot + (chunk - a.pair_chunks) * 2 * V;
     const int hi = turned && !NEIGHBOURS ? lo + a.rot / 2 : lo + V;
     const bool both = hi < a.hd;
-    auto in = [&](int h) {
-        const bool k = h >= a.q_heads;
-        const RopeSide& s = k ? a.k : a.q;
-        return static_cast<const E*>(s.in) + b * s.in_batch + t * s.in_token + (k ? h - a.q_heads : h) * s.in_head;
+    const E* in = static_cast<const E*>(a.q.in) + b * a.q.in_batch + t * a.q.in_token + lo;
+    E* out = static_cast<E*>(a.q.out) + b * a.q.out_batch + t * a.q.out_token + lo;
+    Vec x[2];
+    auto request = [&](const E* p) {
+        x[0] = *reinterpret_cast<const Vec*>(p);
+        if (both) x[1] = *reinterpret_cast<const Vec*>(p + (hi - lo));
     };
-    auto out = [&](int h) {
-        const bool k = h >= a.q_heads;
-        const RopeSide& s = k ? a.k : a.q;
-        return static_cast<E*>(s.out) + b * s.out_batch + t * s.out_token + (k ? h - a.q_heads : h) * s.out_head;
-    };
-    Vec x[kRopeHeads][2];
-    auto request = [&](int h0) {
-#pragma unroll
-        for (int i = 0; i < kRopeHeads; ++i) {
-            const int h = h0 + i * a.lanes;
-            if (h < a.heads) {
-                const E* p = in(h);
-                x[i][0] = *reinterpret_cast<const Vec*>(p + lo);
-                if (both) x[i][1] = *reinterpret_cast<const Vec*>(p + hi);
-            }
-        }
-    };
-    request(static_cast<int>(lane));
-    float c[V], s[V];
-    if (turned) {
+    if (lane < a.q_heads && live) request(in + lane * a.q.in_head);
+    // the warps share a chunk's angles out between them
+    if (live && turned) {
         const int32_t pos = __ldg(a.positions + b * a.pos_batch + t);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            rope_turn(pos, __ldg(a.turns + chunk * V + i), c[i], s[i]);
-            c[i] *= a.cos_factor;
-            s[i] *= a.sin_factor;
+        for (int i = 0; i < (V + kRopeWarps - 1) / kRopeWarps; ++i) {
+            const int pair = i * kRopeWarps + static_cast<int>(warp);
+            if (pair < V) {
+                float2 cs;
+                rope_turn(pos, __ldg(a.turns + chunk * V + pair), cs.x, cs.y);
+                turn[pair][threadIdx.x & 31] = make_float2(cs.x * a.cos_factor, cs.y * a.sin_factor);
+            }
         }
     }
-    for (int h0 = static_cast<int>(lane); h0 < a.heads; h0 += kRopeHeads * a.lanes) {
-        if (h0 != static_cast<int>(lane)) request(h0);
+    __syncthreads();
+    if (!live) return;
+    // (cos, cos), (sin, sin) and (-sin, -sin) of two pairs each
+    constexpr int kTwos = (V + 1) / 2;
+    F2 c[kTwos], sn[kTwos], ns[kTwos];
 #pragma unroll
-        for (int i = 0; i < kRopeHeads; ++i) {
-            const int h = h0 + i * a.lanes;
-            if (h >= a.heads) break;
-            if (turned) {
+    for (int j = 0; j < kTwos; ++j) {
+        const float2 p = turned ? turn[2 * j][threadIdx.x & 31] : make_float2(1.0f, 0.0f);
+        const float2 q = turned && V > 1 ? turn[(2 * j + 1) % V][threadIdx.x & 31] : p;
+        c[j] = F2::of(p.x, q.x);
+        sn[j] = F2::of(p.y, q.y);
+        ns[j] = F2::of(-p.y, -q.y);
+    }
+    auto finish = [&](E* p) {
+        if (turned) {
+            float v[2 * V];
+            rope_unpack<E, V>(x[0], v);
+            rope_unpack<E, V>(x[1], v + V);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    // element e of a pair is x[i][e / V].v[e % V]
-                    constexpr int kStep = NEIGHBOURS ? 1 : V;
-                    const int e = NEIGHBOURS ? 2 * j : j, f = e + kStep;
-                    const float u = Elem<E>::to_f(x[i][e / V].v[e % V]), w = Elem<E>::to_f(x[i][f / V].v[f % V]);
-                    x[i][e / V].v[e % V] = Elem<E>::from_f(fmaf(u, c[j], -w * s[j]));
-                    x[i][f / V].v[f % V] = Elem<E>::from_f(fmaf(u, s[j], w * c[j]));
-                }
+            for (int j = 0; j < kTwos; ++j) {
+                // the first values of pairs 2j and 2j + 1 are v[e] and v[f], their second ones kStep behind
+                constexpr int kStep = NEIGHBOURS ? 1 : V;
+                const int e = NEIGHBOURS ? 4 * j : 2 * j, f = V == 1 ? e : NEIGHBOURS ? e + 2 : e + 1;
+                const F2 m = F2::of(v[e], v[f]), w = F2::of(v[e + kStep], v[f + kStep]);
+                fma2(w, ns[j], m * c[j]).get(v[e], v[f]);
+                fma2(w, c[j], m * sn[j]).get(v[e + kStep], v[f + kStep]);
             }
-            E* p = out(h);
-            *reinterpret_cast<Vec*>(p + lo) = x[i][0];
-            if (both) *reinterpret_cast<Vec*>(p + hi) = x[i][1];
+            rope_pack<E, V>(v, x[0]);
+            rope_pack<E, V>(v + V, x[1]);
         }
+        *reinterpret_cast<Vec*>(p) = x[0];
+        if (both) *reinterpret_cast<Vec*>(p + (hi - lo)) = x[1];
+    };
+    int h = lane;
+    for (; h < a.q_heads; h += a.lanes) {
+        if (h != lane) request(in + h * a.q.in_head);
+        finish(out + h * a.q.out_head);
+    }
+    if (h >= a.heads) return;
+    in = static_cast<const E*>(a.k.in) + b * a.k.in_batch + t * a.k.in_token + lo;
+    out = static_cast<E*>(a.k.out) + b * a.k.out_batch + t * a.k.out_token + lo;
+    for (; h < a.heads; h += a.lanes) {
+        request(in + (h - a.q_heads) * a.k.in_head);
+        finish(out + (h - a.q_heads) * a.k.out_head);
     }
 }
 
@@ -234,9 +277,11 @@ twell_status rope(const twell_rope_heads* q, const twell_rope_heads* k, const in
     a.chunks = a.pair_chunks + (copies ? (hd - rot + 2 * v - 1) / (2 * v) : 0);
     DevInfo dev;
     if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
-    const long long units = tokens * a.chunks, want = 1024ll * dev.sm_count;
-    a.lanes = static_cast<int>(units >= want ? 1 : (want + units - 1) / units < heads ? (want + units - 1) / units : heads);
-    const unsigned blocks = static_cast<unsigned>((units * a.lanes + twell::kRopeThreads - 1) / twell::kRopeThreads);
+    const long long units = (tokens * a.chunks + 31) / 32, want = 16ll * dev.sm_count, most = (heads + twell::kRopeWarps - 1) / twell::kRopeWarps;
+    const long long groups = units >= want ? 1 : (want + units - 1) / units < most ? (want + units - 1) / units : most;
+    a.lanes = static_cast<int>(groups) * twell::kRopeWarps;
+    a.unit_blocks = static_cast<unsigned>(units);
+    const unsigned blocks = static_cast<unsigned>(units * groups);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool nb = neighbours != 0;
     if (dtype == TWELL_BF16) {
