@@ -14,10 +14,10 @@
 namespace twell {
 namespace {
 
-constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxSeqs = 4096;
-constexpr int kPlanPer = kPlanMaxSeqs / kPlanThreads;  // most requests a thread
-constexpr int kPlanQuad = 4;                           // consecutive tokens a thread takes at a time
+constexpr int kPlanQuad = 4;  // consecutive tokens a thread takes at a time
+constexpr int kPlanWarpPer = 4;  // requests a lane where every warp has all of them
+constexpr int kPlanBlocks = 4;   // most blocks an SM
 constexpr int kEnded = -1;
 
 struct PlanArgs {
@@ -37,29 +37,37 @@ __device__ __forceinline__ int sat_add(int a, int b)
     return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu));
 }
 
-// The sum over the threads before this one, and over all of them. `red` has a place for each warp.
-__device__ __forceinline__ int block_scan(int v, int* red, int& total)
+// The sums of two numbers over the lanes before this one and over all of them, in a warp.
+__device__ __forceinline__ void warp_scan(int (&v)[2], int (&total)[2])
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kPlanThreads / 32;
-    int incl = v;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl = sat_add(incl, u);
-    }
-    if (lane == 31) red[warp] = incl;
-    __syncthreads();
-    int w = lane < warps ? red[lane] : 0;
+    for (int e = 0; e < 2; ++e) {
+        int incl = v[e];
 #pragma unroll
-    for (int o = 1; o < warps; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w = sat_add(w, u);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl = sat_add(incl, u);
+        }
+        total[e] = __shfl_sync(0xffffffffu, incl, 31);
+        const int before = __shfl_up_sync(0xffffffffu, incl, 1);
+        v[e] = lane ? before : 0;
     }
-    total = __shfl_sync(0xffffffffu, w, warps - 1);
-    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    const int excl = __shfl_up_sync(0xffffffffu, incl, 1);
+}
+// The same over the threads of a block. `red` has a place for each warp and number.
+template <int THREADS>
+__device__ __forceinline__ void block_scan(int (&v)[2], int (&red)[2][32], int (&total)[2])
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum[2];
+    warp_scan(v, sum);
+    if (lane < 2) red[lane][warp] = sum[lane];
     __syncthreads();
-    return sat_add(warp ? before : 0, lane ? excl : 0);
+    int w[2] = {lane < THREADS / 32 ? red[0][lane] : 0, lane < THREADS / 32 ? red[1][lane] : 0};
+    warp_scan(w, total);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) v[e] = sat_add(v[e], __shfl_sync(0xffffffffu, w[e], warp));
+    __syncthreads();
 }
 
 // The last i < n with at[i] <= v (at ascending, at[0] <= v).
@@ -74,50 +82,58 @@ __device__ __forceinline__ int last_at_most(const int* at, int n, int v)
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
+// PER requests a thread. WARP: every warp has all of them and forms the sums without the others, else the block has.
+template <int PER, int THREADS, bool WARP>
+__global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
 {
     extern __shared__ int plan_smem[];
-    __shared__ int red[32];
+    __shared__ int red[2][32];
     __shared__ int s_taken, s_last;
     pdl_begin();
     int* start = plan_smem;          // [B + 1] of the requests' tokens in the step
     int* past = start + a.B + 1;     // [B] tokens that they had, -1 where they get none
     int* first = past + a.B;         // [B] of their pages among those taken
     int* back = first + a.B;         // [B] of their pages among those given back
-    const int page = 1 << a.page_shift, tid = static_cast<int>(threadIdx.x);
+    const int page = 1 << a.page_shift, tid = static_cast<int>(threadIdx.x), place = WARP ? tid & 31 : tid;
+    const bool writes = !WARP || tid < 32;
+    const int per = (a.B + (WARP ? 32 : THREADS) - 1) / (WARP ? 32 : THREADS), b0 = place * per;
+    int had[PER], add[PER];  // a request: tokens it had, its new ones
+    bool ends[PER], wrong[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool is = i < per && b0 + i < a.B;
+        had[i] = is ? a.lens[b0 + i] : 0;
+        add[i] = is ? a.news[b0 + i] : 0;
+    }
     int head = a.state[0], free = a.state[1];
+    if (!WARP && tid == 0) s_taken = 0;
     bool bad = head < 0 || free < 0 || free > a.n_pages || (head >= a.n_pages && (head != 0 || free != 0));
     if (bad) head = free = 0;  // nothing can be taken from or given to a ring that is not one
     const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll);
-    const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
-    if (tid == 0) s_taken = 0;
-
-    // a request: tokens it had, its new ones, its end
-    int had[kPlanPer], add[kPlanPer];
-    bool ends[kPlanPer], wrong[kPlanPer];
-    int sum = 0;
+    auto scan = [&](int (&v)[2], int (&total)[2]) {
+        if constexpr (WARP) warp_scan(v, total);
+        else block_scan<THREADS>(v, red, total);
+    };
+    int sum[2] = {0, 0}, total[2];
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-        had[i] = add[i] = 0;
-        ends[i] = wrong[i] = false;
-        if (i < per && b0 + i < a.B) {
-            had[i] = a.lens[b0 + i];
-            const int n = a.news[b0 + i];
-            add[i] = max(n, 0);
-            ends[i] = n == kEnded;
-            wrong[i] = n < kEnded || had[i] < 0 || static_cast<long long>(had[i]) + add[i] > cap;
-            sum = sat_add(sum, add[i]);
-        }
+    for (int i = 0; i < PER; ++i) {
+        const int n = add[i];
+        add[i] = max(n, 0);
+        ends[i] = n == kEnded;
+        wrong[i] = n < kEnded || had[i] < 0 || static_cast<long long>(had[i]) + add[i] > cap;
+        sum[0] = sat_add(sum[0], add[i]);
     }
-    int total;
-    int at = block_scan(sum, red, total);
+    scan(sum, total);
+    const int tokens = total[0];
+    int at = sum[0];
     // pages: a request whose tokens do not all have a place in the step or in its row of the table gets none
-    int need[kPlanPer], gives[kPlanPer], need_sum = 0, gives_sum = 0;
+    int need[PER], gives[PER];
+    sum[0] = sum[1] = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         need[i] = gives[i] = 0;
         if (i < per && b0 + i < a.B) {
-            start[b0 + i] = at;
+            if (writes) start[b0 + i] = at;
             if (add[i] > 0 && static_cast<long long>(at) + add[i] > a.M) wrong[i] = true;
             at = sat_add(at, add[i]);
             if (!wrong[i]) {
@@ -126,14 +142,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
                 else if (add[i] > 0) need[i] = static_cast<int>((static_cast<long long>(had[i]) + add[i] + page - 1) >> a.page_shift) - held;
             }
             bad |= wrong[i];
-            need_sum = sat_add(need_sum, need[i]);
-            gives_sum = sat_add(gives_sum, gives[i]);
+            sum[0] = sat_add(sum[0], need[i]);
+            sum[1] = sat_add(sum[1], gives[i]);
         }
     }
-    if (tid == 0) start[a.B] = total;
-    int need_total, given;
-    int take = block_scan(need_sum, red, need_total);
-    int give = block_scan(gives_sum, red, given);
+    if (tid == 0) start[a.B] = tokens;
+    scan(sum, total);
+    int take = sum[0], give = sum[1], given = total[1];
     // more pages than there are: some are given back twice, and none are taken back
     const bool refuse = static_cast<long long>(free) + given > a.n_pages;
     if (refuse) given = 0;
@@ -141,13 +156,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
     bool empty = false;
     int taken = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         if (i < per && b0 + i < a.B) {
             const bool none = need[i] > 0 && sat_add(take, need[i]) > free;
             empty |= none;
-            past[b0 + i] = wrong[i] || none ? -1 : had[i];
-            first[b0 + i] = take;
-            back[b0 + i] = give;
+            if (writes) {
+                past[b0 + i] = wrong[i] || none ? -1 : had[i];
+                first[b0 + i] = take;
+                back[b0 + i] = give;
+            }
             take = sat_add(take, need[i]);
             if (need[i] > 0 && !none) taken = take;
             give = sat_add(give, gives[i]);
@@ -155,11 +172,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
             had[i] = ends[i] && !wrong[i] && !refuse ? 0 : had[i] + add[i];  // the length after the step
         }
     }
-    if (taken > 0) atomicMax(&s_taken, taken);
-    if (bad) report(a.status, TWELL_ERR_DEVICE_CHECK);
-    if (empty) report(a.status, TWELL_ERR_POOL_EMPTY);
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    if (!WARP && (tid & 31) == 0 && taken > 0) atomicMax(&s_taken, taken);
+    if (blockIdx.x == 0 && bad) report(a.status, TWELL_ERR_DEVICE_CHECK);
+    if (blockIdx.x == 0 && empty) report(a.status, TWELL_ERR_POOL_EMPTY);
     __syncthreads();
-    taken = s_taken;
+    if (!WARP) taken = s_taken;
 
     // lengths and state may be written where they were read once every block has read them: the last to say so does it
     const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
@@ -174,9 +192,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
     }
     if (commit) {
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i)
-            if (i < per && b0 + i < a.B) a.lens_out[b0 + i] = had[i];
-        for (int i = tid; i <= a.B; i += kPlanThreads) a.starts[i] = start[i];
+        for (int i = 0; i < PER; ++i)
+            if (writes && i < per && b0 + i < a.B) a.lens_out[b0 + i] = had[i];
+        for (int i = tid; i <= a.B; i += THREADS) a.starts[i] = start[i];
         if (tid == 0) {
             const long long h = static_cast<long long>(head) + taken;
             a.state_out[0] = static_cast<int>(h >= a.n_pages && a.n_pages > 0 ? h - a.n_pages : h);
@@ -191,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
         return a.ring + (j >= a.n_pages ? j - a.n_pages : j);
     };
     auto row = [&](int b, int p) { return a.table + static_cast<long long>(b) * a.max_pages + p; };
-    const unsigned threads = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + tid;
+    const unsigned threads = gridDim.x * THREADS, me = blockIdx.x * THREADS + tid;
 
     // tokens, four at a time
     const unsigned quads = (static_cast<unsigned>(a.M) + kPlanQuad - 1) / kPlanQuad;
@@ -207,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
             const int i = i0 + e;
             slot[e] = own[e] = -1;
             pos[e] = 0;
-            if (i >= min(total, a.M)) continue;
+            if (i >= min(tokens, a.M)) continue;
             while (i >= start[b + 1]) ++b, known = -1;
             if (label_of != b) {
                 label = a.labels ? __ldg(a.labels + b) : b;
@@ -255,6 +273,20 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
     }
 }
 
+// Up to four blocks an SM, so that long prompts are done in one round.
+template <int PER, int THREADS, bool WARP>
+twell_status run_plan(const PlanArgs& a, int sms, cudaStream_t s)
+{
+    auto kern = kv_plan_kernel<PER, THREADS, WARP>;
+    static std::atomic<uint64_t> allowed{0};
+    constexpr size_t kMost = (4 * (WARP ? 32 * PER : PER * THREADS) + 1) * sizeof(int);
+    if (twell_host::allow_smem(kern, kMost, allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    const long long quads = (static_cast<long long>(a.M) + kPlanQuad - 1) / kPlanQuad, want = (quads + THREADS - 1) / THREADS;
+    const long long most = sms * kPlanBlocks;
+    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most)), dim3(THREADS),
+                                  (4 * static_cast<size_t>(a.B) + 1) * sizeof(int), s, a);
+}
+
 }  // namespace
 }  // namespace twell
 
@@ -287,11 +319,8 @@ extern "C" twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page
                                starts,     seq_lens_out, state_out,   dev_status, pool->n_pages, shift, max_pages, B, n_tokens};
     DevInfo dev;
     if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
-    const size_t smem = (4 * static_cast<size_t>(B) + 1) * sizeof(int);
-    static std::atomic<uint64_t> allowed{0};
-    if (allow_smem(twell::kv_plan_kernel, (4 * twell::kPlanMaxSeqs + 1) * sizeof(int), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    const long long quads = (static_cast<long long>(n_tokens) + twell::kPlanQuad - 1) / twell::kPlanQuad;
-    const long long blocks = (quads + twell::kPlanThreads - 1) / twell::kPlanThreads;
-    return launch_dep(twell::kv_plan_kernel, dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < dev.sm_count ? blocks : dev.sm_count)),
-                      dim3(twell::kPlanThreads), smem, static_cast<cudaStream_t>(stream), a);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (B <= 32 * twell::kPlanWarpPer) return twell::run_plan<twell::kPlanWarpPer, 256, true>(a, dev.sm_count, s);
+    if (B <= 512) return twell::run_plan<1, 512, false>(a, dev.sm_count, s);
+    return twell::run_plan<twell::kPlanMaxSeqs / 512, 512, false>(a, dev.sm_count, s);
 }

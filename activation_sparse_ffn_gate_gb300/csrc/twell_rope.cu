@@ -17,6 +17,9 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 constexpr int kRopeThreads = 32 * kRopeWarps;
+// Heads a thread has under way at a time (16001 tokens of 24 heads of 128 in bf16: 33.6 us with two, 34.2 with four, whose
+// registers cost warps; without any in advance 35.0).
+constexpr int kRopeHeads = 2;
 constexpr int kRopeMaxDim = 1024;
 
 struct RopeSide {
@@ -104,14 +107,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
     const int lo = turned ? chunk * (NEIGHBOURS ? 2 * V : V) : a.rot + (chunk - a.pair_chunks) * 2 * V;
     const int hi = turned && !NEIGHBOURS ? lo + a.rot / 2 : lo + V;
     const bool both = hi < a.hd;
-    const E* in = static_cast<const E*>(a.q.in) + b * a.q.in_batch + t * a.q.in_token + lo;
-    E* out = static_cast<E*>(a.q.out) + b * a.q.out_batch + t * a.q.out_token + lo;
-    Vec x[2];
-    auto request = [&](const E* p) {
-        x[0] = *reinterpret_cast<const Vec*>(p);
-        if (both) x[1] = *reinterpret_cast<const Vec*>(p + (hi - lo));
+    // the queries' heads from `lane` on, then the keys', which go on where those ended, so that the lanes have as many
+    bool keys = lane >= a.q_heads;
+    int h = keys ? lane - a.q_heads : lane;
+    const E* in;
+    E* out;
+    auto enter = [&](const RopeSide& s) {
+        in = static_cast<const E*>(s.in) + b * s.in_batch + t * s.in_token + lo;
+        out = static_cast<E*>(s.out) + b * s.out_batch + t * s.out_token + lo;
     };
-    if (lane < a.q_heads && live) request(in + lane * a.q.in_head);
+    enter(keys ? a.k : a.q);
+    Vec x[kRopeHeads][2];
+    // heads first, first + lanes, ... of a side that has `count` of them, `stride` apart
+    auto request = [&](int first, int count, int64_t stride) {
+#pragma unroll
+        for (int i = 0; i < kRopeHeads; ++i)
+            if (first + i * a.lanes < count) {
+                const E* p = in + (first + i * a.lanes) * stride;
+                x[i][0] = *reinterpret_cast<const Vec*>(p);
+                if (both) x[i][1] = *reinterpret_cast<const Vec*>(p + (hi - lo));
+            }
+    };
+    int heads = keys ? a.heads - a.q_heads : a.q_heads;
+    if (live) request(h, heads, keys ? a.k.in_head : a.q.in_head);
     // the warps share a chunk's angles out between them
     if (live && turned) {
         const int32_t pos = __ldg(a.positions + b * a.pos_batch + t);
@@ -138,37 +156,44 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
         sn[j] = F2::of(p.y, q.y);
         ns[j] = F2::of(-p.y, -q.y);
     }
-    auto finish = [&](E* p) {
-        if (turned) {
-            float v[2 * V];
-            rope_unpack<E, V>(x[0], v);
-            rope_unpack<E, V>(x[1], v + V);
+    auto finish = [&](int first, int count, int64_t stride) {
 #pragma unroll
-            for (int j = 0; j < kTwos; ++j) {
-                // the first values of pairs 2j and 2j + 1 are v[e] and v[f], their second ones kStep behind
-                constexpr int kStep = NEIGHBOURS ? 1 : V;
-                const int e = NEIGHBOURS ? 4 * j : 2 * j, f = V == 1 ? e : NEIGHBOURS ? e + 2 : e + 1;
-                const F2 m = F2::of(v[e], v[f]), w = F2::of(v[e + kStep], v[f + kStep]);
-                fma2(w, ns[j], m * c[j]).get(v[e], v[f]);
-                fma2(w, c[j], m * sn[j]).get(v[e + kStep], v[f + kStep]);
+        for (int i = 0; i < kRopeHeads; ++i) {
+            if (first + i * a.lanes >= count) break;
+            if (turned) {
+                float v[2 * V];
+                rope_unpack<E, V>(x[i][0], v);
+                rope_unpack<E, V>(x[i][1], v + V);
+#pragma unroll
+                for (int j = 0; j < kTwos; ++j) {
+                    // the first values of pairs 2j and 2j + 1 are v[e] and v[f], their second ones kStep behind
+                    constexpr int kStep = NEIGHBOURS ? 1 : V;
+                    const int e = NEIGHBOURS ? 4 * j : 2 * j, f = V == 1 ? e : NEIGHBOURS ? e + 2 : e + 1;
+                    const F2 m = F2::of(v[e], v[f]), w = F2::of(v[e + kStep], v[f + kStep]);
+                    fma2(w, ns[j], m * c[j]).get(v[e], v[f]);
+                    fma2(w, c[j], m * sn[j]).get(v[e + kStep], v[f + kStep]);
+                }
+                rope_pack<E, V>(v, x[i][0]);
+                rope_pack<E, V>(v + V, x[i][1]);
             }
-            rope_pack<E, V>(v, x[0]);
-            rope_pack<E, V>(v + V, x[1]);
+            E* p = out + (first + i * a.lanes) * stride;
+            *reinterpret_cast<Vec*>(p) = x[i][0];
+            if (both) *reinterpret_cast<Vec*>(p + (hi - lo)) = x[i][1];
         }
-        *reinterpret_cast<Vec*>(p) = x[0];
-        if (both) *reinterpret_cast<Vec*>(p + (hi - lo)) = x[1];
     };
-    int h = lane;
-    for (; h < a.q_heads; h += a.lanes) {
-        if (h != lane) request(in + h * a.q.in_head);
-        finish(out + h * a.q.out_head);
-    }
-    if (h >= a.heads) return;
-    in = static_cast<const E*>(a.k.in) + b * a.k.in_batch + t * a.k.in_token + lo;
-    out = static_cast<E*>(a.k.out) + b * a.k.out_batch + t * a.k.out_token + lo;
-    for (; h < a.heads; h += a.lanes) {
-        request(in + (h - a.q_heads) * a.k.in_head);
-        finish(out + (h - a.q_heads) * a.k.out_head);
+    const int step = kRopeHeads * a.lanes;
+    bool here = true;  // the heads from h on are requested
+    for (;;) {
+        for (; h < heads; h += step) {
+            if (!here) request(h, heads, keys ? a.k.in_head : a.q.in_head);
+            here = false;
+            finish(h, heads, keys ? a.k.out_head : a.q.out_head);
+        }
+        if (keys || a.q_heads == a.heads) return;
+        keys = true;
+        heads = a.heads - a.q_heads;
+        h = (lane + a.lanes - a.q_heads % a.lanes) % a.lanes;
+        enter(a.k);
     }
 }
 
