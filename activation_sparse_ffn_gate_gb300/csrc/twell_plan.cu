@@ -15,9 +15,8 @@ namespace twell {
 namespace {
 
 constexpr int kPlanMaxSeqs = 4096;
-constexpr int kPlanQuad = 4;  // consecutive tokens a thread takes at a time
-constexpr int kPlanWarpPer = 4;  // requests a lane where every warp has all of them
-constexpr int kPlanBlocks = 4;   // most blocks an SM
+constexpr int kPlanWarpPer = 4;  // requests a lane where one warp has all of them
+constexpr int kPlanBlocks = 8;   // most blocks an SM
 constexpr int kEnded = -1;
 
 struct PlanArgs {
@@ -82,102 +81,118 @@ __device__ __forceinline__ int last_at_most(const int* at, int n, int v)
     return lo;
 }
 
-// PER requests a thread. WARP: every warp has all of them and forms the sums without the others, else the block has.
-template <int PER, int THREADS, bool WARP>
+// What the sums come to: tokens, pages taken and given back, the ring before the step.
+struct PlanSums {
+    int tokens, taken, given, head, free;
+};
+
+// PER requests a thread of the block or, with WARP, of its first warp; Q adjacent tokens at a time.
+template <int PER, int THREADS, bool WARP, int Q>
 __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
 {
     extern __shared__ int plan_smem[];
     __shared__ int red[2][32];
-    __shared__ int s_taken, s_last;
+    __shared__ PlanSums s_sums;
+    __shared__ int s_last;
     pdl_begin();
     int* start = plan_smem;          // [B + 1] of the requests' tokens in the step
     int* past = start + a.B + 1;     // [B] tokens that they had, -1 where they get none
     int* first = past + a.B;         // [B] of their pages among those taken
     int* back = first + a.B;         // [B] of their pages among those given back
-    const int page = 1 << a.page_shift, tid = static_cast<int>(threadIdx.x), place = WARP ? tid & 31 : tid;
-    const bool writes = !WARP || tid < 32;
-    const int per = (a.B + (WARP ? 32 : THREADS) - 1) / (WARP ? 32 : THREADS), b0 = place * per;
+    const int page = 1 << a.page_shift, tid = static_cast<int>(threadIdx.x);
+    constexpr int kSpread = WARP ? 32 : THREADS;  // threads that have the requests
+    const bool counts = !WARP || tid < 32;
+    const int per = (a.B + kSpread - 1) / kSpread, b0 = tid * per;
     int had[PER], add[PER];  // a request: tokens it had, its new ones
     bool ends[PER], wrong[PER];
+    if (counts) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool is = i < per && b0 + i < a.B;
-        had[i] = is ? a.lens[b0 + i] : 0;
-        add[i] = is ? a.news[b0 + i] : 0;
-    }
-    int head = a.state[0], free = a.state[1];
-    if (!WARP && tid == 0) s_taken = 0;
-    bool bad = head < 0 || free < 0 || free > a.n_pages || (head >= a.n_pages && (head != 0 || free != 0));
-    if (bad) head = free = 0;  // nothing can be taken from or given to a ring that is not one
-    const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll);
-    auto scan = [&](int (&v)[2], int (&total)[2]) {
-        if constexpr (WARP) warp_scan(v, total);
-        else block_scan<THREADS>(v, red, total);
-    };
-    int sum[2] = {0, 0}, total[2];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int n = add[i];
-        add[i] = max(n, 0);
-        ends[i] = n == kEnded;
-        wrong[i] = n < kEnded || had[i] < 0 || static_cast<long long>(had[i]) + add[i] > cap;
-        sum[0] = sat_add(sum[0], add[i]);
-    }
-    scan(sum, total);
-    const int tokens = total[0];
-    int at = sum[0];
-    // pages: a request whose tokens do not all have a place in the step or in its row of the table gets none
-    int need[PER], gives[PER];
-    sum[0] = sum[1] = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        need[i] = gives[i] = 0;
-        if (i < per && b0 + i < a.B) {
-            if (writes) start[b0 + i] = at;
-            if (add[i] > 0 && static_cast<long long>(at) + add[i] > a.M) wrong[i] = true;
-            at = sat_add(at, add[i]);
-            if (!wrong[i]) {
-                const int held = (had[i] + page - 1) >> a.page_shift;
-                if (ends[i]) gives[i] = held;
-                else if (add[i] > 0) need[i] = static_cast<int>((static_cast<long long>(had[i]) + add[i] + page - 1) >> a.page_shift) - held;
-            }
-            bad |= wrong[i];
-            sum[0] = sat_add(sum[0], need[i]);
-            sum[1] = sat_add(sum[1], gives[i]);
+        for (int i = 0; i < PER; ++i) {
+            const bool is = i < per && b0 + i < a.B;
+            had[i] = is ? a.lens[b0 + i] : 0;
+            add[i] = is ? a.news[b0 + i] : 0;
         }
-    }
-    if (tid == 0) start[a.B] = tokens;
-    scan(sum, total);
-    int take = sum[0], give = sum[1], given = total[1];
-    // more pages than there are: some are given back twice, and none are taken back
-    const bool refuse = static_cast<long long>(free) + given > a.n_pages;
-    if (refuse) given = 0;
-    bad |= refuse;
-    bool empty = false;
-    int taken = 0;
+        int head = a.state[0], free = a.state[1];
+        if (!WARP && tid == 0) s_sums.taken = 0;
+        bool bad = head < 0 || free < 0 || free > a.n_pages || (head >= a.n_pages && (head != 0 || free != 0));
+        if (bad) head = free = 0;  // nothing can be taken from or given to a ring that is not one
+        const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll);
+        auto scan = [&](int (&v)[2], int (&total)[2]) {
+            if constexpr (WARP) warp_scan(v, total);
+            else block_scan<THREADS>(v, red, total);
+        };
+        int sum[2] = {0, 0}, total[2];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (i < per && b0 + i < a.B) {
-            const bool none = need[i] > 0 && sat_add(take, need[i]) > free;
-            empty |= none;
-            if (writes) {
+        for (int i = 0; i < PER; ++i) {
+            const int n = add[i];
+            add[i] = max(n, 0);
+            ends[i] = n == kEnded;
+            wrong[i] = n < kEnded || had[i] < 0 || static_cast<long long>(had[i]) + add[i] > cap;
+            sum[0] = sat_add(sum[0], add[i]);
+        }
+        scan(sum, total);
+        const int tokens = total[0];
+        int at = sum[0];
+        // pages: a request whose tokens do not all have a place in the step or in its row of the table gets none
+        int need[PER], gives[PER];
+        sum[0] = sum[1] = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            need[i] = gives[i] = 0;
+            if (i < per && b0 + i < a.B) {
+                start[b0 + i] = at;
+                if (add[i] > 0 && static_cast<long long>(at) + add[i] > a.M) wrong[i] = true;
+                at = sat_add(at, add[i]);
+                if (!wrong[i]) {
+                    const int held = (had[i] + page - 1) >> a.page_shift;
+                    if (ends[i]) gives[i] = held;
+                    else if (add[i] > 0) need[i] = static_cast<int>((static_cast<long long>(had[i]) + add[i] + page - 1) >> a.page_shift) - held;
+                }
+                bad |= wrong[i];
+                sum[0] = sat_add(sum[0], need[i]);
+                sum[1] = sat_add(sum[1], gives[i]);
+            }
+        }
+        scan(sum, total);
+        int take = sum[0], give = sum[1], given = total[1];
+        // more pages than there are: some are given back twice, and none are taken back
+        const bool refuse = static_cast<long long>(free) + given > a.n_pages;
+        if (refuse) given = 0;
+        bad |= refuse;
+        bool empty = false;
+        int taken = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (i < per && b0 + i < a.B) {
+                const bool none = need[i] > 0 && sat_add(take, need[i]) > free;
+                empty |= none;
                 past[b0 + i] = wrong[i] || none ? -1 : had[i];
                 first[b0 + i] = take;
                 back[b0 + i] = give;
+                take = sat_add(take, need[i]);
+                if (need[i] > 0 && !none) taken = take;
+                give = sat_add(give, gives[i]);
+                if (wrong[i] || none) add[i] = 0;
+                had[i] = ends[i] && !wrong[i] && !refuse ? 0 : had[i] + add[i];  // the length after the step
             }
-            take = sat_add(take, need[i]);
-            if (need[i] > 0 && !none) taken = take;
-            give = sat_add(give, gives[i]);
-            if (wrong[i] || none) add[i] = 0;
-            had[i] = ends[i] && !wrong[i] && !refuse ? 0 : had[i] + add[i];  // the length after the step
         }
+        taken = __reduce_max_sync(0xffffffffu, taken);
+        if (WARP) {
+            if (tid == 0) s_sums.taken = taken;
+        } else if ((tid & 31) == 0 && taken > 0) {
+            atomicMax(&s_sums.taken, taken);
+        }
+        if (tid == 0) {
+            start[a.B] = s_sums.tokens = tokens;
+            s_sums.given = given;
+            s_sums.head = head;
+            s_sums.free = free;
+        }
+        if (blockIdx.x == 0 && bad) report(a.status, TWELL_ERR_DEVICE_CHECK);
+        if (blockIdx.x == 0 && empty) report(a.status, TWELL_ERR_POOL_EMPTY);
     }
-    taken = __reduce_max_sync(0xffffffffu, taken);
-    if (!WARP && (tid & 31) == 0 && taken > 0) atomicMax(&s_taken, taken);
-    if (blockIdx.x == 0 && bad) report(a.status, TWELL_ERR_DEVICE_CHECK);
-    if (blockIdx.x == 0 && empty) report(a.status, TWELL_ERR_POOL_EMPTY);
     __syncthreads();
-    if (!WARP) taken = s_taken;
+    const int tokens = s_sums.tokens, taken = s_sums.taken, given = s_sums.given, head = s_sums.head, free = s_sums.free;
 
     // lengths and state may be written where they were read once every block has read them: the last to say so does it
     const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
@@ -193,7 +208,7 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
     if (commit) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (writes && i < per && b0 + i < a.B) a.lens_out[b0 + i] = had[i];
+            if (counts && i < per && b0 + i < a.B) a.lens_out[b0 + i] = had[i];
         for (int i = tid; i <= a.B; i += THREADS) a.starts[i] = start[i];
         if (tid == 0) {
             const long long h = static_cast<long long>(head) + taken;
@@ -211,47 +226,55 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
     auto row = [&](int b, int p) { return a.table + static_cast<long long>(b) * a.max_pages + p; };
     const unsigned threads = gridDim.x * THREADS, me = blockIdx.x * THREADS + tid;
 
-    // tokens, four at a time
-    const unsigned quads = (static_cast<unsigned>(a.M) + kPlanQuad - 1) / kPlanQuad;
-    for (unsigned u = me; u < quads; u += threads) {
-        const int i0 = static_cast<int>(u * kPlanQuad);
-        int slot[kPlanQuad], pos[kPlanQuad], own[kPlanQuad];
-        int b = a.B > 0 ? last_at_most(start, a.B, i0) : 0;
-        int known = -1, base = -1;  // the page of the sequence that `base` is the first slot of, -1 where there is none
-        int label = 0;
-        int label_of = -1;
+    // tokens, Q at a time: where each one's page stands, the pages, the slots
+    const unsigned groups = (static_cast<unsigned>(a.M) + Q - 1) / Q;
+    for (unsigned u = me; u < groups; u += threads) {
+        const int i0 = static_cast<int>(u * Q), end = min(tokens, a.M);
+        int pos[Q], own[Q], pg[Q];
+        bool live[Q], same[Q];  // has a place; is in the page of the one before
+        const int32_t* from[Q];
+        int b = a.B > 0 ? last_at_most(start, a.B, i0) : 0, page_of = -1;
 #pragma unroll
-        for (int e = 0; e < kPlanQuad; ++e) {
+        for (int e = 0; e < Q; ++e) {
             const int i = i0 + e;
-            slot[e] = own[e] = -1;
             pos[e] = 0;
-            if (i >= min(tokens, a.M)) continue;
-            while (i >= start[b + 1]) ++b, known = -1;
-            if (label_of != b) {
-                label = a.labels ? __ldg(a.labels + b) : b;
-                label_of = b;
-            }
-            own[e] = label;
+            own[e] = -1;
+            live[e] = same[e] = false;
+            from[e] = nullptr;
+            if (i >= end) continue;
+            while (i >= start[b + 1]) ++b, page_of = -1;
+            own[e] = b;
             if (past[b] < 0) continue;
+            live[e] = true;
             pos[e] = past[b] + (i - start[b]);
-            const int p = pos[e] >> a.page_shift;
-            if (p != known) {
-                const int held = (past[b] + page - 1) >> a.page_shift;
-                const int pg = p < held ? *row(b, p) : *ring_at(first[b] + p - held);
-                known = p;
-                base = -1;
-                if (pg >= 0 && pg < a.n_pages) base = pg << a.page_shift;
-                else report(a.status, TWELL_ERR_DEVICE_CHECK);
-            }
-            if (base >= 0) slot[e] = base + (pos[e] & (page - 1));
+            const int p = pos[e] >> a.page_shift, held = (past[b] + page - 1) >> a.page_shift;
+            same[e] = e > 0 && p == page_of;
+            page_of = p;
+            if (!same[e]) from[e] = p < held ? row(b, p) : ring_at(first[b] + p - held);
         }
-        if (i0 + kPlanQuad <= a.M) {
-            *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-            *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            *reinterpret_cast<int4*>(a.owner + i0) = make_int4(own[0], own[1], own[2], own[3]);
+#pragma unroll
+        for (int e = 0; e < Q; ++e) {
+            pg[e] = from[e] != nullptr ? *from[e] : -1;
+            if (a.labels != nullptr && own[e] >= 0) own[e] = __ldg(a.labels + own[e]);
+        }
+        int slot[Q];
+#pragma unroll
+        for (int e = 0; e < Q; ++e) {
+            if (same[e]) pg[e] = pg[e - (e > 0)];
+            const bool is = live[e] && pg[e] >= 0 && pg[e] < a.n_pages;
+            if (live[e] && !is) report(a.status, TWELL_ERR_DEVICE_CHECK);
+            slot[e] = is ? (pg[e] << a.page_shift) + (pos[e] & (page - 1)) : -1;
+        }
+        if (Q % 4 == 0 && i0 + Q <= a.M) {
+#pragma unroll
+            for (int e = 0; e + 3 < Q; e += 4) {
+                *reinterpret_cast<int4*>(a.slots + i0 + e) = make_int4(slot[e], slot[e + 1], slot[e + 2], slot[e + 3]);
+                *reinterpret_cast<int4*>(a.positions + i0 + e) = make_int4(pos[e], pos[e + 1], pos[e + 2], pos[e + 3]);
+                *reinterpret_cast<int4*>(a.owner + i0 + e) = make_int4(own[e], own[e + 1], own[e + 2], own[e + 3]);
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < kPlanQuad; ++e)
+            for (int e = 0; e < Q; ++e)
                 if (i0 + e < a.M) {
                     a.slots[i0 + e] = slot[e];
                     a.positions[i0 + e] = pos[e];
@@ -259,13 +282,13 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
                 }
         }
     }
-    // pages taken, into the table
-    for (unsigned u = me; u < static_cast<unsigned>(taken); u += threads) {
+    // pages taken, into the table; by the last threads first, since the first ones have tokens
+    for (unsigned u = threads - 1 - me; u < static_cast<unsigned>(taken); u += threads) {
         const int j = static_cast<int>(u), b = last_at_most(first, a.B, j);
         *row(b, ((past[b] + page - 1) >> a.page_shift) + j - first[b]) = *ring_at(j);
     }
     // pages given back, behind the free ones
-    for (unsigned u = me; u < static_cast<unsigned>(given); u += threads) {
+    for (unsigned u = threads - 1 - me; u < static_cast<unsigned>(given); u += threads) {
         const int j = static_cast<int>(u), b = last_at_most(back, a.B, j);
         const int pg = *row(b, j - back[b]);
         if (pg < 0 || pg >= a.n_pages) report(a.status, TWELL_ERR_DEVICE_CHECK);
@@ -273,18 +296,25 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
     }
 }
 
-// Up to four blocks an SM, so that long prompts are done in one round.
-template <int PER, int THREADS, bool WARP>
-twell_status run_plan(const PlanArgs& a, int sms, cudaStream_t s)
+// The page of a token waits for the sums, so that a step is quickest with one token a thread, as far as one block an SM goes (16
+// requests: 2.8 us, with four 4.1); beyond that a thread takes four, most of which share a page (924000 tokens: 7.3 us, 7.8 with
+// eight, 18.8 with one).
+template <int PER, int THREADS, bool WARP, int Q>
+twell_status launch_plan(const PlanArgs& a, long long blocks, cudaStream_t s)
 {
-    auto kern = kv_plan_kernel<PER, THREADS, WARP>;
+    auto kern = kv_plan_kernel<PER, THREADS, WARP, Q>;
     static std::atomic<uint64_t> allowed{0};
     constexpr size_t kMost = (4 * (WARP ? 32 * PER : PER * THREADS) + 1) * sizeof(int);
     if (twell_host::allow_smem(kern, kMost, allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    const long long quads = (static_cast<long long>(a.M) + kPlanQuad - 1) / kPlanQuad, want = (quads + THREADS - 1) / THREADS;
-    const long long most = sms * kPlanBlocks;
-    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most)), dim3(THREADS),
+    return twell_host::launch_dep(kern, dim3(static_cast<unsigned>(std::max(blocks, 1ll))), dim3(THREADS),
                                   (4 * static_cast<size_t>(a.B) + 1) * sizeof(int), s, a);
+}
+template <int PER, int THREADS, bool WARP>
+twell_status run_plan(const PlanArgs& a, int sms, cudaStream_t s)
+{
+    const long long ones = (static_cast<long long>(a.M) + THREADS - 1) / THREADS, most = static_cast<long long>(sms) * kPlanBlocks;
+    if (ones <= sms) return launch_plan<PER, THREADS, WARP, 1>(a, ones, s);
+    return launch_plan<PER, THREADS, WARP, 4>(a, std::min((ones + 3) / 4, most), s);
 }
 
 }  // namespace
@@ -320,6 +350,7 @@ extern "C" twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page
     DevInfo dev;
     if (dev_info(&dev) != TWELL_OK) return TWELL_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (B <= 32) return twell::run_plan<1, 256, true>(a, dev.sm_count, s);
     if (B <= 32 * twell::kPlanWarpPer) return twell::run_plan<twell::kPlanWarpPer, 256, true>(a, dev.sm_count, s);
     if (B <= 512) return twell::run_plan<1, 512, false>(a, dev.sm_count, s);
     return twell::run_plan<twell::kPlanMaxSeqs / 512, 512, false>(a, dev.sm_count, s);
