@@ -33,7 +33,8 @@ struct LoraArgs {
     int32_t* status;
     int64_t ldx, ldy, ldo;
     int L, R, k, n, N;
-    // of larger batches: the number of tiles, then a tile's adapter, first place in `order`, tokens
+    // of larger batches: the number of tiles, then a tile's adapter, first row in t, tokens, and their numbers, a place for each
+    // that a tile can have
     const int32_t* n_tiles;
     const int4* tiles;
     const int32_t* order;
@@ -55,9 +56,11 @@ struct LoraShape {
     static constexpr int kIn = (2 * MT + RT) * 512;                              // a stage of the first product: 32 columns
     static constexpr int kOut = 2 * MT * 512 + 4 * (kRanks / kBlock) * kBlock * 16;  // of the second: 32 columns of y and B's rows
     static constexpr int kWarpSums = kTok * kWarpRanks * 4;
-    // room for three stages of the first product at least, and for kMinOut of the second beside the sums
-    static constexpr int kMinOut = RG == 1 ? 2 : 1;
-    static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut) : (MT == 2 ? 12 : 24) * 1024;
+    // room for three stages of the first product at least, and for kMinOut of the second beside the sums: a part of 512 columns
+    // is two of them, on their way while t is put together
+    static constexpr int kMinOut = RG == 4 ? 1 : 2;
+    static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut)
+                                      : (MT == 1 ? 6 : MT == 2 ? 12 : 24) * 1024;
     static constexpr int kInStages = kRing / kIn > 4 ? 4 : kRing / kIn;
     static constexpr int kOutStages = (kRing - kWarpSums) / kOut > 4 ? 4 : (kRing - kWarpSums) / kOut;
     static constexpr int kFragBytes = MT * kFrags * 2 * 512;
@@ -78,7 +81,7 @@ template <int MT, int RG, int RT>
 struct LoraOutShape {
     using In = LoraShape<MT, RG, RT, false>;
     static constexpr int kRanks = In::kRanks, kBlock = In::kBlock, kFrags = In::kFrags, kStage = In::kOut;
-    static constexpr int kRing = (MT == 2 ? 12 : 24) * 1024;
+    static constexpr int kRing = (MT == 1 ? (RG == 4 ? 18 : RG == 2 ? 10 : 6) : MT == 2 ? 12 : 24) * 1024;
     static constexpr int kStages = kRing / kStage;
     static constexpr size_t kBytes = kLoraWarps * kRing + In::kFragBytes;
 };
@@ -110,6 +113,11 @@ __device__ __forceinline__ uint2 lds8(uint32_t at)
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at));
     return r;
 }
+
+// The two halves of pdl_begin. A kernel that lets the next one start only after its own wait lets that one read, before it waits
+// in turn, whatever was there before this kernel.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void cluster_arrive()
 {
@@ -144,51 +152,162 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     lo = bf16x2_rn(fabsf(ha) <= 3.4e38f ? a - ha : 0.0f, fabsf(hb) <= 3.4e38f ? b - hb : 0.0f);
 }
 
-// The tile of cluster `index` among those of at most kLoraSmallN tokens: tokens are taken in their order by one warp, each is
-// given its number among those of its adapter, and every kTok-th of these begins a tile. All blocks of a cluster find the
-// same. `count` has a place for each adapter.
-template <int TOK>
-__device__ __forceinline__ void lora_find(const LoraArgs& g, int index, int* count, uint16_t* number, int* tok, int& id, int& tokens)
+// How many rows of adapter `id` count (0 for none, and where that number cannot be, which is recorded).
+__device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
 {
-    __shared__ int found[2];  // adapter, number of the tile's first token
-    __shared__ int own[kLoraSmallN];
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
-    for (int i = tid; i < g.N; i += kLoraThreads) {
-        own[i] = lora_id(g, g.ids[i]);
-        count[own[i]] = 0;
+    if (id >= g.L) return 0;
+    const int rank = g.ranks ? __ldg(g.ranks + id) : g.R;
+    if (rank >= 0 && rank <= g.R) return rank;
+    report(g.status, TWELL_ERR_DEVICE_CHECK);
+    return 0;
+}
+
+// A tile of tokens of one adapter.
+struct LoraTile {
+    int id, rank;    // id -1: there is no such tile
+    int first;       // its first row in t
+    int tokens;
+};
+
+// Tile `index` among those of at most kLoraSmallN tokens: adapters in the order of their first tokens, each one's tokens in their
+// own, TOK a tile; everyone who looks for a tile finds the same. Up to 32 tokens every warp does it by itself. More are
+// counted by adapter in shared memory, with the least of each one's tokens (sums and minima: in any order the same), and the
+// tiles before a token's are a scan over the tokens. Returns the tile's tokens, -1 past the last. `scratch`:
+// kLoraFindBytes, free again afterwards.
+constexpr size_t kLoraFindBytes = 2 * sizeof(int) * (kLoraMaxAdapters + 1);
+template <int TOK>
+__device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, void* scratch, LoraTile& tile)
+{
+    __shared__ int tok[kLoraWarps][TOK];
+    __shared__ int found[3];  // adapter, number of the tile's first token, rank
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    tile.id = -1;
+    tile.first = index * TOK;
+    if (g.N <= 32) {
+        const int mine = lane < g.N ? lora_id(g, g.ids[lane]) : -1;
+        const int rank = mine >= 0 ? lora_rank(g, mine) : 0;
+        const unsigned same = __match_any_sync(0xffffffffu, mine), below = (1u << lane) - 1;
+        const int num = __popc(same & below);
+        const unsigned firsts = __ballot_sync(0xffffffffu, mine >= 0 && num % TOK == 0);
+        const unsigned it = __ballot_sync(0xffffffffu, (firsts >> lane & 1) && __popc(firsts & below) == index);
+        if (lane < TOK) tok[warp][lane] = -1;
+        __syncwarp();
+        if (it == 0) return nullptr;
+        const int from = __ffs(it) - 1, base = __shfl_sync(0xffffffffu, num, from);
+        tile.id = __shfl_sync(0xffffffffu, mine, from);
+        tile.rank = __shfl_sync(0xffffffffu, rank, from);
+        tile.tokens = min(__popc(__shfl_sync(0xffffffffu, same, from)) - base, TOK);
+        if (mine == tile.id && num >= base && num < base + TOK) tok[warp][num - base] = lane;
+        __syncwarp();
+        return tok[warp];
     }
+    constexpr int kPer = kLoraSmallN / kLoraThreads;  // tokens a thread; of a warp 32 adjacent ones at a time
+    static_assert(kPer * kLoraWarps <= 32, "a warp adds up the totals");
+    __shared__ int totals[2][32];              // tiles of each 32 tokens; tokens of the adapter
+    int2* bins = static_cast<int2*>(scratch);  // [L + 1]: tokens of an adapter, the first of them
+    int own[kPer], rank[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) own[j] = j * kLoraThreads + tid < g.N ? __ldg(g.ids + j * kLoraThreads + tid) : 0;
+    for (int i = tid; i <= g.L; i += kLoraThreads) bins[i] = make_int2(0, INT32_MAX);
     if (tid == 0) found[0] = -1;
-    if (tid < TOK) tok[tid] = -1;
+    if (tid < TOK) tok[0][tid] = -1;
     __syncthreads();
-    if (tid < 32) {
-        int tiles = 0;
-        for (int i0 = 0; i0 < g.N; i0 += 32) {
-            const int i = i0 + lane;
-            const int mine = i < g.N ? own[i] : -1;
-            const unsigned same = __match_any_sync(0xffffffffu, mine);
-            const int before = __popc(same & ((1u << lane) - 1));
-            const int num = mine >= 0 ? count[mine] + before : 1;
-            __syncwarp();
-            if (mine >= 0) {
-                number[i] = static_cast<uint16_t>(num);
-                if (before == 0) count[mine] += __popc(same);
-            }
-            const unsigned first = __ballot_sync(0xffffffffu, num % TOK == 0);
-            if ((first >> lane & 1) && tiles + __popc(first & ((1u << lane) - 1)) == index) {
-                found[0] = mine;
-                found[1] = num;
-            }
-            tiles += __popc(first);
-            __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = j * kLoraThreads + tid;
+        own[j] = i < g.N ? lora_id(g, own[j]) : -1;
+        rank[j] = own[j] >= 0 && own[j] < g.L && g.ranks ? __ldg(g.ranks + own[j]) : g.R;  // on its way while the tiles are counted
+        const unsigned same = __match_any_sync(0xffffffffu, own[j]);
+        if (i < g.N && (same & ((1u << lane) - 1)) == 0) {
+            atomicAdd(&bins[own[j]].x, __popc(same));
+            atomicMin(&bins[own[j]].y, i);
         }
     }
     __syncthreads();
-    id = found[0];
-    if (id < 0) return;
-    tokens = min(count[id] - found[1], TOK);
-    for (int i = tid; i < g.N; i += kLoraThreads)
-        if (own[i] == id && static_cast<unsigned>(number[i] - found[1]) < static_cast<unsigned>(TOK)) tok[number[i] - found[1]] = i;
+    int tiles[kPer], before[kPer];  // that begin with this token; before it in its 32
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = j * kLoraThreads + tid;
+        tiles[j] = 0;
+        if (own[j] >= 0) {
+            const int2 bin = bins[own[j]];
+            if (bin.y == i) tiles[j] = (bin.x + TOK - 1) / TOK;
+        }
+        int incl = tiles[j];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        before[j] = incl - tiles[j];
+        if (lane == 31) totals[0][j * kLoraWarps + warp] = incl;
+    }
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int at = before[j] + __reduce_add_sync(0xffffffffu, lane < j * kLoraWarps + warp ? totals[0][lane] : 0);
+        if (index >= at && index < at + tiles[j]) {
+            found[0] = own[j];
+            found[1] = (index - at) * TOK;
+            found[2] = own[j] == g.L ? 0 : rank[j];
+        }
+    }
+    __syncthreads();
+    tile.id = found[0];
+    if (tile.id < 0) return nullptr;
+    tile.tokens = min(bins[tile.id].x - found[1], TOK);
+    tile.rank = found[2];
+    if (tile.rank < 0 || tile.rank > g.R) {
+        report(g.status, TWELL_ERR_DEVICE_CHECK);
+        tile.rank = 0;
+    }
+    unsigned mine[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        mine[j] = __ballot_sync(0xffffffffu, own[j] == tile.id);
+        if (lane == 0) totals[1][j * kLoraWarps + warp] = __popc(mine[j]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int num = __popc(mine[j] & ((1u << lane) - 1)) - found[1] +
+                        __reduce_add_sync(0xffffffffu, lane < j * kLoraWarps + warp ? totals[1][lane] : 0);
+        if (own[j] == tile.id && num >= 0 && num < TOK) tok[0][num] = j * kLoraThreads + tid;
+    }
+    __syncthreads();
+    return tok[0];
+}
+
+// Tile `index` of a batch, and the tokens of this lane's rows.
+template <int MT, bool FIND>
+__device__ __forceinline__ bool lora_tile(const LoraArgs& g, int index, uint8_t* smem, LoraTile& tile, int (&token)[MT][2])
+{
+    const int gr = (threadIdx.x & 31) >> 2;
+    if constexpr (FIND) {
+        const int* tok = lora_find<16 * MT>(g, index, smem, tile);
+        if (tile.id < 0) return false;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) token[m][s] = tok[16 * m + 8 * s + gr];
+        __syncthreads();  // the memory is free
+    } else {
+        // requested together: what lies past the last tile is some earlier call's
+        const int n = *g.n_tiles;
+        const int4 t = g.tiles[index];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) token[m][s] = g.order[index * 16 * MT + 16 * m + 8 * s + gr];
+        if (index >= n) return false;
+        tile = LoraTile{t.x, lora_rank(g, t.x), t.y, t.z};
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (16 * m + 8 * s + gr >= tile.tokens) token[m][s] = -1;
+    }
+    return true;
 }
 
 // t = A x over one block's part of k: a warp has kWarpRanks ranks and every kWays-th 64 columns, 32 a stage. Leaves the warps'
@@ -288,15 +407,6 @@ __device__ __forceinline__ uint4 lora_parts(const float4& v, int r0, int rank, f
     split2(r0 < rank ? v.x * scale : 0.0f, r0 + 1 < rank ? v.y * scale : 0.0f, o.x, o.z);
     split2(r0 + 2 < rank ? v.z * scale : 0.0f, r0 + 3 < rank ? v.w * scale : 0.0f, o.y, o.w);
     return o;
-}
-
-__device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
-{
-    if (id >= g.L) return 0;
-    const int rank = g.ranks ? __ldg(g.ranks + id) : g.R;
-    if (rank >= 0 && rank <= g.R) return rank;
-    report(g.status, TWELL_ERR_DEVICE_CHECK);
-    return 0;
 }
 
 // y + B t over 32-column pieces nt0, nt0 + 1, ... nt1 - 1 of a block, of which a warp takes every kLoraWarps-th, through STAGES
@@ -409,31 +519,25 @@ struct LoraOut {
     }
 };
 
-// A batch of at most kLoraSmallN tokens, whole.
+// A batch of few tiles, whole.
 template <int MT, int RG, int RT>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
+__global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
 {
     using S = LoraShape<MT, RG, RT, true>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
-    __shared__ int tok[S::kTok];
     pdl_begin();
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2, c = lane & 3;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2;
     const int blocks = static_cast<int>(cluster_blocks()), part = static_cast<int>(cluster_ctarank());
-    const int index = static_cast<int>(blockIdx.x) / blocks;
-    int id, tokens = 0;
-    {
-        // the counts and numbers lie where the rings come later
-        int* count = reinterpret_cast<int*>(lora_smem);
-        lora_find<S::kTok>(g, index, count, reinterpret_cast<uint16_t*>(count + g.L + 1), tok, id, tokens);
-        if (id < 0) return;
-    }
-    const int rank = lora_rank(g, id);
+    LoraTile tile;
+    const int* tok = lora_find<S::kTok>(g, static_cast<int>(blockIdx.x) / blocks, lora_smem, tile);  // where the rings come later
+    if (tile.id < 0) return;
+    const int id = tile.id, rank = tile.rank;
     const int nt_all = (g.n + 31) / 32, nt0 = static_cast<int>(static_cast<long long>(nt_all) * part / blocks),
               nt1 = static_cast<int>(static_cast<long long>(nt_all) * (part + 1) / blocks);
     if (rank == 0) {  // the same for all blocks of the cluster
         if (g.y == g.out) return;
         const int col0 = nt0 * 4, cols = min(nt1 * 4, g.n / 8) - col0;  // in chunks of 8
-        for (int i = tid; i < tokens * cols; i += kLoraThreads) {
+        for (int i = tid; i < tile.tokens * cols; i += kLoraThreads) {
             const int t = tok[i / cols], col = (col0 + i % cols) * 8;
             *reinterpret_cast<uint4*>(g.out + t * g.ldo + col) = *reinterpret_cast<const uint4*>(g.y + t * g.ldy + col);
         }
@@ -499,36 +603,37 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraArgs g)
     out.template run<S::kOutStages>(frags);
 }
 
-// t of a larger batch: a tile's rows of it, as lora_parts has them, at the tokens' places in `order`. A cluster of blocks shares a
-// tile's k where tiles are few; each then adds up a share of the sums.
-template <int MT, int RG, int RT>
-__global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out)
+// t of a batch: a tile's rows of it, as lora_parts has them. A cluster of blocks shares a tile's k where tiles are few; each then
+// adds up a share of the sums. With FIND each block of a tile leaves its own sums, [tile][part][token][rank], for the second
+// product to add up: its blocks need not start together.
+template <int MT, int RG, int RT, bool FIND>
+__global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out, int most_tiles)
 {
     using S = LoraShape<MT, RG, RT, false>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
-    pdl_begin();
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2;
-    const int blocks = static_cast<int>(cluster_blocks()), part = static_cast<int>(cluster_ctarank());
-    const int index = static_cast<int>(blockIdx.x) / blocks;
-    if (index >= *g.n_tiles) return;
-    const int4 tile = g.tiles[index];
-    const int rank = lora_rank(g, tile.x);
-    if (rank == 0) return;
-    if (blocks > 1) cluster_arrive();
+    pdl_wait();
+    pdl_next();
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
+    const int blocks = FIND ? static_cast<int>(gridDim.x) / most_tiles : static_cast<int>(cluster_blocks());
+    const int index = FIND ? static_cast<int>(blockIdx.x) % most_tiles : static_cast<int>(blockIdx.x) / blocks;
+    const int part = FIND ? static_cast<int>(blockIdx.x) / most_tiles : static_cast<int>(cluster_ctarank());
     int token[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int i = 16 * m + 8 * s + gr;
-            token[m][s] = i < tile.z ? __ldg(g.order + tile.y + i) : -1;
-        }
-    const float scale = __ldg(g.scale + tile.x);
-    lora_shrink<S, MT, RG, RT>(g, tile.x, rank, part, blocks, token, lora_smem + warp * S::kRing, [] {});
+    LoraTile tile;
+    if (!lora_tile<MT, FIND>(g, index, lora_smem, tile, token)) return;
+    const int rank = tile.rank;
+    if (rank == 0) return;
+    if (!FIND && blocks > 1) cluster_arrive();
+    const float scale = __ldg(g.scale + tile.id);
+    lora_shrink<S, MT, RG, RT>(g, tile.id, rank, part, blocks, token, lora_smem + warp * S::kRing, [] {});
     __syncthreads();
     constexpr int kQuads = S::kRanks / 4;
+    if constexpr (FIND) {
+        float4* to = reinterpret_cast<float4*>(t_out) + (static_cast<size_t>(index) * blocks + part) * (S::kTok * kQuads);
+        for (int i = tid; i < tile.tokens * kQuads; i += kLoraThreads) to[i] = lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads);
+        return;
+    }
     auto store = [&](int row, int quad, const float4& v) {
-        if (row < tile.z) t_out[static_cast<size_t>(tile.y + row) * kQuads + quad] = lora_parts(v, 4 * quad, rank, scale);
+        if (row < tile.tokens) t_out[static_cast<size_t>(tile.first + row) * kQuads + quad] = lora_parts(v, 4 * quad, rank, scale);
     };
     if (blocks == 1) {
         for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads)
@@ -554,33 +659,33 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_in_kernel(
     }
 }
 
-// y + B t of a larger batch: a block has a tile's rows and a part of the columns, of which a warp takes every kLoraWarps-th 32.
-template <int MT, int RG, int RT>
-__global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_out_kernel(const LoraArgs g, const uint4* __restrict__ t_in, int most_tiles)
+// y + B t of a batch: a block has a tile's rows and a part of the columns, of which a warp takes every kLoraWarps-th 32. What it
+// reads but t was there before the first product's kernel, which lets this one start after its own wait: the first pieces
+// are on their way while that one runs. `in_parts`: of a tile's sums, with FIND.
+template <int MT, int RG, int RT, bool FIND>
+__global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_out_kernel(const LoraArgs g, const uint4* t_in, int most_tiles, int in_parts)
 {
     using S = LoraOutShape<MT, RG, RT>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
-    pdl_begin();
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2, c = lane & 3;
-    const int index = static_cast<int>(blockIdx.x % static_cast<unsigned>(most_tiles));
-    const int part = static_cast<int>(blockIdx.x / static_cast<unsigned>(most_tiles)), parts = static_cast<int>(gridDim.x / static_cast<unsigned>(most_tiles));
-    if (index >= *g.n_tiles) return;
-    const int4 tile = g.tiles[index];
-    const int rank = lora_rank(g, tile.x);
-    if (rank == 0 && g.y == g.out) return;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
+    const int index = static_cast<int>(blockIdx.x) % most_tiles, part = static_cast<int>(blockIdx.x) / most_tiles,
+              parts = static_cast<int>(gridDim.x) / most_tiles;
     int token[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int i = 16 * m + 8 * s + gr;
-            token[m][s] = i < tile.z ? __ldg(g.order + tile.y + i) : -1;
-        }
+    LoraTile tile;
+    const bool is = lora_tile<MT, FIND>(g, index, lora_smem, tile, token);
+    if (!is || (tile.rank == 0 && g.y == g.out)) {
+        if (blockIdx.x == 0) pdl_wait();  // one block is enough for the grid not to be done before the one before it
+        return;
+    }
+    const int rank = tile.rank;
     const int nt_all = (g.n + 31) / 32, nt0 = static_cast<int>(static_cast<long long>(nt_all) * part / parts),
               nt1 = static_cast<int>(static_cast<long long>(nt_all) * (part + 1) / parts);
-    const LoraOut<MT, RG, RT> out(g, tile.x, rank, nt0, nt1, token, lora_smem + warp * S::kRing);
+    const LoraOut<MT, RG, RT> out(g, tile.id, rank, nt0, nt1, token, lora_smem + warp * S::kRing);
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) out.template request<S::kStages>(i, i);
+    const float scale = FIND && rank > 0 ? __ldg(g.scale + tile.id) : 0.0f;
+    pdl_wait();
+    pdl_next();
     // t as the product's fragments
     uint4* frags = reinterpret_cast<uint4*>(lora_smem + kLoraWarps * S::kRing);
     constexpr int kQuads = S::kRanks / 4;
@@ -593,7 +698,19 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_out_kernel
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 t[s] = make_uint4(0u, 0u, 0u, 0u);
-                if (row + 8 * s < tile.z) t[s] = __ldg(t_in + static_cast<size_t>(tile.y + row + 8 * s) * kQuads + quad);
+                if (row + 8 * s >= tile.tokens) continue;
+                if constexpr (FIND) {
+                    const float4* from = reinterpret_cast<const float4*>(t_in) + static_cast<size_t>(index) * in_parts * (16 * MT * kQuads) +
+                                         (row + 8 * s) * kQuads + quad;
+                    float4 v = __ldcg(from);
+                    for (int p = 1; p < in_parts; ++p) {
+                        const float4 u = __ldcg(from + p * (16 * MT * kQuads));
+                        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+                    }
+                    t[s] = lora_parts(v, 4 * quad, rank, scale);
+                } else {
+                    t[s] = __ldcg(t_in + static_cast<size_t>(tile.first + row + 8 * s) * kQuads + quad);
+                }
             }
             frags[((m * S::kFrags + f) * 2 + 0) * 32 + l] = make_uint4(t[0].x, t[1].x, t[0].y, t[1].y);
             frags[((m * S::kFrags + f) * 2 + 1) * 32 + l] = make_uint4(t[0].z, t[1].z, t[0].w, t[1].w);
@@ -602,8 +719,8 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 2 ? 2 : 1) lora_out_kernel
     out.template run<S::kStages>(frags);
 }
 
-// The tiles of a larger batch: tokens counted by adapter, each adapter's given adjacent places in `order`, and a tile for each
-// tile_tokens of these. One block: the counts are in its shared memory, and a pass's ids are 64 KB, all requested before the
+// The tiles of a larger batch: tokens counted by adapter, a tile for each tile_tokens of an adapter's, and
+// their places in it in `order`. One block: the counts are in its shared memory, and a pass's ids are 64 KB, all requested before the
 // first is counted. Which token of an adapter comes first is left to chance; a token's result does not depend on it.
 __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int tile_tokens, int32_t* n_tiles,
                                                                        int4* tiles, int32_t* order)
@@ -666,7 +783,10 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
 #pragma unroll
     for (int r = 0; r < kPer; ++r) {
         if (r * kLoraGroupThreads >= g.N) break;
-        if (v[r] >= 0) order[count[v[r] >> 16] + (v[r] & 0xffff)] = r * kLoraGroupThreads + tid;
+        if (v[r] >= 0) {
+            const int l = v[r] >> 16, num = v[r] & 0xffff;
+            order[(first_tile[l] + num / tile_tokens) * tile_tokens + num % tile_tokens] = r * kLoraGroupThreads + tid;
+        }
     }
     for (int j = tid; j < s_tiles; j += kLoraGroupThreads) {
         int l = 0, len = g.L + 1;  // the last adapter whose tiles begin at j or before
@@ -707,84 +827,106 @@ twell_status launch_lora(void (*kern)(KArgs...), int clusters, int blocks, size_
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
-// Most blocks a tile whose sums fit an SM, and two of them where one block's do.
+// Most blocks a tile whose sums fit an SM, with `two` two of them where one block's do.
 template <typename S>
-constexpr int most_blocks()
+constexpr int most_blocks(bool two)
 {
     int b = kLoraCluster;
-    while (b > 1 && S::bytes(b) > (S::bytes(1) <= 108u * 1024u ? 108u : 222u) * 1024u) b /= 2;
+    while (b > 1 && S::bytes(b) > (two && S::bytes(1) <= 108u * 1024u ? 108u : 222u) * 1024u) b /= 2;
     return b;
 }
 
 // Tiles of N tokens, at most.
 long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / tok + std::min(N, L + 1)); }
 
-template <int RG, int RT>
-twell_status run_small(const LoraArgs& g, int sms, cudaStream_t s)
-{
-    using S = LoraShape<1, RG, RT, true>;
-    constexpr int kMost = most_blocks<S>();
-    constexpr size_t kFind = sizeof(int) * (kLoraMaxAdapters + 1) + sizeof(uint16_t) * kLoraSmallN;
-    static_assert(kFind <= kLoraWarps * S::kRing, "the counts and numbers lie where the rings come later");
-    const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    int blocks = kMost;
-    while (blocks > 1 && tiles * blocks > 2 * sms - sms / 8) blocks /= 2;
-    auto kern = lora_kernel<1, RG, RT>;
-    static std::atomic<uint64_t> allowed{0};
-    if (twell_host::allow_smem(kern, S::bytes(kMost), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    return launch_lora(kern, tiles, blocks, S::bytes(blocks), s, g);
-}
-
-// Of the larger batches: what the workspace holds of a pass.
-constexpr int kLoraTile = 32;  // least tokens of a tile
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+// Tokens of a tile: 64 above rank 32, where the weights of a tile are as many bytes as its rows of y.
+constexpr int lora_tile_tokens(int N, int R) { return N <= kLoraSmallN ? 16 : R <= 32 ? 32 : 64; }
+
+// Blocks of a tile that share its k where each leaves its own sums: at most kLoraParts, and kLoraSums of all tiles.
+constexpr int kLoraParts = 8, kLoraSums = 1024;
+int lora_parts_of(int tiles, int sms) { return std::max(1, std::min(std::min(kLoraParts, kLoraSums / tiles), 4 * sms / tiles)); }
+
+// What the workspace holds of a pass: of a larger batch its tiles and their tokens, and t.
 struct LoraWs {
     size_t tiles, order, t, total;
     LoraWs(int N, int R)
     {
-        const int n = std::min(N, kLoraPass);
+        const int n = std::min(N, kLoraPass), tok = lora_tile_tokens(N, R);
+        const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok));
+        const bool grouped = N > kLoraSmallN;
         tiles = 16;
-        order = tiles + 16 * static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, kLoraTile));
-        t = (order + sizeof(int32_t) * static_cast<size_t>(n) + 15) / 16 * 16;
-        total = t + static_cast<size_t>(n) * lora_ranks(R) * 4;
+        order = tiles + (grouped ? 16 * most : 0);
+        t = order + (grouped ? sizeof(int32_t) * tok * most : 0);
+        total = t + (grouped ? n : static_cast<size_t>(tok) * kLoraSums) * lora_ranks(R) * 4;
     }
 };
 
-template <int MT, int RG, int RT>
-twell_status run_pass(LoraArgs g, uint8_t* ws, int sms, cudaStream_t s)
+// The two products of a batch whose tiles are found (by FIND, or in g).
+template <int MT, int RG, int RT, bool FIND>
+twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
 {
     using S = LoraShape<MT, RG, RT, false>;
     using O = LoraOutShape<MT, RG, RT>;
-    static_assert(S::kTok >= kLoraTile, "the workspace has room for the tiles");
-    const LoraWs at(g.N, g.R);
+    static_assert(!FIND || (kLoraFindBytes <= kLoraWarps * S::kRing && kLoraFindBytes <= kLoraWarps * O::kRing), "room to find a tile");
+    const int most = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
+    constexpr int kMost = most_blocks<S>(true);
+    auto in = lora_in_kernel<MT, RG, RT, FIND>;
+    auto out = lora_out_kernel<MT, RG, RT, FIND>;
+    static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
+    if (twell_host::allow_smem(in, S::bytes(kMost), in_allowed) != TWELL_OK || twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK)
+        return TWELL_ERR_CUDA;
+    // a block's part of the columns: a ring's worth of pieces a warp, or more where the blocks would be more than kOutRounds an
+    // SM's place
+    constexpr int kOutRounds = 2;
+    const long long places = (MT == 4 ? 1ll : 2ll) * sms * kOutRounds, about = FIND ? most : std::max(1, g.N / S::kTok);
+    const int pieces = (g.n + 31) / 32, ring = kLoraWarps * O::kStages;
+    const long long parts = std::max(1ll, std::min<long long>((places + about - 1) / about, (pieces + (FIND ? ring - 1 : 0)) / ring));
+    if (most * parts > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
+    const dim3 out_blocks(static_cast<unsigned>(most * parts));
+    if constexpr (FIND) {
+        const int in_parts = lora_parts_of(most, sms);
+        const twell_status st = twell_host::launch_dep(in, dim3(static_cast<unsigned>(most * in_parts)), dim3(kLoraThreads), S::bytes(1), s,
+                                                       g, t, most);
+        if (st != TWELL_OK) return st;
+        return twell_host::launch_dep(out, out_blocks, dim3(kLoraThreads), O::kBytes, s, g, t, most, in_parts);
+    } else {
+        const int blocks = lora_blocks(about, sms, kMost);
+        const twell_status st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t, most);
+        if (st != TWELL_OK) return st;
+        return twell_host::launch_dep(out, out_blocks, dim3(kLoraThreads), O::kBytes, s, g, t, most, 0);
+    }
+}
+
+// At most kLoraSmallN tokens: where every tile can have eight SMs to itself, in one kernel; else in two, which share SMs and
+// whose blocks need not start together.
+template <int RG, int RT>
+twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
+{
+    using S = LoraShape<1, RG, RT, true>;
+    constexpr int kMost = most_blocks<S>(false);
+    static_assert(kLoraFindBytes <= kLoraWarps * S::kRing, "room to find a tile");
+    const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
+    if (tiles * kLoraCluster > sms) return run_products<1, RG, RT, true>(g, reinterpret_cast<uint4*>(ws + LoraWs(g.N, g.R).t), sms, s);
+    auto kern = lora_kernel<1, RG, RT>;
+    static std::atomic<uint64_t> allowed{0};
+    if (twell_host::allow_smem(kern, S::bytes(kMost), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    return launch_lora(kern, tiles, kMost, S::bytes(kMost), s, g);
+}
+
+template <int MT, int RG, int RT>
+twell_status run_pass(LoraArgs g, uint8_t* ws, const LoraWs& at, int sms, cudaStream_t s)
+{
     int32_t* n_tiles = reinterpret_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
     int32_t* order = reinterpret_cast<int32_t*>(ws + at.order);
-    uint4* t = reinterpret_cast<uint4*>(ws + at.t);
-    twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g, S::kTok,
-                                             n_tiles, tiles, order);
+    const twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g,
+                                                   16 * MT, n_tiles, tiles, order);
     if (st != TWELL_OK) return st;
     g.n_tiles = n_tiles;
     g.tiles = tiles;
     g.order = order;
-    const int most = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    constexpr int kMost = most_blocks<S>();
-    const int blocks = lora_blocks(g.N / S::kTok, sms, kMost);
-    auto in = lora_in_kernel<MT, RG, RT>;
-    static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
-    if (twell_host::allow_smem(in, S::bytes(kMost), in_allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t);
-    if (st != TWELL_OK) return st;
-    auto out = lora_out_kernel<MT, RG, RT>;
-    if (twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    // a block's part of the columns: kOutRounds blocks an SM's place, but a ring's worth of pieces a warp at least
-    constexpr int kOutRounds = 2;
-    const long long places = (MT == 2 ? 2ll : 1ll) * sms * kOutRounds, tiles_about = std::max(1, g.N / S::kTok);
-    const int nt = (g.n + 31) / 32;
-    const int parts = static_cast<int>(std::max<long long>(1, std::min<long long>((places + tiles_about - 1) / tiles_about, nt / (kLoraWarps * O::kStages))));
-    const long long out_blocks = static_cast<long long>(most) * parts;
-    if (out_blocks > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
-    return twell_host::launch_dep(out, dim3(static_cast<unsigned>(out_blocks)), dim3(kLoraThreads), O::kBytes, s, g, t, most);
+    return run_products<MT, RG, RT, false>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
 }
 
 }  // namespace
@@ -794,7 +936,7 @@ using namespace twell_host;
 
 size_t twell_host::lora_ws_bytes(int N, int R)
 {
-    return N <= twell::kLoraSmallN || R > twell::kLoraMaxRank ? 0 : twell::LoraWs(N, R).total;
+    return N == 0 || R > twell::kLoraMaxRank ? 0 : twell::LoraWs(N, R).total;
 }
 
 extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const twell_adapters* ad,
@@ -828,23 +970,24 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
     twell::LoraArgs g = {static_cast<const bf*>(ad->a), static_cast<const bf*>(ad->b), static_cast<const bf*>(x),
                          static_cast<const bf*>(y), static_cast<bf*>(out), ad->scale, ad->ranks, ids, dev_status,
                          ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, nullptr, nullptr, nullptr};
+    uint8_t* w = static_cast<uint8_t*>(ws);
     if (N <= twell::kLoraSmallN)
-        return ad->rank <= 16   ? twell::run_small<1, 2>(g, dev.sm_count, s)
-               : ad->rank <= 32 ? twell::run_small<1, 4>(g, dev.sm_count, s)
-               : ad->rank <= 64 ? twell::run_small<2, 4>(g, dev.sm_count, s)
-                                : twell::run_small<4, 4>(g, dev.sm_count, s);
-    for (int at = 0; at < N; at += twell::kLoraPass) {
+        return ad->rank <= 16   ? twell::run_small<1, 2>(g, w, dev.sm_count, s)
+               : ad->rank <= 32 ? twell::run_small<1, 4>(g, w, dev.sm_count, s)
+               : ad->rank <= 64 ? twell::run_small<2, 4>(g, w, dev.sm_count, s)
+                                : twell::run_small<4, 4>(g, w, dev.sm_count, s);
+    const twell::LoraWs at(N, ad->rank);
+    for (int from = 0; from < N; from += twell::kLoraPass) {
         twell::LoraArgs p = g;
-        p.N = N - at < twell::kLoraPass ? N - at : twell::kLoraPass;
-        p.ids += at;
-        p.x += at * ldx;
-        p.y += at * ldy;
-        p.out += at * ldo;
-        uint8_t* w = static_cast<uint8_t*>(ws);
-        const twell_status st = ad->rank <= 16   ? twell::run_pass<2, 1, 2>(p, w, dev.sm_count, s)
-                                : ad->rank <= 32 ? twell::run_pass<2, 1, 4>(p, w, dev.sm_count, s)
-                                : ad->rank <= 64 ? twell::run_pass<4, 2, 4>(p, w, dev.sm_count, s)
-                                                 : twell::run_pass<4, 4, 4>(p, w, dev.sm_count, s);
+        p.N = N - from < twell::kLoraPass ? N - from : twell::kLoraPass;
+        p.ids += from;
+        p.x += from * ldx;
+        p.y += from * ldy;
+        p.out += from * ldo;
+        const twell_status st = ad->rank <= 16   ? twell::run_pass<2, 1, 2>(p, w, at, dev.sm_count, s)
+                                : ad->rank <= 32 ? twell::run_pass<2, 1, 4>(p, w, at, dev.sm_count, s)
+                                : ad->rank <= 64 ? twell::run_pass<4, 2, 4>(p, w, at, dev.sm_count, s)
+                                                 : twell::run_pass<4, 4, 4>(p, w, at, dev.sm_count, s);
         if (st != TWELL_OK) return st;
     }
     return TWELL_OK;
