@@ -22,6 +22,8 @@ constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraCluster = 8;      // most blocks a tile
 constexpr int kLoraSmallN = 512;     // up to here every cluster finds its tile from the ids itself
+constexpr int kLoraParts = 4;         // most blocks of a tile that share its k where each leaves its own sums,
+constexpr int kLoraSums = 1024;       // and of all tiles
 constexpr int kLoraGroupThreads = 1024;
 constexpr int kLoraPass = 16384;     // tokens of a larger batch that go together
 
@@ -615,8 +617,7 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_in_kernel(
     pdl_next();
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
     const int blocks = FIND ? static_cast<int>(gridDim.x) / most_tiles : static_cast<int>(cluster_blocks());
-    const int index = FIND ? static_cast<int>(blockIdx.x) % most_tiles : static_cast<int>(blockIdx.x) / blocks;
-    const int part = FIND ? static_cast<int>(blockIdx.x) / most_tiles : static_cast<int>(cluster_ctarank());
+    const int index = static_cast<int>(blockIdx.x) / blocks, part = static_cast<int>(blockIdx.x) % blocks;  // of a cluster: the rank
     int token[MT][2];
     LoraTile tile;
     if (!lora_tile<MT, FIND>(g, index, lora_smem, tile, token)) return;
@@ -668,8 +669,8 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_out_kernel
     using S = LoraOutShape<MT, RG, RT>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
-    const int index = static_cast<int>(blockIdx.x) % most_tiles, part = static_cast<int>(blockIdx.x) / most_tiles,
-              parts = static_cast<int>(gridDim.x) / most_tiles;
+    const int parts = static_cast<int>(gridDim.x) / most_tiles, index = static_cast<int>(blockIdx.x) / parts,
+              part = static_cast<int>(blockIdx.x) % parts;
     int token[MT][2];
     LoraTile tile;
     const bool is = lora_tile<MT, FIND>(g, index, lora_smem, tile, token);
@@ -702,12 +703,14 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_out_kernel
                 if constexpr (FIND) {
                     const float4* from = reinterpret_cast<const float4*>(t_in) + static_cast<size_t>(index) * in_parts * (16 * MT * kQuads) +
                                          (row + 8 * s) * kQuads + quad;
-                    float4 v = __ldcg(from);
-                    for (int p = 1; p < in_parts; ++p) {
-                        const float4 u = __ldcg(from + p * (16 * MT * kQuads));
-                        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-                    }
-                    t[s] = lora_parts(v, 4 * quad, rank, scale);
+                    float4 u[kLoraParts];
+#pragma unroll
+                    for (int p = 0; p < kLoraParts; ++p)
+                        if (p < in_parts) u[p] = __ldcg(from + p * (16 * MT * kQuads));
+#pragma unroll
+                    for (int p = 1; p < kLoraParts; ++p)
+                        if (p < in_parts) u[0].x += u[p].x, u[0].y += u[p].y, u[0].z += u[p].z, u[0].w += u[p].w;
+                    t[s] = lora_parts(u[0], 4 * quad, rank, scale);
                 } else {
                     t[s] = __ldcg(t_in + static_cast<size_t>(tile.first + row + 8 * s) * kQuads + quad);
                 }
@@ -843,8 +846,7 @@ constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ?
 // Tokens of a tile: 64 above rank 32, where the weights of a tile are as many bytes as its rows of y.
 constexpr int lora_tile_tokens(int N, int R) { return N <= kLoraSmallN ? 16 : R <= 32 ? 32 : 64; }
 
-// Blocks of a tile that share its k where each leaves its own sums: at most kLoraParts, and kLoraSums of all tiles.
-constexpr int kLoraParts = 8, kLoraSums = 1024;
+// Blocks of a tile that share its k where each leaves its own sums.
 int lora_parts_of(int tiles, int sms) { return std::max(1, std::min(std::min(kLoraParts, kLoraSums / tiles), 4 * sms / tiles)); }
 
 // What the workspace holds of a pass: of a larger batch its tiles and their tokens, and t.
@@ -878,7 +880,7 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
         return TWELL_ERR_CUDA;
     // a block's part of the columns: a ring's worth of pieces a warp, or more where the blocks would be more than kOutRounds an
     // SM's place
-    constexpr int kOutRounds = 2;
+    constexpr int kOutRounds = FIND ? 1 : 2;
     const long long places = (MT == 4 ? 1ll : 2ll) * sms * kOutRounds, about = FIND ? most : std::max(1, g.N / S::kTok);
     const int pieces = (g.n + 31) / 32, ring = kLoraWarps * O::kStages;
     const long long parts = std::max(1ll, std::min<long long>((places + about - 1) / about, (pieces + (FIND ? ring - 1 : 0)) / ring));
