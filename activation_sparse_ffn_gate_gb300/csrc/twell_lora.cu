@@ -62,7 +62,7 @@ struct LoraShape {
     // is two of them, on their way while t is put together
     static constexpr int kMinOut = RG == 4 ? 1 : 2;
     static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut)
-                                      : (MT == 1 ? 6 : MT == 2 ? 12 : 24) * 1024;
+                                      : (MT == 1 ? 6 : 12) * 1024;
     static constexpr int kInStages = kRing / kIn > 4 ? 4 : kRing / kIn;
     static constexpr int kOutStages = (kRing - kWarpSums) / kOut > 4 ? 4 : (kRing - kWarpSums) / kOut;
     static constexpr int kFragBytes = MT * kFrags * 2 * 512;
@@ -83,7 +83,7 @@ template <int MT, int RG, int RT>
 struct LoraOutShape {
     using In = LoraShape<MT, RG, RT, false>;
     static constexpr int kRanks = In::kRanks, kBlock = In::kBlock, kFrags = In::kFrags, kStage = In::kOut;
-    static constexpr int kRing = (MT == 1 ? (RG == 4 ? 18 : RG == 2 ? 10 : 6) : MT == 2 ? 12 : 24) * 1024;
+    static constexpr int kRing = (MT == 1 ? (RG == 4 ? 18 : RG == 2 ? 10 : 6) : RG == 4 ? 20 : 12) * 1024;
     static constexpr int kStages = kRing / kStage;
     static constexpr size_t kBytes = kLoraWarps * kRing + In::kFragBytes;
 };
@@ -218,6 +218,8 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
     for (int j = 0; j < kPer; ++j) {
         const int i = j * kLoraThreads + tid;
         own[j] = i < g.N ? lora_id(g, own[j]) : -1;
+        rank[j] = 0;
+        if (j * kLoraThreads >= g.N) continue;
         rank[j] = own[j] >= 0 && own[j] < g.L && g.ranks ? __ldg(g.ranks + own[j]) : g.R;  // on its way while the tiles are counted
         const unsigned same = __match_any_sync(0xffffffffu, own[j]);
         if (i < g.N && (same & ((1u << lane) - 1)) == 0) {
@@ -230,7 +232,8 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int i = j * kLoraThreads + tid;
-        tiles[j] = 0;
+        tiles[j] = before[j] = 0;
+        if (j * kLoraThreads >= g.N) continue;
         if (own[j] >= 0) {
             const int2 bin = bins[own[j]];
             if (bin.y == i) tiles[j] = (bin.x + TOK - 1) / TOK;
@@ -247,6 +250,7 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+        if (j * kLoraThreads >= g.N) continue;
         const int at = before[j] + __reduce_add_sync(0xffffffffu, lane < j * kLoraWarps + warp ? totals[0][lane] : 0);
         if (index >= at && index < at + tiles[j]) {
             found[0] = own[j];
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
 // adds up a share of the sums. With FIND each block of a tile leaves its own sums, [tile][part][token][rank], for the second
 // product to add up: its blocks need not start together.
 template <int MT, int RG, int RT, bool FIND>
-__global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out, int most_tiles)
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out, int most_tiles)
 {
     using S = LoraShape<MT, RG, RT, false>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_in_kernel(
 // reads but t was there before the first product's kernel, which lets this one start after its own wait: the first pieces
 // are on their way while that one runs. `in_parts`: of a tile's sums, with FIND.
 template <int MT, int RG, int RT, bool FIND>
-__global__ void __launch_bounds__(kLoraThreads, MT == 4 ? 1 : 2) lora_out_kernel(const LoraArgs g, const uint4* t_in, int most_tiles, int in_parts)
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArgs g, const uint4* t_in, int most_tiles, int in_parts)
 {
     using S = LoraOutShape<MT, RG, RT>;
     extern __shared__ __align__(16) uint8_t lora_smem[];
@@ -745,7 +749,9 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
         if (r * kLoraGroupThreads >= g.N) break;
         const bool live = r * kLoraGroupThreads + tid < g.N;
         const int id = live ? lora_id(g, v[r]) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, id), below = same & ((1u << lane) - 1);
+        // most warps of a prompt have one adapter
+        const bool one = __all_sync(0xffffffffu, id == __shfl_sync(0xffffffffu, id, 0));
+        const unsigned same = one ? 0xffffffffu : __match_any_sync(0xffffffffu, id), below = same & ((1u << lane) - 1);
         int first = 0;
         if (live && below == 0) first = atomicAdd(count + id, __popc(same));
         first = __shfl_sync(0xffffffffu, first, __ffs(same) - 1);
@@ -843,8 +849,9 @@ constexpr int most_blocks(bool two)
 long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / tok + std::min(N, L + 1)); }
 
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
-// Tokens of a tile: 64 above rank 32, where the weights of a tile are as many bytes as its rows of y.
-constexpr int lora_tile_tokens(int N, int R) { return N <= kLoraSmallN ? 16 : R <= 32 ? 32 : 64; }
+// A larger batch's tiles have 32 tokens: with 64 their weights are read half as often, but a block takes an SM for itself (16384
+// tokens, 2048 x 2048, rank 64: 64.7 us and 73.6; rank 16, 2048 x 4096: 70 and 120).
+constexpr int kLoraMT = 2;
 
 // Blocks of a tile that share its k where each leaves its own sums.
 int lora_parts_of(int tiles, int sms) { return std::max(1, std::min(std::min(kLoraParts, kLoraSums / tiles), 4 * sms / tiles)); }
@@ -854,9 +861,9 @@ struct LoraWs {
     size_t tiles, order, t, total;
     LoraWs(int N, int R)
     {
-        const int n = std::min(N, kLoraPass), tok = lora_tile_tokens(N, R);
-        const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok));
         const bool grouped = N > kLoraSmallN;
+        const int n = std::min(N, kLoraPass), tok = grouped ? 16 * kLoraMT : 16;
+        const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok));
         tiles = 16;
         order = tiles + (grouped ? 16 * most : 0);
         t = order + (grouped ? sizeof(int32_t) * tok * most : 0);
@@ -878,12 +885,13 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
     static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
     if (twell_host::allow_smem(in, S::bytes(kMost), in_allowed) != TWELL_OK || twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK)
         return TWELL_ERR_CUDA;
-    // a block's part of the columns: a ring's worth of pieces a warp, or more where the blocks would be more than kOutRounds an
-    // SM's place
-    constexpr int kOutRounds = FIND ? 1 : 2;
-    const long long places = (MT == 4 ? 1ll : 2ll) * sms * kOutRounds, about = FIND ? most : std::max(1, g.N / S::kTok);
+    // a block's part of the columns: a ring's worth of pieces a warp at least, and one round of blocks, or kOutRounds where the tiles
+    // alone are more
+    constexpr int kOutRounds = 2;
+    const long long places = 2ll * sms, about = FIND ? most : std::max(1, g.N / S::kTok);
     const int pieces = (g.n + 31) / 32, ring = kLoraWarps * O::kStages;
-    const long long parts = std::max(1ll, std::min<long long>((places + about - 1) / about, (pieces + (FIND ? ring - 1 : 0)) / ring));
+    const long long fill = most <= places ? places / most : (kOutRounds * places + about - 1) / about;
+    const long long parts = std::max(1ll, std::min<long long>(fill, (pieces + (FIND ? ring - 1 : 0)) / ring));
     if (most * parts > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
     const dim3 out_blocks(static_cast<unsigned>(most * parts));
     if constexpr (FIND) {
@@ -916,19 +924,19 @@ twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
     return launch_lora(kern, tiles, kMost, S::bytes(kMost), s, g);
 }
 
-template <int MT, int RG, int RT>
+template <int RG, int RT>
 twell_status run_pass(LoraArgs g, uint8_t* ws, const LoraWs& at, int sms, cudaStream_t s)
 {
     int32_t* n_tiles = reinterpret_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
     int32_t* order = reinterpret_cast<int32_t*>(ws + at.order);
     const twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g,
-                                                   16 * MT, n_tiles, tiles, order);
+                                                   16 * kLoraMT, n_tiles, tiles, order);
     if (st != TWELL_OK) return st;
     g.n_tiles = n_tiles;
     g.tiles = tiles;
     g.order = order;
-    return run_products<MT, RG, RT, false>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
+    return run_products<kLoraMT, RG, RT, false>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
 }
 
 }  // namespace
@@ -986,10 +994,10 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
         p.x += from * ldx;
         p.y += from * ldy;
         p.out += from * ldo;
-        const twell_status st = ad->rank <= 16   ? twell::run_pass<2, 1, 2>(p, w, at, dev.sm_count, s)
-                                : ad->rank <= 32 ? twell::run_pass<2, 1, 4>(p, w, at, dev.sm_count, s)
-                                : ad->rank <= 64 ? twell::run_pass<4, 2, 4>(p, w, at, dev.sm_count, s)
-                                                 : twell::run_pass<4, 4, 4>(p, w, at, dev.sm_count, s);
+        const twell_status st = ad->rank <= 16   ? twell::run_pass<1, 2>(p, w, at, dev.sm_count, s)
+                                : ad->rank <= 32 ? twell::run_pass<1, 4>(p, w, at, dev.sm_count, s)
+                                : ad->rank <= 64 ? twell::run_pass<2, 4>(p, w, at, dev.sm_count, s)
+                                                 : twell::run_pass<4, 4>(p, w, at, dev.sm_count, s);
         if (st != TWELL_OK) return st;
     }
     return TWELL_OK;
