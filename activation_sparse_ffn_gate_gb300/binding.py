@@ -1185,7 +1185,8 @@ def twell_w4_matvec(x: torch.Tensor, W: W4Weights, y: Optional[torch.Tensor] = N
 
 # What a served step needs beside the layer's own calls: the plan of its tokens, their rotation, and adapters.
 
-_PI = Fraction("3.14159265358979323846264338327950288419716939937510")  # to 2^-166
+# 1 / 2 pi times 2^160, to the last bit but one: pi to 2^-166
+_TURN = int(2 ** 159 / Fraction("3.14159265358979323846264338327950288419716939937510"))
 
 
 def scaled_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: int = 0,
@@ -1233,23 +1234,11 @@ class Rotary:
             raise ValueError("frequencies must be finite, one to head_dim / 2 of them")
         if not (math.isfinite(factor) and factor > 0):
             raise ValueError("factor must be positive")
-        # 2^64 times the turns a position, modulo 2^64, formed without rounding but for the last bit
-        turns = [round(Fraction(v) / (2 * _PI) * 2 ** 64) % 2 ** 64 for v in f]
+        # 2^64 times the turns a position, modulo 2^64, in integers: off by the last bit at most
+        turns = [((n * _TURN // d >> 95) + 1 >> 1) % 2 ** 64 for n, d in (v.as_integer_ratio() for v in f)]
         device = device or torch.device("cuda", torch.cuda.current_device())
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64).to(device)
         self.head_dim, self.rot_dim, self.interleaved, self.factor = head_dim, 2 * len(f), bool(interleaved), float(factor)
-
-
-def _rope(backward, name, q, k, positions, rotary, q_out, k_out, stream):
-    if q_out is None:
-        q_out = _empty(q.shape, q.dtype, q.device, stream)
-    if k_out is None and k is not None:
-        k_out = _empty(k.shape, k.dtype, k.device, stream)
-    code = (_native or _calls()).rope(q, k, positions, rotary.turns, rotary.factor, rotary.interleaved, rotary.head_dim, q_out,
-                                      k_out, backward, None if stream is None else stream.cuda_stream)
-    if code:
-        _check(code, name)
-    return q_out, k_out
 
 
 def twell_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rotary: Rotary,
@@ -1259,13 +1248,29 @@ def twell_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.
     q and k [tokens, heads, head_dim] with int32 positions [tokens], or [sequences, tokens, heads, head_dim] with positions
     [sequences, tokens] or [tokens]; bf16 or fp32, any strides with head_dim contiguous (slices of a fused projection,
     head-first tensors transposed). q_out may be q and k_out k: the call then works in place."""
-    return _rope(False, "twell_rope_fwd", q, k, positions, rotary, q_out, k_out, stream)
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    if k_out is None and k is not None:
+        k_out = _empty(k.shape, k.dtype, k.device, stream)
+    code = (_native or _calls()).rope(q, k, positions, rotary.turns, rotary.factor, rotary.interleaved, rotary.head_dim, q_out,
+                                      k_out, False, None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "twell_rope_fwd")
+    return q_out, k_out
 
 
 def twell_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor, rotary: Rotary,
                    q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
     """Gradients of twell_rope_fwd's outputs to those of its inputs: the same call with the opposite turn."""
-    return _rope(True, "twell_rope_bwd", dq, dk, positions, rotary, q_out, k_out, stream)
+    if q_out is None:
+        q_out = _empty(dq.shape, dq.dtype, dq.device, stream)
+    if k_out is None and dk is not None:
+        k_out = _empty(dk.shape, dk.dtype, dk.device, stream)
+    code = (_native or _calls()).rope(dq, dk, positions, rotary.turns, rotary.factor, rotary.interleaved, rotary.head_dim, q_out,
+                                      k_out, True, None if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "twell_rope_bwd")
+    return q_out, k_out
 
 
 @dataclasses.dataclass

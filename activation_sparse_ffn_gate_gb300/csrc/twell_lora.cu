@@ -35,7 +35,7 @@ struct LoraArgs {
     int32_t* status;
     int64_t ldx, ldy, ldo;
     int L, R, k, n, N;
-    // of larger batches: the number of tiles, then a tile's adapter, first row in t, tokens, and their numbers, a place for each
+    // of larger batches: the number of tiles, then a tile's adapter, first row in t, tokens and rank, and the tokens' numbers, a place for each
     // that a tile can have
     const int32_t* n_tiles;
     const int4* tiles;
@@ -306,7 +306,7 @@ __device__ __forceinline__ bool lora_tile(const LoraArgs& g, int index, uint8_t*
 #pragma unroll
             for (int s = 0; s < 2; ++s) token[m][s] = g.order[index * 16 * MT + 16 * m + 8 * s + gr];
         if (index >= n) return false;
-        tile = LoraTile{t.x, lora_rank(g, t.x), t.y, t.z};
+        tile = LoraTile{t.x, t.w, t.y, t.z};
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
             len -= half;
         }
         const int from = count[l] + (j - first_tile[l]) * tile_tokens;
-        tiles[j] = make_int4(l, from, min(tile_tokens, (l < g.L ? count[l + 1] : g.N) - from), 0);
+        tiles[j] = make_int4(l, from, min(tile_tokens, (l < g.L ? count[l + 1] : g.N) - from), lora_rank(g, l));
     }
 }
 

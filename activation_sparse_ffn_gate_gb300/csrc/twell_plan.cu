@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
         if (!WARP && tid == 0) s_sums.taken = 0;
         bool bad = head < 0 || free < 0 || free > a.n_pages || (head >= a.n_pages && (head != 0 || free != 0));
         if (bad) head = free = 0;  // nothing can be taken from or given to a ring that is not one
-        const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll);
+        // a length rounded up to a page stays within 32 bits
+        const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll - 1023);
         auto scan = [&](int (&v)[2], int (&total)[2]) {
             if constexpr (WARP) warp_scan(v, total);
             else block_scan<THREADS>(v, red, total);
@@ -340,6 +341,7 @@ extern "C" twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page
         return TWELL_ERR_INVALID;
     if (n_tokens > 0 && (slots == nullptr || positions == nullptr || owner == nullptr)) return TWELL_ERR_INVALID;
     if (!aligned16(slots) || !aligned16(positions) || !aligned16(owner)) return TWELL_ERR_INVALID;
+    if (B > 0 && seq_lens_out == new_lens) return TWELL_ERR_INVALID;  // read while it is written
     const void* words[] = {pool->ring, pool->state, page_table, seq_lens, new_lens, labels, starts, seq_lens_out, state_out};
     for (const void* p : words)
         if (reinterpret_cast<uintptr_t>(p) % sizeof(int32_t) != 0) return TWELL_ERR_INVALID;

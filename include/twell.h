@@ -482,7 +482,7 @@ TWELL_API twell_status twell_w4_matvec(const void* x, const void* words, const v
 /* Rotary positions. A side (queries or keys) of B sequences of S tokens: element j of head h of token t of sequence b is
  * at in + b * in_batch + t * in_token + h * in_head + j and goes to out + b * out_batch + t * out_token + h * out_head + j.
  * in may be out, with the same strides (the call then works in place); else the two do not overlap. The heads of an output
- * lie apart. Strides in elements; addresses need only the element type's alignment (16-byte vectors are used where the
+ * lie apart, and so do the outputs of queries and keys. Strides in elements; addresses need only the element type's alignment (16-byte vectors are used where the
  * addresses, strides and rot_dim allow them, 8-, 4- and 2-byte ones else). */
 typedef struct {
     const void* in;
@@ -525,9 +525,9 @@ typedef struct {
  * New pages come from the ring's front, in the order of requests and positions, into the requests' rows; the pages of a
  * request that has ended go to its back, where later calls find them, its row stays as it is and its length becomes 0.
  * seq_lens_out [B] receives the lengths after the step and state_out [4] the pool's state; they may be seq_lens and
- * pool->state. A request gets nothing (length and row stay, its tokens receive slot -1 and position 0) if
+ * pool->state, and lie apart from everything else. A request gets nothing (length and row stay, its tokens receive slot -1 and position 0) if
  *  - the pages of the requests up to it that need any are more than the free ones: TWELL_ERR_POOL_EMPTY in *dev_status;
- *  - its length is negative or does not fit its row, its new tokens do not fit n_tokens, or new_lens[b] < -1:
+ *  - its length is negative, does not fit its row or exceeds 2^31 - 1024, its new tokens do not fit n_tokens, or new_lens[b] < -1:
  *    TWELL_ERR_DEVICE_CHECK.
  * More pages given back than are missing (none are taken back then), a state outside the ring (nothing is taken or given
  * then; the ring counts as empty from there on), and pages outside [0, n_pages) in a row or the ring (slot -1) are

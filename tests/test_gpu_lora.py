@@ -104,6 +104,33 @@ def test_larger_batches(cuda_dev, N, k, n, R, L, form):
         assert torch.equal(binding.twell_lora_add(y.clone(), x, ad, ids), out)
 
 
+@pytest.mark.parametrize("N,L,R", [(30, 4096, 16), (400, 4096, 64), (3000, 4096, 8), (512, 1, 128), (16384, 3, 16), (16384 + 777, 40, 24),
+                                   (33000, 2, 128)])
+def test_many_adapters_and_many_tokens(cuda_dev, N, L, R):
+    """Up to 4096 adapters, and batches of several passes."""
+    k, n = 64, 72
+    ad = _adapters(cuda_dev, L, R, k, n, seed=N, ragged=True)
+    ids = _ids(cuda_dev, N, L, N + 1, "any")
+    x, y = _rand(cuda_dev, N, k, seed=N + 2), _rand(cuda_dev, N, n, seed=N + 3)
+    out = binding.twell_lora_add(y, x, ad, ids, out=torch.full_like(y, 7.0))
+    # the formula for all tokens at once: t of a token's own adapter, what lies past its rank left out
+    own = ids.long().clamp_min(0)
+    low = torch.arange(R, device=cuda_dev) < ad.ranks[own][:, None]
+    use = low & (ids >= 0)[:, None]
+    for rows in torch.arange(N, device=cuda_dev).split(4096):
+        i, u, X, Y = own[rows], use[rows], x[rows].double(), y[rows].double()
+        A, B = ad.a[i].double().masked_fill(~u[..., None], 0), ad.b[i].double().masked_fill(~u[:, None], 0)
+        s = ad.scale[i].double()[:, None]
+        t = torch.einsum("mrk,mk->mr", A, X)
+        off = k * 2.0 ** -22 * torch.einsum("mrk,mk->mr", A.abs(), X.abs()) + (2.0 ** -16 + 2.0 ** -23) * t.abs()
+        ref = Y + s * torch.einsum("mnr,mr->mn", B, t)
+        room = s.abs() * (torch.einsum("mnr,mr->mn", B.abs(), off + R * 2.0 ** -22 * t.abs())) + 2.0 ** -23 * (Y.abs() + ref.abs())
+        err = (out[rows].double() - ref).abs()
+        assert (err <= room + 2.0 ** -8 * (ref.abs() + room)).all()
+    assert torch.equal(out[ids < 0], y[ids < 0])
+    assert torch.equal(binding.twell_lora_add(y.clone(), x, ad, ids), out)
+
+
 @pytest.mark.parametrize("N", [1, 12, 100, 300, 1500])
 def test_a_row_does_not_depend_on_the_others(cuda_dev, N):
     """The same bits in another order, beside other rows, and whatever the others hold."""

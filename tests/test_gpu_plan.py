@@ -28,7 +28,7 @@ def _walk(ring, state, page, table, lens, new, M, labels=None):
         head, free = 0, 0
         codes.add(CHECK)
     slots, positions, owner = [-1] * M, [0] * M, [-1] * M
-    cap = min(cols * page, 2 ** 31 - 1)
+    cap = min(cols * page, 2 ** 31 - 1024)
     starts, at, wanted, taken = [], 0, 0, 0
     gives = []
     for b, (past, add) in enumerate(zip(list(lens), new)):
@@ -206,6 +206,19 @@ def test_requests_that_are_refused(cuda_dev):
         _same(_run(cuda_dev, ring, state, page, table, lens, new, M), want)
 
 
+def test_lengths_near_32_bits(cuda_dev):
+    """A row of 2^21 pages of 1024 tokens: the last length that is taken, and the first that is not."""
+    cols, page = 1 << 21, 1024
+    table = torch.zeros((2, cols), dtype=I32, device=cuda_dev)
+    table[0, cols - 2] = 5
+    lens = torch.tensor([2 ** 31 - 1025, 2 ** 31 - 1024], dtype=I32, device=cuda_dev)
+    status = torch.zeros(1, dtype=I32, device=cuda_dev)
+    pool = binding.PagePool.full(8, page, cuda_dev)
+    p = binding.twell_kv_plan(pool, table, lens, torch.ones_like(lens), 2, status=status)
+    assert p.positions.tolist() == [2 ** 31 - 1025, 0] and p.slots.tolist() == [5 * 1024 + 1023, -1]
+    assert lens.tolist() == [2 ** 31 - 1024] * 2 and pool.state.tolist() == [0, 8, 0, 0] and binding.twell_read_status(status) == CHECK
+
+
 def test_rows_that_do_not_hold_the_step(cuda_dev):
     ring, state, table, lens, new = _make(4, 12, 8, 50, lambda r: r.randint(1, 9))
     for M in (0, 1, sum(new) - 1, sum(new[:6])):
@@ -259,7 +272,8 @@ def test_refusals(cuda_dev):
         with pytest.raises(ValueError):
             bad()
     for bad, code in ((lambda: f(binding.PagePool(pool.ring, pool.state, 12), i(2, 3), i(2), i(2), 4), 2),
-                      (lambda: f(pool, i(4097, 1), i(4097), i(4097), 4), 2), (lambda: f(pool, i(2, 0), i(2), i(2), 4), 1)):
+                      (lambda: f(pool, i(4097, 1), i(4097), i(4097), 4), 2), (lambda: f(pool, i(2, 0), i(2), i(2), 4), 1),
+                      (lambda: (lambda n: f(pool, i(2, 3), i(2), n, 4, seq_lens_out=n))(i(2)), 1)):
         with pytest.raises(binding.TwellError) as e:
             bad()
         assert e.value.code == code

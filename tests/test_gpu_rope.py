@@ -195,7 +195,8 @@ def test_refusals(cuda_dev):
     with pytest.raises(TypeError):
         binding.twell_rope_fwd(q.half(), None, pos, r)
     for bad in (lambda: binding.twell_rope_fwd(q, None, pos, r, q[:1].expand(4, 2, 32)),  # rows over one another
-                lambda: binding.twell_rope_fwd(q, None, pos, r, q.view(2, 4, 32).transpose(0, 1))):  # in place, other strides
+                lambda: binding.twell_rope_fwd(q, None, pos, r, q.view(2, 4, 32).transpose(0, 1)),  # in place, other strides
+                lambda: (lambda o: binding.twell_rope_fwd(q, q, pos, r, o, o))(torch.empty_like(q))):  # one output for both
         with pytest.raises(binding.TwellError) as e:
             bad()
         assert e.value.code == 1

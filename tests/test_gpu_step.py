@@ -156,7 +156,7 @@ def test_steps_replay_in_a_cuda_graph(cuda_dev):
 
 
 class Lora:
-    """An adapters' call that is large enough for a workspace."""
+    """An adapters' call whose kernels leave something in the workspace for one another."""
 
     def __init__(self, dev, seed, N=1100, k=128, n=136, L=5):
         self.ad = _adapters(dev, L, 16, k, n, seed)
@@ -178,8 +178,9 @@ def _capture(call, stream):
     return graph, out
 
 
-def test_threads_that_share_a_stream(cuda_dev):
-    calls = [Lora(cuda_dev, 10 * i, N=700 + 311 * i) for i in range(5)]
+@pytest.mark.parametrize("sizes", [[(700 + 311 * i, 5) for i in range(5)], [(60 + 90 * i, 50) for i in range(5)]], ids=["grouped", "found"])
+def test_threads_that_share_a_stream(cuda_dev, sizes):
+    calls = [Lora(cuda_dev, 10 * i, N=N, L=L) for i, (N, L) in enumerate(sizes)]
     want = [c() for c in calls]
     torch.cuda.synchronize()
     got, errors, start = [[] for _ in calls], [], threading.Barrier(len(calls))
@@ -201,10 +202,12 @@ def test_threads_that_share_a_stream(cuda_dev):
     assert not errors and all(torch.equal(o, w) for os, w in zip(got, want) for o in os)
 
 
-def test_graphs_beside_calls(cuda_dev):
+@pytest.mark.parametrize("sizes", [[(900, 5), (1400, 5), (1900, 5)], [(64, 64), (200, 40), (500, 30)], [(3, 5), (16, 9), (100, 2)]],
+                         ids=["grouped", "found", "whole"])
+def test_graphs_beside_calls(cuda_dev, sizes):
     """Two graphs captured on one stream and plain calls on it, at once on three streams; then tensors that fill what the
     allocator has free keep their values through the replays."""
-    a, b, c = (Lora(cuda_dev, 10 * i, N=900 + 500 * i) for i in range(3))
+    a, b, c = (Lora(cuda_dev, 10 * i, N=N, L=L) for i, (N, L) in enumerate(sizes))
     want = [x() for x in (a, b, c)]
     side, others = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(2)]
     graphs = [_capture(x, side) for x in (a, b)]
@@ -226,8 +229,9 @@ def test_graphs_beside_calls(cuda_dev):
     assert all(bool((t == 7).all()) for t in fills) and torch.equal(graphs[0][1], want[0])
 
 
-def test_a_workspace_of_the_callers(cuda_dev):
-    call = Lora(cuda_dev, 3)
+@pytest.mark.parametrize("N,L", [(1100, 5), (64, 64), (4, 5)])
+def test_a_workspace_of_the_callers(cuda_dev, N, L):
+    call = Lora(cuda_dev, 3, N=N, L=L)
     n = binding.twell_workspace_bytes(binding.OP_LORA_ADD, call.x.shape[0], call.ad.a.shape[1], 1)
     ws = torch.full((max(n, 16),), 255, dtype=torch.uint8, device=cuda_dev)  # its contents do not matter
     assert torch.equal(call(ws=ws), call())
