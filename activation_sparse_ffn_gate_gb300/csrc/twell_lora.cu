@@ -22,6 +22,9 @@ constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraCluster = 8;      // most blocks a tile
 constexpr int kLoraSmallN = 512;     // up to here every cluster finds its tile from the ids itself
+// A larger batch's tiles have 32 tokens: with 64 their weights are read half as often, but a block takes an SM for itself (16384
+// tokens, 2048 x 2048, rank 64: 64.7 us and 73.6; rank 16, 2048 x 4096: 70 and 120).
+constexpr int kLoraMT = 2;
 constexpr int kLoraParts = 4;         // most blocks of a tile that share its k where each leaves its own sums,
 constexpr int kLoraSums = 1024;       // and of all tiles
 constexpr int kLoraGroupThreads = 1024;
@@ -726,12 +729,12 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
     out.template run<S::kStages>(frags);
 }
 
-// The tiles of a larger batch: tokens counted by adapter, a tile for each tile_tokens of an adapter's, and
+// The tiles of a larger batch: tokens counted by adapter, a tile for each 16 kLoraMT of an adapter's, and
 // their places in it in `order`. One block: the counts are in its shared memory, and a pass's ids are 64 KB, all requested before the
 // first is counted. Which token of an adapter comes first is left to chance; a token's result does not depend on it.
-__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int tile_tokens, int32_t* n_tiles,
-                                                                       int4* tiles, int32_t* order)
+__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int32_t* n_tiles, int4* tiles, int32_t* order)
 {
+    constexpr int kTok = 16 * kLoraMT;                   // tokens a tile
     constexpr int kPer = kLoraPass / kLoraGroupThreads;  // tokens a thread
     extern __shared__ int count[];                       // [L + 1] of tokens, then their first place; [L + 1] of the first tiles
     __shared__ int warp_sum[2][32], s_tiles;
@@ -762,7 +765,7 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
     int sum = 0, tsum = 0;
     for (int l = l0; l < l1; ++l) {
         sum += count[l];
-        tsum += (count[l] + tile_tokens - 1) / tile_tokens;
+        tsum += (count[l] + kTok - 1) / kTok;
     }
     int incl = sum, tincl = tsum;
 #pragma unroll
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
         count[l] = at;
         first_tile[l] = tile;
         at += have;
-        tile += (have + tile_tokens - 1) / tile_tokens;
+        tile += (have + kTok - 1) / kTok;
     }
     if (tid == kLoraGroupThreads - 1) *n_tiles = s_tiles = tile;
     __syncthreads();
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
         if (r * kLoraGroupThreads >= g.N) break;
         if (v[r] >= 0) {
             const int l = v[r] >> 16, num = v[r] & 0xffff;
-            order[(first_tile[l] + num / tile_tokens) * tile_tokens + num % tile_tokens] = r * kLoraGroupThreads + tid;
+            order[(first_tile[l] + num / kTok) * kTok + num % kTok] = r * kLoraGroupThreads + tid;
         }
     }
     for (int j = tid; j < s_tiles; j += kLoraGroupThreads) {
@@ -804,8 +807,8 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
             if (first_tile[l + half] <= j) l += half;
             len -= half;
         }
-        const int from = count[l] + (j - first_tile[l]) * tile_tokens;
-        tiles[j] = make_int4(l, from, min(tile_tokens, (l < g.L ? count[l + 1] : g.N) - from), lora_rank(g, l));
+        const int from = count[l] + (j - first_tile[l]) * kTok;
+        tiles[j] = make_int4(l, from, min(kTok, (l < g.L ? count[l + 1] : g.N) - from), lora_rank(g, l));
     }
 }
 
@@ -849,9 +852,6 @@ constexpr int most_blocks(bool two)
 long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / tok + std::min(N, L + 1)); }
 
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
-// A larger batch's tiles have 32 tokens: with 64 their weights are read half as often, but a block takes an SM for itself (16384
-// tokens, 2048 x 2048, rank 64: 64.7 us and 73.6; rank 16, 2048 x 4096: 70 and 120).
-constexpr int kLoraMT = 2;
 
 // Blocks of a tile that share its k where each leaves its own sums.
 int lora_parts_of(int tiles, int sms) { return std::max(1, std::min(std::min(kLoraParts, kLoraSums / tiles), 4 * sms / tiles)); }
@@ -931,7 +931,7 @@ twell_status run_pass(LoraArgs g, uint8_t* ws, const LoraWs& at, int sms, cudaSt
     int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
     int32_t* order = reinterpret_cast<int32_t*>(ws + at.order);
     const twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g,
-                                                   16 * kLoraMT, n_tiles, tiles, order);
+                                                   n_tiles, tiles, order);
     if (st != TWELL_OK) return st;
     g.n_tiles = n_tiles;
     g.tiles = tiles;
