@@ -1,13 +1,23 @@
 // twell_lora.cu -- low-rank adapters of many requests beside a shared projection: to each token's row y the product
 // s B (A x) of its own adapter (or of none) is added, A [R, k] and B [n, R] of bf16.
 //
-// Tokens of one adapter go together, 16 MT of them a tile, so that its weights are read once a tile. A cluster of blocks does
-// a tile: each block has a part of k for t = A x, the parts go to all blocks through distributed shared memory and are added
-// there in one order, and each block then has a part of n for y + B t. So one launch does, t never reaches memory, and a
-// single token's weights are spread over eight SMs. Both products are mma.sync with the tokens as rows; a warp's weights are
-// its own, so that they go straight from memory into fragments. Which element of k (or of a rank) stands where in a fragment
-// is free as long as both operands agree: a lane takes 16 adjacent bytes of a row, and 8 adjacent columns of y.
-// t enters the second product as hi + lo bf16: 16 bits of it, for twice the products of a small rank.
+// Tokens of one adapter go together in tiles, so that its weights are read once a tile. Both products are mma.sync with the
+// tokens as rows; a warp's weights, and its piece of x or y, are its own. Which element of k (or which rank) stands where in a
+// fragment is free as long as both operands agree: a lane takes 16 adjacent bytes of a row, and 8 adjacent columns of y. They
+// pass through slots of shared memory that belong to the lane, copied there a few pieces ahead, so that no barrier orders
+// them. t = A x is summed in fp32 over warps and blocks in one order, and enters the second product as hi + lo bf16: 16 bits
+// of it, for twice the products of a small rank.
+// What costs a small batch is its chain of loads, what costs a large one its bytes; hence three ways:
+// - Few tiles, each of which can have eight SMs: one kernel, a cluster of eight blocks a tile. Each has a part of k, the sums go
+//   to all of them through distributed shared memory, and each then has a part of n, whose first pieces are on their way
+//   meanwhile. One token, 2048 x 2048, rank 16: 4.5 us, of which the launch is 1.6; the rest is ids, x and A, the
+//   exchange, y. One token of rank 64, 2048 x 4096: 7.5 us (10.6 with one piece of B under way instead of two).
+// - Up to 512 tokens else: two kernels, whose blocks need not start together as a cluster's do; the second one's copies run
+//   while the first is at work. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 13.3 us (18.0 in clusters); 256
+//   tokens of rank 16: 8.5 (15.8).
+// - Larger ones: the same two after a kernel that groups the tokens by adapter. 16384 tokens, 2048 x 4096, rank 16: 67 us, of
+//   which grouping takes 6, the first product 15 (67 MB) and the second 44 (268 MB, 91% of the copy rate). Above rank 32 the
+//   weights that each tile brings from L2 count: rank 64, 2048 x 2048: 65 us for 182 MB.
 #include "twell_mma.cuh"
 #include "twell_ops.cuh"
 
@@ -21,12 +31,14 @@ constexpr int kLoraMaxDim = 1 << 20;
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraCluster = 8;      // most blocks a tile
-constexpr int kLoraSmallN = 512;     // up to here every cluster finds its tile from the ids itself
+constexpr int kLoraSmallN = 512;     // up to here every block finds its tile from the ids itself
 // A larger batch's tiles have 32 tokens: with 64 their weights are read half as often, but a block takes an SM for itself (16384
 // tokens, 2048 x 2048, rank 64: 64.7 us and 73.6; rank 16, 2048 x 4096: 70 and 120).
 constexpr int kLoraMT = 2;
-constexpr int kLoraParts = 4;         // most blocks of a tile that share its k where each leaves its own sums,
-constexpr int kLoraSums = 1024;       // and of all tiles
+// Most blocks of a tile that share its k where each leaves its own sums (64 tokens of rank 16, 2048 x 2048: 6.9 us with four, 8.9
+// with eight), and of all tiles.
+constexpr int kLoraParts = 4;
+constexpr int kLoraSums = 1024;
 constexpr int kLoraGroupThreads = 1024;
 constexpr int kLoraPass = 16384;     // tokens of a larger batch that go together
 
@@ -38,8 +50,8 @@ struct LoraArgs {
     int32_t* status;
     int64_t ldx, ldy, ldo;
     int L, R, k, n, N;
-    // of larger batches: the number of tiles, then a tile's adapter, first row in t, tokens and rank, and the tokens' numbers, a place for each
-    // that a tile can have
+    // of larger batches: the number of tiles; of each its adapter, first row in t, tokens and rank; and the tokens' numbers, with a
+    // place for each token that a tile can have
     const int32_t* n_tiles;
     const int4* tiles;
     const int32_t* order;
@@ -65,7 +77,7 @@ struct LoraShape {
     // is two of them, on their way while t is put together
     static constexpr int kMinOut = RG == 4 ? 1 : 2;
     static constexpr int kRing = BOTH ? (3 * kIn > kWarpSums + kMinOut * kOut ? 3 * kIn : kWarpSums + kMinOut * kOut)
-                                      : (MT == 1 ? 6 : 12) * 1024;
+                                      : (MT == 1 && RG == 1 ? 6 : 12) * 1024;
     static constexpr int kInStages = kRing / kIn > 4 ? 4 : kRing / kIn;
     static constexpr int kOutStages = (kRing - kWarpSums) / kOut > 4 ? 4 : (kRing - kWarpSums) / kOut;
     static constexpr int kFragBytes = MT * kFrags * 2 * 512;
@@ -224,9 +236,8 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
         rank[j] = 0;
         if (j * kLoraThreads >= g.N) continue;
         rank[j] = own[j] >= 0 && own[j] < g.L && g.ranks ? __ldg(g.ranks + own[j]) : g.R;  // on its way while the tiles are counted
-        const unsigned same = __match_any_sync(0xffffffffu, own[j]);
-        if (i < g.N && (same & ((1u << lane) - 1)) == 0) {
-            atomicAdd(&bins[own[j]].x, __popc(same));
+        if (i < g.N) {
+            atomicAdd(&bins[own[j]].x, 1);
             atomicMin(&bins[own[j]].y, i);
         }
     }
@@ -746,19 +757,22 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
     for (int r = 0; r < kPer; ++r) v[r] = r * kLoraGroupThreads + tid < g.N ? __ldg(g.ids + r * kLoraGroupThreads + tid) : INT32_MIN;
     for (int i = tid; i <= g.L; i += kLoraGroupThreads) count[i] = 0;
     __syncthreads();
-    // a token's number among those of its adapter; equal ids of a warp are counted by one lane
+    // a token's number among those of its adapter; a warp whose tokens have one adapter (most of a prompt's) counts them at once
 #pragma unroll
     for (int r = 0; r < kPer; ++r) {
         if (r * kLoraGroupThreads >= g.N) break;
         const bool live = r * kLoraGroupThreads + tid < g.N;
         const int id = live ? lora_id(g, v[r]) : -1;
-        // most warps of a prompt have one adapter
-        const bool one = __all_sync(0xffffffffu, id == __shfl_sync(0xffffffffu, id, 0));
-        const unsigned same = one ? 0xffffffffu : __match_any_sync(0xffffffffu, id), below = same & ((1u << lane) - 1);
-        int first = 0;
-        if (live && below == 0) first = atomicAdd(count + id, __popc(same));
-        first = __shfl_sync(0xffffffffu, first, __ffs(same) - 1);
-        v[r] = live ? (id << 16) | (first + __popc(below)) : -1;  // at most 4096 adapters and 2^15 tokens
+        const int first = __shfl_sync(0xffffffffu, id, 0);  // by all lanes, whatever they have
+        const bool one = __all_sync(0xffffffffu, live && id == first);
+        int num = 0;
+        if (one) {
+            if (lane == 0) num = atomicAdd(count + id, 32);
+            num = __shfl_sync(0xffffffffu, num, 0) + lane;
+        } else if (live) {
+            num = atomicAdd(count + id, 1);
+        }
+        v[r] = live ? (id << 16) | num : -1;  // at most 4096 adapters and 2^15 tokens
     }
     __syncthreads();
     const int per = (g.L + kLoraGroupThreads) / kLoraGroupThreads, l0 = tid * per, l1 = min(l0 + per, g.L + 1);
@@ -812,7 +826,7 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
     }
 }
 
-// A tile's blocks: as many as give each SM one.
+// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 25.0 us with two, 29.1 with four).
 int lora_blocks(long long tiles, int sms, int most)
 {
     int b = 1;
