@@ -50,6 +50,7 @@ struct LoraArgs {
     int32_t* status;
     int64_t ldx, ldy, ldo;
     int L, R, k, n, N;
+    uint64_t limit_ns;  // of a wait
     // of larger batches: the number of tiles; of each its adapter, first row in t, tokens and rank; and the tokens' numbers, with a
     // place for each token that a tile can have
     const int32_t* n_tiles;
@@ -151,6 +152,13 @@ __device__ __forceinline__ uint32_t cluster_blocks()
 __device__ __forceinline__ void st_cluster16(uint32_t at, const float4& v)
 {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+// The same, counted on an mbarrier of that block's: whoever waits there for the bytes needs no fence from the sender.
+__device__ __forceinline__ void st_counted16(uint32_t at, const float4& v, uint32_t bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+                 "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(bar)
+                 : "memory");
 }
 
 // A token's adapter, L for none (-1, or one that does not exist, which is recorded).
@@ -547,7 +555,8 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
     extern __shared__ __align__(16) uint8_t lora_smem[];
     pdl_begin();
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2;
-    const int blocks = static_cast<int>(cluster_blocks()), part = static_cast<int>(cluster_ctarank());
+    constexpr int blocks = kLoraCluster;
+    const int part = static_cast<int>(cluster_ctarank());
     LoraTile tile;
     const int* tok = lora_find<S::kTok>(g, static_cast<int>(blockIdx.x) / blocks, lora_smem, tile);  // where the rings come later
     if (tile.id < 0) return;
@@ -563,7 +572,14 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
         }
         return;
     }
-    if (blocks > 1) cluster_arrive();  // this block runs: the others may write to its shared memory
+    constexpr int kQuads = S::kRanks / 4;
+    __shared__ uint64_t bar;
+    if (tid == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&bar, static_cast<uint32_t>(blocks * tile.tokens * kQuads * 16));
+    }
+    cluster_arrive();  // this block runs and its barrier counts: the others may write to its shared memory
 
     int token[MT][2];
 #pragma unroll
@@ -580,25 +596,20 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
         for (int i = 0; i < S::kOutStages; ++i) out.template request<S::kOutStages>(i, i);
     });
     __syncthreads();
-    if (blocks > 1) cluster_wait();
+    cluster_wait();
     uint4* frags = reinterpret_cast<uint4*>(lora_smem + kLoraWarps * S::kRing);
     float* recv = reinterpret_cast<float*>(lora_smem + kLoraWarps * S::kRing + S::kFragBytes);
-    constexpr int kQuads = S::kRanks / 4;
-    for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads) {
+    for (int i = tid; i < tile.tokens * kQuads; i += kLoraThreads) {
         const int row = i / kQuads, quad = i % kQuads;
         const float4 v = lora_sum<S, RG>(lora_smem, row, quad);
-        float* to = recv + part * S::kSum + row * S::kPitch + quad * 4;
-        if (blocks == 1) {
-            *reinterpret_cast<float4*>(to) = v;
-        } else {
-            for (int d = 0; d < blocks; ++d) st_cluster16(mapa_shared(smem_u32(to), d), v);
-        }
+        const uint32_t to = smem_u32(recv + part * S::kSum + row * S::kPitch + quad * 4);
+#pragma unroll
+        for (int d = 0; d < blocks; ++d) st_counted16(mapa_shared(to, d), v, mapa_shared(smem_u32(&bar), d));
     }
-    if (blocks > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
+    const bool all = wait_bounded<true>(&bar, 0, nullptr, g.status, g.limit_ns);
+    if (__syncthreads_or(!all)) {  // recorded; what is under way to this block's own memory ends first
+        copies_wait<0>();
+        return;
     }
     // t, whole, under its scale, as the second product's fragments: [row tile][16 ranks][hi, lo][lane]
     for (int i = tid; i < MT * S::kFrags * 32; i += kLoraThreads) {
@@ -609,7 +620,9 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
         uint4 t[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
+            // of a row without a token nothing was sent: what it holds stays in it
             float4 v = *reinterpret_cast<const float4*>(p + s * 8 * S::kPitch);
+#pragma unroll
             for (int d = 1; d < blocks; ++d) {
                 const float4 u = *reinterpret_cast<const float4*>(p + d * S::kSum + s * 8 * S::kPitch);
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
@@ -853,12 +866,12 @@ twell_status launch_lora(void (*kern)(KArgs...), int clusters, int blocks, size_
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
-// Most blocks a tile whose sums fit an SM, with `two` two of them where one block's do.
+// Most blocks in a cluster whose sums fit an SM, two of them where one block's do.
 template <typename S>
-constexpr int most_blocks(bool two)
+constexpr int most_blocks()
 {
     int b = kLoraCluster;
-    while (b > 1 && S::bytes(b) > (two && S::bytes(1) <= 108u * 1024u ? 108u : 222u) * 1024u) b /= 2;
+    while (b > 1 && S::bytes(b) > (S::bytes(1) <= 108u * 1024u ? 108u : 222u) * 1024u) b /= 2;
     return b;
 }
 
@@ -893,7 +906,7 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
     using O = LoraOutShape<MT, RG, RT>;
     static_assert(!FIND || (kLoraFindBytes <= kLoraWarps * S::kRing && kLoraFindBytes <= kLoraWarps * O::kRing), "room to find a tile");
     const int most = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    constexpr int kMost = most_blocks<S>(true);
+    constexpr int kMost = most_blocks<S>();
     auto in = lora_in_kernel<MT, RG, RT, FIND>;
     auto out = lora_out_kernel<MT, RG, RT, FIND>;
     static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
@@ -928,14 +941,14 @@ template <int RG, int RT>
 twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
 {
     using S = LoraShape<1, RG, RT, true>;
-    constexpr int kMost = most_blocks<S>(false);
     static_assert(kLoraFindBytes <= kLoraWarps * S::kRing, "room to find a tile");
+    static_assert(S::bytes(kLoraCluster) <= 224 * 1024, "a block's shared memory");
     const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
     if (tiles * kLoraCluster > sms) return run_products<1, RG, RT, true>(g, reinterpret_cast<uint4*>(ws + LoraWs(g.N, g.R).t), sms, s);
     auto kern = lora_kernel<1, RG, RT>;
     static std::atomic<uint64_t> allowed{0};
-    if (twell_host::allow_smem(kern, S::bytes(kMost), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
-    return launch_lora(kern, tiles, kMost, S::bytes(kMost), s, g);
+    if (twell_host::allow_smem(kern, S::bytes(kLoraCluster), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
+    return launch_lora(kern, tiles, kLoraCluster, S::bytes(kLoraCluster), s, g);
 }
 
 template <int RG, int RT>
@@ -993,7 +1006,7 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     twell::LoraArgs g = {static_cast<const bf*>(ad->a), static_cast<const bf*>(ad->b), static_cast<const bf*>(x),
                          static_cast<const bf*>(y), static_cast<bf*>(out), ad->scale, ad->ranks, ids, dev_status,
-                         ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, nullptr, nullptr, nullptr};
+                         ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, wait_limit_ns(), nullptr, nullptr, nullptr};
     uint8_t* w = static_cast<uint8_t*>(ws);
     if (N <= twell::kLoraSmallN)
         return ad->rank <= 16   ? twell::run_small<1, 2>(g, w, dev.sm_count, s)
