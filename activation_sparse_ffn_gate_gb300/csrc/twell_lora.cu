@@ -149,11 +149,8 @@ __device__ __forceinline__ uint32_t cluster_blocks()
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void st_cluster16(uint32_t at, const float4& v)
-{
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
-// The same, counted on an mbarrier of that block's: whoever waits there for the bytes needs no fence from the sender.
+// A store to another block's shared memory, counted on an mbarrier of that block's: whoever waits there for the bytes needs no fence
+// from the sender (a cluster barrier behind plain stores was 1 us of a call).
 __device__ __forceinline__ void st_counted16(uint32_t at, const float4& v, uint32_t bar)
 {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
@@ -552,7 +549,7 @@ template <int MT, int RG, int RT>
 __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
 {
     using S = LoraShape<MT, RG, RT, true>;
-    extern __shared__ __align__(16) uint8_t lora_smem[];
+    extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
     pdl_begin();
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2;
     constexpr int blocks = kLoraCluster;
@@ -643,7 +640,7 @@ template <int MT, int RG, int RT, bool FIND>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out, int most_tiles)
 {
     using S = LoraShape<MT, RG, RT, false>;
-    extern __shared__ __align__(16) uint8_t lora_smem[];
+    extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
     pdl_wait();
     pdl_next();
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
@@ -654,40 +651,44 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
     if (!lora_tile<MT, FIND>(g, index, lora_smem, tile, token)) return;
     const int rank = tile.rank;
     if (rank == 0) return;
-    if (!FIND && blocks > 1) cluster_arrive();
+    constexpr int kQuads = S::kRanks / 4;
+    const int quads = tile.tokens * kQuads;  // quad i is added up by block i % blocks
+    __shared__ uint64_t bar;
+    if (!FIND && blocks > 1) {
+        if (tid == 0) {
+            mbar_init(&bar, 1);
+            fence_mbar_init();
+            mbar_arrive_expect_tx(&bar, static_cast<uint32_t>(blocks * ((quads + blocks - 1 - part) / blocks) * 16));
+        }
+        cluster_arrive();  // this block runs and its barrier counts
+    }
     const float scale = __ldg(g.scale + tile.id);
     lora_shrink<S, MT, RG, RT>(g, tile.id, rank, part, blocks, token, lora_smem + warp * S::kRing, [] {});
     __syncthreads();
-    constexpr int kQuads = S::kRanks / 4;
     if constexpr (FIND) {
         float4* to = reinterpret_cast<float4*>(t_out) + (static_cast<size_t>(index) * blocks + part) * (S::kTok * kQuads);
-        for (int i = tid; i < tile.tokens * kQuads; i += kLoraThreads) to[i] = lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads);
+        for (int i = tid; i < quads; i += kLoraThreads) to[i] = lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads);
         return;
     }
-    auto store = [&](int row, int quad, const float4& v) {
-        if (row < tile.tokens) t_out[static_cast<size_t>(tile.first + row) * kQuads + quad] = lora_parts(v, 4 * quad, rank, scale);
-    };
+    auto store = [&](int i, const float4& v) { t_out[static_cast<size_t>(tile.first) * kQuads + i] = lora_parts(v, i % kQuads * 4, rank, scale); };
     if (blocks == 1) {
-        for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads)
-            store(i / kQuads, i % kQuads, lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads));
+        for (int i = tid; i < quads; i += kLoraThreads) store(i, lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads));
         return;
     }
-    // quad i is added up by block i % blocks
     float4* recv = reinterpret_cast<float4*>(lora_smem + kLoraWarps * S::kRing);
     const int share = S::kTok * kQuads / blocks;
     cluster_wait();
-    for (int i = tid; i < S::kTok * kQuads; i += kLoraThreads)
-        st_cluster16(mapa_shared(smem_u32(recv + part * share + i / blocks), i % blocks), lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads));
-    cluster_arrive();
-    cluster_wait();
-    for (int j = tid; j < share; j += kLoraThreads) {
-        const int i = j * blocks + part;
-        float4 v = recv[j];
+    for (int i = tid; i < quads; i += kLoraThreads)
+        st_counted16(mapa_shared(smem_u32(recv + part * share + i / blocks), i % blocks), lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads),
+                     mapa_shared(smem_u32(&bar), i % blocks));
+    if (!wait_bounded<true>(&bar, 0, nullptr, g.status, g.limit_ns)) return;  // recorded
+    for (int i = part + tid * blocks; i < quads; i += kLoraThreads * blocks) {
+        float4 v = recv[i / blocks];
         for (int d = 1; d < blocks; ++d) {
-            const float4 u = recv[d * share + j];
+            const float4 u = recv[d * share + i / blocks];
             v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
         }
-        store(i / kQuads, i % kQuads, v);
+        store(i, v);
     }
 }
 
@@ -698,7 +699,7 @@ template <int MT, int RG, int RT, bool FIND>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArgs g, const uint4* t_in, int most_tiles, int in_parts)
 {
     using S = LoraOutShape<MT, RG, RT>;
-    extern __shared__ __align__(16) uint8_t lora_smem[];
+    extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
     const int parts = static_cast<int>(gridDim.x) / most_tiles, index = static_cast<int>(blockIdx.x) / parts,
               part = static_cast<int>(blockIdx.x) % parts;
@@ -935,8 +936,8 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
     }
 }
 
-// At most kLoraSmallN tokens: where every tile can have eight SMs to itself, in one kernel; else in two, which share SMs and
-// whose blocks need not start together.
+// At most kLoraSmallN tokens: where the device holds all tiles' clusters at once, in one kernel; else in two, whose blocks need not
+// start together.
 template <int RG, int RT>
 twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
 {
@@ -944,7 +945,9 @@ twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
     static_assert(kLoraFindBytes <= kLoraWarps * S::kRing, "room to find a tile");
     static_assert(S::bytes(kLoraCluster) <= 224 * 1024, "a block's shared memory");
     const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    if (tiles * kLoraCluster > sms) return run_products<1, RG, RT, true>(g, reinterpret_cast<uint4*>(ws + LoraWs(g.N, g.R).t), sms, s);
+    // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.5 us and 5.4 in two kernels; of rank 64, 2048 x
+    // 4096: 10.7 and 9.0)
+    if (tiles * kLoraCluster > (RG == 1 ? 2 : 1) * sms) return run_products<1, RG, RT, true>(g, reinterpret_cast<uint4*>(ws + LoraWs(g.N, g.R).t), sms, s);
     auto kern = lora_kernel<1, RG, RT>;
     static std::atomic<uint64_t> allowed{0};
     if (twell_host::allow_smem(kern, S::bytes(kLoraCluster), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
