@@ -99,7 +99,7 @@ template <int MT, int RG, int RT>
 struct LoraOutShape {
     using In = LoraShape<MT, RG, RT, false>;
     static constexpr int kRanks = In::kRanks, kBlock = In::kBlock, kFrags = In::kFrags, kStage = In::kOut;
-    static constexpr int kRing = (MT == 1 ? (RG == 4 ? 18 : RG == 2 ? 10 : 6) : RG == 4 ? 20 : 12) * 1024;
+    static constexpr int kRing = (MT == 1 ? (RG == 4 ? 18 : RG == 2 ? 10 : 6) : RT == 2 ? 9 : 12) * 1024;
     static constexpr int kStages = kRing / kStage;
     static constexpr size_t kBytes = kLoraWarps * kRing + In::kFragBytes;
 };
@@ -841,10 +841,10 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
 }
 
 // A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 25.0 us with two, 29.1 with four).
-int lora_blocks(long long tiles, int sms, int most)
+int lora_blocks(long long tiles, int sms)
 {
     int b = 1;
-    while (b < most && tiles * b < sms) b *= 2;
+    while (b < kLoraCluster && tiles * b < sms) b *= 2;
     return b;
 }
 
@@ -865,15 +865,6 @@ twell_status launch_lora(void (*kern)(KArgs...), int clusters, int blocks, size_
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
-}
-
-// Most blocks in a cluster whose sums fit an SM, two of them where one block's do.
-template <typename S>
-constexpr int most_blocks()
-{
-    int b = kLoraCluster;
-    while (b > 1 && S::bytes(b) > (S::bytes(1) <= 108u * 1024u ? 108u : 222u) * 1024u) b /= 2;
-    return b;
 }
 
 // Tiles of N tokens, at most.
@@ -907,19 +898,17 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
     using O = LoraOutShape<MT, RG, RT>;
     static_assert(!FIND || (kLoraFindBytes <= kLoraWarps * S::kRing && kLoraFindBytes <= kLoraWarps * O::kRing), "room to find a tile");
     const int most = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    constexpr int kMost = most_blocks<S>();
+    static_assert(2 * S::bytes(kLoraCluster) <= 226 * 1024, "two blocks an SM");
     auto in = lora_in_kernel<MT, RG, RT, FIND>;
     auto out = lora_out_kernel<MT, RG, RT, FIND>;
     static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
-    if (twell_host::allow_smem(in, S::bytes(kMost), in_allowed) != TWELL_OK || twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK)
+    if (twell_host::allow_smem(in, S::bytes(kLoraCluster), in_allowed) != TWELL_OK || twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK)
         return TWELL_ERR_CUDA;
-    // a block's part of the columns: a ring's worth of pieces a warp at least, and one round of blocks, or kOutRounds where the tiles
-    // alone are more
+    // a block's part of the columns: two pieces a warp at least, and one round of blocks, or kOutRounds where the tiles alone are more
     constexpr int kOutRounds = 2;
     const long long places = 2ll * sms, about = FIND ? most : std::max(1, g.N / S::kTok);
-    const int pieces = (g.n + 31) / 32, ring = kLoraWarps * O::kStages;
     const long long fill = most <= places ? places / most : (kOutRounds * places + about - 1) / about;
-    const long long parts = std::max(1ll, std::min<long long>(fill, (pieces + (FIND ? ring - 1 : 0)) / ring));
+    const long long parts = std::max(1ll, std::min<long long>(fill, ((g.n + 31) / 32 + 2 * kLoraWarps - 1) / (2 * kLoraWarps)));
     if (most * parts > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
     const dim3 out_blocks(static_cast<unsigned>(most * parts));
     if constexpr (FIND) {
@@ -929,7 +918,7 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
         if (st != TWELL_OK) return st;
         return twell_host::launch_dep(out, out_blocks, dim3(kLoraThreads), O::kBytes, s, g, t, most, in_parts);
     } else {
-        const int blocks = lora_blocks(about, sms, kMost);
+        const int blocks = lora_blocks(about, sms);
         const twell_status st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t, most);
         if (st != TWELL_OK) return st;
         return twell_host::launch_dep(out, out_blocks, dim3(kLoraThreads), O::kBytes, s, g, t, most, 0);
