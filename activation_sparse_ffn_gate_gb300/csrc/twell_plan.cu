@@ -341,7 +341,7 @@ extern "C" twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page
         return TWELL_ERR_INVALID;
     if (n_tokens > 0 && (slots == nullptr || positions == nullptr || owner == nullptr)) return TWELL_ERR_INVALID;
     if (!aligned16(slots) || !aligned16(positions) || !aligned16(owner)) return TWELL_ERR_INVALID;
-    if (B > 0 && seq_lens_out == new_lens) return TWELL_ERR_INVALID;  // read while it is written
+    if (B > 0 && (seq_lens_out == new_lens || seq_lens_out == labels)) return TWELL_ERR_INVALID;  // read while it is written
     const void* words[] = {pool->ring, pool->state, page_table, seq_lens, new_lens, labels, starts, seq_lens_out, state_out};
     for (const void* p : words)
         if (reinterpret_cast<uintptr_t>(p) % sizeof(int32_t) != 0) return TWELL_ERR_INVALID;

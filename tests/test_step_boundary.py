@@ -54,7 +54,7 @@ def test_rope_refuses(lib, bwd):
     assert _rope(lib, bwd=bwd, S=0, pos=None) == OK and _rope(lib, bwd=bwd, B=0, pos=None) == OK
 
 
-def _plan(lib, n_pages=8, page=16, ring=1 << 20, state=1 << 20, table=A, mp=4, lens=A, news=A, labels=None, B=2, M=8, slots=A,
+def _plan(lib, n_pages=8, page=16, ring=1 << 20, state=1 << 20, table=A, mp=4, lens=A, news=1 << 22, labels=None, B=2, M=8, slots=A,
           pos=A, own=A, starts=A, lo=A, so=A, st=A):
     pool = binding._PagePool(n_pages, page, ring, state)
     return lib.twell_kv_plan(ctypes.byref(pool), table, mp, lens, news, labels, B, M, slots, pos, own, starts, lo, so, st, None)
@@ -64,7 +64,7 @@ def test_plan_refuses(lib):
     for bad in (dict(n_pages=-1), dict(page=0), dict(ring=None), dict(state=None), dict(table=None), dict(mp=0), dict(lens=None),
                 dict(news=None), dict(B=-1), dict(M=-1), dict(slots=None), dict(pos=None), dict(own=None), dict(starts=None),
                 dict(lo=None), dict(so=None), dict(st=None), dict(slots=ODD), dict(pos=ODD), dict(own=ODD), dict(lens=BYTE),
-                dict(labels=BYTE), dict(table=BYTE), dict(state=(1 << 20) + 2)):
+                dict(labels=BYTE), dict(table=BYTE), dict(state=(1 << 20) + 2), dict(lo=1 << 22), dict(labels=1 << 23, lo=1 << 23)):
         assert _plan(lib, **bad) == INVALID, bad
     for bad in (dict(page=12), dict(page=2048), dict(B=4097), dict(n_pages=1 << 27), dict(M=(1 << 31) - 1)):
         assert _plan(lib, **bad) == UNSUPPORTED, bad
