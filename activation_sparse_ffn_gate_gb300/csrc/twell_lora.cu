@@ -10,14 +10,15 @@
 // What costs a small batch is its chain of loads, what costs a large one its bytes; hence three ways:
 // - Few tiles, each of which can have eight SMs: one kernel, a cluster of eight blocks a tile. Each has a part of k, the sums go
 //   to all of them through distributed shared memory, and each then has a part of n, whose first pieces are on their way
-//   meanwhile. One token, 2048 x 2048, rank 16: 4.5 us, of which the launch is 1.6; the rest is ids, x and A, the
-//   exchange, y. One token of rank 64, 2048 x 4096: 7.5 us (10.6 with one piece of B under way instead of two).
+//   meanwhile. One token, 2048 x 2048, rank 16: 3.5 us, of which the launch is 1.6; the rest is ids, x and A, the
+//   exchange, y. One token of rank 64, 2048 x 4096: 5.0 us.
 // - Up to 512 tokens else: two kernels, whose blocks need not start together as a cluster's do; the second one's copies run
-//   while the first is at work. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 13.3 us (18.0 in clusters); 256
-//   tokens of rank 16: 8.5 (15.8).
-// - Larger ones: the same two after a kernel that groups the tokens by adapter. 16384 tokens, 2048 x 4096, rank 16: 67 us, of
+//   while the first is at work. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 10.7 us (16.8 in clusters; floor
+//   3.0); 256 tokens with 64 adapters of rank 16, 2048 x 2048: 7.2 (9.7; floor 1.7).
+// - Larger ones: the same two after a kernel that groups the tokens by adapter. 16384 tokens, 2048 x 4096, rank 16: 66 us, of
 //   which grouping takes 6, the first product 15 (67 MB) and the second 44 (268 MB, 91% of the copy rate). Above rank 32 the
-//   weights that each tile brings from L2 count: rank 64, 2048 x 2048: 65 us for 182 MB.
+//   weights that each tile brings from L2 count: rank 64, 2048 x 2048: 61 us for 182 MB. Both products in one kernel, by a
+//   block or a cluster a tile, were no faster: 84 us for those 16384 tokens, 22.6 against 23.7 for 3001 of rank 24.
 #include "twell_mma.cuh"
 #include "twell_ops.cuh"
 
@@ -32,11 +33,12 @@ constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraCluster = 8;      // most blocks a tile
 constexpr int kLoraSmallN = 512;     // up to here every block finds its tile from the ids itself
-// A larger batch's tiles have 32 tokens: with 64 their weights are read half as often, but a block takes an SM for itself (16384
-// tokens, 2048 x 2048, rank 64: 64.7 us and 73.6; rank 16, 2048 x 4096: 70 and 120).
+// A larger batch's tiles have 32 tokens. With 16 their weights are read twice as often (9000 tokens, 1024 x 3000, rank 128: 102 us
+// against 65; 16384 of rank 64, 2048 x 2048: 68 and 61). With 64 they are read half as often, but a block takes an SM for
+// itself (before the last steps: the 16384 of rank 64 73.6 against 64.7, of rank 16, 2048 x 4096, 120 against 70).
 constexpr int kLoraMT = 2;
-// Most blocks of a tile that share its k where each leaves its own sums (64 tokens of rank 16, 2048 x 2048: 6.9 us with four, 8.9
-// with eight), and of all tiles.
+// Most blocks of a tile that share its k where each leaves its own sums (64 tokens of rank 16, 2048 x 2048: 5.8 us with four, 6.1
+// with two, 7.4 with eight; 500 of rank 64, 4096 x 4096: 12.7, 15.4 and 13.2), and of all tiles.
 constexpr int kLoraParts = 4;
 constexpr int kLoraSums = 1024;
 constexpr int kLoraGroupThreads = 1024;
@@ -840,7 +842,8 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
     }
 }
 
-// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 25.0 us with two, 29.1 with four).
+// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 23.7 us with two, 24.8 with one,
+// 27.3 with four).
 int lora_blocks(long long tiles, int sms)
 {
     int b = 1;
@@ -935,8 +938,8 @@ twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
     static_assert(kLoraFindBytes <= kLoraWarps * S::kRing, "room to find a tile");
     static_assert(S::bytes(kLoraCluster) <= 224 * 1024, "a block's shared memory");
     const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.5 us and 5.4 in two kernels; of rank 64, 2048 x
-    // 4096: 10.7 and 9.0)
+    // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.5 us and 5.0 in two kernels; 18 of rank 64, 2048
+    // x 4096: 5.5 and 6.6; 30 of them: 10.0 and 7.2)
     if (tiles * kLoraCluster > (RG == 1 ? 2 : 1) * sms) return run_products<1, RG, RT, true>(g, reinterpret_cast<uint4*>(ws + LoraWs(g.N, g.R).t), sms, s);
     auto kern = lora_kernel<1, RG, RT>;
     static std::atomic<uint64_t> allowed{0};

@@ -4,7 +4,8 @@
 //
 // Bounded by memory traffic where tokens are many (every value read and written once) and by the launch where they are
 // few. A thread keeps the turns of V pairs of one token in registers and takes them through the heads, so that an angle is
-// formed once a token where tokens fill the device.
+// formed once a token where tokens fill the device. 16001 tokens of 24 heads of 128 in bf16 34.0 us, 86% of the copy rate (what
+// is left: 68 registers a thread leave 38% of the warps, too few loads under way); 16384 in fp32 61.1 us, 97%; one token 1.75.
 // The angle is formed in integers: a frequency is a count of 2^-64 turns a position, so that position x frequency modulo
 // 2^64 is the fraction of a turn, whatever the position (an fp32 product is off by 0.06 rad a million positions away). The
 // upper 32 bits are cut into a quarter of a turn and a rest within +-1/8, whose sine and cosine are their power series.
