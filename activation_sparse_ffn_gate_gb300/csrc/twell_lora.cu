@@ -31,15 +31,18 @@ constexpr int kLoraMaxTokens = 1 << 20;
 constexpr int kLoraMaxDim = 1 << 20;
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
-constexpr int kLoraCluster = 8;      // most blocks a tile
-constexpr int kLoraSmallN = 512;     // up to here every block finds its tile from the ids itself
+constexpr int kLoraClusterShift = 3, kLoraCluster = 1 << kLoraClusterShift;  // most blocks a tile
+// Every block finds its tile from the ids itself up to so many tokens a thread, 32 adjacent ones of a warp at a time: always
+// up to kLoraSmallN tokens, up to kLoraFindN where the adapters are many (lora_finds).
+constexpr int kLoraFindPer = 2, kLoraFindMore = 4;
+constexpr int kLoraSmallN = kLoraFindPer * kLoraThreads, kLoraFindN = kLoraFindMore * kLoraThreads;
 // A larger batch's tiles have 32 tokens. With 16 their weights are read twice as often (9000 tokens, 1024 x 3000, rank 128: 102 us
 // against 65; 16384 of rank 64, 2048 x 2048: 68 and 61). With 64 they are read half as often, but a block takes an SM for
 // itself (before the last steps: the 16384 of rank 64 73.6 against 64.7, of rank 16, 2048 x 4096, 120 against 70).
 constexpr int kLoraMT = 2;
 // Most blocks of a tile that share its k where each leaves its own sums (64 tokens of rank 16, 2048 x 2048: 5.8 us with four, 6.1
 // with two, 7.4 with eight; 500 of rank 64, 4096 x 4096: 12.7, 15.4 and 13.2), and of all tiles.
-constexpr int kLoraParts = 4;
+constexpr int kLoraParts = 8;
 constexpr int kLoraSums = 1024;
 constexpr int kLoraGroupThreads = 1024;
 constexpr int kLoraPass = 16384;     // tokens of a larger batch that go together
@@ -186,6 +189,17 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
     return 0;
 }
 
+// Blocks that share a tile, of `blocks` for `tiles` (the host knows only how many tiles there may be), as a power of two: a
+// division would be 0.1 us before the first load.
+__device__ __forceinline__ int lora_sharers(int blocks, int tiles, int most)
+{
+    int s = 0;
+    while (2 << s <= most && tiles << (s + 1) <= blocks) ++s;
+    return s;
+}
+// Where block `part` of 2^shift has its share of n.
+__device__ __forceinline__ int lora_share(int n, int part, int shift) { return n * part >> shift; }
+
 // A tile of tokens of one adapter.
 struct LoraTile {
     int id, rank;    // id -1: there is no such tile
@@ -193,26 +207,27 @@ struct LoraTile {
     int tokens;
 };
 
-// Tile `index` among those of at most kLoraSmallN tokens: adapters in the order of their first tokens, each one's tokens in their
+// Tile place(number of tiles) among those of at most PER kLoraThreads tokens: adapters in the order of their first tokens, each one's tokens in their
 // own, TOK a tile; everyone who looks for a tile finds the same. Up to 32 tokens every warp does it by itself. More are
 // counted by adapter in shared memory, with the least of each one's tokens (sums and minima: in any order the same), and the
 // tiles before a token's are a scan over the tokens. Returns the tile's tokens, -1 past the last. `scratch`:
 // kLoraFindBytes, free again afterwards.
 constexpr size_t kLoraFindBytes = 2 * sizeof(int) * (kLoraMaxAdapters + 1);
-template <int TOK>
-__device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, void* scratch, LoraTile& tile)
+template <int TOK, int PER, typename F>
+__device__ __forceinline__ const int* lora_find(const LoraArgs& g, F place, void* scratch, LoraTile& tile)
 {
     __shared__ int tok[kLoraWarps][TOK];
     __shared__ int found[3];  // adapter, number of the tile's first token, rank
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     tile.id = -1;
-    tile.first = index * TOK;
+    tile.first = 0;
     if (g.N <= 32) {
         const int mine = lane < g.N ? lora_id(g, g.ids[lane]) : -1;
         const int rank = mine >= 0 ? lora_rank(g, mine) : 0;
         const unsigned same = __match_any_sync(0xffffffffu, mine), below = (1u << lane) - 1;
         const int num = __popc(same & below);
         const unsigned firsts = __ballot_sync(0xffffffffu, mine >= 0 && num % TOK == 0);
+        const int index = place(__popc(firsts));
         const unsigned it = __ballot_sync(0xffffffffu, (firsts >> lane & 1) && __popc(firsts & below) == index);
         if (lane < TOK) tok[warp][lane] = -1;
         __syncwarp();
@@ -225,19 +240,18 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
         __syncwarp();
         return tok[warp];
     }
-    constexpr int kPer = kLoraSmallN / kLoraThreads;  // tokens a thread; of a warp 32 adjacent ones at a time
-    static_assert(kPer * kLoraWarps <= 32, "a warp adds up the totals");
+    static_assert(PER * kLoraWarps <= 32, "a warp adds up the totals");
     __shared__ int totals[2][32];              // tiles of each 32 tokens; tokens of the adapter
     int2* bins = static_cast<int2*>(scratch);  // [L + 1]: tokens of an adapter, the first of them
-    int own[kPer], rank[kPer];
+    int own[PER], rank[PER];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) own[j] = j * kLoraThreads + tid < g.N ? __ldg(g.ids + j * kLoraThreads + tid) : 0;
+    for (int j = 0; j < PER; ++j) own[j] = j * kLoraThreads + tid < g.N ? __ldg(g.ids + j * kLoraThreads + tid) : 0;
     for (int i = tid; i <= g.L; i += kLoraThreads) bins[i] = make_int2(0, INT32_MAX);
     if (tid == 0) found[0] = -1;
     if (tid < TOK) tok[0][tid] = -1;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
         const int i = j * kLoraThreads + tid;
         own[j] = i < g.N ? lora_id(g, own[j]) : -1;
         rank[j] = 0;
@@ -249,9 +263,9 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
         }
     }
     __syncthreads();
-    int tiles[kPer], before[kPer];  // that begin with this token; before it in its 32
+    int tiles[PER], before[PER];  // that begin with this token; before it in its 32
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
         const int i = j * kLoraThreads + tid;
         tiles[j] = before[j] = 0;
         if (j * kLoraThreads >= g.N) continue;
@@ -269,8 +283,9 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
         if (lane == 31) totals[0][j * kLoraWarps + warp] = incl;
     }
     __syncthreads();
+    const int index = place(__reduce_add_sync(0xffffffffu, 32 * lane < g.N ? totals[0][lane] : 0));
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
         if (j * kLoraThreads >= g.N) continue;
         const int at = before[j] + __reduce_add_sync(0xffffffffu, lane < j * kLoraWarps + warp ? totals[0][lane] : 0);
         if (index >= at && index < at + tiles[j]) {
@@ -288,15 +303,15 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
         report(g.status, TWELL_ERR_DEVICE_CHECK);
         tile.rank = 0;
     }
-    unsigned mine[kPer];
+    unsigned mine[PER];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
         mine[j] = __ballot_sync(0xffffffffu, own[j] == tile.id);
         if (lane == 0) totals[1][j * kLoraWarps + warp] = __popc(mine[j]);
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
         const int num = __popc(mine[j] & ((1u << lane) - 1)) - found[1] +
                         __reduce_add_sync(0xffffffffu, lane < j * kLoraWarps + warp ? totals[1][lane] : 0);
         if (own[j] == tile.id && num >= 0 && num < TOK) tok[0][num] = j * kLoraThreads + tid;
@@ -305,13 +320,14 @@ __device__ __forceinline__ const int* lora_find(const LoraArgs& g, int index, vo
     return tok[0];
 }
 
-// Tile `index` of a batch, and the tokens of this lane's rows.
-template <int MT, bool FIND>
-__device__ __forceinline__ bool lora_tile(const LoraArgs& g, int index, uint8_t* smem, LoraTile& tile, int (&token)[MT][2])
+// Tile place(number of tiles) of a batch, and the tokens of this lane's rows. `known`: of a larger batch, the tile whatever that
+// number is, so that it is requested with it.
+template <int MT, int FIND, typename F>
+__device__ __forceinline__ bool lora_tile(const LoraArgs& g, F place, int known, uint8_t* smem, LoraTile& tile, int (&token)[MT][2])
 {
     const int gr = (threadIdx.x & 31) >> 2;
-    if constexpr (FIND) {
-        const int* tok = lora_find<16 * MT>(g, index, smem, tile);
+    if constexpr (FIND != 0) {
+        const int* tok = lora_find<16 * MT, FIND>(g, place, smem, tile);
         if (tile.id < 0) return false;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -320,7 +336,8 @@ __device__ __forceinline__ bool lora_tile(const LoraArgs& g, int index, uint8_t*
         __syncthreads();  // the memory is free
     } else {
         // requested together: what lies past the last tile is some earlier call's
-        const int n = *g.n_tiles;
+        const int n = *g.n_tiles, index = known >= 0 ? known : place(n);
+        if (known < 0 && index >= n) return false;
         const int4 t = g.tiles[index];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -340,7 +357,7 @@ __device__ __forceinline__ bool lora_tile(const LoraArgs& g, int index, uint8_t*
 // t = A x over one block's part of k: a warp has kWarpRanks ranks and every kWays-th 64 columns, 32 a stage. Leaves the warps'
 // sums in their rings, which are free but for that; `between` runs once a warp's ring is (the copies of what comes next).
 template <typename S, int MT, int RG, int RT, typename F>
-__device__ __forceinline__ void lora_shrink(const LoraArgs& g, int id, int rank, int part, int blocks, const int (&token)[MT][2],
+__device__ __forceinline__ void lora_shrink(const LoraArgs& g, int id, int rank, int part, int shift, const int (&token)[MT][2],
                                             uint8_t* ring_at, F between)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, c = lane & 3;
@@ -348,8 +365,7 @@ __device__ __forceinline__ void lora_shrink(const LoraArgs& g, int id, int rank,
     const int rg = warp % RG, way = warp / RG;
     float acc[MT][RT][4] = {};
     {
-        const int kb_all = (g.k + 63) / 64, kb0 = static_cast<int>(static_cast<long long>(kb_all) * part / blocks) + way,
-                  kb1 = static_cast<int>(static_cast<long long>(kb_all) * (part + 1) / blocks);
+        const int kb_all = (g.k + 63) / 64, kb0 = lora_share(kb_all, part, shift) + way, kb1 = lora_share(kb_all, part + 1, shift);
         const int row0 = rg * S::kWarpRanks + gr;
         // a warp whose ranks all lie past the adapter's has nothing to do
         const int stages = rg * S::kWarpRanks < rank && kb0 < kb1 ? (kb1 - kb0 + S::kWays - 1) / S::kWays * 2 : 0;
@@ -554,14 +570,13 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
     extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
     pdl_begin();
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, gr = lane >> 2;
-    constexpr int blocks = kLoraCluster;
+    constexpr int blocks = kLoraCluster, shift = kLoraClusterShift;
     const int part = static_cast<int>(cluster_ctarank());
     LoraTile tile;
-    const int* tok = lora_find<S::kTok>(g, static_cast<int>(blockIdx.x) / blocks, lora_smem, tile);  // where the rings come later
+    const int* tok = lora_find<S::kTok, kLoraFindPer>(g, [&](int) { return static_cast<int>(blockIdx.x) / blocks; }, lora_smem, tile);  // where the rings come later
     if (tile.id < 0) return;
     const int id = tile.id, rank = tile.rank;
-    const int nt_all = (g.n + 31) / 32, nt0 = static_cast<int>(static_cast<long long>(nt_all) * part / blocks),
-              nt1 = static_cast<int>(static_cast<long long>(nt_all) * (part + 1) / blocks);
+    const int nt_all = (g.n + 31) / 32, nt0 = lora_share(nt_all, part, shift), nt1 = lora_share(nt_all, part + 1, shift);
     if (rank == 0) {  // the same for all blocks of the cluster
         if (g.y == g.out) return;
         const int col0 = nt0 * 4, cols = min(nt1 * 4, g.n / 8) - col0;  // in chunks of 8
@@ -590,7 +605,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
     // the first pieces of the second product are on their way while t is put together
     const LoraOut<MT, RG, RT> out(g, id, rank, nt0, nt1, token, ring_at + S::kWarpSums);
     const float scale = __ldg(g.scale + id);
-    lora_shrink<S, MT, RG, RT>(g, id, rank, part, blocks, token, ring_at, [&] {
+    lora_shrink<S, MT, RG, RT>(g, id, rank, part, shift, token, ring_at, [&] {
 #pragma unroll
         for (int i = 0; i < S::kOutStages; ++i) out.template request<S::kOutStages>(i, i);
     });
@@ -638,25 +653,31 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
 // t of a batch: a tile's rows of it, as lora_parts has them. A cluster of blocks shares a tile's k where tiles are few; each then
 // adds up a share of the sums. With FIND each block of a tile leaves its own sums, [tile][part][token][rank], for the second
 // product to add up: its blocks need not start together.
-template <int MT, int RG, int RT, bool FIND>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out, int most_tiles)
+template <int MT, int RG, int RT, int FIND>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs g, uint4* __restrict__ t_out)
 {
     using S = LoraShape<MT, RG, RT, false>;
     extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
     pdl_wait();
     pdl_next();
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
-    const int blocks = FIND ? static_cast<int>(gridDim.x) / most_tiles : static_cast<int>(cluster_blocks());
-    const int index = static_cast<int>(blockIdx.x) / blocks, part = static_cast<int>(blockIdx.x) % blocks;  // of a cluster: the rank
+    int shift, blocks, index, part;  // of a cluster: the rank
+    auto take = [&](int s) {
+        shift = s, blocks = 1 << s, index = static_cast<int>(blockIdx.x) >> s, part = static_cast<int>(blockIdx.x) & (blocks - 1);
+        return index;
+    };
+    if constexpr (FIND == 0) take(31 - __clz(static_cast<int>(cluster_blocks())));
+    else index = -1;
+    auto place = [&](int tiles) { return take(lora_sharers(static_cast<int>(gridDim.x), tiles, kLoraParts)); };
     int token[MT][2];
     LoraTile tile;
-    if (!lora_tile<MT, FIND>(g, index, lora_smem, tile, token)) return;
+    if (!lora_tile<MT, FIND>(g, place, index, lora_smem, tile, token)) return;
     const int rank = tile.rank;
     if (rank == 0) return;
     constexpr int kQuads = S::kRanks / 4;
     const int quads = tile.tokens * kQuads;  // quad i is added up by block i % blocks
     __shared__ uint64_t bar;
-    if (!FIND && blocks > 1) {
+    if (FIND == 0 && blocks > 1) {
         if (tid == 0) {
             mbar_init(&bar, 1);
             fence_mbar_init();
@@ -665,9 +686,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
         cluster_arrive();  // this block runs and its barrier counts
     }
     const float scale = __ldg(g.scale + tile.id);
-    lora_shrink<S, MT, RG, RT>(g, tile.id, rank, part, blocks, token, lora_smem + warp * S::kRing, [] {});
+    lora_shrink<S, MT, RG, RT>(g, tile.id, rank, part, shift, token, lora_smem + warp * S::kRing, [] {});
     __syncthreads();
-    if constexpr (FIND) {
+    if constexpr (FIND != 0) {
         float4* to = reinterpret_cast<float4*>(t_out) + (static_cast<size_t>(index) * blocks + part) * (S::kTok * kQuads);
         for (int i = tid; i < quads; i += kLoraThreads) to[i] = lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads);
         return;
@@ -696,29 +717,42 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
 
 // y + B t of a batch: a block has a tile's rows and a part of the columns, of which a warp takes every kLoraWarps-th 32. What it
 // reads but t was there before the first product's kernel, which lets this one start after its own wait: the first pieces
-// are on their way while that one runs. `in_parts`: of a tile's sums, with FIND.
-template <int MT, int RG, int RT, bool FIND>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArgs g, const uint4* t_in, int most_tiles, int in_parts)
+// are on their way while that one runs. `most_parts`: of a tile's columns, by the number of tiles; 0: one of gridDim.x / most_tiles,
+// whatever that number is. `in_blocks`: of the first product, with FIND.
+template <int MT, int RG, int RT, int FIND>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArgs g, const uint4* t_in, int most_tiles, int most_parts, int in_blocks)
 {
     using S = LoraOutShape<MT, RG, RT>;
     extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
-    const int parts = static_cast<int>(gridDim.x) / most_tiles, index = static_cast<int>(blockIdx.x) / parts,
-              part = static_cast<int>(blockIdx.x) % parts;
+    int index = -1, in_parts = 1;
+    unsigned parts = 1, part = 0;
+    auto place = [&](int tiles) {
+        if (FIND != 0) in_parts = 1 << lora_sharers(in_blocks, tiles, kLoraParts);
+        if (most_parts == 0) return index;
+        parts = max(1u, min(static_cast<unsigned>(most_parts), gridDim.x / max(tiles, 1)));
+        part = blockIdx.x % parts;
+        return index = static_cast<int>(blockIdx.x / parts);
+    };
+    if (most_parts == 0) {
+        parts = gridDim.x / static_cast<unsigned>(most_tiles);
+        part = blockIdx.x % parts;
+        index = static_cast<int>(blockIdx.x / parts);
+    }
     int token[MT][2];
     LoraTile tile;
-    const bool is = lora_tile<MT, FIND>(g, index, lora_smem, tile, token);
+    const bool is = lora_tile<MT, FIND>(g, place, index, lora_smem, tile, token);
     if (!is || (tile.rank == 0 && g.y == g.out)) {
         if (blockIdx.x == 0) pdl_wait();  // one block is enough for the grid not to be done before the one before it
         return;
     }
     const int rank = tile.rank;
-    const int nt_all = (g.n + 31) / 32, nt0 = static_cast<int>(static_cast<long long>(nt_all) * part / parts),
-              nt1 = static_cast<int>(static_cast<long long>(nt_all) * (part + 1) / parts);
+    const unsigned nt_all = (g.n + 31) / 32;
+    const int nt0 = static_cast<int>(nt_all * part / parts), nt1 = static_cast<int>(nt_all * (part + 1) / parts);
     const LoraOut<MT, RG, RT> out(g, tile.id, rank, nt0, nt1, token, lora_smem + warp * S::kRing);
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) out.template request<S::kStages>(i, i);
-    const float scale = FIND && rank > 0 ? __ldg(g.scale + tile.id) : 0.0f;
+    const float scale = FIND != 0 && rank > 0 ? __ldg(g.scale + tile.id) : 0.0f;
     pdl_wait();
     pdl_next();
     // t as the product's fragments
@@ -734,7 +768,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
             for (int s = 0; s < 2; ++s) {
                 t[s] = make_uint4(0u, 0u, 0u, 0u);
                 if (row + 8 * s >= tile.tokens) continue;
-                if constexpr (FIND) {
+                if constexpr (FIND != 0) {
                     const float4* from = reinterpret_cast<const float4*>(t_in) + static_cast<size_t>(index) * in_parts * (16 * MT * kQuads) +
                                          (row + 8 * s) * kQuads + quad;
                     float4 u[kLoraParts];
@@ -875,27 +909,31 @@ long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / 
 
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
-// Blocks of a tile that share its k where each leaves its own sums: as far as two blocks an SM go (256 tokens with 64 adapters of
-// rank 16, 2048 x 2048: 7.2 us, 8.2 with a second round of blocks; 300 of rank 64: 12.0 and 12.7).
-int lora_parts_of(int tiles, int sms) { return std::max(1, std::min(std::min(kLoraParts, kLoraSums / tiles), 2 * sms / tiles)); }
+// Blocks of the first product where each leaves its own sums: as far as two an SM go (256 tokens with 64 adapters of rank 16, 2048 x
+// 2048: 7.2 us, 8.2 with a second round of blocks; 300 of rank 64: 12.0 and 12.7).
+int lora_in_blocks(int tiles, int sms) { return std::max(tiles, std::min(std::min(kLoraParts * tiles, 2 * sms), kLoraSums)); }
 
-// What the workspace holds of a pass: of a larger batch its tiles and their tokens, and t.
+// Whether every block finds its tile itself. Beyond kLoraSmallN tokens its tiles of 16 cost more weights than the grouping saves,
+// unless the adapters are so many that tiles of 32 would be half empty (1000 tokens, 64 adapters of rank 16, 2048 x 2048: 12.0 us and
+// 15.2 grouped; 1000 tokens with long runs of 8 adapters of rank 32, 2048 x 4096: 14.7 and 13.6).
+bool lora_finds(int N, int L) { return N <= kLoraSmallN || (N <= kLoraFindN && L >= N / 32); }
+
+// What the workspace holds of a pass: the tiles and their tokens where they are grouped, and t; else the blocks' sums.
 struct LoraWs {
     size_t tiles, order, t, total;
     LoraWs(int N, int R)
     {
-        const bool grouped = N > kLoraSmallN;
-        const int n = std::min(N, kLoraPass), tok = grouped ? 16 * kLoraMT : 16;
-        const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok));
+        const int n = std::min(N, kLoraPass), tok = 16 * kLoraMT;
+        const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok)), row = lora_ranks(R) * sizeof(float);
         tiles = 16;
-        order = tiles + (grouped ? 16 * most : 0);
-        t = order + (grouped ? sizeof(int32_t) * tok * most : 0);
-        total = t + (grouped ? n : static_cast<size_t>(tok) * kLoraSums) * lora_ranks(R) * 4;
+        order = tiles + 16 * most;
+        t = order + sizeof(int32_t) * tok * most;
+        total = std::max(N > kLoraSmallN ? t + n * row : 0, N <= kLoraFindN ? 16 * kLoraSums * row : 0);
     }
 };
 
 // The two products of a batch whose tiles are found (by FIND, or in g).
-template <int MT, int RG, int RT, bool FIND>
+template <int MT, int RG, int RT, int FIND>
 twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
 {
     using S = LoraShape<MT, RG, RT, false>;
@@ -910,37 +948,40 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
         return TWELL_ERR_CUDA;
     // a block's part of the columns: two pieces a warp at least, and one round of blocks, or kOutRounds where the tiles alone are more
     constexpr int kOutRounds = 2;
-    const long long places = 2ll * sms, about = FIND ? most : std::max(1, g.N / S::kTok);
-    const long long fill = most <= places ? places / most : (kOutRounds * places + about - 1) / about;
-    const long long parts = std::max(1ll, std::min<long long>(fill, ((g.n + 31) / 32 + 2 * kLoraWarps - 1) / (2 * kLoraWarps)));
-    if (most * parts > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
-    const dim3 out_blocks(static_cast<unsigned>(most * parts));
-    if constexpr (FIND) {
-        const int in_parts = lora_parts_of(most, sms);
-        const twell_status st = twell_host::launch_dep(in, dim3(static_cast<unsigned>(most * in_parts)), dim3(kLoraThreads), S::bytes(1), s,
-                                                       g, t, most);
+    const long long places = 2ll * sms, most_parts = ((g.n + 31) / 32 + 2 * kLoraWarps - 1) / (2 * kLoraWarps);
+    const int about = std::max(1, g.N / S::kTok);
+    const bool one = most <= places;
+    const long long out_blocks = one ? std::min(places, most * most_parts) : most * std::min((kOutRounds * places + about - 1) / about, most_parts);
+    if (out_blocks > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
+    const dim3 out_grid(static_cast<unsigned>(out_blocks)), threads(kLoraThreads);
+    const int by_tiles = one ? static_cast<int>(most_parts) : 0;
+    if constexpr (FIND != 0) {
+        const int in_blocks = lora_in_blocks(most, sms);
+        const twell_status st = twell_host::launch_dep(in, dim3(static_cast<unsigned>(in_blocks)), threads, S::bytes(1), s, g, t);
         if (st != TWELL_OK) return st;
-        return twell_host::launch_dep(out, out_blocks, dim3(kLoraThreads), O::kBytes, s, g, t, most, in_parts);
+        return twell_host::launch_dep(out, out_grid, threads, O::kBytes, s, g, t, most, by_tiles, in_blocks);
     } else {
         const int blocks = lora_blocks(about, sms);
-        const twell_status st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t, most);
+        const twell_status st = launch_lora(in, most, blocks, S::bytes(blocks), s, g, t);
         if (st != TWELL_OK) return st;
-        return twell_host::launch_dep(out, out_blocks, dim3(kLoraThreads), O::kBytes, s, g, t, most, 0);
+        return twell_host::launch_dep(out, out_grid, threads, O::kBytes, s, g, t, most, by_tiles, 0);
     }
 }
 
-// At most kLoraSmallN tokens: where the device holds all tiles' clusters at once, in one kernel; else in two, whose blocks need not
+// A batch whose blocks find their tiles: where the device holds all tiles' clusters at once, in one kernel; else in two, whose blocks need not
 // start together.
 template <int RG, int RT>
 twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
 {
+    uint4* sums = reinterpret_cast<uint4*>(ws);
+    if (g.N > kLoraSmallN) return run_products<1, RG, RT, kLoraFindMore>(g, sums, sms, s);
     using S = LoraShape<1, RG, RT, true>;
     static_assert(kLoraFindBytes <= kLoraWarps * S::kRing, "room to find a tile");
     static_assert(S::bytes(kLoraCluster) <= 224 * 1024, "a block's shared memory");
     const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
     // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.5 us and 5.0 in two kernels; 18 of rank 64, 2048
     // x 4096: 5.5 and 6.6; 30 of them: 10.0 and 7.2)
-    if (tiles * kLoraCluster > (RG == 1 ? 2 : 1) * sms) return run_products<1, RG, RT, true>(g, reinterpret_cast<uint4*>(ws + LoraWs(g.N, g.R).t), sms, s);
+    if (tiles * kLoraCluster > (RG == 1 ? 2 : 1) * sms) return run_products<1, RG, RT, kLoraFindPer>(g, sums, sms, s);
     auto kern = lora_kernel<1, RG, RT>;
     static std::atomic<uint64_t> allowed{0};
     if (twell_host::allow_smem(kern, S::bytes(kLoraCluster), allowed) != TWELL_OK) return TWELL_ERR_CUDA;
@@ -959,7 +1000,7 @@ twell_status run_pass(LoraArgs g, uint8_t* ws, const LoraWs& at, int sms, cudaSt
     g.n_tiles = n_tiles;
     g.tiles = tiles;
     g.order = order;
-    return run_products<kLoraMT, RG, RT, false>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
+    return run_products<kLoraMT, RG, RT, 0>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
 }
 
 }  // namespace
@@ -1004,7 +1045,7 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
                          static_cast<const bf*>(y), static_cast<bf*>(out), ad->scale, ad->ranks, ids, dev_status,
                          ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, wait_limit_ns(), nullptr, nullptr, nullptr};
     uint8_t* w = static_cast<uint8_t*>(ws);
-    if (N <= twell::kLoraSmallN)
+    if (twell::lora_finds(N, ad->n_adapters))
         return ad->rank <= 16   ? twell::run_small<1, 2>(g, w, dev.sm_count, s)
                : ad->rank <= 32 ? twell::run_small<1, 4>(g, w, dev.sm_count, s)
                : ad->rank <= 64 ? twell::run_small<2, 4>(g, w, dev.sm_count, s)

@@ -93,6 +93,7 @@ def test_decode_batches(cuda_dev, N, k, n, R, ragged, form):
 
 @pytest.mark.parametrize("form", ["any", "one", "runs"])
 @pytest.mark.parametrize("N,k,n,R,L", [(65, 128, 64, 16, 3), (257, 520, 264, 8, 40), (513, 256, 136, 24, 2), (700, 264, 512, 128, 5), (1025, 72, 80, 64, 300),
+                                       (513, 136, 264, 16, 16), (700, 264, 136, 32, 22), (991, 520, 1032, 64, 4000), (1024, 2048, 72, 128, 64),
                                        (2000, 512, 520, 32, 4), (5000, 136, 264, 16, 9)])
 def test_larger_batches(cuda_dev, N, k, n, R, L, form):
     for ragged in (False, True):
