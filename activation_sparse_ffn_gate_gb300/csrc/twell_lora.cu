@@ -369,24 +369,35 @@ __device__ __forceinline__ void lora_shrink(const LoraArgs& g, int id, int rank,
         const int row0 = rg * S::kWarpRanks + gr;
         // a warp whose ranks all lie past the adapter's has nothing to do
         const int stages = rg * S::kWarpRanks < rank && kb0 < kb1 ? (kb1 - kb0 + S::kWays - 1) / S::kWays * 2 : 0;
-        const __nv_bfloat16* A = g.a + (static_cast<int64_t>(id) * g.R + row0) * g.k;
+        // rows' addresses and how many bytes of a row's 16 there are: what a copy costs beside itself is one sum and one mask
+        const char* A[RT];
+        const char* X[MT][2];
+        int a_bytes[RT], x_bytes[MT][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const bool live = row0 + 8 * r < rank;
+            A[r] = reinterpret_cast<const char*>(live ? g.a + (static_cast<int64_t>(id) * g.R + row0 + 8 * r) * g.k : g.a);
+            a_bytes[r] = live ? 16 : 0;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bool live = token[m][s] >= 0;
+                X[m][s] = reinterpret_cast<const char*>(live ? g.x + token[m][s] * g.ldx : g.x);
+                x_bytes[m][s] = live ? 16 : 0;
+            }
         auto request = [&](int i, int slot) {
             if (i < stages) {
-                const int col = 64 * (kb0 + (i >> 1) * S::kWays) + 32 * (i & 1) + 8 * c;
+                const int col = 64 * (kb0 + (i >> 1) * S::kWays) + 32 * (i & 1) + 8 * c, in = col < g.k ? -1 : 0;
+                const unsigned off = 2 * col & in;
                 const uint32_t at = mine + slot * S::kIn;
-                const bool in = col < g.k;
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const bool live = in && row0 + 8 * r < rank;
-                    copy16(at + r * 512, live ? A + static_cast<int64_t>(8 * r) * g.k + col : g.a, live ? 16 : 0);
-                }
+                for (int r = 0; r < RT; ++r) copy16(at + r * 512, A[r] + off, a_bytes[r] & in);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const bool live = in && token[m][s] >= 0;
-                        copy16(at + (RT + 2 * m + s) * 512, live ? g.x + token[m][s] * g.ldx + col : g.x, live ? 16 : 0);
-                    }
+                    for (int s = 0; s < 2; ++s) copy16(at + (RT + 2 * m + s) * 512, X[m][s] + off, x_bytes[m][s] & in);
             }
             copies_end();
         };
@@ -459,14 +470,28 @@ struct LoraOut {
     using S = LoraOutShape<MT, RG, RT>;
     static constexpr int kKb = S::kRanks / S::kBlock, kPer = S::kBlock / 4;  // ranks a lane takes at a time
     const LoraArgs& g;
-    const __nv_bfloat16* B;
-    const int (&token)[MT][2];
+    const char *B, *y[MT][2];  // of this lane: its first row of the adapter's, its tokens' rows
+    char* out[MT][2];
+    int y_bytes[MT][2], b_bytes[kKb];  // that there are of a copy's 16 or 8
     uint32_t mine;
     int rank, first, stages;
     __device__ __forceinline__ LoraOut(const LoraArgs& g, int id, int rank, int nt0, int nt1, const int (&token)[MT][2], const uint8_t* ring_at)
-        : g(g), B(g.b + static_cast<int64_t>(id) * g.n * g.R), token(token), rank(rank)
+        : g(g), rank(rank)
     {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb) b_bytes[kb] = 2 * min(max(rank - kb * S::kBlock - kPer * c, 0), kPer);
+        B = reinterpret_cast<const char*>(g.b);
+        if (b_bytes[0] > 0) B += ((static_cast<int64_t>(id) * g.n + 8 * (gr >> 1) + (gr & 1)) * g.R + kPer * c) * 2;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int t = max(token[m][s], 0);
+                y[m][s] = reinterpret_cast<const char*>(g.y + t * g.ldy);
+                out[m][s] = reinterpret_cast<char*>(g.out + t * g.ldo);
+                y_bytes[m][s] = token[m][s] >= 0 ? 16 : 0;
+            }
         mine = smem_u32(ring_at) + lane * 16;
         first = nt0 + 2 * warp;
         const int left = nt1 - first;  // a warp has pieces 0 and 1 of every 2 kLoraWarps
@@ -478,26 +503,25 @@ struct LoraOut {
     {
         if (i < stages) {
             const int lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
-            const int base = column(i), col = base + 8 * c, brow = base + 8 * (gr >> 1);
+            const int base = column(i), col = base + 8 * c, in = col < g.n ? -1 : 0, rows = base + 8 * (gr >> 1) < g.n ? -1 : 0;
+            const unsigned off = 2 * col & in;
             const uint32_t at = mine + slot * S::kStage;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const bool live = col < g.n && token[m][s] >= 0;
-                    copy16(at + (2 * m + s) * 512, live ? g.y + token[m][s] * g.ldy + col : g.y, live ? 16 : 0);
-                }
+                for (int s = 0; s < 2; ++s) copy16(at + (2 * m + s) * 512, y[m][s] + off, y_bytes[m][s] & in);
+            const char* from = B + static_cast<int64_t>(base & rows) * g.R * 2;
 #pragma unroll
-            for (int kb = 0; kb < kKb; ++kb)
+            for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int kb = 0; kb < kKb; ++kb) {
                     // what lies past the rank becomes zeros, whatever it is
-                    const int r0 = kb * S::kBlock + kPer * c, live = brow < g.n ? min(max(rank - r0, 0), kPer) : 0;
-                    const __nv_bfloat16* from = live ? B + static_cast<int64_t>(brow + 2 * u + (gr & 1)) * g.R + r0 : g.b;
                     const uint32_t to = at + 2 * MT * 512 + (kb * 4 + u) * (kPer * 64);
-                    if constexpr (kPer == 8) copy16(to, from, 2 * live);
-                    else copy8(to - lane * 8, from, 2 * live);
+                    if constexpr (kPer == 8) copy16(to, from + kb * (S::kBlock * 2), b_bytes[kb] & rows);
+                    else copy8(to - lane * 8, from + kb * (S::kBlock * 2), b_bytes[kb] & rows);
                 }
+                from += 4 * g.R;
+            }
         }
         copies_end();
     }
@@ -553,7 +577,7 @@ struct LoraOut {
                         }
                         y = pack16(v, static_cast<__nv_bfloat16*>(nullptr));
                     }
-                    if (col < g.n && token[m][s] >= 0) *reinterpret_cast<uint4*>(g.out + token[m][s] * g.ldo + col) = y;
+                    if (col < g.n && y_bytes[m][s] > 0) *reinterpret_cast<uint4*>(out[m][s] + 2 * col) = y;
                 }
             request<STAGES>(i + STAGES, slot);
             slot = slot + 1 == STAGES ? 0 : slot + 1;
