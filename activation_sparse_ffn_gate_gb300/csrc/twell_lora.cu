@@ -10,15 +10,16 @@
 // What costs a small batch is its chain of loads, what costs a large one its bytes; hence three ways:
 // - Few tiles, each of which can have eight SMs: one kernel, a cluster of eight blocks a tile. Each has a part of k, the sums go
 //   to all of them through distributed shared memory, and each then has a part of n, whose first pieces are on their way
-//   meanwhile. One token, 2048 x 2048, rank 16: 3.5 us, of which the launch is 1.6; the rest is ids, x and A, the
+//   meanwhile. One token, 2048 x 2048, rank 16: 3.4 us, of which the launch is 1.6; the rest is ids, x and A, the
 //   exchange, y. One token of rank 64, 2048 x 4096: 5.0 us.
-// - Up to 512 tokens else: two kernels, whose blocks need not start together as a cluster's do; the second one's copies run
-//   while the first is at work. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 10.7 us (16.8 in clusters; floor
-//   3.0); 256 tokens with 64 adapters of rank 16, 2048 x 2048: 7.2 (9.7; floor 1.7).
-// - Larger ones: the same two after a kernel that groups the tokens by adapter. 16384 tokens, 2048 x 4096, rank 16: 66 us, of
+// - Up to 512 tokens else (1024 where the adapters are many): two kernels, whose blocks need not start together as a cluster's do;
+//   the second one's copies run while the first is at work. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 10.2 us
+//   (16.2 in clusters; floor 3.0); 256 tokens with 64 adapters of rank 16, 2048 x 2048: 6.9 (9.5; floor 1.7).
+// - Larger ones: the same two after a kernel that groups the tokens by adapter. 16384 tokens, 2048 x 4096, rank 16: 65 us, of
 //   which grouping takes 6, the first product 15 (67 MB) and the second 44 (268 MB, 91% of the copy rate). Above rank 32 the
 //   weights that each tile brings from L2 count: rank 64, 2048 x 2048: 61 us for 182 MB. Both products in one kernel, by a
-//   block or a cluster a tile, were no faster: 84 us for those 16384 tokens, 22.6 against 23.7 for 3001 of rank 24.
+//   block or a cluster a tile, were no faster: 84 us for those 16384 tokens, 22.6 against 23.7 for 3001 of rank 24; nor were rows
+//   brought to L2 while the tokens are grouped (68, 24.2).
 #include "twell_mma.cuh"
 #include "twell_ops.cuh"
 
@@ -36,12 +37,13 @@ constexpr int kLoraClusterShift = 3, kLoraCluster = 1 << kLoraClusterShift;  // 
 // up to kLoraSmallN tokens, up to kLoraFindN where the adapters are many (lora_finds).
 constexpr int kLoraFindPer = 2, kLoraFindMore = 4;
 constexpr int kLoraSmallN = kLoraFindPer * kLoraThreads, kLoraFindN = kLoraFindMore * kLoraThreads;
-// A larger batch's tiles have 32 tokens. With 16 their weights are read twice as often (9000 tokens, 1024 x 3000, rank 128: 102 us
-// against 65; 16384 of rank 64, 2048 x 2048: 68 and 61). With 64 they are read half as often, but a block takes an SM for
-// itself (before the last steps: the 16384 of rank 64 73.6 against 64.7, of rank 16, 2048 x 4096, 120 against 70).
+// A larger batch's tiles have 32 tokens. With 16 their weights are read twice as often (9000 tokens, 1024 x 3000, rank 128: 98 us
+// against 62; 16384 of rank 64, 2048 x 2048: 68 and 61; 3001 of rank 24: 25.0 and 23.3). With 64 they are read half as often, but
+// a block takes an SM for itself (before the last steps: the 16384 of rank 64 73.6 against 64.7, of rank 16, 2048 x 4096, 120
+// against 70).
 constexpr int kLoraMT = 2;
-// Most blocks of a tile that share its k where each leaves its own sums (64 tokens of rank 16, 2048 x 2048: 5.8 us with four, 6.1
-// with two, 7.4 with eight; 500 of rank 64, 4096 x 4096: 12.7, 15.4 and 13.2), and of all tiles.
+// Most blocks of a tile that share its k where each leaves its own sums (325 tokens of few adapters of rank 64, 7312 x 704: 11.7 us,
+// 12.3 with four; 64 of rank 16, 2048 x 2048: 5.2 and 5.5), and of all tiles.
 constexpr int kLoraParts = 8;
 constexpr int kLoraSums = 1024;
 constexpr int kLoraGroupThreads = 1024;
@@ -189,8 +191,8 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
     return 0;
 }
 
-// Blocks that share a tile, of `blocks` for `tiles` (the host knows only how many tiles there may be), as a power of two: a
-// division would be 0.1 us before the first load.
+// Blocks that share a tile, of `blocks` for `tiles` (the host knows only how many tiles there may be), as a power of two:
+// divisions here and for the shares were 0.4 of 6.2 us before the first loads.
 __device__ __forceinline__ int lora_sharers(int blocks, int tiles, int most)
 {
     int s = 0;
@@ -207,10 +209,10 @@ struct LoraTile {
     int tokens;
 };
 
-// Tile place(number of tiles) among those of at most PER kLoraThreads tokens: adapters in the order of their first tokens, each one's tokens in their
-// own, TOK a tile; everyone who looks for a tile finds the same. Up to 32 tokens every warp does it by itself. More are
-// counted by adapter in shared memory, with the least of each one's tokens (sums and minima: in any order the same), and the
-// tiles before a token's are a scan over the tokens. Returns the tile's tokens, -1 past the last. `scratch`:
+// Tile place(number of tiles) among those of at most PER kLoraThreads tokens: adapters in the order of their first tokens, each
+// one's tokens in their own, TOK a tile; everyone who looks for a tile finds the same. Up to 32 tokens every warp does it by
+// itself. More are counted by adapter in shared memory, with the least of each one's tokens (sums and minima: in any order the
+// same), and the tiles before a token's are a scan over the tokens. Returns the tile's tokens, -1 past the last. `scratch`:
 // kLoraFindBytes, free again afterwards.
 constexpr size_t kLoraFindBytes = 2 * sizeof(int) * (kLoraMaxAdapters + 1);
 template <int TOK, int PER, typename F>
@@ -900,8 +902,8 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
     }
 }
 
-// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 23.7 us with two, 24.8 with one,
-// 27.3 with four).
+// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 23.3 us with two, 24.4 with one,
+// 26.7 with four).
 int lora_blocks(long long tiles, int sms)
 {
     int b = 1;
@@ -933,13 +935,14 @@ long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / 
 
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
-// Blocks of the first product where each leaves its own sums: as far as two an SM go (256 tokens with 64 adapters of rank 16, 2048 x
-// 2048: 7.2 us, 8.2 with a second round of blocks; 300 of rank 64: 12.0 and 12.7).
+// Blocks of the first product where each leaves its own sums: as far as two an SM go (when this was chosen, 256 tokens with 64 adapters
+// of rank 16, 2048 x 2048: 7.2 us, 8.2 with a second round of blocks; 300 of rank 64: 12.0 and 12.7).
 int lora_in_blocks(int tiles, int sms) { return std::max(tiles, std::min(std::min(kLoraParts * tiles, 2 * sms), kLoraSums)); }
 
-// Whether every block finds its tile itself. Beyond kLoraSmallN tokens its tiles of 16 cost more weights than the grouping saves,
-// unless the adapters are so many that tiles of 32 would be half empty (1000 tokens, 64 adapters of rank 16, 2048 x 2048: 12.0 us and
-// 15.2 grouped; 1000 tokens with long runs of 8 adapters of rank 32, 2048 x 4096: 14.7 and 13.6).
+// Whether every block finds its tile itself. Beyond kLoraSmallN tokens its tiles of 16 can cost more weights than the grouping saves,
+// unless the adapters are so many that tiles of 32 would be half empty (1000 tokens, 64 adapters of rank 16, 2048 x 2048: 10.3 us and
+// 14.0 grouped; 1000 of 64 adapters of rank 64, 2048 x 4096: 21.2 and 28.5; 846 of 8 adapters of rank 128, 2048 x 2048: 21.5 and
+// 19.7).
 bool lora_finds(int N, int L) { return N <= kLoraSmallN || (N <= kLoraFindN && L >= N / 32); }
 
 // What the workspace holds of a pass: the tiles and their tokens where they are grouped, and t; else the blocks' sums.
@@ -1004,7 +1007,7 @@ twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
     static_assert(S::bytes(kLoraCluster) <= 224 * 1024, "a block's shared memory");
     const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
     // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.5 us and 5.0 in two kernels; 18 of rank 64, 2048
-    // x 4096: 5.5 and 6.6; 30 of them: 10.0 and 7.2)
+    // x 4096: 5.4 and 6.6; 30 of them: 9.9 and 7.0)
     if (tiles * kLoraCluster > (RG == 1 ? 2 : 1) * sms) return run_products<1, RG, RT, kLoraFindPer>(g, sums, sms, s);
     auto kern = lora_kernel<1, RG, RT>;
     static std::atomic<uint64_t> allowed{0};

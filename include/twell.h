@@ -555,7 +555,8 @@ typedef struct {
 /* out[i] = y[i] + scale[c] b[c] (a[c] x[i]) with c = ids[i], for N <= 2^20 tokens in any order; out[i] = y[i] where c = -1.
  * x [N, k], y and out [N, n] bf16, rows ldx, ldy and ldo elements apart (multiples of 8: slices of a fused projection are
  * fine). out may be y with the same stride (rows without an adapter are then not touched); else they do not overlap, and out
- * never overlaps x. Sums are fp32, in an order that the sizes and the device's number of SMs fix, and out is rounded once;
+ * never overlaps x. Sums are fp32, in an order that the sizes, how many tokens each adapter has and the device's number of SMs
+ * fix, and out is rounded once;
  * a[c] x[i] enters the second product with 16 bits or more. A row's result does not depend on the other tokens' rows or on
  * their order. An id outside [-1, n_adapters) or a rank outside [0, rank] is reported as
  * TWELL_ERR_DEVICE_CHECK and counts as -1. Blocks that share a token's sums wait for one another; should that wait run out,
