@@ -152,6 +152,31 @@ def test_a_row_does_not_depend_on_the_others(cuda_dev, N):
         assert int(ids[1]) < 0 or torch.isnan(spoilt[1]).all()
 
 
+@pytest.mark.parametrize("N,R", [(3, 16), (16, 64), (300, 64), (1000, 16), (1000, 128), (1500, 32)])
+def test_replays_take_the_ids_of_their_time(cuda_dev, N, R):
+    """A captured call, replayed with other ids: few adapters and many, long runs, none at all. The blocks share what tiles there are."""
+    k, n, L = 648, 1032, 40
+    ad = _adapters(cuda_dev, L, R, k, n, seed=R, ragged=True)
+    x, y = _rand(cuda_dev, N, k, seed=1), _rand(cuda_dev, N, n, seed=2)
+    out, ids = torch.empty_like(y), _ids(cuda_dev, N, L, 3, "any")
+    binding.twell_lora_add(y, x, ad, ids, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.twell_lora_add(y, x, ad, ids, out=out)
+    kinds = [_ids(cuda_dev, N, L, 4, "runs"), torch.full_like(ids, -1), _ids(cuda_dev, N, L, 5, "one"), _ids(cuda_dev, N, L, 6, "any")]
+    got = []
+    for other in kinds * 3:  # without a wait between them
+        ids.copy_(other)
+        graph.replay()
+        got.append(out.clone())
+    for other, o in zip(kinds * 3, got):
+        assert torch.equal(o, binding.twell_lora_add(y, x, ad, other, out=torch.empty_like(y)))
+    _check(got[0], y, x, ad, kinds[0])
+    _check(got[3], y, x, ad, kinds[3])
+    assert torch.equal(got[1], y)
+
+
 @pytest.mark.parametrize("N", [5, 80, 900])
 def test_slices_of_wider_rows(cuda_dev, N):
     """Rows of a fused projection: the columns beside the slice stay, and rows without an adapter are not written."""
