@@ -3,6 +3,7 @@
 // status reporting.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -75,12 +76,13 @@ twell_status make_tmap_bf16(CUtensorMap* out, const void* base, uint64_t inner, 
     return r == CUDA_SUCCESS ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
+// TWELL_WAIT_LIMIT_MS may have a fraction.
 uint64_t wait_limit_ns()
 {
     static uint64_t lim = [] {
         const char* s = std::getenv("TWELL_WAIT_LIMIT_MS");
-        long v = s ? std::strtol(s, nullptr, 10) : 0;
-        return static_cast<uint64_t>(v > 0 ? v : 2000) * 1000000ull;
+        const double v = s ? std::strtod(s, nullptr) : 0.0;
+        return static_cast<uint64_t>(v > 0.0 ? std::min(std::max(v * 1e6, 1.0), 1e15) : 2e9);
     }();
     return lim;
 }

@@ -165,6 +165,33 @@ __device__ __forceinline__ void st_counted16(uint32_t at, const float4& v, uint3
                  : "memory");
 }
 
+// The wait for the other blocks' stores. What wait_bounded tests with suspends a thread for as long as the hardware sees fit, so
+// that a limit of under a millisecond (the environment's) is kept by polling.
+constexpr uint64_t kLoraPollNs = 1000000;
+__device__ __forceinline__ bool lora_wait(uint64_t* bar, int32_t* status, uint64_t limit_ns)
+{
+    if (limit_ns >= kLoraPollNs) return wait_bounded<true>(bar, 0, nullptr, status, limit_ns);
+    for (const uint64_t t0 = globaltimer_ns();;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar))
+            : "memory");
+        if (ok) return true;
+        if (globaltimer_ns() - t0 > limit_ns) break;
+    }
+    report(status, TWELL_ERR_TIMEOUT);
+    return false;
+}
+// A block whose wait for the other blocks' stores ran out stays until they have come, since they go on to write to its shared memory: from
+// the cluster barrier on, which all have passed, they send without a wait of their own. Whoever of its threads waits here keeps
+// the memory. A limit of its own, whatever the wait's is.
+constexpr uint64_t kLoraDrainNs = 2000000000ull;
+__device__ __forceinline__ void lora_drain(uint64_t* bar) { wait_bounded<true>(bar, 0, nullptr, nullptr, kLoraDrainNs); }
+
 // A token's adapter, L for none (-1, or one that does not exist, which is recorded).
 __device__ __forceinline__ int lora_id(const LoraArgs& g, int id)
 {
@@ -646,9 +673,10 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
 #pragma unroll
         for (int d = 0; d < blocks; ++d) st_counted16(mapa_shared(to, d), v, mapa_shared(smem_u32(&bar), d));
     }
-    const bool all = wait_bounded<true>(&bar, 0, nullptr, g.status, g.limit_ns);
-    if (__syncthreads_or(!all)) {  // recorded; what is under way to this block's own memory ends first
+    const bool all = lora_wait(&bar, g.status, g.limit_ns);
+    if (__syncthreads_or(!all)) {  // recorded
         copies_wait<0>();
+        lora_drain(&bar);
         return;
     }
     // t, whole, under its scale, as the second product's fragments: [row tile][16 ranks][hi, lo][lane]
@@ -730,7 +758,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
     for (int i = tid; i < quads; i += kLoraThreads)
         st_counted16(mapa_shared(smem_u32(recv + part * share + i / blocks), i % blocks), lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads),
                      mapa_shared(smem_u32(&bar), i % blocks));
-    if (!wait_bounded<true>(&bar, 0, nullptr, g.status, g.limit_ns)) return;  // recorded
+    if (!lora_wait(&bar, g.status, g.limit_ns)) {  // recorded
+        lora_drain(&bar);
+        return;
+    }
     for (int i = part + tid * blocks; i < quads; i += kLoraThreads * blocks) {
         float4 v = recv[i / blocks];
         for (int d = 1; d < blocks; ++d) {
