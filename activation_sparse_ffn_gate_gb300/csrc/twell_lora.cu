@@ -63,6 +63,7 @@ struct LoraArgs {
     const int32_t* n_tiles;
     const int4* tiles;
     const int32_t* order;
+    int32_t* lost;  // of each tile: a part of its t was given up, and its rows stay as they are
 };
 
 // Shared memory of a block: of each warp a ring of copies (in which it also leaves its sums), the fragments of t, the blocks'
@@ -759,6 +760,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
         st_counted16(mapa_shared(smem_u32(recv + part * share + i / blocks), i % blocks), lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads),
                      mapa_shared(smem_u32(&bar), i % blocks));
     if (!lora_wait(&bar, g.status, g.limit_ns)) {  // recorded
+        g.lost[index] = 1;
         lora_drain(&bar);
         return;
     }
@@ -812,6 +814,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
     const float scale = FIND != 0 && rank > 0 ? __ldg(g.scale + tile.id) : 0.0f;
     pdl_wait();
     pdl_next();
+    const int lost = FIND == 0 ? __ldcg(g.lost + index) : 0;  // under way with t
     // t as the product's fragments
     uint4* frags = reinterpret_cast<uint4*>(lora_smem + kLoraWarps * S::kRing);
     constexpr int kQuads = S::kRanks / 4;
@@ -843,14 +846,21 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
             frags[((m * S::kFrags + f) * 2 + 0) * 32 + l] = make_uint4(t[0].x, t[1].x, t[0].y, t[1].y);
             frags[((m * S::kFrags + f) * 2 + 1) * 32 + l] = make_uint4(t[0].z, t[1].z, t[0].w, t[1].w);
         }
-    __syncthreads();
+    if constexpr (FIND == 0) {
+        if (__syncthreads_or(lost)) {
+            copies_wait<0>();
+            return;
+        }
+    } else {
+        __syncthreads();
+    }
     out.template run<S::kStages>(frags);
 }
 
 // The tiles of a larger batch: tokens counted by adapter, a tile for each 16 kLoraMT of an adapter's, and
 // their places in it in `order`. One block: the counts are in its shared memory, and a pass's ids are 64 KB, all requested before the
 // first is counted. Which token of an adapter comes first is left to chance; a token's result does not depend on it.
-__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int32_t* n_tiles, int4* tiles, int32_t* order)
+__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int32_t* n_tiles, int4* tiles, int32_t* order, int32_t* lost)
 {
     constexpr int kTok = 16 * kLoraMT;                   // tokens a tile
     constexpr int kPer = kLoraPass / kLoraGroupThreads;  // tokens a thread
@@ -930,6 +940,7 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
         }
         const int from = count[l] + (j - first_tile[l]) * kTok;
         tiles[j] = make_int4(l, from, min(kTok, (l < g.L ? count[l + 1] : g.N) - from), lora_rank(g, l));
+        lost[j] = 0;
     }
 }
 
@@ -976,16 +987,17 @@ int lora_in_blocks(int tiles, int sms) { return std::max(tiles, std::min(std::mi
 // 19.7).
 bool lora_finds(int N, int L) { return N <= kLoraSmallN || (N <= kLoraFindN && L >= N / 32); }
 
-// What the workspace holds of a pass: the tiles and their tokens where they are grouped, and t; else the blocks' sums.
+// What the workspace holds of a pass: the tiles, their tokens, which of them are lost, and t where tokens are grouped; else the blocks' sums.
 struct LoraWs {
-    size_t tiles, order, t, total;
+    size_t tiles, order, lost, t, total;
     LoraWs(int N, int R)
     {
         const int n = std::min(N, kLoraPass), tok = 16 * kLoraMT;
         const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok)), row = lora_ranks(R) * sizeof(float);
         tiles = 16;
         order = tiles + 16 * most;
-        t = order + sizeof(int32_t) * tok * most;
+        lost = order + sizeof(int32_t) * tok * most;
+        t = (lost + sizeof(int32_t) * most + 15) / 16 * 16;
         total = std::max(N > kLoraSmallN ? t + n * row : 0, N <= kLoraFindN ? 16 * kLoraSums * row : 0);
     }
 };
@@ -1052,12 +1064,14 @@ twell_status run_pass(LoraArgs g, uint8_t* ws, const LoraWs& at, int sms, cudaSt
     int32_t* n_tiles = reinterpret_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
     int32_t* order = reinterpret_cast<int32_t*>(ws + at.order);
+    int32_t* lost = reinterpret_cast<int32_t*>(ws + at.lost);
     const twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g,
-                                                   n_tiles, tiles, order);
+                                                   n_tiles, tiles, order, lost);
     if (st != TWELL_OK) return st;
     g.n_tiles = n_tiles;
     g.tiles = tiles;
     g.order = order;
+    g.lost = lost;
     return run_products<kLoraMT, RG, RT, 0>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
 }
 
@@ -1101,7 +1115,7 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     twell::LoraArgs g = {static_cast<const bf*>(ad->a), static_cast<const bf*>(ad->b), static_cast<const bf*>(x),
                          static_cast<const bf*>(y), static_cast<bf*>(out), ad->scale, ad->ranks, ids, dev_status,
-                         ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, wait_limit_ns(), nullptr, nullptr, nullptr};
+                         ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, wait_limit_ns(), nullptr, nullptr, nullptr, nullptr};
     uint8_t* w = static_cast<uint8_t*>(ws);
     if (twell::lora_finds(N, ad->n_adapters))
         return ad->rank <= 16   ? twell::run_small<1, 2>(g, w, dev.sm_count, s)

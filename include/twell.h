@@ -560,7 +560,7 @@ typedef struct {
  * a[c] x[i] enters the second product with 16 bits or more. A row's result does not depend on the other tokens' rows or on
  * their order. An id outside [-1, n_adapters) or a rank outside [0, rank] is reported as
  * TWELL_ERR_DEVICE_CHECK and counts as -1. Blocks that share a token's sums wait for one another; should that wait run out,
- * TWELL_ERR_TIMEOUT is reported and those rows are not written. ws: twell_workspace_bytes(TWELL_OP_LORA_ADD, N, rank, 1, 0, 0, 0) bytes; two calls
+ * TWELL_ERR_TIMEOUT is reported, and of those rows some columns, or all, stay as they were. ws: twell_workspace_bytes(TWELL_OP_LORA_ADD, N, rank, 1, 0, 0, 0) bytes; two calls
  * in flight at the same time must not share it. */
 TWELL_API twell_status twell_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const twell_adapters* ad,
                             const int32_t* ids, int32_t N, void* out, int64_t ldo, void* ws, size_t ws_bytes,

@@ -1,6 +1,6 @@
 """Waits of the adapters' kernels that run out, without a fault or a hang: in a process whose limit is a nanosecond, a block gives up
-on sums that the others of its cluster are about to send. It stays until they have come, records TWELL_ERR_TIMEOUT and writes none
-of its columns.
+on sums that the others of its cluster are about to send. It stays until they have come, records TWELL_ERR_TIMEOUT, and what
+would need those sums is not written: its own columns, or the rows whose t it had to put together.
 
 Small integers: every sum is exact, so that an output is the formula's or untouched, to the bit."""
 import os
@@ -34,24 +34,28 @@ def _case(N, L, R, k, n):
 
 def _child():
     from activation_sparse_ffn_gate_gb300 import binding
-    gave_up = 0
+    gave_up = []
     # one kernel, a cluster of eight blocks a tile; then tokens grouped first, eight blocks and fewer a tile in the first product
     for N, L, R, k, n in ((1, 2, 16, 1024, 1032), (3, 2, 64, 512, 520), (40, 2, 128, 520, 264), (1100, 2, 16, 1024, 264), (2100, 3, 40, 264, 136)):
         x, a, b, y, ids, want = _case(N, L, R, k, n)
         ad = binding.Adapters(a, b, torch.ones(L, device="cuda"))
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(binding.twell_workspace_bytes(binding.OP_LORA_ADD, N, R, 1), dtype=torch.uint8, device="cuda")
+        gave_up.append(0)
         for i in range(60):
             out = y.clone()
-            binding.twell_lora_add(out, x, ad, ids, status=status)
+            ws.fill_(255)  # what no call has written is not a number
+            binding.twell_lora_add(out, x, ad, ids, ws=ws, status=status)
             code = binding.twell_read_status(status)
             assert code in (0, TIMEOUT), code
-            gave_up += code == TIMEOUT
-            if N <= 512:
-                assert ((out == y) | (out == want)).all(), (N, i)
+            gave_up[-1] += code == TIMEOUT
+            assert ((out == y) | (out == want)).all(), (N, i)
+            if N > 512:  # a tile's rows together
+                assert ((out == y).all(1) | (out == want).all(1)).all(), (N, i)
             if code == 0:
                 assert torch.equal(out, want), (N, i)
     torch.cuda.synchronize()
-    print("gave up", gave_up)
+    print("gave up", *gave_up)
 
 
 def test_waits_that_run_out(cuda_dev):
@@ -60,7 +64,9 @@ def test_waits_that_run_out(cuda_dev):
     run = subprocess.run([sys.executable, os.path.abspath(__file__)], env={**os.environ, "TWELL_WAIT_LIMIT_MS": "0.000001"}, cwd=ROOT,
                          capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stdout + run.stderr
-    assert int(run.stdout.split("gave up")[1]) > 0
+    counts = [int(v) for v in run.stdout.split("gave up")[1].split()]
+    print(counts)
+    assert sum(counts[:3]) > 0 and sum(counts[3:]) > 0  # in one kernel, and after the tokens are grouped
 
 
 if __name__ == "__main__":
