@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a)
         int head = a.state[0], free = a.state[1];
         if (!WARP && tid == 0) s_sums.taken = 0;
         bool bad = head < 0 || free < 0 || free > a.n_pages || (head >= a.n_pages && (head != 0 || free != 0));
-        if (bad) head = free = 0;  // nothing can be taken from or given to a ring that is not one
+        if (bad) head = free = 0;  // an empty ring: nothing is taken from it, and the pages of ended requests go to its cells from 0 on
         // a length rounded up to a page stays within 32 bits
         const long long cap = min(static_cast<long long>(a.max_pages) << a.page_shift, 0x7fffffffll - 1023);
         auto scan = [&](int (&v)[2], int (&total)[2]) {

@@ -529,8 +529,9 @@ typedef struct {
  *  - the pages of the requests up to it that need any are more than the free ones: TWELL_ERR_POOL_EMPTY in *dev_status;
  *  - its length is negative, does not fit its row or exceeds 2^31 - 1024, its new tokens do not fit n_tokens, or new_lens[b] < -1:
  *    TWELL_ERR_DEVICE_CHECK.
- * More pages given back than are missing (none are taken back then), a state outside the ring (nothing is taken or given
- * then; the ring counts as empty from there on), and pages outside [0, n_pages) in a row or the ring (slot -1) are
+ * More pages given back than are missing (none are taken back then), a state outside the ring (the ring then counts as empty: no
+ * page is taken, and those of requests that have ended are put into its cells from 0 on, which are all that it has after
+ * the step), and pages outside [0, n_pages) in a row or the ring (slot -1) are
  * TWELL_ERR_DEVICE_CHECK too. Calls on one pool must follow one another. All integers: the same from call to call. */
 TWELL_API twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page_table, int32_t max_pages,
                            const int32_t* seq_lens, const int32_t* new_lens, const int32_t* labels, int32_t B,
