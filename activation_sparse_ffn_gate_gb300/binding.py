@@ -1300,6 +1300,22 @@ class StepPlan:
     owner: torch.Tensor  # [n_tokens] the request's label, or its number
     starts: torch.Tensor  # [B + 1] where each request's tokens begin
 
+    def per_token(self, page_table: torch.Tensor, seq_lens: torch.Tensor, stream=None):
+        """(page_table [n_tokens, max_pages], seq_lens [n_tokens]): for each token its request's row of page_table [B, max_pages] and
+        how many of its tokens there are up to this one, of the lengths [B] after the step; 0 where a token has no slot. What
+        twell_paged_attn_decode and DecoderLayer.decode take, whose row i is token i, of a step in which some requests have
+        no new token, or several."""
+        B, n = page_table.shape[0], self.slots.numel()
+        if self.starts.numel() != B + 1 or seq_lens.numel() != B:
+            raise ValueError(f"the plan is of {self.starts.numel() - 1} requests, not {B} and {seq_lens.numel()}")
+        with under_stream(stream):
+            if B == 0:
+                return page_table.new_zeros((n, page_table.shape[1])), seq_lens.new_zeros(n)
+            token = torch.arange(n, dtype=torch.int32, device=self.starts.device)
+            owner = (torch.searchsorted(self.starts, token, right=True) - 1).clamp_(max=B - 1)
+            behind = self.starts[owner + 1] - 1 - token  # tokens of its request behind it
+            return page_table[owner], torch.where(self.slots >= 0, seq_lens[owner] - behind, 0)
+
 
 def twell_kv_plan(pool: PagePool, page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, n_tokens: int,
                   labels: Optional[torch.Tensor] = None, plan: Optional[StepPlan] = None,

@@ -4,8 +4,9 @@ DECODE_MAX_N sequences, and the training step of the FFN's half of the layer.
 The residual stream travels as (delta, h): what the last sublayer added and the stream before it. The
 addition itself is the first half of twell_add_rmsnorm_fwd, so a sublayer reads and writes the stream once.
 Positions turn the queries and keys of a step before the keys are stored: by `rotary`, from the positions that the step is
-given (twell_kv_plan makes them, with the slots), or by `rotate`, the caller's own, which is called with views of the fused
-projection's output, to be changed in place. Adapters of the projections are added for the tokens that have one.
+given (twell_kv_plan makes them, with the slots; StepPlan.per_token the tokens' rows of the page table), or by `rotate`, the
+caller's own, which is called with views of the fused projection's output, to be changed in place. Adapters of the projections
+are added for the tokens that have one.
 With a `stream`, a step runs under it: its kernels, what `rotate` queues, and the memory of what it returns.
 """
 from __future__ import annotations
@@ -46,7 +47,9 @@ class DecoderLayer:
         """One new token per sequence: delta [N, d] bf16 and h [N, d] (bf16 or fp32; None for the first layer, whose
         stream is delta) in, the same pair for the next layer out. The tokens' keys and values go to
         `slots`; seq_lens counts them. positions int32 [N] for `rotary`; adapter_ids int32 [N] (-1: none; without them no
-        adapter is added): what twell_kv_plan makes of the requests, where each has one new token."""
+        adapter is added): the slots, positions and owners of twell_kv_plan. Row i of page_table and seq_lens is token i's: the
+        requests' own where each has one new token; of a step in which some have none, or several, what StepPlan.per_token
+        makes of them, once for all layers (a token then sees its request's up to itself, and one without a slot nothing)."""
         N = delta.shape[0]
         hq, hk = self.n_heads, self.n_kv_heads
         if self.rotary is not None and positions is None:

@@ -68,7 +68,7 @@ def main():
     x = torch.randn((a.seqs, layer.attn_norm.numel()), device=dev, dtype=torch.bfloat16)
     one = torch.ones_like(lens)
 
-    def step():  # one more token a sequence
+    def step():  # one more token a sequence, so that token i is sequence i's (StepPlan.per_token is for other steps)
         p = binding.twell_kv_plan(pool, table, lens, one, a.seqs, labels=adapter)
         return layer.decode(x, None, cache, p.slots, table, lens, positions=p.positions,
                             adapter_ids=p.owner if a.adapters else None)
