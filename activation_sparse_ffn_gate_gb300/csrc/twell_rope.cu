@@ -281,7 +281,7 @@ twell_status rope(const twell_rope_heads* q, const twell_rope_heads* k, const in
     twell::RopeArgs a = {};
     if (positions == nullptr || turns == nullptr || reinterpret_cast<uintptr_t>(positions) % 4 != 0 ||
         reinterpret_cast<uintptr_t>(turns) % 8 != 0 || pos_batch < 0 || !rope_side(q, B, S, hd, elem, &a.q) ||
-        (k != nullptr && (!rope_side(k, B, S, hd, elem, &a.k) || k->out == q->out)))
+        (k != nullptr && (!rope_side(k, B, S, hd, elem, &a.k) || k->out == q->out || k->out == q->in || q->out == k->in)))
         return TWELL_ERR_INVALID;
     const long long tokens = static_cast<long long>(B) * S, heads = static_cast<long long>(q->n_heads) + (k ? k->n_heads : 0);
     if (tokens * hd > INT32_MAX || heads > 65535) return TWELL_ERR_UNSUPPORTED;

@@ -482,7 +482,8 @@ TWELL_API twell_status twell_w4_matvec(const void* x, const void* words, const v
 /* Rotary positions. A side (queries or keys) of B sequences of S tokens: element j of head h of token t of sequence b is
  * at in + b * in_batch + t * in_token + h * in_head + j and goes to out + b * out_batch + t * out_token + h * out_head + j.
  * in may be out, with the same strides (the call then works in place); else the two do not overlap. The heads of an output
- * lie apart, and so do the outputs of queries and keys. Strides in elements; addresses need only the element type's alignment (16-byte vectors are used where the
+ * lie apart, and so do the outputs of queries and keys; neither output lies over the other side's input (at its address it is
+ * refused). Strides in elements; addresses need only the element type's alignment (16-byte vectors are used where the
  * addresses, strides and rot_dim allow them, 8-, 4- and 2-byte ones else). */
 typedef struct {
     const void* in;
