@@ -141,7 +141,9 @@ __device__ __forceinline__ uint2 lds8(uint32_t at)
 }
 
 // The two halves of pdl_begin. A kernel that lets the next one start only after its own wait lets that one read, before it waits
-// in turn, whatever was there before this kernel.
+// in turn, whatever was there before this kernel. lora_in_kernel and lora_out_kernel are the one such pair, and the exception to
+// launch_dep's rule that a kernel begins with pdl_begin: lora_out_kernel reads ids, tiles, y and B before its wait, which is right
+// only as long as lora_in_kernel waits first and lets it start then.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -528,7 +530,6 @@ struct LoraOut {
         stages = left > 0 ? (left - 1) / (2 * kLoraWarps) * 2 + min((left - 1) % (2 * kLoraWarps) + 1, 2) : 0;
     }
     __device__ __forceinline__ int column(int i) const { return 32 * (first + (i >> 1) * (2 * kLoraWarps) + (i & 1)); }
-    template <int STAGES>
     __device__ __forceinline__ void request(int i, int slot) const
     {
         if (i < stages) {
@@ -609,7 +610,7 @@ struct LoraOut {
                     }
                     if (col < g.n && y_bytes[m][s] > 0) *reinterpret_cast<uint4*>(out[m][s] + 2 * col) = y;
                 }
-            request<STAGES>(i + STAGES, slot);
+            request(i + STAGES, slot);
             slot = slot + 1 == STAGES ? 0 : slot + 1;
         }
         copies_wait<0>();
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
     const float scale = __ldg(g.scale + id);
     lora_shrink<S, MT, RG, RT>(g, id, rank, part, shift, token, ring_at, [&] {
 #pragma unroll
-        for (int i = 0; i < S::kOutStages; ++i) out.template request<S::kOutStages>(i, i);
+        for (int i = 0; i < S::kOutStages; ++i) out.request(i, i);
     });
     __syncthreads();
     cluster_wait();
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
 {
     using S = LoraShape<MT, RG, RT, false>;
     extern __shared__ __align__(128) uint8_t lora_smem[];  // a warp's 512 bytes a vector begin on a 128-byte line
-    pdl_wait();
+    pdl_wait();  // in this order: lora_out_kernel reads what the kernels before this one wrote without a wait for them
     pdl_next();
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
     int shift, blocks, index, part;  // of a cluster: the rank
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
     const int nt0 = static_cast<int>(nt_all * part / parts), nt1 = static_cast<int>(nt_all * (part + 1) / parts);
     const LoraOut<MT, RG, RT> out(g, tile.id, rank, nt0, nt1, token, lora_smem + warp * S::kRing);
 #pragma unroll
-    for (int i = 0; i < S::kStages; ++i) out.template request<S::kStages>(i, i);
+    for (int i = 0; i < S::kStages; ++i) out.request(i, i);
     const float scale = FIND != 0 && rank > 0 ? __ldg(g.scale + tile.id) : 0.0f;
     pdl_wait();
     pdl_next();

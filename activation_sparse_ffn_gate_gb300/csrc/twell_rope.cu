@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
 }
 
 // Elements of a vector that every address of the call allows: a power of two up to 16 bytes.
-int vector_of(const RopeArgs& a, bool has_k, bool neighbours, int elem, bool copies)
+int vector_of(const RopeArgs& a, bool has_k, int elem, bool copies)
 {
     int v = 16 / elem;
     auto fits = [&](int64_t n) { return n % v == 0; };
@@ -209,7 +209,7 @@ int vector_of(const RopeArgs& a, bool has_k, bool neighbours, int elem, bool cop
                (a.tokens == a.S || (fits(s.in_batch) && fits(s.out_batch))) &&
                (a.S == 1 || (fits(s.in_token) && fits(s.out_token))) && (heads == 1 || (fits(s.in_head) && fits(s.out_head)));
     };
-    (void)neighbours;  // rot / 2 pairs in vectors of V: the same condition for both layouts
+    // rot / 2 pairs in vectors of V: the same condition for both layouts
     while (v > 1 && !(fits(a.rot / 2) && (!copies || fits(a.hd - a.rot)) && side(a.q, a.q_heads) &&
                       (!has_k || side(a.k, a.heads - a.q_heads))))
         v /= 2;
@@ -298,7 +298,7 @@ twell_status rope(const twell_rope_heads* q, const twell_rope_heads* k, const in
     a.sin_factor = backward ? -factor : factor;
     // in place the rest of a head stays where it is
     const bool copies = rot < hd && (q->in != q->out || (k != nullptr && k->in != k->out));
-    const int v = twell::vector_of(a, k != nullptr, neighbours != 0, elem, copies);
+    const int v = twell::vector_of(a, k != nullptr, elem, copies);
     a.pair_chunks = rot / 2 / v;
     a.chunks = a.pair_chunks + (copies ? (hd - rot + 2 * v - 1) / (2 * v) : 0);
     DevInfo dev;
