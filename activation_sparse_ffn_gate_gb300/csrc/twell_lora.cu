@@ -63,7 +63,6 @@ struct LoraArgs {
     const int32_t* n_tiles;
     const int4* tiles;
     const int32_t* order;
-    int32_t* lost;  // of each tile: a part of its t was given up, and its rows stay as they are
 };
 
 // Shared memory of a block: of each warp a ring of copies (in which it also leaves its sums), the fragments of t, the blocks'
@@ -168,12 +167,13 @@ __device__ __forceinline__ void st_counted16(uint32_t at, const float4& v, uint3
                  : "memory");
 }
 
-// The wait for the other blocks' stores. What wait_bounded tests with suspends a thread for as long as the hardware sees fit, so
-// that a limit of under a millisecond (the environment's) is kept by polling.
-constexpr uint64_t kLoraPollNs = 1000000;
+// The wait for the other blocks' stores. Whoever gives up records it and stays until they have come all the same (or for kLoraStayNs
+// more), since they go on to write to this block's shared memory: from the cluster barrier on, which all have passed, they send
+// without a wait of their own. Polls: try_wait may suspend a thread past any limit, and the sums are a microsecond away.
+constexpr uint64_t kLoraStayNs = 2000000000ull;
 __device__ __forceinline__ bool lora_wait(uint64_t* bar, int32_t* status, uint64_t limit_ns)
 {
-    if (limit_ns >= kLoraPollNs) return wait_bounded<true>(bar, 0, nullptr, status, limit_ns);
+    bool in_time = true;
     for (const uint64_t t0 = globaltimer_ns();;) {
         uint32_t ok;
         asm volatile(
@@ -183,17 +183,14 @@ __device__ __forceinline__ bool lora_wait(uint64_t* bar, int32_t* status, uint64
             : "=r"(ok)
             : "r"(smem_u32(bar))
             : "memory");
-        if (ok) return true;
-        if (globaltimer_ns() - t0 > limit_ns) break;
+        if (ok) return in_time;
+        const uint64_t spent = globaltimer_ns() - t0;
+        if (spent <= limit_ns) continue;
+        if (in_time) report(status, TWELL_ERR_TIMEOUT);
+        in_time = false;
+        if (spent - limit_ns > kLoraStayNs) return false;
     }
-    report(status, TWELL_ERR_TIMEOUT);
-    return false;
 }
-// A block whose wait for the other blocks' stores ran out stays until they have come, since they go on to write to its shared memory: from
-// the cluster barrier on, which all have passed, they send without a wait of their own. Whoever of its threads waits here keeps
-// the memory. A limit of its own, whatever the wait's is.
-constexpr uint64_t kLoraDrainNs = 2000000000ull;
-__device__ __forceinline__ void lora_drain(uint64_t* bar) { wait_bounded<true>(bar, 0, nullptr, nullptr, kLoraDrainNs); }
 
 // A token's adapter, L for none (-1, or one that does not exist, which is recorded).
 __device__ __forceinline__ int lora_id(const LoraArgs& g, int id)
@@ -210,6 +207,9 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xffff0000u);
     lo = bf16x2_rn(fabsf(ha) <= 3.4e38f ? a - ha : 0.0f, fabsf(hb) <= 3.4e38f ? b - hb : 0.0f);
 }
+
+// Lo parts that split2 never gives (two NaNs): t was given up here.
+constexpr uint32_t kLoraLost = 0xffffffffu;
 
 // How many rows of adapter `id` count (0 for none, and where that number cannot be, which is recorded).
 __device__ __forceinline__ int lora_rank(const LoraArgs& g, int id)
@@ -678,7 +678,6 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs g)
     const bool all = lora_wait(&bar, g.status, g.limit_ns);
     if (__syncthreads_or(!all)) {  // recorded
         copies_wait<0>();
-        lora_drain(&bar);
         return;
     }
     // t, whole, under its scale, as the second product's fragments: [row tile][16 ranks][hi, lo][lane]
@@ -760,12 +759,12 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_in_kernel(const LoraArgs
     for (int i = tid; i < quads; i += kLoraThreads)
         st_counted16(mapa_shared(smem_u32(recv + part * share + i / blocks), i % blocks), lora_sum<S, RG>(lora_smem, i / kQuads, i % kQuads),
                      mapa_shared(smem_u32(&bar), i % blocks));
-    if (!lora_wait(&bar, g.status, g.limit_ns)) {  // recorded
-        g.lost[index] = 1;
-        lora_drain(&bar);
-        return;
-    }
+    const bool in_time = lora_wait(&bar, g.status, g.limit_ns);
     for (int i = part + tid * blocks; i < quads; i += kLoraThreads * blocks) {
+        if (!in_time) {  // recorded; the second product leaves the tile's rows as they are
+            t_out[static_cast<size_t>(tile.first) * kQuads + i].z = kLoraLost;
+            continue;
+        }
         float4 v = recv[i / blocks];
         for (int d = 1; d < blocks; ++d) {
             const float4 u = recv[d * share + i / blocks];
@@ -815,7 +814,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
     const float scale = FIND != 0 && rank > 0 ? __ldg(g.scale + tile.id) : 0.0f;
     pdl_wait();
     pdl_next();
-    const int lost = FIND == 0 ? __ldcg(g.lost + index) : 0;  // under way with t
+    bool lost = false;
     // t as the product's fragments
     uint4* frags = reinterpret_cast<uint4*>(lora_smem + kLoraWarps * S::kRing);
     constexpr int kQuads = S::kRanks / 4;
@@ -842,6 +841,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
                     t[s] = lora_parts(u[0], 4 * quad, rank, scale);
                 } else {
                     t[s] = __ldcg(t_in + static_cast<size_t>(tile.first + row + 8 * s) * kQuads + quad);
+                    lost |= t[s].z == kLoraLost;
                 }
             }
             frags[((m * S::kFrags + f) * 2 + 0) * 32 + l] = make_uint4(t[0].x, t[1].x, t[0].y, t[1].y);
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_out_kernel(const LoraArg
 // The tiles of a larger batch: tokens counted by adapter, a tile for each 16 kLoraMT of an adapter's, and
 // their places in it in `order`. One block: the counts are in its shared memory, and a pass's ids are 64 KB, all requested before the
 // first is counted. Which token of an adapter comes first is left to chance; a token's result does not depend on it.
-__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int32_t* n_tiles, int4* tiles, int32_t* order, int32_t* lost)
+__global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const LoraArgs g, int32_t* n_tiles, int4* tiles, int32_t* order)
 {
     constexpr int kTok = 16 * kLoraMT;                   // tokens a tile
     constexpr int kPer = kLoraPass / kLoraGroupThreads;  // tokens a thread
@@ -941,7 +941,6 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
         }
         const int from = count[l] + (j - first_tile[l]) * kTok;
         tiles[j] = make_int4(l, from, min(kTok, (l < g.L ? count[l + 1] : g.N) - from), lora_rank(g, l));
-        lost[j] = 0;
     }
 }
 
@@ -988,17 +987,16 @@ int lora_in_blocks(int tiles, int sms) { return std::max(tiles, std::min(std::mi
 // 19.7).
 bool lora_finds(int N, int L) { return N <= kLoraSmallN || (N <= kLoraFindN && L >= N / 32); }
 
-// What the workspace holds of a pass: the tiles, their tokens, which of them are lost, and t where tokens are grouped; else the blocks' sums.
+// What the workspace holds of a pass: the tiles and their tokens where they are grouped, and t; else the blocks' sums.
 struct LoraWs {
-    size_t tiles, order, lost, t, total;
+    size_t tiles, order, t, total;
     LoraWs(int N, int R)
     {
         const int n = std::min(N, kLoraPass), tok = 16 * kLoraMT;
         const size_t most = static_cast<size_t>(lora_tiles(n, kLoraMaxAdapters, tok)), row = lora_ranks(R) * sizeof(float);
         tiles = 16;
         order = tiles + 16 * most;
-        lost = order + sizeof(int32_t) * tok * most;
-        t = (lost + sizeof(int32_t) * most + 15) / 16 * 16;
+        t = order + sizeof(int32_t) * tok * most;
         total = std::max(N > kLoraSmallN ? t + n * row : 0, N <= kLoraFindN ? 16 * kLoraSums * row : 0);
     }
 };
@@ -1065,14 +1063,12 @@ twell_status run_pass(LoraArgs g, uint8_t* ws, const LoraWs& at, int sms, cudaSt
     int32_t* n_tiles = reinterpret_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(ws + at.tiles);
     int32_t* order = reinterpret_cast<int32_t*>(ws + at.order);
-    int32_t* lost = reinterpret_cast<int32_t*>(ws + at.lost);
     const twell_status st = twell_host::launch_dep(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 2 * sizeof(int) * (g.L + 1), s, g,
-                                                   n_tiles, tiles, order, lost);
+                                                   n_tiles, tiles, order);
     if (st != TWELL_OK) return st;
     g.n_tiles = n_tiles;
     g.tiles = tiles;
     g.order = order;
-    g.lost = lost;
     return run_products<kLoraMT, RG, RT, 0>(g, reinterpret_cast<uint4*>(ws + at.t), sms, s);
 }
 
@@ -1116,7 +1112,7 @@ extern "C" twell_status twell_lora_add(const void* y, int64_t ldy, const void* x
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     twell::LoraArgs g = {static_cast<const bf*>(ad->a), static_cast<const bf*>(ad->b), static_cast<const bf*>(x),
                          static_cast<const bf*>(y), static_cast<bf*>(out), ad->scale, ad->ranks, ids, dev_status,
-                         ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, wait_limit_ns(), nullptr, nullptr, nullptr, nullptr};
+                         ldx, ldy, ldo, ad->n_adapters, ad->rank, ad->k, ad->n, N, wait_limit_ns(), nullptr, nullptr, nullptr};
     uint8_t* w = static_cast<uint8_t*>(ws);
     if (twell::lora_finds(N, ad->n_adapters))
         return ad->rank <= 16   ? twell::run_small<1, 2>(g, w, dev.sm_count, s)
