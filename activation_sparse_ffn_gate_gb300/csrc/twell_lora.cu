@@ -10,11 +10,13 @@
 // What costs a small batch is its chain of loads, what costs a large one its bytes; hence three ways:
 // - Few tiles, each of which can have eight SMs: one kernel, a cluster of eight blocks a tile. Each has a part of k, the sums go
 //   to all of them through distributed shared memory, and each then has a part of n, whose first pieces are on their way
-//   meanwhile. One token, 2048 x 2048, rank 16: 3.4 us, of which the launch is 1.6; the rest is ids, x and A, the
+//   meanwhile. One token, 2048 x 2048, rank 16: 3.5 us, of which the launch is 1.6; the rest is ids, x and A, the
 //   exchange, y. One token of rank 64, 2048 x 4096: 5.0 us.
-// - Up to 512 tokens else (1024 where the adapters are many): two kernels, whose blocks need not start together as a cluster's do;
-//   the second one's copies run while the first is at work. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 10.2 us
-//   (16.2 in clusters; floor 3.0); 256 tokens with 64 adapters of rank 16, 2048 x 2048: 6.9 (9.5; floor 1.7).
+// - Up to 512 tokens else (1024 where the adapters are many): two kernels, whose blocks need not start together as a cluster's do.
+//   The second one's blocks request their first copies as soon as they find room: beside two of the first's on an SM up to rank
+//   16, where those end above it (at rank 32 the registers are short, at rank 64 the shared memory), and above rank 64 one takes
+//   an SM for itself. 64 tokens with 64 adapters of ranks up to 64, 2048 x 4096: 10.1 us (16.1 in clusters; floor
+//   3.0); 256 tokens with 64 adapters of rank 16, 2048 x 2048: 6.8 (9.6; floor 1.7).
 // - Larger ones: the same two after a kernel that groups the tokens by adapter. 16384 tokens, 2048 x 4096, rank 16: 65 us, of
 //   which grouping takes 6, the first product 15 (67 MB) and the second 44 (268 MB, 91% of the copy rate). Above rank 32 the
 //   weights that each tile brings from L2 count: rank 64, 2048 x 2048: 61 us for 182 MB. Both products in one kernel, by a
@@ -37,13 +39,13 @@ constexpr int kLoraClusterShift = 3, kLoraCluster = 1 << kLoraClusterShift;  // 
 // up to kLoraSmallN tokens, up to kLoraFindN where the adapters are many (lora_finds).
 constexpr int kLoraFindPer = 2, kLoraFindMore = 4;
 constexpr int kLoraSmallN = kLoraFindPer * kLoraThreads, kLoraFindN = kLoraFindMore * kLoraThreads;
-// A larger batch's tiles have 32 tokens. With 16 their weights are read twice as often (9000 tokens, 1024 x 3000, rank 128: 98 us
-// against 62; 16384 of rank 64, 2048 x 2048: 68 and 61; 3001 of rank 24: 25.0 and 23.3). With 64 they are read half as often, but
-// a block takes an SM for itself (before the last steps: the 16384 of rank 64 73.6 against 64.7, of rank 16, 2048 x 4096, 120
-// against 70).
+// A larger batch's tiles have 32 tokens. With 16 their weights are read twice as often (9000 tokens, 1024 x 3000, rank 128: 99 us
+// against 62; 16384 of rank 64, 2048 x 2048: 68 and 61; 3001 of rank 24: 25.2 and 23.3), which between 600 and 2400 tokens can be
+// the quicker all the same (1000 of 8 adapters of rank 32: 11.7 and 14.2). With 64 they would be read half as often, but two
+// blocks' rings no longer fit an SM.
 constexpr int kLoraMT = 2;
 // Most blocks of a tile that share its k where each leaves its own sums (325 tokens of few adapters of rank 64, 7312 x 704: 11.7 us,
-// 12.3 with four; 64 of rank 16, 2048 x 2048: 5.2 and 5.5), and of all tiles.
+// 12.5 with four; 256 of 64 adapters of rank 16, 2048 x 2048: 6.8 and 7.3), and of all tiles.
 constexpr int kLoraParts = 8;
 constexpr int kLoraSums = 1024;
 constexpr int kLoraGroupThreads = 1024;
@@ -944,8 +946,8 @@ __global__ void __launch_bounds__(kLoraGroupThreads) lora_group_kernel(const Lor
     }
 }
 
-// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 23.3 us with two, 24.4 with one,
-// 26.7 with four).
+// A tile's blocks in a cluster: as many as give each SM one (3001 tokens, 2560 x 2568: 23.3 us with two, 24.5 with one,
+// 26.9 with four).
 int lora_blocks(long long tiles, int sms)
 {
     int b = 1;
@@ -977,13 +979,13 @@ long long lora_tiles(int N, int L, int tok) { return std::min<long long>(N, N / 
 
 constexpr int lora_ranks(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
-// Blocks of the first product where each leaves its own sums: as far as two an SM go (when this was chosen, 256 tokens with 64 adapters
-// of rank 16, 2048 x 2048: 7.2 us, 8.2 with a second round of blocks; 300 of rank 64: 12.0 and 12.7).
+// Blocks of the first product where each leaves its own sums: as far as two an SM go (256 tokens with 64 adapters of rank 16, 2048 x
+// 2048: 6.8 us, 8.3 with a second round of blocks; 300 of rank 64: 11.7 and 14.8).
 int lora_in_blocks(int tiles, int sms) { return std::max(tiles, std::min(std::min(kLoraParts * tiles, 2 * sms), kLoraSums)); }
 
 // Whether every block finds its tile itself. Beyond kLoraSmallN tokens its tiles of 16 can cost more weights than the grouping saves,
-// unless the adapters are so many that tiles of 32 would be half empty (1000 tokens, 64 adapters of rank 16, 2048 x 2048: 10.3 us and
-// 14.0 grouped; 1000 of 64 adapters of rank 64, 2048 x 4096: 21.2 and 28.5; 846 of 8 adapters of rank 128, 2048 x 2048: 21.5 and
+// unless the adapters are so many that tiles of 32 would be half empty (1000 tokens, 64 adapters of rank 16, 2048 x 2048: 10.4 us and
+// 14.3 grouped; 1000 of 64 adapters of rank 64, 2048 x 4096: 21.2 and 28.5; 846 of 8 adapters of rank 128, 2048 x 2048: 21.5 and
 // 19.7).
 bool lora_finds(int N, int L) { return N <= kLoraSmallN || (N <= kLoraFindN && L >= N / 32); }
 
@@ -1015,7 +1017,8 @@ twell_status run_products(const LoraArgs& g, uint4* t, int sms, cudaStream_t s)
     static std::atomic<uint64_t> in_allowed{0}, out_allowed{0};
     if (twell_host::allow_smem(in, S::bytes(kLoraCluster), in_allowed) != TWELL_OK || twell_host::allow_smem(out, O::kBytes, out_allowed) != TWELL_OK)
         return TWELL_ERR_CUDA;
-    // a block's part of the columns: two pieces a warp at least, and one round of blocks, or kOutRounds where the tiles alone are more
+    // a block's part of the columns: two pieces a warp at least, and one round of two blocks an SM (tiles of 16 above rank 64 leave
+    // room for one, 152 KB), or kOutRounds where the tiles alone are more
     constexpr int kOutRounds = 2;
     const long long places = 2ll * sms, most_parts = ((g.n + 31) / 32 + 2 * kLoraWarps - 1) / (2 * kLoraWarps);
     const int about = std::max(1, g.N / S::kTok);
@@ -1048,8 +1051,8 @@ twell_status run_small(const LoraArgs& g, uint8_t* ws, int sms, cudaStream_t s)
     static_assert(kLoraFindBytes <= kLoraWarps * S::kRing, "room to find a tile");
     static_assert(S::bytes(kLoraCluster) <= 224 * 1024, "a block's shared memory");
     const int tiles = static_cast<int>(lora_tiles(g.N, g.L, S::kTok));
-    // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.5 us and 5.0 in two kernels; 18 of rank 64, 2048
-    // x 4096: 5.4 and 6.6; 30 of them: 9.9 and 7.0)
+    // (up to rank 32 two of its blocks share an SM: 30 tiles of rank 16, 2048 x 2048: 4.6 us and 5.0 in two kernels; 18 of rank 64, 2048
+    // x 4096: 5.5 and 6.6; 30 of them: 10.0 and 7.0)
     if (tiles * kLoraCluster > (RG == 1 ? 2 : 1) * sms) return run_products<1, RG, RT, kLoraFindPer>(g, sums, sms, s);
     auto kern = lora_kernel<1, RG, RT>;
     static std::atomic<uint64_t> allowed{0};

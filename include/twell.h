@@ -498,7 +498,8 @@ typedef struct {
  *   (a, b) -> factor (a cos t - b sin t, a sin t + b cos t)
  * and the other values are copied. positions: device int32, of token t of sequence b at b * pos_batch + t (pos_batch 0: the
  * same for all sequences), any value. turns: device uint64 [rot_dim / 2], 2^64 times the turns a position, modulo 2^64: the
- * fraction of a turn is then exact for every position, and t is off by at most 2^-22. k may be null.
+ * fraction of a turn is then off by 2^-33 and by the 2^-34 that the rounding of turns comes to, at most, at any position, and t,
+ * whose rest after the nearest quarter is taken in fp32, by 2^-22. k may be null.
  * dtype TWELL_BF16 or TWELL_F32; products in fp32, rounded once. factor > 0; head_dim <= 1024 and B * S * head_dim < 2^31
  * (else TWELL_ERR_UNSUPPORTED). twell_rope_bwd takes gradients of the outputs to those of the inputs: the same with -t. */
 TWELL_API twell_status twell_rope_fwd(const twell_rope_heads* q, const twell_rope_heads* k, const int32_t* positions,
@@ -533,7 +534,8 @@ typedef struct {
  * More pages given back than are missing (none are taken back then), a state outside the ring (the ring then counts as empty: no
  * page is taken, and those of requests that have ended are put into its cells from 0 on, which are all that it has after
  * the step), and pages outside [0, n_pages) in a row or the ring (slot -1) are
- * TWELL_ERR_DEVICE_CHECK too. Calls on one pool must follow one another. All integers: the same from call to call. */
+ * TWELL_ERR_DEVICE_CHECK too. A page belongs to one request (one that two rows shared would be given back twice, which is noticed
+ * only where the pages are then more than there are). Calls on one pool must follow one another. All integers: the same from call to call. */
 TWELL_API twell_status twell_kv_plan(const twell_page_pool* pool, int32_t* page_table, int32_t max_pages,
                            const int32_t* seq_lens, const int32_t* new_lens, const int32_t* labels, int32_t B,
                            int32_t n_tokens, int32_t* slots, int32_t* positions, int32_t* owner, int32_t* starts,
